@@ -16,8 +16,11 @@ Entry points (same names as the C ABI):
     attn_set_wait_give_up, attn_fwd_padded
     attn_vsa_layout, attn_vsa_tile_map, attn_gather_rows, attn_vsa_pool, attn_vsa_list_size,
     attn_vsa_block_map, attn_fwd_vsa
+    attn_kv_cache_write_fp8, attn_kv_cache_read_fp8, attn_fwd_paged_fp8,
+    attn_fwd_paged_fp8_workspace_size: the 8-bit paged KV cache
 Compositions of those calls: attn_fwd_masked (padding mask), attn_vsa (block-sparse
-video attention, with VsaPlan holding one geometry's layout on the device).
+video attention, with VsaPlan holding one geometry's layout on the device),
+attn_fwd_paged_prefill_fp8 (several new tokens a sequence over the 8-bit cache).
 """
 
 from __future__ import annotations
@@ -35,6 +38,7 @@ OUT_BF16, OUT_F32 = 0, 1
 DEV_BAD_INDEX, DEV_TIMEOUT, DEV_BAD_SEQLEN = 1, 2, 4
 STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "alignment", 4: "workspace",
                 5: "cuda", 6: "device", 7: "scratch limit"}
+KV_E4M3, KV_E5M2 = 0, 1
 NOALLOC_SCRATCH_BYTES = 32 << 20  # GBATTN_NOALLOC_SCRATCH_BYTES
 
 # (name, restype, argtypes) for every symbol of include/gbattn.h
@@ -65,6 +69,11 @@ SIGNATURES = {
     "attn_vsa_pool": (_I, [_P, _I, _I, _I, _P, _P, _P, _P]),
     "attn_vsa_list_size": (_I, [_I, _I, _I, _I, ctypes.POINTER(ctypes.c_longlong)]),
     "attn_vsa_block_map": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P]),
+    "attn_kv_cache_write_fp8": (_I, [_P, _P, _L, _L, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "attn_kv_cache_read_fp8": (_I, [_P, _P, _I, _I, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "attn_fwd_paged_fp8_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "attn_fwd_paged_fp8": (_I, [_P, _L, _P, _P, _I, _I, _I, _P, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P, _I, _P, _P, _Z,
+                                _P, _P]),
     "attn_fwd_vsa": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P, _L, _I, _I, _I, _F, _P, _I, _P, _P, _P]),
 }
 
@@ -345,6 +354,193 @@ def attn_fwd_paged_prefill(q, kv_cache, block_table, seq_lens, cu_seqlens_q, max
                                                _ptr(dev_status), _stream_handle(stream))
     _check("attn_fwd_paged_prefill", st)
     return out, lse
+
+
+# ---- 8-bit paged KV cache.  These calls run on their tensors' device, whichever
+# is current, and allocate what they return (and a workspace not given) on the
+# stream they run on.
+_KV_CODE = {torch.float8_e4m3fn: KV_E4M3, torch.float8_e5m2: KV_E5M2}
+
+
+def _fp8_cache(kv_cache, kv_scales):
+    """(code format, num_blocks, block_size, Hkv, D) of an 8-bit cache."""
+    code = _KV_CODE.get(kv_cache.dtype)
+    if code is None or kv_cache.dim() != 5 or kv_cache.shape[0] != 2:
+        raise ValueError("kv_cache must be a float8_e4m3fn or float8_e5m2 tensor [2, num_blocks, block_size, Hkv, D]")
+    _, nb, bs, hkv, d = kv_cache.shape
+    if kv_scales.dtype != torch.uint8 or tuple(kv_scales.shape) != (2, nb, hkv, bs):
+        raise ValueError(f"kv_scales must be a uint8 tensor [2, {nb}, {hkv}, {bs}] (num_blocks, Hkv, block_size)")
+    if not kv_cache.is_contiguous() or not kv_scales.is_contiguous():
+        raise ValueError("kv_cache and kv_scales must be contiguous")
+    return code, nb, bs, hkv, d
+
+
+def _on_device(dev, *named):
+    """Raise ValueError unless every tensor given is on the CUDA device dev."""
+    if dev.type != "cuda":
+        raise ValueError("the 8-bit cache calls take CUDA tensors")
+    for name, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, with the cache")
+
+
+def _index_table(name, t, dim):
+    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension{'s' if dim > 1 else ''}")
+
+
+def _status_ok(dev_status):
+    if dev_status is not None and (dev_status.element_size() != 4 or dev_status.numel() < 1):
+        raise ValueError("dev_status must be a 32-bit integer tensor")
+
+
+def _run_fp8(name, dev, stream, args):
+    """One C call on dev and stream (None: the device's current one)."""
+    fn = getattr(load_library(), name)
+    if dev.index == torch.cuda.current_device():
+        return _check(name, fn(*args, _stream_handle(stream)))
+    with torch.cuda.device(dev):
+        return _check(name, fn(*args, _stream_handle(stream)))
+
+
+def _empty_on(stream, dev, shape, dtype):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _token_rows(name, t, heads, d):
+    """Element stride between the tokens of a bf16 [T, heads, D] tensor whose [heads, D] rows are contiguous."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be a bfloat16 tensor [tokens, {heads}, {d}]")
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: a token's [heads, D] must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def attn_kv_cache_write_fp8(key, value, slot_mapping, kv_cache, kv_scales, dev_status=None, stream=None):
+    """Store key / value [T, Hkv, D] (bf16; tokens may be strided, as parts of
+    a fused projection's output) into the 8-bit cache kv_cache [2, nb, bs, Hkv,
+    D] (float8_e4m3fn or float8_e5m2) and its exponent bytes kv_scales [2, nb,
+    Hkv, bs] (uint8), in place, at slot_mapping [T] (int32): token t goes to
+    block slot // bs, offset slot % bs; negative slots store nothing.  A row
+    is codes c and a byte b that stand for c * 2^(b - 127).  Returns
+    (kv_cache, kv_scales)."""
+    code, nb, bs, hkv, d = _fp8_cache(kv_cache, kv_scales)
+    ks, vs = _token_rows("key", key, hkv, d), _token_rows("value", value, hkv, d)
+    _index_table("slot_mapping", slot_mapping, 1)
+    T = slot_mapping.numel()
+    if key.shape[0] != T or value.shape[0] != T:
+        raise ValueError("key, value and slot_mapping disagree on the token count")
+    _status_ok(dev_status)
+    dev = kv_cache.device
+    _on_device(dev, ("key", key), ("value", value), ("slot_mapping", slot_mapping), ("kv_scales", kv_scales),
+               ("dev_status", dev_status))
+    _run_fp8("attn_kv_cache_write_fp8", dev, stream,
+             (key.data_ptr(), value.data_ptr(), ks, vs, slot_mapping.data_ptr(), T, kv_cache.data_ptr(),
+              kv_scales.data_ptr(), code, nb, bs, hkv, d, _ptr(dev_status)))
+    return kv_cache, kv_scales
+
+
+def attn_kv_cache_read_fp8(kv_cache, kv_scales, block_table, cu_seqlens_k, total_tokens, k=None, v=None,
+                           dev_status=None, stream=None):
+    """The first cu_seqlens_k[s + 1] - cu_seqlens_k[s] context tokens of every
+    sequence s, read from the 8-bit cache through block_table [S, max_blocks]
+    (int32), as packed bf16 rows (k, v), each [total_tokens, Hkv, D]: what
+    attn_fwd_varlen takes.  total_tokens (host int) is at least
+    cu_seqlens_k[S]; rows past that are left as they were."""
+    code, nb, bs, hkv, d = _fp8_cache(kv_cache, kv_scales)
+    _index_table("block_table", block_table, 2)
+    _index_table("cu_seqlens_k", cu_seqlens_k, 1)
+    S = cu_seqlens_k.numel() - 1
+    if S < 0 or block_table.shape[0] != S:
+        raise ValueError("block_table must have a row, and cu_seqlens_k a boundary, for each sequence")
+    _status_ok(dev_status)
+    dev, T = kv_cache.device, int(total_tokens)
+    _on_device(dev, ("kv_scales", kv_scales), ("block_table", block_table), ("cu_seqlens_k", cu_seqlens_k), ("k", k),
+               ("v", v), ("dev_status", dev_status))
+    for name, t in (("k", k), ("v", v)):
+        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, hkv, d) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{T}, {hkv}, {d}]")
+    if k is None:
+        k = _empty_on(stream, dev, (T, hkv, d), torch.bfloat16)
+    if v is None:
+        v = _empty_on(stream, dev, (T, hkv, d), torch.bfloat16)
+    _run_fp8("attn_kv_cache_read_fp8", dev, stream,
+             (kv_cache.data_ptr(), kv_scales.data_ptr(), code, nb, bs, block_table.data_ptr(),
+              max(1, block_table.shape[1]), cu_seqlens_k.data_ptr(), S, T, hkv, d, k.data_ptr(), v.data_ptr(),
+              _ptr(dev_status)))
+    return k, v
+
+
+def attn_fwd_paged_fp8_workspace_size(num_seqs, Hq, Hkv, D, max_seq_len) -> int:
+    return int(load_library().attn_fwd_paged_fp8_workspace_size(num_seqs, Hq, Hkv, D, max_seq_len))
+
+
+def attn_fwd_paged_fp8(q, kv_cache, kv_scales, block_table, seq_lens, max_seq_len, softmax_scale=None, causal=True,
+                       out=None, lse=None, out_dtype=torch.float32, workspace=None, dev_status=None, stream=None):
+    """attn_fwd_paged over an 8-bit cache (attn_kv_cache_write_fp8): q [S, Hq,
+    D] bf16 (sequences may be strided); kv_cache [2, nb, 128, Hkv, D] float8;
+    kv_scales [2, nb, Hkv, 128] uint8; block_table int32 [S, max_blocks];
+    seq_lens int32 [S]; max_seq_len host int.  Returns (out [S, Hq, D], lse
+    [S, Hq] or None).  A workspace tensor of at least
+    ``attn_fwd_paged_fp8_workspace_size`` bytes may be passed (it is allocated
+    here otherwise); calls that can overlap need one each."""
+    code, nb, bs, hkv, d = _fp8_cache(kv_cache, kv_scales)
+    if q.dim() != 3:
+        raise ValueError("q must be [S, Hq, D]")
+    S, Hq = q.shape[0], q.shape[1]
+    qs = _token_rows("q", q, Hq, d)
+    _index_table("block_table", block_table, 2)
+    _index_table("seq_lens", seq_lens, 1)
+    if block_table.shape[0] != S or seq_lens.shape[0] != S:
+        raise ValueError("block_table and seq_lens must have a row for each of q's sequences")
+    _status_ok(dev_status)
+    dev, max_seq_len = kv_cache.device, int(max_seq_len)
+    is_lse = torch.is_tensor(lse)
+    _on_device(dev, ("q", q), ("kv_scales", kv_scales), ("block_table", block_table), ("seq_lens", seq_lens),
+               ("out", out), ("lse", lse if is_lse else None), ("workspace", workspace), ("dev_status", dev_status))
+    if out is None:
+        out = _empty_on(stream, dev, (S, Hq, d), out_dtype)
+    elif tuple(out.shape) != (S, Hq, d) or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous tensor [{S}, {Hq}, {d}]")
+    if is_lse:
+        if lse.dtype != torch.float32 or tuple(lse.shape) != (S, Hq) or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor [{S}, {Hq}]")
+    else:
+        lse = _empty_on(stream, dev, (S, Hq), torch.float32) if lse else None
+    need = load_library().attn_fwd_paged_fp8_workspace_size(S, Hq, hkv, d, max_seq_len)
+    if workspace is None:
+        workspace = _empty_on(stream, dev, (need,), torch.uint8) if need else None
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
+    _run_fp8("attn_fwd_paged_fp8", dev, stream,
+             (q.data_ptr(), qs, kv_cache.data_ptr(), kv_scales.data_ptr(), code, nb, bs, block_table.data_ptr(),
+              block_table.shape[1], seq_lens.data_ptr(), S, max_seq_len, Hq, hkv, d, scale, int(bool(causal)),
+              out.data_ptr(), _out_code(out.dtype), _ptr(lse), _ptr(workspace), ws_bytes, _ptr(dev_status)))
+    return out, lse
+
+
+def attn_fwd_paged_prefill_fp8(q, kv_cache, kv_scales, block_table, cu_seqlens_q, cu_seqlens_k, total_tokens,
+                               max_seqlen_q, max_seq_len, softmax_scale=None, causal=True, out=None, lse=None,
+                               out_dtype=torch.float32, dev_status=None, stream=None):
+    """Several query tokens a sequence (packed by cu_seqlens_q, the last tokens
+    of each context) against the 8-bit cache: the contexts are read back
+    (attn_kv_cache_read_fp8) and attended as packed documents
+    (attn_fwd_varlen).  cu_seqlens_k [S + 1] (int32) holds the contexts' running
+    sum, total_tokens >= cu_seqlens_k[S], max_seqlen_q and max_seq_len are
+    host ints.  Returns (out [Tq, Hq, D], lse [Hq, Tq] or None)."""
+    T = int(total_tokens)
+    k, v = attn_kv_cache_read_fp8(kv_cache, kv_scales, block_table, cu_seqlens_k, T, dev_status=dev_status,
+                                  stream=stream)
+    with torch.cuda.device(kv_cache.device):
+        s = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(s):
+            return attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seq_len, softmax_scale, causal,
+                                   out, lse, out_dtype, dev_status, stream)
 
 
 def attn_mask_to_varlen(mask, stream=None):

@@ -86,6 +86,21 @@ bool encode_rows_heads_d(CUtensorMap* m, const void* base, long long rows, int h
     return r == CUDA_SUCCESS;
 }
 
+// 8-bit cache [rows, heads, D] as a 3-D TMA map of bytes, box {128, 1, 128},
+// 128-byte swizzle: a box is one head's 128 rows, zeros past D.
+bool encode_fp8_cache(CUtensorMap* m, const void* base, long long rows, int heads, int d) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads) * d};
+    cuuint32_t box[3] = {128, 1, 128};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // Shared by the dense and varlen entries: validation of what they have in common.
 // k and v may be null only when there are no keys at all (has_keys == false).
 gbattn_status check_common(const void* q, const void* k, const void* v, const void* out, int Hq, int Hkv, int D,
@@ -116,6 +131,16 @@ gbattn_status run_prefill(const void* q, const void* k, const void* v, long long
         !encode_rows_heads_d(&to, p.out, Tq, p.Hq, D, 128, p.out_f32 != 0))
         return GBATTN_ERR_CUDA;
     return gbattn::launch_prefill(D, tq, tk, tv, to, p, di.sms, st) == cudaSuccess ? GBATTN_OK : GBATTN_ERR_CUDA;
+}
+
+// Shared by the calls on the 8-bit cache: its sizes and code format.
+gbattn_status check_fp8_cache(int num_blocks, int block_size, int Hkv, int D, gbattn_kv_dtype kv) {
+    if (num_blocks <= 0 || block_size <= 0 || Hkv <= 0) return GBATTN_ERR_INVALID_ARG;
+    if (!head_size_ok(D)) return GBATTN_ERR_UNSUPPORTED;
+    if (kv != GBATTN_KV_E4M3 && kv != GBATTN_KV_E5M2) return GBATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_blocks) * block_size > 0x7fffffffLL) return GBATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(Hkv) * D > 0x3fffffffLL) return GBATTN_ERR_UNSUPPORTED;  // 32-bit offsets in a row
+    return GBATTN_OK;
 }
 
 // 1: the prefill kernels give up every pipeline wait (attn_set_wait_give_up).
@@ -530,6 +555,148 @@ gbattn_status attn_fwd_paged(const void* q, const void* kv_cache, int num_blocks
                : GBATTN_ERR_CUDA;
 }
 
+
+// ---------------------------------------------------------------- 8-bit KV cache
+gbattn_status attn_kv_cache_write_fp8(const void* key, const void* value, long long key_stride, long long value_stride,
+                                      const int32_t* slot_mapping, int num_tokens, void* kv_cache, uint8_t* kv_scales,
+                                      gbattn_kv_dtype kv_dtype, int num_blocks, int block_size, int Hkv, int D,
+                                      uint32_t* dev_status, void* stream) {
+    gbattn_status s = check_fp8_cache(num_blocks, block_size, Hkv, D, kv_dtype);
+    if (s != GBATTN_OK) return s;
+    if (num_tokens < 0) return GBATTN_ERR_INVALID_ARG;
+    const long long row = static_cast<long long>(Hkv) * D;
+    if (num_tokens > 1 && (key_stride < row || value_stride < row)) return GBATTN_ERR_INVALID_ARG;
+    if (num_tokens == 0) return GBATTN_OK;
+    if (!key || !value || !slot_mapping || !kv_cache || !kv_scales) return GBATTN_ERR_INVALID_ARG;
+    if (!aligned16(key) || !aligned16(value) || !aligned16(kv_cache) || !aligned16(kv_scales) || key_stride % 8 != 0 ||
+        value_stride % 8 != 0)
+        return GBATTN_ERR_ALIGNMENT;
+    DeviceInfo di;
+    s = device_info(&di);
+    if (s != GBATTN_OK) return s;
+    gbattn::CacheWriteFp8Params p{};
+    p.key = static_cast<const uint16_t*>(key);
+    p.value = static_cast<const uint16_t*>(value);
+    p.key_stride = key_stride;
+    p.value_stride = value_stride;
+    p.slot_mapping = slot_mapping;
+    p.cache = static_cast<uint8_t*>(kv_cache);
+    p.scales = kv_scales;
+    p.num_tokens = num_tokens;
+    p.num_slots = static_cast<long long>(num_blocks) * block_size;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.Hkv = Hkv;
+    p.e5m2 = kv_dtype == GBATTN_KV_E5M2;
+    p.status = dev_status;
+    return gbattn::launch_cache_write_fp8(p, D, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GBATTN_OK
+               : GBATTN_ERR_CUDA;
+}
+
+gbattn_status attn_kv_cache_read_fp8(const void* kv_cache, const uint8_t* kv_scales, gbattn_kv_dtype kv_dtype,
+                                     int num_blocks, int block_size, const int32_t* block_table, int max_blocks_per_seq,
+                                     const int32_t* cu_seqlens_k, int num_seqs, int Tk, int Hkv, int D, void* k, void* v,
+                                     uint32_t* dev_status, void* stream) {
+    gbattn_status s = check_fp8_cache(num_blocks, block_size, Hkv, D, kv_dtype);
+    if (s != GBATTN_OK) return s;
+    if (num_seqs < 0 || Tk < 0 || max_blocks_per_seq <= 0) return GBATTN_ERR_INVALID_ARG;
+    if (Tk > 0x7fffffff - 64) return GBATTN_ERR_UNSUPPORTED;  // row counters are 32-bit on the device
+    if (num_seqs == 0 || Tk == 0) return GBATTN_OK;
+    if (!kv_cache || !kv_scales || !block_table || !cu_seqlens_k || !k || !v) return GBATTN_ERR_INVALID_ARG;
+    if (!aligned16(kv_cache) || !aligned16(kv_scales) || !aligned16(k) || !aligned16(v)) return GBATTN_ERR_ALIGNMENT;
+    DeviceInfo di;
+    s = device_info(&di);
+    if (s != GBATTN_OK) return s;
+    gbattn::CacheReadFp8Params p{};
+    p.cache = static_cast<const uint8_t*>(kv_cache);
+    p.scales = kv_scales;
+    p.block_table = block_table;
+    p.cu = cu_seqlens_k;
+    p.k = static_cast<uint4*>(k);
+    p.v = static_cast<uint4*>(v);
+    p.num_slots = static_cast<long long>(num_blocks) * block_size;
+    p.num_seqs = num_seqs;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.total = Tk;
+    p.e5m2 = kv_dtype == GBATTN_KV_E5M2;
+    p.status = dev_status;
+    return gbattn::launch_cache_read_fp8(p, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GBATTN_OK
+                                                                                                  : GBATTN_ERR_CUDA;
+}
+
+size_t attn_fwd_paged_fp8_workspace_size(int num_seqs, int Hq, int Hkv, int D, int max_seq_len) {
+    if (num_seqs <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_seq_len < 0 || !head_size_ok(D)) return 0;
+    return gbattn::paged_fp8_plan(num_seqs, Hq, Hkv, D, max_seq_len).workspace_bytes;
+}
+
+gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* kv_cache, const uint8_t* kv_scales,
+                                 gbattn_kv_dtype kv_dtype, int num_blocks, int block_size, const int32_t* block_table,
+                                 int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs, int max_seq_len, int Hq,
+                                 int Hkv, int D, float softmax_scale, int causal, void* out, gbattn_dtype out_dtype,
+                                 float* lse, void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                 void* stream) {
+    (void)causal;  // one query token sees its whole context under the bottom-right rule
+    if (!q || !kv_cache || !kv_scales || !block_table || !seq_lens || !out) return GBATTN_ERR_INVALID_ARG;
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || !scale_ok(softmax_scale)) return GBATTN_ERR_INVALID_ARG;
+    if (max_blocks_per_seq <= 0 || num_seqs < 0 || max_seq_len < 0) return GBATTN_ERR_INVALID_ARG;
+    gbattn_status s = check_fp8_cache(num_blocks, block_size, Hkv, D, kv_dtype);
+    if (s != GBATTN_OK) return s;
+    if (block_size != 128) return GBATTN_ERR_UNSUPPORTED;
+    if (out_dtype != GBATTN_OUT_BF16 && out_dtype != GBATTN_OUT_F32) return GBATTN_ERR_UNSUPPORTED;
+    if (2LL * num_blocks * 128 > 0x7FFFFFFFLL) return GBATTN_ERR_UNSUPPORTED;  // TMA row coordinate is int32
+    if (num_seqs > 1 && q_stride < static_cast<long long>(Hq) * D) return GBATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(kv_scales) || !aligned16(out) || q_stride % 8 != 0)
+        return GBATTN_ERR_ALIGNMENT;
+    if (num_seqs == 0) return GBATTN_OK;
+    const gbattn::PagedFp8Plan plan = gbattn::paged_fp8_plan(num_seqs, Hq, Hkv, D, max_seq_len);
+    if (plan.n_hgroups * plan.chunks > 0x7fffffffLL || (Hq + 3) / 4 > 65535) return GBATTN_ERR_UNSUPPORTED;
+    if (plan.workspace_bytes &&
+        (!workspace || workspace_bytes < plan.workspace_bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return GBATTN_ERR_WORKSPACE;
+    DeviceInfo di;
+    s = device_info(&di);
+    if (s != GBATTN_OK) return s;
+    CUtensorMap tm;
+    if (!encode_fp8_cache(&tm, kv_cache, 2LL * num_blocks * 128, Hkv, D)) return GBATTN_ERR_CUDA;
+    gbattn::PagedFp8Params p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_stride = q_stride;
+    p.scales = kv_scales;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.out = out;
+    p.lse = lse;
+    p.status = dev_status;
+    char* ws = static_cast<char*>(workspace);
+    if (plan.chunks > 1) {
+        p.part_o = reinterpret_cast<float*>(ws);
+        p.part_lse = reinterpret_cast<float*>(ws + plan.o_bytes);
+        p.joins = reinterpret_cast<int2*>(ws + plan.o_bytes + plan.lse_bytes);
+    }
+    p.num_seqs = num_seqs;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    const long long cap = 128LL * max_blocks_per_seq;
+    p.cap = cap < max_seq_len ? static_cast<int>(cap) : max_seq_len;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.group = Hq / Hkv;
+    p.subs = plan.subs;
+    p.heads_per_sub = plan.heads_per_sub;
+    p.head_cols = plan.head_cols;
+    p.n_hgroups = static_cast<int>(plan.n_hgroups);
+    p.chunks = plan.chunks;
+    p.scale_log2 = softmax_scale * kLog2e;
+    p.out_f32 = out_dtype == GBATTN_OUT_F32;
+    p.e5m2 = kv_dtype == GBATTN_KV_E5M2;
+    return gbattn::launch_paged_fp8(D, tm, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GBATTN_OK
+                                                                                             : GBATTN_ERR_CUDA;
+}
 
 // ---------------------------------------------------------------- block-sparse video attention
 gbattn_status attn_gather_rows(const void* src, long long src_rows, const int32_t* index, long long dst_rows,

@@ -131,6 +131,71 @@ struct CacheWriteParams {
 };
 cudaError_t launch_cache_write(const CacheWriteParams& p, int num_sms, cudaStream_t stream);
 
+// 8-bit KV cache (cache_fp8.cu): codes [2, num_blocks, block_size, Hkv, D]
+// (e4m3fn, or e5m2) and one exponent byte a row, [2, num_blocks, Hkv,
+// block_size]; a code c of exponent byte b stands for c * 2^(b - 127).
+struct CacheWriteFp8Params {
+    const uint16_t* key;  // bf16 [T, Hkv, D], token t at t * key_stride elements
+    const uint16_t* value;
+    long long key_stride, value_stride;
+    const int32_t* slot_mapping;
+    uint8_t* cache;
+    uint8_t* scales;
+    long long num_tokens;
+    long long num_slots;  // num_blocks * block_size
+    int num_blocks, block_size, Hkv;
+    int e5m2;
+    uint32_t* status;
+};
+cudaError_t launch_cache_write_fp8(const CacheWriteFp8Params& p, int D, int num_sms, cudaStream_t stream);
+
+struct CacheReadFp8Params {
+    const uint8_t* cache;
+    const uint8_t* scales;
+    const int32_t* block_table;  // [num_seqs, max_blocks]
+    const int32_t* cu;           // [num_seqs + 1]
+    uint4* k;                    // bf16 [total, Hkv, D]
+    uint4* v;
+    long long num_slots;
+    int num_seqs, max_blocks, num_blocks, block_size, Hkv, D, total;
+    int e5m2;
+    uint32_t* status;
+};
+cudaError_t launch_cache_read_fp8(const CacheReadFp8Params& p, int num_sms, cudaStream_t stream);
+
+// Paged decode over the 8-bit cache (decode_fp8.cu), blocks of 128 tokens.
+struct PagedFp8Params {
+    const uint16_t* q;  // bf16 [S, Hq, D], sequence s at s * q_stride elements
+    long long q_stride;
+    const uint8_t* scales;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    void* out;
+    float* lse;
+    uint32_t* status;
+    float* part_o;    // [chunks, 2, Hq, D]
+    float* part_lse;  // [chunks, 2, Hq], base 2
+    int2* joins;      // [chunks]: the sequence that begins in the chunk and goes on, and its last chunk; or -1
+    int num_seqs, num_blocks, max_blocks;
+    int cap;          // largest context: min(max_seq_len, 128 * max_blocks)
+    int Hq, Hkv, group;
+    int subs, heads_per_sub, head_cols;  // a KV head's query heads in `subs` runs of heads_per_sub, padded to head_cols
+    int n_hgroups;    // Hkv * subs
+    int chunks;
+    float scale_log2;
+    int out_f32, e5m2;
+};
+struct PagedFp8Plan {
+    int subs, heads_per_sub, head_cols, chunks;
+    long long n_hgroups;
+    size_t o_bytes, lse_bytes;  // workspace sections, each 256-byte aligned; then the joins
+    size_t workspace_bytes;
+};
+// num_seqs, Hq, Hkv, D > 0, Hq % Hkv == 0.
+PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_len);
+// tmKV: the cache as bytes {D, Hkv, 2 * num_blocks * 128}, box {128, 1, 128}, 128-byte swizzle.
+cudaError_t launch_paged_fp8(int D, const CUtensorMap& tmKV, const PagedFp8Params& p, cudaStream_t stream);
+
 // Padding mask <-> packed varlen (masks.cu).  mask [B, S] bytes (nonzero =
 // token); cu_seqlens [B + 1]; packed_pos [B * S]: the token's packed row or -1.
 cudaError_t launch_mask_to_varlen(const uint8_t* mask, int B, int S, int32_t* cu_seqlens, int32_t* packed_pos,

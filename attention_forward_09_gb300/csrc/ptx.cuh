@@ -329,6 +329,35 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {  // round 
     return r;
 }
 
+// Two fp32 values to two 8-bit codes (the first in the low byte), round to
+// nearest even, beyond the largest code saturated, NaN to NaN; and back.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t pack_fp8x2(float lo, float hi) {
+    uint16_t r;
+    if constexpr (E5M2)
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool E5M2>
+__device__ __forceinline__ float2 unpack_fp8x2(uint32_t c) {
+    uint32_t h;
+    if constexpr (E5M2)
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
+    else
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
+    float2 f;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h));
+    return f;
+}
+// 2^(b - 127) of an exponent byte b (b = 0 stands for 2^-127, as e8m0 has it).
+__device__ __forceinline__ float exp2_byte(int b) {
+    return __uint_as_float(b ? static_cast<uint32_t>(b) << 23 : 0x00400000u);
+}
+
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                              uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),

@@ -63,6 +63,12 @@ typedef enum {
     GBATTN_OUT_F32 = 1
 } gbattn_dtype;
 
+/* Code format of the 8-bit KV cache. */
+typedef enum {
+    GBATTN_KV_E4M3 = 0, /* float8 e4m3fn: 4 significant bits, largest 448 */
+    GBATTN_KV_E5M2 = 1  /* float8 e5m2: 3 significant bits, largest 57344 */
+} gbattn_kv_dtype;
+
 /* Bits the kernels OR into *dev_status. */
 #define GBATTN_DEV_BAD_INDEX 1u   /* block_table entry, slot or row index out of range (skipped) */
 #define GBATTN_DEV_TIMEOUT 2u     /* a pipeline wait gave up; that tile's output is invalid */
@@ -362,6 +368,83 @@ gbattn_status attn_fwd_paged_noalloc(const void* q, const void* kv_cache, int nu
                                      int Hq, int Hkv, int D, float softmax_scale, int causal,
                                      void* out, gbattn_dtype out_dtype, float* lse,
                                      uint32_t* dev_status, void* stream);
+
+/*
+ * 8-bit paged KV cache: attn_kv_cache_write, the context read-back and
+ * attn_fwd_paged over a cache of half the bytes.  An addition of this library
+ * (the pages' quantised attention is for another device and keeps no 8-bit
+ * cache on this path).
+ *
+ *   kv_cache   device bytes [2, num_blocks, block_size, Hkv, D]: codes, [0] of
+ *              keys, [1] of values, in the format kv_dtype
+ *   kv_scales  device bytes [2, num_blocks, Hkv, block_size]: one exponent byte
+ *              for each row of D codes
+ * A code c in a row of exponent byte b (0 to 254) stands for c * 2^(b - 127).
+ * Both are 16-byte aligned.
+ *
+ * attn_kv_cache_write_fp8 -- as attn_kv_cache_write, quantising on the way.
+ *   key, value    device bf16, token t's [Hkv, D] at t * key_stride (value_stride)
+ *                 elements, so that they may be parts of a fused projection's
+ *                 output; strides at least Hkv * D and multiples of 8, key and
+ *                 value 16-byte aligned
+ *   slot_mapping  device int32 [num_tokens], as for attn_kv_cache_write
+ *   block_size    any positive size (attn_fwd_paged_fp8 reads 128)
+ * With c_max the format's largest code, a row's exponent e = b - 127 is the
+ * least one >= -126 with max |x| <= c_max * 2^e over its finite values (-126
+ * for a row without a non-zero one); its codes are x / 2^e rounded to nearest,
+ * ties to even, and NaN where x is NaN or infinite.
+ * Repeated slots, slots past the cache and errors as for attn_kv_cache_write
+ * (for a repeated slot, each row of codes and each exponent byte is one of
+ * the tokens', not necessarily the same one's), plus GBATTN_ERR_UNSUPPORTED
+ * for an unknown kv_dtype.
+ *
+ * attn_kv_cache_read_fp8 -- the contexts of num_seqs sequences as packed bf16
+ * rows, the k and v of attn_fwd_varlen (a prefill over a cached context).
+ *   block_table   device int32 [num_seqs, max_blocks_per_seq]: token i of
+ *                 sequence s is in block block_table[s, i / block_size], slot
+ *                 i % block_size
+ *   cu_seqlens_k  device int32 [num_seqs + 1], 0 = c[0] <= ... <= c[num_seqs] <= Tk:
+ *                 sequence s's first c[s+1] - c[s] tokens go to rows [c[s], c[s+1])
+ *   k, v          out, device bf16 [Tk, Hkv, D], 16-byte aligned; rows at or
+ *                 past c[num_seqs] are left as they were
+ * Values are exact (a code has at most 4 significant bits) unless below bf16's
+ * smallest normal number.  A block_table entry outside [0, num_blocks) sets
+ * GBATTN_DEV_BAD_INDEX and its tokens' rows are zeros; a sequence whose
+ * cu_seqlens_k decrease, run past Tk or past max_blocks_per_seq blocks sets
+ * GBATTN_DEV_BAD_SEQLEN, and its rows are left as they were.
+ *
+ * attn_fwd_paged_fp8 -- attn_fwd_paged over the 8-bit cache: the same results
+ * as over a bf16 cache that holds the values the codes stand for, the softmax
+ * weights of a block of 128 tokens held to 12 significant bits for bf16 output
+ * and to 16 for fp32.
+ *   q         device bf16, sequence s's [Hq, D] at s * q_stride elements
+ *             (at least Hq * D, a multiple of 8)
+ *   workspace at least attn_fwd_paged_fp8_workspace_size bytes (may be 0:
+ *             workspace is then not used), 256-byte aligned, contents need no
+ *             initialisation; calls that can overlap need one each
+ * The other arguments, the treatment of unused slots and table entries, of
+ * empty sequences, bad blocks (their tokens are skipped) and bad lengths, and
+ * the errors are those of attn_fwd_paged.  block_size must be 128.  A query
+ * value that is NaN or infinite makes its head's result NaN.
+ *
+ * attn_fwd_paged_fp8_workspace_size -- pure host arithmetic, as
+ * attn_fwd_paged_workspace_size.
+ */
+gbattn_status attn_kv_cache_write_fp8(const void* key, const void* value, long long key_stride, long long value_stride,
+                                      const int32_t* slot_mapping, int num_tokens, void* kv_cache, uint8_t* kv_scales,
+                                      gbattn_kv_dtype kv_dtype, int num_blocks, int block_size, int Hkv, int D,
+                                      uint32_t* dev_status, void* stream);
+gbattn_status attn_kv_cache_read_fp8(const void* kv_cache, const uint8_t* kv_scales, gbattn_kv_dtype kv_dtype,
+                                     int num_blocks, int block_size, const int32_t* block_table, int max_blocks_per_seq,
+                                     const int32_t* cu_seqlens_k, int num_seqs, int Tk, int Hkv, int D, void* k, void* v,
+                                     uint32_t* dev_status, void* stream);
+size_t attn_fwd_paged_fp8_workspace_size(int num_seqs, int Hq, int Hkv, int D, int max_seq_len);
+gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* kv_cache, const uint8_t* kv_scales,
+                                 gbattn_kv_dtype kv_dtype, int num_blocks, int block_size, const int32_t* block_table,
+                                 int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs, int max_seq_len, int Hq,
+                                 int Hkv, int D, float softmax_scale, int causal, void* out, gbattn_dtype out_dtype,
+                                 float* lse, void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                 void* stream);
 
 /*
  * attn_set_wait_give_up -- a switch for testing the failure path of the

@@ -21,3 +21,4 @@ from .attention import (  # noqa: F401
     vsa_pool,
     vsa_blocks,
 )
+from .fp8_cache import code_values, kv_cache_write_fp8, quantise_rows, stands_for  # noqa: F401
