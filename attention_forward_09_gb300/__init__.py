@@ -376,12 +376,12 @@ def _fp8_cache(kv_cache, kv_scales):
 
 
 def _on_device(dev, *named):
-    """Raise ValueError unless every tensor given is on the CUDA device dev."""
-    if dev.type != "cuda":
+    """Raise ValueError unless every tensor given is on CUDA device number dev."""
+    if dev < 0:
         raise ValueError("the 8-bit cache calls take CUDA tensors")
     for name, t in named:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, with the cache")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev}, with the cache")
 
 
 def _index_table(name, t, dim):
@@ -389,25 +389,33 @@ def _index_table(name, t, dim):
         raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension{'s' if dim > 1 else ''}")
 
 
-def _status_ok(dev_status):
-    if dev_status is not None and (dev_status.element_size() != 4 or dev_status.numel() < 1):
+def _status_ptr(dev_status):
+    if dev_status is None:
+        return None
+    if dev_status.element_size() != 4 or dev_status.numel() < 1:
         raise ValueError("dev_status must be a 32-bit integer tensor")
+    return dev_status.data_ptr()
 
 
 def _run_fp8(name, dev, stream, args):
-    """One C call on dev and stream (None: the device's current one)."""
-    fn = getattr(load_library(), name)
-    if dev.index == torch.cuda.current_device():
-        return _check(name, fn(*args, _stream_handle(stream)))
-    with torch.cuda.device(dev):
-        return _check(name, fn(*args, _stream_handle(stream)))
+    """One C call on device number dev and stream (None: the device's current one)."""
+    fn = getattr(_lib or load_library(), name)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st != 0:
+        raise GbattnError(name, st)
 
 
-def _empty_on(stream, dev, shape, dtype):
+def _empty_on(stream, like, shape, dtype):
+    """An uninitialised tensor on like's device, of the stream that will write it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _token_rows(name, t, heads, d):
@@ -433,13 +441,12 @@ def attn_kv_cache_write_fp8(key, value, slot_mapping, kv_cache, kv_scales, dev_s
     T = slot_mapping.numel()
     if key.shape[0] != T or value.shape[0] != T:
         raise ValueError("key, value and slot_mapping disagree on the token count")
-    _status_ok(dev_status)
-    dev = kv_cache.device
+    status, dev = _status_ptr(dev_status), kv_cache.get_device()
     _on_device(dev, ("key", key), ("value", value), ("slot_mapping", slot_mapping), ("kv_scales", kv_scales),
                ("dev_status", dev_status))
     _run_fp8("attn_kv_cache_write_fp8", dev, stream,
              (key.data_ptr(), value.data_ptr(), ks, vs, slot_mapping.data_ptr(), T, kv_cache.data_ptr(),
-              kv_scales.data_ptr(), code, nb, bs, hkv, d, _ptr(dev_status)))
+              kv_scales.data_ptr(), code, nb, bs, hkv, d, status))
     return kv_cache, kv_scales
 
 
@@ -456,21 +463,20 @@ def attn_kv_cache_read_fp8(kv_cache, kv_scales, block_table, cu_seqlens_k, total
     S = cu_seqlens_k.numel() - 1
     if S < 0 or block_table.shape[0] != S:
         raise ValueError("block_table must have a row, and cu_seqlens_k a boundary, for each sequence")
-    _status_ok(dev_status)
-    dev, T = kv_cache.device, int(total_tokens)
+    status, dev, T = _status_ptr(dev_status), kv_cache.get_device(), int(total_tokens)
     _on_device(dev, ("kv_scales", kv_scales), ("block_table", block_table), ("cu_seqlens_k", cu_seqlens_k), ("k", k),
                ("v", v), ("dev_status", dev_status))
     for name, t in (("k", k), ("v", v)):
         if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, hkv, d) or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{T}, {hkv}, {d}]")
     if k is None:
-        k = _empty_on(stream, dev, (T, hkv, d), torch.bfloat16)
+        k = _empty_on(stream, kv_cache, (T, hkv, d), torch.bfloat16)
     if v is None:
-        v = _empty_on(stream, dev, (T, hkv, d), torch.bfloat16)
+        v = _empty_on(stream, kv_cache, (T, hkv, d), torch.bfloat16)
     _run_fp8("attn_kv_cache_read_fp8", dev, stream,
              (kv_cache.data_ptr(), kv_scales.data_ptr(), code, nb, bs, block_table.data_ptr(),
               max(1, block_table.shape[1]), cu_seqlens_k.data_ptr(), S, T, hkv, d, k.data_ptr(), v.data_ptr(),
-              _ptr(dev_status)))
+              status))
     return k, v
 
 
@@ -496,31 +502,32 @@ def attn_fwd_paged_fp8(q, kv_cache, kv_scales, block_table, seq_lens, max_seq_le
     _index_table("seq_lens", seq_lens, 1)
     if block_table.shape[0] != S or seq_lens.shape[0] != S:
         raise ValueError("block_table and seq_lens must have a row for each of q's sequences")
-    _status_ok(dev_status)
-    dev, max_seq_len = kv_cache.device, int(max_seq_len)
-    is_lse = torch.is_tensor(lse)
+    status, dev, max_seq_len = _status_ptr(dev_status), kv_cache.get_device(), int(max_seq_len)
+    given = lse if torch.is_tensor(lse) else None
     _on_device(dev, ("q", q), ("kv_scales", kv_scales), ("block_table", block_table), ("seq_lens", seq_lens),
-               ("out", out), ("lse", lse if is_lse else None), ("workspace", workspace), ("dev_status", dev_status))
+               ("out", out), ("lse", given), ("workspace", workspace), ("dev_status", dev_status))
     if out is None:
-        out = _empty_on(stream, dev, (S, Hq, d), out_dtype)
+        out = _empty_on(stream, kv_cache, (S, Hq, d), out_dtype)
     elif tuple(out.shape) != (S, Hq, d) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous tensor [{S}, {Hq}, {d}]")
-    if is_lse:
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (S, Hq) or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous float32 tensor [{S}, {Hq}]")
-    else:
-        lse = _empty_on(stream, dev, (S, Hq), torch.float32) if lse else None
-    need = load_library().attn_fwd_paged_fp8_workspace_size(S, Hq, hkv, d, max_seq_len)
+    if given is None:
+        lse = _empty_on(stream, kv_cache, (S, Hq), torch.float32) if lse else None
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (S, Hq) or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor [{S}, {Hq}]")
     if workspace is None:
-        workspace = _empty_on(stream, dev, (need,), torch.uint8) if need else None
-    elif not workspace.is_contiguous():
+        ws_bytes = load_library().attn_fwd_paged_fp8_workspace_size(S, Hq, hkv, d, max_seq_len)
+        if ws_bytes:
+            workspace = _empty_on(stream, kv_cache, (ws_bytes,), torch.uint8)
+    elif workspace.is_contiguous():
+        ws_bytes = workspace.numel() * workspace.element_size()
+    else:
         raise ValueError("workspace must be contiguous")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
     _run_fp8("attn_fwd_paged_fp8", dev, stream,
              (q.data_ptr(), qs, kv_cache.data_ptr(), kv_scales.data_ptr(), code, nb, bs, block_table.data_ptr(),
-              block_table.shape[1], seq_lens.data_ptr(), S, max_seq_len, Hq, hkv, d, scale, int(bool(causal)),
-              out.data_ptr(), _out_code(out.dtype), _ptr(lse), _ptr(workspace), ws_bytes, _ptr(dev_status)))
+              block_table.shape[1], seq_lens.data_ptr(), S, max_seq_len, Hq, hkv, d, scale, 1 if causal else 0,
+              out.data_ptr(), _out_code(out.dtype), None if lse is None else lse.data_ptr(),
+              None if workspace is None else workspace.data_ptr(), ws_bytes, status))
     return out, lse
 
 

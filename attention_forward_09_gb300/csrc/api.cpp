@@ -654,7 +654,7 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
         return GBATTN_ERR_ALIGNMENT;
     if (num_seqs == 0) return GBATTN_OK;
     const gbattn::PagedFp8Plan plan = gbattn::paged_fp8_plan(num_seqs, Hq, Hkv, D, max_seq_len);
-    if (plan.n_hgroups * plan.chunks > 0x7fffffffLL || (Hq + 3) / 4 > 65535) return GBATTN_ERR_UNSUPPORTED;
+    if (plan.n_hgroups * plan.chunks > 0x7fffffffLL || Hq > 65535) return GBATTN_ERR_UNSUPPORTED;
     if (plan.workspace_bytes &&
         (!workspace || workspace_bytes < plan.workspace_bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return GBATTN_ERR_WORKSPACE;
@@ -673,7 +673,7 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
     p.lse = lse;
     p.status = dev_status;
     char* ws = static_cast<char*>(workspace);
-    if (plan.chunks > 1) {
+    if (plan.workspace_bytes) {
         p.part_o = reinterpret_cast<float*>(ws);
         p.part_lse = reinterpret_cast<float*>(ws + plan.o_bytes);
         p.joins = reinterpret_cast<int2*>(ws + plan.o_bytes + plan.lse_bytes);
@@ -691,6 +691,7 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
     p.head_cols = plan.head_cols;
     p.n_hgroups = static_cast<int>(plan.n_hgroups);
     p.chunks = plan.chunks;
+    p.cluster = plan.cluster;
     p.scale_log2 = softmax_scale * kLog2e;
     p.out_f32 = out_dtype == GBATTN_OUT_F32;
     p.e5m2 = kv_dtype == GBATTN_KV_E5M2;

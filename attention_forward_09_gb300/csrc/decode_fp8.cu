@@ -30,7 +30,8 @@
 // equal runs ("chunks"), and CTA (c, h) takes chunk c of KV head (or head
 // group) h, heads fastest, so that CTAs running side by side read neighbouring
 // rows.  A sequence inside one chunk is written out directly; one that crosses
-// chunks leaves fp32 partials (o, lse), which paged_fp8_combine joins.
+// chunks leaves fp32 partials (o, lse), which paged_fp8_combine joins.  Few
+// short sequences take a cluster of CTAs each instead, which join on chip.
 #include <math.h>
 
 #include <mutex>
@@ -43,20 +44,27 @@ namespace gbattn {
 namespace {
 
 constexpr int kTok = 128;      // tokens of a cache block: the MMA's M
-constexpr int kThreads = 192;  // warps 0-3 softmax and output, 4 TMA, 5 MMA
-constexpr int kSoft = 128;
+constexpr int kWg = 128;       // threads of a softmax warpgroup, one a token lane
+constexpr int kMaxCluster = 8; // portable cluster size
 constexpr float kLow = -1e30f;  // a reference below every score, finite so that differences are defined
 constexpr float kLn2f = 0.6931471805599453f;
 
 constexpr int up16(int n) { return (n + 15) / 16 * 16; }
 constexpr int pow2_cols(int n) { return n <= 32 ? 32 : (n <= 64 ? 64 : (n <= 128 ? 128 : (n <= 256 ? 256 : 512))); }
 
+// HG query heads a CTA.  Up to four heads one warpgroup does the softmax; eight
+// are shared by two, four heads each, so that a block's chain of products and
+// softmax stays short.  A last warp loads and issues the products.
 template <int D_, int HG_, int NP_>
 struct Fp8Cfg {
     static constexpr int D = D_, HG = HG_, NP = NP_;
+    static constexpr int NWG = HG > 4 ? 2 : 1;
+    static constexpr int HT = HG / NWG;              // heads a thread
+    static constexpr int SOFT = NWG * kWg;
+    static constexpr int THREADS = SOFT + 32;
     static constexpr int NCH = (D + 127) / 128;      // 128-byte chunks of a row (zero-filled past D)
     static constexpr int NQ = up16(2 * HG);          // columns of S^T: piece * HG + head
-    static constexpr int NW = up16(NP * HG);         // columns of O^T
+    static constexpr int NW = up16(NP * HG);         // columns of O^T: (warpgroup * NP + piece) * HT + head
     static constexpr int HALF_BYTES = NCH * kTok * 128;
     static constexpr int SLOT_BYTES = 2 * HALF_BYTES;
     static constexpr int CTAS = NCH == 1 ? 2 : 1;    // per SM
@@ -66,7 +74,7 @@ struct Fp8Cfg {
     static constexpr int OFF_Q = STAGES * SLOT_BYTES;
     static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
     static constexpr int OFF_SC = OFF_P + P_BYTES;             // exponent bytes: [stage][K, V][128]
-    static constexpr int OFF_RED = OFF_SC + STAGES * 256;      // [2][4][HG] f32
+    static constexpr int OFF_RED = OFF_SC + STAGES * 256;      // [warpgroup][2][4][HT] f32
     static constexpr int OFF_QF = OFF_RED + 2 * 4 * HG * 4;    // [2][HG] f32: 2^f * scale_log2
     static constexpr int OFF_LEN = OFF_QF + 2 * HG * 4;        // valid tokens of each slot's block
     static constexpr int OFF_BAR = (OFF_LEN + STAGES * 4 + 7) & ~7;
@@ -77,6 +85,7 @@ struct Fp8Cfg {
     static constexpr int TM_COLS = pow2_cols(2 * NQ + NCH * NW);
     static_assert(SMEM_BYTES <= (CTAS == 2 ? 115712 : 232448), "shared memory budget");
     static_assert(TM_COLS * CTAS <= 512, "tensor memory budget");
+    static_assert(HG * (D + 1) * 4 <= SLOT_BYTES, "a cluster's partials lie in the first slot");
 };
 
 // Instruction descriptor of kind::f8f6f4, fp32 accumulation: A format in bits
@@ -111,18 +120,31 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// N consecutive 32-bit columns of this warp's lanes.
 template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
-    static_assert(N % 16 == 0, "");
-#pragma unroll
-    for (int i = 0; i < N; i += 16)
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
+    if constexpr (N >= 16) {
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
             "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-            : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]),
-              "=r"(r[i + 6]), "=r"(r[i + 7]), "=r"(r[i + 8]), "=r"(r[i + 9]), "=r"(r[i + 10]), "=r"(r[i + 11]),
-              "=r"(r[i + 12]), "=r"(r[i + 13]), "=r"(r[i + 14]), "=r"(r[i + 15])
-            : "r"(taddr + i));
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+        if constexpr (N > 16) tmem_ld<N - 16>(taddr + 16, r + 16);
+    } else if constexpr (N >= 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+        if constexpr (N > 8) tmem_ld<N - 8>(taddr + 8, r + 8);
+    } else if constexpr (N >= 4) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr));
+        if constexpr (N > 4) tmem_ld<N - 4>(taddr + 4, r + 4);
+    } else {
+        static_assert(N == 2, "");
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
+    }
 }
 
 // OR of a predicate over the `n` threads of barrier `id` (uniform answer).
@@ -139,10 +161,50 @@ __device__ __forceinline__ bool named_bar_or(int id, int n, bool x) {
     return r != 0;
 }
 
-__device__ __forceinline__ float warp_max(float x) {
+__device__ __forceinline__ float warp_max(float x) {  // NaN ignored unless every lane has it
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+
+// The weights of two heads, y <= 256 each, as NP pairs of e4m3 codes, each
+// piece 16 times finer than the one before.  With three pieces (12 bits) the
+// weights go through fp16 (11 bits, its smallest step 2^-32 of the largest
+// weight), whose packed arithmetic halves the work: the differences are exact.
+template <int NP>
+__device__ __forceinline__ void split_pair(float2 y, uint32_t (&c)[NP]) {
+    if constexpr (NP == 3) {
+        uint32_t x;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(y.y), "f"(y.x));
 #pragma unroll
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
+        for (int i = 0; i < NP; ++i) {
+            uint16_t r;
+            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+            c[i] = r;
+            if (i + 1 < NP) {
+                uint32_t f;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(r));
+                asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %0, %1;\n\tmul.rn.f16x2 %0, t, %2;\n\t}"
+                    : "+r"(x)
+                    : "r"(f), "r"(0x4C004C00u));  // 16, 16
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            c[i] = pack_fp8x2<false>(y.x, y.y);
+            if (i + 1 < NP) {
+                const float2 f = unpack_fp8x2<false>(c[i]);
+                y = __fmul2_rn(__fadd2_rn(y, make_float2(-f.x, -f.y)), splat(16.f));
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ int clamp_len(const PagedFp8Params& p, int s) {
@@ -201,63 +263,80 @@ struct Walk {
     }
 };
 
-// The queries of sequence s, heads [h0, h0 + nh), as two e4m3 pieces a value
-// into a buffer of K-major 128-byte swizzled rows, row piece * HG + head; and
-// 2^f * scale_log2 of each head.  One warp a head.  A row with a NaN or an
-// infinity becomes NaN where it has it, so that head's result is NaN.
+// The queries of one sequence: each warpgroup those of its own heads, warp by
+// warp (heads at or past nh are zeros).  Loaded into registers early, laid out later as two e4m3 pieces
+// a value, K-major 128-byte swizzled rows, row piece * HG + head; and 2^f *
+// scale_log2 of each head.  A row with a NaN or an infinity becomes NaN where
+// it has it, so that head's result is NaN.
 template <class C>
-__device__ __forceinline__ void put_queries(const PagedFp8Params& p, int s, int h0, int nh, uint8_t* sq, float* qf,
-                                            int warp, int lane) {
-    constexpr int PAIRS = C::D / 2, PL = (PAIRS + 31) / 32;
-    for (int h = warp; h < C::HG; h += 4) {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + s * p.q_stride + static_cast<long long>(h0 + h) * C::D);
-        uint32_t x[PL];
-        uint32_t mx = 0;
+struct Queries {
+    static constexpr int PAIRS = C::D / 2, PL = (PAIRS + 31) / 32, NHW = (C::HT + 3) / 4;
+    uint32_t x[NHW][PL];
+
+    __device__ __forceinline__ void load(const PagedFp8Params& p, int s, int h0, int nh, int warp, int lane) {
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            const int pr = lane + 32 * i;
-            x[i] = (h < nh && pr < PAIRS) ? src[pr] : 0u;
-            const uint32_t a = x[i] & 0x7FFFu, b = (x[i] >> 16) & 0x7FFFu;
-            if (a < 0x7F80u) mx = max(mx, a);
-            if (b < 0x7F80u) mx = max(mx, b);
+        for (int k = 0; k < NHW; ++k) {
+            const int h = (warp / 4) * C::HT + (warp & 3) + 4 * k;
+            const uint32_t* src =
+                reinterpret_cast<const uint32_t*>(p.q + s * p.q_stride + static_cast<long long>(h0 + h) * C::D);
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                const int pr = lane + 32 * i;
+                x[k][i] = ((warp & 3) + 4 * k < C::HT && h < nh && pr < PAIRS) ? src[pr] : 0u;
+            }
         }
-        mx = __reduce_max_sync(0xffffffffu, mx);
-        int fb = static_cast<int>(mx >> 7) - 8 + ((mx & 0x7Fu) > 0x60u ? 1 : 0);  // as in the cache's rule, c_max = 448
-        fb = fb < 1 ? 1 : fb;
-        const float inv = __uint_as_float(static_cast<uint32_t>(254 - fb) << 23);
-        if (lane == 0) qf[h] = exp2_byte(fb) * p.scale_log2;
+    }
+    __device__ __forceinline__ void put(const PagedFp8Params& p, uint8_t* sq, float* qf, int warp, int lane) const {
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            const int pr = lane + 32 * i;
-            if (pr < PAIRS) {
-                float lo = __uint_as_float(x[i] << 16), hi = __uint_as_float(x[i] & 0xFFFF0000u);
-                if ((x[i] & 0x7F80u) == 0x7F80u) lo = NAN;
-                if ((x[i] & 0x7F800000u) == 0x7F800000u) hi = NAN;
-                lo *= inv;
-                hi *= inv;
-                const uint32_t c0 = pack_fp8x2<false>(lo, hi);
-                const float2 f0 = unpack_fp8x2<false>(c0);
-                const uint32_t c1 = pack_fp8x2<false>((lo - f0.x) * 16.f, (hi - f0.y) * 16.f);
-                const int e = 2 * pr, ch = e >> 7, col = e & 127;
+        for (int k = 0; k < NHW; ++k) {
+            const int h = (warp / 4) * C::HT + (warp & 3) + 4 * k;
+            if ((warp & 3) + 4 * k >= C::HT) break;
+            uint32_t mx = 0;
 #pragma unroll
-                for (int piece = 0; piece < 2; ++piece) {
-                    const int row = piece * C::HG + h;
-                    *reinterpret_cast<uint16_t*>(sq + ch * (C::NQ * 128) + row * 128 + (((col >> 4) ^ (row & 7)) << 4) +
-                                                 (col & 15)) = static_cast<uint16_t>(piece ? c1 : c0);
+            for (int i = 0; i < PL; ++i) {
+                const uint32_t a = x[k][i] & 0x7FFFu, b = (x[k][i] >> 16) & 0x7FFFu;
+                if (a < 0x7F80u) mx = max(mx, a);
+                if (b < 0x7F80u) mx = max(mx, b);
+            }
+            mx = __reduce_max_sync(0xffffffffu, mx);
+            int fb = static_cast<int>(mx >> 7) - 8 + ((mx & 0x7Fu) > 0x60u ? 1 : 0);  // as in the cache's rule, c_max = 448
+            fb = fb < 1 ? 1 : fb;
+            const float inv = __uint_as_float(static_cast<uint32_t>(254 - fb) << 23);
+            if (lane == 0) qf[h] = exp2_byte(fb) * p.scale_log2;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                const int pr = lane + 32 * i;
+                if (pr < PAIRS) {
+                    float lo = __uint_as_float(x[k][i] << 16), hi = __uint_as_float(x[k][i] & 0xFFFF0000u);
+                    if ((x[k][i] & 0x7F80u) == 0x7F80u) lo = NAN;
+                    if ((x[k][i] & 0x7F800000u) == 0x7F800000u) hi = NAN;
+                    lo *= inv;
+                    hi *= inv;
+                    const uint32_t c0 = pack_fp8x2<false>(lo, hi);
+                    const float2 f0 = unpack_fp8x2<false>(c0);
+                    const uint32_t c1 = pack_fp8x2<false>((lo - f0.x) * 16.f, (hi - f0.y) * 16.f);
+                    const int e = 2 * pr, ch = e >> 7, col = e & 127;
+#pragma unroll
+                    for (int piece = 0; piece < 2; ++piece) {
+                        const int row = piece * C::HG + h;
+                        *reinterpret_cast<uint16_t*>(sq + ch * (C::NQ * 128) + row * 128 +
+                                                     (((col >> 4) ^ (row & 7)) << 4) + (col & 15)) =
+                            static_cast<uint16_t>(piece ? c1 : c0);
+                    }
                 }
             }
         }
     }
-}
+};
 
-template <class C>
-__global__ void __launch_bounds__(kThreads, C::CTAS)
+template <class C, bool CLUSTER>
+__global__ void __launch_bounds__(C::THREADS, C::CTAS)
     paged_decode_fp8_sm103a(const __grid_constant__ CUtensorMap tmKV, const PagedFp8Params p) {
-    constexpr int D = C::D, HG = C::HG, NP = C::NP, NQ = C::NQ, NW = C::NW, NCH = C::NCH, STAGES = C::STAGES;
+    constexpr int D = C::D, HG = C::HG, HT = C::HT, NP = C::NP, NQ = C::NQ, NW = C::NW, NCH = C::NCH;
+    constexpr int STAGES = C::STAGES, SOFT_WARPS = C::SOFT / 32, WARPS = C::THREADS / 32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
-    float* sred = reinterpret_cast<float*>(smem + C::OFF_RED);
     float* sqf = reinterpret_cast<float*>(smem + C::OFF_QF);
     volatile int* slen = reinterpret_cast<volatile int*>(smem + C::OFF_LEN);
     const uint32_t bar0 = sb + C::OFF_BAR;
@@ -267,21 +346,37 @@ __global__ void __launch_bounds__(kThreads, C::CTAS)
     auto b_sempty = [&](int i) { return bar0 + 8 * (2 * STAGES + 2 + i); };
     auto b_qfull = [&](int i) { return bar0 + 8 * (2 * STAGES + 4 + i); };
     const uint32_t b_pfull = bar0 + 8 * (2 * STAGES + 6), b_ofull = b_pfull + 8, b_done = b_pfull + 16;
-    __shared__ int abort_storage;
-    __shared__ uint32_t tmem_base_storage;
-    __shared__ long long s_sum[kThreads / 32];
+    __shared__ int abort_storage, s_skip;
+    __shared__ uint32_t tmem_base_storage, s_issued;  // s_issued: blocks whose loads were issued
+    __shared__ long long s_sum[WARPS];
     __shared__ long long s_u[3];  // u0, u1, U
     __shared__ int s_first[2];    // first sequence, first block of it
-    __shared__ uint32_t s_issued; // blocks whose loads were issued
+    __shared__ int2 s_join;       // as PagedFp8Params::joins, of this chunk
+    __shared__ int s_parts;       // of a cluster: the parts its sequence is in, where more than one
     volatile int* abort_flag = &abort_storage;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int chunk = blockIdx.x / p.n_hgroups, hg = blockIdx.x % p.n_hgroups;
+    // a cluster holds the parts of one sequence and head; otherwise heads vary fastest
+    const int chunk = CLUSTER ? blockIdx.x % p.chunks : blockIdx.x / p.n_hgroups;
+    const int hg = CLUSTER ? blockIdx.x / p.chunks % p.n_hgroups : blockIdx.x % p.n_hgroups;
     const int kvh = hg / p.subs, sub = hg % p.subs;
     const int h0 = kvh * p.group + sub * p.heads_per_sub;
     const int nh = min(p.heads_per_sub, p.group - sub * p.heads_per_sub);
     grid_launch_dependents();  // the combine may queue up; it waits for this grid to finish
 
+    // ---- this chunk's units: the total, then the sequence its first unit lies
+    // in.  Lengths are read once where a pass of the block covers them all.
+    const bool one_pass = p.num_seqs <= C::THREADS;
+    const int own = CLUSTER ? blockIdx.x / (p.chunks * p.n_hgroups) : 0;  // a cluster's sequence
+    long long sum = 0;
+    int T = 0;
+    bool bad = false;
+    for (int s = CLUSTER ? own : threadIdx.x; s < (CLUSTER ? own + 1 : p.num_seqs); s += C::THREADS) {
+        const int L = p.seq_lens[s];
+        bad |= L < 0 || L > p.cap;
+        T = blocks_of(L < 0 ? 0 : (L > p.cap ? p.cap : L));
+        sum += T;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(b_full(i), 1);
@@ -289,74 +384,88 @@ __global__ void __launch_bounds__(kThreads, C::CTAS)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_sfull(i), 1);
-            mbar_init(b_sempty(i), 4);
-            mbar_init(b_qfull(i), 4);
+            mbar_init(b_sempty(i), SOFT_WARPS);
+            mbar_init(b_qfull(i), SOFT_WARPS);
         }
-        mbar_init(b_pfull, 4);
+        mbar_init(b_pfull, SOFT_WARPS);
         mbar_init(b_ofull, 1);
         mbar_init(b_done, 1);
         abort_storage = 0;
         s_issued = 0;
+        s_join = make_int2(-1, 0);
+        s_parts = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmKV);
+        s_skip = status_has_timeout(p.status, kDevTimeout);
     }
-    if (warp == 5) {
+    if (warp == SOFT_WARPS) {
         tmem_alloc(smem_u32(&tmem_base_storage), C::TM_COLS);
         tmem_relinquish();
     }
-
-    // ---- this chunk's units: total, then the sequence its first unit lies in
-    {
-        long long sum = 0;
-        bool bad = false;
-        for (int s = threadIdx.x; s < p.num_seqs; s += kThreads) {
-            const int L = p.seq_lens[s];
-            bad |= L < 0 || L > p.cap;
-            sum += blocks_of(clamp_len(p, s));
+    if (bad && (CLUSTER ? threadIdx.x == 0 : blockIdx.x == 0) && p.status) atomicOr(p.status, kDevBadSeqlen);
+    if constexpr (CLUSTER) {
+        if (threadIdx.x == 0) {
+            const long long N = T < p.chunks ? T : p.chunks;
+            const long long u0 = chunk_start(chunk, T, N);
+            s_u[0] = u0;
+            s_u[1] = s_skip ? u0 : chunk_start(chunk + 1, T, N);
+            s_u[2] = T;
+            s_first[0] = own;
+            s_first[1] = static_cast<int>(u0);
+            s_parts = N > 1 ? static_cast<int>(N) : 0;
         }
-        if (bad && blockIdx.x == 0 && p.status) atomicOr(p.status, kDevBadSeqlen);
+    } else {
+        long long incl = sum;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) s_sum[warp] = sum;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long n = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += n;
+        }
+        if (lane == 31) s_sum[warp] = incl;
         __syncthreads();
-        long long U = 0;
+        long long U = 0, before = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) U += s_sum[w];
-        __syncthreads();
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) before += s_sum[w];
+            U += s_sum[w];
+        }
         const long long N = U < p.chunks ? U : p.chunks;
         const long long u0 = chunk_start(chunk, U, N), u1 = chunk_start(chunk + 1, U, N);
         if (threadIdx.x == 0) {
             s_u[0] = u0;
-            s_u[1] = status_has_timeout(p.status, kDevTimeout) ? u0 : u1;  // after a give-up nothing more is begun
+            s_u[1] = s_skip ? u0 : u1;  // after a give-up nothing more is begun
             s_u[2] = U;
         }
-        long long run = 0;
-        if (u1 > u0) {
-            for (int base = 0; base < p.num_seqs; base += kThreads) {
+        if (one_pass) {
+            const long long at = before + incl - T;  // units before sequence threadIdx.x
+            if (T > 0 && at <= u0 && u0 < at + T) {
+                s_first[0] = threadIdx.x;
+                s_first[1] = static_cast<int>(u0 - at);
+            }
+        } else if (u1 > u0) {
+            long long run = 0;
+            for (int base = 0; base < p.num_seqs && run <= u0; base += C::THREADS) {  // run <= u0: not found yet (uniform)
                 const int s = base + threadIdx.x;
-                const int T = s < p.num_seqs ? blocks_of(clamp_len(p, s)) : 0;
-                long long incl = T;
+                T = s < p.num_seqs ? blocks_of(clamp_len(p, s)) : 0;
+                incl = T;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const long long n = __shfl_up_sync(0xffffffffu, incl, o);
                     if (lane >= o) incl += n;
                 }
+                __syncthreads();  // s_sum was read by all
                 if (lane == 31) s_sum[warp] = incl;
                 __syncthreads();
-                long long before = run, all = 0;
+                long long at = run + incl - T;
 #pragma unroll
-                for (int w = 0; w < kThreads / 32; ++w) {
-                    if (w < warp) before += s_sum[w];
-                    all += s_sum[w];
+                for (int w = 0; w < WARPS; ++w) {
+                    if (w < warp) at += s_sum[w];
+                    run += s_sum[w];
                 }
-                const long long at = before + incl - T;  // units before sequence s
                 if (T > 0 && at <= u0 && u0 < at + T) {
                     s_first[0] = s;
                     s_first[1] = static_cast<int>(u0 - at);
                 }
-                run += all;
-                __syncthreads();
-                if (run > u0) break;  // found (uniform)
             }
         }
     }
@@ -364,27 +473,34 @@ __global__ void __launch_bounds__(kThreads, C::CTAS)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_base_storage;
-    const long long u0 = s_u[0], u1 = s_u[1], U = s_u[2];
-    const uint32_t n_units = static_cast<uint32_t>(u1 - u0);
+    const long long u1 = s_u[1], U = s_u[2];
+    const uint32_t n_units = static_cast<uint32_t>(u1 - s_u[0]);
     bool ok = true;
 
-    if (warp < 4) {
+    if (warp < SOFT_WARPS) {
         // ---------------------------------------------------- softmax and output
-        if (hg == 0 && threadIdx.x == 0 && p.chunks > 1 && n_units == 0) p.joins[chunk] = make_int2(-1, 0);
+        const int wg = warp / 4, tok = threadIdx.x % kWg;
+        const int hw = wg * HT;  // this warpgroup's first head
+        float* sred = reinterpret_cast<float*>(smem + C::OFF_RED) + wg * 2 * 4 * HT;
         // sequences without context, of this chunk's share: zeros and -inf
+        auto zero_row = [&](long long s) {  // one warp
+            const long long row = s * p.Hq + h0;
+            for (int i = lane; i < nh * D; i += 32) {
+                if (p.out_f32)
+                    static_cast<float*>(p.out)[row * D + i] = 0.f;
+                else
+                    static_cast<uint16_t*>(p.out)[row * D + i] = 0;
+            }
+            if (lane < nh && p.lse) p.lse[row + lane] = -INFINITY;
+        };
         auto zero_empty = [&]() {
-            for (long long i0 = warp * 32; i0 * p.chunks < p.num_seqs; i0 += kSoft) {
-                const long long s = chunk + (i0 + lane) * p.chunks;
-                unsigned none = __ballot_sync(0xffffffffu, s < p.num_seqs && clamp_len(p, static_cast<int>(s)) == 0);
-                for (; none; none &= none - 1) {
-                    const long long row = (chunk + (i0 + __ffs(static_cast<int>(none)) - 1) * p.chunks) * p.Hq + h0;
-                    for (int i = lane; i < nh * D; i += 32) {
-                        if (p.out_f32)
-                            static_cast<float*>(p.out)[row * D + i] = 0.f;
-                        else
-                            static_cast<uint16_t*>(p.out)[row * D + i] = 0;
-                    }
-                    if (lane < nh && p.lse) p.lse[row + lane] = -INFINITY;
+            if constexpr (CLUSTER) {
+                if (U == 0 && chunk == 0 && warp == 0) zero_row(own);
+            } else {
+                for (long long i0 = warp * 32; i0 * p.chunks < p.num_seqs; i0 += C::SOFT) {
+                    const long long s = chunk + (i0 + lane) * p.chunks;
+                    unsigned none = __ballot_sync(0xffffffffu, s < p.num_seqs && clamp_len(p, static_cast<int>(s)) == 0);
+                    for (; none; none &= none - 1) zero_row(chunk + (i0 + __ffs(static_cast<int>(none)) - 1) * p.chunks);
                 }
             }
         };
@@ -393,397 +509,459 @@ __global__ void __launch_bounds__(kThreads, C::CTAS)
             Walk w, ahead;  // `ahead` is one segment further: its queries are laid out early
             w.start(p, s_first[0], s_first[1], n_units);
             ahead = w;
-            put_queries<C>(p, w.s, h0, nh, smem + C::OFF_Q, sqf, warp, lane);
+            Queries<C> qs;
+            qs.load(p, w.s, h0, nh, warp, lane);
+            zero_empty();  // while they come
+            qs.put(p, smem + C::OFF_Q, sqf, warp, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(b_qfull(0));
-            named_bar_sync(1, kSoft);  // sqf is read by every warp
-            zero_empty();
-            const uint32_t tlane = static_cast<uint32_t>(warp) << 21;  // this warp's 32 TMEM lanes
+            named_bar_sync(1 + wg, kWg);  // sqf is read by the warpgroup's four warps
+            const uint32_t tlane = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 TMEM lanes
             uint32_t g = 0;  // blocks done
             int seg = 0;
             bool more = true;
             while (more) {
-                if (ahead.next(p)) {  // queries of the next segment: its buffer's last reader was segment seg - 1
-                    put_queries<C>(p, ahead.s, h0, nh, smem + C::OFF_Q + ((seg + 1) & 1) * C::Q_BYTES,
-                                   sqf + ((seg + 1) & 1) * HG, warp, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(b_qfull((seg + 1) & 1));
-                }
-                float o[NCH][HG], R[HG], Mp[HG], mref[HG], l[HG];
+                // queries of the next segment: asked for now, laid out after this
+                // segment's first block (its buffer's last reader was segment seg - 1)
+                const bool has_next = ahead.next(p);
+                if (has_next) qs.load(p, ahead.s, h0, nh, warp, lane);
+                float2 o[NCH][HT / 2], R[HT / 2], M8[HT / 2], mref[HT / 2], l[HT / 2];
 #pragma unroll
-                for (int h = 0; h < HG; ++h) {
-                    R[h] = mref[h] = Mp[h] = kLow;
-                    l[h] = 0.f;
+                for (int h = 0; h < HT / 2; ++h) {
+                    R[h] = mref[h] = M8[h] = splat(kLow);
+                    l[h] = splat(0.f);
 #pragma unroll
-                    for (int c = 0; c < NCH; ++c) o[c][h] = 0.f;
+                    for (int c = 0; c < NCH; ++c) o[c][h] = splat(0.f);
                 }
-                // O^T of the block before: o += 2^(M - R - 8) sum_i piece_i / 16^i
+                // O^T of the block before: o += 2^(M - 8 - R) sum_i piece_i / 16^i
                 auto add_o = [&](uint32_t gi) {
                     if (!mbar_wait(b_ofull, gi & 1, abort_flag)) ok = false;
                     tc_fence_after();
-                    float beta[HG];
+                    uint32_t r[NCH][NP * HT];
 #pragma unroll
-                    for (int h = 0; h < HG; ++h) {
-                        if (Mp[h] > R[h] + 40.f) {  // same in every thread
-                            const float a = ex2(R[h] - Mp[h]);
-                            R[h] = Mp[h];
+                    for (int c = 0; c < NCH; ++c) tmem_ld<NP * HT>(tm + tlane + C::TM_O + c * NW + wg * NP * HT, r[c]);
+                    float2 beta[HT / 2];
 #pragma unroll
-                            for (int c = 0; c < NCH; ++c) o[c][h] *= a;
+                    for (int h = 0; h < HT / 2; ++h) {
+                        if (M8[h].x > R[h].x + 40.f || M8[h].y > R[h].y + 40.f) {  // same in every thread
+                            const float2 n = make_float2(fmaxf(R[h].x, M8[h].x), fmaxf(R[h].y, M8[h].y));
+                            const float2 a = make_float2(ex2(R[h].x - n.x), ex2(R[h].y - n.y));
+                            R[h] = n;
+#pragma unroll
+                            for (int c = 0; c < NCH; ++c) o[c][h] = __fmul2_rn(o[c][h], a);
                         }
-                        beta[h] = ex2(Mp[h] - R[h] - 8.f);
+                        beta[h] = make_float2(ex2(M8[h].x - R[h].x), ex2(M8[h].y - R[h].y));
                     }
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < NCH; ++c) {
-                        uint32_t r[NW];
-                        tmem_ld<NW>(tm + tlane + C::TM_O + c * NW, r);
-                        tmem_wait_ld();
+                    for (int c = 0; c < NCH; ++c)
 #pragma unroll
-                        for (int h = 0; h < HG; ++h) {
-                            float x = __uint_as_float(r[(NP - 1) * HG + h]);
+                        for (int h = 0; h < HT / 2; ++h) {
+                            auto piece = [&](int i) {
+                                return make_float2(__uint_as_float(r[c][i * HT + 2 * h]), __uint_as_float(r[c][i * HT + 2 * h + 1]));
+                            };
+                            float2 x = piece(NP - 1);
 #pragma unroll
-                            for (int i = NP - 2; i >= 0; --i) x = fmaf(x, 0.0625f, __uint_as_float(r[i * HG + h]));
-                            o[c][h] = fmaf(x, beta[h], o[c][h]);
+                            for (int i = NP - 2; i >= 0; --i) x = __ffma2_rn(x, splat(0.0625f), piece(i));
+                            o[c][h] = __ffma2_rn(x, beta[h], o[c][h]);
                         }
-                    }
                     tc_fence_before();
                 };
-                const float* qf = sqf + (seg & 1) * HG;
+                const float2* qf = reinterpret_cast<const float2*>(sqf + (seg & 1) * HG + hw);
                 bool quit = false;
                 for (int b = w.b0; b < w.b1; ++b, ++g) {
                     const int slot = static_cast<int>(g % STAGES);
                     if (!mbar_wait(b_full(slot), (g / STAGES) & 1, abort_flag)) ok = false;
                     if (!mbar_wait(b_sfull(g & 1), (g >> 1) & 1, abort_flag)) ok = false;
                     tc_fence_after();
-                    uint32_t r[NQ];
-                    tmem_ld<NQ>(tm + tlane + C::TM_S + (g & 1) * NQ, r);
+                    uint32_t r0[HT], r1[HT];
+                    tmem_ld<HT>(tm + tlane + C::TM_S + (g & 1) * NQ + hw, r0);
+                    tmem_ld<HT>(tm + tlane + C::TM_S + (g & 1) * NQ + HG + hw, r1);
                     const int nvalid = slen[slot];
-                    const bool valid = static_cast<int>(threadIdx.x) < nvalid;
+                    const bool valid = tok < nvalid;
                     const uint8_t* sc = smem + C::OFF_SC + slot * 256;
-                    const float kf = exp2_byte(sc[threadIdx.x]);
-                    const float ev = static_cast<float>(static_cast<int>(sc[128 + threadIdx.x]) - 127);
+                    const float kf = exp2_byte(sc[tok]);
+                    const float ev = static_cast<float>(static_cast<int>(sc[128 + tok]) - 127);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(b_sempty(g & 1));
-                    float u[HG];
+                    float2 u[HT / 2], d[HT / 2];
+                    float dmax = kLow;
 #pragma unroll
-                    for (int h = 0; h < HG; ++h) {
-                        const float dot = fmaf(__uint_as_float(r[HG + h]), 0.0625f, __uint_as_float(r[h]));
-                        const float s = dot * kf * qf[h];
-                        if (valid) {
-                            if (s > mref[h] + 60.f) {  // fp32 has room for sums of 2^60 and more
-                                l[h] *= ex2(mref[h] - s);
-                                mref[h] = s;
-                            }
-                            l[h] += ex2(s - mref[h]);
+                    for (int h = 0; h < HT / 2; ++h) {
+                        const float2 dot =
+                            __ffma2_rn(make_float2(__uint_as_float(r1[2 * h]), __uint_as_float(r1[2 * h + 1])), splat(0.0625f),
+                                       make_float2(__uint_as_float(r0[2 * h]), __uint_as_float(r0[2 * h + 1])));
+                        u[h] = __fmul2_rn(__fmul2_rn(dot, splat(kf)), qf[h]);
+                        if (nvalid < kTok) u[h] = valid ? u[h] : splat(-INFINITY);
+                        d[h] = __fadd2_rn(u[h], make_float2(-mref[h].x, -mref[h].y));
+                        dmax = fmax3(dmax, d[h].x, d[h].y);
+                    }
+                    if (dmax > 60.f) {  // rarely: fp32 has room for sums of 2^60 and more
+#pragma unroll
+                        for (int h = 0; h < HT / 2; ++h) {
+                            const float2 m = make_float2(d[h].x > 60.f ? u[h].x : mref[h].x, d[h].y > 60.f ? u[h].y : mref[h].y);
+                            l[h] = make_float2(l[h].x * ex2(mref[h].x - m.x), l[h].y * ex2(mref[h].y - m.y));
+                            mref[h] = m;
+                            d[h] = make_float2(u[h].x - m.x, u[h].y - m.y);
                         }
-                        u[h] = valid ? s + ev : -INFINITY;
                     }
-                    float* red = sred + (g & 1) * 4 * HG;
+                    float m[HT];
 #pragma unroll
-                    for (int h = 0; h < HG; ++h) {
-                        const float m = warp_max(u[h]);
-                        if (lane == 0) red[warp * HG + h] = m;
+                    for (int h = 0; h < HT / 2; ++h) {
+                        l[h] = __fadd2_rn(l[h], make_float2(ex2(d[h].x), ex2(d[h].y)));
+                        u[h] = __fadd2_rn(u[h], splat(ev));
+                        m[2 * h] = warp_max(u[h].x);
+                        m[2 * h + 1] = warp_max(u[h].y);
                     }
-                    if (named_bar_or(1, kSoft, !ok)) {  // all four warps leave together
+                    float* red = sred + (g & 1) * 4 * HT;
+                    if (lane == 0) {
+#pragma unroll
+                        for (int h = 0; h < HT; h += 2) *reinterpret_cast<float2*>(red + (warp & 3) * HT + h) = make_float2(m[h], m[h + 1]);
+                    }
+                    if (named_bar_or(1 + wg, kWg, !ok)) {  // a warpgroup's four warps leave together
                         quit = true;
                         break;
                     }
                     // the value rows past the context meet weight 0: they must be finite
-                    if (!valid) {
+                    if (!valid && wg == 0) {
 #pragma unroll
                         for (int c = 0; c < NCH; ++c) {
-                            uint4* v = reinterpret_cast<uint4*>(smem + slot * C::SLOT_BYTES + C::HALF_BYTES + c * kTok * 128 +
-                                                                threadIdx.x * 128);
+                            uint4* v = reinterpret_cast<uint4*>(smem + slot * C::SLOT_BYTES + C::HALF_BYTES + c * kTok * 128 + tok * 128);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                     if (b > w.b0) add_o(g - 1);  // the weights' buffer and O^T are free again
-                    float y[NP * HG];
+                    // weights 256 w = 2^(u - M + 8) and their pieces
+                    constexpr int WORDS = (NP * HT + 3) / 4;
+                    uint32_t w8[WORDS];
 #pragma unroll
-                    for (int h = 0; h < HG; ++h) {
-                        const float M = fmaxf(fmaxf(fmaxf(red[h], red[HG + h]), fmaxf(red[2 * HG + h], red[3 * HG + h])), kLow);
-                        Mp[h] = M;
-                        y[h] = ex2(u[h] - M + 8.f);
-                    }
-                    // pieces, lowest column first: column piece * HG + head
-                    uint32_t w8[NW / 4];
+                    for (int i = 0; i < WORDS; ++i) w8[i] = 0u;
 #pragma unroll
-                    for (int i = 0; i < NW / 4; ++i) w8[i] = 0u;
-                    if constexpr (HG == 1) {
-                        float x = y[0];
+                    for (int h = 0; h < HT / 2; ++h) {
+                        const float2* rm = reinterpret_cast<const float2*>(red) + h;
+                        const float2 a = rm[0], b2 = rm[HT / 2], c2 = rm[HT], d2 = rm[3 * HT / 2];
+                        M8[h] = make_float2(fmaxf(fmax3(a.x, b2.x, c2.x), fmaxf(d2.x, kLow)) - 8.f,
+                                            fmaxf(fmax3(a.y, b2.y, c2.y), fmaxf(d2.y, kLow)) - 8.f);
+                        const float2 e = __fadd2_rn(u[h], make_float2(-M8[h].x, -M8[h].y));
+                        uint32_t c[NP];
+                        split_pair<NP>(make_float2(ex2(e.x), ex2(e.y)), c);
 #pragma unroll
                         for (int i = 0; i < NP; ++i) {
-                            const uint32_t c = pack_fp8x2<false>(x, 0.f);
-                            w8[0] |= (c & 0xFFu) << (8 * i);
-                            x = (x - unpack_fp8x2<false>(c).x) * 16.f;
-                        }
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < HG; h += 2) {
-                            float x0 = y[h], x1 = y[h + 1];
-#pragma unroll
-                            for (int i = 0; i < NP; ++i) {
-                                const uint32_t c = pack_fp8x2<false>(x0, x1);
-                                const int col = i * HG + h;
-                                w8[col / 4] |= c << (8 * (col & 3));
-                                if (i + 1 < NP) {
-                                    const float2 f = unpack_fp8x2<false>(c);
-                                    x0 = (x0 - f.x) * 16.f;
-                                    x1 = (x1 - f.y) * 16.f;
-                                }
-                            }
+                            const int col = i * HT + 2 * h;
+                            w8[col / 4] |= c[i] << (8 * (col & 3));
                         }
                     }
+                    // column j of token t at (j / 16) * 2048 + t * 16 + j % 16
 #pragma unroll
-                    for (int i = 0; i < NW / 16; ++i)
-                        st_shared_v4(sb + C::OFF_P + i * (kTok * 16) + threadIdx.x * 16, w8[4 * i], w8[4 * i + 1],
-                                     w8[4 * i + 2], w8[4 * i + 3]);
+                    for (int i = 0; i < WORDS; ++i) {
+                        const int col = wg * NP * HT + 4 * i;
+                        *reinterpret_cast<uint32_t*>(smem + C::OFF_P + (col / 16) * (kTok * 16) + tok * 16 + (col % 16)) = w8[i];
+                    }
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(b_pfull);
+                    if (has_next && b == w.b0) {
+                        qs.put(p, smem + C::OFF_Q + ((seg + 1) & 1) * C::Q_BYTES, sqf + ((seg + 1) & 1) * HG, warp, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_qfull((seg + 1) & 1));
+                    }
                 }
                 if (quit) break;
                 add_o(g - 1);
                 // ---- the segment's softmax sum over the 128 token lanes, then its output
-                float inv[HG], lse2[HG];
+                float inv[HT], lse2[HT];
 #pragma unroll
-                for (int h = 0; h < HG; ++h) {
-                    const float m = warp_max(mref[h]);
-                    if (lane == 0) sred[warp * HG + h] = m;
+                for (int h = 0; h < HT; ++h) {
+                    const float m = warp_max(h & 1 ? mref[h / 2].y : mref[h / 2].x);
+                    if (lane == 0) sred[(warp & 3) * HT + h] = m;
                 }
-                named_bar_sync(1, kSoft);
+                named_bar_sync(1 + wg, kWg);
+                float mall[HT];
 #pragma unroll
-                for (int h = 0; h < HG; ++h) {
-                    const float m = fmaxf(fmaxf(sred[h], sred[HG + h]), fmaxf(sred[2 * HG + h], sred[3 * HG + h]));
-                    float x = l[h] * ex2(mref[h] - m);
+                for (int h = 0; h < HT; ++h) {
+                    const float m = fmaxf(fmaxf(sred[h], sred[HT + h]), fmaxf(sred[2 * HT + h], sred[3 * HT + h]));
+                    float x = h & 1 ? l[h / 2].y * ex2(mref[h / 2].y - m) : l[h / 2].x * ex2(mref[h / 2].x - m);
 #pragma unroll
                     for (int of = 16; of; of >>= 1) x += __shfl_xor_sync(0xffffffffu, x, of);
-                    if (lane == 0) sred[4 * HG + warp * HG + h] = x;
-                    mref[h] = m;
+                    if (lane == 0) sred[4 * HT + (warp & 3) * HT + h] = x;
+                    mall[h] = m;
                 }
-                if (named_bar_or(1, kSoft, !ok)) break;
+                if (named_bar_or(1 + wg, kWg, !ok)) break;
 #pragma unroll
-                for (int h = 0; h < HG; ++h) {
-                    const float* x = sred + 4 * HG + h;
-                    const float sum = (x[0] + x[HG]) + (x[2 * HG] + x[3 * HG]);
-                    inv[h] = sum == 0.f ? 0.f : ex2(R[h] - mref[h]) / sum;
-                    lse2[h] = sum == 0.f ? -INFINITY : mref[h] + __log2f(sum);
+                for (int h = 0; h < HT; ++h) {
+                    const float* x = sred + 4 * HT + h;
+                    const float all = (x[0] + x[HT]) + (x[2 * HT] + x[3 * HT]);
+                    inv[h] = all == 0.f ? 0.f : ex2((h & 1 ? R[h / 2].y : R[h / 2].x) - mall[h]) / all;
+                    lse2[h] = all == 0.f ? -INFINITY : mall[h] + __log2f(all);
                 }
                 const bool whole = w.b0 == 0 && w.b1 == w.nblk;
-                if (hg == 0 && threadIdx.x == 0 && p.chunks > 1 && w.rem == 0) {
-                    // does this segment's sequence begin here and go on in other chunks?
-                    const long long end = u1 + (w.nblk - w.b1);
-                    const bool begins = w.b0 == 0 && w.b1 < w.nblk;
-                    const long long N = U < p.chunks ? U : p.chunks;
-                    p.joins[chunk] = begins ? make_int2(w.s, static_cast<int>((end * N + U - 1) / U - 1))
-                                            : make_int2(-1, 0);
+                if (!CLUSTER && threadIdx.x == 0 && w.b0 == 0 && w.b1 < w.nblk) {
+                    // this segment's sequence begins here and goes on: up to the chunk of its last unit
+                    const long long N = U < p.chunks ? U : p.chunks, end = u1 + (w.nblk - w.b1);
+                    s_join = make_int2(w.s, static_cast<int>((end * N + U - 1) / U - 1));
                 }
+                // Partials: in the workspace, slot 1 where the sequence begins and slot 0
+                // where it goes on; or, of a cluster, in the first slot of the ring, which
+                // nothing reads or fills any more (a cluster's CTA has one segment).
                 const long long part = (static_cast<long long>(chunk) * 2 + (w.b0 == 0 ? 1 : 0)) * p.Hq + h0;
+                float* po = CLUSTER ? reinterpret_cast<float*>(smem) : p.part_o + part * D;
+                float* pl = CLUSTER ? reinterpret_cast<float*>(smem) + HG * D : p.part_lse + part;
                 const long long row = static_cast<long long>(w.s) * p.Hq + h0;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
-                    const int d = c * 128 + threadIdx.x;
+                    const int d = c * 128 + tok;
                     if (d < D) {
 #pragma unroll
-                        for (int h = 0; h < HG; ++h)
+                        for (int k = 0; k < HT; ++k) {
+                            const int h = hw + k;
                             if (h < nh) {
-                                const float x = o[c][h] * inv[h];
+                                const float x = (k & 1 ? o[c][k / 2].y : o[c][k / 2].x) * inv[k];
                                 if (!whole)
-                                    p.part_o[(part + h) * D + d] = x;
+                                    po[h * D + d] = x;
                                 else if (p.out_f32)
                                     static_cast<float*>(p.out)[(row + h) * D + d] = x;
                                 else
                                     static_cast<uint16_t*>(p.out)[(row + h) * D + d] =
                                         static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xFFFFu);
                             }
+                        }
                     }
                 }
-                if (threadIdx.x == 0) {
+                if (tok == 0) {
 #pragma unroll
-                    for (int h = 0; h < HG; ++h)
+                    for (int k = 0; k < HT; ++k) {
+                        const int h = hw + k;
                         if (h < nh) {
                             if (!whole)
-                                p.part_lse[part + h] = lse2[h];
+                                pl[h] = lse2[k];
                             else if (p.lse)
-                                p.lse[row + h] = lse2[h] * kLn2f;
+                                p.lse[row + h] = lse2[k] * kLn2f;
                         }
+                    }
                 }
                 ++seg;
                 more = w.next(p);
-                named_bar_sync(1, kSoft);  // the reduction scratch is free again
+                if (more) named_bar_sync(1 + wg, kWg);  // the reduction scratch is free again
             }
         }
-    } else if (warp == 4) {
-        // ---------------------------------------------------- cache loads
-        if (n_units > 0) {
-            Walk w;
-            w.start(p, s_first[0], s_first[1], n_units);
-            uint32_t g = 0;
-            bool more = true;
-            while (more && ok) {
-                const int32_t* row = p.block_table + static_cast<long long>(w.s) * p.max_blocks;
-                int ids = 0;  // 32 table entries, one a lane
-                for (int b = w.b0; b < w.b1; ++b, ++g) {
-                    const int slot = static_cast<int>(g % STAGES);
-                    const int at = (b - w.b0) & 31;
-                    if (at == 0) ids = b + lane < w.b1 ? row[b + lane] : 0;
-                    const int blk = __shfl_sync(0xffffffffu, ids, at);
-                    if (g >= STAGES && !mbar_wait(b_empty(slot), (g / STAGES - 1) & 1, abort_flag)) ok = false;
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (elect_one()) {
-                        const bool good = blk >= 0 && blk < p.num_blocks;
-                        slen[slot] = good ? min(kTok, w.L - b * kTok) : 0;
-                        if (good) {
-                            mbar_arrive_expect_tx(b_full(slot), C::SLOT_BYTES + 256);
+        if (!ok) *abort_flag = 1;
+    } else if (n_units > 0) {
+        // ---------------------------------------------------- loads and products
+        // Per unit i: unit i - 1's product with V is done, so its slot takes unit
+        // i - 1 + STAGES; S^T of unit i + 1 is issued; then, once the weights of
+        // unit i are there, its product with V.
+        const uint32_t id_s = idesc_f8(128, NQ, p.e5m2 ? 1u : 0u, false, false);
+        const uint32_t id_o = idesc_f8(128, NW, p.e5m2 ? 1u : 0u, true, true);
+        Walk wl, w;  // of the loads, of the products
+        wl.start(p, s_first[0], s_first[1], n_units);
+        w = wl;
+        uint32_t loaded = 0;
+        int lb = wl.b0, ids = 0, seg = 0, b = w.b0;
+        auto load = [&]() {  // the next unit, into its (free) slot
+            const int slot = static_cast<int>(loaded % STAGES);
+            const int at = (lb - wl.b0) & 31;  // 32 table entries are held, one a lane
+            if (at == 0) ids = lb + lane < wl.b1 ? p.block_table[static_cast<long long>(wl.s) * p.max_blocks + lb + lane] : 0;
+            const int blk = __shfl_sync(0xffffffffu, ids, at);
+            if (elect_one()) {
+                const bool good = blk >= 0 && blk < p.num_blocks;
+                slen[slot] = good ? min(kTok, wl.L - lb * kTok) : 0;
+                if (good) {
+                    mbar_arrive_expect_tx(b_full(slot), C::SLOT_BYTES + 256);
 #pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const long long r = static_cast<long long>(half) * p.num_blocks + blk;
+                    for (int half = 0; half < 2; ++half) {
+                        const long long r = static_cast<long long>(half) * p.num_blocks + blk;
 #pragma unroll
-                                for (int c = 0; c < NCH; ++c)
-                                    tma_load_3d(sb + slot * C::SLOT_BYTES + half * C::HALF_BYTES + c * kTok * 128, &tmKV,
-                                                b_full(slot), c * 128, kvh, static_cast<int>(r * kTok));
-                                bulk_load(sb + C::OFF_SC + slot * 256 + half * 128, p.scales + (r * p.Hkv + kvh) * kTok, 128,
-                                          b_full(slot));
-                            }
-                        } else {
-                            if (p.status) atomicOr(p.status, kDevBadIndex);
-                            mbar_arrive(b_full(slot));
-                        }
-                        s_issued = g + 1;
+                        for (int c = 0; c < NCH; ++c)
+                            tma_load_3d(sb + slot * C::SLOT_BYTES + half * C::HALF_BYTES + c * kTok * 128, &tmKV, b_full(slot),
+                                        c * 128, kvh, static_cast<int>(r * kTok));
+                        bulk_load(sb + C::OFF_SC + slot * 256 + half * 128, p.scales + (r * p.Hkv + kvh) * kTok, 128, b_full(slot));
                     }
-                    __syncwarp();
+                } else {
+                    if (p.status) atomicOr(p.status, kDevBadIndex);
+                    mbar_arrive(b_full(slot));
                 }
-                if (ok) more = w.next(p);
+                s_issued = loaded + 1;
             }
-            if (!ok) *abort_flag = 1;
-        }
-    } else {
-        // ---------------------------------------------------- matrix products
-        if (n_units > 0) {
-            const uint32_t id_s = idesc_f8(128, NQ, p.e5m2 ? 1u : 0u, false, false);
-            const uint32_t id_o = idesc_f8(128, NW, p.e5m2 ? 1u : 0u, true, true);
-            Walk w;
-            w.start(p, s_first[0], s_first[1], n_units);
-            int seg = 0, b = w.b0;
-            bool more = true;
-            // S^T of unit i, one unit ahead of O^T
-            auto issue_s = [&](uint32_t i) {
-                const int slot = static_cast<int>(i % STAGES);
-                bool got = mbar_wait(b_full(slot), (i / STAGES) & 1, abort_flag);
-                if (b == w.b0) got = got && mbar_wait(b_qfull(seg & 1), (seg >> 1) & 1, abort_flag);
-                if (i >= 2) got = got && mbar_wait(b_sempty(i & 1), ((i >> 1) - 1) & 1, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) return false;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t k = sb + slot * C::SLOT_BYTES, q = sb + C::OFF_Q + (seg & 1) * C::Q_BYTES;
-#pragma unroll
-                    for (int ks = 0; ks < D / 32; ++ks)
-                        mma_f8_ss(tm + C::TM_S + (i & 1) * NQ,
-                                  sdesc_sw128(k + (ks / 4) * (kTok * 128) + (ks % 4) * 32, 16, 1024),
-                                  sdesc_sw128(q + (ks / 4) * (NQ * 128) + (ks % 4) * 32, 16, 1024), id_s, ks > 0);
-                    mma_commit(b_sfull(i & 1));
-                }
-                __syncwarp();
-                if (++b == w.b1) {
-                    more = w.next(p);
-                    b = w.b0;
-                    ++seg;
-                }
-                return true;
-            };
-            ok = issue_s(0);
-            for (uint32_t i = 0; ok && i < n_units; ++i) {
-                ok = !more || issue_s(i + 1);
-                const int slot = static_cast<int>(i % STAGES);
-                ok = __all_sync(0xffffffffu, ok && mbar_wait(b_pfull, i & 1, abort_flag));
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t v = sb + slot * C::SLOT_BYTES + C::HALF_BYTES, pp = sb + C::OFF_P;
-#pragma unroll
-                    for (int c = 0; c < NCH; ++c)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f8_ss(tm + C::TM_O + c * NW, sdesc_sw128(v + c * (kTok * 128) + ks * 4096, 16, 1024),
-                                      sdesc_plain(pp + ks * 512, 128, kTok * 16), id_o, ks > 0);
-                    mma_commit(b_ofull);
-                    mma_commit(b_empty(slot));
-                }
-                __syncwarp();
-            }
-            if (!ok) *abort_flag = 1;
-            if (elect_one()) mma_commit(b_done);  // every product issued has finished before TMEM is freed
             __syncwarp();
-            mbar_wait_drain(b_done, 0);
+            ++loaded;
+            if (++lb == wl.b1 && loaded < n_units) {
+                wl.next(p);
+                lb = wl.b0;
+            }
+        };
+        auto issue_s = [&](uint32_t i) {
+            const int slot = static_cast<int>(i % STAGES);
+            bool got = mbar_wait(b_full(slot), (i / STAGES) & 1, abort_flag);
+            if (b == w.b0) got = got && mbar_wait(b_qfull(seg & 1), (seg >> 1) & 1, abort_flag);
+            if (i >= 2) got = got && mbar_wait(b_sempty(i & 1), ((i >> 1) - 1) & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t k = sb + slot * C::SLOT_BYTES, q = sb + C::OFF_Q + (seg & 1) * C::Q_BYTES;
+#pragma unroll
+                for (int ks = 0; ks < D / 32; ++ks)
+                    mma_f8_ss(tm + C::TM_S + (i & 1) * NQ, sdesc_sw128(k + (ks / 4) * (kTok * 128) + (ks % 4) * 32, 16, 1024),
+                              sdesc_sw128(q + (ks / 4) * (NQ * 128) + (ks % 4) * 32, 16, 1024), id_s, ks > 0);
+                mma_commit(b_sfull(i & 1));
+            }
+            __syncwarp();
+            if (++b == w.b1 && i + 1 < n_units) {
+                w.next(p);
+                b = w.b0;
+                ++seg;
+            }
+            return true;
+        };
+        while (loaded < STAGES && loaded < n_units) load();
+        ok = issue_s(0);
+        for (uint32_t i = 0; ok && i < n_units; ++i) {
+            if (i > 0 && loaded < n_units) {
+                ok = __all_sync(0xffffffffu, mbar_wait(b_empty((i - 1) % STAGES), ((i - 1) / STAGES) & 1, abort_flag));
+                if (!ok) break;
+                load();
+            }
+            if (i + 1 < n_units) ok = issue_s(i + 1);
+            const int slot = static_cast<int>(i % STAGES);
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(b_pfull, i & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t v = sb + slot * C::SLOT_BYTES + C::HALF_BYTES, pp = sb + C::OFF_P;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f8_ss(tm + C::TM_O + c * NW, sdesc_sw128(v + c * (kTok * 128) + ks * 4096, 16, 1024),
+                                  sdesc_plain(pp + ks * 512, 128, kTok * 16), id_o, ks > 0);
+                mma_commit(b_ofull);
+                mma_commit(b_empty(slot));
+            }
+            __syncwarp();
         }
+        if (!ok) *abort_flag = 1;
+        if (elect_one()) mma_commit(b_done);  // every product issued has finished before TMEM is freed
+        __syncwarp();
+        mbar_wait_drain(b_done, 0);
     }
-    if (warp < 4 && !ok) *abort_flag = 1;
     __syncthreads();
     if (*abort_flag) {
-        if (threadIdx.x == 0 && p.status) atomicOr(p.status, kDevTimeout);
-        // copies still in flight land (bounded) before the block's memory is given up
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0) {
+            if (p.status) atomicOr(p.status, kDevTimeout);
+            // copies still in flight land (bounded) before the block's memory is given up
             for (uint32_t g = s_issued < STAGES ? 0 : s_issued - STAGES; g < s_issued; ++g)
                 mbar_wait_drain(b_full(g % STAGES), (g / STAGES) & 1);
+        }
     }
     __syncthreads();
-    if (warp == 5) {
+    if (warp == SOFT_WARPS) {
         tc_fence_after();
         tmem_dealloc(tm, C::TM_COLS);
+    }
+    if constexpr (CLUSTER) {
+        // Parts of one sequence: part c joins heads c, c + parts, ... of all parts'
+        // partials, read from their shared memory.
+        if (p.chunks > 1) cluster_sync();
+        const int parts = s_parts;
+        if (chunk < parts) {
+            for (int h = chunk; h < nh; h += parts) {
+                float w[kMaxCluster], m = kLow, all = 0.f;
+#pragma unroll
+                for (int i = 0; i < kMaxCluster; ++i) {
+                    w[i] = i < parts ? ld_cluster_f1(mapa_shared(sb + (HG * D + h) * 4, i)) : -INFINITY;
+                    m = fmaxf(m, w[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kMaxCluster; ++i) {
+                    w[i] = ex2(w[i] - m);
+                    all += w[i];
+                }
+                const float inv = all == 0.f ? 0.f : 1.f / all;
+                const long long row = static_cast<long long>(own) * p.Hq + h0 + h;
+                for (int d = threadIdx.x; d < D; d += C::THREADS) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kMaxCluster; ++i)
+                        if (i < parts) x = fmaf(w[i], ld_cluster_f1(mapa_shared(sb + (h * D + d) * 4, i)), x);
+                    x *= inv;
+                    if (p.out_f32)
+                        static_cast<float*>(p.out)[row * D + d] = x;
+                    else
+                        static_cast<uint16_t*>(p.out)[row * D + d] = static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xFFFFu);
+                }
+                if (threadIdx.x == 0 && p.lse) p.lse[row] = all == 0.f ? -INFINITY : (m + __log2f(all)) * kLn2f;
+            }
+        }
+        if (p.chunks > 1) cluster_sync();  // no part's memory goes before it is read
+    } else {
+        if (threadIdx.x == 0 && hg == 0 && p.chunks > 1) p.joins[chunk] = s_join;
     }
 }
 
 // Joins the partials of a sequence that crosses chunks: chunk c's second slot
 // (the sequence begins there), the first slots of the chunks up to its last.
-// One warp a (chunk, query head); chunks where none begins leave at once.
-__global__ void __launch_bounds__(128) paged_fp8_combine(const PagedFp8Params p, int D) {
+// One CTA a (chunk, query head), its threads in groups of D / 4 that take the
+// partials in turn, each with a running maximum, joined through shared memory;
+// where no sequence begins that goes on, the CTA leaves at once.
+constexpr int kJoin = 256;
+__global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params p, int D) {
+    __shared__ float4 so[kJoin];
+    __shared__ float2 sm[kJoin / 16];
+    const int c = blockIdx.x, h = blockIdx.y;
+    const int per = D / 4, groups = kJoin / per, grp = threadIdx.x / per, t = threadIdx.x % per;
     grid_dependency_wait();  // launched behind the decode grid, whose partials it reads
-    const int lane = threadIdx.x & 31;
-    const int c = blockIdx.x, h = blockIdx.y * 4 + (threadIdx.x >> 5);
     const int2 j = p.joins[c];
     // a decode that gave up may not have written its join: nothing out of range is followed
-    if (j.x < 0 || j.x >= p.num_seqs || j.y <= c || j.y >= p.chunks || h >= p.Hq) return;
-    if (status_has_timeout(p.status, kDevTimeout)) return;
-    auto slot = [&](int i) { return (static_cast<long long>(i) * 2 + (i == c ? 1 : 0)) * p.Hq + h; };
-    float mx = -INFINITY;
-    for (int i = c + lane; i <= j.y; i += 32) mx = fmaxf(mx, p.part_lse[slot(i)]);
-    mx = warp_max(mx);
-    const float ms = mx == -INFINITY ? 0.f : mx;
-    float acc[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-    float sum = 0.f;
+    if (j.x < 0 || j.x >= p.num_seqs || j.y <= c || j.y >= p.chunks) return;
+    float m = kLow, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (grp < groups) {
 #pragma unroll 4
-    for (int i = c; i <= j.y; ++i) {
-        const long long r = slot(i);
-        const float w = ex2(p.part_lse[r] - ms);
-        sum += w;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (lane + 32 * k < D) acc[k] = fmaf(w, p.part_o[r * D + lane + 32 * k], acc[k]);
+        for (int i = c + grp; i <= j.y; i += groups) {
+            const long long r = (static_cast<long long>(i) * 2 + (i == c ? 1 : 0)) * p.Hq + h;
+            const float x = p.part_lse[r];
+            const float4 v = reinterpret_cast<const float4*>(p.part_o + r * D)[t];
+            const float mn = fmaxf(m, x), a = ex2(m - mn), w = ex2(x - mn);
+            m = mn;
+            sum = fmaf(sum, a, w);
+            acc.x = fmaf(acc.x, a, w * v.x);
+            acc.y = fmaf(acc.y, a, w * v.y);
+            acc.z = fmaf(acc.z, a, w * v.z);
+            acc.w = fmaf(acc.w, a, w * v.w);
+        }
+        so[threadIdx.x] = acc;
+        if (t == 0) sm[grp] = make_float2(m, sum);
+    }
+    __syncthreads();
+    if (grp != 0) return;
+    for (int g = 1; g < groups && c + g <= j.y; ++g) {
+        const float2 ms = sm[g];
+        const float4 v = so[g * per + t];
+        const float mn = fmaxf(m, ms.x), a = ex2(m - mn), w = ex2(ms.x - mn);
+        m = mn;
+        sum = sum * a + ms.y * w;
+        acc.x = acc.x * a + v.x * w;
+        acc.y = acc.y * a + v.y * w;
+        acc.z = acc.z * a + v.z * w;
+        acc.w = acc.w * a + v.w * w;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long row = static_cast<long long>(j.x) * p.Hq + h;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (lane + 32 * k < D) {
-            const float x = acc[k] * inv;
-            if (p.out_f32)
-                static_cast<float*>(p.out)[row * D + lane + 32 * k] = x;
-            else
-                static_cast<uint16_t*>(p.out)[row * D + lane + 32 * k] =
-                    static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xFFFFu);
-        }
-    if (lane == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (ms + __log2f(sum)) * kLn2f;
+    if (p.out_f32)
+        reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D)[t] =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    else
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D)[t] =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (t == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * kLn2f;
 }
 
-template <class C>
+template <class C, bool CLUSTER>
 cudaError_t launch_cfg(const CUtensorMap& tm, const PagedFp8Params& p, cudaStream_t st) {
     static bool attr_done[64];  // the attribute is per function and device
     static std::mutex mu;
@@ -792,37 +970,47 @@ cudaError_t launch_cfg(const CUtensorMap& tm, const PagedFp8Params& p, cudaStrea
     {
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-            cudaError_t e = cudaFuncSetAttribute(paged_decode_fp8_sm103a<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 C::SMEM_BYTES);
+            cudaError_t e = cudaFuncSetAttribute(paged_decode_fp8_sm103a<C, CLUSTER>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
             if (e != cudaSuccess) return e;
             if (dev >= 0 && dev < 64) attr_done[dev] = true;
         }
     }
-    paged_decode_fp8_sm103a<C><<<static_cast<unsigned>(p.chunks) * p.n_hgroups, kThreads, C::SMEM_BYTES, st>>>(tm, p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.chunks == 1) return e;  // one chunk: no sequence crosses chunks
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>((p.Hq + 3) / 4));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.chunks) * p.n_hgroups * (CLUSTER ? p.num_seqs : 1));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = st;
     cfg.attrs = at;
+    if (CLUSTER && p.chunks > 1) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = static_cast<unsigned>(p.chunks);
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+    }
+    cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_fp8_sm103a<C, CLUSTER>, tm, p);
+    if (e != cudaSuccess || CLUSTER || p.chunks == 1) return e != cudaSuccess ? e : cudaGetLastError();
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>(p.Hq));
+    cfg.blockDim = dim3(kJoin);
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, paged_fp8_combine, p, static_cast<int>(C::D));
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D, int HG>
 cudaError_t launch_np(const CUtensorMap& tm, const PagedFp8Params& p, cudaStream_t st) {
-    return p.out_f32 ? launch_cfg<Fp8Cfg<D, HG, 4>>(tm, p, st) : launch_cfg<Fp8Cfg<D, HG, 3>>(tm, p, st);
+    if (p.cluster)
+        return p.out_f32 ? launch_cfg<Fp8Cfg<D, HG, 4>, true>(tm, p, st) : launch_cfg<Fp8Cfg<D, HG, 3>, true>(tm, p, st);
+    return p.out_f32 ? launch_cfg<Fp8Cfg<D, HG, 4>, false>(tm, p, st) : launch_cfg<Fp8Cfg<D, HG, 3>, false>(tm, p, st);
 }
 
 template <int D>
 cudaError_t launch_d(const CUtensorMap& tm, const PagedFp8Params& p, cudaStream_t st) {
     switch (p.head_cols) {
-        case 1: return launch_np<D, 1>(tm, p, st);
         case 2: return launch_np<D, 2>(tm, p, st);
         case 4: return launch_np<D, 4>(tm, p, st);
         case 8: return launch_np<D, 8>(tm, p, st);
@@ -838,13 +1026,22 @@ PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_le
     pl.subs = (group + 7) / 8;
     pl.heads_per_sub = (group + pl.subs - 1) / pl.subs;
     pl.subs = (group + pl.heads_per_sub - 1) / pl.heads_per_sub;  // none of them empty
-    pl.head_cols = 1;
+    pl.head_cols = 2;  // heads are worked in pairs
     while (pl.head_cols < pl.heads_per_sub) pl.head_cols *= 2;
     pl.n_hgroups = static_cast<long long>(Hkv) * pl.subs;
+    // Few and short sequences: a cluster of up to 8 CTAs a (sequence, head), each
+    // with at most four blocks, all of them running at once; the parts are
+    // joined on chip, in the same launch and without a workspace.
+    const long long slots = 152LL * (D <= 128 ? 2 : 1), blocks = (static_cast<long long>(max_seq_len) + 127) / 128;
+    const long long parts = blocks < 1 ? 1 : (blocks < kMaxCluster ? blocks : kMaxCluster);
+    if (blocks <= 4 * parts && num_seqs * pl.n_hgroups * parts <= slots) {
+        pl.cluster = 1;
+        pl.chunks = static_cast<int>(parts);
+        return pl;
+    }
     // Chunks: as many CTAs as run at once (152 SMs, two each up to D = 128),
     // or a few waves of them where the heads fill one badly; never more than
     // there can be blocks of context.
-    const long long slots = 152LL * (D <= 128 ? 2 : 1);
     long long best = 1;
     double best_use = 0.0;
     for (int waves = 1; waves <= 4; ++waves) {
@@ -856,7 +1053,7 @@ PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_le
             best = c;
         }
     }
-    const long long units = static_cast<long long>(num_seqs) * ((max_seq_len + 127) / 128);
+    const long long units = num_seqs * blocks;
     if (best > units) best = units;
     pl.chunks = static_cast<int>(best < 1 ? 1 : best);
     if (pl.chunks > 1) {

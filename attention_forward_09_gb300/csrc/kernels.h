@@ -181,12 +181,13 @@ struct PagedFp8Params {
     int Hq, Hkv, group;
     int subs, heads_per_sub, head_cols;  // a KV head's query heads in `subs` runs of heads_per_sub, padded to head_cols
     int n_hgroups;    // Hkv * subs
-    int chunks;
+    int chunks;       // of all context blocks; or, with cluster set, parts of each sequence
+    int cluster;      // 1: a cluster of `chunks` CTAs a (sequence, head group) joins on chip; no workspace
     float scale_log2;
     int out_f32, e5m2;
 };
 struct PagedFp8Plan {
-    int subs, heads_per_sub, head_cols, chunks;
+    int subs, heads_per_sub, head_cols, chunks, cluster;
     long long n_hgroups;
     size_t o_bytes, lse_bytes;  // workspace sections, each 256-byte aligned; then the joins
     size_t workspace_bytes;

@@ -116,7 +116,7 @@ def test_read_validation(lib):
 
 
 def paged(lib, **kw):
-    a = dict(q=P, qs=4096, cache=P, scales=P, kv=0, nb=16, bs=128, bt=P, maxb=4, sl=P, S=2, maxlen=512, Hq=32, Hkv=8,
+    a = dict(q=P, qs=4096, cache=P, scales=P, kv=0, nb=16, bs=128, bt=P, maxb=4, sl=P, S=2, maxlen=8192, Hq=32, Hkv=8,
              D=128, scale=0.1, causal=1, out=P, odt=1, lse=None, ws=P, wsb=1 << 30)
     a.update(kw)
     return lib.attn_fwd_paged_fp8(*a.values(), None, None)
@@ -141,6 +141,7 @@ def test_workspace_size_is_pure(lib):
     size = lib.attn_fwd_paged_fp8_workspace_size
     assert size(0, 8, 8, 128, 100) == 0 and size(1, 8, 3, 128, 100) == 0 and size(1, 8, 8, 100, 100) == 0
     assert size(1, 32, 8, 128, 128) == 0  # one block: nothing to join
+    assert size(1, 32, 8, 128, 4096) == 0  # a cluster of CTAs joins on chip
     a = size(64, 32, 8, 128, 32768)
     assert a == size(64, 32, 8, 128, 32768) > 0
     assert size(64, 32, 8, 128, 131072) == a  # by the card's size, not the context's

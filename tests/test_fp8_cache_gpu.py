@@ -294,9 +294,10 @@ def test_decode_head_sizes(D, out_dtype, kind):
     c = Ctx([1, 0, 127, 128, 129, 600], 2, D, kind, seed=D)
     q = bf16(6, 8, D, seed=D + 1)
     status = status_word()
-    out, lse = run_decode(c, q, out_dtype=out_dtype, status=status)
-    assert int(status) == 0
-    check_decode(c, q, out, lse)
+    for max_len in (max(c.lens), 1 << 20):  # a cluster a sequence and head; chunks of all blocks
+        out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype, status=status)
+        assert int(status) == 0
+        check_decode(c, q, out, lse)
 
 
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (2, 1), (3, 1), (5, 1), (12, 2), (7, 1), (8, 1), (9, 1), (16, 1), (34, 2), (40, 1), (40, 40)])
@@ -304,11 +305,12 @@ def test_decode_gqa_ratios(hq, hkv):
     for out_dtype in (torch.float32, torch.bfloat16):
         c = Ctx([300, 5, 0, 1000], hkv, 64, seed=hq)
         q = bf16(4, hq, 64, seed=hq + 1)
-        out, lse = run_decode(c, q, out_dtype=out_dtype)
-        check_decode(c, q, out, lse)
+        for max_len in (max(c.lens), 1 << 20):
+            out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
+            check_decode(c, q, out, lse)
 
 
-@pytest.mark.parametrize("lens", [[5000], [20000], [1] * 700, [0] * 300 + [129] + [0] * 300, [64, 9000, 64, 0, 3000], [0, 0, 0]])
+@pytest.mark.parametrize("lens", [[1025], [4096, 0, 7], [5000], [20000], [1] * 700, [0] * 300 + [129] + [0] * 300, [64, 9000, 64, 0, 3000], [0, 0, 0]])
 def test_decode_splits(lens):
     """One long sequence over all chunks, many short ones in a chunk, long and short."""
     c = Ctx(lens, 2, 64, seed=len(lens))
@@ -329,8 +331,9 @@ def test_decode_scales_of_any_size():
     q[:, 1] *= 2.0 ** -40
     q[:, 2, ::2] *= 2.0 ** -13
     q[0, 3] = 0
-    out, lse = run_decode(c, q)
-    check_decode(c, q, out, lse)
+    for max_len in (max(c.lens), 1 << 20):
+        out, lse = run_decode(c, q, max_len=max_len)
+        check_decode(c, q, out, lse)
 
 
 def test_decode_sink_with_a_tiny_value_row():
@@ -357,19 +360,21 @@ def test_decode_sink_with_a_tiny_value_row():
 def test_decode_large_logits():
     c = Ctx([129, 1000], 1, 128, seed=4, exps=(122, 126))
     q = bf16(2, 4, 128, seed=5, spread=30.0)  # scores of some thousands: one key takes all the weight
-    out, lse = run_decode(c, q)
-    check_decode(c, q, out, lse)
+    for max_len in (max(c.lens), 1 << 20):
+        out, lse = run_decode(c, q, max_len=max_len)
+        check_decode(c, q, out, lse)
 
 
-def test_decode_nan_stays_in_its_sequence_and_head():
+@pytest.mark.parametrize("max_len", [200, 1 << 20])
+def test_decode_nan_stays_in_its_sequence_and_head(max_len):
     c = Ctx([200, 200, 200], 2, 64, seed=6)
     q = bf16(3, 4, 64, seed=7)
-    clean, clean_lse = run_decode(c, q)
+    clean, clean_lse = run_decode(c, q, max_len=max_len)
     b = int(c.table[1, 0])
     c.codes[0, b, 7, 1, 3] = 127     # a key of sequence 1, KV head 1
     c.codes[1, int(c.table[2, 1]), 2, 0, 9] = 127  # a value of sequence 2, KV head 0, column 9
     q[0, 2, 5] = float("inf")
-    out, lse = run_decode(c, q)
+    out, lse = run_decode(c, q, max_len=max_len)
     nan, nan_lse = torch.isnan(out).cpu(), torch.isnan(lse).cpu()
     want, want_lse = torch.zeros(3, 4, 64, dtype=torch.bool), torch.zeros(3, 4, dtype=torch.bool)
     want[1, 2:], want_lse[1, 2:] = True, True
@@ -379,20 +384,21 @@ def test_decode_nan_stays_in_its_sequence_and_head():
     assert torch.equal(out.cpu()[~want], clean.cpu()[~want]) and torch.equal(lse.cpu()[~want_lse], clean_lse.cpu()[~want_lse])
 
 
-def test_decode_bad_block_is_skipped_and_reported():
+@pytest.mark.parametrize("max_len", [300, 1 << 20])
+def test_decode_bad_block_is_skipped_and_reported(max_len):
     c = Ctx([300, 100], 1, 64, seed=8)
     q = bf16(2, 2, 64, seed=9)
     kept = Ctx([300, 100], 1, 64, seed=8)
     c.table[0, 1] = 1 << 20
     status = status_word()
-    out, lse = run_decode(c, q, status=status)
+    out, lse = run_decode(c, q, max_len=max_len, status=status)
     assert int(status) == gb.DEV_BAD_INDEX
     # the same as without those 128 tokens: blocks 0 and 2 of the sequence
     kept.table[0, 1] = kept.table[0, 2]
     kept.lens = [300 - 128, 100]
     check_decode(kept, q, out, lse)
     c.table[0, :3] = -7  # no block left: an empty row
-    out, lse = run_decode(c, q)
+    out, lse = run_decode(c, q, max_len=max_len)
     assert not out[0].any() and torch.isinf(lse[0]).all()
 
 
@@ -405,6 +411,12 @@ def test_decode_bad_lengths_are_clamped_and_reported():
     assert int(status) == gb.DEV_BAD_SEQLEN
     c.lens = [300, 0, 50]
     check_decode(c, q, out, lse)
+    many = 100  # past 300 * many the bound is the table's: chunks
+    status.zero_()
+    out, lse = gb.attn_fwd_paged_fp8(q.to(dev()), cache, scales, table[:, :3].contiguous(), ints([1 << 30, -3, 50]), 300 * many, lse=True, dev_status=status)
+    assert int(status) & gb.DEV_BAD_SEQLEN
+    c.lens = [384, 0, 50]
+    assert torch.isfinite(lse[2]).all() and torch.isinf(lse[1]).all()
 
 
 def test_decode_strided_queries_given_outputs_and_workspace():
@@ -412,34 +424,36 @@ def test_decode_strided_queries_given_outputs_and_workspace():
     qkv = bf16(3, 4 + 4, 96, seed=4).to(dev())
     q = qkv[:, :4]
     cache, scales, table = c.on_gpu()
-    need = gb.attn_fwd_paged_fp8_workspace_size(3, 4, 2, 96, 1300)
+    need = gb.attn_fwd_paged_fp8_workspace_size(3, 4, 2, 96, 13000)
     assert need > 0
     ws = torch.full((need + 256,), 255, dtype=torch.uint8, device=dev())
     out, lse = torch.empty(3, 4, 96, dtype=torch.bfloat16, device=dev()), torch.empty(3, 4, device=dev())
-    got = gb.attn_fwd_paged_fp8(q, cache, scales, table, ints(c.lens), 1300, out=out, lse=lse, workspace=ws[:need])
+    got = gb.attn_fwd_paged_fp8(q, cache, scales, table, ints(c.lens), 13000, out=out, lse=lse, workspace=ws[:need])
     assert got[0] is out and got[1] is lse
     check_decode(c, q.cpu(), out, lse)
     assert (ws[need:] == 255).all()  # nothing behind the stated size
     with pytest.raises(gb.GbattnError) as e:
-        gb.attn_fwd_paged_fp8(q, cache, scales, table, ints(c.lens), 1300, workspace=ws[:need - 256])
+        gb.attn_fwd_paged_fp8(q, cache, scales, table, ints(c.lens), 13000, workspace=ws[:need - 256])
     assert e.value.status == 4
     for bad in (dict(out=torch.empty(3, 4, 64, device=dev())), dict(lse=torch.empty(4, 3, device=dev())), dict(out=out.transpose(0, 1))):
         with pytest.raises(ValueError):
             gb.attn_fwd_paged_fp8(q, cache, scales, table, ints(c.lens), 1300, **bad)
 
 
-def test_decode_repeats_bit_for_bit():
+@pytest.mark.parametrize("max_len", [3000, 30000])
+def test_decode_repeats_bit_for_bit(max_len):
     c = Ctx([3000, 50, 700], 2, 128, seed=12)
     q = bf16(3, 8, 128, seed=13).to(dev())
     cache, scales, table = c.on_gpu()
     sl = ints(c.lens)
-    a = gb.attn_fwd_paged_fp8(q, cache, scales, table, sl, 3000, lse=True)
+    a = gb.attn_fwd_paged_fp8(q, cache, scales, table, sl, max_len, lse=True)
     for _ in range(20):
-        b = gb.attn_fwd_paged_fp8(q, cache, scales, table, sl, 3000, lse=True)
+        b = gb.attn_fwd_paged_fp8(q, cache, scales, table, sl, max_len, lse=True)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_decode_on_two_streams_at_once_and_in_graphs():
+@pytest.mark.parametrize("max_len", [2000, 20000])
+def test_decode_on_two_streams_at_once_and_in_graphs(max_len):
     """Two streams with a workspace each; a captured graph replayed with new
     lengths, queries and cache contents, beside eager calls."""
     c = Ctx([2000, 900, 0, 128], 2, 128, seed=14)
@@ -447,13 +461,13 @@ def test_decode_on_two_streams_at_once_and_in_graphs():
     q = bf16(4, 8, 128, seed=15)
     cache, scales, table = c.on_gpu()
     qd, sl = q.to(dev()), ints(c.lens)
-    want = gb.attn_fwd_paged_fp8(qd, cache, scales, table, sl, 2000, lse=True)
+    want = gb.attn_fwd_paged_fp8(qd, cache, scales, table, sl, max_len, lse=True)
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
     outs = [[], []]
     for _ in range(10):
         for i, s in enumerate(streams):
-            outs[i].append(gb.attn_fwd_paged_fp8(qd, cache, scales, table, sl, 2000, lse=True, stream=s))
+            outs[i].append(gb.attn_fwd_paged_fp8(qd, cache, scales, table, sl, max_len, lse=True, stream=s))
     torch.cuda.synchronize()
     for o in outs[0] + outs[1]:
         assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
@@ -461,14 +475,14 @@ def test_decode_on_two_streams_at_once_and_in_graphs():
     for _ in range(2):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            graphs.append((g, gb.attn_fwd_paged_fp8(qd, cache, scales, table, sl, 2000, lse=True)))
+            graphs.append((g, gb.attn_fwd_paged_fp8(qd, cache, scales, table, sl, max_len, lse=True)))
     c.lens = [2000, 1, 0, 128]
     sl.copy_(ints(c.lens))
     q = bf16(4, 8, 128, seed=16)
     qd.copy_(q)
     for g, _ in graphs:
         g.replay()
-    eager = gb.attn_fwd_paged_fp8(qd, cache, scales, table, sl, 2000, lse=True)
+    eager = gb.attn_fwd_paged_fp8(qd, cache, scales, table, sl, max_len, lse=True)
     torch.cuda.synchronize()
     for o in [x for _, x in graphs] + [eager]:
         check_decode(c, q, *o)
