@@ -86,17 +86,18 @@ bool encode_rows_heads_d(CUtensorMap* m, const void* base, long long rows, int h
     return r == CUDA_SUCCESS;
 }
 
-// 8-bit cache [rows, heads, D] as a 3-D TMA map of bytes, box {128, 1, 128},
-// 128-byte swizzle: a box is one head's 128 rows, zeros past D.
-bool encode_fp8_cache(CUtensorMap* m, const void* base, long long rows, int heads, int d) {
+// 8-bit cache [rows, heads, D] as a 3-D TMA map of bytes: a box is `width`
+// (128 or 64) columns of one head's 128 rows, zeros past D, swizzled over their span.
+bool encode_fp8_cache(CUtensorMap* m, const void* base, long long rows, int heads, int d, int width) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads) * d};
-    cuuint32_t box[3] = {128, 1, 128};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(width), 1, 128};
     cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapSwizzle swizzle = width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
@@ -662,7 +663,7 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
     s = device_info(&di);
     if (s != GBATTN_OK) return s;
     CUtensorMap tm;
-    if (!encode_fp8_cache(&tm, kv_cache, 2LL * num_blocks * 128, Hkv, D)) return GBATTN_ERR_CUDA;
+    if (!encode_fp8_cache(&tm, kv_cache, 2LL * num_blocks * 128, Hkv, D, gbattn::paged_fp8_box(D))) return GBATTN_ERR_CUDA;
     gbattn::PagedFp8Params p{};
     p.q = static_cast<const uint16_t*>(q);
     p.q_stride = q_stride;

@@ -46,6 +46,7 @@ namespace {
 constexpr int kTok = 128;      // tokens of a cache block: the MMA's M
 constexpr int kWg = 128;       // threads of a softmax warpgroup, one a token lane
 constexpr int kMaxCluster = 8; // portable cluster size
+constexpr int kNewSeg = 256;
 constexpr float kLow = -1e30f;  // a reference below every score, finite so that differences are defined
 constexpr float kLn2f = 0.6931471805599453f;
 
@@ -54,21 +55,24 @@ constexpr int pow2_cols(int n) { return n <= 32 ? 32 : (n <= 64 ? 64 : (n <= 128
 
 // HG query heads a CTA.  Up to four heads one warpgroup does the softmax; eight
 // are shared by two, four heads each, so that a block's chain of products and
-// softmax stays short.  A last warp loads and issues the products.
+// softmax stays short.  Two more warps load and issue the products.
 template <int D_, int HG_, int NP_>
 struct Fp8Cfg {
     static constexpr int D = D_, HG = HG_, NP = NP_;
     static constexpr int NWG = HG > 4 ? 2 : 1;
     static constexpr int HT = HG / NWG;              // heads a thread
     static constexpr int SOFT = NWG * kWg;
-    static constexpr int THREADS = SOFT + 32;
-    static constexpr int NCH = (D + 127) / 128;      // 128-byte chunks of a row (zero-filled past D)
+    static constexpr int THREADS = SOFT + 64;
+    static constexpr int NCH = (D + 127) / 128;      // 128-column blocks of O^T, and 128-byte chunks of a query row
+    static constexpr int PW = paged_fp8_box(D);      // bytes of a row in one TMA box, and its swizzle span
+    static constexpr int NPC = (D + PW - 1) / PW;    // boxes of 128 rows (the last zero-filled past D)
+    static constexpr int PIECE_BYTES = kTok * PW;    // a slot: value boxes, then key boxes
     static constexpr int NQ = up16(2 * HG);          // columns of S^T: piece * HG + head
     static constexpr int NW = up16(NP * HG);         // columns of O^T: (warpgroup * NP + piece) * HT + head
-    static constexpr int HALF_BYTES = NCH * kTok * 128;
+    static constexpr int HALF_BYTES = NPC * PIECE_BYTES;
     static constexpr int SLOT_BYTES = 2 * HALF_BYTES;
-    static constexpr int CTAS = NCH == 1 ? 2 : 1;    // per SM
-    static constexpr int STAGES = 3;
+    static constexpr int CTAS = paged_fp8_ctas(D, HG);  // per SM
+    static constexpr int STAGES = (CTAS == 3 ? 65536 : (CTAS == 2 ? 98304 : 196608)) / SLOT_BYTES;
     static constexpr int Q_BYTES = NCH * NQ * 128;   // one buffer of query pieces
     static constexpr int P_BYTES = NW * kTok;
     static constexpr int OFF_Q = STAGES * SLOT_BYTES;
@@ -78,12 +82,12 @@ struct Fp8Cfg {
     static constexpr int OFF_QF = OFF_RED + 2 * 4 * HG * 4;    // [2][HG] f32: 2^f * scale_log2
     static constexpr int OFF_LEN = OFF_QF + 2 * HG * 4;        // valid tokens of each slot's block
     static constexpr int OFF_BAR = (OFF_LEN + STAGES * 4 + 7) & ~7;
-    static constexpr int N_BAR = 2 * STAGES + 2 + 2 + 2 + 1 + 1 + 1;
+    static constexpr int N_BAR = 2 * STAGES + 2 + 2 + 1 + 1 + 1;
     static constexpr int SMEM_BYTES = 1024 + OFF_BAR + N_BAR * 8;
     static constexpr int TM_S = 0;                   // two S^T buffers
     static constexpr int TM_O = 2 * NQ;
     static constexpr int TM_COLS = pow2_cols(2 * NQ + NCH * NW);
-    static_assert(SMEM_BYTES <= (CTAS == 2 ? 115712 : 232448), "shared memory budget");
+    static_assert((SMEM_BYTES + 1024 + 256) * CTAS <= 233472, "shared memory budget");
     static_assert(TM_COLS * CTAS <= 512, "tensor memory budget");
     static_assert(HG * (D + 1) * 4 <= SLOT_BYTES, "a cluster's partials lie in the first slot");
 };
@@ -103,6 +107,14 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// sdesc_sw128 for rows of PW bytes, 128 or 64, with the swizzle of that span.
+template <int PW>
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr, uint32_t lbo) {
+    constexpr uint64_t mode = PW == 128 ? 2 : 4;
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+           static_cast<uint64_t>(8 * PW >> 4) << 32 | static_cast<uint64_t>(1) << 46 | mode << 61;
 }
 
 // Matrix descriptor without swizzle, MN-major: 16-byte rows of 16 columns, 8
@@ -338,14 +350,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
     float* sqf = reinterpret_cast<float*>(smem + C::OFF_QF);
-    volatile int* slen = reinterpret_cast<volatile int*>(smem + C::OFF_LEN);
+    volatile int* slen = reinterpret_cast<volatile int*>(smem + C::OFF_LEN);  // + kNewSeg in a segment's first block
     const uint32_t bar0 = sb + C::OFF_BAR;
     auto b_full = [&](int i) { return bar0 + 8 * i; };
     auto b_empty = [&](int i) { return bar0 + 8 * (STAGES + i); };
     auto b_sfull = [&](int i) { return bar0 + 8 * (2 * STAGES + i); };
-    auto b_sempty = [&](int i) { return bar0 + 8 * (2 * STAGES + 2 + i); };
-    auto b_qfull = [&](int i) { return bar0 + 8 * (2 * STAGES + 4 + i); };
-    const uint32_t b_pfull = bar0 + 8 * (2 * STAGES + 6), b_ofull = b_pfull + 8, b_done = b_pfull + 16;
+    auto b_qfull = [&](int i) { return bar0 + 8 * (2 * STAGES + 2 + i); };
+    const uint32_t b_pfull = bar0 + 8 * (2 * STAGES + 4), b_ofull = b_pfull + 8, b_done = b_pfull + 16;
     __shared__ int abort_storage, s_skip;
     __shared__ uint32_t tmem_base_storage, s_issued;  // s_issued: blocks whose loads were issued
     __shared__ long long s_sum[WARPS];
@@ -384,7 +395,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_sfull(i), 1);
-            mbar_init(b_sempty(i), SOFT_WARPS);
             mbar_init(b_qfull(i), SOFT_WARPS);
         }
         mbar_init(b_pfull, SOFT_WARPS);
@@ -518,8 +528,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             if (lane == 0) mbar_arrive(b_qfull(0));
             named_bar_sync(1 + wg, kWg);  // sqf is read by the warpgroup's four warps
             const uint32_t tlane = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 TMEM lanes
-            uint32_t g = 0;  // blocks done
-            int seg = 0;
+            uint32_t g = 0, phase = 0;  // blocks done; the ring's parity
+            int slot = 0, seg = 0;
             bool more = true;
             while (more) {
                 // queries of the next segment: asked for now, laid out after this
@@ -534,13 +544,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
                     for (int c = 0; c < NCH; ++c) o[c][h] = splat(0.f);
                 }
-                // O^T of the block before: o += 2^(M - 8 - R) sum_i piece_i / 16^i
-                auto add_o = [&](uint32_t gi) {
+                // O^T of the block before: asked for early, and then
+                // o += 2^(M - 8 - R) sum_i piece_i / 16^i
+                uint32_t ro[NCH][NP * HT];
+                auto ask_o = [&](uint32_t gi) {
                     if (!mbar_wait(b_ofull, gi & 1, abort_flag)) ok = false;
                     tc_fence_after();
-                    uint32_t r[NCH][NP * HT];
 #pragma unroll
-                    for (int c = 0; c < NCH; ++c) tmem_ld<NP * HT>(tm + tlane + C::TM_O + c * NW + wg * NP * HT, r[c]);
+                    for (int c = 0; c < NCH; ++c) tmem_ld<NP * HT>(tm + tlane + C::TM_O + c * NW + wg * NP * HT, ro[c]);
+                };
+                auto add_o = [&]() {
                     float2 beta[HT / 2];
 #pragma unroll
                     for (int h = 0; h < HT / 2; ++h) {
@@ -559,7 +572,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
                         for (int h = 0; h < HT / 2; ++h) {
                             auto piece = [&](int i) {
-                                return make_float2(__uint_as_float(r[c][i * HT + 2 * h]), __uint_as_float(r[c][i * HT + 2 * h + 1]));
+                                return make_float2(__uint_as_float(ro[c][i * HT + 2 * h]), __uint_as_float(ro[c][i * HT + 2 * h + 1]));
                             };
                             float2 x = piece(NP - 1);
 #pragma unroll
@@ -571,22 +584,18 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 const float2* qf = reinterpret_cast<const float2*>(sqf + (seg & 1) * HG + hw);
                 bool quit = false;
                 for (int b = w.b0; b < w.b1; ++b, ++g) {
-                    const int slot = static_cast<int>(g % STAGES);
-                    if (!mbar_wait(b_full(slot), (g / STAGES) & 1, abort_flag)) ok = false;
+                    if (!mbar_wait(b_full(slot), phase, abort_flag)) ok = false;
+                    const int nvalid = slen[slot] & (kNewSeg - 1);
+                    const bool valid = tok < nvalid;
+                    const uint8_t* sc = smem + C::OFF_SC + slot * 256;
+                    const float kf = exp2_byte(sc[tok]);
+                    const float ev = static_cast<float>(static_cast<int>(sc[128 + tok]) - 127);
                     if (!mbar_wait(b_sfull(g & 1), (g >> 1) & 1, abort_flag)) ok = false;
                     tc_fence_after();
                     uint32_t r0[HT], r1[HT];
                     tmem_ld<HT>(tm + tlane + C::TM_S + (g & 1) * NQ + hw, r0);
                     tmem_ld<HT>(tm + tlane + C::TM_S + (g & 1) * NQ + HG + hw, r1);
-                    const int nvalid = slen[slot];
-                    const bool valid = tok < nvalid;
-                    const uint8_t* sc = smem + C::OFF_SC + slot * 256;
-                    const float kf = exp2_byte(sc[tok]);
-                    const float ev = static_cast<float>(static_cast<int>(sc[128 + tok]) - 127);
                     tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(b_sempty(g & 1));
                     float2 u[HT / 2], d[HT / 2];
                     float dmax = kLow;
 #pragma unroll
@@ -621,6 +630,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
                         for (int h = 0; h < HT; h += 2) *reinterpret_cast<float2*>(red + (warp & 3) * HT + h) = make_float2(m[h], m[h + 1]);
                     }
+                    if (b > w.b0) ask_o(g - 1);
                     if (named_bar_or(1 + wg, kWg, !ok)) {  // a warpgroup's four warps leave together
                         quit = true;
                         break;
@@ -628,13 +638,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     // the value rows past the context meet weight 0: they must be finite
                     if (!valid && wg == 0) {
 #pragma unroll
-                        for (int c = 0; c < NCH; ++c) {
-                            uint4* v = reinterpret_cast<uint4*>(smem + slot * C::SLOT_BYTES + C::HALF_BYTES + c * kTok * 128 + tok * 128);
+                        for (int c = 0; c < C::NPC; ++c) {
+                            uint4* v = reinterpret_cast<uint4*>(smem + slot * C::SLOT_BYTES + c * C::PIECE_BYTES + tok * C::PW);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int i = 0; i < C::PW / 16; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
-                    if (b > w.b0) add_o(g - 1);  // the weights' buffer and O^T are free again
+                    if (b > w.b0) add_o();  // the weights' buffer and O^T are free again
                     // weights 256 w = 2^(u - M + 8) and their pieces
                     constexpr int WORDS = (NP * HT + 3) / 4;
                     uint32_t w8[WORDS];
@@ -665,6 +675,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(b_pfull);
+                    if (++slot == STAGES) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                     if (has_next && b == w.b0) {
                         qs.put(p, smem + C::OFF_Q + ((seg + 1) & 1) * C::Q_BYTES, sqf + ((seg + 1) & 1) * HG, warp, lane);
                         fence_proxy_async_smem();
@@ -673,7 +687,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     }
                 }
                 if (quit) break;
-                add_o(g - 1);
+                ask_o(g - 1);
+                add_o();
                 // ---- the segment's softmax sum over the 128 token lanes, then its output
                 float inv[HT], lse2[HT];
 #pragma unroll
@@ -752,102 +767,107 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
         if (!ok) *abort_flag = 1;
     } else if (n_units > 0) {
-        // ---------------------------------------------------- loads and products
-        // Per unit i: unit i - 1's product with V is done, so its slot takes unit
-        // i - 1 + STAGES; S^T of unit i + 1 is issued; then, once the weights of
-        // unit i are there, its product with V.
+        if (warp == SOFT_WARPS) {
+            // ------------------------------------------------ cache loads
+            Walk w;
+            w.start(p, s_first[0], s_first[1], n_units);
+            int ids = 0, slot = 0, b = w.b0;
+            uint32_t phase = 1;  // (the first round of waits on the ring passes at once)
+            for (uint32_t g = 0; g < n_units; ++g) {
+                const int at = (b - w.b0) & 31;  // 32 table entries are held, one a lane
+                if (at == 0) ids = b + lane < w.b1 ? p.block_table[static_cast<long long>(w.s) * p.max_blocks + b + lane] : 0;
+                const int blk = __shfl_sync(0xffffffffu, ids, at);
+                ok = __all_sync(0xffffffffu, mbar_wait(b_empty(slot), phase, abort_flag));
+                if (!ok) break;
+                if (elect_one()) {
+                    const bool good = blk >= 0 && blk < p.num_blocks;
+                    slen[slot] = (good ? min(kTok, w.L - b * kTok) : 0) + (b == w.b0 ? kNewSeg : 0);
+                    if (good) {
+                        mbar_arrive_expect_tx(b_full(slot), C::SLOT_BYTES + 256);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const long long r = static_cast<long long>(half) * p.num_blocks + blk;
+#pragma unroll
+                            for (int c = 0; c < C::NPC; ++c)
+                                tma_load_3d(sb + slot * C::SLOT_BYTES + (1 - half) * C::HALF_BYTES + c * C::PIECE_BYTES, &tmKV,
+                                            b_full(slot), c * C::PW, kvh, static_cast<int>(r * kTok));
+                            bulk_load(sb + C::OFF_SC + slot * 256 + half * 128, p.scales + (r * p.Hkv + kvh) * kTok, 128, b_full(slot));
+                        }
+                    } else {
+                        if (p.status) atomicOr(p.status, kDevBadIndex);
+                        mbar_arrive(b_full(slot));
+                    }
+                    s_issued = g + 1;
+                }
+                __syncwarp();
+                if (++b == w.b1) {
+                    w.next(p);
+                    b = w.b0;
+                }
+                if (++slot == STAGES) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            if (!ok) *abort_flag = 1;
+        } else {
+        // ---------------------------------------------------- products
+        // Unit by unit: S^T of the next unit, whose buffer was read before the
+        // weights of the unit before came; then, once this unit's weights are
+        // there, O^T.
         const uint32_t id_s = idesc_f8(128, NQ, p.e5m2 ? 1u : 0u, false, false);
         const uint32_t id_o = idesc_f8(128, NW, p.e5m2 ? 1u : 0u, true, true);
-        Walk wl, w;  // of the loads, of the products
-        wl.start(p, s_first[0], s_first[1], n_units);
-        w = wl;
-        uint32_t loaded = 0;
-        int lb = wl.b0, ids = 0, seg = 0, b = w.b0;
-        auto load = [&]() {  // the next unit, into its (free) slot
-            const int slot = static_cast<int>(loaded % STAGES);
-            const int at = (lb - wl.b0) & 31;  // 32 table entries are held, one a lane
-            if (at == 0) ids = lb + lane < wl.b1 ? p.block_table[static_cast<long long>(wl.s) * p.max_blocks + lb + lane] : 0;
-            const int blk = __shfl_sync(0xffffffffu, ids, at);
-            if (elect_one()) {
-                const bool good = blk >= 0 && blk < p.num_blocks;
-                slen[slot] = good ? min(kTok, wl.L - lb * kTok) : 0;
-                if (good) {
-                    mbar_arrive_expect_tx(b_full(slot), C::SLOT_BYTES + 256);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const long long r = static_cast<long long>(half) * p.num_blocks + blk;
-#pragma unroll
-                        for (int c = 0; c < NCH; ++c)
-                            tma_load_3d(sb + slot * C::SLOT_BYTES + half * C::HALF_BYTES + c * kTok * 128, &tmKV, b_full(slot),
-                                        c * 128, kvh, static_cast<int>(r * kTok));
-                        bulk_load(sb + C::OFF_SC + slot * 256 + half * 128, p.scales + (r * p.Hkv + kvh) * kTok, 128, b_full(slot));
-                    }
-                } else {
-                    if (p.status) atomicOr(p.status, kDevBadIndex);
-                    mbar_arrive(b_full(slot));
-                }
-                s_issued = loaded + 1;
-            }
-            __syncwarp();
-            ++loaded;
-            if (++lb == wl.b1 && loaded < n_units) {
-                wl.next(p);
-                lb = wl.b0;
-            }
-        };
+        int kslot = 0, vslot = 0, seg = -1;
+        uint32_t kphase = 0;
         auto issue_s = [&](uint32_t i) {
-            const int slot = static_cast<int>(i % STAGES);
-            bool got = mbar_wait(b_full(slot), (i / STAGES) & 1, abort_flag);
-            if (b == w.b0) got = got && mbar_wait(b_qfull(seg & 1), (seg >> 1) & 1, abort_flag);
-            if (i >= 2) got = got && mbar_wait(b_sempty(i & 1), ((i >> 1) - 1) & 1, abort_flag);
+            bool got = mbar_wait(b_full(kslot), kphase, abort_flag);
+            if (got && slen[kslot] >= kNewSeg) {
+                ++seg;
+                got = mbar_wait(b_qfull(seg & 1), (seg >> 1) & 1, abort_flag);
+            }
             if (!__all_sync(0xffffffffu, got)) return false;
             tc_fence_after();
             if (elect_one()) {
-                const uint32_t k = sb + slot * C::SLOT_BYTES, q = sb + C::OFF_Q + (seg & 1) * C::Q_BYTES;
+                const uint32_t k = sb + kslot * C::SLOT_BYTES + C::HALF_BYTES, q = sb + C::OFF_Q + (seg & 1) * C::Q_BYTES;
 #pragma unroll
                 for (int ks = 0; ks < D / 32; ++ks)
-                    mma_f8_ss(tm + C::TM_S + (i & 1) * NQ, sdesc_sw128(k + (ks / 4) * (kTok * 128) + (ks % 4) * 32, 16, 1024),
+                    mma_f8_ss(tm + C::TM_S + (i & 1) * NQ, sdesc_rows<C::PW>(k + ks * 32 / C::PW * C::PIECE_BYTES + ks * 32 % C::PW, 16),
                               sdesc_sw128(q + (ks / 4) * (NQ * 128) + (ks % 4) * 32, 16, 1024), id_s, ks > 0);
                 mma_commit(b_sfull(i & 1));
             }
             __syncwarp();
-            if (++b == w.b1 && i + 1 < n_units) {
-                w.next(p);
-                b = w.b0;
-                ++seg;
+            if (++kslot == STAGES) {
+                kslot = 0;
+                kphase ^= 1;
             }
             return true;
         };
-        while (loaded < STAGES && loaded < n_units) load();
         ok = issue_s(0);
         for (uint32_t i = 0; ok && i < n_units; ++i) {
-            if (i > 0 && loaded < n_units) {
-                ok = __all_sync(0xffffffffu, mbar_wait(b_empty((i - 1) % STAGES), ((i - 1) / STAGES) & 1, abort_flag));
-                if (!ok) break;
-                load();
-            }
             if (i + 1 < n_units) ok = issue_s(i + 1);
-            const int slot = static_cast<int>(i % STAGES);
             ok = __all_sync(0xffffffffu, ok && mbar_wait(b_pfull, i & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                const uint32_t v = sb + slot * C::SLOT_BYTES + C::HALF_BYTES, pp = sb + C::OFF_P;
+                // V^T's rows past D (lanes that nobody reads) are zeros or repeat the block's only box
+                const uint32_t v = sb + vslot * C::SLOT_BYTES, pp = sb + C::OFF_P;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_f8_ss(tm + C::TM_O + c * NW, sdesc_sw128(v + c * (kTok * 128) + ks * 4096, 16, 1024),
+                        mma_f8_ss(tm + C::TM_O + c * NW, sdesc_rows<C::PW>(v + c * (kTok * 128) + ks * 32 * C::PW, D - c * 128 <= C::PW ? 0 : C::PIECE_BYTES),
                                   sdesc_plain(pp + ks * 512, 128, kTok * 16), id_o, ks > 0);
                 mma_commit(b_ofull);
-                mma_commit(b_empty(slot));
+                mma_commit(b_empty(vslot));
             }
             __syncwarp();
+            if (++vslot == STAGES) vslot = 0;
         }
         if (!ok) *abort_flag = 1;
         if (elect_one()) mma_commit(b_done);  // every product issued has finished before TMEM is freed
         __syncwarp();
         mbar_wait_drain(b_done, 0);
+        }
     }
     __syncthreads();
     if (*abort_flag) {
@@ -1032,14 +1052,14 @@ PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_le
     // Few and short sequences: a cluster of up to 8 CTAs a (sequence, head), each
     // with at most four blocks, all of them running at once; the parts are
     // joined on chip, in the same launch and without a workspace.
-    const long long slots = 152LL * (D <= 128 ? 2 : 1), blocks = (static_cast<long long>(max_seq_len) + 127) / 128;
+    const long long slots = 152LL * paged_fp8_ctas(D, pl.head_cols), blocks = (static_cast<long long>(max_seq_len) + 127) / 128;
     const long long parts = blocks < 1 ? 1 : (blocks < kMaxCluster ? blocks : kMaxCluster);
     if (blocks <= 4 * parts && num_seqs * pl.n_hgroups * parts <= slots) {
         pl.cluster = 1;
         pl.chunks = static_cast<int>(parts);
         return pl;
     }
-    // Chunks: as many CTAs as run at once (152 SMs, two each up to D = 128),
+    // Chunks: as many CTAs as run at once (152 SMs),
     // or a few waves of them where the heads fill one badly; never more than
     // there can be blocks of context.
     long long best = 1;

@@ -194,7 +194,16 @@ struct PagedFp8Plan {
 };
 // num_seqs, Hq, Hkv, D > 0, Hq % Hkv == 0.
 PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_len);
-// tmKV: the cache as bytes {D, Hkv, 2 * num_blocks * 128}, box {128, 1, 128}, 128-byte swizzle.
+// Bytes of a row in one TMA box of the decode, and the box's swizzle span: 64
+// where that divides D and 128 does not, so that shared memory holds no
+// padding and more of the context is in flight (contexts of 16384, D = 192:
+// 6.2 -> 6.8 TB/s, D = 64: 5.1 -> 5.4).  At D = 96 boxes of 32 bytes are slower
+// than padding to 128 (5.1 and 6.1 TB/s): a box's rows cost by number.
+constexpr int paged_fp8_box(int D) { return D % 128 != 0 && D % 64 == 0 ? 64 : 128; }
+// CTAs an SM holds of the decode (by shared memory and registers), for head
+// size D and `heads` query heads a CTA.
+constexpr int paged_fp8_ctas(int D, int heads) { return D > 128 ? 1 : (D == 64 && heads <= 4 ? 3 : 2); }
+// tmKV: the cache as bytes {D, Hkv, 2 * num_blocks * 128}, box {paged_fp8_box(D), 1, 128}.
 cudaError_t launch_paged_fp8(int D, const CUtensorMap& tmKV, const PagedFp8Params& p, cudaStream_t stream);
 
 // Padding mask <-> packed varlen (masks.cu).  mask [B, S] bytes (nonzero =
