@@ -72,14 +72,15 @@ struct Fp8Cfg {
     static constexpr int HALF_BYTES = NPC * PIECE_BYTES;
     static constexpr int SLOT_BYTES = 2 * HALF_BYTES;
     static constexpr int CTAS = paged_fp8_ctas(D, HG);  // per SM
-    static constexpr int STAGES = (CTAS == 3 ? 65536 : (CTAS == 2 ? 98304 : 196608)) / SLOT_BYTES;
+    static constexpr int STAGES = (CTAS == 3 ? 49152 : (CTAS == 2 ? 98304 : 196608)) / SLOT_BYTES;
     static constexpr int Q_BYTES = NCH * NQ * 128;   // one buffer of query pieces
     static constexpr int P_BYTES = NW * kTok;
     static constexpr int OFF_Q = STAGES * SLOT_BYTES;
     static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
     static constexpr int OFF_SC = OFF_P + P_BYTES;             // exponent bytes: [stage][K, V][128]
     static constexpr int OFF_RED = OFF_SC + STAGES * 256;      // [warpgroup][2][4][HT] f32
-    static constexpr int OFF_QF = OFF_RED + 2 * 4 * HG * 4;    // [2][HG] f32: 2^f * scale_log2
+    static constexpr int OFF_SUM = OFF_RED + 2 * 4 * HG * 4;   // [warpgroup][4][HT] f32 x 2: a segment's sums
+    static constexpr int OFF_QF = OFF_SUM + 4 * HG * 8;        // [2][HG] f32: 2^f * scale_log2
     static constexpr int OFF_LEN = OFF_QF + 2 * HG * 4;        // valid tokens of each slot's block
     static constexpr int OFF_BAR = (OFF_LEN + STAGES * 4 + 7) & ~7;
     static constexpr int N_BAR = 2 * STAGES + 2 + 2 + 1 + 1 + 1;
@@ -492,6 +493,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const int wg = warp / 4, tok = threadIdx.x % kWg;
         const int hw = wg * HT;  // this warpgroup's first head
         float* sred = reinterpret_cast<float*>(smem + C::OFF_RED) + wg * 2 * 4 * HT;
+        float2* ssum = reinterpret_cast<float2*>(smem + C::OFF_SUM) + wg * 4 * HT;
         // sequences without context, of this chunk's share: zeros and -inf
         auto zero_row = [&](long long s) {  // one warp
             const long long row = s * p.Hq + h0;
@@ -690,30 +692,24 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 ask_o(g - 1);
                 add_o();
                 // ---- the segment's softmax sum over the 128 token lanes, then its output
+#pragma unroll
+                for (int h = 0; h < HT; ++h) {
+                    const float mr = h & 1 ? mref[h / 2].y : mref[h / 2].x;
+                    const float m = warp_max(mr);
+                    float x = (h & 1 ? l[h / 2].y : l[h / 2].x) * ex2(mr - m);
+#pragma unroll
+                    for (int of = 16; of; of >>= 1) x += __shfl_xor_sync(0xffffffffu, x, of);
+                    if (lane == 0) ssum[(warp & 3) * HT + h] = make_float2(m, x);
+                }
+                if (named_bar_or(1 + wg, kWg, !ok)) break;
                 float inv[HT], lse2[HT];
 #pragma unroll
                 for (int h = 0; h < HT; ++h) {
-                    const float m = warp_max(h & 1 ? mref[h / 2].y : mref[h / 2].x);
-                    if (lane == 0) sred[(warp & 3) * HT + h] = m;
-                }
-                named_bar_sync(1 + wg, kWg);
-                float mall[HT];
-#pragma unroll
-                for (int h = 0; h < HT; ++h) {
-                    const float m = fmaxf(fmaxf(sred[h], sred[HT + h]), fmaxf(sred[2 * HT + h], sred[3 * HT + h]));
-                    float x = h & 1 ? l[h / 2].y * ex2(mref[h / 2].y - m) : l[h / 2].x * ex2(mref[h / 2].x - m);
-#pragma unroll
-                    for (int of = 16; of; of >>= 1) x += __shfl_xor_sync(0xffffffffu, x, of);
-                    if (lane == 0) sred[4 * HT + (warp & 3) * HT + h] = x;
-                    mall[h] = m;
-                }
-                if (named_bar_or(1 + wg, kWg, !ok)) break;
-#pragma unroll
-                for (int h = 0; h < HT; ++h) {
-                    const float* x = sred + 4 * HT + h;
-                    const float all = (x[0] + x[HT]) + (x[2 * HT] + x[3 * HT]);
-                    inv[h] = all == 0.f ? 0.f : ex2((h & 1 ? R[h / 2].y : R[h / 2].x) - mall[h]) / all;
-                    lse2[h] = all == 0.f ? -INFINITY : mall[h] + __log2f(all);
+                    const float2 a = ssum[h], b = ssum[HT + h], c = ssum[2 * HT + h], d = ssum[3 * HT + h];
+                    const float m = fmaxf(fmax3(a.x, b.x, c.x), d.x);
+                    const float all = (a.y * ex2(a.x - m) + b.y * ex2(b.x - m)) + (c.y * ex2(c.x - m) + d.y * ex2(d.x - m));
+                    inv[h] = all == 0.f ? 0.f : __fdividef(ex2((h & 1 ? R[h / 2].y : R[h / 2].x) - m), all);  // 2^-22 off at most
+                    lse2[h] = all == 0.f ? -INFINITY : m + __log2f(all);
                 }
                 const bool whole = w.b0 == 0 && w.b1 == w.nblk;
                 if (!CLUSTER && threadIdx.x == 0 && w.b0 == 0 && w.b1 < w.nblk) {
@@ -762,7 +758,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 }
                 ++seg;
                 more = w.next(p);
-                if (more) named_bar_sync(1 + wg, kWg);  // the reduction scratch is free again
             }
         }
         if (!ok) *abort_flag = 1;
@@ -814,7 +809,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // ---------------------------------------------------- products
         // Unit by unit: S^T of the next unit, whose buffer was read before the
         // weights of the unit before came; then, once this unit's weights are
-        // there, O^T.
+        // there, O^T.  (Taking whichever is ready first frees value blocks
+        // earlier, but was slower: 7.1 -> 6.6 TB/s at D = 128.)
         const uint32_t id_s = idesc_f8(128, NQ, p.e5m2 ? 1u : 0u, false, false);
         const uint32_t id_o = idesc_f8(128, NW, p.e5m2 ? 1u : 0u, true, true);
         int kslot = 0, vslot = 0, seg = -1;
@@ -842,11 +838,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             }
             return true;
         };
-        ok = issue_s(0);
-        for (uint32_t i = 0; ok && i < n_units; ++i) {
-            if (i + 1 < n_units) ok = issue_s(i + 1);
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(b_pfull, i & 1, abort_flag));
-            if (!ok) break;
+        auto issue_o = [&]() {
             tc_fence_after();
             if (elect_one()) {
                 // V^T's rows past D (lanes that nobody reads) are zeros or repeat the block's only box
@@ -862,6 +854,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             }
             __syncwarp();
             if (++vslot == STAGES) vslot = 0;
+        };
+        ok = issue_s(0);
+        for (uint32_t i = 0; ok && i < n_units; ++i) {
+            if (i + 1 < n_units) ok = issue_s(i + 1);
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(b_pfull, i & 1, abort_flag));
+            if (ok) issue_o();
         }
         if (!ok) *abort_flag = 1;
         if (elect_one()) mma_commit(b_done);  // every product issued has finished before TMEM is freed
@@ -925,50 +923,66 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
 // Joins the partials of a sequence that crosses chunks: chunk c's second slot
 // (the sequence begins there), the first slots of the chunks up to its last.
-// One CTA a (chunk, query head), its threads in groups of D / 4 that take the
-// partials in turn, each with a running maximum, joined through shared memory;
-// where no sequence begins that goes on, the CTA leaves at once.
-constexpr int kJoin = 256;
+// One CTA a (chunk, query head): groups of D / 4 threads take the partials in
+// turn, kLoad loads in flight each, the first of them asked for before every
+// warp finds the largest lse for itself; then one group adds the groups' sums.
+// Where no sequence begins that goes on, the CTA leaves at once.
+constexpr int kJoin = 256, kLoad = 6;
 __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params p, int D) {
     __shared__ float4 so[kJoin];
-    __shared__ float2 sm[kJoin / 16];
-    const int c = blockIdx.x, h = blockIdx.y;
+    __shared__ float ssum[kJoin / 16];
+    const int c = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
     const int per = D / 4, groups = kJoin / per, grp = threadIdx.x / per, t = threadIdx.x % per;
     grid_dependency_wait();  // launched behind the decode grid, whose partials it reads
     const int2 j = p.joins[c];
     // a decode that gave up may not have written its join: nothing out of range is followed
     if (j.x < 0 || j.x >= p.num_seqs || j.y <= c || j.y >= p.chunks) return;
-    float m = kLow, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (grp < groups) {
-#pragma unroll 4
-        for (int i = c + grp; i <= j.y; i += groups) {
-            const long long r = (static_cast<long long>(i) * 2 + (i == c ? 1 : 0)) * p.Hq + h;
-            const float x = p.part_lse[r];
-            const float4 v = reinterpret_cast<const float4*>(p.part_o + r * D)[t];
-            const float mn = fmaxf(m, x), a = ex2(m - mn), w = ex2(x - mn);
-            m = mn;
-            sum = fmaf(sum, a, w);
-            acc.x = fmaf(acc.x, a, w * v.x);
-            acc.y = fmaf(acc.y, a, w * v.y);
-            acc.z = fmaf(acc.z, a, w * v.z);
-            acc.w = fmaf(acc.w, a, w * v.w);
+    const int n = grp < groups ? j.y - c + 1 : 0;
+    auto slot = [&](int i) { return (static_cast<long long>(c + i) * 2 + (i == 0 ? 1 : 0)) * p.Hq + h; };
+    float w[kLoad];
+    float4 v[kLoad];
+    auto ask = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < kLoad; ++k) {
+            const int i = i0 + k * groups;
+            w[k] = -INFINITY;
+            if (i < n) {
+                w[k] = p.part_lse[slot(i)];
+                v[k] = reinterpret_cast<const float4*>(p.part_o + slot(i) * D)[t];
+            }
         }
-        so[threadIdx.x] = acc;
-        if (t == 0) sm[grp] = make_float2(m, sum);
+    };
+    ask(grp);
+    float m = kLow;
+    for (int i = lane; i <= j.y - c; i += 32) m = fmaxf(m, p.part_lse[slot(i)]);
+    m = warp_max(m);
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = grp; i0 < n;) {
+#pragma unroll
+        for (int k = 0; k < kLoad; ++k) {
+            if (i0 + k * groups >= n) break;
+            const float x = ex2(w[k] - m);
+            sum += x;
+            acc.x = fmaf(x, v[k].x, acc.x);
+            acc.y = fmaf(x, v[k].y, acc.y);
+            acc.z = fmaf(x, v[k].z, acc.z);
+            acc.w = fmaf(x, v[k].w, acc.w);
+        }
+        i0 += groups * kLoad;
+        ask(i0);
     }
+    so[threadIdx.x] = acc;
+    if (t == 0 && grp < groups) ssum[grp] = sum;
     __syncthreads();
     if (grp != 0) return;
-    for (int g = 1; g < groups && c + g <= j.y; ++g) {
-        const float2 ms = sm[g];
-        const float4 v = so[g * per + t];
-        const float mn = fmaxf(m, ms.x), a = ex2(m - mn), w = ex2(ms.x - mn);
-        m = mn;
-        sum = sum * a + ms.y * w;
-        acc.x = acc.x * a + v.x * w;
-        acc.y = acc.y * a + v.y * w;
-        acc.z = acc.z * a + v.z * w;
-        acc.w = acc.w * a + v.w * w;
+    for (int g = 1; g < groups && g < n; ++g) {
+        const float4 b = so[g * per + t];
+        sum += ssum[g];
+        acc.x += b.x;
+        acc.y += b.y;
+        acc.z += b.z;
+        acc.w += b.w;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long row = static_cast<long long>(j.x) * p.Hq + h;
