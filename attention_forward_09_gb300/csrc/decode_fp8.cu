@@ -226,36 +226,49 @@ __device__ __forceinline__ int clamp_len(const PagedFp8Params& p, int s) {
 }
 __device__ __forceinline__ int blocks_of(int L) { return (L + kTok - 1) / kTok; }
 
-// U units are cut into N = min(chunks, U) runs, none of them empty: chunk c < N
-// holds units [c U / N, (c + 1) U / N), the others none.
-__device__ __forceinline__ long long chunk_start(long long c, long long U, long long N) { return c >= N ? U : c * U / N; }
+// U units (fewer than 2^31) are cut into N = min(chunks, U) runs that differ by
+// one unit at most, none of them empty; chunks from N on hold none.
+struct Cut {
+    uint32_t U, per, more;  // the first `more` of N runs hold per + 1 units, the others per
+    __device__ __forceinline__ Cut(uint32_t U_, uint32_t chunks) : U(U_) {
+        const uint32_t N = U < chunks ? U : chunks;
+        per = N ? U / N : 0;
+        more = N ? U - per * N : 0;
+    }
+    __device__ __forceinline__ uint32_t start(uint32_t c) const {  // first unit of chunk c
+        return min(U, c * per + min(c, more));  // (c * per + c <= U + chunks)
+    }
+    __device__ __forceinline__ uint32_t chunk_of(uint32_t u) const {  // the chunk that holds unit u < U
+        const uint32_t a = more * (per + 1);
+        return u < a ? u / (per + 1) : more + (u - a) / per;
+    }
+};
 
 // A warp's walk over its chunk's segments: [b0, b1) of sequence s, of `nblk`
 // blocks in all.  Every lane of the warp calls next(); the lengths of 32
 // sequences are held across the lanes.
 struct Walk {
     int s, L, nblk, b0, b1;
-    long long rem;  // units of the chunk after this segment
+    int rem;  // units of the chunk after this segment
     int base, Llane;
 
     __device__ __forceinline__ void load(const PagedFp8Params& p, int lane) {
         const int i = base + lane;
         Llane = i < p.num_seqs ? clamp_len(p, i) : 0;
     }
-    __device__ __forceinline__ void take(int lane, long long n, int from) {
+    __device__ __forceinline__ void take(int n, int from) {
         L = __shfl_sync(0xffffffffu, Llane, s - base);
         nblk = blocks_of(L);
         b0 = from;
-        const long long left = nblk - from;
-        b1 = from + static_cast<int>(left < n ? left : n);
+        b1 = from + min(nblk - from, n);
         rem = n - (b1 - b0);
     }
-    __device__ __forceinline__ void start(const PagedFp8Params& p, int s0, int off, long long n) {
+    __device__ __forceinline__ void start(const PagedFp8Params& p, int s0, int off, int n) {
         const int lane = threadIdx.x & 31;
         s = s0;
         base = s0;
         load(p, lane);
-        take(lane, n, off);
+        take(n, off);
     }
     // The next sequence that has tokens; false when the chunk is done.
     __device__ __forceinline__ bool next(const PagedFp8Params& p) {
@@ -265,7 +278,7 @@ struct Walk {
             const unsigned has = __ballot_sync(0xffffffffu, Llane > 0 && base + lane > s);
             if (has) {
                 s = base + __ffs(static_cast<int>(has)) - 1;
-                take(lane, rem, 0);
+                take(rem, 0);
                 return true;
             }
             s = base + 31;
@@ -358,10 +371,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     auto b_sfull = [&](int i) { return bar0 + 8 * (2 * STAGES + i); };
     auto b_qfull = [&](int i) { return bar0 + 8 * (2 * STAGES + 2 + i); };
     const uint32_t b_pfull = bar0 + 8 * (2 * STAGES + 4), b_ofull = b_pfull + 8, b_done = b_pfull + 16;
-    __shared__ int abort_storage, s_skip;
+    __shared__ int abort_storage;
     __shared__ uint32_t tmem_base_storage, s_issued;  // s_issued: blocks whose loads were issued
-    __shared__ long long s_sum[WARPS];
-    __shared__ long long s_u[3];  // u0, u1, U
+    __shared__ uint32_t s_sum[WARPS];
+    __shared__ uint32_t s_u[3];   // u0, u1, U
     __shared__ int s_first[2];    // first sequence, first block of it
     __shared__ int2 s_join;       // as PagedFp8Params::joins, of this chunk
     __shared__ int s_parts;       // of a cluster: the parts its sequence is in, where more than one
@@ -378,9 +391,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
     // ---- this chunk's units: the total, then the sequence its first unit lies
     // in.  Lengths are read once where a pass of the block covers them all.
+    const uint32_t given_up = threadIdx.x == 0 && status_has_timeout(p.status, kDevTimeout);
     const bool one_pass = p.num_seqs <= C::THREADS;
     const int own = CLUSTER ? blockIdx.x / (p.chunks * p.n_hgroups) : 0;  // a cluster's sequence
-    long long sum = 0;
+    uint32_t sum = 0;
     int T = 0;
     bool bad = false;
     for (int s = CLUSTER ? own : threadIdx.x; s < (CLUSTER ? own + 1 : p.num_seqs); s += C::THREADS) {
@@ -407,7 +421,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         s_parts = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmKV);
-        s_skip = status_has_timeout(p.status, kDevTimeout);
     }
     if (warp == SOFT_WARPS) {
         tmem_alloc(smem_u32(&tmem_base_storage), C::TM_COLS);
@@ -416,58 +429,58 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     if (bad && (CLUSTER ? threadIdx.x == 0 : blockIdx.x == 0) && p.status) atomicOr(p.status, kDevBadSeqlen);
     if constexpr (CLUSTER) {
         if (threadIdx.x == 0) {
-            const long long N = T < p.chunks ? T : p.chunks;
-            const long long u0 = chunk_start(chunk, T, N);
-            s_u[0] = u0;
-            s_u[1] = s_skip ? u0 : chunk_start(chunk + 1, T, N);
+            const Cut cut(T, p.chunks);
+            s_u[0] = cut.start(chunk);
+            s_u[1] = given_up ? s_u[0] : cut.start(chunk + 1);
             s_u[2] = T;
             s_first[0] = own;
-            s_first[1] = static_cast<int>(u0);
-            s_parts = N > 1 ? static_cast<int>(N) : 0;
+            s_first[1] = static_cast<int>(s_u[0]);
+            s_parts = T > 1 ? min(T, p.chunks) : 0;
         }
     } else {
-        long long incl = sum;
+        uint32_t incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long n = __shfl_up_sync(0xffffffffu, incl, o);
+            const uint32_t n = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += n;
         }
         if (lane == 31) s_sum[warp] = incl;
         __syncthreads();
-        long long U = 0, before = 0;
+        uint32_t U = 0, before = 0;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
             if (w < warp) before += s_sum[w];
             U += s_sum[w];
         }
-        const long long N = U < p.chunks ? U : p.chunks;
-        const long long u0 = chunk_start(chunk, U, N), u1 = chunk_start(chunk + 1, U, N);
+        const Cut cut(U, p.chunks);
+        const uint32_t u0 = cut.start(chunk), u1 = cut.start(chunk + 1);
         if (threadIdx.x == 0) {
             s_u[0] = u0;
-            s_u[1] = s_skip ? u0 : u1;  // after a give-up nothing more is begun
+            s_u[1] = given_up ? u0 : u1;  // after a give-up nothing more is begun
             s_u[2] = U;
         }
         if (one_pass) {
-            const long long at = before + incl - T;  // units before sequence threadIdx.x
+            const uint32_t at = before + incl - T;  // units before sequence threadIdx.x
             if (T > 0 && at <= u0 && u0 < at + T) {
                 s_first[0] = threadIdx.x;
                 s_first[1] = static_cast<int>(u0 - at);
             }
         } else if (u1 > u0) {
-            long long run = 0;
+            uint32_t run = 0;
+#pragma unroll 1
             for (int base = 0; base < p.num_seqs && run <= u0; base += C::THREADS) {  // run <= u0: not found yet (uniform)
                 const int s = base + threadIdx.x;
                 T = s < p.num_seqs ? blocks_of(clamp_len(p, s)) : 0;
                 incl = T;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const long long n = __shfl_up_sync(0xffffffffu, incl, o);
+                    const uint32_t n = __shfl_up_sync(0xffffffffu, incl, o);
                     if (lane >= o) incl += n;
                 }
                 __syncthreads();  // s_sum was read by all
                 if (lane == 31) s_sum[warp] = incl;
                 __syncthreads();
-                long long at = run + incl - T;
+                uint32_t at = run + incl - T;
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) {
                     if (w < warp) at += s_sum[w];
@@ -484,8 +497,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_base_storage;
-    const long long u1 = s_u[1], U = s_u[2];
-    const uint32_t n_units = static_cast<uint32_t>(u1 - s_u[0]);
+    const uint32_t n_units = s_u[1] - s_u[0];
     bool ok = true;
 
     if (warp < SOFT_WARPS) {
@@ -494,36 +506,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const int hw = wg * HT;  // this warpgroup's first head
         float* sred = reinterpret_cast<float*>(smem + C::OFF_RED) + wg * 2 * 4 * HT;
         float2* ssum = reinterpret_cast<float2*>(smem + C::OFF_SUM) + wg * 4 * HT;
-        // sequences without context, of this chunk's share: zeros and -inf
-        auto zero_row = [&](long long s) {  // one warp
-            const long long row = s * p.Hq + h0;
-            for (int i = lane; i < nh * D; i += 32) {
-                if (p.out_f32)
-                    static_cast<float*>(p.out)[row * D + i] = 0.f;
-                else
-                    static_cast<uint16_t*>(p.out)[row * D + i] = 0;
-            }
-            if (lane < nh && p.lse) p.lse[row + lane] = -INFINITY;
-        };
-        auto zero_empty = [&]() {
-            if constexpr (CLUSTER) {
-                if (U == 0 && chunk == 0 && warp == 0) zero_row(own);
-            } else {
-                for (long long i0 = warp * 32; i0 * p.chunks < p.num_seqs; i0 += C::SOFT) {
-                    const long long s = chunk + (i0 + lane) * p.chunks;
-                    unsigned none = __ballot_sync(0xffffffffu, s < p.num_seqs && clamp_len(p, static_cast<int>(s)) == 0);
-                    for (; none; none &= none - 1) zero_row(chunk + (i0 + __ffs(static_cast<int>(none)) - 1) * p.chunks);
-                }
-            }
-        };
-        if (n_units == 0) zero_empty();
         if (n_units > 0) {
             Walk w, ahead;  // `ahead` is one segment further: its queries are laid out early
             w.start(p, s_first[0], s_first[1], n_units);
             ahead = w;
             Queries<C> qs;
             qs.load(p, w.s, h0, nh, warp, lane);
-            zero_empty();  // while they come
             qs.put(p, smem + C::OFF_Q, sqf, warp, lane);
             fence_proxy_async_smem();
             __syncwarp();
@@ -610,10 +598,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                         d[h] = __fadd2_rn(u[h], make_float2(-mref[h].x, -mref[h].y));
                         dmax = fmax3(dmax, d[h].x, d[h].y);
                     }
-                    if (dmax > 60.f) {  // rarely: fp32 has room for sums of 2^60 and more
+                    if (__any_sync(0xffffffffu, dmax > 60.f)) {  // rarely: fp32 has room for sums of 2^60 and more
 #pragma unroll
                         for (int h = 0; h < HT / 2; ++h) {
-                            const float2 m = make_float2(d[h].x > 60.f ? u[h].x : mref[h].x, d[h].y > 60.f ? u[h].y : mref[h].y);
+                            const float2 m = make_float2(fmaxf(mref[h].x, warp_max(u[h].x)), fmaxf(mref[h].y, warp_max(u[h].y)));
                             l[h] = make_float2(l[h].x * ex2(mref[h].x - m.x), l[h].y * ex2(mref[h].y - m.y));
                             mref[h] = m;
                             d[h] = make_float2(u[h].x - m.x, u[h].y - m.y);
@@ -691,31 +679,47 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 if (quit) break;
                 ask_o(g - 1);
                 add_o();
-                // ---- the segment's softmax sum over the 128 token lanes, then its output
-#pragma unroll
-                for (int h = 0; h < HT; ++h) {
-                    const float mr = h & 1 ? mref[h / 2].y : mref[h / 2].x;
-                    const float m = warp_max(mr);
-                    float x = (h & 1 ? l[h / 2].y : l[h / 2].x) * ex2(mr - m);
-#pragma unroll
-                    for (int of = 16; of; of >>= 1) x += __shfl_xor_sync(0xffffffffu, x, of);
-                    if (lane == 0) ssum[(warp & 3) * HT + h] = make_float2(m, x);
+                // ---- the segment's softmax sum over the 128 token lanes, then its output.
+                // A warp's HT sums at once: while there are several, a lane gives
+                // away one half of its heads and keeps the other.
+                float hsum;
+                if constexpr (HT == 4) {
+                    const bool up = lane & 16, up2 = lane & 8;
+                    float2 a = up ? l[1] : l[0];
+                    const float2 b = up ? l[0] : l[1];
+                    a.x += __shfl_xor_sync(0xffffffffu, b.x, 16);
+                    a.y += __shfl_xor_sync(0xffffffffu, b.y, 16);
+                    hsum = (up2 ? a.y : a.x) + __shfl_xor_sync(0xffffffffu, up2 ? a.x : a.y, 8);
+                } else {
+                    static_assert(HT == 2, "");
+                    const bool up = lane & 16;
+                    hsum = (up ? l[0].y : l[0].x) + __shfl_xor_sync(0xffffffffu, up ? l[0].x : l[0].y, 16);
+                    hsum += __shfl_xor_sync(0xffffffffu, hsum, 8);
                 }
+#pragma unroll
+                for (int of = 4; of; of >>= 1) hsum += __shfl_xor_sync(0xffffffffu, hsum, of);
+                const int hl = HT == 4 ? lane >> 3 : lane >> 4;  // this lane's head
+                float mh = mref[0].x, Rh = R[0].x;
+#pragma unroll
+                for (int h = 1; h < HT; ++h)
+                    if (hl == h) {
+                        mh = h & 1 ? mref[h / 2].y : mref[h / 2].x;
+                        Rh = h & 1 ? R[h / 2].y : R[h / 2].x;
+                    }
+                if ((lane & 7) == 0) ssum[(warp & 3) * HT + hl] = make_float2(mh, hsum);
                 if (named_bar_or(1 + wg, kWg, !ok)) break;
-                float inv[HT], lse2[HT];
+                const float2 sa = ssum[hl], sb2 = ssum[HT + hl], sc2 = ssum[2 * HT + hl], sd = ssum[3 * HT + hl];
+                const float mt = fmaxf(fmax3(sa.x, sb2.x, sc2.x), sd.x);
+                const float all = (sa.y * ex2(sa.x - mt) + sb2.y * ex2(sb2.x - mt)) + (sc2.y * ex2(sc2.x - mt) + sd.y * ex2(sd.x - mt));
+                const float inv_l = all == 0.f ? 0.f : __fdividef(ex2(Rh - mt), all);  // 2^-22 off at most
+                const float lse_l = all == 0.f ? -INFINITY : mt + __log2f(all);
+                float inv[HT];
 #pragma unroll
-                for (int h = 0; h < HT; ++h) {
-                    const float2 a = ssum[h], b = ssum[HT + h], c = ssum[2 * HT + h], d = ssum[3 * HT + h];
-                    const float m = fmaxf(fmax3(a.x, b.x, c.x), d.x);
-                    const float all = (a.y * ex2(a.x - m) + b.y * ex2(b.x - m)) + (c.y * ex2(c.x - m) + d.y * ex2(d.x - m));
-                    inv[h] = all == 0.f ? 0.f : __fdividef(ex2((h & 1 ? R[h / 2].y : R[h / 2].x) - m), all);  // 2^-22 off at most
-                    lse2[h] = all == 0.f ? -INFINITY : m + __log2f(all);
-                }
+                for (int h = 0; h < HT; ++h) inv[h] = __shfl_sync(0xffffffffu, inv_l, h * (32 / HT));
                 const bool whole = w.b0 == 0 && w.b1 == w.nblk;
                 if (!CLUSTER && threadIdx.x == 0 && w.b0 == 0 && w.b1 < w.nblk) {
                     // this segment's sequence begins here and goes on: up to the chunk of its last unit
-                    const long long N = U < p.chunks ? U : p.chunks, end = u1 + (w.nblk - w.b1);
-                    s_join = make_int2(w.s, static_cast<int>((end * N + U - 1) / U - 1));
+                    s_join = make_int2(w.s, static_cast<int>(Cut(s_u[2], p.chunks).chunk_of(s_u[1] + (w.nblk - w.b1) - 1)));
                 }
                 // Partials: in the workspace, slot 1 where the sequence begins and slot 0
                 // where it goes on; or, of a cluster, in the first slot of the ring, which
@@ -744,25 +748,19 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                         }
                     }
                 }
-                if (tok == 0) {
-#pragma unroll
-                    for (int k = 0; k < HT; ++k) {
-                        const int h = hw + k;
-                        if (h < nh) {
-                            if (!whole)
-                                pl[h] = lse2[k];
-                            else if (p.lse)
-                                p.lse[row + h] = lse2[k] * kLn2f;
-                        }
-                    }
+                if ((warp & 3) == 0 && (lane & (32 / HT - 1)) == 0 && hw + hl < nh) {
+                    if (!whole)
+                        pl[hw + hl] = lse_l;
+                    else if (p.lse)
+                        p.lse[row + hw + hl] = lse_l * kLn2f;
                 }
                 ++seg;
                 more = w.next(p);
             }
         }
         if (!ok) *abort_flag = 1;
-    } else if (n_units > 0) {
-        if (warp == SOFT_WARPS) {
+    } else if (warp == SOFT_WARPS) {
+        if (n_units > 0) {
             // ------------------------------------------------ cache loads
             Walk w;
             w.start(p, s_first[0], s_first[1], n_units);
@@ -805,7 +803,28 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 }
             }
             if (!ok) *abort_flag = 1;
+        }
+        // sequences without context, of this chunk's share: zeros and -inf
+        auto zero_row = [&](long long s) {
+            const long long row = s * p.Hq + h0;
+            for (int i = lane; i < nh * D; i += 32) {
+                if (p.out_f32)
+                    static_cast<float*>(p.out)[row * D + i] = 0.f;
+                else
+                    static_cast<uint16_t*>(p.out)[row * D + i] = 0;
+            }
+            if (lane < nh && p.lse) p.lse[row + lane] = -INFINITY;
+        };
+        if constexpr (CLUSTER) {
+            if (s_u[2] == 0 && chunk == 0) zero_row(own);
         } else {
+            for (long long i0 = 0; i0 * p.chunks < p.num_seqs; i0 += 32) {
+                const long long s = chunk + (i0 + lane) * p.chunks;
+                unsigned none = __ballot_sync(0xffffffffu, s < p.num_seqs && clamp_len(p, static_cast<int>(s)) == 0);
+                for (; none; none &= none - 1) zero_row(chunk + (i0 + __ffs(static_cast<int>(none)) - 1) * p.chunks);
+            }
+        }
+    } else if (n_units > 0) {
         // ---------------------------------------------------- products
         // Unit by unit: S^T of the next unit, whose buffer was read before the
         // weights of the unit before came; then, once this unit's weights are
@@ -865,7 +884,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         if (elect_one()) mma_commit(b_done);  // every product issued has finished before TMEM is freed
         __syncwarp();
         mbar_wait_drain(b_done, 0);
-        }
     }
     __syncthreads();
     if (*abort_flag) {
