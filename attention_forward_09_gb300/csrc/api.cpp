@@ -654,9 +654,9 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
     if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(kv_scales) || !aligned16(out) || q_stride % 8 != 0)
         return GBATTN_ERR_ALIGNMENT;
     if (num_seqs == 0) return GBATTN_OK;
-    // units of work (128-token blocks of all sequences) are counted in 32 bits
+    // units of work (a sequence's 128-token blocks and one more) are counted in 32 bits
     const long long blocks = (max_seq_len + 127LL) / 128;
-    if (num_seqs * (blocks < max_blocks_per_seq ? blocks : max_blocks_per_seq) > 0x7fffffffLL)
+    if (num_seqs * ((blocks < max_blocks_per_seq ? blocks : max_blocks_per_seq) + 1) > 0x7fffffffLL)
         return GBATTN_ERR_UNSUPPORTED;
     const gbattn::PagedFp8Plan plan = gbattn::paged_fp8_plan(num_seqs, Hq, Hkv, D, max_seq_len);
     if (plan.n_hgroups * plan.chunks > 0x7fffffffLL || Hq > 65535) return GBATTN_ERR_UNSUPPORTED;
