@@ -567,6 +567,8 @@ gbattn_status attn_kv_cache_write_fp8(const void* key, const void* value, long l
     if (num_tokens < 0) return GBATTN_ERR_INVALID_ARG;
     const long long row = static_cast<long long>(Hkv) * D;
     if (num_tokens > 1 && (key_stride < row || value_stride < row)) return GBATTN_ERR_INVALID_ARG;
+    // the kernel numbers the (token, K or V, head) rows in 32 bits
+    if (2LL * num_tokens * Hkv >= 0xFFF00000LL) return GBATTN_ERR_UNSUPPORTED;
     if (num_tokens == 0) return GBATTN_OK;
     if (!key || !value || !slot_mapping || !kv_cache || !kv_scales) return GBATTN_ERR_INVALID_ARG;
     if (!aligned16(key) || !aligned16(value) || !aligned16(kv_cache) || !aligned16(kv_scales) || key_stride % 8 != 0 ||
@@ -588,6 +590,10 @@ gbattn_status attn_kv_cache_write_fp8(const void* key, const void* value, long l
     p.num_blocks = num_blocks;
     p.block_size = block_size;
     p.Hkv = Hkv;
+    p.wide = ((reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(value)) & 31) == 0 &&
+             (num_tokens == 1 || (key_stride % 16 == 0 && value_stride % 16 == 0));
+    p.by_heads = gbattn::FastDiv::of(static_cast<uint32_t>(Hkv));
+    p.by_block = gbattn::FastDiv::of(static_cast<uint32_t>(block_size));
     p.e5m2 = kv_dtype == GBATTN_KV_E5M2;
     p.status = dev_status;
     return gbattn::launch_cache_write_fp8(p, D, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -624,6 +630,7 @@ gbattn_status attn_kv_cache_read_fp8(const void* kv_cache, const uint8_t* kv_sca
     p.Hkv = Hkv;
     p.D = D;
     p.total = Tk;
+    p.by_block = gbattn::FastDiv::of(static_cast<uint32_t>(block_size));
     p.e5m2 = kv_dtype == GBATTN_KV_E5M2;
     p.status = dev_status;
     return gbattn::launch_cache_read_fp8(p, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GBATTN_OK

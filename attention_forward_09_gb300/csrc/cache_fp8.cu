@@ -38,96 +38,107 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t x) {
 }
 
 // ---------------------------------------------------------------- write
-// LPR lanes share a row, each VPL vectors of 8 bf16 (D = 8 LPR VPL), so a
-// row's maximum is log2(LPR) shuffles and a warp takes 32 / LPR heads at once.
+// LPR lanes share a row, each VPL vectors of 16 bf16 (D = 16 LPR VPL): wide
+// loads (a whole 32-byte sector), wide stores (16 codes), log2(LPR) shuffles
+// for the row's maximum, and RPW rows a warp.
 template <int D>
 struct WriteCfg {
-    static constexpr int VPL = D % 96 == 0 ? 3 : 1;
-    static constexpr int LPR = D / 8 / VPL;
+    static constexpr int VPL = D % 96 == 0 ? 3 : 2;
+    static constexpr int LPR = D / 16 / VPL;
     static constexpr int RPW = 32 / LPR;
-    static_assert(LPR * VPL * 8 == D && 32 % LPR == 0, "lane map");
+    static_assert(LPR * VPL * 16 == D && 32 % LPR == 0, "lane map");
 };
 
-// A warp takes one (token, K or V): its heads in steps of RPW, kUnroll steps'
-// loads in flight, asked for before the slot is known.
+struct Vec16 {  // 16 bf16
+    uint32_t x[8];
+};
+__device__ __forceinline__ Vec16 ld_32B(const uint4* p, bool wide) {  // wide: p is a multiple of 32
+    Vec16 r;
+    if (wide) {
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r.x[0]), "=r"(r.x[1]), "=r"(r.x[2]), "=r"(r.x[3]), "=r"(r.x[4]), "=r"(r.x[5]), "=r"(r.x[6]),
+                       "=r"(r.x[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = ld_once(p), b = ld_once(p + 1);
+        r = Vec16{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    }
+    return r;
+}
+
+// The rows of all tokens, K and V and heads are numbered in a line, and a warp
+// takes RPW of them at a time whatever the number of heads; its loads are in
+// flight together, asked for before the slots are known.  (Two turns' loads in
+// flight gain 2% on a prefill of 27654 tokens and lose 13% on 4099.)
 template <int D, bool E5M2>
 __global__ void __launch_bounds__(256) kv_cache_write_fp8_sm103a(const CacheWriteFp8Params p) {
     using C = WriteCfg<D>;
-    constexpr int kUnroll = C::VPL == 1 ? 4 : 2;
     const int lane = threadIdx.x & 31;
     const int sub = lane / C::LPR, lr = lane % C::LPR;
-    const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
-    for (long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; w < 2 * p.num_tokens; w += nwarps) {
-        const long long t = w >> 1;
-        const int half = static_cast<int>(w & 1);  // 0: key, 1: value
+    const uint32_t rows = static_cast<uint32_t>(p.num_tokens) * 2u * p.Hkv;  // below 2^32 - 2^20
+    const uint32_t step = ((gridDim.x * blockDim.x) >> 5) * C::RPW;
+    for (uint32_t r0 = ((blockIdx.x * blockDim.x + threadIdx.x) >> 5) * C::RPW; r0 < rows; r0 += step) {
+        const bool live = r0 + sub < rows;
+        const uint32_t row = live ? r0 + sub : r0;
+        const uint32_t th = p.by_heads.div(row);  // 2 * token + half (0: key, 1: value)
+        const uint32_t h = row - th * p.Hkv;
+        const long long t = th >> 1;
+        const int half = th & 1;
         const int slot = p.slot_mapping[t];
-        const uint4* src = reinterpret_cast<const uint4*>(half ? p.value + t * p.value_stride : p.key + t * p.key_stride);
-        for (int h0 = sub; h0 - sub < p.Hkv; h0 += C::RPW * kUnroll) {
-            uint4 r[kUnroll][C::VPL];
+        const uint4* src = reinterpret_cast<const uint4*>(half ? p.value + t * p.value_stride : p.key + t * p.key_stride) +
+                           h * (D / 8) + 2 * lr;
+        Vec16 r[C::VPL];
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int h = h0 + k * C::RPW;
+        for (int v = 0; v < C::VPL; ++v) r[v] = ld_32B(src + 2 * v * C::LPR, p.wide);
+        uint32_t mx = 0;
 #pragma unroll
-                for (int v = 0; v < C::VPL; ++v) {
-                    r[k][v] = make_uint4(0u, 0u, 0u, 0u);
-                    if (h < p.Hkv) r[k][v] = ld_once(src + h * (D / 8) + lr + v * C::LPR);
+        for (int v = 0; v < C::VPL; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx = absmax_bf16x2(mx, r[v].x[i]);
+#pragma unroll
+        for (int o = 1; o < C::LPR; o <<= 1) mx = absmax_bf16x2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        uint32_t m16 = max(mx & 0xFFFFu, mx >> 16);
+        if (__any_sync(0xffffffffu, m16 >= 0x7F80u)) {  // an infinity somewhere: infinities become NaN, maximum again
+            uint32_t mi = 0;
+#pragma unroll
+            for (int v = 0; v < C::VPL; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t& x = r[v].x[i];
+                    if ((x & 0x7FFFu) == 0x7F80u) x |= 0x7Fu;
+                    if ((x & 0x7FFF0000u) == 0x7F800000u) x |= 0x7F0000u;
+                    mi = absmax_bf16x2(mi, x);
                 }
+#pragma unroll
+            for (int o = 1; o < C::LPR; o <<= 1) mi = absmax_bf16x2(mi, __shfl_xor_sync(0xffffffffu, mi, o));
+            m16 = max(mi & 0xFFFFu, mi >> 16);
+        }
+        // max = 1.f * 2^(E - 127), c_max = 1.75 * 2^n: b = E - n, one more if 1.f > 1.75
+        const int E = static_cast<int>(m16 >> 7);
+        int b = E - (E5M2 ? 15 : 8) + ((m16 & 0x7Fu) > 0x60u ? 1 : 0);
+        b = b < 1 ? 1 : b;
+        const float inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);  // 2^(127 - b), exact
+        if (!live || slot < 0) continue;  // a padding token
+        if (slot >= p.num_slots) {
+            if (lr == 0 && p.status) atomicOr(p.status, kDevBadIndex);
+            continue;
+        }
+        uint8_t* dst = p.cache + ((static_cast<long long>(half) * p.num_slots + slot) * p.Hkv + h) * D + lr * 16;
+#pragma unroll
+        for (int v = 0; v < C::VPL; ++v) {
+            uint32_t c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t x = r[v].x[i];
+                c[i] = pack_fp8x2<E5M2>(__uint_as_float(x << 16) * inv, __uint_as_float(x & 0xFFFF0000u) * inv);
             }
-            if (slot < 0) break;  // padding token (warp-uniform)
-            if (slot >= p.num_slots) {
-                if (lane == 0 && p.status) atomicOr(p.status, kDevBadIndex);
-                break;
-            }
-            const int block = slot / p.block_size, at = slot - block * p.block_size;
-            uint8_t* dst = p.cache + (static_cast<long long>(half) * p.num_slots + slot) * p.Hkv * D;
-            uint8_t* exps = p.scales + (static_cast<long long>(half) * p.num_blocks + block) * p.Hkv * p.block_size + at;
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int h = h0 + k * C::RPW;
-                uint32_t mx = 0;
-#pragma unroll
-                for (int v = 0; v < C::VPL; ++v) {
-                    mx = absmax_bf16x2(mx, r[k][v].x);
-                    mx = absmax_bf16x2(mx, r[k][v].y);
-                    mx = absmax_bf16x2(mx, r[k][v].z);
-                    mx = absmax_bf16x2(mx, r[k][v].w);
-                }
-#pragma unroll
-                for (int o = 1; o < C::LPR; o <<= 1) mx = absmax_bf16x2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                uint32_t m16 = max(mx & 0xFFFFu, mx >> 16);
-                if (__any_sync(0xffffffffu, m16 >= 0x7F80u)) {  // an infinity somewhere: infinities become NaN, maximum again
-                    uint32_t mi = 0;
-#pragma unroll
-                    for (int v = 0; v < C::VPL; ++v) {
-                        uint32_t* x = reinterpret_cast<uint32_t*>(&r[k][v]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if ((x[i] & 0x7FFFu) == 0x7F80u) x[i] |= 0x7Fu;
-                            if ((x[i] & 0x7FFF0000u) == 0x7F800000u) x[i] |= 0x7F0000u;
-                            mi = absmax_bf16x2(mi, x[i]);
-                        }
-                    }
-#pragma unroll
-                    for (int o = 1; o < C::LPR; o <<= 1) mi = absmax_bf16x2(mi, __shfl_xor_sync(0xffffffffu, mi, o));
-                    m16 = max(mi & 0xFFFFu, mi >> 16);
-                }
-                // max = 1.f * 2^(E - 127), c_max = 1.75 * 2^n: b = E - n, one more if 1.f > 1.75
-                const int E = static_cast<int>(m16 >> 7);
-                int b = E - (E5M2 ? 15 : 8) + ((m16 & 0x7Fu) > 0x60u ? 1 : 0);
-                b = b < 1 ? 1 : b;
-                const float inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);  // 2^(127 - b), exact
-                if (h >= p.Hkv) continue;
-#pragma unroll
-                for (int v = 0; v < C::VPL; ++v) {
-                    const uint32_t x[4] = {r[k][v].x, r[k][v].y, r[k][v].z, r[k][v].w};
-                    uint32_t c[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        c[i] = pack_fp8x2<E5M2>(__uint_as_float(x[i] << 16) * inv, __uint_as_float(x[i] & 0xFFFF0000u) * inv);
-                    *reinterpret_cast<uint2*>(dst + h * D + (lr + v * C::LPR) * 8) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-                }
-                if (lr == 0) exps[static_cast<long long>(h) * p.block_size] = static_cast<uint8_t>(b);
-            }
+            *reinterpret_cast<uint4*>(dst + v * C::LPR * 16) =
+                make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
+        }
+        if (lr == 0) {
+            const int block = static_cast<int>(p.by_block.div(slot)), at = slot - block * p.block_size;
+            p.scales[((static_cast<long long>(half) * p.num_blocks + block) * p.Hkv + h) * p.block_size + at] =
+                static_cast<uint8_t>(b);
         }
     }
 }
@@ -157,90 +168,91 @@ __device__ __forceinline__ void st_32B(uint4* p, const uint32_t (&x)[8]) {
     }
 }
 
-// A warp takes TOK consecutive packed rows: lane i the 16-code vectors i, i +
-// 32, ... of each token's keys and values, [2][Hkv][D] in turn, kAhead of them
-// asked for at once.  The sequence is found by a binary search for the first
-// row and by stepping on for the others.  TOK is 2; 1 where that leaves SMs
-// without a warp.
-template <int D, bool E5M2, int TOK>
-__global__ void __launch_bounds__(256) kv_cache_read_fp8_sm103a(const CacheReadFp8Params p) {
-    constexpr int kAhead = 2;
+// A warp takes `group` consecutive packed rows (a power of two up to 32): lane u
+// finds where row u lies (a binary search for its sequence, the table), all of
+// them at once; then the lanes share the rows' 16-code vectors, [group][2][Hkv]
+// [D / 16] in a line whatever the number of heads, kAhead each in flight.
+template <int D, bool E5M2>
+__global__ void __launch_bounds__(256, 5) kv_cache_read_fp8_sm103a(const CacheReadFp8Params p, int group) {
+    constexpr int kAhead = 4;
     const int lane = threadIdx.x & 31;
     const int nwarps = static_cast<int>((gridDim.x * blockDim.x) >> 5);
-    const int groups = (p.total + TOK - 1) / TOK;
-    const int vecs = p.Hkv * (D / 16);
+    const int groups = (p.total + group - 1) / group;
+    const int vecs = p.Hkv * (D / 16), n = 2 * vecs;  // vectors of a token's keys; of its keys and values
     for (int g = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5); g < groups; g += nwarps) {
-        const int t0 = g * TOK;
-        const int end = p.cu[p.num_seqs];
-        int s = 0, hi = p.num_seqs;  // cu[s] <= t0 < cu[hi], were cu in order
-        while (hi - s > 1) {
-            const int mid = (s + hi) >> 1;
-            if (p.cu[mid] <= t0) s = mid; else hi = mid;
+        const int t0 = g * group, t = t0 + lane;
+        int slot = -1, at = 0;  // the row's cache slot (-1: not written, -2: zeros), its place in the block
+        if (lane < group && t < p.total && t < p.cu[p.num_seqs]) {
+            int s = 0, hi = p.num_seqs;  // cu[s] <= t < cu[hi], were cu in order
+            while (hi - s > 1) {
+                const int mid = (s + hi) >> 1;
+                if (p.cu[mid] <= t) s = mid; else hi = mid;
+            }
+            const int c0 = p.cu[s], c1 = p.cu[s + 1], pos = t - c0;
+            if (c0 < 0 || pos < 0 || t >= c1 || c1 > p.total ||
+                static_cast<int>(p.by_block.div(c1 - 1 - c0)) >= p.max_blocks) {
+                if (p.status) atomicOr(p.status, kDevBadSeqlen);
+            } else {
+                const int bi = static_cast<int>(p.by_block.div(pos));
+                const int blk = p.block_table[static_cast<long long>(s) * p.max_blocks + bi];
+                at = pos - bi * p.block_size;
+                if (blk < 0 || blk >= p.num_blocks) {
+                    if (p.status) atomicOr(p.status, kDevBadIndex);
+                    slot = -2;
+                } else {
+                    slot = blk * p.block_size + at;
+                }
+            }
         }
-        if (t0 >= end) continue;  // behind the last sequence: left as they are
-        int c0 = p.cu[s], c1 = p.cu[s + 1];
-        long long row[TOK], exps[TOK];  // first vector of the token's keys; its first exponent byte
-        int kind[TOK];                  // 0: not written, 1: zeros, 2: read
-#pragma unroll
-        for (int u = 0; u < TOK; ++u) {
-            const int t = t0 + u;
-            kind[u] = 0;
-            row[u] = exps[u] = 0;
-            while (t >= c1 && s + 1 < p.num_seqs) {
-                ++s;
-                c0 = c1;
-                c1 = p.cu[s + 1];
-            }
-            if (t >= p.total || t >= c1) continue;
-            const int pos = t - c0, bi = pos / p.block_size;
-            if (c0 < 0 || pos < 0 || c1 > p.total || (c1 - 1 - c0) / p.block_size >= p.max_blocks) {
-                if (lane == 0 && p.status) atomicOr(p.status, kDevBadSeqlen);
-                continue;
-            }
-            const int blk = p.block_table[static_cast<long long>(s) * p.max_blocks + bi];
-            if (blk < 0 || blk >= p.num_blocks) {
-                if (lane == 0 && p.status) atomicOr(p.status, kDevBadIndex);
-                kind[u] = 1;
-                continue;
-            }
-            const int at = pos - bi * p.block_size;
-            kind[u] = 2;
-            row[u] = (static_cast<long long>(blk) * p.block_size + at) * vecs;
-            exps[u] = static_cast<long long>(blk) * p.Hkv * p.block_size + at;
-        }
-        for (int i0 = lane; i0 < 2 * vecs; i0 += 32 * kAhead) {
-            uint4 c[kAhead][TOK];
-            int b[kAhead][TOK];
+        int u = 0, i = lane;  // the lane's next vector: row u of the group, vector i of it
+        for (int q = 0; q < group * n; q += 32 * kAhead) {
+            uint4 c[kAhead];
+            int b[kAhead], sl[kAhead], tu[kAhead], j[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const int i = i0 + 32 * k, half = i >= vecs, j = i - (half ? vecs : 0), h = j / (D / 16);
-#pragma unroll
-                for (int u = 0; u < TOK; ++u) {
-                    c[k][u] = make_uint4(0u, 0u, 0u, 0u);
-                    b[k][u] = 1;
-                    if (kind[u] == 2 && i < 2 * vecs) {
-                        c[k][u] = ld_once(reinterpret_cast<const uint4*>(p.cache) + (half ? p.num_slots * vecs : 0) + row[u] + j);
-                        b[k][u] = p.scales[(half ? p.num_slots * p.Hkv : 0) + exps[u] + static_cast<long long>(h) * p.block_size];
-                    }
+                while (i >= n) {
+                    i -= n;
+                    ++u;
                 }
+                sl[k] = __shfl_sync(0xffffffffu, slot, u & 31);
+                const int au = __shfl_sync(0xffffffffu, at, u & 31);
+                if (u >= group) sl[k] = -1;
+                tu[k] = t0 + u;
+                j[k] = i;
+                const int half = i >= vecs, v = i - (half ? vecs : 0);
+                c[k] = make_uint4(0u, 0u, 0u, 0u);
+                b[k] = 1;
+                if (sl[k] >= 0) {
+                    const long long row = (half ? p.num_slots : 0) + sl[k];
+                    c[k] = ld_once(reinterpret_cast<const uint4*>(p.cache) + row * vecs + v);
+                    b[k] = p.scales[(row - au) * p.Hkv + static_cast<long long>(v / (D / 16)) * p.block_size + au];
+                }
+                i += 32;
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const int i = i0 + 32 * k, half = i >= vecs, j = i - (half ? vecs : 0);
-#pragma unroll
-                for (int u = 0; u < TOK; ++u) {
-                    if (kind[u] == 0 || i >= 2 * vecs) continue;
-                    uint32_t x[8];
-                    decode16<E5M2>(c[k][u], exp2_byte(b[k][u]), x);
-                    st_32B((half ? p.v : p.k) + (static_cast<long long>(t0 + u) * vecs + j) * 2, x);
-                }
+                if (sl[k] == -1) continue;
+                uint32_t x[8];
+                decode16<E5M2>(c[k], exp2_byte(b[k]), x);
+                const int half = j[k] >= vecs;
+                st_32B((half ? p.v : p.k) + (static_cast<long long>(tu[k]) * vecs + j[k] - (half ? vecs : 0)) * 2, x);
             }
         }
     }
 }
 
+unsigned warp_grid(long long warps, int num_sms) {
+    // CTAs of 8 warps; 40 an SM, so that they are dealt out as SMs come free (8 an
+    // SM: a prefill's write 30.9 -> 29.0 us so, 16 contexts read 272 -> 264 us)
+    const long long cap = static_cast<long long>(num_sms > 0 ? num_sms : 1) * 40;
+    const long long g = (warps + 7) / 8;
+    return static_cast<unsigned>(g < 1 ? 1 : (g > cap ? cap : g));
+}
+
 template <int D>
-cudaError_t write_d(const CacheWriteFp8Params& p, unsigned grid, cudaStream_t st) {
+cudaError_t write_d(const CacheWriteFp8Params& p, int num_sms, cudaStream_t st) {
+    constexpr int rows = WriteCfg<D>::RPW;  // a warp's turn
+    const unsigned grid = warp_grid((p.num_tokens * 2 * p.Hkv + rows - 1) / rows, num_sms);
     if (p.e5m2)
         kv_cache_write_fp8_sm103a<D, true><<<grid, 256, 0, st>>>(p);
     else
@@ -248,37 +260,31 @@ cudaError_t write_d(const CacheWriteFp8Params& p, unsigned grid, cudaStream_t st
     return cudaGetLastError();
 }
 
-unsigned warp_grid(long long warps, int num_sms) {
-    const long long cap = static_cast<long long>(num_sms > 0 ? num_sms : 1) * 8;  // 8 CTAs of 8 warps per SM
-    const long long g = (warps + 7) / 8;
-    return static_cast<unsigned>(g < 1 ? 1 : (g > cap ? cap : g));
-}
-
-template <int D, bool E5M2>
-cudaError_t read_tok(const CacheReadFp8Params& p, int num_sms, cudaStream_t st) {
-    if (p.total / 2 >= num_sms * 8)
-        kv_cache_read_fp8_sm103a<D, E5M2, 2><<<warp_grid((p.total + 1) / 2, num_sms), 256, 0, st>>>(p);
-    else
-        kv_cache_read_fp8_sm103a<D, E5M2, 1><<<warp_grid(p.total, num_sms), 256, 0, st>>>(p);
-    return cudaGetLastError();
-}
-
 template <int D>
 cudaError_t read_d(const CacheReadFp8Params& p, int num_sms, cudaStream_t st) {
-    return p.e5m2 ? read_tok<D, true>(p, num_sms, st) : read_tok<D, false>(p, num_sms, st);
+    // rows a warp: enough to fill its loads while every SM still has a few warps,
+    // and up to 16 where that leaves every SM some 160 warps' turns
+    const int n = 2 * p.Hkv * (D / 16);
+    int group = 1;
+    while (group < 16 && ((group * n < 128 && p.total / (2 * group) >= num_sms * 8) || p.total / (2 * group) >= num_sms * 160)) group *= 2;
+    const unsigned grid = warp_grid((p.total + group - 1) / group, num_sms);
+    if (p.e5m2)
+        kv_cache_read_fp8_sm103a<D, true><<<grid, 256, 0, st>>>(p, group);
+    else
+        kv_cache_read_fp8_sm103a<D, false><<<grid, 256, 0, st>>>(p, group);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_cache_write_fp8(const CacheWriteFp8Params& p, int D, int num_sms, cudaStream_t st) {
     if (p.num_tokens <= 0) return cudaSuccess;
-    const unsigned grid = warp_grid(p.num_tokens * 2, num_sms);
     switch (D) {
-        case 64: return write_d<64>(p, grid, st);
-        case 96: return write_d<96>(p, grid, st);
-        case 128: return write_d<128>(p, grid, st);
-        case 192: return write_d<192>(p, grid, st);
-        case 256: return write_d<256>(p, grid, st);
+        case 64: return write_d<64>(p, num_sms, st);
+        case 96: return write_d<96>(p, num_sms, st);
+        case 128: return write_d<128>(p, num_sms, st);
+        case 192: return write_d<192>(p, num_sms, st);
+        case 256: return write_d<256>(p, num_sms, st);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -960,18 +960,34 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
 // Joins the partials of a sequence that crosses chunks: chunk c's second slot
 // (the sequence begins there), the first slots of the chunks up to its last.
-// One CTA a (chunk, query head): groups of D / 4 threads take the partials in
-// turn, kLoad loads in flight each, the first of them asked for before every
-// warp finds the largest lse for itself; then one group adds the groups' sums.
-// Where no sequence begins that goes on, the CTA leaves at once.  Small CTAs
-// where a sequence has few partials, so that all of them run at once.
+// Groups of `width` / 4 threads take the partials in turn, kLoad loads in
+// flight each, the first of them asked for before every warp finds the largest
+// lse for itself; then one group adds the groups' sums.
+//   Many sequences (few partials each): a small CTA a (chunk, query head), which
+// leaves at once where no sequence begins that goes on.
+//   Few sequences: a CTA a (sequence, query head, 32 columns), which finds the
+// sequence's chunk among the joins.  (Two sequences of 76 partials, D = 256, 8
+// heads: 4.6 us a (chunk, head) with 256 threads, -JOIN- us so.)
 constexpr int kJoin = 256, kJoinSmall = 64, kLoad = 6;
-__global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params p, int D) {
+__global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params p, int D, int width) {
     __shared__ float4 so[kJoin];
-    __shared__ float ssum[kJoin / 16];
-    const int c = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
-    const int per = D / 4, groups = blockDim.x / per, grp = threadIdx.x / per, t = threadIdx.x % per;
+    __shared__ float ssum[kJoin / 8];
+    __shared__ int s_chunk;
+    const int h = blockIdx.y, lane = threadIdx.x & 31;
+    const int per = width / 4, groups = blockDim.x / per, grp = threadIdx.x / per, t = blockIdx.z * per + threadIdx.x % per;
+    int c = blockIdx.x;
+    if (width != D) {
+        if (threadIdx.x == 0) s_chunk = -1;
+        __syncthreads();
+    }
     grid_dependency_wait();  // launched behind the decode grid, whose partials it reads
+    if (width != D) {
+        for (int i = threadIdx.x; i < p.chunks; i += blockDim.x)
+            if (p.joins[i].x == static_cast<int>(blockIdx.x)) s_chunk = i;  // one at most
+        __syncthreads();
+        c = s_chunk;
+        if (c < 0) return;
+    }
     const int2 j = p.joins[c];
     // a decode that gave up may not have written its join: nothing out of range is followed
     if (j.x < 0 || j.x >= p.num_seqs || j.y <= c || j.y >= p.chunks) return;
@@ -1011,11 +1027,11 @@ __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params 
         ask(i0);
     }
     so[threadIdx.x] = acc;
-    if (t == 0 && grp < groups) ssum[grp] = sum;
+    if (threadIdx.x % per == 0 && grp < groups) ssum[grp] = sum;
     __syncthreads();
     if (grp != 0) return;
     for (int g = 1; g < groups && g < n; ++g) {
-        const float4 b = so[g * per + t];
+        const float4 b = so[g * per + threadIdx.x];
         sum += ssum[g];
         acc.x += b.x;
         acc.y += b.y;
@@ -1066,10 +1082,13 @@ cudaError_t launch_cfg(const CUtensorMap& tm, const PagedFp8Params& p, cudaStrea
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>(p.Hq));
-    cfg.blockDim = dim3(p.chunks < 8 * p.num_seqs ? kJoinSmall : kJoin);
+    const bool few = p.num_seqs * 8 <= p.chunks;
+    const int width = few ? 32 : C::D;
+    cfg.gridDim = few ? dim3(static_cast<unsigned>(p.num_seqs), static_cast<unsigned>(p.Hq), C::D / 32)
+                      : dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>(p.Hq));
+    cfg.blockDim = dim3(few ? kJoin : kJoinSmall);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, paged_fp8_combine, p, static_cast<int>(C::D));
+    e = cudaLaunchKernelEx(&cfg, paged_fp8_combine, p, static_cast<int>(C::D), width);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

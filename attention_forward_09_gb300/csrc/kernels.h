@@ -134,6 +134,26 @@ cudaError_t launch_cache_write(const CacheWriteParams& p, int num_sms, cudaStrea
 // 8-bit KV cache (cache_fp8.cu): codes [2, num_blocks, block_size, Hkv, D]
 // (e4m3fn, or e5m2) and one exponent byte a row, [2, num_blocks, Hkv,
 // block_size]; a code c of exponent byte b stands for c * 2^(b - 127).
+
+// Division of numbers below 2^31 (div) by a divisor fixed on the host: with
+// 2^s >= d, m = floor(2^32 (2^s - d) / d) + 1, n / d = (hi32(n m) + n) >> s;
+// n below 2^32 as long as the sum is kept in 33 bits.
+struct FastDiv {
+    uint32_t m;
+    int s;
+    static FastDiv of(uint32_t d) {
+        FastDiv f{0, 0};
+        while (f.s < 32 && (1ull << f.s) < d) ++f.s;
+        f.m = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.s) - d)) / d + 1);
+        return f;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t div(uint32_t n) const {
+        return static_cast<uint32_t>((static_cast<uint64_t>(__umulhi(n, m)) + n) >> s);
+    }
+#endif
+};
+
 struct CacheWriteFp8Params {
     const uint16_t* key;  // bf16 [T, Hkv, D], token t at t * key_stride elements
     const uint16_t* value;
@@ -144,6 +164,8 @@ struct CacheWriteFp8Params {
     long long num_tokens;
     long long num_slots;  // num_blocks * block_size
     int num_blocks, block_size, Hkv;
+    FastDiv by_heads, by_block;  // by Hkv, by block_size
+    bool wide;                   // key, value and the strides are multiples of 32 bytes
     int e5m2;
     uint32_t* status;
 };
@@ -158,6 +180,7 @@ struct CacheReadFp8Params {
     uint4* v;
     long long num_slots;
     int num_seqs, max_blocks, num_blocks, block_size, Hkv, D, total;
+    FastDiv by_block;
     int e5m2;
     uint32_t* status;
 };

@@ -126,6 +126,13 @@ def test_write_strided_tokens_and_one_token_tensors():
     gb.attn_kv_cache_write_fp8(k.contiguous(), v.contiguous(), slots, *b)
     assert np.array_equal(raw(a[0]), raw(b[0])) and torch.equal(a[1], b[1])
     assert int(a[1][0, 0, :, :T].min()) > 0
+    # starts and strides that are multiples of 16 bytes only
+    odd = torch.zeros(T * (hkv * D + 8) + 8, dtype=torch.bfloat16, device=dev())[8:].view(T, hkv * D + 8)
+    odd = odd[:, :hkv * D].unflatten(1, (hkv, D))
+    odd.copy_(k)
+    c = tuple(torch.zeros_like(t) for t in a)
+    gb.attn_kv_cache_write_fp8(odd, v, slots, *c)
+    assert np.array_equal(raw(c[0]), raw(b[0])) and torch.equal(c[1], b[1])
     gb.attn_kv_cache_write_fp8(k[3:4], v[3:4], slots[:1].contiguous(), *a)  # a stride that is never used
     gb.attn_kv_cache_write_fp8(k[3:4].contiguous(), v[3:4].contiguous(), slots[:1].contiguous(), *b)
     assert np.array_equal(raw(a[0]), raw(b[0])) and torch.equal(a[1], b[1])
