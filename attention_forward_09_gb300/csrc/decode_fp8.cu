@@ -68,7 +68,7 @@ struct Fp8Cfg {
     static constexpr int NPC = (D + PW - 1) / PW;    // boxes of 128 rows (the last zero-filled past D)
     static constexpr int PIECE_BYTES = kTok * PW;    // a slot: value boxes, then key boxes
     static constexpr int NQ = up16(2 * HG);          // columns of S^T: piece * HG + head
-    static constexpr int NW = up16(NP * HG);         // columns of O^T: (warpgroup * NP + piece) * HT + head
+    static constexpr int NW = NWG * 16;               // columns of O^T: warpgroup * 16 + piece * HT + head
     static constexpr int HALF_BYTES = NPC * PIECE_BYTES;
     static constexpr int SLOT_BYTES = 2 * HALF_BYTES;
     static constexpr int CTAS = paged_fp8_ctas(D, HG);  // per SM
@@ -90,6 +90,7 @@ struct Fp8Cfg {
     static constexpr int TM_COLS = pow2_cols(2 * NQ + NCH * NW);
     static_assert((SMEM_BYTES + 1024 + 256) * CTAS <= 233472, "shared memory budget");
     static_assert(TM_COLS * CTAS <= 512, "tensor memory budget");
+    static_assert(NP * HT <= 16, "a warpgroup's pieces of weights are one 16-byte row a token");
     static_assert(HG * (D + 1) * 4 <= SLOT_BYTES, "a cluster's partials lie in the first slot");
 };
 
@@ -553,21 +554,29 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     if (!mbar_wait(b_ofull, gi & 1, abort_flag)) ok = false;
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < NCH; ++c) tmem_ld<NP * HT>(tm + tlane + C::TM_O + c * NW + wg * NP * HT, ro[c]);
+                    for (int c = 0; c < NCH; ++c) tmem_ld<NP * HT>(tm + tlane + C::TM_O + c * NW + wg * 16, ro[c]);
                 };
                 auto add_o = [&]() {
                     float2 beta[HT / 2];
+                    float dm = kLow;
 #pragma unroll
                     for (int h = 0; h < HT / 2; ++h) {
-                        if (M8[h].x > R[h].x + 40.f || M8[h].y > R[h].y + 40.f) {  // same in every thread
+                        beta[h] = __fadd2_rn(M8[h], make_float2(-R[h].x, -R[h].y));
+                        dm = fmax3(dm, beta[h].x, beta[h].y);
+                    }
+                    if (dm > 40.f) {  // a larger reference, the same in every thread
+#pragma unroll
+                        for (int h = 0; h < HT / 2; ++h) {
                             const float2 n = make_float2(fmaxf(R[h].x, M8[h].x), fmaxf(R[h].y, M8[h].y));
                             const float2 a = make_float2(ex2(R[h].x - n.x), ex2(R[h].y - n.y));
                             R[h] = n;
+                            beta[h] = make_float2(M8[h].x - n.x, M8[h].y - n.y);
 #pragma unroll
                             for (int c = 0; c < NCH; ++c) o[c][h] = __fmul2_rn(o[c][h], a);
                         }
-                        beta[h] = make_float2(ex2(M8[h].x - R[h].x), ex2(M8[h].y - R[h].y));
                     }
+#pragma unroll
+                    for (int h = 0; h < HT / 2; ++h) beta[h] = make_float2(ex2(beta[h].x), ex2(beta[h].y));
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < NCH; ++c)
@@ -590,8 +599,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     const int nvalid = slen[slot] & (kNewSeg - 1);
                     const bool valid = tok < nvalid;
                     const uint8_t* sc = smem + C::OFF_SC + slot * 256;
-                    const float kf = exp2_byte(sc[tok]);
-                    const float ev = static_cast<float>(static_cast<int>(sc[128 + tok]) - 127);
+                    // 2^(b - 127) (for b = 0, 2^-127, zero is as good: no score feels it), and
+                    // b - 127 by way of 2^23 + b
+                    const float kf = __uint_as_float(static_cast<uint32_t>(sc[tok]) << 23);
+                    const float ev = __uint_as_float(0x4B000000u | sc[128 + tok]) - (8388608.f + 127.f);
                     if (!mbar_wait(b_sfull(g & 1), (g >> 1) & 1, abort_flag)) ok = false;
                     tc_fence_after();
                     uint32_t r0[HT], r1[HT];
@@ -629,8 +640,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     }
                     float* red = sred + (g & 1) * 4 * HT;
                     if (lane == 0) {
-#pragma unroll
-                        for (int h = 0; h < HT; h += 2) *reinterpret_cast<float2*>(red + (warp & 3) * HT + h) = make_float2(m[h], m[h + 1]);
+                        if constexpr (HT == 4)
+                            *reinterpret_cast<float4*>(red + (warp & 3) * HT) = make_float4(m[0], m[1], m[2], m[3]);
+                        else
+                            *reinterpret_cast<float2*>(red + (warp & 3) * HT) = make_float2(m[0], m[1]);
                     }
                     if (b > w.b0) ask_o(g - 1);
                     if (named_bar_or(1 + wg, kWg, !ok)) {  // a warpgroup's four warps leave together
@@ -647,17 +660,26 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                         }
                     }
                     if (b > w.b0) add_o();  // the weights' buffer and O^T are free again
-                    // weights 256 w = 2^(u - M + 8) and their pieces
-                    constexpr int WORDS = (NP * HT + 3) / 4;
-                    uint32_t w8[WORDS];
+                    // weights 256 w = 2^(u - M + 8) and their pieces, byte piece * HT + head
+                    float wm[4][HT];  // the four warps' maxima
 #pragma unroll
-                    for (int i = 0; i < WORDS; ++i) w8[i] = 0u;
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (HT == 4) {
+                            const float4 a = *reinterpret_cast<const float4*>(red + k * HT);
+                            wm[k][0] = a.x, wm[k][1] = a.y, wm[k][2] = a.z, wm[k][3] = a.w;
+                        } else {
+                            const float2 a = *reinterpret_cast<const float2*>(red + k * HT);
+                            wm[k][0] = a.x, wm[k][1] = a.y;
+                        }
+                    }
+                    uint32_t w8[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
                     for (int h = 0; h < HT / 2; ++h) {
-                        const float2* rm = reinterpret_cast<const float2*>(red) + h;
-                        const float2 a = rm[0], b2 = rm[HT / 2], c2 = rm[HT], d2 = rm[3 * HT / 2];
-                        M8[h] = make_float2(fmaxf(fmax3(a.x, b2.x, c2.x), fmaxf(d2.x, kLow)) - 8.f,
-                                            fmaxf(fmax3(a.y, b2.y, c2.y), fmaxf(d2.y, kLow)) - 8.f);
+                        float mm[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            mm[k] = fmaxf(fmax3(wm[0][2 * h + k], wm[1][2 * h + k], wm[2][2 * h + k]), fmaxf(wm[3][2 * h + k], kLow));
+                        M8[h] = make_float2(mm[0] - 8.f, mm[1] - 8.f);
                         const float2 e = __fadd2_rn(u[h], make_float2(-M8[h].x, -M8[h].y));
                         uint32_t c[NP];
                         split_pair<NP>(make_float2(ex2(e.x), ex2(e.y)), c);
@@ -667,12 +689,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                             w8[col / 4] |= c[i] << (8 * (col & 3));
                         }
                     }
-                    // column j of token t at (j / 16) * 2048 + t * 16 + j % 16
-#pragma unroll
-                    for (int i = 0; i < WORDS; ++i) {
-                        const int col = wg * NP * HT + 4 * i;
-                        *reinterpret_cast<uint32_t*>(smem + C::OFF_P + (col / 16) * (kTok * 16) + tok * 16 + (col % 16)) = w8[i];
-                    }
+                    st_shared_v4(sb + C::OFF_P + wg * (kTok * 16) + tok * 16, w8[0], w8[1], w8[2], w8[3]);
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
