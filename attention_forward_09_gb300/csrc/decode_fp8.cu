@@ -396,22 +396,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const int kvh = hg / p.subs, sub = hg % p.subs;
     const int h0 = kvh * p.group + sub * p.heads_per_sub;
     const int nh = min(p.heads_per_sub, p.group - sub * p.heads_per_sub);
-    grid_launch_dependents();  // the combine may queue up; it waits for this grid to finish
-
-    // ---- this chunk's units: the total, then the sequence its first unit lies
-    // in.  Lengths are read once where a pass of the block covers them all.
-    const uint32_t given_up = threadIdx.x == 0 && status_has_timeout(p.status, kDevTimeout);
-    const bool one_pass = p.num_seqs <= C::THREADS;
-    const int own = CLUSTER ? blockIdx.x / (p.chunks * p.n_hgroups) : 0;  // a cluster's sequence
-    uint32_t sum = 0;
-    int T = 0;  // of a sequence: its units
-    bool bad = false;
-    for (int s = CLUSTER ? own : threadIdx.x; s < (CLUSTER ? own + 1 : p.num_seqs); s += C::THREADS) {
-        const int L = p.seq_lens[s];
-        bad |= L < 0 || L > p.cap;
-        T = units_of(L < 0 ? 0 : (L > p.cap ? p.cap : L));
-        sum += T;
-    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(b_full(i), 1);
@@ -429,13 +413,32 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         s_join = make_int2(-1, 0);
         s_parts = 0;
         s_first[2] = 0;
-        s_stop = given_up;  // after a give-up nothing more is begun
         fence_mbar_init();
         tma_prefetch_desc(&tmKV);
     }
     if (warp == SOFT_WARPS) {
         tmem_alloc(smem_u32(&tmem_base_storage), C::TM_COLS);
         tmem_relinquish();
+    }
+    // Launched as a programmatic dependent of whatever comes before on the stream:
+    // up to here nothing of global memory is read or written.
+    grid_dependency_wait();
+    grid_launch_dependents();  // the combine may queue up; it waits for this grid to finish
+
+    // ---- this chunk's units: the total, then the sequence its first unit lies
+    // in.  Lengths are read once where a pass of the block covers them all.
+    const uint32_t given_up = threadIdx.x == 0 && status_has_timeout(p.status, kDevTimeout);
+    if (threadIdx.x == 0) s_stop = given_up;  // after a give-up nothing more is begun
+    const bool one_pass = p.num_seqs <= C::THREADS;
+    const int own = CLUSTER ? blockIdx.x / (p.chunks * p.n_hgroups) : 0;  // a cluster's sequence
+    uint32_t sum = 0;
+    int T = 0;  // of a sequence: its units
+    bool bad = false;
+    for (int s = CLUSTER ? own : threadIdx.x; s < (CLUSTER ? own + 1 : p.num_seqs); s += C::THREADS) {
+        const int L = p.seq_lens[s];
+        bad |= L < 0 || L > p.cap;
+        T = units_of(L < 0 ? 0 : (L > p.cap ? p.cap : L));
+        sum += T;
     }
     if (bad && (CLUSTER ? threadIdx.x == 0 : blockIdx.x == 0) && p.status) atomicOr(p.status, kDevBadSeqlen);
     if constexpr (CLUSTER) {
@@ -998,6 +1001,7 @@ __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params 
         __syncthreads();
     }
     grid_dependency_wait();  // launched behind the decode grid, whose partials it reads
+    grid_launch_dependents();
     if (width != D) {
         for (int i = threadIdx.x; i < p.chunks; i += blockDim.x)
             if (p.joins[i].x == static_cast<int>(blockIdx.x)) s_chunk = i;  // one at most
@@ -1081,24 +1085,24 @@ cudaError_t launch_cfg(const CUtensorMap& tm, const PagedFp8Params& p, cudaStrea
             if (dev >= 0 && dev < 64) attr_done[dev] = true;
         }
     }
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.chunks) * p.n_hgroups * (CLUSTER ? p.num_seqs : 1));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = st;
     cfg.attrs = at;
+    cfg.numAttrs = 1;
     if (CLUSTER && p.chunks > 1) {
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = static_cast<unsigned>(p.chunks);
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.numAttrs = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = static_cast<unsigned>(p.chunks);
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
     }
     cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_fp8_sm103a<C, CLUSTER>, tm, p);
     if (e != cudaSuccess || CLUSTER || p.chunks == 1) return e != cudaSuccess ? e : cudaGetLastError();
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
     const bool few = p.num_seqs * 8 <= p.chunks;
     const int width = few ? 32 : C::D;
     cfg.gridDim = few ? dim3(static_cast<unsigned>(p.num_seqs), static_cast<unsigned>(p.Hq), C::D / 32)
