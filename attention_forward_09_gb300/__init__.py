@@ -375,11 +375,11 @@ def _fp8_cache(kv_cache, kv_scales):
     return code, nb, bs, hkv, d
 
 
-def _on_device(dev, *named):
+def _on_device(dev, **tensors):
     """Raise ValueError unless every tensor given is on CUDA device number dev."""
     if dev < 0:
         raise ValueError("the 8-bit cache calls take CUDA tensors")
-    for name, t in named:
+    for name, t in tensors.items():
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name} must be on cuda:{dev}, with the cache")
 
@@ -397,8 +397,17 @@ def _status_ptr(dev_status):
     return dev_status.data_ptr()
 
 
+def _host_int(name, x):
+    x = int(x)
+    if x >= 1 << 31:  # (a negative one is the library's to refuse)
+        raise ValueError(f"{name} must be below 2**31")
+    return x
+
+
 def _run_fp8(name, dev, stream, args):
     """One C call on device number dev and stream (None: the device's current one)."""
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"stream must be of cuda:{dev}, where the cache is")
     fn = getattr(_lib or load_library(), name)
     handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == torch._C._cuda_getDevice():
@@ -442,8 +451,7 @@ def attn_kv_cache_write_fp8(key, value, slot_mapping, kv_cache, kv_scales, dev_s
     if key.shape[0] != T or value.shape[0] != T:
         raise ValueError("key, value and slot_mapping disagree on the token count")
     status, dev = _status_ptr(dev_status), kv_cache.get_device()
-    _on_device(dev, ("key", key), ("value", value), ("slot_mapping", slot_mapping), ("kv_scales", kv_scales),
-               ("dev_status", dev_status))
+    _on_device(dev, key=key, value=value, slot_mapping=slot_mapping, kv_scales=kv_scales, dev_status=dev_status)
     _run_fp8("attn_kv_cache_write_fp8", dev, stream,
              (key.data_ptr(), value.data_ptr(), ks, vs, slot_mapping.data_ptr(), T, kv_cache.data_ptr(),
               kv_scales.data_ptr(), code, nb, bs, hkv, d, status))
@@ -463,9 +471,9 @@ def attn_kv_cache_read_fp8(kv_cache, kv_scales, block_table, cu_seqlens_k, total
     S = cu_seqlens_k.numel() - 1
     if S < 0 or block_table.shape[0] != S:
         raise ValueError("block_table must have a row, and cu_seqlens_k a boundary, for each sequence")
-    status, dev, T = _status_ptr(dev_status), kv_cache.get_device(), int(total_tokens)
-    _on_device(dev, ("kv_scales", kv_scales), ("block_table", block_table), ("cu_seqlens_k", cu_seqlens_k), ("k", k),
-               ("v", v), ("dev_status", dev_status))
+    status, dev, T = _status_ptr(dev_status), kv_cache.get_device(), _host_int("total_tokens", total_tokens)
+    _on_device(dev, kv_scales=kv_scales, block_table=block_table, cu_seqlens_k=cu_seqlens_k, k=k, v=v,
+               dev_status=dev_status)
     for name, t in (("k", k), ("v", v)):
         if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, hkv, d) or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{T}, {hkv}, {d}]")
@@ -475,13 +483,14 @@ def attn_kv_cache_read_fp8(kv_cache, kv_scales, block_table, cu_seqlens_k, total
         v = _empty_on(stream, kv_cache, (T, hkv, d), torch.bfloat16)
     _run_fp8("attn_kv_cache_read_fp8", dev, stream,
              (kv_cache.data_ptr(), kv_scales.data_ptr(), code, nb, bs, block_table.data_ptr(),
-              max(1, block_table.shape[1]), cu_seqlens_k.data_ptr(), S, T, hkv, d, k.data_ptr(), v.data_ptr(),
+              block_table.shape[1], cu_seqlens_k.data_ptr(), S, T, hkv, d, k.data_ptr(), v.data_ptr(),
               status))
     return k, v
 
 
 def attn_fwd_paged_fp8_workspace_size(num_seqs, Hq, Hkv, D, max_seq_len) -> int:
-    return int(load_library().attn_fwd_paged_fp8_workspace_size(num_seqs, Hq, Hkv, D, max_seq_len))
+    return int(load_library().attn_fwd_paged_fp8_workspace_size(num_seqs, Hq, Hkv, D,
+                                                                _host_int("max_seq_len", max_seq_len)))
 
 
 def attn_fwd_paged_fp8(q, kv_cache, kv_scales, block_table, seq_lens, max_seq_len, softmax_scale=None, causal=True,
@@ -502,10 +511,10 @@ def attn_fwd_paged_fp8(q, kv_cache, kv_scales, block_table, seq_lens, max_seq_le
     _index_table("seq_lens", seq_lens, 1)
     if block_table.shape[0] != S or seq_lens.shape[0] != S:
         raise ValueError("block_table and seq_lens must have a row for each of q's sequences")
-    status, dev, max_seq_len = _status_ptr(dev_status), kv_cache.get_device(), int(max_seq_len)
+    status, dev, max_seq_len = _status_ptr(dev_status), kv_cache.get_device(), _host_int("max_seq_len", max_seq_len)
     given = lse if torch.is_tensor(lse) else None
-    _on_device(dev, ("q", q), ("kv_scales", kv_scales), ("block_table", block_table), ("seq_lens", seq_lens),
-               ("out", out), ("lse", given), ("workspace", workspace), ("dev_status", dev_status))
+    _on_device(dev, q=q, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens, out=out, lse=given,
+               workspace=workspace, dev_status=dev_status)
     if out is None:
         out = _empty_on(stream, kv_cache, (S, Hq, d), out_dtype)
     elif tuple(out.shape) != (S, Hq, d) or not out.is_contiguous():

@@ -607,9 +607,10 @@ gbattn_status attn_kv_cache_read_fp8(const void* kv_cache, const uint8_t* kv_sca
                                      uint32_t* dev_status, void* stream) {
     gbattn_status s = check_fp8_cache(num_blocks, block_size, Hkv, D, kv_dtype);
     if (s != GBATTN_OK) return s;
-    if (num_seqs < 0 || Tk < 0 || max_blocks_per_seq <= 0) return GBATTN_ERR_INVALID_ARG;
+    if (num_seqs < 0 || Tk < 0 || max_blocks_per_seq < 0) return GBATTN_ERR_INVALID_ARG;
     if (Tk > 0x7fffffff - 64) return GBATTN_ERR_UNSUPPORTED;  // row counters are 32-bit on the device
     if (num_seqs == 0 || Tk == 0) return GBATTN_OK;
+    if (max_blocks_per_seq == 0) return GBATTN_ERR_INVALID_ARG;
     if (!kv_cache || !kv_scales || !block_table || !cu_seqlens_k || !k || !v) return GBATTN_ERR_INVALID_ARG;
     if (!aligned16(kv_cache) || !aligned16(kv_scales) || !aligned16(k) || !aligned16(v)) return GBATTN_ERR_ALIGNMENT;
     DeviceInfo di;

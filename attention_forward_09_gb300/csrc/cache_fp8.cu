@@ -266,7 +266,7 @@ cudaError_t read_d(const CacheReadFp8Params& p, int num_sms, cudaStream_t st) {
     // and up to 16 where that leaves every SM some 160 warps' turns
     const int n = 2 * p.Hkv * (D / 16);
     int group = 1;
-    while (group < 16 && ((group * n < 128 && p.total / (2 * group) >= num_sms * 8) || p.total / (2 * group) >= num_sms * 160)) group *= 2;
+    while (group < 16 && n < (1 << 20) && ((group * n < 128 && p.total / (2 * group) >= num_sms * 8) || p.total / (2 * group) >= num_sms * 160)) group *= 2;
     const unsigned grid = warp_grid((p.total + group - 1) / group, num_sms);
     if (p.e5m2)
         kv_cache_read_fp8_sm103a<D, true><<<grid, 256, 0, st>>>(p, group);

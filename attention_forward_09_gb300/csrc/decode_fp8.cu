@@ -416,14 +416,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         fence_mbar_init();
         tma_prefetch_desc(&tmKV);
     }
-    if (warp == SOFT_WARPS) {
-        tmem_alloc(smem_u32(&tmem_base_storage), C::TM_COLS);
-        tmem_relinquish();
-    }
     // Launched as a programmatic dependent of whatever comes before on the stream:
     // up to here nothing of global memory is read or written.
     grid_dependency_wait();
     grid_launch_dependents();  // the combine may queue up; it waits for this grid to finish
+    // Tensor memory only now: the grid before may have CTAs here that still ask for theirs.
+    if (warp == SOFT_WARPS) {
+        tmem_alloc(smem_u32(&tmem_base_storage), C::TM_COLS);
+        tmem_relinquish();
+    }
 
     // ---- this chunk's units: the total, then the sequence its first unit lies
     // in.  Lengths are read once where a pass of the block covers them all.
