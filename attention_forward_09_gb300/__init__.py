@@ -364,24 +364,24 @@ _KV_CODE = {torch.float8_e4m3fn: KV_E4M3, torch.float8_e5m2: KV_E5M2}
 
 def _fp8_cache(kv_cache, kv_scales):
     """(code format, num_blocks, block_size, Hkv, D) of an 8-bit cache."""
-    code = _KV_CODE.get(kv_cache.dtype)
-    if code is None or kv_cache.dim() != 5 or kv_cache.shape[0] != 2:
+    code, shape = _KV_CODE.get(kv_cache.dtype), kv_cache.shape
+    if code is None or len(shape) != 5 or shape[0] != 2:
         raise ValueError("kv_cache must be a float8_e4m3fn or float8_e5m2 tensor [2, num_blocks, block_size, Hkv, D]")
-    _, nb, bs, hkv, d = kv_cache.shape
-    if kv_scales.dtype != torch.uint8 or tuple(kv_scales.shape) != (2, nb, hkv, bs):
+    _, nb, bs, hkv, d = shape
+    if kv_scales.dtype != torch.uint8 or kv_scales.shape != (2, nb, hkv, bs):
         raise ValueError(f"kv_scales must be a uint8 tensor [2, {nb}, {hkv}, {bs}] (num_blocks, Hkv, block_size)")
-    if not kv_cache.is_contiguous() or not kv_scales.is_contiguous():
+    if not (kv_cache.is_contiguous() and kv_scales.is_contiguous()):
         raise ValueError("kv_cache and kv_scales must be contiguous")
     return code, nb, bs, hkv, d
 
 
-def _on_device(dev, **tensors):
+def _on_device(dev, names, *tensors):
     """Raise ValueError unless every tensor given is on CUDA device number dev."""
     if dev < 0:
         raise ValueError("the 8-bit cache calls take CUDA tensors")
-    for name, t in tensors.items():
+    for i, t in enumerate(tensors):
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on cuda:{dev}, with the cache")
+            raise ValueError(f"{names.split()[i]} must be on cuda:{dev}, with the cache")
 
 
 def _index_table(name, t, dim):
@@ -429,11 +429,13 @@ def _empty_on(stream, like, shape, dtype):
 
 def _token_rows(name, t, heads, d):
     """Element stride between the tokens of a bf16 [T, heads, D] tensor whose [heads, D] rows are contiguous."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+    shape = t.shape
+    if t.dtype != torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != d:
         raise ValueError(f"{name} must be a bfloat16 tensor [tokens, {heads}, {d}]")
-    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+    tokens, row, col = t.stride()
+    if (d > 1 and col != 1) or (heads > 1 and row != d):
         raise ValueError(f"{name}: a token's [heads, D] must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    return tokens if shape[0] > 1 else heads * d
 
 
 def attn_kv_cache_write_fp8(key, value, slot_mapping, kv_cache, kv_scales, dev_status=None, stream=None):
@@ -451,7 +453,7 @@ def attn_kv_cache_write_fp8(key, value, slot_mapping, kv_cache, kv_scales, dev_s
     if key.shape[0] != T or value.shape[0] != T:
         raise ValueError("key, value and slot_mapping disagree on the token count")
     status, dev = _status_ptr(dev_status), kv_cache.get_device()
-    _on_device(dev, key=key, value=value, slot_mapping=slot_mapping, kv_scales=kv_scales, dev_status=dev_status)
+    _on_device(dev, "key value slot_mapping kv_scales dev_status", key, value, slot_mapping, kv_scales, dev_status)
     _run_fp8("attn_kv_cache_write_fp8", dev, stream,
              (key.data_ptr(), value.data_ptr(), ks, vs, slot_mapping.data_ptr(), T, kv_cache.data_ptr(),
               kv_scales.data_ptr(), code, nb, bs, hkv, d, status))
@@ -472,8 +474,8 @@ def attn_kv_cache_read_fp8(kv_cache, kv_scales, block_table, cu_seqlens_k, total
     if S < 0 or block_table.shape[0] != S:
         raise ValueError("block_table must have a row, and cu_seqlens_k a boundary, for each sequence")
     status, dev, T = _status_ptr(dev_status), kv_cache.get_device(), _host_int("total_tokens", total_tokens)
-    _on_device(dev, kv_scales=kv_scales, block_table=block_table, cu_seqlens_k=cu_seqlens_k, k=k, v=v,
-               dev_status=dev_status)
+    _on_device(dev, "kv_scales block_table cu_seqlens_k k v dev_status", kv_scales, block_table, cu_seqlens_k, k, v,
+               dev_status)
     for name, t in (("k", k), ("v", v)):
         if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (T, hkv, d) or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{T}, {hkv}, {d}]")
@@ -505,7 +507,7 @@ def attn_fwd_paged_fp8(q, kv_cache, kv_scales, block_table, seq_lens, max_seq_le
     code, nb, bs, hkv, d = _fp8_cache(kv_cache, kv_scales)
     if q.dim() != 3:
         raise ValueError("q must be [S, Hq, D]")
-    S, Hq = q.shape[0], q.shape[1]
+    S, Hq, _ = q.shape
     qs = _token_rows("q", q, Hq, d)
     _index_table("block_table", block_table, 2)
     _index_table("seq_lens", seq_lens, 1)
@@ -513,18 +515,18 @@ def attn_fwd_paged_fp8(q, kv_cache, kv_scales, block_table, seq_lens, max_seq_le
         raise ValueError("block_table and seq_lens must have a row for each of q's sequences")
     status, dev, max_seq_len = _status_ptr(dev_status), kv_cache.get_device(), _host_int("max_seq_len", max_seq_len)
     given = lse if torch.is_tensor(lse) else None
-    _on_device(dev, q=q, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens, out=out, lse=given,
-               workspace=workspace, dev_status=dev_status)
+    _on_device(dev, "q kv_scales block_table seq_lens out lse workspace dev_status", q, kv_scales, block_table,
+               seq_lens, out, given, workspace, dev_status)
     if out is None:
         out = _empty_on(stream, kv_cache, (S, Hq, d), out_dtype)
-    elif tuple(out.shape) != (S, Hq, d) or not out.is_contiguous():
+    elif out.shape != (S, Hq, d) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous tensor [{S}, {Hq}, {d}]")
     if given is None:
         lse = _empty_on(stream, kv_cache, (S, Hq), torch.float32) if lse else None
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (S, Hq) or not lse.is_contiguous():
+    elif lse.dtype != torch.float32 or lse.shape != (S, Hq) or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous float32 tensor [{S}, {Hq}]")
     if workspace is None:
-        ws_bytes = load_library().attn_fwd_paged_fp8_workspace_size(S, Hq, hkv, d, max_seq_len)
+        ws_bytes = (_lib or load_library()).attn_fwd_paged_fp8_workspace_size(S, Hq, hkv, d, max_seq_len)
         if ws_bytes:
             workspace = _empty_on(stream, kv_cache, (ws_bytes,), torch.uint8)
     elif workspace.is_contiguous():
