@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 // leaves at once where no sequence begins that goes on.
 //   Few sequences: a CTA a (sequence, query head, 32 columns), which finds the
 // sequence's chunk among the joins.  (Two sequences of 76 partials, D = 256, 8
-// heads: 4.6 us a (chunk, head) with 256 threads, -JOIN- us so.)
+// heads: the call took 35.1 us with a CTA a (chunk, head), 33.3 us so.)
 constexpr int kJoin = 256, kJoinSmall = 64, kLoad = 6;
 __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params p, int D, int width) {
     __shared__ float4 so[kJoin];
@@ -1144,10 +1144,17 @@ PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_le
     pl.n_hgroups = static_cast<long long>(Hkv) * pl.subs;
     // Few and short sequences: a cluster of up to 8 CTAs a (sequence, head), each
     // with at most four blocks, all of them running at once; the parts are
-    // joined on chip, in the same launch and without a workspace.
-    const long long slots = 152LL * paged_fp8_ctas(D, pl.head_cols), blocks = (static_cast<long long>(max_seq_len) + 127) / 128;
-    const long long parts = blocks < 1 ? 1 : (blocks < kMaxCluster ? blocks : kMaxCluster);
-    if (blocks <= 4 * parts && num_seqs * pl.n_hgroups * parts <= slots) {
+    // joined on chip, in the same launch and without a workspace.  (D = 128, 8 KV
+    // heads, clusters and chunks: one sequence of 512 tokens 6.0 and 7.7 us, of
+    // 4096 7.9 and 8.4, four of 4096 9.0 and 10.9.)  Clusters lie within a GPC and
+    // do not fill every SM: at one CTA an SM 128 of them in clusters of 8 take
+    // two turns (four sequences of 1024, D = 256, 4 KV heads: 12.8 and 8.4 us).
+    const int ctas = paged_fp8_ctas(D, pl.head_cols);
+    const long long slots = 152LL * ctas, blocks = (static_cast<long long>(max_seq_len) + 127) / 128;
+    const long long room = (ctas == 1 ? slots / 2 : slots * 27 / 32) / (num_seqs * pl.n_hgroups);
+    long long parts = blocks < kMaxCluster ? blocks : kMaxCluster;
+    parts = parts < room ? parts : room;
+    if (parts >= 1 && blocks <= 4 * parts) {
         pl.cluster = 1;
         pl.chunks = static_cast<int>(parts);
         return pl;
