@@ -18,13 +18,17 @@
 //     s_t + v_t of this block and head: the value's exponent goes into the
 //     weight's, and since every block has a reference of its own no weight is
 //     lost to a far larger one in another block.  256 w is split into NP e4m3
-//     pieces, each 16 times finer: NP = 3 holds 12 significant bits (bf16
-//     output, whose own rounding is 2^-9), NP = 4 holds 16 (fp32 output).
+//     pieces, each 16 times finer: NP = 3 holds an fp16 number's 11 significant
+//     bits (for bf16 output, which keeps 8), NP = 4 holds 16 (for fp32 output).
 // O^T of a block is read from TMEM and added, times 2^(M - R), to fp32
 // registers (thread = column d of the output), so nothing is rescaled in TMEM.
-// The softmax sum is kept apart from the weights, in fp32, each thread (token
-// lane) with its own reference, so a value row of zeros or of any scale does
-// not touch it.
+// The softmax sum is kept apart from the weights, in fp32, each warp with a
+// reference of its own, so a value row of zeros or of any scale does not touch it.
+// What bounds it now (one GB300, contexts of 16384, 64 sequences, bf16 output,
+// of 6787 GB/s copied): D = 128, 4 heads a KV head 7.03 TB/s, 8 heads 6.93,
+// D = 256 7.1, D = 192 6.6, D = 96 6.3 (a third of its shared memory is padding),
+// D = 64 6.5 with up to 4 heads, 5.5 with 8 (the softmax warps); above 8 heads a
+// KV head's rows go to several CTAs, 5.3 TB/s at 16 (the L2's reads).
 //
 // Work split: the context blocks of all sequences, in order, are cut into C
 // equal runs ("chunks"), and CTA (c, h) takes chunk c of KV head (or head
@@ -43,9 +47,9 @@ namespace gbattn {
 
 namespace {
 
-constexpr int kTok = 128;      // tokens of a cache block: the MMA's M
-constexpr int kWg = 128;       // threads of a softmax warpgroup, one a token lane
-constexpr int kMaxCluster = 8; // portable cluster size
+constexpr int kTok = 128;       // tokens of a cache block: the MMA's M
+constexpr int kWg = 128;        // threads of a softmax warpgroup, one a token lane
+constexpr int kMaxCluster = 8;  // portable cluster size
 constexpr int kNewSeg = 256, kLastBlock = 512;  // flags beside a slot's token count
 constexpr float kLow = -1e30f;  // a reference below every score, finite so that differences are defined
 constexpr float kLn2f = 0.6931471805599453f;
@@ -744,7 +748,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 const float2 sa = ssum[hl], sb2 = ssum[HT + hl], sc2 = ssum[2 * HT + hl], sd = ssum[3 * HT + hl];
                 const float mt = fmaxf(fmax3(sa.x, sb2.x, sc2.x), sd.x);
                 const float all = (sa.y * ex2(sa.x - mt) + sb2.y * ex2(sb2.x - mt)) + (sc2.y * ex2(sc2.x - mt) + sd.y * ex2(sd.x - mt));
-                const float inv_l = all == 0.f ? 0.f : __fdividef(ex2(Rh - mt), all);  // 2^-22 off at most
+                // 2^(Rh - mt) / all: the exponent of `all` goes into the power, so that
+                // neither of the two overflows alone; 2^-21 off at most
+                const int abits = __float_as_int(all), ae = ((abits >> 23) & 255) - 127;
+                const float am = __int_as_float((abits & 0x7FFFFF) | 0x3F800000);
+                float inv_l = __fdividef(ex2(Rh - mt - static_cast<float>(ae)), am);
+                if (all == 0.f) inv_l = 0.f;
+                if (!(all < INFINITY)) inv_l = NAN;
                 const float lse_l = all == 0.f ? -INFINITY : mt + __log2f(all);
                 float inv[HT];
 #pragma unroll
@@ -883,7 +893,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 const uint32_t k = sb + kslot * C::SLOT_BYTES + C::HALF_BYTES, q = sb + C::OFF_Q + (seg & 1) * C::Q_BYTES;
 #pragma unroll
                 for (int ks = 0; ks < D / 32; ++ks)
-                    mma_f8_ss(tm + C::TM_S + (i & 1) * NQ, sdesc_rows<C::PW>(k + ks * 32 / C::PW * C::PIECE_BYTES + ks * 32 % C::PW, 16),
+                    mma_f8_ss(tm + C::TM_S + (i & 1) * NQ,
+                              sdesc_rows<C::PW>(k + ks * 32 / C::PW * C::PIECE_BYTES + ks * 32 % C::PW, 16),
                               sdesc_sw128(q + (ks / 4) * (NQ * 128) + (ks % 4) * 32, 16, 1024), id_s, ks > 0);
                 mma_commit(b_sfull(i & 1));
             }
@@ -903,7 +914,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 for (int c = 0; c < NCH; ++c)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_f8_ss(tm + C::TM_O + c * NW, sdesc_rows<C::PW>(v + c * (kTok * 128) + ks * 32 * C::PW, D - c * 128 <= C::PW ? 0 : C::PIECE_BYTES),
+                        mma_f8_ss(tm + C::TM_O + c * NW,
+                                  sdesc_rows<C::PW>(v + c * (kTok * 128) + ks * 32 * C::PW,
+                                                    D - c * 128 <= C::PW ? 0 : C::PIECE_BYTES),
                                   sdesc_plain(pp + ks * 512, 128, kTok * 16), id_o, ks > 0);
                 mma_commit(b_ofull);
                 mma_commit(b_empty(vslot));

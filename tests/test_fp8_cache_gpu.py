@@ -365,6 +365,29 @@ def test_decode_sink_with_a_tiny_value_row():
     assert np.abs(to_np(out) - ref).max() <= 2.0 ** -14 * 4 * scale_of_sum  # 16-bit weights, values up to about 4
 
 
+@pytest.mark.parametrize("max_len", [900, 1 << 20])
+def test_decode_rising_scores_and_values_near_the_top_of_fp32(max_len):
+    """Scores that rise from block to block by less than a reference is moved
+    for, and value rows of up to 2^110: neither the sum, the references nor
+    their quotient leaves fp32's range."""
+    D, n = 64, 900
+    g = torch.Generator().manual_seed(2)
+    key = torch.randn(n, 1, D, generator=g)
+    key[:, 0, 0] = 8 * 27.0 * (torch.arange(n) // 128)  # by e^27 = 2^39 a block of 128
+    value = torch.randn(n, 1, D, generator=g) * 2.0 ** 108
+    cache, scales = torch.zeros(2, 8, 128, 1, D, device=dev()).to(torch.float8_e4m3fn), torch.ones(2, 8, 1, 128, dtype=torch.uint8, device=dev())
+    gb.attn_kv_cache_write_fp8(key.to(torch.bfloat16).to(dev()), value.to(torch.bfloat16).to(dev()), ints(range(n)), cache, scales)
+    c = Ctx([n], 1, D)
+    c.codes, c.scales, c.table = cache.view(torch.uint8).cpu(), scales.cpu(), torch.arange(8, dtype=torch.int32).view(1, 8)
+    q = torch.zeros(1, 3, D, dtype=torch.bfloat16)
+    q[:, :, 0] = torch.tensor([1.0, 0.5, 1.0])
+    q[0, 2, 1:] = 0.5
+    for out_dtype in (torch.float32, torch.bfloat16):
+        out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
+        assert torch.isfinite(out).all()
+        check_decode(c, q, out, lse)
+
+
 def test_decode_large_logits():
     c = Ctx([129, 1000], 1, 128, seed=4, exps=(122, 126))
     q = bf16(2, 4, 128, seed=5, spread=30.0)  # scores of some thousands: one key takes all the weight
@@ -480,10 +503,16 @@ def test_decode_on_two_streams_at_once_and_in_graphs(max_len):
     for o in outs[0] + outs[1]:
         assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
     graphs = []
-    for _ in range(2):
+    given = torch.empty(4, 8, 128, device=dev())
+    for i in range(2):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            graphs.append((g, gb.attn_fwd_paged_fp8(qd, cache, scales, table, sl, max_len, lse=True)))
+            lens = sl
+            if i == 1:  # behind a copy and a memset in the graph
+                lens = torch.empty_like(sl)
+                lens.copy_(sl)
+                given.zero_()
+            graphs.append((g, gb.attn_fwd_paged_fp8(qd, cache, scales, table, lens, max_len, lse=True, out=given if i else None)))
     c.lens = [2000, 1, 0, 128]
     sl.copy_(ints(c.lens))
     q = bf16(4, 8, 128, seed=16)
