@@ -688,8 +688,8 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
     char* ws = static_cast<char*>(workspace);
     if (plan.workspace_bytes) {
         p.part_o = reinterpret_cast<float*>(ws);
-        p.part_lse = reinterpret_cast<float*>(ws + plan.o_bytes);
-        p.joins = reinterpret_cast<int2*>(ws + plan.o_bytes + plan.lse_bytes);
+        p.part_sum = reinterpret_cast<float2*>(ws + plan.o_bytes);
+        p.joins = reinterpret_cast<int2*>(ws + plan.o_bytes + plan.sum_bytes);
     }
     p.num_seqs = num_seqs;
     p.num_blocks = num_blocks;

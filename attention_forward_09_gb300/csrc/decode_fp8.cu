@@ -23,18 +23,24 @@
 // O^T of a block is read from TMEM and added, times 2^(M - R), to fp32
 // registers (thread = column d of the output), so nothing is rescaled in TMEM.
 // The softmax sum is kept apart from the weights, in fp32, each warp with a
-// reference of its own, so a value row of zeros or of any scale does not touch it.
+// reference of its own (one of its scores, moved rarely), so a value row of zeros
+// or of any scale does not touch it.  What is added to a score is added to its
+// difference from that reference, and partials are kept as (reference, sum), so
+// that nothing is lost beside scores of up to 2^23; above, M's own step passes 1.
+// (Plain sums u + v_t and an lse a partial take 3% less time at D = 64 with eight
+// heads or short sequences, 1 to 3% elsewhere, and are 2^-11 off at scores of 2^13.)
 // What bounds it now (one GB300, contexts of 16384, 64 sequences, bf16 output,
 // of 6787 GB/s copied): D = 128, 4 heads a KV head 7.03 TB/s, 8 heads 6.93,
 // D = 256 7.1, D = 192 6.6, D = 96 6.3 (a third of its shared memory is padding),
-// D = 64 6.5 with up to 4 heads, 5.5 with 8 (the softmax warps); above 8 heads a
+// D = 64 6.5 with up to 4 heads, 5.1 with 8 (the softmax warps); above 8 heads a
 // KV head's rows go to several CTAs, 5.3 TB/s at 16 (the L2's reads).
 //
 // Work split: the context blocks of all sequences, in order, are cut into C
 // equal runs ("chunks"), and CTA (c, h) takes chunk c of KV head (or head
 // group) h, heads fastest, so that CTAs running side by side read neighbouring
 // rows.  A sequence inside one chunk is written out directly; one that crosses
-// chunks leaves fp32 partials (o, lse), which paged_fp8_combine joins.  Few
+// chunks leaves fp32 partials (o, the scores' reference, the sum less it: an lse
+// would lose the sum's bits beside a large score), which paged_fp8_combine joins.  Few
 // short sequences take a cluster of CTAs each instead, which join on chip.
 #include <math.h>
 
@@ -95,7 +101,7 @@ struct Fp8Cfg {
     static_assert((SMEM_BYTES + 1024 + 256) * CTAS <= 233472, "shared memory budget");
     static_assert(TM_COLS * CTAS <= 512, "tensor memory budget");
     static_assert(NP * HT <= 16, "a warpgroup's pieces of weights are one 16-byte row a token");
-    static_assert(HG * (D + 1) * 4 <= SLOT_BYTES, "a cluster's partials lie in the first slot");
+    static_assert(HG * (D + 2) * 4 <= SLOT_BYTES, "a cluster's partials lie in the first slot");
 };
 
 // Instruction descriptor of kind::f8f6f4, fp32 accumulation: A format in bits
@@ -187,6 +193,11 @@ __device__ __forceinline__ float warp_max(float x) {  // NaN ignored unless ever
 __device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
     return v;
 }
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
@@ -617,34 +628,39 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     tmem_ld<HT>(tm + tlane + C::TM_S + (g & 1) * NQ + hw, r0);
                     tmem_ld<HT>(tm + tlane + C::TM_S + (g & 1) * NQ + HG + hw, r1);
                     tmem_wait_ld();
-                    float2 u[HT / 2], d[HT / 2];
+                    float2 dot[HT / 2], kq[HT / 2], d[HT / 2];  // a score is dot * kq; d: less the warp's reference
                     float dmax = kLow;
 #pragma unroll
                     for (int h = 0; h < HT / 2; ++h) {
-                        const float2 dot =
+                        dot[h] =
                             __ffma2_rn(make_float2(__uint_as_float(r1[2 * h]), __uint_as_float(r1[2 * h + 1])), splat(0.0625f),
                                        make_float2(__uint_as_float(r0[2 * h]), __uint_as_float(r0[2 * h + 1])));
-                        u[h] = __fmul2_rn(__fmul2_rn(dot, splat(kf)), qf[h]);
-                        if (nvalid < kTok) u[h] = valid ? u[h] : splat(-INFINITY);
-                        d[h] = __fadd2_rn(u[h], make_float2(-mref[h].x, -mref[h].y));
+                        kq[h] = __fmul2_rn(qf[h], splat(kf));  // (first: dot * kf may overflow)
+                        d[h] = __ffma2_rn(dot[h], kq[h], make_float2(-mref[h].x, -mref[h].y));
+                        if (nvalid < kTok) d[h] = valid ? d[h] : splat(-INFINITY);
                         dmax = fmax3(dmax, d[h].x, d[h].y);
                     }
                     if (__any_sync(0xffffffffu, dmax > 60.f)) {  // rarely: fp32 has room for sums of 2^60 and more
 #pragma unroll
                         for (int h = 0; h < HT / 2; ++h) {
-                            const float2 m = make_float2(fmaxf(mref[h].x, warp_max(u[h].x)), fmaxf(mref[h].y, warp_max(u[h].y)));
+                            float2 u = __fmul2_rn(dot[h], kq[h]);
+                            if (!valid) u = splat(-INFINITY);
+                            const float2 m = make_float2(fmaxf(mref[h].x, warp_max(u.x)), fmaxf(mref[h].y, warp_max(u.y)));
                             l[h] = make_float2(l[h].x * ex2(mref[h].x - m.x), l[h].y * ex2(mref[h].y - m.y));
                             mref[h] = m;
-                            d[h] = make_float2(u[h].x - m.x, u[h].y - m.y);
+                            d[h] = __ffma2_rn(dot[h], kq[h], make_float2(-m.x, -m.y));
+                            if (!valid) d[h] = splat(-INFINITY);
                         }
                     }
                     float m[HT];
 #pragma unroll
                     for (int h = 0; h < HT / 2; ++h) {
                         l[h] = __fadd2_rn(l[h], make_float2(ex2(d[h].x), ex2(d[h].y)));
-                        u[h] = __fadd2_rn(u[h], splat(ev));
-                        m[2 * h] = warp_max(u[h].x);
-                        m[2 * h + 1] = warp_max(u[h].y);
+                        // the value's exponent counts in full beside a large score: added to the difference
+                        d[h] = __fadd2_rn(d[h], splat(ev));
+                        const float2 top = __fadd2_rn(make_float2(warp_max(d[h].x), warp_max(d[h].y)), mref[h]);
+                        m[2 * h] = top.x;
+                        m[2 * h + 1] = top.y;
                     }
                     float* red = sred + (g & 1) * 4 * HT;
                     if (lane == 0) {
@@ -668,7 +684,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                         }
                     }
                     if (b > w.b0) add_o();  // the weights' buffer and O^T are free again
-                    // weights 256 w = 2^(u - M + 8) and their pieces, byte piece * HT + head
+                    // weights 256 w = 2^(s + v - M + 8) and their pieces, byte piece * HT + head
                     float wm[4][HT];  // the four warps' maxima
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -688,7 +704,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                         for (int k = 0; k < 2; ++k)
                             mm[k] = fmaxf(fmax3(wm[0][2 * h + k], wm[1][2 * h + k], wm[2][2 * h + k]), fmaxf(wm[3][2 * h + k], kLow));
                         M8[h] = make_float2(mm[0] - 8.f, mm[1] - 8.f);
-                        const float2 e = __fadd2_rn(u[h], make_float2(-M8[h].x, -M8[h].y));
+                        const float2 e = __fadd2_rn(d[h], __fadd2_rn(mref[h], make_float2(-M8[h].x, -M8[h].y)));
                         uint32_t c[NP];
                         split_pair<NP>(make_float2(ex2(e.x), ex2(e.y)), c);
 #pragma unroll
@@ -755,7 +771,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 float inv_l = __fdividef(ex2(Rh - mt - static_cast<float>(ae)), am);
                 if (all == 0.f) inv_l = 0.f;
                 if (!(all < INFINITY)) inv_l = NAN;
-                const float lse_l = all == 0.f ? -INFINITY : mt + __log2f(all);
                 float inv[HT];
 #pragma unroll
                 for (int h = 0; h < HT; ++h) inv[h] = __shfl_sync(0xffffffffu, inv_l, h * (32 / HT));
@@ -769,7 +784,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 // nothing reads or fills any more (a cluster's CTA has one segment).
                 const long long part = (static_cast<long long>(chunk) * 2 + (w.b0 == 0 ? 1 : 0)) * p.Hq + h0;
                 float* po = CLUSTER ? reinterpret_cast<float*>(smem) : p.part_o + part * D;
-                float* pl = CLUSTER ? reinterpret_cast<float*>(smem) + HG * D : p.part_lse + part;
+                float2* pl = CLUSTER ? reinterpret_cast<float2*>(smem + HG * D * 4) : p.part_sum + part;
                 const long long row = static_cast<long long>(w.s) * p.Hq + h0;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
@@ -793,9 +808,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 }
                 if ((warp & 3) == 0 && (lane & (32 / HT - 1)) == 0 && hw + hl < nh) {
                     if (!whole)
-                        pl[hw + hl] = lse_l;
+                        pl[hw + hl] = make_float2(all == 0.f ? -INFINITY : mt, all);
                     else if (p.lse)
-                        p.lse[row + hw + hl] = lse_l * kLn2f;
+                        p.lse[row + hw + hl] = (all == 0.f ? -INFINITY : mt + __log2f(all)) * kLn2f;
                 }
                 ++seg;
                 more = w.next(p);
@@ -959,15 +974,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const int parts = s_parts;
         if (chunk < parts) {
             for (int h = chunk; h < nh; h += parts) {
-                float w[kMaxCluster], m = kLow, all = 0.f;
+                float r[kMaxCluster], w[kMaxCluster], m = kLow, all = 0.f;
 #pragma unroll
                 for (int i = 0; i < kMaxCluster; ++i) {
-                    w[i] = i < parts ? ld_cluster_f1(mapa_shared(sb + (HG * D + h) * 4, i)) : -INFINITY;
-                    m = fmaxf(m, w[i]);
+                    const float2 x = i < parts ? ld_cluster_f2(mapa_shared(sb + HG * D * 4 + h * 8, i)) : make_float2(-INFINITY, 0.f);
+                    r[i] = x.x, w[i] = x.y;
+                    m = fmaxf(m, r[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < kMaxCluster; ++i) {
-                    w[i] = ex2(w[i] - m);
+                    w[i] *= ex2(r[i] - m);
                     all += w[i];
                 }
                 const float inv = all == 0.f ? 0.f : 1.f / all;
@@ -996,7 +1012,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 // (the sequence begins there), the first slots of the chunks up to its last.
 // Groups of `width` / 4 threads take the partials in turn, kLoad loads in
 // flight each, the first of them asked for before every warp finds the largest
-// lse for itself; then one group adds the groups' sums.
+// reference for itself; then one group adds the groups' sums.
 //   Many sequences (few partials each): a small CTA a (chunk, query head), which
 // leaves at once where no sequence begins that goes on.
 //   Few sequences: a CTA a (sequence, query head, 32 columns), which finds the
@@ -1028,22 +1044,22 @@ __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params 
     if (j.x < 0 || j.x >= p.num_seqs || j.y <= c || j.y >= p.chunks) return;
     const int n = grp < groups ? j.y - c + 1 : 0;
     auto slot = [&](int i) { return (static_cast<long long>(c + i) * 2 + (i == 0 ? 1 : 0)) * p.Hq + h; };
-    float w[kLoad];
+    float2 w[kLoad];
     float4 v[kLoad];
     auto ask = [&](int i0) {
 #pragma unroll
         for (int k = 0; k < kLoad; ++k) {
             const int i = i0 + k * groups;
-            w[k] = -INFINITY;
+            w[k] = make_float2(-INFINITY, 0.f);
             if (i < n) {
-                w[k] = p.part_lse[slot(i)];
+                w[k] = p.part_sum[slot(i)];
                 v[k] = reinterpret_cast<const float4*>(p.part_o + slot(i) * D)[t];
             }
         }
     };
     ask(grp);
     float m = kLow;
-    for (int i = lane; i <= j.y - c; i += 32) m = fmaxf(m, p.part_lse[slot(i)]);
+    for (int i = lane; i <= j.y - c; i += 32) m = fmaxf(m, p.part_sum[slot(i)].x);
     m = warp_max(m);
     float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1051,7 +1067,7 @@ __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params 
 #pragma unroll
         for (int k = 0; k < kLoad; ++k) {
             if (i0 + k * groups >= n) break;
-            const float x = ex2(w[k] - m);
+            const float x = w[k].y * ex2(w[k].x - m);
             sum += x;
             acc.x = fmaf(x, v[k].x, acc.x);
             acc.y = fmaf(x, v[k].y, acc.y);
@@ -1197,8 +1213,8 @@ PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_le
     if (pl.chunks > 1) {
         const size_t rows = static_cast<size_t>(pl.chunks) * 2 * Hq;
         pl.o_bytes = (rows * D * 4 + 255) & ~size_t(255);
-        pl.lse_bytes = (rows * 4 + 255) & ~size_t(255);
-        pl.workspace_bytes = pl.o_bytes + pl.lse_bytes + ((static_cast<size_t>(pl.chunks) * 8 + 255) & ~size_t(255));
+        pl.sum_bytes = (rows * 8 + 255) & ~size_t(255);
+        pl.workspace_bytes = pl.o_bytes + pl.sum_bytes + ((static_cast<size_t>(pl.chunks) * 8 + 255) & ~size_t(255));
     }
     return pl;
 }

@@ -197,7 +197,7 @@ struct PagedFp8Params {
     float* lse;
     uint32_t* status;
     float* part_o;    // [chunks, 2, Hq, D]
-    float* part_lse;  // [chunks, 2, Hq], base 2
+    float2* part_sum; // [chunks, 2, Hq]: the scores' reference (base 2; -inf: no score), the softmax sum less it
     int2* joins;      // [chunks]: the sequence that begins in the chunk and goes on, and its last chunk; or -1
     int num_seqs, num_blocks, max_blocks;
     int cap;          // largest context: min(max_seq_len, 128 * max_blocks)
@@ -212,7 +212,7 @@ struct PagedFp8Params {
 struct PagedFp8Plan {
     int subs, heads_per_sub, head_cols, chunks, cluster;
     long long n_hgroups;
-    size_t o_bytes, lse_bytes;  // workspace sections, each 256-byte aligned; then the joins
+    size_t o_bytes, sum_bytes;  // workspace sections, each 256-byte aligned; then the joins
     size_t workspace_bytes;
 };
 // num_seqs, Hq, Hkv, D > 0, Hq % Hkv == 0.

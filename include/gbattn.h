@@ -416,7 +416,7 @@ gbattn_status attn_fwd_paged_noalloc(const void* q, const void* kv_cache, int nu
  * attn_fwd_paged_fp8 -- attn_fwd_paged over the 8-bit cache: the same results
  * as over a bf16 cache that holds the values the codes stand for, the softmax
  * weights of a block of 128 tokens held to 11 significant bits for bf16 output
- * and to 16 for fp32.
+ * and to 16 for fp32.  Scores are fp32 and may be of any size up to 2^23.
  *   q         device bf16, sequence s's [Hq, D] at s * q_stride elements
  *             (at least Hq * D, a multiple of 8)
  *   workspace at least attn_fwd_paged_fp8_workspace_size bytes (may be 0:

@@ -388,6 +388,62 @@ def test_decode_rising_scores_and_values_near_the_top_of_fp32(max_len):
         check_decode(c, q, out, lse)
 
 
+@pytest.mark.parametrize("max_len", [300, 1 << 20])
+def test_decode_scores_and_scales_near_the_ends_of_fp32(max_len):
+    """Equal keys, so that the result is the values' mean: scores of about
+    -2^23, and keys of 2^120 under queries of 2^-110."""
+    D, n = 128, 300
+    value = torch.randn(n, 1, D, generator=torch.Generator().manual_seed(3))
+    for qv, kv in ((2.0 ** 60, -(2.0 ** -41)), (2.0 ** -110, 2.0 ** 120)):
+        cache, scales = torch.zeros(2, 3, 128, 1, D, device=dev()).to(torch.float8_e4m3fn), torch.ones(2, 3, 1, 128, dtype=torch.uint8, device=dev())
+        gb.attn_kv_cache_write_fp8(torch.full((n, 1, D), kv, dtype=torch.bfloat16, device=dev()), value.to(torch.bfloat16).to(dev()),
+                                   ints(range(n)), cache, scales)
+        q = torch.full((1, 2, D), qv, dtype=torch.bfloat16)
+        out, lse = gb.attn_fwd_paged_fp8(q.to(dev()), cache, scales, ints(range(3)).view(1, 3), ints([n]), max_len, lse=True)
+        v = oracle.stands_for(cache.view(torch.uint8).cpu().numpy(), scales.cpu().numpy(), "e4m3")[1].reshape(-1, D)[:n]
+        # every weight is the same number, so only the fp32 sums and the quotient round
+        assert np.abs(to_np(out)[0] - v.mean(0)).max() <= 2.0 ** -16 * np.abs(v).max()
+        want = qv * kv * math.sqrt(D) + math.log(n)
+        assert np.abs(to_np(lse) - want).max() <= 2.0 ** -20 * (1 + abs(want))
+
+
+@pytest.mark.parametrize("max_len", [700, 1 << 20])
+def test_decode_references_that_move(max_len):
+    """Scores that jump up and down by thousands from block to block, a first
+    block that is not there, far negative scores behind it, and values whose
+    exponents differ: the last bits of the exponents still count."""
+    D, n = 64, 700
+    base = torch.tensor([0.0, -3e6, 2e3, -5e3, 1e7, 1e7])  # by block; the two last share the weight
+    key = torch.zeros(n, 1, D)
+    key[:, 0, 0] = base[torch.arange(n) // 128]
+    key[:, 0, 1] = torch.randn(n, generator=torch.Generator().manual_seed(4))
+    value = torch.randn(n, 1, D, generator=torch.Generator().manual_seed(5)) * torch.exp2(torch.arange(n) % 7 * 1.0).view(n, 1, 1)
+    cache, scales = torch.zeros(2, 6, 128, 1, D, device=dev()).to(torch.float8_e4m3fn), torch.ones(2, 6, 1, 128, dtype=torch.uint8, device=dev())
+    gb.attn_kv_cache_write_fp8(key.to(torch.bfloat16).to(dev()), value.to(torch.bfloat16).to(dev()), ints(range(n)), cache, scales)
+    vals = oracle.stands_for(cache.view(torch.uint8).cpu().numpy(), scales.cpu().numpy(), "e4m3")
+    k, v = vals[0].reshape(-1, D)[:n], vals[1].reshape(-1, D)[:n]
+    q = torch.zeros(1, 2, D, dtype=torch.bfloat16)
+    q[0, 0, 0], q[0, 1, 0], q[0, 1, 1] = 8.0, 0.125, 1.0  # head 0: scores of up to 1e7; head 1: to 2e5
+    for lens, first in (([n], 0), ([n], 1), ([256], 1), ([400], 1)):
+        table = ints(range(6)).view(1, 6)
+        if first:
+            table[0, 0] = -1
+        status = status_word()
+        out, lse = gb.attn_fwd_paged_fp8(q.to(dev()), cache, scales, table, ints(lens), max_len, lse=True, dev_status=status)
+        assert int(status) == (gb.DEV_BAD_INDEX if first else 0)
+        rows = slice(128 * first, lens[0])
+        for h in range(2):
+            x = k[rows] @ q[0, h].double().numpy() / 8
+            w = np.exp(x - x.max())
+            want, want_lse = (w / w.sum()) @ v[rows], x.max() + np.log(w.sum())
+            # products with one or two columns of q: a score is off by four roundings of fp32
+            ds = 2.0 ** -22 * np.abs(x[x > x.max() - 40]).max()
+            same = np.ptp(x[x > x.max() - 40]) == 0  # one number in all scores that count: off by the same
+            V = np.abs(v[rows]).max()
+            assert np.abs(to_np(out)[0, h] - want).max() <= V * ((0 if same else 4 * ds) + 2.0 ** -15)
+            assert abs(to_np(lse)[0, h] - want_lse) <= 2 * ds + 2.0 ** -20 * (1 + abs(want_lse))
+
+
 def test_decode_large_logits():
     c = Ctx([129, 1000], 1, 128, seed=4, exps=(122, 126))
     q = bf16(2, 4, 128, seed=5, spread=30.0)  # scores of some thousands: one key takes all the weight
