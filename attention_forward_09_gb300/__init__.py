@@ -551,14 +551,28 @@ def attn_fwd_paged_prefill_fp8(q, kv_cache, kv_scales, block_table, cu_seqlens_q
     (attn_fwd_varlen).  cu_seqlens_k [S + 1] (int32) holds the contexts' running
     sum, total_tokens >= cu_seqlens_k[S], max_seqlen_q and max_seq_len are
     host ints.  Returns (out [Tq, Hq, D], lse [Hq, Tq] or None)."""
-    T = int(total_tokens)
+    _, _, _, hkv, d = _fp8_cache(kv_cache, kv_scales)
+    T, max_seqlen_q, max_seq_len = int(total_tokens), _host_int("max_seqlen_q", max_seqlen_q), _host_int("max_seq_len", max_seq_len)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != d or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous bfloat16 tensor [tokens, Hq, {d}]")
+    Tq, Hq, _ = q.shape
+    _index_table("cu_seqlens_q", cu_seqlens_q, 1)
+    if cu_seqlens_q.shape != cu_seqlens_k.shape:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must have as many boundaries")
+    if out is not None and (out.shape != q.shape or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous tensor [{Tq}, {Hq}, {d}]")
+    given = lse if torch.is_tensor(lse) else None
+    if given is not None and (lse.dtype != torch.float32 or lse.shape != (Hq, Tq) or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor [{Hq}, {Tq}]")
+    _on_device(kv_cache.get_device(), "q cu_seqlens_q out lse", q, cu_seqlens_q, out, given)
     k, v = attn_kv_cache_read_fp8(kv_cache, kv_scales, block_table, cu_seqlens_k, T, dev_status=dev_status,
                                   stream=stream)
     with torch.cuda.device(kv_cache.device):
         s = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(s):
             return attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seq_len, softmax_scale, causal,
-                                   out, lse, out_dtype, dev_status, stream)
+                                   out, given if given is not None else True if lse else None, out_dtype,
+                                   dev_status, stream)
 
 
 def attn_mask_to_varlen(mask, stream=None):

@@ -198,3 +198,23 @@ def test_paged_binding_refuses(lib, change, message):
          "sl": torch.zeros(1, dtype=torch.int32), "status": None, **change}
     with pytest.raises(ValueError, match=message):
         gb.attn_fwd_paged_fp8(a["q"], a["cache"], a["scales"], a["bt"], a["sl"], 256, dev_status=a["status"])
+
+
+@pytest.mark.parametrize("change, message", [
+    (dict(q=torch.zeros(3, 4, 64)), "q must be"),
+    (dict(q=torch.zeros(3, 4, 96, dtype=torch.bfloat16)), "q must be"),
+    (dict(q=torch.zeros(3, 64, 4, dtype=torch.bfloat16).transpose(1, 2)), "q must be"),
+    (dict(cu_q=torch.zeros(2, dtype=torch.int64)), "cu_seqlens_q"),
+    (dict(cu_q=torch.zeros(3, dtype=torch.int32)), "boundaries"),
+    (dict(out=torch.zeros(2, 4, 64)), "out must be"),
+    (dict(lse=torch.zeros(3, 4)), "lse must be"),
+    (dict(most=2 ** 31), "max_seqlen_q"),
+    (dict(), "CUDA"),
+])
+def test_paged_prefill_binding_refuses(lib, change, message):
+    a = {**_args(), "q": torch.zeros(3, 4, 64, dtype=torch.bfloat16), "bt": torch.zeros(1, 2, dtype=torch.int32),
+         "cu": torch.zeros(2, dtype=torch.int32), "cu_q": torch.zeros(2, dtype=torch.int32), "out": None, "lse": None,
+         "most": 3, **change}
+    with pytest.raises(ValueError, match=message):
+        gb.attn_fwd_paged_prefill_fp8(a["q"], a["cache"], a["scales"], a["bt"], a["cu_q"], a["cu"], 10, a["most"], 256,
+                                      out=a["out"], lse=a["lse"])

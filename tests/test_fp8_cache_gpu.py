@@ -697,6 +697,29 @@ def test_a_prefill_then_decode_steps():
     assert int(status) == 0
 
 
+def test_prefill_with_rows_behind_the_contexts():
+    """total_tokens above the contexts' sum: the rows behind them are whatever
+    the allocator's memory held, here NaN, and no result feels them."""
+    hq, hkv, D, lens = 4, 2, 64, [130, 77]
+    c = Ctx(lens, hkv, D, seed=21)
+    cache, scales, table = c.on_gpu()
+    q_lens, T = [130, 20], 1000
+    q = bf16(sum(q_lens), hq, D, seed=22)
+    cu_q, cu_k = ints(np.cumsum([0] + q_lens)), ints(np.cumsum([0] + lens))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    poison = [torch.full((T, hkv, D), float("nan"), dtype=torch.bfloat16, device=dev()) for _ in range(8)]
+    del poison
+    status = status_word()
+    out, lse = gb.attn_fwd_paged_prefill_fp8(q.to(dev()), cache, scales, table, cu_q, cu_k, T, max(q_lens), max(lens), lse=True,
+                                             dev_status=status)
+    ref, ref_lse = oracle.attention_paged_prefill(q, c.values(), c.table, lens, cu_q, 1 / math.sqrt(D), True)
+    assert int(status) == 0
+    assert np.abs(to_np(out) - ref).max() <= 1e-2 and np.abs(to_np(lse) - ref_lse).max() <= 1e-3  # the prefill kernels' bounds
+    with pytest.raises(ValueError, match="q must be on"):
+        gb.attn_fwd_paged_prefill_fp8(q, cache, scales, table, cu_q, cu_k, T, max(q_lens), max(lens))
+
+
 def test_decode_of_a_quantised_cache_is_near_the_bf16_decode():
     """Against attn_fwd_paged over the unquantised cache: the difference is that
     of the codes, at most half a step (2^-4) of each key and value."""
