@@ -466,7 +466,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             s_first[0] = own;
             s_first[1] = static_cast<int>(b0);
             s_first[2] = given_up ? 0 : static_cast<int>(cut.start(chunk + 1) - b0);
-            s_parts = blocks > 1 ? min(blocks, p.chunks) : 0;
+            const int parts = min(blocks, p.chunks);
+            s_parts = parts > 1 ? parts : 0;  // one part is the whole: written out, nothing to join
         }
     } else {
         uint32_t incl = sum;

@@ -328,6 +328,22 @@ def test_decode_splits(lens):
         check_decode(c, q, out, lse)
 
 
+@pytest.mark.parametrize("D,hq,hkv", [(64, 4, 2), (128, 4, 2), (128, 16, 2), (192, 2, 1), (256, 10, 2)])
+@pytest.mark.parametrize("S", [1, 9, 14, 20, 27, 36, 48, 60, 75, 76, 80, 100, 123, 160, 200])
+def test_decode_short_sequences_in_any_number(S, D, hq, hkv):
+    """From a cluster of eight CTAs a sequence down to one, each with one to
+    several blocks, and chunks where the sequences are too many for that."""
+    longest = {1: 4096}.get(S, 1000 if S < 40 else 511)
+    lens = [longest - 128 * (i % 4) - 3 * (i % 5) for i in range(S)]
+    c = Ctx(lens, hkv, D, seed=S)
+    q = bf16(S, hq, D, seed=S + 1)
+    out, lse = run_decode(c, q, max_len=longest)
+    keep = sorted({0, S // 3, S // 2, S - 2, S - 1} & set(range(S)))  # the oracle takes a few of them
+    c.table, c.lens = c.table[keep], [lens[i] for i in keep]
+    check_decode(c, q[keep], out[keep], lse[keep])
+    assert torch.isfinite(out).all() and float(out.abs().max()) <= 60.0 * 4 * 2.0 ** -4  # an average of values
+
+
 def test_decode_scales_of_any_size():
     """Keys and values whose rows differ by many binades within a block, value
     rows of zeros, and queries of any size (scores kept moderate)."""
