@@ -1184,11 +1184,11 @@ PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_le
     const long long room = (ctas == 1 ? slots / 2 : slots * 27 / 32) / (num_seqs * pl.n_hgroups);
     long long parts = blocks < kMaxCluster ? blocks : kMaxCluster;
     parts = parts < room ? parts : room;
-    // Single CTAs (sequences of at most four blocks) need no GPC and may fill the
-    // SMs, and a little more: three sequences of 194 tokens, 192 heads, D = 256
-    // (96 CTAs) 8.9 us and 13.5 in chunks; 184 CTAs 11.9 and 12.4; 512 of them on
-    // 304 places 14.2 and 11.7.
-    if (parts < 1 && num_seqs * pl.n_hgroups <= slots * 5 / 4) parts = 1;
+    // Single CTAs (sequences of at most four blocks) need no GPC and may come in
+    // up to two waves: three sequences of 194 tokens, 192 heads, D = 256 (96 CTAs)
+    // 6.6 us and 13.5 in chunks; on 304 places 512 CTAs of two blocks 10.8 and 11.7,
+    // of 1 to 4 blocks 13.6 and 14.5, but 1024 of one block 17.3 and 13.6.
+    if (parts < 1 && num_seqs * pl.n_hgroups <= slots * 2) parts = 1;
     if (parts >= 1 && blocks <= 4 * parts) {
         pl.cluster = 1;
         pl.chunks = static_cast<int>(parts);
