@@ -344,6 +344,15 @@ def test_decode_short_sequences_in_any_number(S, D, hq, hkv):
     assert torch.isfinite(out).all() and float(out.abs().max()) <= 60.0 * 4 * 2.0 ** -4  # an average of values
 
 
+@pytest.mark.parametrize("hkv,lens", [(2000, [300, 0, 5]), (153, [200] * 6 + [1, 0, 129]), (1, [1 + i % 3 for i in range(2500)])])
+def test_decode_many_heads_or_sequences(hkv, lens):
+    """More heads than CTAs run at once, and more sequences than a CTA has threads."""
+    c = Ctx(lens, hkv, 64, seed=hkv)
+    q = bf16(len(lens), hkv, 64, seed=7)
+    out, lse = run_decode(c, q)
+    check_decode(c, q, out, lse)
+
+
 def test_decode_scales_of_any_size():
     """Keys and values whose rows differ by many binades within a block, value
     rows of zeros, and queries of any size (scores kept moderate)."""
