@@ -619,9 +619,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     const int nvalid = slen[slot] & (kNewSeg - 1);
                     const bool valid = tok < nvalid;
                     const uint8_t* sc = smem + C::OFF_SC + slot * 256;
-                    // 2^(b - 127) (for b = 0, 2^-127, zero is as good: no score feels it), and
-                    // b - 127 by way of 2^23 + b
-                    const float kf = __uint_as_float(static_cast<uint32_t>(sc[tok]) << 23);
+                    // 2^(b - 127) (2^-127 is a subnormal number), and b - 127 by way of 2^23 + b
+                    const float kf = __uint_as_float(max(static_cast<uint32_t>(sc[tok]) << 23, 0x400000u));
                     const float ev = __uint_as_float(0x4B000000u | sc[128 + tok]) - (8388608.f + 127.f);
                     if (!mbar_wait(b_sfull(g & 1), (g >> 1) & 1, abort_flag)) ok = false;
                     tc_fence_after();

@@ -432,6 +432,32 @@ def test_decode_scores_and_scales_near_the_ends_of_fp32(max_len):
         assert np.abs(to_np(lse) - want).max() <= 2.0 ** -20 * (1 + abs(want))
 
 
+def test_decode_exponent_byte_zero():
+    """Exponent byte 0 (2^-127) under queries of 2^126: scores of some hundreds
+    of either sign.  A scale that is not positive is refused."""
+    D, n, scale = 64, 200, 2.0 ** -7
+    codes, scales = torch.zeros(2, 2, 128, 1, D, dtype=torch.uint8), torch.zeros(2, 2, 1, 128, dtype=torch.uint8)
+    codes[0] = 0x7E  # 448
+    codes[0, :, ::3] |= 0x80
+    codes[1] = torch.randint(0, 0x7F, codes[1].shape, generator=torch.Generator().manual_seed(6), dtype=torch.uint8)
+    scales[1] = 120
+    q = torch.full((1, 2, D), 2.0 ** 126, dtype=torch.bfloat16)
+    vals = oracle.stands_for(codes.numpy(), scales.numpy(), "e4m3")
+    table = torch.arange(2, dtype=torch.int32).view(1, 2)
+    ref, ref_lse = oracle.attention_paged(q, vals, table, [n], scale)
+    for max_len in (n, 1 << 20):
+        out, lse = gb.attn_fwd_paged_fp8(q.to(dev()), codes.to(dev()).view(torch.float8_e4m3fn), scales.to(dev()), table.to(dev()),
+                                         ints([n]), max_len, scale, lse=True)
+        # scores of +-112: one number in all that count, so only the sums and the quotient round
+        assert np.abs(to_np(out) - ref).max() <= 2.0 ** -15 * np.abs(vals[1]).max()
+        assert np.abs(to_np(lse) - ref_lse).max() <= 2.0 ** -20 * (1 + np.abs(ref_lse).max())
+    for bad in (-scale, 0.0, float("nan")):
+        with pytest.raises(gb.GbattnError) as e:
+            gb.attn_fwd_paged_fp8(q.to(dev()), codes.to(dev()).view(torch.float8_e4m3fn), scales.to(dev()), table.to(dev()),
+                                  ints([n]), n, bad)
+        assert e.value.status == 1
+
+
 @pytest.mark.parametrize("max_len", [700, 1 << 20])
 def test_decode_references_that_move(max_len):
     """Scores that jump up and down by thousands from block to block, a first
