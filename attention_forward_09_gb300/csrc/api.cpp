@@ -609,10 +609,14 @@ gbattn_status attn_kv_cache_read_fp8(const void* kv_cache, const uint8_t* kv_sca
     if (s != GBATTN_OK) return s;
     if (num_seqs < 0 || Tk < 0 || max_blocks_per_seq < 0) return GBATTN_ERR_INVALID_ARG;
     if (Tk > 0x7fffffff - 64) return GBATTN_ERR_UNSUPPORTED;  // row counters are 32-bit on the device
-    if (num_seqs == 0 || Tk == 0) return GBATTN_OK;
-    if (max_blocks_per_seq == 0) return GBATTN_ERR_INVALID_ARG;
-    if (!kv_cache || !kv_scales || !block_table || !cu_seqlens_k || !k || !v) return GBATTN_ERR_INVALID_ARG;
-    if (!aligned16(kv_cache) || !aligned16(kv_scales) || !aligned16(k) || !aligned16(v)) return GBATTN_ERR_ALIGNMENT;
+    if (num_seqs == 0) return GBATTN_OK;
+    if (Tk == 0) {  // nothing to read; boundaries that say otherwise are reported
+        if (!dev_status || !cu_seqlens_k) return GBATTN_OK;
+    } else {
+        if (max_blocks_per_seq == 0) return GBATTN_ERR_INVALID_ARG;
+        if (!kv_cache || !kv_scales || !block_table || !cu_seqlens_k || !k || !v) return GBATTN_ERR_INVALID_ARG;
+        if (!aligned16(kv_cache) || !aligned16(kv_scales) || !aligned16(k) || !aligned16(v)) return GBATTN_ERR_ALIGNMENT;
+    }
     DeviceInfo di;
     s = device_info(&di);
     if (s != GBATTN_OK) return s;

@@ -168,10 +168,21 @@ __device__ __forceinline__ void st_32B(uint4* p, const uint32_t (&x)[8]) {
     }
 }
 
+// Whether sequence s, of boundaries c0 and c1, is one to be read: its rows lie
+// in [0, total) and its blocks in the table.
+__device__ __forceinline__ bool readable(const CacheReadFp8Params& p, int c0, int c1) {
+    return c0 >= 0 && c0 <= c1 && c1 <= p.total &&
+           (c0 == c1 || static_cast<int>(p.by_block.div(c1 - 1 - c0)) < p.max_blocks);
+}
+
 // A warp takes `group` consecutive packed rows (a power of two up to 32): lane u
 // finds where row u lies (a binary search for its sequence, the table), all of
 // them at once; then the lanes share the rows' 16-code vectors, [group][2][Hkv]
 // [D / 16] in a line whatever the number of heads, kAhead each in flight.
+//   Boundaries that decrease leave a binary search without meaning, so what it
+// finds is checked, and a row without a sequence makes the warp look, once,
+// whether any decrease (in order, such a row lies behind the last sequence);
+// only then are the sequences searched one by one.
 template <int D, bool E5M2>
 __global__ void __launch_bounds__(256, 5) kv_cache_read_fp8_sm103a(const CacheReadFp8Params p, int group) {
     constexpr int kAhead = 4;
@@ -179,29 +190,45 @@ __global__ void __launch_bounds__(256, 5) kv_cache_read_fp8_sm103a(const CacheRe
     const int nwarps = static_cast<int>((gridDim.x * blockDim.x) >> 5);
     const int groups = (p.total + group - 1) / group;
     const int vecs = p.Hkv * (D / 16), n = 2 * vecs;  // vectors of a token's keys; of its keys and values
+    int ordered = -1;                                 // whether no boundary decreases; -1: not looked at
     for (int g = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5); g < groups; g += nwarps) {
         const int t0 = g * group, t = t0 + lane;
         int slot = -1, at = 0;  // the row's cache slot (-1: not written, -2: zeros), its place in the block
-        if (lane < group && t < p.total && t < p.cu[p.num_seqs]) {
-            int s = 0, hi = p.num_seqs;  // cu[s] <= t < cu[hi], were cu in order
-            while (hi - s > 1) {
-                const int mid = (s + hi) >> 1;
-                if (p.cu[mid] <= t) s = mid; else hi = mid;
+        int s = -1, c0 = 0;     // its sequence (-1: none), and where that begins
+        const bool mine = lane < group && t < p.total;
+        if (mine) {
+            int lo = 0, hi = p.num_seqs;  // cu[lo] <= t < cu[hi], were cu in order
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.cu[mid] <= t) lo = mid; else hi = mid;
             }
-            const int c0 = p.cu[s], c1 = p.cu[s + 1], pos = t - c0;
-            if (c0 < 0 || pos < 0 || t >= c1 || c1 > p.total ||
-                static_cast<int>(p.by_block.div(c1 - 1 - c0)) >= p.max_blocks) {
-                if (p.status) atomicOr(p.status, kDevBadSeqlen);
-            } else {
-                const int bi = static_cast<int>(p.by_block.div(pos));
-                const int blk = p.block_table[static_cast<long long>(s) * p.max_blocks + bi];
-                at = pos - bi * p.block_size;
-                if (blk < 0 || blk >= p.num_blocks) {
-                    if (p.status) atomicOr(p.status, kDevBadIndex);
-                    slot = -2;
-                } else {
-                    slot = blk * p.block_size + at;
+            c0 = p.cu[lo];
+            const int c1 = p.cu[lo + 1];
+            if (c0 <= t && t < c1 && readable(p, c0, c1)) s = lo;
+        }
+        if (__any_sync(0xffffffffu, mine && s < 0)) {
+            if (ordered < 0) {
+                bool down = false;
+                for (int i = lane; i < p.num_seqs; i += 32) down |= p.cu[i + 1] < p.cu[i];
+                ordered = !__any_sync(0xffffffffu, down);
+            }
+            if (!ordered && mine && s < 0) {
+                for (int i = 0; i < p.num_seqs && s < 0; ++i) {
+                    c0 = p.cu[i];
+                    const int c1 = p.cu[i + 1];
+                    if (c0 <= t && t < c1 && readable(p, c0, c1)) s = i;
                 }
+            }
+        }
+        if (s >= 0) {
+            const int pos = t - c0, bi = static_cast<int>(p.by_block.div(pos));
+            const int blk = p.block_table[static_cast<long long>(s) * p.max_blocks + bi];
+            at = pos - bi * p.block_size;
+            if (blk < 0 || blk >= p.num_blocks) {
+                if (p.status) atomicOr(p.status, kDevBadIndex);
+                slot = -2;
+            } else {
+                slot = blk * p.block_size + at;
             }
         }
         int u = 0, i = lane;  // the lane's next vector: row u of the group, vector i of it
@@ -238,6 +265,12 @@ __global__ void __launch_bounds__(256, 5) kv_cache_read_fp8_sm103a(const CacheRe
                 st_32B((half ? p.v : p.k) + (static_cast<long long>(tu[k]) * vecs + j[k] - (half ? vecs : 0)) * 2, x);
             }
         }
+    }
+    // every boundary is looked at once, also of sequences that no row falls into
+    if (p.status && blockIdx.x == gridDim.x - 1) {
+        bool bad = threadIdx.x == 0 && p.cu[0] != 0;
+        for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x) bad |= !readable(p, p.cu[i], p.cu[i + 1]);
+        if (bad) atomicOr(p.status, kDevBadSeqlen);
     }
 }
 
@@ -290,7 +323,7 @@ cudaError_t launch_cache_write_fp8(const CacheWriteFp8Params& p, int D, int num_
 }
 
 cudaError_t launch_cache_read_fp8(const CacheReadFp8Params& p, int num_sms, cudaStream_t st) {
-    if (p.total <= 0 || p.num_seqs <= 0) return cudaSuccess;
+    if (p.num_seqs <= 0 || (p.total <= 0 && !p.status)) return cudaSuccess;  // (without rows: the boundaries are looked at)
     switch (p.D) {
         case 64: return read_d<64>(p, num_sms, st);
         case 96: return read_d<96>(p, num_sms, st);

@@ -409,9 +409,11 @@ gbattn_status attn_fwd_paged_noalloc(const void* q, const void* kv_cache, int nu
  *                 past c[num_seqs] are left as they were
  * Values are exact (a code has at most 4 significant bits) unless below bf16's
  * smallest normal number.  A block_table entry outside [0, num_blocks) sets
- * GBATTN_DEV_BAD_INDEX and its tokens' rows are zeros; a sequence whose
- * cu_seqlens_k decrease, run past Tk or past max_blocks_per_seq blocks sets
- * GBATTN_DEV_BAD_SEQLEN, and its rows are left as they were.
+ * GBATTN_DEV_BAD_INDEX and its tokens' rows are zeros.  A sequence whose
+ * cu_seqlens_k decrease, run past Tk or past max_blocks_per_seq blocks, or
+ * c[0] other than 0, sets GBATTN_DEV_BAD_SEQLEN; that sequence's rows are left
+ * as they were, and every other one's are read (a row in the range of two
+ * sequences, which takes boundaries that decrease, holds either's).
  *
  * attn_fwd_paged_fp8 -- attn_fwd_paged over the 8-bit cache: the same results
  * as over a bf16 cache that holds the values the codes stand for, the softmax
