@@ -550,9 +550,17 @@ def attn_fwd_paged_prefill_fp8(q, kv_cache, kv_scales, block_table, cu_seqlens_q
     (attn_kv_cache_read_fp8) and attended as packed documents
     (attn_fwd_varlen).  cu_seqlens_k [S + 1] (int32) holds the contexts' running
     sum, total_tokens >= cu_seqlens_k[S], max_seqlen_q and max_seq_len are
-    host ints.  Returns (out [Tq, Hq, D], lse [Hq, Tq] or None)."""
-    _, _, _, hkv, d = _fp8_cache(kv_cache, kv_scales)
+    host ints.  A sequence whose boundaries decrease or run past total_tokens,
+    its length bound or its row of the table sets DEV_BAD_SEQLEN and is
+    skipped: its rows of out and lse are left unwritten.  (Boundaries that
+    decrease can let two other sequences claim the same rows: the results of
+    those two are undefined.)  Returns (out [Tq, Hq, D], lse [Hq, Tq] or None)."""
+    _, _, bs, hkv, d = _fp8_cache(kv_cache, kv_scales)
+    _index_table("block_table", block_table, 2)
     T, max_seqlen_q, max_seq_len = int(total_tokens), _host_int("max_seqlen_q", max_seqlen_q), _host_int("max_seq_len", max_seq_len)
+    # the read-back refuses a context that its row of the table cannot hold and
+    # leaves its rows unwritten: attn_fwd_varlen has to skip that sequence too
+    max_seq_len = min(max_seq_len, bs * block_table.shape[1])
     if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != d or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous bfloat16 tensor [tokens, Hq, {d}]")
     Tq, Hq, _ = q.shape

@@ -76,3 +76,44 @@ def test_read_with_boundaries_in_order_reports_nothing():
     assert int(status) == 0
     gb.attn_kv_cache_read_fp8(cache, scales, c.table.to(dev()), ints([0, 0, 0, 0, 0, 3]), 0, dev_status=status)  # no rows for these
     assert int(status) == gb.DEV_BAD_SEQLEN
+
+
+# ---------------------------------------------------------------- several new tokens a sequence
+def poison_free_memory(rows, hkv, d):
+    """NaN into memory that the allocator will hand out for the contexts."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [torch.full((rows, hkv, d), float("nan"), dtype=torch.bfloat16, device=dev()) for _ in range(8)]
+    del held
+
+
+@pytest.mark.parametrize("cu_k,skipped", [
+    ([0, 300, 700, 850], [1]),      # 400 tokens, and a table of three blocks
+    ([0, 300, 250, 400], [1]),      # decreasing; the third is [250, 400), whose first rows the first claims too
+    ([0, 300, 300, 2000], [2]),     # past total_tokens
+    ([0, 300, 600, 750], []),
+])
+def test_prefill_skips_the_sequences_that_the_read_back_refuses(cu_k, skipped):
+    hq, hkv, D, T = 4, 2, 64, 1000
+    c = Ctx([512] * 3, hkv, D, seed=23)
+    cache, scales, table = c.on_gpu()
+    q_lens = [20, 0 if cu_k[2] == cu_k[1] else 30, 25]
+    cu_q = np.cumsum([0] + q_lens)
+    q = bf16(int(cu_q[-1]), hq, D, seed=24)
+    out = torch.full((int(cu_q[-1]), hq, D), 77.0, device=dev())
+    lse = torch.full((hq, int(cu_q[-1])), 77.0, device=dev())
+    status = status_word()
+    poison_free_memory(T, hkv, D)
+    gb.attn_fwd_paged_prefill_fp8(q.to(dev()), cache, scales, table[:, :3].contiguous(), ints(cu_q), ints(cu_k), T, 30, 900,
+                                  out=out, lse=lse, dev_status=status)
+    assert int(status) == (gb.DEV_BAD_SEQLEN if skipped else 0)
+    for s in range(3):
+        rows = slice(int(cu_q[s]), int(cu_q[s + 1]))
+        if s in skipped:
+            assert (out[rows] == 77).all() and (lse[:, rows] == 77).all()
+        elif cu_k[1:3] != [300, 250]:  # (there the rows that two sequences claim hold either's)
+            n = cu_k[s + 1] - cu_k[s]
+            ref, ref_lse = oracle.attention_paged_prefill(q[rows], c.values(), c.table[s:s + 1], [n], [0, q_lens[s]], 1 / math.sqrt(D), True)
+            assert np.abs(to_np(out[rows]) - ref).max(initial=0) <= 1e-2  # the prefill kernels' bounds
+            assert np.abs(to_np(lse[:, rows]) - ref_lse).max(initial=0) <= 1e-3
+        assert torch.isfinite(out[rows]).all()
