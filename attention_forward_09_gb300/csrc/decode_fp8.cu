@@ -765,15 +765,22 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 const float mt = fmaxf(fmax3(sa.x, sb2.x, sc2.x), sd.x);
                 const float all = (sa.y * ex2(sa.x - mt) + sb2.y * ex2(sb2.x - mt)) + (sc2.y * ex2(sc2.x - mt) + sd.y * ex2(sd.x - mt));
                 // 2^(Rh - mt) / all: the exponent of `all` goes into the power, so that
-                // neither of the two overflows alone; 2^-21 off at most
+                // neither of the two overflows alone; 2^-21 off at most.  What the power
+                // has below 2^-100 is a factor of its own: ex2 flushes below 2^-126, and
+                // the sums it meets are 2^8 times the values and more.
                 const int abits = __float_as_int(all), ae = ((abits >> 23) & 255) - 127;
                 const float am = __int_as_float((abits & 0x7FFFFF) | 0x3F800000);
-                float inv_l = __fdividef(ex2(Rh - mt - static_cast<float>(ae)), am);
+                const float power = Rh - mt - static_cast<float>(ae), above = fmaxf(power, -100.f);
+                float inv_l = __fdividef(ex2(above), am);
+                const float low_l = ex2(power - above);  // 1 as a rule
                 if (all == 0.f) inv_l = 0.f;
                 if (!(all < INFINITY)) inv_l = NAN;
-                float inv[HT];
+                float inv[HT], low[HT];
 #pragma unroll
-                for (int h = 0; h < HT; ++h) inv[h] = __shfl_sync(0xffffffffu, inv_l, h * (32 / HT));
+                for (int h = 0; h < HT; ++h) {
+                    inv[h] = __shfl_sync(0xffffffffu, inv_l, h * (32 / HT));
+                    low[h] = __shfl_sync(0xffffffffu, low_l, h * (32 / HT));
+                }
                 const bool whole = w.b0 == 0 && w.b1 == w.nblk;
                 if (!CLUSTER && threadIdx.x == 0 && w.b0 == 0 && w.b1 < w.nblk) {
                     // this segment's sequence begins here and goes on: up to the chunk of its last unit
@@ -794,7 +801,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                         for (int k = 0; k < HT; ++k) {
                             const int h = hw + k;
                             if (h < nh) {
-                                const float x = (k & 1 ? o[c][k / 2].y : o[c][k / 2].x) * inv[k];
+                                const float x = (k & 1 ? o[c][k / 2].y : o[c][k / 2].x) * inv[k] * low[k];
                                 if (!whole)
                                     po[h * D + d] = x;
                                 else if (p.out_f32)

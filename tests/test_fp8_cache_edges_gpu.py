@@ -117,3 +117,48 @@ def test_prefill_skips_the_sequences_that_the_read_back_refuses(cu_k, skipped):
             assert np.abs(to_np(out[rows]) - ref).max(initial=0) <= 1e-2  # the prefill kernels' bounds
             assert np.abs(to_np(lse[:, rows]) - ref_lse).max(initial=0) <= 1e-3
         assert torch.isfinite(out[rows]).all()
+
+
+# ---------------------------------------------------------------- decode: values near the ends of fp32
+def written(key, value, d, kind="e4m3"):
+    """One sequence's keys and values [n, 1, d], written into a cache of its own blocks in order."""
+    n = key.shape[0]
+    nb = -(-n // 128)
+    cache = torch.zeros(2, nb, 128, 1, d, device=dev()).to(DTYPES[kind])
+    scales = torch.ones(2, nb, 1, 128, dtype=torch.uint8, device=dev())
+    gb.attn_kv_cache_write_fp8(key.to(torch.bfloat16).to(dev()), value.to(torch.bfloat16).to(dev()), ints(range(n)), cache, scales)
+    c = Ctx([1], 1, d, kind)
+    c.lens, c.codes, c.scales = [n], cache.view(torch.uint8).cpu(), scales.cpu()
+    c.table = torch.arange(nb, dtype=torch.int32).view(1, nb)
+    return c
+
+
+@pytest.mark.parametrize("byte", [1, 9, 20, 27, 40])
+@pytest.mark.parametrize("n,max_len", [(517, 517), (4096, 1 << 20), (131072, 1 << 20)])
+def test_decode_of_values_near_the_bottom_of_fp32(n, max_len, byte):
+    """Value rows whose exponent bytes are the least: fp32 and bf16 hold the
+    results (of 2^-126 and a little below), and so do the outputs."""
+    c = Ctx([n], 1, 64, seed=byte, exps=(119, 123), vexps=(byte, byte + 2), extra=0)
+    q = bf16(1, 2, 64, seed=n)
+    for out_dtype in (torch.float32, torch.bfloat16):
+        out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
+        check_decode(c, q, out, lse)
+        # relative to what an average of n values of one sign or the other comes to
+        assert float(out.double().norm()) > 0.1 / math.sqrt(n) * 8 * float(np.nanstd(c.values()[1, c.table[0, 0], :, 0]))
+
+
+@pytest.mark.parametrize("n,max_len", [(900, 900), (4096, 4096), (900, 1 << 20), (100000, 1 << 20)])
+def test_decode_of_small_values_under_rising_scores(n, max_len):
+    """As above, with scores that rise from block to block by e^27, less than a
+    reference is moved for."""
+    g = torch.Generator().manual_seed(n)
+    key = torch.randn(n, 1, 64, generator=g)
+    key[:, 0, 0] = 8 * 27.0 * (torch.arange(n) // 128 % 7)
+    value = torch.randn(n, 1, 64, generator=g) * 2.0 ** -112
+    c = written(key, value, 64)
+    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    q[:, :, 0] = torch.tensor([1.0, 0.5])
+    q[0, 1, 1:] = 0.5
+    for out_dtype in (torch.float32, torch.bfloat16):
+        out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
+        check_decode(c, q, out, lse)
