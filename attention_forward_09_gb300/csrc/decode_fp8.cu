@@ -994,13 +994,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     all += w[i];
                 }
                 const float inv = all == 0.f ? 0.f : 1.f / all;
+#pragma unroll
+                for (int i = 0; i < kMaxCluster; ++i) w[i] *= inv;  // (before they meet values: a sum may be 2^60 and more)
                 const long long row = static_cast<long long>(own) * p.Hq + h0 + h;
                 for (int d = threadIdx.x; d < D; d += C::THREADS) {
                     float x = 0.f;
 #pragma unroll
                     for (int i = 0; i < kMaxCluster; ++i)
                         if (i < parts) x = fmaf(w[i], ld_cluster_f1(mapa_shared(sb + (h * D + d) * 4, i)), x);
-                    x *= inv;
                     if (p.out_f32)
                         static_cast<float*>(p.out)[row * D + d] = x;
                     else
@@ -1019,7 +1020,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 // (the sequence begins there), the first slots of the chunks up to its last.
 // Groups of `width` / 4 threads take the partials in turn, kLoad loads in
 // flight each, the first of them asked for before every warp finds the largest
-// reference for itself; then one group adds the groups' sums.
+// reference and the whole softmax sum for itself; then one group adds the groups'
+// results.  The weights are made relative to that sum before they meet values: a
+// partial's sum may be 2^60 and more, and a value 2^127.
 //   Many sequences (few partials each): a small CTA a (chunk, query head), which
 // leaves at once where no sequence begins that goes on.
 //   Few sequences: a CTA a (sequence, query head, 32 columns), which finds the
@@ -1028,7 +1031,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 constexpr int kJoin = 256, kJoinSmall = 64, kLoad = 6;
 __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params p, int D, int width) {
     __shared__ float4 so[kJoin];
-    __shared__ float ssum[kJoin / 8];
     __shared__ int s_chunk;
     const int h = blockIdx.y, lane = threadIdx.x & 31;
     const int per = width / 4, groups = blockDim.x / per, grp = threadIdx.x / per, t = blockIdx.z * per + threadIdx.x % per;
@@ -1065,17 +1067,24 @@ __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params 
         }
     };
     ask(grp);
-    float m = kLow;
-    for (int i = lane; i <= j.y - c; i += 32) m = fmaxf(m, p.part_sum[slot(i)].x);
-    m = warp_max(m);
-    float sum = 0.f;
+    float m = kLow, sum = 0.f;
+    for (int i = lane; i <= j.y - c; i += 32) {
+        const float2 x = p.part_sum[slot(i)];
+        const float n = fmaxf(m, x.x);
+        sum = fmaf(x.y, ex2(x.x - n), sum * ex2(m - n));
+        m = n;
+    }
+    const float top = warp_max(m);
+    sum *= ex2(m - top);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = grp; i0 < n;) {
 #pragma unroll
         for (int k = 0; k < kLoad; ++k) {
             if (i0 + k * groups >= n) break;
-            const float x = w[k].y * ex2(w[k].x - m);
-            sum += x;
+            const float x = w[k].y * ex2(w[k].x - top) * inv;
             acc.x = fmaf(x, v[k].x, acc.x);
             acc.y = fmaf(x, v[k].y, acc.y);
             acc.z = fmaf(x, v[k].z, acc.z);
@@ -1085,26 +1094,22 @@ __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params 
         ask(i0);
     }
     so[threadIdx.x] = acc;
-    if (threadIdx.x % per == 0 && grp < groups) ssum[grp] = sum;
     __syncthreads();
     if (grp != 0) return;
     for (int g = 1; g < groups && g < n; ++g) {
         const float4 b = so[g * per + threadIdx.x];
-        sum += ssum[g];
         acc.x += b.x;
         acc.y += b.y;
         acc.z += b.z;
         acc.w += b.w;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long row = static_cast<long long>(j.x) * p.Hq + h;
     if (p.out_f32)
-        reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D)[t] =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D)[t] = acc;
     else
         reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D)[t] =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (t == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * kLn2f;
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    if (t == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2f;
 }
 
 template <class C, bool CLUSTER>

@@ -162,3 +162,20 @@ def test_decode_of_small_values_under_rising_scores(n, max_len):
     for out_dtype in (torch.float32, torch.bfloat16):
         out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
         check_decode(c, q, out, lse)
+
+
+@pytest.mark.parametrize("D,n,max_len", [(64, 4096, 4096), (128, 4096, 4096), (64, 200000, 200000), (256, 150000, 1 << 20)])
+def test_decode_joins_of_large_values_under_rising_scores(D, n, max_len):
+    """Scores of the last block e^27 above all others, less than a reference is
+    moved for, so that the last part's softmax sum is 2^40 and more, and values
+    of 2^110: the joined result is finite, and so is every product on the way."""
+    g = torch.Generator().manual_seed(n)
+    key = torch.randn(n, 1, D, generator=g)
+    key[:, 0, 0] = math.sqrt(D) * 27.0 * (torch.arange(n) // 128 == (n - 1) // 128)
+    value = torch.randn(n, 1, D, generator=g) * 2.0 ** 108
+    c = written(key, value, D)
+    q = torch.zeros(1, 2, D, dtype=torch.bfloat16)
+    q[:, :, 0] = torch.tensor([1.0, 0.5])
+    for out_dtype in (torch.float32, torch.bfloat16):
+        out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
+        check_decode(c, q, out, lse)
