@@ -42,6 +42,7 @@
 // chunks leaves fp32 partials (o, the scores' reference, the sum less it: an lse
 // would lose the sum's bits beside a large score), which paged_fp8_combine joins.  Few
 // short sequences take a cluster of CTAs each instead, which join on chip.
+#include <float.h>
 #include <math.h>
 
 #include <mutex>
@@ -635,7 +636,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                         dot[h] =
                             __ffma2_rn(make_float2(__uint_as_float(r1[2 * h]), __uint_as_float(r1[2 * h + 1])), splat(0.0625f),
                                        make_float2(__uint_as_float(r0[2 * h]), __uint_as_float(r0[2 * h + 1])));
-                        kq[h] = __fmul2_rn(qf[h], splat(kf));  // (first: dot * kf may overflow)
+                        // (first: dot * kf may overflow; and held finite, so that a dot of 0 is a score of 0)
+                        kq[h] = __fmul2_rn(qf[h], splat(kf));
+                        kq[h] = make_float2(fminf(kq[h].x, FLT_MAX), fminf(kq[h].y, FLT_MAX));
                         d[h] = __ffma2_rn(dot[h], kq[h], make_float2(-mref[h].x, -mref[h].y));
                         if (nvalid < kTok) d[h] = valid ? d[h] : splat(-INFINITY);
                         dmax = fmax3(dmax, d[h].x, d[h].y);

@@ -179,3 +179,22 @@ def test_decode_joins_of_large_values_under_rising_scores(D, n, max_len):
     for out_dtype in (torch.float32, torch.bfloat16):
         out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
         check_decode(c, q, out, lse)
+
+
+@pytest.mark.parametrize("D,hq", [(64, 2), (128, 4), (64, 8)])
+def test_decode_of_large_queries_beside_large_keys_they_do_not_meet(D, hq):
+    """Queries and keys of 2^100 in columns of their own: the factor of a score
+    overflows, the score is 0 or moderate all the same."""
+    n = 200
+    key = torch.zeros(n, 1, D)
+    key[::3, 0, 1] = 2.0 ** 100            # meets zeros of q
+    key[1::3, 0, 0] = 2.0 ** -98           # scores of 4 / sqrt(D)
+    key[1::3, 0, 2] = torch.randn(n // 3 + 1, generator=torch.Generator().manual_seed(1))[: len(key[1::3])] * 2.0 ** -98
+    value = torch.randn(n, 1, D, generator=torch.Generator().manual_seed(2))
+    c = written(key, value, D)
+    q = torch.zeros(1, hq, D, dtype=torch.bfloat16)
+    q[:, :, 0] = 2.0 ** 100
+    q[:, 0, 2] = 2.0 ** 99
+    for max_len in (n, 1 << 20):
+        out, lse = run_decode(c, q, max_len=max_len)
+        check_decode(c, q, out, lse)
