@@ -17,9 +17,9 @@
 //     weights are w_t = 2^(s_t + v_t - M), v_t = vb_t - 127, M the largest
 //     s_t + v_t of this block and head: the value's exponent goes into the
 //     weight's, and since every block has a reference of its own no weight is
-//     lost to a far larger one in another block.  256 w is split into NP e4m3
-//     pieces, each 16 times finer: NP = 3 holds an fp16 number's 11 significant
-//     bits (for bf16 output, which keeps 8), NP = 4 holds 16 (for fp32 output).
+//     lost to a far larger one in another block.  256 w is split into four e4m3
+//     pieces, each 16 times finer, which hold it to 2^-16 of itself, but to
+//     2^-30 of the block's largest at best (split_pair).
 // O^T of a block is read from TMEM and added, times 2^(M - R), to fp32
 // registers (thread = column d of the output), so nothing is rescaled in TMEM.
 // The softmax sum is kept apart from the weights, in fp32, each warp with a
@@ -67,9 +67,10 @@ constexpr int pow2_cols(int n) { return n <= 32 ? 32 : (n <= 64 ? 64 : (n <= 128
 // HG query heads a CTA.  Up to four heads one warpgroup does the softmax; eight
 // are shared by two, four heads each, so that a block's chain of products and
 // softmax stays short.  Two more warps load and issue the products.
-template <int D_, int HG_, int NP_>
+template <int D_, int HG_>
 struct Fp8Cfg {
-    static constexpr int D = D_, HG = HG_, NP = NP_;
+    static constexpr int D = D_, HG = HG_;
+    static constexpr int NP = 4;                     // e4m3 pieces of a weight
     static constexpr int NWG = HG > 4 ? 2 : 1;
     static constexpr int HT = HG / NWG;              // heads a thread
     static constexpr int SOFT = NWG * kWg;
@@ -203,36 +204,23 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
 }
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
 
-// The weights of two heads, y <= 256 each, as NP pairs of e4m3 codes, each
-// piece 16 times finer than the one before.  With three pieces (12 bits) the
-// weights go through fp16 (11 bits, its smallest step 2^-32 of the largest
-// weight), whose packed arithmetic halves the work: the differences are exact.
+// The weights of two heads, y of about 256 at most, as NP pairs of e4m3 codes, each
+// piece 16 times finer than the one before.  A piece takes 4 bits while it is a
+// normal number (2^-6 and up), so NP pieces are 2^-4NP of a weight off at most; below,
+// the last one's step is fixed, and what is lost is up to 2^-10 * 16^-(NP-1) of the
+// 256 that the block's largest weight is: 2^-30 of that weight for NP = 4.  A
+// value row with a larger exponent byte than its codes need, or with one column far
+// above the others, so costs the other rows of its block bits.  (Three pieces of an
+// fp16 number, 11 bits and 2^-26, take 5% less time at D = 64 with eight heads and
+// no less elsewhere: they were bf16 output's until its last bits were compared.)
 template <int NP>
 __device__ __forceinline__ void split_pair(float2 y, uint32_t (&c)[NP]) {
-    if constexpr (NP == 3) {
-        uint32_t x;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(y.y), "f"(y.x));
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            uint16_t r;
-            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
-            c[i] = r;
-            if (i + 1 < NP) {
-                uint32_t f;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(r));
-                asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %0, %1;\n\tmul.rn.f16x2 %0, t, %2;\n\t}"
-                    : "+r"(x)
-                    : "r"(f), "r"(0x4C004C00u));  // 16, 16
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            c[i] = pack_fp8x2<false>(y.x, y.y);
-            if (i + 1 < NP) {
-                const float2 f = unpack_fp8x2<false>(c[i]);
-                y = __fmul2_rn(__fadd2_rn(y, make_float2(-f.x, -f.y)), splat(16.f));
-            }
+    for (int i = 0; i < NP; ++i) {
+        c[i] = pack_fp8x2<false>(y.x, y.y);
+        if (i + 1 < NP) {
+            const float2 f = unpack_fp8x2<false>(c[i]);
+            y = __fmul2_rn(__fadd2_rn(y, make_float2(-f.x, -f.y)), splat(16.f));
         }
     }
 }
@@ -1159,18 +1147,16 @@ cudaError_t launch_cfg(const CUtensorMap& tm, const PagedFp8Params& p, cudaStrea
 }
 
 template <int D, int HG>
-cudaError_t launch_np(const CUtensorMap& tm, const PagedFp8Params& p, cudaStream_t st) {
-    if (p.cluster)
-        return p.out_f32 ? launch_cfg<Fp8Cfg<D, HG, 4>, true>(tm, p, st) : launch_cfg<Fp8Cfg<D, HG, 3>, true>(tm, p, st);
-    return p.out_f32 ? launch_cfg<Fp8Cfg<D, HG, 4>, false>(tm, p, st) : launch_cfg<Fp8Cfg<D, HG, 3>, false>(tm, p, st);
+cudaError_t launch_hg(const CUtensorMap& tm, const PagedFp8Params& p, cudaStream_t st) {
+    return p.cluster ? launch_cfg<Fp8Cfg<D, HG>, true>(tm, p, st) : launch_cfg<Fp8Cfg<D, HG>, false>(tm, p, st);
 }
 
 template <int D>
 cudaError_t launch_d(const CUtensorMap& tm, const PagedFp8Params& p, cudaStream_t st) {
     switch (p.head_cols) {
-        case 2: return launch_np<D, 2>(tm, p, st);
-        case 4: return launch_np<D, 4>(tm, p, st);
-        case 8: return launch_np<D, 8>(tm, p, st);
+        case 2: return launch_hg<D, 2>(tm, p, st);
+        case 4: return launch_hg<D, 4>(tm, p, st);
+        case 8: return launch_hg<D, 8>(tm, p, st);
         default: return cudaErrorInvalidValue;
     }
 }

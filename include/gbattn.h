@@ -415,10 +415,22 @@ gbattn_status attn_fwd_paged_noalloc(const void* q, const void* kv_cache, int nu
  * as they were, and every other one's are read (a row in the range of two
  * sequences, which takes boundaries that decrease, holds either's).
  *
- * attn_fwd_paged_fp8 -- attn_fwd_paged over the 8-bit cache: the same results
- * as over a bf16 cache that holds the values the codes stand for, the softmax
- * weights of a block of 128 tokens held to 11 significant bits for bf16 output
- * and to 16 for fp32.  Scores are fp32 and may be of any size up to 2^23.
+ * attn_fwd_paged_fp8 -- attn_fwd_paged over the 8-bit cache: the softmax of
+ * the values that the codes stand for, with these roundings beside fp32's.
+ *  - Scores are fp32 and may be of any size up to 2^23.
+ *  - A query value is exact unless it is more than 2^14 below the largest of
+ *    its head; below, it is off by up to 2^-21 of that largest one.
+ *  - A token's weight p_t (its softmax weight) times its value row's scale,
+ *    w_t = p_t * 2^(b_t - 127), is held to 2^-16 of itself, but no finer than to
+ *    2^-30 of the largest w_t of its block of 128 tokens.  Column d of a result
+ *    is then off by up to the sum over the tokens of |code of d| times that.  So a
+ *    value row whose exponent byte is larger than its codes need (rows written
+ *    by attn_kv_cache_write_fp8 never are), or that has one column far above the
+ *    others, costs the results that it does not reach itself: with a w_t 2^20
+ *    above all others of its block, those keep 9 bits.  A byte of zero codes
+ *    counts too; the write gives such rows the byte 1.
+ *  - Infinite codes (e5m2's, which the write never stores) have no defined
+ *    result in the heads (keys) or columns (values) that they are in.
  *   q         device bf16, sequence s's [Hq, D] at s * q_stride elements
  *             (at least Hq * D, a multiple of 8)
  *   workspace at least attn_fwd_paged_fp8_workspace_size bytes (may be 0:

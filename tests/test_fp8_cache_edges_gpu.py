@@ -198,3 +198,94 @@ def test_decode_of_large_queries_beside_large_keys_they_do_not_meet(D, hq):
     for max_len in (n, 1 << 20):
         out, lse = run_decode(c, q, max_len=max_len)
         check_decode(c, q, out, lse)
+
+
+# ---------------------------------------------------------------- decode: the weights' bits, column by column
+def check_columns(c, q, out, scale=None):
+    """Every column of the result against its own bound: w_t = p_t 2^(b_t - 127)
+    is off by up to 2^-16 w_t + 2^-30 max(w of the block), four pieces of four
+    bits, and by 4 ds + 2^-18 of itself as in check_decode (scores, ex2, fp32
+    sums); a result by that times |code|, summed over the tokens."""
+    S, hq, D = q.shape
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    values = c.values()
+    ks, vs = oracle.paged_gather(values, c.table, c.lens)
+    powers = np.exp2(c.scales[1].double().numpy() - 127.0)  # [nb, Hkv, bs]
+    got, g = to_np(out), hq // values.shape[3]
+    qd = q.double().numpy()
+    for s in range(S):
+        n = c.lens[s]
+        blocks = [np.arange(b, min(b + 128, n)) for b in range(0, n, 128)]
+        for h in range(hq):
+            k, v = ks[s][:, h // g], vs[s][:, h // g]
+            size = np.concatenate([powers[int(c.table[s, i]), h // g, :len(b)] for i, b in enumerate(blocks)])
+            x = scale * (k @ qd[s, h])
+            p = np.exp(x - x.max())
+            p /= p.sum()
+            w = p * size
+            ds = (D / 32 + 12) * 2.0 ** -23 * scale * float((np.abs(k) @ np.abs(qd[s, h])).max())
+            off = (2.0 ** -16 + 2.0 ** -18 + 4 * ds) * w
+            for b in blocks:
+                off[b] += 2.0 ** -30 * w[b].max()
+            want, tol = p @ v, (off / size) @ np.abs(v)
+            if out.dtype == torch.bfloat16:
+                tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want)
+            err = np.abs(got[s, h] - want)
+            assert (err <= tol).all(), (s, h, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D,hq,hkv", [(64, 8, 1), (64, 2, 2), (128, 4, 1), (192, 8, 2), (256, 6, 1)])
+def test_decode_columns_beside_one_far_larger_value(D, hq, hkv, out_dtype):
+    """A value row in each block with one column 2^6 to 2^24 above everything,
+    its other codes zero: the other columns keep what its bits leave."""
+    n = 900
+    c = Ctx([n, 300], hkv, D, seed=D)
+    for s, length in enumerate(c.lens):
+        for i in range(-(-length // 128)):
+            b, t = int(c.table[s, i]), (37 * i) % min(128, length - 128 * i)
+            c.codes[1, b, t] = 0
+            c.codes[1, b, t, :, (11 * i + s) % D] = 0x7E  # 448
+            c.scales[1, b, :, t] = 121 + 6 + 3 * (i % 7)
+    q = bf16(2, hq, D, seed=D + 1)
+    for max_len in (n, 1 << 20):
+        out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
+        check_columns(c, q, out)
+        check_decode(c, q, out, lse)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vexps,kexps", [((118, 124), (119, 123)), ((110, 130), (119, 123)), ((60, 190), (105, 124)), ((1, 30), (119, 123))])
+def test_decode_columns_with_scales_of_any_size(vexps, kexps, out_dtype):
+    """Value rows whose sizes differ by up to 2^130, block by block and row by row."""
+    c = Ctx([400, 700, 128, 1], 2, 128, seed=9, exps=kexps, vexps=vexps)
+    q = bf16(4, 6, 128, seed=10)
+    for max_len in (max(c.lens), 1 << 20):
+        out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
+        check_columns(c, q, out)
+        check_decode(c, q, out, lse)
+
+
+def test_decode_to_bf16_is_the_rounding_of_the_result_to_fp32():
+    """The two output types differ by one rounding, whatever the head count."""
+    for D, hq, hkv, lens in ((64, 20, 4, [1, 900, 4097]), (128, 32, 8, [517]), (256, 8, 1, [9000, 20000])):
+        c = Ctx(lens, hkv, D, seed=hq)
+        q = bf16(len(lens), hq, D, seed=D)
+        a, la = run_decode(c, q)
+        b, lb = run_decode(c, q, out_dtype=torch.bfloat16)
+        assert torch.equal(a.to(torch.bfloat16), b) and torch.equal(la, lb)
+
+
+def test_decode_of_infinite_codes_reaches_its_own_heads_and_columns_only():
+    c = Ctx([200, 200], 2, 64, "e5m2", seed=6)
+    q = bf16(2, 4, 64, seed=7)
+    for max_len in (200, 1 << 20):
+        clean, clean_lse = run_decode(c, q, max_len=max_len)
+        bad = Ctx([200, 200], 2, 64, "e5m2", seed=6)
+        bad.codes[0, int(bad.table[0, 0]), 7, 1, 3] = 0x7C   # a key of sequence 0, KV head 1
+        bad.codes[1, int(bad.table[1, 1]), 2, 0, 9] = 0xFC   # a value of sequence 1, KV head 0, column 9
+        out, lse = run_decode(bad, q, max_len=max_len)
+        free, free_lse = torch.ones(2, 4, 64, dtype=torch.bool), torch.ones(2, 4, dtype=torch.bool)
+        free[0, 2:], free_lse[0, 2:], free[1, :2, 9] = False, False, False
+        assert torch.equal(out.cpu()[free], clean.cpu()[free]) and torch.equal(lse.cpu()[free_lse], clean_lse.cpu()[free_lse])
+        assert not torch.isfinite(out[1, :2, 9]).any()
