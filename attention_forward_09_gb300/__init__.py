@@ -578,6 +578,9 @@ def attn_fwd_paged_prefill_fp8(q, kv_cache, kv_scales, block_table, cu_seqlens_q
     with torch.cuda.device(kv_cache.device):
         s = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(s):
+            if Tq == 0:  # no query, no result
+                out = torch.empty(0, Hq, d, dtype=out_dtype, device=q.device) if out is None else out
+                return out, given if given is not None else q.new_empty(Hq, 0, dtype=torch.float32) if lse else None
             return attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seq_len, softmax_scale, causal,
                                    out, given if given is not None else True if lse else None, out_dtype,
                                    dev_status, stream)

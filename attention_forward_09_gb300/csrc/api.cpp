@@ -506,9 +506,10 @@ gbattn_status attn_fwd_paged(const void* q, const void* kv_cache, int num_blocks
                              int causal, void* out, gbattn_dtype out_dtype, float* lse, void* workspace,
                              size_t workspace_bytes, uint32_t* dev_status, void* stream) {
     (void)causal;  // one query token sees its whole context under the bottom-right rule
-    if (!q || !kv_cache || !block_table || !seq_lens || !out) return GBATTN_ERR_INVALID_ARG;
+    // without sequences the arrays over them are empty, and may be null
+    if (!kv_cache || (num_seqs != 0 && (!q || !block_table || !seq_lens || !out))) return GBATTN_ERR_INVALID_ARG;
     if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || !scale_ok(softmax_scale)) return GBATTN_ERR_INVALID_ARG;
-    if (num_blocks <= 0 || max_blocks_per_seq <= 0 || num_seqs < 0 || max_seq_len < 0)
+    if (num_blocks <= 0 || max_blocks_per_seq < (num_seqs != 0 ? 1 : 0) || num_seqs < 0 || max_seq_len < 0)
         return GBATTN_ERR_INVALID_ARG;
     if (!head_size_ok(D)) return GBATTN_ERR_UNSUPPORTED;
     if (block_size != 128) return GBATTN_ERR_UNSUPPORTED;
@@ -654,9 +655,11 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
                                  float* lse, void* workspace, size_t workspace_bytes, uint32_t* dev_status,
                                  void* stream) {
     (void)causal;  // one query token sees its whole context under the bottom-right rule
-    if (!q || !kv_cache || !kv_scales || !block_table || !seq_lens || !out) return GBATTN_ERR_INVALID_ARG;
+    // without sequences the arrays over them are empty, and may be null
+    if (!kv_cache || !kv_scales || (num_seqs != 0 && (!q || !block_table || !seq_lens || !out)))
+        return GBATTN_ERR_INVALID_ARG;
     if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || !scale_ok(softmax_scale)) return GBATTN_ERR_INVALID_ARG;
-    if (max_blocks_per_seq <= 0 || num_seqs < 0 || max_seq_len < 0) return GBATTN_ERR_INVALID_ARG;
+    if (max_blocks_per_seq < (num_seqs != 0 ? 1 : 0) || num_seqs < 0 || max_seq_len < 0) return GBATTN_ERR_INVALID_ARG;
     gbattn_status s = check_fp8_cache(num_blocks, block_size, Hkv, D, kv_dtype);
     if (s != GBATTN_OK) return s;
     if (block_size != 128) return GBATTN_ERR_UNSUPPORTED;

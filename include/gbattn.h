@@ -325,7 +325,9 @@ size_t attn_fwd_paged_workspace_size(int num_seqs, int Hq, int Hkv, int D, int m
  * Slots of the last block past seq_len are never used.  A block_table
  * entry outside [0, num_blocks) sets GBATTN_DEV_BAD_INDEX and its tokens are
  * skipped; a seq_len above max_seq_len sets GBATTN_DEV_BAD_SEQLEN and is
- * clamped.  A sequence with seq_len 0 gets out = 0 and lse = -inf.
+ * clamped.  A sequence with seq_len 0 gets out = 0 and lse = -inf.  With
+ * num_seqs = 0 nothing is done, and q, block_table, seq_lens, out and workspace
+ * may be NULL.
  */
 gbattn_status attn_fwd_paged(const void* q, const void* kv_cache, int num_blocks, int block_size,
                              const int32_t* block_table, int max_blocks_per_seq,

@@ -289,3 +289,38 @@ def test_decode_of_infinite_codes_reaches_its_own_heads_and_columns_only():
         free[0, 2:], free_lse[0, 2:], free[1, :2, 9] = False, False, False
         assert torch.equal(out.cpu()[free], clean.cpu()[free]) and torch.equal(lse.cpu()[free_lse], clean_lse.cpu()[free_lse])
         assert not torch.isfinite(out[1, :2, 9]).any()
+
+
+# ---------------------------------------------------------------- calls without work
+@pytest.mark.parametrize("columns", [0, 3])
+def test_calls_without_sequences_or_tokens(columns):
+    """Empty tensors have no address; a batch of no sequences is a batch all the same."""
+    hq, hkv, D = 4, 2, 64
+    c = Ctx([5], hkv, D)
+    cache, scales, _ = c.on_gpu()
+    before = raw(cache), scales.cpu()
+    plain = torch.zeros(2, 3, 128, hkv, D, dtype=torch.bfloat16, device=dev())
+    q = torch.empty(0, hq, D, dtype=torch.bfloat16, device=dev())
+    kv = torch.empty(0, hkv, D, dtype=torch.bfloat16, device=dev())
+    table, none = torch.empty(0, columns, dtype=torch.int32, device=dev()), ints([])
+    for max_len in (0, 300, 1 << 20):
+        for out, lse in (gb.attn_fwd_paged_fp8(q, cache, scales, table, none, max_len, lse=True),
+                         gb.attn_fwd_paged(q, plain, table, none, max_len, lse=True),
+                         gb.attn_fwd_paged_noalloc(q, plain, table, none, max_len, lse=True)):
+            assert out.shape == (0, hq, D) and lse.shape == (0, hq)
+    gb.attn_kv_cache_write_fp8(kv, kv, none, cache, scales)
+    assert np.array_equal(raw(cache), before[0]) and torch.equal(scales.cpu(), before[1])
+    k, v = gb.attn_kv_cache_read_fp8(cache, scales, table, ints([0]), 0)
+    assert k.shape == v.shape == (0, hkv, D)
+    k, _ = gb.attn_kv_cache_read_fp8(cache, scales, table, ints([0]), 7)
+    assert k.shape == (7, hkv, D)
+    out, lse = gb.attn_fwd_paged_prefill_fp8(q, cache, scales, table, ints([0]), ints([0]), 0, 0, 300, lse=True)
+    assert out.shape == (0, hq, D) and lse.shape == (hq, 0)
+    # sequences, but no token of any
+    table = torch.full((2, max(columns, 1)), -1, dtype=torch.int32, device=dev())
+    status = status_word()
+    out, lse = gb.attn_fwd_paged_prefill_fp8(q, cache, scales, table, ints([0, 0, 0]), ints([0, 0, 0]), 0, 0, 300, dev_status=status)
+    assert out.shape == (0, hq, D) and lse is None
+    out, lse = gb.attn_fwd_paged_fp8(torch.zeros(2, hq, D, dtype=torch.bfloat16, device=dev()), cache, scales, table, ints([0, 0]), 0,
+                                     lse=True, dev_status=status)
+    assert not out.any() and torch.isneginf(lse).all() and int(status) == 0
