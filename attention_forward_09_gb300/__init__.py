@@ -559,8 +559,9 @@ def attn_fwd_paged_prefill_fp8(q, kv_cache, kv_scales, block_table, cu_seqlens_q
     _index_table("block_table", block_table, 2)
     T, max_seqlen_q, max_seq_len = int(total_tokens), _host_int("max_seqlen_q", max_seqlen_q), _host_int("max_seq_len", max_seq_len)
     # the read-back refuses a context that its row of the table cannot hold and
-    # leaves its rows unwritten: attn_fwd_varlen has to skip that sequence too
-    max_seq_len = min(max_seq_len, bs * block_table.shape[1])
+    # leaves its rows unwritten: attn_fwd_varlen has to skip that sequence too (and
+    # takes no bound above the rows there are)
+    max_seq_len = min(max_seq_len, bs * block_table.shape[1], T)
     if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != d or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous bfloat16 tensor [tokens, Hq, {d}]")
     Tq, Hq, _ = q.shape

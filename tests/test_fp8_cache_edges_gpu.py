@@ -324,3 +324,22 @@ def test_calls_without_sequences_or_tokens(columns):
     out, lse = gb.attn_fwd_paged_fp8(torch.zeros(2, hq, D, dtype=torch.bfloat16, device=dev()), cache, scales, table, ints([0, 0]), 0,
                                      lse=True, dev_status=status)
     assert not out.any() and torch.isneginf(lse).all() and int(status) == 0
+
+
+@pytest.mark.parametrize("most", [10 ** 6, 700])
+def test_prefill_with_a_length_bound_above_the_contexts_sum(most):
+    """max_seq_len bounds the contexts; it may be the model's longest."""
+    hq, hkv, D, lens = 4, 2, 64, [130, 77]
+    c = Ctx(lens, hkv, D, seed=25)
+    cache, scales, table = c.on_gpu()
+    wide = torch.full((2, 10000), -1, dtype=torch.int32, device=dev())
+    wide[:, :table.shape[1]] = table
+    q_lens = [30, 77]
+    q = bf16(sum(q_lens), hq, D, seed=26)
+    cu_q, cu_k = ints(np.cumsum([0] + q_lens)), ints(np.cumsum([0] + lens))
+    ref, ref_lse = oracle.attention_paged_prefill(q, c.values(), c.table, lens, cu_q, 1 / math.sqrt(D), True)
+    status = status_word()
+    out, lse = gb.attn_fwd_paged_prefill_fp8(q.to(dev()), cache, scales, wide, cu_q, cu_k, sum(lens), max(q_lens), most, lse=True,
+                                             dev_status=status)
+    assert int(status) == 0
+    assert np.abs(to_np(out) - ref).max() <= 1e-2 and np.abs(to_np(lse) - ref_lse).max() <= 1e-3  # the prefill kernels' bounds
