@@ -189,7 +189,7 @@ def attn_fwd_dense_plan(B, Sq, Sk, Hq, Hkv, D, causal=False):
 
 
 def attn_set_wait_give_up(on) -> bool:
-    """Make the prefill kernels launched from now on give up their pipeline
+    """Make the prefill and 8-bit decode kernels launched from now on give up their pipeline
     waits at once (a test of the failure path: GBATTN_DEV_TIMEOUT is set,
     the call returns, outputs are undefined); returns the previous setting."""
     prev = ctypes.c_int(0)

@@ -144,12 +144,12 @@ gbattn_status check_fp8_cache(int num_blocks, int block_size, int Hkv, int D, gb
     return GBATTN_OK;
 }
 
-// 1: the prefill kernels give up every pipeline wait (attn_set_wait_give_up).
+// 1: the prefill and 8-bit decode kernels give up every pipeline wait (attn_set_wait_give_up).
 std::atomic<int> g_give_up{0};
 
 }  // namespace
 
-int gbattn::prefill_give_up() { return g_give_up.load(std::memory_order_relaxed); }
+int gbattn::wait_give_up() { return g_give_up.load(std::memory_order_relaxed); }
 
 extern "C" {
 
@@ -185,7 +185,7 @@ gbattn_status attn_fwd_dense(const void* q, const void* k, const void* v, int B,
         return GBATTN_ERR_UNSUPPORTED;  // row counts are 32-bit on the device
     if (B == 0 || Sq == 0) return GBATTN_OK;
     PrefillParams p{};
-    p.give_up = gbattn::prefill_give_up();
+    p.give_up = gbattn::wait_give_up();
     p.out = out;
     p.lse = lse;
     p.status = dev_status;
@@ -222,7 +222,7 @@ gbattn_status attn_fwd_padded(const void* q, const void* k, const void* v, const
         return GBATTN_ERR_UNSUPPORTED;  // row counts are 32-bit on the device
     if (B == 0 || Sq == 0) return GBATTN_OK;
     PrefillParams p{};
-    p.give_up = gbattn::prefill_give_up();
+    p.give_up = gbattn::wait_give_up();
     p.out = out;
     p.lse = lse;
     p.status = dev_status;
@@ -319,7 +319,7 @@ gbattn_status attn_fwd_varlen(const void* q, const void* k, const void* v, const
     if (num_docs > 65535) return GBATTN_ERR_UNSUPPORTED;
     if (num_docs == 0 || Tq == 0 || max_seqlen_q == 0) return GBATTN_OK;
     PrefillParams p{};
-    p.give_up = gbattn::prefill_give_up();
+    p.give_up = gbattn::wait_give_up();
     p.out = out;
     p.lse = lse;
     p.status = dev_status;
@@ -391,7 +391,7 @@ gbattn_status attn_fwd_paged_prefill(const void* q, const void* kv_cache, int nu
     s = device_info(&di);
     if (s != GBATTN_OK) return s;
     PrefillParams p{};
-    p.give_up = gbattn::prefill_give_up();
+    p.give_up = gbattn::wait_give_up();
     p.out = out;
     p.lse = lse;
     p.status = dev_status;
@@ -715,6 +715,7 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
     p.scale_log2 = softmax_scale * kLog2e;
     p.out_f32 = out_dtype == GBATTN_OUT_F32;
     p.e5m2 = kv_dtype == GBATTN_KV_E5M2;
+    p.give_up = gbattn::wait_give_up();
     return gbattn::launch_paged_fp8(D, tm, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GBATTN_OK
                                                                                              : GBATTN_ERR_CUDA;
 }

@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         mbar_init(b_pfull, SOFT_WARPS);
         mbar_init(b_ofull, 1);
         mbar_init(b_done, 1);
-        abort_storage = 0;
+        abort_storage = p.give_up ? 1 : 0;  // 1: give up every wait (failure-path test)
         s_issued = 0;
         s_join = make_int2(-1, 0);
         s_parts = 0;
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             s_first[1] = static_cast<int>(b0);
             s_first[2] = given_up ? 0 : static_cast<int>(cut.start(chunk + 1) - b0);
             const int parts = min(blocks, p.chunks);
-            s_parts = parts > 1 ? parts : 0;  // one part is the whole: written out, nothing to join
+            s_parts = parts > 1 && !given_up ? parts : 0;  // one part is the whole: written out, nothing to join
         }
     } else {
         uint32_t incl = sum;
@@ -662,6 +662,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     }
                     if (b > w.b0) ask_o(g - 1);
                     if (named_bar_or(1 + wg, kWg, !ok)) {  // a warpgroup's four warps leave together
+                        tmem_wait_ld();  // (what ask_o asked for, before tensor memory is freed)
                         quit = true;
                         break;
                     }
@@ -937,7 +938,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             __syncwarp();
             if (++vslot == STAGES) vslot = 0;
         };
-        ok = issue_s(0);
+        // A launch told to give up (p.give_up) stops here, before any product.
+        ok = !__any_sync(0xffffffffu, *abort_flag) && issue_s(0);
         for (uint32_t i = 0; ok; ++i) {
             const bool another = more;
             if (another) ok = issue_s(i + 1);

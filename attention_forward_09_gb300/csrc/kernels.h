@@ -63,8 +63,8 @@ struct PrefillParams {
     const int32_t* lens_k;
 };
 
-// The give-up setting the host API passes to the prefill kernels (process-wide).
-int prefill_give_up();
+// The give-up setting the host API passes to the prefill and 8-bit decode kernels (process-wide).
+int wait_give_up();
 
 // Tensor maps are built by the host (api.cpp) over q [Tq, Hq, D] and
 // k / v [Tk, Hkv, D] (box {64, 1, rows}) and over out [Tq, Hq, D] (box
@@ -208,6 +208,7 @@ struct PagedFp8Params {
     int cluster;      // 1: a cluster of `chunks` CTAs a (sequence, head group) joins on chip; no workspace
     float scale_log2;
     int out_f32, e5m2;
+    int give_up;  // as PrefillParams::give_up
 };
 struct PagedFp8Plan {
     int subs, heads_per_sub, head_cols, chunks, cluster;

@@ -464,8 +464,8 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
 
 /*
  * attn_set_wait_give_up -- a switch for testing the failure path of the
- * prefill kernels (attn_fwd_dense, attn_fwd_varlen, attn_fwd_paged_prefill),
- * process-wide, for the launches made after the call.  on = 1: each CTA
+ * prefill kernels (attn_fwd_dense, attn_fwd_varlen, attn_fwd_paged_prefill)
+ * and of attn_fwd_paged_fp8, process-wide, for the launches made after the call.  on = 1: each CTA
  * gives up its pipeline waits at once, as if they had run out of time: it
  * issues no MMA, lets its copies land, frees its tensor memory, sets
  * GBATTN_DEV_TIMEOUT in dev_status and returns; the call comes back with

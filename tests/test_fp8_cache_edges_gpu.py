@@ -343,3 +343,32 @@ def test_prefill_with_a_length_bound_above_the_contexts_sum(most):
                                              dev_status=status)
     assert int(status) == 0
     assert np.abs(to_np(out) - ref).max() <= 1e-2 and np.abs(to_np(lse) - ref_lse).max() <= 1e-3  # the prefill kernels' bounds
+
+
+# ---------------------------------------------------------------- waits that give up
+@pytest.mark.parametrize("max_len", [3000, 1 << 20])  # a cluster a sequence and head; chunks and a join
+@pytest.mark.parametrize("D,hq,hkv", [(64, 4, 2), (128, 8, 1), (256, 4, 4)])
+def test_decode_that_gives_up_reports_timeout_and_the_context_stays_usable(D, hq, hkv, max_len):
+    """Loads are issued and land, no product is; nothing is left waiting."""
+    c = Ctx([3000, 0, 129, 700], hkv, D, seed=27)
+    q = bf16(4, hq, D, seed=28)
+    prev = gb.attn_set_wait_give_up(True)
+    try:
+        status = status_word()
+        _, lse = run_decode(c, q, max_len=max_len, status=status)
+        torch.cuda.synchronize()  # the call comes back
+        assert int(status) == gb.DEV_TIMEOUT
+        assert torch.isneginf(lse[1]).all()  # the empty sequence waits for nothing
+    finally:
+        gb.attn_set_wait_give_up(prev)
+    # a status word that already holds a timeout: nothing more is begun
+    out, lse = torch.full((4, hq, D), 77.0, device=dev()), torch.full((4, hq), 77.0, device=dev())
+    cache, scales, table = c.on_gpu()
+    for _ in range(2):
+        gb.attn_fwd_paged_fp8(q.to(dev()), cache, scales, table, ints(c.lens), max_len, out=out, lse=lse, dev_status=status)
+        assert int(status) == gb.DEV_TIMEOUT
+        assert (out[[0, 2, 3]] == 77).all() and (lse[[0, 2, 3]] == 77).all() and not out[1].any()
+    status.zero_()
+    out, lse = run_decode(c, q, max_len=max_len, status=status)
+    assert int(status) == 0
+    check_decode(c, q, out, lse)
