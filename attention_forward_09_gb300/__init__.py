@@ -392,7 +392,7 @@ def _index_table(name, t, dim):
 def _status_ptr(dev_status):
     if dev_status is None:
         return None
-    if dev_status.element_size() != 4 or dev_status.numel() < 1:
+    if dev_status.dtype not in (torch.int32, torch.uint32) or dev_status.numel() < 1:
         raise ValueError("dev_status must be a 32-bit integer tensor")
     return dev_status.data_ptr()
 
