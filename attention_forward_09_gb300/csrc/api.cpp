@@ -134,6 +134,9 @@ gbattn_status run_prefill(const void* q, const void* k, const void* v, long long
     return gbattn::launch_prefill(D, tq, tk, tv, to, p, di.sms, st) == cudaSuccess ? GBATTN_OK : GBATTN_ERR_CUDA;
 }
 
+// Query heads of the 8-bit decode: rows of a grid (and small enough for the plan's 32-bit counts).
+constexpr int kFp8MaxHeads = 65535;
+
 // Shared by the calls on the 8-bit cache: its sizes and code format.
 gbattn_status check_fp8_cache(int num_blocks, int block_size, int Hkv, int D, gbattn_kv_dtype kv) {
     if (num_blocks <= 0 || block_size <= 0 || Hkv <= 0) return GBATTN_ERR_INVALID_ARG;
@@ -644,7 +647,8 @@ gbattn_status attn_kv_cache_read_fp8(const void* kv_cache, const uint8_t* kv_sca
 }
 
 size_t attn_fwd_paged_fp8_workspace_size(int num_seqs, int Hq, int Hkv, int D, int max_seq_len) {
-    if (num_seqs <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_seq_len < 0 || !head_size_ok(D)) return 0;
+    if (num_seqs <= 0 || Hq <= 0 || Hq > kFp8MaxHeads || Hkv <= 0 || Hq % Hkv != 0 || max_seq_len < 0 || !head_size_ok(D))
+        return 0;
     return gbattn::paged_fp8_plan(num_seqs, Hq, Hkv, D, max_seq_len).workspace_bytes;
 }
 
@@ -664,6 +668,7 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
     if (s != GBATTN_OK) return s;
     if (block_size != 128) return GBATTN_ERR_UNSUPPORTED;
     if (out_dtype != GBATTN_OUT_BF16 && out_dtype != GBATTN_OUT_F32) return GBATTN_ERR_UNSUPPORTED;
+    if (Hq > kFp8MaxHeads) return GBATTN_ERR_UNSUPPORTED;
     if (2LL * num_blocks * 128 > 0x7FFFFFFFLL) return GBATTN_ERR_UNSUPPORTED;  // TMA row coordinate is int32
     if (num_seqs > 1 && q_stride < static_cast<long long>(Hq) * D) return GBATTN_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(kv_scales) || !aligned16(out) || q_stride % 8 != 0)
@@ -674,7 +679,7 @@ gbattn_status attn_fwd_paged_fp8(const void* q, long long q_stride, const void* 
     if (num_seqs * ((blocks < max_blocks_per_seq ? blocks : max_blocks_per_seq) + 1) > 0x7fffffffLL)
         return GBATTN_ERR_UNSUPPORTED;
     const gbattn::PagedFp8Plan plan = gbattn::paged_fp8_plan(num_seqs, Hq, Hkv, D, max_seq_len);
-    if (plan.n_hgroups * plan.chunks > 0x7fffffffLL || Hq > 65535) return GBATTN_ERR_UNSUPPORTED;
+    if (plan.n_hgroups * plan.chunks * (plan.cluster ? num_seqs : 1) > 0x7fffffffLL) return GBATTN_ERR_UNSUPPORTED;
     if (plan.workspace_bytes &&
         (!workspace || workspace_bytes < plan.workspace_bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return GBATTN_ERR_WORKSPACE;

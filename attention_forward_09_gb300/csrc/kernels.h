@@ -216,7 +216,7 @@ struct PagedFp8Plan {
     size_t o_bytes, sum_bytes;  // workspace sections, each 256-byte aligned; then the joins
     size_t workspace_bytes;
 };
-// num_seqs, Hq, Hkv, D > 0, Hq % Hkv == 0.
+// num_seqs, Hq, Hkv, D > 0, Hq % Hkv == 0, Hq <= 65535.
 PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_len);
 // Bytes of a row in one TMA box of the decode, and the box's swizzle span: 64
 // where that divides D and 128 does not, so that shared memory holds no

@@ -440,7 +440,7 @@ gbattn_status attn_fwd_paged_noalloc(const void* q, const void* kv_cache, int nu
  *             initialisation; calls that can overlap need one each
  * The other arguments, the treatment of unused slots and table entries, of
  * empty sequences, bad blocks (their tokens are skipped) and bad lengths, and
- * the errors are those of attn_fwd_paged.  block_size must be 128.  A query
+ * the errors are those of attn_fwd_paged.  block_size must be 128, and Hq at most 65535.  A query
  * value that is NaN or infinite makes its head's result NaN.
  *
  * attn_fwd_paged_fp8_workspace_size -- pure host arithmetic, as
