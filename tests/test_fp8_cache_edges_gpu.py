@@ -372,3 +372,79 @@ def test_decode_that_gives_up_reports_timeout_and_the_context_stays_usable(D, hq
     out, lse = run_decode(c, q, max_len=max_len, status=status)
     assert int(status) == 0
     check_decode(c, q, out, lse)
+
+
+# ---------------------------------------------------------------- bad lengths, streams, the prompt form
+@pytest.mark.parametrize("max_len,clamped", [(300, 300), (30000, 384)])  # a cluster each; chunks, where the table's end is the bound
+def test_decode_clamps_bad_lengths_to_what_there_is(max_len, clamped):
+    lens = [1 << 30, -3, 50, 300]
+    c = Ctx([384, 100, 50, 384], 2, 64, seed=8)
+    c.table = c.table[:, :3].contiguous()
+    q = bf16(4, 4, 64, seed=9)
+    cache, scales, table = c.on_gpu()
+    status = status_word()
+    out, lse = gb.attn_fwd_paged_fp8(q.to(dev()), cache, scales, table, ints(lens), max_len, lse=True, dev_status=status)
+    assert int(status) == gb.DEV_BAD_SEQLEN
+    c.lens = [clamped, 0, 50, 300]
+    check_decode(c, q, out, lse)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("D", HEAD_SIZES)
+def test_prefill_head_sizes_and_formats_on_a_stream_of_its_own(D, kind):
+    """The whole way on a stream that is not the current one: the write, the
+    prompt form, the read-back and a decode, with nothing but that stream's order."""
+    hq, hkv, lens, q_lens = 6, 2, [300, 1, 0, 140], [7, 1, 0, 140]
+    S, nblk = len(lens), 3
+    k, v = bf16(sum(lens), hkv, D, seed=1).to(dev()), bf16(sum(lens), hkv, D, seed=2, spread=3.0).to(dev())
+    q = bf16(sum(q_lens), hq, D, seed=3)
+    table = torch.randperm(S * nblk, generator=torch.Generator().manual_seed(D)).to(torch.int32).view(S, nblk)
+    where = torch.cat([table[s, torch.arange(n) // 128] * 128 + torch.arange(n) % 128 for s, n in enumerate(lens)]).to(torch.int32)
+    cache = torch.zeros(2, S * nblk, 128, hkv, D, device=dev()).to(DTYPES[kind])
+    scales = torch.ones(2, S * nblk, hkv, 128, dtype=torch.uint8, device=dev())
+    cu_q, cu_k, sl = ints(np.cumsum([0] + q_lens)), ints(np.cumsum([0] + lens)), ints(lens)
+    last = torch.stack([q[max(0, sum(q_lens[:s + 1]) - 1)] for s in range(S)])
+    qd, where, table_d, last_d, status = q.to(dev()), where.to(dev()), table.to(dev()), last.to(dev()), status_word()
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gb.attn_kv_cache_write_fp8(k, v, where, cache, scales, dev_status=status, stream=stream)
+    out, lse = gb.attn_fwd_paged_prefill_fp8(qd, cache, scales, table_d, cu_q, cu_k, sum(lens), max(q_lens), max(lens), lse=True,
+                                             dev_status=status, stream=stream)
+    rk, rv = gb.attn_kv_cache_read_fp8(cache, scales, table_d, cu_k, sum(lens), dev_status=status, stream=stream)
+    one, one_lse = gb.attn_fwd_paged_fp8(last_d, cache, scales, table_d, sl, max(lens), lse=True, dev_status=status, stream=stream)
+    stream.synchronize()
+    assert int(status) == 0
+    c = Ctx([1], hkv, D, kind)
+    c.lens, c.table, c.codes, c.scales = lens, table, cache.view(torch.uint8).cpu(), scales.cpu()
+    gathered = oracle.paged_gather(c.values(), table, lens)
+    for got, want in zip((rk, rv), gathered):
+        assert np.array_equal(to_np(got), np.concatenate(want))  # (codes of at most 4 bits: bf16 holds them)
+    ref, ref_lse = oracle.attention_paged_prefill(q, c.values(), table, lens, cu_q.cpu(), 1 / math.sqrt(D), True)
+    # the prefill kernels' weights are bf16, 2^-8 of themselves off at most; as much again for everything else
+    tol = 2.0 ** -7 * max(float(np.abs(x).max()) for x in gathered[1] if x.size)
+    assert np.abs(to_np(out) - ref).max() <= tol and np.abs(to_np(lse) - ref_lse).max() <= 1e-3
+    check_decode(c, last, one, one_lse)
+
+
+def test_read_and_write_in_a_graph_with_new_contents():
+    """Captured once, replayed with other tokens, slots and boundaries."""
+    hkv, D, T = 2, 96, 300
+    key, slots, cu = bf16(T, hkv, D, seed=1).to(dev()), ints(range(T)), ints([0, 100, 300])
+    cache = torch.zeros(2, 4, 128, hkv, D, device=dev()).to(torch.float8_e4m3fn)
+    scales = torch.ones(2, 4, hkv, 128, dtype=torch.uint8, device=dev())
+    table, status = ints([[0, 1, 2, 3], [3, 2, 1, 0]]).view(2, 4), status_word()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gb.attn_kv_cache_write_fp8(key, key, slots, cache, scales, dev_status=status)
+        k, v = gb.attn_kv_cache_read_fp8(cache, scales, table, cu, T, dev_status=status)
+    for seed, bounds in ((2, [0, 300, 300]), (3, [0, 17, 290])):
+        key.copy_(bf16(T, hkv, D, seed=seed))
+        slots.copy_(torch.randperm(512, generator=torch.Generator().manual_seed(seed))[:T])
+        cu.copy_(ints(bounds))
+        g.replay()
+        torch.cuda.synchronize()
+        want = oracle.paged_gather(oracle.stands_for(raw(cache), scales.cpu().numpy(), "e4m3"), table.cpu(),
+                                   [bounds[1], bounds[2] - bounds[1]])
+        assert int(status) == 0
+        for got, x in zip((k, v), want):
+            assert np.array_equal(to_np(got[:bounds[2]]), np.concatenate(x))
