@@ -443,8 +443,9 @@ def attn_kv_cache_write_fp8(key, value, slot_mapping, kv_cache, kv_scales, dev_s
     a fused projection's output) into the 8-bit cache kv_cache [2, nb, bs, Hkv,
     D] (float8_e4m3fn or float8_e5m2) and its exponent bytes kv_scales [2, nb,
     Hkv, bs] (uint8), in place, at slot_mapping [T] (int32): token t goes to
-    block slot // bs, offset slot % bs; negative slots store nothing.  A row
-    is codes c and a byte b that stand for c * 2^(b - 127).  Returns
+    block slot // bs, offset slot % bs; negative slots store nothing, and a
+    slot is to be given once (what one given twice stands for is undefined).
+    A row is codes c and a byte b that stand for c * 2^(b - 127).  Returns
     (kv_cache, kv_scales)."""
     code, nb, bs, hkv, d = _fp8_cache(kv_cache, kv_scales)
     ks, vs = _token_rows("key", key, hkv, d), _token_rows("value", value, hkv, d)

@@ -395,10 +395,11 @@ gbattn_status attn_fwd_paged_noalloc(const void* q, const void* kv_cache, int nu
  * least one >= -126 with max |x| <= c_max * 2^e over its finite values (-126
  * for a row without a non-zero one); its codes are x / 2^e rounded to nearest,
  * ties to even, and NaN where x is NaN or infinite.
- * Repeated slots, slots past the cache and errors as for attn_kv_cache_write
- * (for a repeated slot, each row of codes and each exponent byte is one of
- * the tokens', not necessarily the same one's), plus GBATTN_ERR_UNSUPPORTED
- * for an unknown kv_dtype.
+ * Slots past the cache and errors as for attn_kv_cache_write, plus
+ * GBATTN_ERR_UNSUPPORTED for an unknown kv_dtype.  A slot is to be given once:
+ * of tokens with the same slot, codes of one may lie beside codes and the
+ * exponent byte of another, so that the slot stands for neither (other slots
+ * are not touched).
  *
  * attn_kv_cache_read_fp8 -- the contexts of num_seqs sequences as packed bf16
  * rows, the k and v of attn_fwd_varlen (a prefill over a cached context).
