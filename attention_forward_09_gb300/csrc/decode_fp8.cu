@@ -225,6 +225,21 @@ __device__ __forceinline__ void split_pair(float2 y, uint32_t (&c)[NP]) {
     }
 }
 
+// A part of a sequence, (reference, softmax sum less it), among others: its weight is
+// sum * 2^(reference - top), with `top` the largest of all parts' reference plus
+// exponent of the sum (a reference may lie 60 and more below its part's scores).  It
+// is given as a number of 2^-100 at least and what is below that as a factor of its
+// own, 1 as a rule: a part of weight 2^-150 still counts where its values are 2^150
+// times the others'.
+__device__ __forceinline__ int sum_exponent(float2 part) { return ((__float_as_int(part.y) >> 23) & 255) - 127; }
+__device__ __forceinline__ float part_top(float2 part) { return part.x + static_cast<float>(sum_exponent(part)); }
+__device__ __forceinline__ float part_weight(float2 part, float top, float& low) {
+    const float mant = __int_as_float((__float_as_int(part.y) & 0x7FFFFF) | 0x3F800000);
+    const float power = (part.x - top) + static_cast<float>(sum_exponent(part)), above = fmaxf(power, -100.f);
+    low = ex2(power - above);
+    return part.y < INFINITY ? mant * ex2(above) : NAN;
+}
+
 __device__ __forceinline__ int clamp_len(const PagedFp8Params& p, int s) {
     const int L = p.seq_lens[s];
     return L < 0 ? 0 : (L > p.cap ? p.cap : L);
@@ -974,27 +989,27 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const int parts = s_parts;
         if (chunk < parts) {
             for (int h = chunk; h < nh; h += parts) {
-                float r[kMaxCluster], w[kMaxCluster], m = kLow, all = 0.f;
+                float2 part[kMaxCluster];
+                float w[kMaxCluster], low[kMaxCluster], m = kLow, all = 0.f;
 #pragma unroll
                 for (int i = 0; i < kMaxCluster; ++i) {
-                    const float2 x = i < parts ? ld_cluster_f2(mapa_shared(sb + HG * D * 4 + h * 8, i)) : make_float2(-INFINITY, 0.f);
-                    r[i] = x.x, w[i] = x.y;
-                    m = fmaxf(m, r[i]);
+                    part[i] = i < parts ? ld_cluster_f2(mapa_shared(sb + HG * D * 4 + h * 8, i)) : make_float2(-INFINITY, 0.f);
+                    m = fmaxf(m, part_top(part[i]));
                 }
 #pragma unroll
                 for (int i = 0; i < kMaxCluster; ++i) {
-                    w[i] *= ex2(r[i] - m);
-                    all += w[i];
+                    w[i] = part_weight(part[i], m, low[i]);
+                    all = fmaf(w[i], low[i], all);
                 }
                 const float inv = all == 0.f ? 0.f : 1.f / all;
 #pragma unroll
-                for (int i = 0; i < kMaxCluster; ++i) w[i] *= inv;  // (before they meet values: a sum may be 2^60 and more)
+                for (int i = 0; i < kMaxCluster; ++i) w[i] *= inv;  // (before they meet values, which may be 2^127)
                 const long long row = static_cast<long long>(own) * p.Hq + h0 + h;
                 for (int d = threadIdx.x; d < D; d += C::THREADS) {
                     float x = 0.f;
 #pragma unroll
                     for (int i = 0; i < kMaxCluster; ++i)
-                        if (i < parts) x = fmaf(w[i], ld_cluster_f1(mapa_shared(sb + (h * D + d) * 4, i)), x);
+                        if (i < parts) x = fmaf(w[i], ld_cluster_f1(mapa_shared(sb + (h * D + d) * 4, i)) * low[i], x);
                     if (p.out_f32)
                         static_cast<float*>(p.out)[row * D + d] = x;
                     else
@@ -1014,8 +1029,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 // Groups of `width` / 4 threads take the partials in turn, kLoad loads in
 // flight each, the first of them asked for before every warp finds the largest
 // reference and the whole softmax sum for itself; then one group adds the groups'
-// results.  The weights are made relative to that sum before they meet values: a
-// partial's sum may be 2^60 and more, and a value 2^127.
+// results.  The weights are made relative to that sum before they meet values.
 //   Many sequences (few partials each): a small CTA a (chunk, query head), which
 // leaves at once where no sequence begins that goes on.
 //   Few sequences: a CTA a (sequence, query head, 32 columns), which finds the
@@ -1063,8 +1077,10 @@ __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params 
     float m = kLow, sum = 0.f;
     for (int i = lane; i <= j.y - c; i += 32) {
         const float2 x = p.part_sum[slot(i)];
-        const float n = fmaxf(m, x.x);
-        sum = fmaf(x.y, ex2(x.x - n), sum * ex2(m - n));
+        const float n = fmaxf(m, part_top(x));
+        float low;
+        const float y = part_weight(x, n, low);
+        sum = fmaf(y, low, sum * ex2(m - n));
         m = n;
     }
     const float top = warp_max(m);
@@ -1077,11 +1093,12 @@ __global__ void __launch_bounds__(kJoin) paged_fp8_combine(const PagedFp8Params 
 #pragma unroll
         for (int k = 0; k < kLoad; ++k) {
             if (i0 + k * groups >= n) break;
-            const float x = w[k].y * ex2(w[k].x - top) * inv;
-            acc.x = fmaf(x, v[k].x, acc.x);
-            acc.y = fmaf(x, v[k].y, acc.y);
-            acc.z = fmaf(x, v[k].z, acc.z);
-            acc.w = fmaf(x, v[k].w, acc.w);
+            float low;
+            const float x = part_weight(w[k], top, low) * inv;
+            acc.x = fmaf(x, v[k].x * low, acc.x);
+            acc.y = fmaf(x, v[k].y * low, acc.y);
+            acc.z = fmaf(x, v[k].z * low, acc.z);
+            acc.w = fmaf(x, v[k].w * low, acc.w);
         }
         i0 += groups * kLoad;
         ask(i0);

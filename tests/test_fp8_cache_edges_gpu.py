@@ -448,3 +448,26 @@ def test_read_and_write_in_a_graph_with_new_contents():
         assert int(status) == 0
         for got, x in zip((k, v), want):
             assert np.array_equal(to_np(got[:bounds[2]]), np.concatenate(x))
+
+
+# ---------------------------------------------------------------- decode: parts of little weight and large values
+@pytest.mark.parametrize("top,size", [(87.5, 40), (160.0, 110)])  # weights of e^(40 - top): 2^-68, 2^-173
+@pytest.mark.parametrize("D,n,max_len", [(64, 4096, 4096), (128, 4096, 1 << 20), (64, 200000, 200000), (256, 4096, 4096)])
+def test_decode_joins_of_parts_with_little_weight_and_large_values(D, n, max_len, top, size):
+    """The first block takes nearly all the weight; the last one, whose scores
+    lie e^40 above those before it (less than a reference is moved for), has
+    values large enough to matter all the same."""
+    g = torch.Generator().manual_seed(n)
+    key = torch.randn(n, 1, D, generator=g)
+    block = torch.arange(n) // 128
+    key[:, 0, 0] = math.sqrt(D) * (top * (block == 0) + 40.0 * (block == block[-1]))
+    value = torch.randn(n, 1, D, generator=g)
+    value[block < block[-1]] *= 2.0 ** (-30 if size == 40 else -60)
+    value[block == block[-1]] *= 2.0 ** size
+    c = written(key, value, D)
+    q = torch.zeros(1, 2, D, dtype=torch.bfloat16)
+    q[:, :, 0], q[0, 1, 1] = 1.0, 0.25
+    for out_dtype in (torch.float32, torch.bfloat16):
+        out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
+        check_columns(c, q, out)
+        check_decode(c, q, out, lse)
