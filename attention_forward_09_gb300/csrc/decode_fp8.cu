@@ -29,11 +29,12 @@
 // that nothing is lost beside scores of up to 2^23; above, M's own step passes 1.
 // (Plain sums u + v_t and an lse a partial take 3% less time at D = 64 with eight
 // heads or short sequences, 1 to 3% elsewhere, and are 2^-11 off at scores of 2^13.)
-// What bounds it now (one GB300, contexts of 16384, 64 sequences, bf16 output,
-// of 6787 GB/s copied): D = 128, 4 heads a KV head 7.03 TB/s, 8 heads 6.93,
-// D = 256 7.1, D = 192 6.6, D = 96 6.3 (a third of its shared memory is padding),
-// D = 64 6.5 with up to 4 heads, 5.1 with 8 (the softmax warps); above 8 heads a
-// KV head's rows go to several CTAs, 5.3 TB/s at 16 (the L2's reads).
+// What bounds it now (one GB300, contexts of 16384, 64 sequences, 8 KV heads, of
+// 6787 GB/s copied; 4 and 8 heads a KV head, either output): D = 128 7.0 and 6.8
+// TB/s, D = 256 7.1 and 7.0, D = 192 6.6 and 6.4, D = 96 6.1 and 6.1 (a quarter of
+// its shared memory is padding), D = 64 6.4 and 4.7 (the softmax warps); above 8
+// heads a KV head's rows go to several CTAs, which read them from the L2: at 16
+// D = 64 2.4, D = 128 4.7, D = 256 5.0.
 //
 // Work split: the context blocks of all sequences, in order, are cut into C
 // equal runs ("chunks"), and CTA (c, h) takes chunk c of KV head (or head
@@ -1191,6 +1192,8 @@ PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_le
     pl.head_cols = 2;  // heads are worked in pairs
     while (pl.head_cols < pl.heads_per_sub) pl.head_cols *= 2;
     pl.n_hgroups = static_cast<long long>(Hkv) * pl.subs;
+    // (152 SMs: the size of the workspace is asked for without a device.  On a part
+    // with fewer the CTAs of a wave would take turns: right, but slower.)
     // Few and short sequences: a cluster of up to 8 CTAs a (sequence, head), each
     // with at most four blocks, all of them running at once; the parts are
     // joined on chip, in the same launch and without a workspace.  (D = 128, 8 KV

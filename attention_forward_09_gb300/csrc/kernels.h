@@ -220,9 +220,10 @@ struct PagedFp8Plan {
 PagedFp8Plan paged_fp8_plan(int num_seqs, int Hq, int Hkv, int D, int max_seq_len);
 // Bytes of a row in one TMA box of the decode, and the box's swizzle span: 64
 // where that divides D and 128 does not, so that shared memory holds no
-// padding and more of the context is in flight (contexts of 16384, D = 192:
-// 6.2 -> 6.8 TB/s, D = 64: 5.1 -> 5.4).  At D = 96 boxes of 32 bytes are slower
-// than padding to 128 (5.1 and 6.1 TB/s): a box's rows cost by number.
+// padding and more of the context is in flight (64 contexts of 16384, 8 KV heads,
+// D = 192, 4 heads a KV head: 6.26 TB/s in boxes of 128 bytes, 6.63 in boxes of
+// 64).  At D = 96 boxes of 32 bytes are slower than padding to 128 (5.1 and 6.1
+// TB/s): a box's rows cost by number.
 constexpr int paged_fp8_box(int D) { return D % 128 != 0 && D % 64 == 0 ? 64 : 128; }
 // CTAs an SM holds of the decode (by shared memory and registers), for head
 // size D and `heads` query heads a CTA.
