@@ -467,7 +467,8 @@ def attn_kv_cache_read_fp8(kv_cache, kv_scales, block_table, cu_seqlens_k, total
     sequence s, read from the 8-bit cache through block_table [S, max_blocks]
     (int32), as packed bf16 rows (k, v), each [total_tokens, Hkv, D]: what
     attn_fwd_varlen takes.  total_tokens (host int) is at least
-    cu_seqlens_k[S]; rows past that are left as they were."""
+    cu_seqlens_k[S]; rows past that are left as they were, and so are those of a
+    sequence whose boundaries make no sense (DEV_BAD_SEQLEN)."""
     code, nb, bs, hkv, d = _fp8_cache(kv_cache, kv_scales)
     _index_table("block_table", block_table, 2)
     _index_table("cu_seqlens_k", cu_seqlens_k, 1)

@@ -413,10 +413,11 @@ gbattn_status attn_fwd_paged_noalloc(const void* q, const void* kv_cache, int nu
  * Values are exact (a code has at most 4 significant bits) unless below bf16's
  * smallest normal number.  A block_table entry outside [0, num_blocks) sets
  * GBATTN_DEV_BAD_INDEX and its tokens' rows are zeros.  A sequence whose
- * cu_seqlens_k decrease, run past Tk or past max_blocks_per_seq blocks, or
- * c[0] other than 0, sets GBATTN_DEV_BAD_SEQLEN; that sequence's rows are left
- * as they were, and every other one's are read (a row in the range of two
- * sequences, which takes boundaries that decrease, holds either's).
+ * cu_seqlens_k decrease, are negative, run past Tk or past max_blocks_per_seq
+ * blocks sets GBATTN_DEV_BAD_SEQLEN and its rows are left as they were; every
+ * other one's are read (a row in the range of two sequences, which takes
+ * boundaries that decrease, holds either's).  c[0] above 0 sets it too; no
+ * sequence is refused for that.
  *
  * attn_fwd_paged_fp8 -- attn_fwd_paged over the 8-bit cache: the softmax of
  * the values that the codes stand for, with these roundings beside fp32's.
@@ -441,8 +442,9 @@ gbattn_status attn_fwd_paged_noalloc(const void* q, const void* kv_cache, int nu
  *             initialisation; calls that can overlap need one each
  * The other arguments, the treatment of unused slots and table entries, of
  * empty sequences, bad blocks (their tokens are skipped) and bad lengths, and
- * the errors are those of attn_fwd_paged.  block_size must be 128, and Hq at most 65535.  A query
- * value that is NaN or infinite makes its head's result NaN.
+ * the errors are those of attn_fwd_paged.  block_size must be 128, and Hq at
+ * most 65535.  A query value that is NaN or infinite makes its head's result
+ * NaN.
  *
  * attn_fwd_paged_fp8_workspace_size -- pure host arithmetic, as
  * attn_fwd_paged_workspace_size.
