@@ -471,3 +471,74 @@ def test_decode_joins_of_parts_with_little_weight_and_large_values(D, n, max_len
         out, lse = run_decode(c, q, max_len=max_len, out_dtype=out_dtype)
         check_columns(c, q, out)
         check_decode(c, q, out, lse)
+
+
+# ---------------------------------------------------------------- sizes and captures
+def test_many_sequences_that_share_blocks():
+    """70000 sequences, empty ones among them, over four blocks that they share."""
+    S, hkv, hq, D = 70000, 1, 2, 64
+    g = torch.Generator().manual_seed(1)
+    c = Ctx([512], hkv, D, seed=30, extra=0)
+    lens = torch.randint(0, 4, (S,), generator=g, dtype=torch.int32) * torch.randint(0, 60, (S,), generator=g, dtype=torch.int32)
+    c.table = torch.randint(0, 4, (S, 2), generator=g, dtype=torch.int32)
+    cache, scales, table = c.on_gpu()
+    q = bf16(S, hq, D, seed=31)
+    status = status_word()
+    out, lse = gb.attn_fwd_paged_fp8(q.to(dev()), cache, scales, table, lens.to(dev()), 177, lse=True, dev_status=status)
+    cu = torch.cat([torch.zeros(1, dtype=torch.int32), lens.cumsum(0).to(torch.int32)])
+    k, v = gb.attn_kv_cache_read_fp8(cache, scales, table, cu.to(dev()), int(cu[-1]), dev_status=status)
+    assert int(status) == 0
+    keep = sorted({0, 1, 3333, 35000, S - 1} | set(torch.randint(0, S, (40,), generator=g).tolist()))
+    gathered = oracle.paged_gather(c.values(), c.table[keep], lens[keep].tolist())
+    for i, s in enumerate(keep):
+        rows = slice(int(cu[s]), int(cu[s + 1]))
+        assert np.array_equal(to_np(k[rows]), gathered[0][i]) and np.array_equal(to_np(v[rows]), gathered[1][i])
+    empty = lens == 0
+    assert not out.cpu()[empty].any() and torch.isneginf(lse.cpu()[empty]).all() and torch.isfinite(lse.cpu()[~empty]).all()
+    c.table, c.lens = c.table[keep], lens[keep].tolist()
+    check_decode(c, q[keep], out[keep], lse[keep])
+
+
+@pytest.mark.parametrize("hq,hkv", [(65535, 1), (65535, 4369)])
+def test_decode_of_the_most_heads(hq, hkv):
+    c = Ctx([130], hkv, 64, seed=32, extra=0)
+    q = bf16(1, hq, 64, seed=33)
+    for max_len in (130, 1 << 20):
+        out, lse = run_decode(c, q, max_len=max_len)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        part = Ctx([130], hkv, 64, seed=32, extra=0)
+        g = hq // hkv
+        for h in (0, hkv // 2, hkv - 1):  # the oracle takes some KV heads
+            part.codes, part.scales = c.codes[:, :, :, h:h + 1], c.scales[:, :, h:h + 1]
+            rows = [h * g + i for i in sorted({0, 1, 7, 8, g // 2, g - 1})]
+            check_decode(part, q[:, rows], out[:, rows], lse[:, rows])
+
+
+def test_prompt_form_in_a_graph_with_new_contents():
+    """Captured once; replayed with other contexts, queries and boundaries."""
+    hq, hkv, D, T, Tq = 4, 2, 128, 700, 90
+    c = Ctx([600, 600], hkv, D, seed=34)
+    cache, scales, table = c.on_gpu()
+    q, cu_q, cu_k = bf16(Tq, hq, D, seed=35).to(dev()), ints([0, 40, 90]), ints([0, 300, 700])
+    status = status_word()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out, lse = gb.attn_fwd_paged_prefill_fp8(q, cache, scales, table, cu_q, cu_k, T, 90, 1000, lse=True, dev_status=status)
+    for seed, lens, q_lens in ((40, [300, 400], [40, 50]), (41, [600, 5], [85, 5]), (42, [1, 0], [1, 0])):
+        fresh = Ctx([600, 600], hkv, D, seed=seed)
+        cache.view(torch.uint8).copy_(fresh.codes)
+        scales.copy_(fresh.scales)
+        table.copy_(fresh.table)
+        x = bf16(Tq, hq, D, seed=seed + 10)
+        q.copy_(x)
+        cu_q.copy_(ints(np.cumsum([0] + q_lens)))
+        cu_k.copy_(ints(np.cumsum([0] + lens)))
+        out.fill_(77.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        n = sum(q_lens)
+        ref, ref_lse = oracle.attention_paged_prefill(x[:n], fresh.values(), fresh.table, lens, np.cumsum([0] + q_lens), 1 / math.sqrt(D), True)
+        assert int(status) == 0
+        assert np.abs(to_np(out[:n]) - ref).max() <= 1e-2 and np.abs(to_np(lse[:, :n]) - ref_lse).max() <= 1e-3  # the prefill kernels' bounds
+        assert (out[n:] == 77).all()
