@@ -18,6 +18,8 @@ Entry points (same names as the C ABI):
     attn_vsa_block_map, attn_fwd_vsa
     attn_kv_cache_write_fp8, attn_kv_cache_read_fp8, attn_fwd_paged_fp8,
     attn_fwd_paged_fp8_workspace_size: the 8-bit paged KV cache
+    attn_bwd_dense, attn_bwd_padded, attn_bwd_varlen, attn_bwd_workspace_size: gradients
+    (include/gbattn_bwd.h)
 Compositions of those calls: attn_fwd_masked (padding mask), attn_vsa (block-sparse
 video attention, with VsaPlan holding one geometry's layout on the device),
 attn_fwd_paged_prefill_fp8 (several new tokens a sequence over the 8-bit cache).
@@ -75,6 +77,12 @@ SIGNATURES = {
     "attn_fwd_paged_fp8": (_I, [_P, _L, _P, _P, _I, _I, _I, _P, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P, _I, _P, _P, _Z,
                                 _P, _P]),
     "attn_fwd_vsa": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P, _L, _I, _I, _I, _F, _P, _I, _P, _P, _P]),
+    "attn_bwd_workspace_size": (_Z, [_I, _I, _I]),
+    "attn_bwd_dense": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, _P, _Z, _P, _P]),
+    "attn_bwd_padded": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, _P, _Z,
+                             _P, _P]),
+    "attn_bwd_varlen": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P,
+                             _P, _Z, _P, _P]),
 }
 
 _lib = None
@@ -859,3 +867,129 @@ def attn_vsa(q, k, v, plan: VsaPlan, topk=64, softmax_scale=None, lse=False, out
     return attn_fwd_vsa(qt, kt, vt, kv_list, kv_num, plan.num_blocks, plan.num_prefix_blocks, topk,
                         out_index=plan.tile_index, out_rows=S, softmax_scale=softmax_scale,
                         lse=True if lse else None, out_dtype=out_dtype, dev_status=dev_status, stream=stream)
+
+
+# ---- gradients (gbattn_bwd.h).  These calls run on their tensors' device,
+# whichever one is current, and allocate what they return (and a workspace not
+# given) on the stream they run on.
+def _run_on(name, dev, stream, args):
+    """One C call on device number dev and stream (None: the device's current one)."""
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"stream must be of cuda:{dev}, where the tensors are")
+    fn = getattr(_lib or load_library(), name)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st != 0:
+        raise GbattnError(name, st)
+
+
+def _tensor(name, t, dev, dtype, shape):
+    """Raise ValueError unless t is a contiguous tensor of this type and shape on CUDA device number dev."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, with q")
+
+
+def attn_bwd_workspace_size(num_docs, Tq, Hq) -> int:
+    """Bytes of workspace a backward call needs for num_docs documents (or batch entries) of Tq query rows in all."""
+    return int((_lib or load_library()).attn_bwd_workspace_size(_host_int("num_docs", num_docs), _host_int("Tq", Tq), Hq))
+
+
+def _bwd(name, q, k, v, out, lse, dout, dlse, index, sizes, docs, heads, lse_shape, softmax_scale, causal, dq, dk, dv,
+         workspace, dev_status, stream):
+    """The part the backward calls share: checks, allocation and the C call.  index: (name, tensor, entries) of the
+    int32 tensors the call takes; sizes: its sizes up to D; docs: documents or batch entries."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("the gradients take CUDA tensors")
+    Hq, Hkv, D = heads
+    bf16 = torch.bfloat16
+    for n, t, like in (("q", q, q), ("k", k, k), ("v", v, k), ("dout", dout, q)):
+        _tensor(n, t, dev, bf16, like.shape)
+    _tensor("out", out, dev, bf16 if out.dtype == bf16 else torch.float32, q.shape)
+    _tensor("lse", lse, dev, torch.float32, lse_shape)
+    if dlse is not None:
+        _tensor("dlse", dlse, dev, torch.float32, lse_shape)
+    for n, t, entries in index:
+        if t is not None:
+            _tensor(n, t, dev, torch.int32, (entries,))
+    status = _status_ptr(dev_status)
+    if dev_status is not None and dev_status.get_device() != dev:
+        raise ValueError(f"dev_status must be on cuda:{dev}, with q")
+    grads = []
+    for n, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
+        if t is None:
+            t = _empty_on(stream, q, like.shape, bf16)
+        else:
+            _tensor(n, t, dev, bf16, like.shape)
+        grads.append(t)
+    if workspace is None:
+        ws_bytes = attn_bwd_workspace_size(docs, q.numel() // (Hq * D) if Hq * D else 0, Hq)
+        workspace = _empty_on(stream, q, (ws_bytes,), torch.uint8)
+    elif workspace.is_contiguous() and workspace.get_device() == dev:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    else:
+        raise ValueError(f"workspace must be contiguous and on cuda:{dev}, with q")
+    scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
+    _run_on(name, dev, stream,
+            (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _out_code(out.dtype), lse.data_ptr(),
+             dout.data_ptr(), None if dlse is None else dlse.data_ptr(),
+             *(None if t is None else t.data_ptr() for _, t, _ in index), *sizes, Hq, Hkv, D, scale, 1 if causal else 0,
+             *(t.data_ptr() for t in grads), workspace.data_ptr(), ws_bytes, status))
+    return tuple(grads)
+
+
+def _bwd_batch(q, k):
+    """(B, Sq, Sk, Hq, Hkv, D) of a batch's q and k."""
+    if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
+        raise ValueError("q must be [B, Sq, Hq, D], k and v [B, Sk, Hkv, D]")
+    B, Sq, Hq, D = q.shape
+    return B, Sq, k.shape[1], Hq, k.shape[2], D
+
+
+def attn_bwd_dense(q, k, v, out, lse, dout, softmax_scale=None, causal=False, dlse=None, dq=None, dk=None, dv=None,
+                   workspace=None, dev_status=None, stream=None):
+    """Gradients of attn_fwd_dense from what it took and returned: q, dout
+    [B, Sq, Hq, D] and k, v [B, Sk, Hkv, D] bf16, out (bf16 or fp32) and lse
+    [B, Hq, Sq] as it returned them, dout the gradient of out and dlse that of
+    lse (None: lse is not used further on).  Returns (dq, dk, dv) in bf16;
+    tensors given for them are written.  A workspace of at least
+    ``attn_bwd_workspace_size(B, B * Sq, Hq)`` bytes may be passed (it is
+    allocated here otherwise); calls that can overlap need one each."""
+    B, Sq, Sk, Hq, Hkv, D = _bwd_batch(q, k)
+    return _bwd("attn_bwd_dense", q, k, v, out, lse, dout, dlse, (), (B, Sq, Sk), B, (Hq, Hkv, D), (B, Hq, Sq),
+                softmax_scale, causal, dq, dk, dv, workspace, dev_status, stream)
+
+
+def attn_bwd_padded(q, k, v, out, lse, dout, lens_q=None, lens_k=None, softmax_scale=None, causal=False, dlse=None,
+                    dq=None, dk=None, dv=None, workspace=None, dev_status=None, stream=None):
+    """Gradients of attn_fwd_padded: as attn_bwd_dense, entry b using its first
+    lens_q[b] query rows and lens_k[b] keys (int32 [B], or None for all rows).
+    Rows past them get zeros and never reach a result, whatever they hold."""
+    B, Sq, Sk, Hq, Hkv, D = _bwd_batch(q, k)
+    return _bwd("attn_bwd_padded", q, k, v, out, lse, dout, dlse, (("lens_q", lens_q, B), ("lens_k", lens_k, B)),
+                (B, Sq, Sk), B, (Hq, Hkv, D), (B, Hq, Sq), softmax_scale, causal, dq, dk, dv, workspace, dev_status, stream)
+
+
+def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale=None,
+                    causal=False, dlse=None, dq=None, dk=None, dv=None, workspace=None, dev_status=None, stream=None):
+    """Gradients of attn_fwd_varlen: q, out, dout [Tq, Hq, D], k, v [Tk, Hkv,
+    D], lse [Hq, Tq], cu_seqlens int32 [N + 1], max_seqlen_q/k host ints.
+    Returns (dq, dk, dv); rows that belong to no document are left as they
+    were.  Workspace: ``attn_bwd_workspace_size(N, Tq, Hq)`` bytes."""
+    if q.dim() != 3 or k.dim() != 3 or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [Tq, Hq, D], k and v [Tk, Hkv, D]")
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    N = cu_seqlens_q.numel() - 1
+    if N < 0:
+        raise ValueError("cu_seqlens_q must have a boundary more than there are documents")
+    return _bwd("attn_bwd_varlen", q, k, v, out, lse, dout, dlse,
+                (("cu_seqlens_q", cu_seqlens_q, N + 1), ("cu_seqlens_k", cu_seqlens_k, N + 1)),
+                (N, Tq, Tk, _host_int("max_seqlen_q", max_seqlen_q), _host_int("max_seqlen_k", max_seqlen_k)), N,
+                (Hq, Hkv, D), (Hq, Tq), softmax_scale, causal, dq, dk, dv, workspace, dev_status, stream)

@@ -2,6 +2,7 @@
 // TMA tensor-map encoding and kernel launches.  No allocation, no
 // synchronisation; every launch goes to the caller's stream.
 #include "../../include/gbattn.h"
+#include "../../include/gbattn_bwd.h"
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -147,7 +148,69 @@ gbattn_status check_fp8_cache(int num_blocks, int block_size, int Hkv, int D, gb
     return GBATTN_OK;
 }
 
-// 1: the prefill and 8-bit decode kernels give up every pipeline wait (attn_set_wait_give_up).
+// The sections of the backward pass's workspace, each a multiple of 256 bytes.
+size_t bwd_stat_bytes(long long Tq, int num_docs, int Hq) {
+    return ((static_cast<size_t>(gbattn::bwd_stat_stride(Tq, num_docs)) * Hq * 4) + 255) & ~size_t(255);
+}
+
+// What the entries of the backward pass have in common.  Sizes are validated
+// before anything is read; `p` comes with the row counts, bounds and layouts.
+gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
+                      const float* lse, const void* dout, const float* dlse, int D, float scale, int causal, void* dq,
+                      void* dk, void* dv, void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                      gbattn::BwdParams& p, cudaStream_t st) {
+    const bool rows = p.Tq > 0 && p.num_docs > 0, keys = p.Tk > 0 && p.num_docs > 0;
+    if (p.Hq <= 0 || p.Hkv <= 0 || p.Hq % p.Hkv != 0 || !scale_ok(scale)) return GBATTN_ERR_INVALID_ARG;
+    if (rows && (!q || !out || !lse || !dout || !dq)) return GBATTN_ERR_INVALID_ARG;
+    if (keys && (!k || !v || !dk || !dv)) return GBATTN_ERR_INVALID_ARG;
+    if (!head_size_ok(D)) return GBATTN_ERR_UNSUPPORTED;
+    if (out_dtype != GBATTN_OUT_BF16 && out_dtype != GBATTN_OUT_F32) return GBATTN_ERR_UNSUPPORTED;
+    for (const void* x : {q, k, v, out, dout, static_cast<const void*>(dq), static_cast<const void*>(dk), static_cast<const void*>(dv)})
+        if (!aligned16(x)) return GBATTN_ERR_ALIGNMENT;
+    p.tiles_q = static_cast<int>((static_cast<long long>(p.max_q) + 127) / 128);
+    p.tiles_k = static_cast<int>((static_cast<long long>(p.max_k) + 127) / 128);
+    // grids are one-dimensional, an item a block
+    constexpr long long kMost = 0x7fffffffLL;
+    const long long qh = static_cast<long long>(p.tiles_q) * p.num_docs, kh = static_cast<long long>(p.tiles_k) * p.num_docs;
+    if (qh > kMost / p.Hq || kh > kMost / p.Hkv) return GBATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(p.max_q) > kMost / p.Hq * 8) return GBATTN_ERR_UNSUPPORTED;
+    if (!rows && !keys) return GBATTN_OK;
+    const size_t stat = bwd_stat_bytes(p.Tq, p.num_docs, p.Hq);
+    if (!workspace || workspace_bytes < 2 * stat || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return GBATTN_ERR_WORKSPACE;
+    DeviceInfo di;
+    gbattn_status s = device_info(&di);
+    if (s != GBATTN_OK) return s;
+    p.give_up = gbattn::wait_give_up();
+    p.out = out;
+    p.dout = dout;
+    p.lse = lse;
+    p.dlse = dlse;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.neg_lse2 = static_cast<float*>(workspace);
+    p.neg_delta = reinterpret_cast<float*>(static_cast<char*>(workspace) + stat);
+    p.stat_stride = gbattn::bwd_stat_stride(p.Tq, p.num_docs);
+    p.status = dev_status;
+    p.group = p.Hq / p.Hkv;
+    p.scale = scale;
+    p.scale_log2 = scale * kLog2e;
+    p.causal = causal ? 1 : 0;
+    p.out_f32 = out_dtype == GBATTN_OUT_F32;
+    // Without rows (or keys) nothing of that side is ever loaded; its maps
+    // then view the other side's tensor so that they are well-formed.
+    CUtensorMap tq, tg, tk, tv;
+    const int box = gbattn::bwd_box_rows(D);
+    const long long rq = rows ? p.Tq : p.Tk, rk = keys ? p.Tk : p.Tq;
+    const int hq = rows ? p.Hq : p.Hkv, hk = keys ? p.Hkv : p.Hq;
+    if (!encode_rows_heads_d(&tq, rows ? q : k, rq, hq, D, box) || !encode_rows_heads_d(&tg, rows ? dout : v, rq, hq, D, box) ||
+        !encode_rows_heads_d(&tk, keys ? k : q, rk, hk, D, box) || !encode_rows_heads_d(&tv, keys ? v : dout, rk, hk, D, box))
+        return GBATTN_ERR_CUDA;
+    return gbattn::launch_bwd(D, tq, tg, tk, tv, p, st) == cudaSuccess ? GBATTN_OK : GBATTN_ERR_CUDA;
+}
+
+// 1: the prefill, backward and 8-bit decode kernels give up every pipeline wait (attn_set_wait_give_up).
 std::atomic<int> g_give_up{0};
 
 }  // namespace
@@ -829,6 +892,69 @@ gbattn_status attn_fwd_vsa(const void* q_tiled, const void* k_tiled, const void*
     return gbattn::launch_vsa_fwd(D, tq, tk, tv, p, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GBATTN_OK
                : GBATTN_ERR_CUDA;
+}
+
+size_t attn_bwd_workspace_size(int num_docs, int Tq, int Hq) {
+    if (num_docs < 0 || num_docs > 65535 || Tq < 0 || Hq <= 0) return 0;
+    return 2 * bwd_stat_bytes(Tq, num_docs, Hq);
+}
+
+gbattn_status attn_bwd_padded(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
+                              const float* lse, const void* dout, const float* dlse, const int32_t* lens_q,
+                              const int32_t* lens_k, int B, int Sq, int Sk, int Hq, int Hkv, int D, float softmax_scale,
+                              int causal, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                              uint32_t* dev_status, void* stream) {
+    if (B < 0 || Sq < 0 || Sk < 0) return GBATTN_ERR_INVALID_ARG;
+    if (B > 65535 || static_cast<long long>(B) * Sq > 0x7fffffffLL || static_cast<long long>(B) * Sk > 0x7fffffffLL)
+        return GBATTN_ERR_UNSUPPORTED;  // row counts are 32-bit on the device
+    gbattn::BwdParams p{};
+    p.lens_q = lens_q;
+    p.lens_k = lens_k;
+    p.num_docs = B;
+    p.Tq = B * Sq;
+    p.Tk = B * Sk;
+    p.max_q = Sq;
+    p.max_k = Sk;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.lse_bstride = static_cast<long long>(Hq) * Sq;
+    p.lse_hstride = Sq;
+    return run_bwd(q, k, v, out, out_dtype, lse, dout, dlse, D, softmax_scale, causal, dq, dk, dv, workspace,
+                   workspace_bytes, dev_status, p, static_cast<cudaStream_t>(stream));
+}
+
+gbattn_status attn_bwd_dense(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
+                             const float* lse, const void* dout, const float* dlse, int B, int Sq, int Sk, int Hq,
+                             int Hkv, int D, float softmax_scale, int causal, void* dq, void* dk, void* dv,
+                             void* workspace, size_t workspace_bytes, uint32_t* dev_status, void* stream) {
+    return attn_bwd_padded(q, k, v, out, out_dtype, lse, dout, dlse, nullptr, nullptr, B, Sq, Sk, Hq, Hkv, D,
+                           softmax_scale, causal, dq, dk, dv, workspace, workspace_bytes, dev_status, stream);
+}
+
+gbattn_status attn_bwd_varlen(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
+                              const float* lse, const void* dout, const float* dlse, const int32_t* cu_seqlens_q,
+                              const int32_t* cu_seqlens_k, int num_docs, int Tq, int Tk, int max_seqlen_q,
+                              int max_seqlen_k, int Hq, int Hkv, int D, float softmax_scale, int causal, void* dq,
+                              void* dk, void* dv, void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                              void* stream) {
+    if (num_docs < 0 || Tq < 0 || Tk < 0 || max_seqlen_q < 0 || max_seqlen_k < 0) return GBATTN_ERR_INVALID_ARG;
+    if (max_seqlen_q > Tq || max_seqlen_k > Tk) return GBATTN_ERR_INVALID_ARG;
+    if (num_docs > 0 && (!cu_seqlens_q || !cu_seqlens_k)) return GBATTN_ERR_INVALID_ARG;
+    if (num_docs > 65535) return GBATTN_ERR_UNSUPPORTED;
+    gbattn::BwdParams p{};
+    p.cu_q = cu_seqlens_q;
+    p.cu_k = cu_seqlens_k;
+    p.num_docs = num_docs;
+    p.Tq = Tq;
+    p.Tk = Tk;
+    p.max_q = max_seqlen_q;
+    p.max_k = max_seqlen_k;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.lse_hstride = Tq;
+    p.lse_row_global = 1;
+    return run_bwd(q, k, v, out, out_dtype, lse, dout, dlse, D, softmax_scale, causal, dq, dk, dv, workspace,
+                   workspace_bytes, dev_status, p, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

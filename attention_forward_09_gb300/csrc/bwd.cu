@@ -1,0 +1,711 @@
+// bwd.cu -- gradients of the fused attention for sm_103a (dense, padded and
+// packed documents), from what the forward pass returned.
+//
+// With s_ij = scale q_i.k_j over the visible pairs, the probabilities are
+// recomputed from the row's log-sum-exp and never stored:
+//   p_ij    = exp(s_ij - lse_i)
+//   delta_i = dout_i . out_i - dlse_i
+//   ds_ij   = p_ij (dout_i.v_j - delta_i)
+//   dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
+//
+// Three kernels:
+//   attn_bwd_stat_sm103a   -lse log2(e) and -delta of every query row and
+//     head (fp32), one pass over out and dout, HBM-bound;
+//   attn_bwd_sm103a, keys resident: a tile of 128 keys of one KV head stays
+//     in shared memory while the queries of every head that shares it stream
+//     by; S^T = K Q^T and dP^T = V dO^T go to TMEM, two warpgroups turn them
+//     into P^T and dS^T (bf16, written over them), which are the A operands
+//     of dV += P^T dO and dK += dS^T Q straight from TMEM;
+//   attn_bwd_sm103a, queries resident: the same pipeline with the roles
+//     exchanged: S = Q K^T, dP = dO V^T, dQ += dS K.
+// A gradient row is summed by one CTA in one order, the heads of a group
+// included, so results do not depend on timing: there are no atomics.  The
+// price is that S and dP are formed twice, seven products for the five that
+// one pass with atomics on dQ would need.
+//
+// P and dS are rounded to bf16 as operands of the second products, as P is in
+// the forward kernels (at most 2^-8 of each term, independent of one another);
+// lse, delta, P in ds = p (dp - delta) and every sum are fp32.
+//
+// A resident tile is 128 rows (TMEM lanes); a streamed tile is BN = 128 rows,
+// 64 for D > 128 where the accumulators need the TMEM columns.  At D = 256 dV
+// and dK do not fit beside each other (2 x 256 columns): they are two
+// launches of the keys-resident kernel, one accumulator each.
+//
+// Shared-memory layout and descriptors are those of the forward kernels: 64
+// column chunks of [rows x 128 B], 128-byte swizzle; a streamed tile is read
+// K-major by S / dP and MN-major by the second products.
+#include <math.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace gbattn {
+
+namespace {
+
+// What a launch of attn_bwd_sm103a sums.
+enum BwdMode {
+    kBwdKV,  // keys resident: dV and dK
+    kBwdV,   // keys resident: dV alone
+    kBwdK,   // keys resident: dK alone
+    kBwdQ    // queries resident: dQ
+};
+
+template <int D_, int MODE_>
+struct BwdCfg {
+    static constexpr int D = D_, MODE = MODE_;
+    static constexpr int BM = 128;                    // resident rows
+    static constexpr int BN = D <= 128 ? 128 : 64;    // streamed rows
+    static constexpr bool KEYS = MODE != kBwdQ;       // keys resident, queries streamed
+    static constexpr bool HAS_P = MODE == kBwdKV || MODE == kBwdV;  // sums dV
+    static constexpr bool HAS_DS = MODE != kBwdV;     // needs dP; sums dK or dQ
+    static constexpr int ACCS = MODE == kBwdKV ? 2 : 1;
+    static constexpr int NCH = (D + 63) / 64;         // 64-column chunks
+    static constexpr int RES = HAS_DS ? 2 : 1;        // resident tiles: K (and V), or Q and dO
+    static constexpr int R_BYTES = NCH * BM * 128;
+    static constexpr int C_BYTES = NCH * BN * 128;    // one streamed tile
+    static constexpr int STAT_BYTES = KEYS ? 2 * BN * 4 : 0;  // -lse log2 e, -delta of a streamed tile's rows
+    // TMEM: S buffers, dP, accumulators.  A second S buffer where it fits lets
+    // the next scores be formed before the current ones are used up.
+    static constexpr int SB = (2 + (HAS_DS ? 1 : 0)) * BN + ACCS * D <= 512 ? 2 : 1;
+    static constexpr int T_S = 0;
+    static constexpr int T_DP = SB * BN;
+    static constexpr int T_ACC = T_DP + (HAS_DS ? BN : 0);
+    static constexpr int BARS_FIXED = 10;
+    static constexpr int ROOM = 232448 - 1024 - RES * R_BYTES - 16 - BARS_FIXED * 8;
+    static constexpr int FIT = ROOM / (C_BYTES + STAT_BYTES + 16);
+    static constexpr int SLOTS = FIT < 6 ? FIT : 6;
+    static constexpr int NUM_BARS = BARS_FIXED + 2 * SLOTS;
+    static constexpr int SMEM_BYTES = 1024 + RES * R_BYTES + SLOTS * (C_BYTES + STAT_BYTES) + NUM_BARS * 8 + 16;
+    static constexpr int REG_MATH = 208, REG_OTHER = 88;  // setmaxnreg split of 384 x 168
+    static_assert(T_ACC + ACCS * D <= 512, "TMEM budget");
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(SLOTS >= 3, "C1 of the next step is needed before C1 and C2 of this one are released");
+    static_assert(SMEM_BYTES > 116 * 1024, "one CTA an SM: it takes all TMEM columns");
+    static_assert(SB == 2 || HAS_P, "one S buffer is freed by the P it becomes");
+    static_assert(2 * 128 * REG_MATH + 128 * REG_OTHER <= 384 * 168, "register split");
+};
+
+// One document's (or batch entry's) rows.
+struct BwdDoc {
+    int q_start, k_start;  // first rows in the tensors
+    int Lq, Lk;            // rows used
+    int Lq_all, Lk_all;    // rows to be written (padding included)
+    bool bad;
+};
+
+__device__ __forceinline__ BwdDoc bwd_doc(const BwdParams& p, int doc, bool report) {
+    BwdDoc d;
+    d.bad = false;
+    if (p.cu_q) {
+        d.q_start = p.cu_q[doc];
+        d.k_start = p.cu_k[doc];
+        const int q_end = p.cu_q[doc + 1], k_end = p.cu_k[doc + 1];
+        d.bad = d.q_start < 0 || q_end < d.q_start || q_end > p.Tq || d.k_start < 0 || k_end < d.k_start ||
+                k_end > p.Tk || q_end - d.q_start > p.max_q || k_end - d.k_start > p.max_k;
+        if (d.bad) {
+            if (report && p.status) atomicOr(p.status, kDevBadSeqlen);
+            return d;
+        }
+        d.Lq = d.Lq_all = q_end - d.q_start;
+        d.Lk = d.Lk_all = k_end - d.k_start;
+    } else {
+        d.q_start = doc * p.max_q;
+        d.k_start = doc * p.max_k;
+        d.Lq = d.Lq_all = p.max_q;
+        d.Lk = d.Lk_all = p.max_k;
+        if (p.lens_q) {
+            const int n = p.lens_q[doc];
+            if ((n < 0 || n > p.max_q) && report && p.status) atomicOr(p.status, kDevBadSeqlen);
+            d.Lq = min(max(n, 0), p.max_q);
+        }
+        if (p.lens_k) {
+            const int n = p.lens_k[doc];
+            if ((n < 0 || n > p.max_k) && report && p.status) atomicOr(p.status, kDevBadSeqlen);
+            d.Lk = min(max(n, 0), p.max_k);
+        }
+    }
+    return d;
+}
+
+// Where a document's row statistics begin within a head's array: multiples of
+// four floats (a bulk copy starts on 16 bytes), never overlapping: the starts
+// of documents n and n + 1 are at least len + 1 apart.
+__device__ __forceinline__ long long bwd_stat_base(int q_start, int doc) {
+    return (static_cast<long long>(q_start) + 4ll * doc + 3) & ~3ll;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+}  // namespace
+
+// ------------------------------------------------------------- row statistics
+// LANES lanes a (row, head); reads 16 bytes of dout and 16 or 32 of out a lane.
+template <int D, bool F32>
+__global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p) {
+    constexpr int LANES = D <= 64 ? 8 : (D <= 128 ? 16 : 32), PER_CTA = 256 / LANES;
+    const int doc = blockIdx.y;
+    const BwdDoc d = bwd_doc(p, doc, threadIdx.x == 0 && blockIdx.x == 0);
+    if (d.bad) return;
+    const int sub = threadIdx.x % LANES;
+    const long long pair = static_cast<long long>(blockIdx.x) * PER_CTA + threadIdx.x / LANES;
+    const int i = static_cast<int>(pair / p.Hq), h = static_cast<int>(pair % p.Hq);
+    const bool live = i < d.Lq;
+    float acc = 0.f;
+    if (live && sub * 8 < D) {
+        const long long at = ((static_cast<long long>(d.q_start) + i) * p.Hq + h) * D + sub * 8;
+        const uint4 g = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dout) + at));
+        const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+        float o[8];
+        if (F32) {
+            const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.out) + at);
+            const float4 a = __ldg(src), b = __ldg(src + 1);
+            o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+        } else {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out) + at));
+            const uint32_t ow[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack_bf16x2(ow[e]);
+                o[2 * e] = f.x, o[2 * e + 1] = f.y;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_bf16x2(gw[e]);
+            acc = fmaf(f.x, o[2 * e], acc);
+            acc = fmaf(f.y, o[2 * e + 1], acc);
+        }
+    }
+#pragma unroll
+    for (int s = LANES / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
+    if (live && sub == 0) {
+        const long long row = p.lse_row_global ? static_cast<long long>(d.q_start) + i : i;
+        const long long at = doc * p.lse_bstride + h * p.lse_hstride + row;
+        const long long to = h * p.stat_stride + bwd_stat_base(d.q_start, doc) + i;
+        // a row that sees no key (lse = -inf) has p = 2^(s - inf) = 0
+        const float lse = p.lse[at];
+        p.neg_lse2[to] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+        p.neg_delta[to] = (p.dlse ? p.dlse[at] : 0.f) - acc;
+    }
+}
+
+// ------------------------------------------------------------- the two passes
+// 384 threads:
+//   warps 0-3, 4-7  math: thread = one resident row (TMEM lane), each
+//                   warpgroup one half of a streamed tile's columns
+//   warp 8          TMA producer: resident tiles, then a ring of streamed
+//                   tiles in the order C1(0) C2(0) C1(1) ... (C1 = Q or K, C2
+//                   = dO or V); a Q tile's slot also gets its rows' statistics
+//   warp 9          TMEM allocator and MMA issuer
+// Order of the products, one S buffer:
+//   S(0) dP(0) | dV(j) S(j+1) dK(j) dP(j+1) | ...
+// so the exponentials of tile j + 1 run while the tensor core forms dK(j) and
+// dP(j+1), and its dS while it forms dV(j+1) and S(j+2).  The tensor core works
+// in order, so S(j+1) over P(j) and dP(j+1) over dS(j) need no wait of their
+// own.  With two S buffers S(j+1) comes first.
+// P and dS (bf16 pairs) are written over the half of the S or dP columns that
+// the same thread has read, so the two warpgroups need not meet.
+template <class C>
+__global__ void __launch_bounds__(384, 1)
+    attn_bwd_sm103a(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const BwdParams p) {
+    constexpr int D = C::D, BM = C::BM, BN = C::BN, NCH = C::NCH, SLOTS = C::SLOTS, SB = C::SB, H = BN / 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sR = smem_u32(smem);
+    const uint32_t sC = sR + C::RES * C::R_BYTES;
+    const uint32_t sStat = sC + SLOTS * C::C_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RES * C::R_BYTES + SLOTS * (C::C_BYTES + C::STAT_BYTES));
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NUM_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    auto b_res = [&](int r) { return smem_u32(&bars[r]); };
+    auto b_s_full = [&](int b) { return smem_u32(&bars[2 + b]); };
+    auto b_p_full = [&](int b) { return smem_u32(&bars[4 + b]); };
+    const uint32_t b_dp_full = smem_u32(&bars[6]), b_ds_full = smem_u32(&bars[7]);
+    const uint32_t b_done = smem_u32(&bars[8]), b_drain = smem_u32(&bars[9]);
+    auto b_full = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + s]); };
+    auto b_empty = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + SLOTS + s]); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // ------------------------------------------------------------------- item
+    // (tile, head, document): heads fastest and tiles slowest for causal
+    // launches (the keys' first tiles and the queries' last ones are the
+    // heaviest and come first), tiles fastest otherwise (neighbouring CTAs
+    // stream the same head).
+    const int heads = C::KEYS ? p.Hkv : p.Hq;
+    int tile, head, doc;
+    {
+        uint32_t it = blockIdx.x;
+        if (p.causal) {
+            head = it % heads;
+            it /= heads;
+            doc = it % p.num_docs;
+            tile = it / p.num_docs;
+            if (!C::KEYS) tile = p.tiles_q - 1 - tile;
+        } else {
+            const int tiles = C::KEYS ? p.tiles_k : p.tiles_q;
+            tile = it % tiles;
+            it /= tiles;
+            head = it % heads;
+            doc = it / heads;
+        }
+    }
+    const BwdDoc d = bwd_doc(p, doc, false);
+    if (d.bad) return;
+    const int r0 = tile * BM;                                   // first resident row within the document
+    const int res_all = C::KEYS ? d.Lk_all : d.Lq_all, res_len = C::KEYS ? d.Lk : d.Lq;
+    if (r0 >= res_all) return;  // CTA-uniform, before any barrier or TMEM use
+    if (status_has_timeout(p.status, kDevTimeout)) return;
+    const int res_start = C::KEYS ? d.k_start : d.q_start, str_start = C::KEYS ? d.q_start : d.k_start;
+    const int str_len = C::KEYS ? d.Lq : d.Lk;
+    const int diag = d.Lk - d.Lq;  // causal: row i sees key j iff j <= i + diag
+    // streamed tiles [t_lo, t_lo + nt) of each of `rounds` heads
+    int t_lo = 0, t_hi = (str_len + BN - 1) / BN;
+    if (r0 >= res_len) {
+        t_hi = 0;
+    } else if (p.causal) {
+        if (C::KEYS)
+            t_lo = max(0, r0 - diag) / BN;  // the first row that sees key r0
+        else
+            t_hi = (max(0, min(d.Lk, min(r0 + BM, d.Lq) + diag)) + BN - 1) / BN;
+    }
+    const int nt = max(0, t_hi - t_lo);
+    const int rounds = C::KEYS ? p.group : 1;
+    const int n = nt * rounds;
+
+    // ------------------------------------------------------------------ setup
+    if (threadIdx.x == 0) {
+        mbar_init(b_res(0), 1);
+        mbar_init(b_res(1), 1);
+        mbar_init(b_s_full(0), 1);
+        mbar_init(b_s_full(1), 1);
+        mbar_init(b_dp_full, 1);
+        mbar_init(b_p_full(0), 8);
+        mbar_init(b_p_full(1), 8);
+        mbar_init(b_ds_full, 8);
+        mbar_init(b_done, 1);
+        mbar_init(b_drain, 1);
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(b_full(s), 1);
+            mbar_init(b_empty(s), 1);
+        }
+        *abort_flag = p.give_up ? 1 : 0;  // 1: give up every wait (failure-path test)
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+
+    if (warp >= 8) {
+        regs_dec<C::REG_OTHER>();
+        if (warp == 8 && lane == 0 && n > 0) {
+            // -------------------------------------------------------- producer
+            const CUtensorMap *mR1 = C::KEYS ? &tmK : &tmQ, *mR2 = C::KEYS ? &tmV : &tmG;
+            const CUtensorMap *mC1 = C::KEYS ? &tmQ : &tmK, *mC2 = C::KEYS ? &tmG : &tmV;
+            const int res_head = head;
+            int str_head = C::KEYS ? head * p.group : head / p.group;
+            for (int r = 0; r < C::RES; ++r) {
+                mbar_arrive_expect_tx(b_res(r), C::R_BYTES);
+                for (int c = 0; c < NCH; ++c)
+                    for (int b = 0; b < BM / BN; ++b)
+                        tma_load_3d(sR + r * C::R_BYTES + c * (BM * 128) + b * (BN * 128), r ? mR2 : mR1, b_res(r),
+                                    c * 64, res_head, res_start + r0 + b * BN);
+            }
+            int slot = 0, issued = 0;
+            uint32_t ph = 1;  // parity of the slot's previous release; the first turn needs none
+            int t = t_lo;
+            for (int j = 0; ok && j < n; ++j) {
+                for (int x = 0; x < 2; ++x) {
+                    if (issued >= SLOTS && !mbar_wait(b_empty(slot), ph, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool stat = C::KEYS && x == 0;
+                    mbar_arrive_expect_tx(b_full(slot), C::C_BYTES + (stat ? C::STAT_BYTES : 0));
+                    for (int c = 0; c < NCH; ++c)
+                        tma_load_3d(sC + slot * C::C_BYTES + c * (BN * 128), x ? mC2 : mC1, b_full(slot), c * 64,
+                                    str_head, str_start + t * BN);
+                    if (stat) {
+                        const long long at =
+                            str_head * p.stat_stride + bwd_stat_base(d.q_start, doc) + static_cast<long long>(t) * BN;
+                        bulk_load(sStat + slot * C::STAT_BYTES, p.neg_lse2 + at, BN * 4, b_full(slot));
+                        bulk_load(sStat + slot * C::STAT_BYTES + BN * 4, p.neg_delta + at, BN * 4, b_full(slot));
+                    }
+                    ++issued;
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (++t == t_hi) {
+                    t = t_lo;
+                    ++str_head;
+                }
+            }
+            if (!ok || *abort_flag) {
+                // Let every copy this thread started land before the CTA retires.
+                for (int r = 0; r < C::RES; ++r) mbar_wait_drain(b_res(r), 0);
+                for (int g = (issued > SLOTS ? issued - SLOTS : 0); g < issued; ++g)
+                    mbar_wait_drain(b_full(g % SLOTS), (g / SLOTS) & 1);
+            }
+        } else if (warp == 9 && n > 0) {
+            // ------------------------------------------------------------- MMA
+            // The whole warp walks the schedule; one elected lane issues.
+            constexpr uint32_t kIdS = idesc_bf16_f32(BM, BN, false, false);
+            constexpr uint32_t kIdA = idesc_bf16_f32(BM, D, false, true);
+            const bool leader = elect_one();
+            const uint64_t dR = sdesc_sw128(sR, 16, 1024);
+            const uint64_t dCk = sdesc_sw128(sC, 16, 1024);           // streamed tile, K-major
+            const uint64_t dCm = sdesc_sw128(sC, BN * 128, 1024);     // streamed tile, MN-major
+            auto wait_all = [&](uint32_t bar, uint32_t ph) {
+                return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag));
+            };
+            // The streamed tile of load g (2 j: C1, 2 j + 1: C2) is in slot g % SLOTS.
+            auto slot_of = [&](int g) { return g % SLOTS; };
+            // Rows of a streamed tile that no resident row may see at all (past
+            // the document, the neighbours' rows, or rows without a key) may
+            // hold anything; P and dS are 0 there but 0 * NaN is not, so the
+            // tile's rows are zeroed before the second products read them.
+            auto take = [&](int g, int t, bool zero) -> bool {
+                const int s = slot_of(g);
+                if (!wait_all(b_full(s), (g / SLOTS) & 1)) return false;
+                if (zero) {
+                    const int hi = min(BN, str_len - t * BN);
+                    const int lo = (C::KEYS && p.causal) ? min(hi, max(0, -diag - t * BN)) : 0;
+                    if (hi < BN || lo > 0) {
+                        for (int x = lane; x < (lo + BN - hi) * NCH * 8; x += 32) {
+                            const int u = x & 7, rc = x >> 3, c = rc % NCH, r = rc / NCH;
+                            st_shared_v4(sC + s * C::C_BYTES + c * (BN * 128) + (r < lo ? r : hi + r - lo) * 128 + u * 16,
+                                         0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                tc_fence_after();
+                return true;
+            };
+            // X (128 x BN) = resident r * streamed tile in slot s
+            auto scores = [&](uint32_t to, int r, int s) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const int c = k >> 2, kk = k & 3;
+                    mma_bf16_ss(tmem + to, dR + ((r * C::R_BYTES + c * BM * 128 + kk * 32) >> 4),
+                                dCk + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((c * BN * 128 + kk * 32) >> 4), kIdS,
+                                k > 0 ? 1u : 0u);
+                }
+            };
+            // acc += A (bf16 pairs over X's columns, a half for each warpgroup) * streamed tile in slot s
+            auto accumulate = [&](uint32_t acc, uint32_t a, int s, bool first) {
+#pragma unroll
+                for (int k = 0; k < BN / 16; ++k)
+                    mma_bf16_ts(tmem + acc, tmem + a + (k < BN / 32 ? k * 8 : H + (k - BN / 32) * 8),
+                                dCm + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((k * 16 * 128) >> 4), kIdA,
+                                (!first || k > 0) ? 1u : 0u);
+            };
+            constexpr uint32_t kAccP = C::T_ACC, kAccDS = C::T_ACC + (C::HAS_P ? D : 0);
+            auto issue_s = [&](int j, int t) -> bool {
+                if (!take(2 * j, t, true)) return false;
+                if (leader) {
+                    scores(C::T_S + (j % SB) * BN, 0, slot_of(2 * j));
+                    mma_commit(b_s_full(j % SB));
+                }
+                __syncwarp();
+                return true;
+            };
+            auto issue_dp = [&](int j, int t) -> bool {
+                if (!take(2 * j + 1, t, C::HAS_P)) return false;
+                if (leader) {
+                    scores(C::T_DP, 1, slot_of(2 * j + 1));
+                    if (!C::HAS_P) mma_commit(b_empty(slot_of(2 * j + 1)));
+                    mma_commit(b_dp_full);
+                }
+                __syncwarp();
+                return true;
+            };
+            int t = t_lo;
+            ok = !*abort_flag && wait_all(b_res(0), 0);
+            ok = ok && issue_s(0, t);
+            if (C::HAS_DS) ok = ok && wait_all(b_res(1), 0) && issue_dp(0, t);
+            for (int j = 0; ok && j < n; ++j) {
+                const int tn = t + 1 == t_hi ? t_lo : t + 1;  // tile of step j + 1
+                const bool more = j + 1 < n;
+                if (SB == 2 && more && !(ok = issue_s(j + 1, tn))) break;
+                if (C::HAS_P) {
+                    if (!C::HAS_DS && !(ok = take(2 * j + 1, t, true))) break;
+                    if (!(ok = wait_all(b_p_full(j % SB), (j / SB) & 1))) break;
+                    tc_fence_after();
+                    if (leader) {
+                        accumulate(kAccP, C::T_S + (j % SB) * BN, slot_of(2 * j + 1), j == 0);
+                        // (the math warps are done with the statistics in C1's slot, too)
+                        if (!C::HAS_DS) mma_commit(b_empty(slot_of(2 * j)));
+                        mma_commit(b_empty(slot_of(2 * j + 1)));
+                    }
+                    __syncwarp();
+                }
+                if (SB == 1 && more && !(ok = issue_s(j + 1, tn))) break;
+                if (C::HAS_DS) {
+                    if (!(ok = wait_all(b_ds_full, j & 1))) break;
+                    tc_fence_after();
+                    if (leader) {
+                        accumulate(kAccDS, C::T_DP, slot_of(2 * j), j == 0);
+                        mma_commit(b_empty(slot_of(2 * j)));
+                    }
+                    __syncwarp();
+                    if (more && !(ok = issue_dp(j + 1, tn))) break;
+                }
+                t = tn;
+            }
+            if (ok && leader) mma_commit(b_done);
+            // Everything issued above must finish before TMEM is released.
+            if (leader) mma_commit(b_drain);
+            __syncwarp();
+            mbar_wait_drain(b_drain, 0);
+        }
+    } else {
+        regs_inc<C::REG_MATH>();
+        // ---------------------------------------------------------------- math
+        const int wg = warp >> 2;
+        const int r = (warp & 3) * 32 + lane;   // resident row within the tile == TMEM lane
+        const int row = r0 + r;                 // within the document
+        const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const float c2 = p.scale_log2;
+        float row_nl = -INFINITY, row_nd = 0.f;
+        if (!C::KEYS && row < d.Lq) {
+            const long long at = head * p.stat_stride + bwd_stat_base(d.q_start, doc) + row;
+            row_nl = p.neg_lse2[at];
+            row_nd = p.neg_delta[at];
+        }
+        int t = t_lo;
+        for (int j = 0; j < n; ++j) {
+            const int c0 = t * BN + wg * H;  // this thread's first streamed row
+            // columns [lo, hi) of the thread's H are visible
+            int lo = 0, hi = str_len - c0;
+            if (p.causal) {
+                if (C::KEYS)
+                    lo = row - diag - c0;
+                else
+                    hi = min(hi, row + diag + 1 - c0);
+            }
+            const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < H);
+            const uint32_t st = sStat + ((2 * j) % SLOTS) * C::STAT_BYTES + wg * (H * 4);
+            if (C::KEYS) ok = mbar_wait(b_full((2 * j) % SLOTS), ((2 * j) / SLOTS) & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(b_s_full(j % SB), (j / SB) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tS = tl + C::T_S + (j % SB) * BN + wg * H, tDP = tl + C::T_DP + wg * H;
+            uint32_t pr[H];  // P, fp32
+#pragma unroll
+            for (int c = 0; c < H / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&pr[c * 32]));
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < H; e += 4) {
+                float4 nl = make_float4(row_nl, row_nl, row_nl, row_nl);
+                if (C::KEYS) nl = ld_shared_f4(st + e * 4);
+                const float2 cc = make_float2(c2, c2);
+                const float2 a = __ffma2_rn(make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])), cc,
+                                            make_float2(nl.x, nl.y));
+                const float2 b = __ffma2_rn(make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])), cc,
+                                            make_float2(nl.z, nl.w));
+                pr[e] = __float_as_uint(ex2(a.x));
+                pr[e + 1] = __float_as_uint(ex2(a.y));
+                pr[e + 2] = __float_as_uint(ex2(b.x));
+                pr[e + 3] = __float_as_uint(ex2(b.y));
+            }
+            if (edge) {
+#pragma unroll
+                for (int e = 0; e < H; ++e)
+                    if (e < lo || e >= hi) pr[e] = 0u;
+            }
+            if (C::HAS_P) {
+#pragma unroll
+                for (int c = 0; c < H / 32; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pk[e] = pack_bf16x2(__uint_as_float(pr[c * 32 + 2 * e]), __uint_as_float(pr[c * 32 + 2 * e + 1]));
+                    tmem_st16(tS + c * 16, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p_full(j % SB));
+            }
+            if (C::HAS_DS) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_dp_full, j & 1, abort_flag)))) break;
+                tc_fence_after();
+                uint32_t dp[H];
+#pragma unroll
+                for (int c = 0; c < H / 32; ++c) tmem_ld32(tDP + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&dp[c * 32]));
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < H; e += 4) {
+                    float4 nd = make_float4(row_nd, row_nd, row_nd, row_nd);
+                    if (C::KEYS) nd = ld_shared_f4(st + BN * 4 + e * 4);
+                    float2 a = __fadd2_rn(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
+                                          make_float2(nd.x, nd.y));
+                    float2 b = __fadd2_rn(make_float2(__uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3])),
+                                          make_float2(nd.z, nd.w));
+                    a = __fmul2_rn(a, make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])));
+                    b = __fmul2_rn(b, make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])));
+                    dp[e] = __float_as_uint(a.x);
+                    dp[e + 1] = __float_as_uint(a.y);
+                    dp[e + 2] = __float_as_uint(b.x);
+                    dp[e + 3] = __float_as_uint(b.y);
+                }
+                if (edge) {  // 0 * (anything) is not always 0
+#pragma unroll
+                    for (int e = 0; e < H; ++e)
+                        if (e < lo || e >= hi) dp[e] = 0u;
+                }
+#pragma unroll
+                for (int c = 0; c < H / 32; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pk[e] = pack_bf16x2(__uint_as_float(dp[c * 32 + 2 * e]), __uint_as_float(dp[c * 32 + 2 * e + 1]));
+                    tmem_st16(tDP + c * 16, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_ds_full);
+            }
+            if (++t == t_hi) t = t_lo;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && n > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(b_done, 0, abort_flag));
+            tc_fence_after();
+        }
+        // ------------------------------------------------------------ epilogue
+        // Two accumulators: one a warpgroup.  One: the 32-column chunks in turn.
+        if (ok) {
+            const bool used = n > 0 && row < res_len;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                if (C::ACCS == 1 && (c & 1) != wg) continue;
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(tl + C::T_ACC + (C::ACCS == 2 ? wg * D : 0) + c * 32, o);
+                    tmem_wait_ld();
+                }
+                if (row < res_all) {
+                    const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && wg == 0);
+                    const float f = is_dv ? 1.f : p.scale;
+                    void* base = C::KEYS ? (is_dv ? p.dv : p.dk) : p.dq;
+                    uint16_t* dst = static_cast<uint16_t*>(base) +
+                                    ((static_cast<long long>(res_start) + row) * heads + head) * D + c * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            w[x] = used ? pack_bf16x2(__uint_as_float(o[e + 2 * x]) * f, __uint_as_float(o[e + 2 * x + 1]) * f)
+                                        : 0u;
+                        st_global_v4(dst + e, w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    }
+
+    // --------------------------------------------------------------- teardown
+    if (!ok) {
+        *abort_flag = 1;
+        if (p.status) atomicOr(p.status, kDevTimeout);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------- launches
+int bwd_box_rows(int D) { return D <= 128 ? 128 : 64; }
+
+long long bwd_stat_stride(long long Tq, int num_docs) {
+    // rows, the documents' alignment, and a last tile that is read whole
+    return ((Tq + 4ll * num_docs + 3) & ~3ll) + 128;
+}
+
+namespace {
+
+template <class C>
+cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                        const BwdParams& p, cudaStream_t stream) {
+    const long long items =
+        static_cast<long long>(C::KEYS ? p.tiles_k : p.tiles_q) * (C::KEYS ? p.Hkv : p.Hq) * p.num_docs;
+    if (items == 0) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(attn_bwd_sm103a<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    attn_bwd_sm103a<C><<<static_cast<unsigned>(items), 384, C::SMEM_BYTES, stream>>>(tmQ, tmG, tmK, tmV, p);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                     const BwdParams& p, cudaStream_t stream) {
+    if (p.max_q > 0) {
+        constexpr int PER_CTA = 256 / (D <= 64 ? 8 : (D <= 128 ? 16 : 32));
+        const long long ctas = (static_cast<long long>(p.max_q) * p.Hq + PER_CTA - 1) / PER_CTA;
+        const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(p.num_docs));
+        if (p.out_f32)
+            attn_bwd_stat_sm103a<D, true><<<grid, 256, 0, stream>>>(p);
+        else
+            attn_bwd_stat_sm103a<D, false><<<grid, 256, 0, stream>>>(p);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    cudaError_t e;
+    if constexpr (D <= 192) {
+        e = launch_pass<BwdCfg<D, kBwdKV>>(tmQ, tmG, tmK, tmV, p, stream);
+    } else {
+        e = launch_pass<BwdCfg<D, kBwdV>>(tmQ, tmG, tmK, tmV, p, stream);
+        if (e == cudaSuccess) e = launch_pass<BwdCfg<D, kBwdK>>(tmQ, tmG, tmK, tmV, p, stream);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_pass<BwdCfg<D, kBwdQ>>(tmQ, tmG, tmK, tmV, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_bwd(int D, const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK,
+                       const CUtensorMap& tmV, const BwdParams& p, cudaStream_t stream) {
+    switch (D) {
+        case 64: return launch_d<64>(tmQ, tmG, tmK, tmV, p, stream);
+        case 96: return launch_d<96>(tmQ, tmG, tmK, tmV, p, stream);
+        case 128: return launch_d<128>(tmQ, tmG, tmK, tmV, p, stream);
+        case 192: return launch_d<192>(tmQ, tmG, tmK, tmV, p, stream);
+        case 256: return launch_d<256>(tmQ, tmG, tmK, tmV, p, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace gbattn

@@ -316,4 +316,36 @@ cudaError_t launch_vsa_block_map(const float* pq, const float* pk, const int32_t
 cudaError_t launch_vsa_fwd(int D, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                            const VsaFwdParams& p, cudaStream_t st);
 
+// Backward pass (bwd.cu): gradients of q, k, v from out, lse and the gradient
+// of out (and of lse).  Dense and padded batches have cu_q == nullptr and
+// max_q / max_k rows an entry; packed documents use cu_q / cu_k.
+struct BwdParams {
+    const void* out;        // [Tq, Hq, D] bf16 or fp32 (out_f32)
+    const void* dout;       // [Tq, Hq, D] bf16
+    const float* lse;       // as the forward pass wrote it
+    const float* dlse;      // the same layout, or null
+    void *dq, *dk, *dv;     // bf16, the shapes of q, k, v
+    float* neg_lse2;        // workspace [Hq, stat_stride]: -lse log2 e (-inf: the row sees no key)
+    float* neg_delta;       // workspace [Hq, stat_stride]: dlse - dout.out
+    long long stat_stride;
+    uint32_t* status;
+    const int32_t *cu_q, *cu_k;
+    const int32_t *lens_q, *lens_k;  // padded batch, or null
+    int num_docs;
+    int Tq, Tk;
+    int max_q, max_k;       // rows of the longest document, or of every entry
+    int tiles_q, tiles_k;   // 128-row tiles of max_q, max_k
+    int Hq, Hkv, group;
+    float scale, scale_log2;
+    int causal, out_f32;
+    long long lse_bstride, lse_hstride;  // as PrefillParams
+    int lse_row_global;
+    int give_up;            // as PrefillParams
+};
+int bwd_box_rows(int D);  // rows of the tensor maps' boxes
+long long bwd_stat_stride(long long Tq, int num_docs);
+// tmQ, tmG (dout), tmK, tmV: [rows, heads, D] bf16, box {64, 1, bwd_box_rows(D)}, 128-byte swizzle.
+cudaError_t launch_bwd(int D, const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK,
+                       const CUtensorMap& tmV, const BwdParams& p, cudaStream_t stream);
+
 }  // namespace gbattn
