@@ -20,6 +20,8 @@ Entry points (same names as the C ABI):
     attn_fwd_paged_fp8_workspace_size: the 8-bit paged KV cache
     attn_bwd_dense, attn_bwd_padded, attn_bwd_varlen, attn_bwd_workspace_size: gradients
     (include/gbattn_bwd.h)
+    attn_rotary, attn_rotary_kv_cache_write, attn_rotary_frequencies, attn_rotary_steps: rotary
+    positions (include/gbattn_rotary.h), with RotaryPlan holding a head's frequencies on the device
 Compositions of those calls: attn_fwd_masked (padding mask), attn_vsa (block-sparse
 video attention, with VsaPlan holding one geometry's layout on the device),
 attn_fwd_paged_prefill_fp8 (several new tokens a sequence over the 8-bit cache).
@@ -45,6 +47,7 @@ NOALLOC_SCRATCH_BYTES = 32 << 20  # GBATTN_NOALLOC_SCRATCH_BYTES
 
 # (name, restype, argtypes) for every symbol of include/gbattn.h
 _P, _I, _F, _Z, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
+_D = ctypes.c_double
 SIGNATURES = {
     "attn_fwd_dense": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _I, _P, _P, _P]),
     "attn_fwd_varlen": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _I, _P, _P, _P]),
@@ -83,6 +86,11 @@ SIGNATURES = {
                              _P, _P]),
     "attn_bwd_varlen": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P,
                              _P, _Z, _P, _P]),
+    "attn_rotary_frequencies": (_I, [_I, _D, _I, _D, _D, _D, _D, _P, _P]),
+    "attn_rotary_steps": (_I, [_P, _I, _P]),
+    "attn_rotary": (_I, [_P, _L, _P, _L, _P, _I, _P, _I, _I, _I, _F, _I, _I, _I, _P, _L, _P, _L, _P]),
+    "attn_rotary_kv_cache_write": (_I, [_P, _L, _P, _L, _P, _L, _P, _P, _I, _P, _I, _I, _F, _P, _L, _P, _I, _I, _I, _I, _I,
+                                        _P, _P]),
 }
 
 _lib = None
@@ -993,3 +1001,136 @@ def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seq
                 (("cu_seqlens_q", cu_seqlens_q, N + 1), ("cu_seqlens_k", cu_seqlens_k, N + 1)),
                 (N, Tq, Tk, _host_int("max_seqlen_q", max_seqlen_q), _host_int("max_seqlen_k", max_seqlen_k)), N,
                 (Hq, Hkv, D), (Hq, Tq), softmax_scale, causal, dq, dk, dv, workspace, dev_status, stream)
+
+
+# ---- rotary positions (gbattn_rotary.h)
+ROTARY_SCALINGS = {"linear": 1, "ntk": 2, "by_parts": 3, "yarn": 4}  # gbattn_rotary_scaling
+
+
+def attn_rotary_frequencies(rot_dim, base=10000.0, scaling=None):
+    """(frequencies, gain) of a head whose first rot_dim values are turned, as
+    Python floats.  scaling: None, or a dict with "kind" (linear, ntk, by_parts,
+    yarn), "factor", and for the last two "low", "high" and "length" (the
+    trained length); gbattn_rotary.h has the formulas."""
+    scaling = dict(scaling or {})
+    kind = scaling.pop("kind", None)
+    if kind is not None and kind not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling kind must be one of {sorted(ROTARY_SCALINGS)}")
+    takes = () if kind is None else ("factor",) if kind in ("linear", "ntk") else ("factor", "low", "high", "length")
+    if sorted(scaling) != sorted(takes):
+        raise ValueError(f"scaling {kind} takes {', '.join(takes) or 'nothing'}")
+    n = max(int(rot_dim) // 2, 0)
+    f, gain = (ctypes.c_double * max(n, 1))(), ctypes.c_double()
+    st = load_library().attn_rotary_frequencies(_host_int("rot_dim", rot_dim), float(base), ROTARY_SCALINGS.get(kind, 0),
+                                                *(float(scaling.get(x, 0.0)) for x in ("factor", "low", "high", "length")),
+                                                f, ctypes.byref(gain))
+    _check("attn_rotary_frequencies", st)
+    return list(f)[:n], gain.value
+
+
+def attn_rotary_steps(inv_freq):
+    """Frequencies (floats) as fixed-point turns: Python ints, f / 2 pi modulo 1 in units of 2^-64."""
+    n = len(inv_freq)
+    f, steps = (ctypes.c_double * max(n, 1))(*map(float, inv_freq)), (ctypes.c_uint64 * max(n, 1))()
+    _check("attn_rotary_steps", load_library().attn_rotary_steps(f, n, steps))
+    return list(steps)[:n]
+
+
+class RotaryPlan:
+    """A head's rotary frequencies on the device, made once and given to
+    attn_rotary and attn_rotary_kv_cache_write: the first rot_dim values are
+    turned, in pairs (i, i + rot_dim / 2) or, interleaved, (2 i, 2 i + 1).
+    scaling as for attn_rotary_frequencies; or inv_freq, rot_dim / 2 frequencies
+    of one's own.  gain (None: the scaling's, 1 but for yarn) multiplies what is
+    turned."""
+
+    def __init__(self, rot_dim, base=10000.0, interleaved=False, scaling=None, inv_freq=None, gain=None, device="cuda"):
+        if inv_freq is None:
+            self.inv_freq, own_gain = attn_rotary_frequencies(rot_dim, base, scaling)
+        else:
+            if scaling is not None:
+                raise ValueError("give a scaling or the frequencies themselves")
+            self.inv_freq, own_gain = [float(f) for f in inv_freq], 1.0
+            if 2 * len(self.inv_freq) != rot_dim:
+                raise ValueError(f"inv_freq must hold {rot_dim // 2} frequencies")
+        self.rot_dim, self.interleaved = int(rot_dim), bool(interleaved)
+        self.gain = own_gain if gain is None else float(gain)
+        steps = [s - (1 << 64) if s >> 63 else s for s in attn_rotary_steps(self.inv_freq)]
+        self.steps = torch.tensor(steps, dtype=torch.int64).to(device)
+
+
+def _rotary_rows(name, t, dev, tokens=None, heads=None, d=None):
+    """(heads, D, token stride) of a bf16 [T, heads, D] tensor on device number dev."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, D]")
+    T, H, D = t.shape
+    stride = _token_rows(name, t, H if heads is None else heads, D if d is None else d)
+    if tokens is not None and T != tokens:
+        raise ValueError(f"{name} must have {tokens} tokens, as q")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, with q")
+    return H, D, stride
+
+
+def attn_rotary(q, k, positions, plan: RotaryPlan, transpose=False, q_out=None, k_out=None, stream=None):
+    """Turn queries q [T, Hq, D] and keys k [T, Hkv, D] (bf16; tokens may be
+    strided, as parts of a fused projection's output; k may be None) by their
+    positions [T] (int32).  transpose=True turns gradients back.  Returns
+    (q_out, k_out): new tensors, or those given, which may be q and k
+    themselves (in place)."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("attn_rotary takes CUDA tensors")
+    Hq, D, qs = _rotary_rows("q", q, dev)
+    T, Hkv, ks, kos = q.shape[0], 0, 0, 0
+    if k is not None:
+        Hkv, _, ks = _rotary_rows("k", k, dev, T, None, D)
+    elif k_out is not None:
+        raise ValueError("k_out is given without k")
+    _tensor("positions", positions, dev, torch.int32, (T,))
+    _tensor("plan.steps", plan.steps, dev, torch.int64, (plan.rot_dim // 2,))
+    if q_out is None:
+        q_out = _empty_on(stream, q, q.shape, torch.bfloat16)
+    qos = _rotary_rows("q_out", q_out, dev, T, Hq, D)[2]
+    if k is not None:
+        if k_out is None:
+            k_out = _empty_on(stream, k, k.shape, torch.bfloat16)
+        kos = _rotary_rows("k_out", k_out, dev, T, Hkv, D)[2]
+    _run_on("attn_rotary", dev, stream,
+            (q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, positions.data_ptr(), T, plan.steps.data_ptr(),
+             plan.rot_dim, 1 if plan.interleaved else 0, 1 if transpose else 0, plan.gain, Hq, Hkv, D, q_out.data_ptr(), qos,
+             None if k is None else k_out.data_ptr(), kos))
+    return q_out, k_out
+
+
+def attn_rotary_kv_cache_write(q, key, value, positions, plan: RotaryPlan, slot_mapping, kv_cache, q_out=None,
+                               dev_status=None, stream=None):
+    """attn_rotary of q, and attn_kv_cache_write of the turned key and of value
+    into kv_cache [2, nb, bs, Hkv, D], in place, at slot_mapping [T] (int32;
+    negative: not stored; a slot is to be given once), in one pass.  q [T, Hq,
+    D], key, value [T, Hkv, D]; tokens may be strided.  Returns q_out: a new
+    tensor, or the one given, which may be q itself."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("attn_rotary_kv_cache_write takes CUDA tensors")
+    Hq, D, qs = _rotary_rows("q", q, dev)
+    T = q.shape[0]
+    Hkv, _, ks = _rotary_rows("key", key, dev, T, None, D)
+    vs = _rotary_rows("value", value, dev, T, Hkv, D)[2]
+    _tensor("positions", positions, dev, torch.int32, (T,))
+    _tensor("slot_mapping", slot_mapping, dev, torch.int32, (T,))
+    _tensor("plan.steps", plan.steps, dev, torch.int64, (plan.rot_dim // 2,))
+    if kv_cache.dim() != 5 or kv_cache.shape[0] != 2 or kv_cache.shape[3:] != (Hkv, D):
+        raise ValueError(f"kv_cache must be [2, num_blocks, block_size, {Hkv}, {D}]")
+    _tensor("kv_cache", kv_cache, dev, torch.bfloat16, kv_cache.shape)
+    status = _status_ptr(dev_status)
+    if dev_status is not None and dev_status.get_device() != dev:
+        raise ValueError(f"dev_status must be on cuda:{dev}, with q")
+    if q_out is None:
+        q_out = _empty_on(stream, q, q.shape, torch.bfloat16)
+    qos = _rotary_rows("q_out", q_out, dev, T, Hq, D)[2]
+    _run_on("attn_rotary_kv_cache_write", dev, stream,
+            (q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, positions.data_ptr(), slot_mapping.data_ptr(), T,
+             plan.steps.data_ptr(), plan.rot_dim, 1 if plan.interleaved else 0, plan.gain, q_out.data_ptr(), qos,
+             kv_cache.data_ptr(), kv_cache.shape[1], kv_cache.shape[2], Hq, Hkv, D, status))
+    return q_out

@@ -3,6 +3,7 @@
 // synchronisation; every launch goes to the caller's stream.
 #include "../../include/gbattn.h"
 #include "../../include/gbattn_bwd.h"
+#include "../../include/gbattn_rotary.h"
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -208,6 +209,25 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
         !encode_rows_heads_d(&tk, keys ? k : q, rk, hk, D, box) || !encode_rows_heads_d(&tv, keys ? v : dout, rk, hk, D, box))
         return GBATTN_ERR_CUDA;
     return gbattn::launch_bwd(D, tq, tg, tk, tv, p, st) == cudaSuccess ? GBATTN_OK : GBATTN_ERR_CUDA;
+}
+
+// What the two calls on rotary positions have in common; `p` comes with their sizes.
+gbattn_status check_rotary(const gbattn::RotaryParams& p, int rot_dim, int interleaved, int transpose) {
+    if (p.num_tokens < 0 || p.Hq <= 0 || p.Hkv < 0 || !isfinite(p.gain)) return GBATTN_ERR_INVALID_ARG;
+    if ((interleaved != 0 && interleaved != 1) || (transpose != 0 && transpose != 1)) return GBATTN_ERR_INVALID_ARG;
+    if (!head_size_ok(p.D) || rot_dim < 2 || rot_dim > p.D || rot_dim % 2 != 0) return GBATTN_ERR_UNSUPPORTED;
+    if (p.num_tokens >= (1ll << 30) || (static_cast<long long>(p.Hq) + 2ll * p.Hkv) * p.D >= (1ll << 30))
+        return GBATTN_ERR_UNSUPPORTED;
+    if (p.num_tokens == 0) return GBATTN_OK;
+    if (!p.q || !p.q_out || !p.positions || !p.steps || (p.Hkv > 0 && (!p.k || !p.k_out))) return GBATTN_ERR_INVALID_ARG;
+    // (a stride is not used with one token)
+    const long long hq = static_cast<long long>(p.Hq) * p.D, hk = static_cast<long long>(p.Hkv) * p.D;
+    if (p.num_tokens > 1 && (p.q_stride < hq || p.q_out_stride < hq || p.k_stride < hk)) return GBATTN_ERR_INVALID_ARG;
+    if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.q_out) || !aligned16(p.k_out) ||
+        (reinterpret_cast<uintptr_t>(p.steps) & 7u) != 0)
+        return GBATTN_ERR_ALIGNMENT;
+    if (p.num_tokens > 1 && ((p.q_stride | p.q_out_stride | p.k_stride) & 7) != 0) return GBATTN_ERR_ALIGNMENT;
+    return GBATTN_OK;
 }
 
 // 1: the prefill, backward and 8-bit decode kernels give up every pipeline wait (attn_set_wait_give_up).
@@ -955,6 +975,85 @@ gbattn_status attn_bwd_varlen(const void* q, const void* k, const void* v, const
     p.lse_row_global = 1;
     return run_bwd(q, k, v, out, out_dtype, lse, dout, dlse, D, softmax_scale, causal, dq, dk, dv, workspace,
                    workspace_bytes, dev_status, p, static_cast<cudaStream_t>(stream));
+}
+
+gbattn_status attn_rotary(const void* q, long long q_stride, const void* k, long long k_stride, const int32_t* positions,
+                          int num_tokens, const uint64_t* steps, int rot_dim, int interleaved, int transpose, float gain,
+                          int Hq, int Hkv, int D, void* q_out, long long q_out_stride, void* k_out,
+                          long long k_out_stride, void* stream) {
+    gbattn::RotaryParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.k_out = static_cast<uint16_t*>(k_out);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    p.positions = positions;
+    p.steps = reinterpret_cast<const unsigned long long*>(steps);
+    p.num_tokens = num_tokens;
+    p.half = rot_dim / 2;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.interleaved = interleaved;
+    p.transpose = transpose;
+    p.gain = gain;
+    gbattn_status s = check_rotary(p, rot_dim, interleaved, transpose);
+    if (s != GBATTN_OK || num_tokens == 0) return s;
+    if (Hkv > 0 && num_tokens > 1) {
+        if (k_out_stride < static_cast<long long>(Hkv) * D) return GBATTN_ERR_INVALID_ARG;
+        if ((k_out_stride & 7) != 0) return GBATTN_ERR_ALIGNMENT;
+    }
+    p.in_place = q == q_out && q_stride == q_out_stride && (Hkv == 0 || (k == k_out && k_stride == k_out_stride));
+    DeviceInfo di;
+    s = device_info(&di);
+    if (s != GBATTN_OK) return s;
+    return gbattn::launch_rotary(p, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GBATTN_OK : GBATTN_ERR_CUDA;
+}
+
+gbattn_status attn_rotary_kv_cache_write(const void* q, long long q_stride, const void* key, long long key_stride,
+                                         const void* value, long long value_stride, const int32_t* positions,
+                                         const int32_t* slot_mapping, int num_tokens, const uint64_t* steps, int rot_dim,
+                                         int interleaved, float gain, void* q_out, long long q_out_stride,
+                                         void* kv_cache, int num_blocks, int block_size, int Hq, int Hkv, int D,
+                                         uint32_t* dev_status, void* stream) {
+    gbattn::RotaryParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(key);
+    p.v = static_cast<const uint16_t*>(value);
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.k_out = static_cast<uint16_t*>(kv_cache);
+    p.q_stride = q_stride;
+    p.k_stride = key_stride;
+    p.v_stride = value_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = static_cast<long long>(Hkv) * D;
+    p.positions = positions;
+    p.slot_mapping = slot_mapping;
+    p.steps = reinterpret_cast<const unsigned long long*>(steps);
+    p.num_tokens = num_tokens;
+    p.num_slots = static_cast<long long>(num_blocks) * block_size;
+    p.half = rot_dim / 2;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.interleaved = interleaved;
+    p.gain = gain;
+    p.status = dev_status;
+    if (num_blocks <= 0 || block_size <= 0 || Hkv <= 0) return GBATTN_ERR_INVALID_ARG;
+    gbattn_status s = check_rotary(p, rot_dim, interleaved, 0);
+    if (s != GBATTN_OK) return s;
+    if (p.num_slots > 0x7fffffffLL) return GBATTN_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return GBATTN_OK;
+    if (!value || !slot_mapping) return GBATTN_ERR_INVALID_ARG;
+    if (num_tokens > 1 && value_stride < p.k_out_stride) return GBATTN_ERR_INVALID_ARG;
+    if (!aligned16(value) || (num_tokens > 1 && (value_stride & 7) != 0)) return GBATTN_ERR_ALIGNMENT;
+    DeviceInfo di;
+    s = device_info(&di);
+    if (s != GBATTN_OK) return s;
+    return gbattn::launch_rotary(p, di.sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GBATTN_OK : GBATTN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -348,4 +348,24 @@ long long bwd_stat_stride(long long Tq, int num_docs);
 cudaError_t launch_bwd(int D, const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK,
                        const CUtensorMap& tmV, const BwdParams& p, cudaStream_t stream);
 
+// Rotary positions (rotary.cu) of q and k; with slot_mapping k_out is the
+// paged cache [2, num_slots, Hkv, D] and v is stored beside the keys.
+struct RotaryParams {
+    const uint16_t *q, *k, *v;  // bf16, token t at t * stride elements
+    uint16_t *q_out, *k_out;
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    const int32_t* positions;
+    const int32_t* slot_mapping;       // null: k_out is laid out by token
+    const unsigned long long* steps;   // [half]: frequencies in 2^-64 turns
+    long long num_tokens, num_slots;
+    int half, Hq, Hkv, D;
+    int interleaved, transpose;
+    int in_place;  // every output is its input: what is not turned need not be copied
+    float gain;
+    uint32_t* status;
+    int units, parts;  // set by launch_rotary: units a head, warps a token
+    FastDiv by_units;
+};
+cudaError_t launch_rotary(RotaryParams p, int num_sms, cudaStream_t stream);
+
 }  // namespace gbattn

@@ -22,4 +22,5 @@ from .attention import (  # noqa: F401
     vsa_blocks,
 )
 from .gradients import attention_gradients  # noqa: F401
+from .rotary import rotary  # noqa: F401
 from .fp8_cache import code_values, kv_cache_write_fp8, quantise_rows, stands_for  # noqa: F401
