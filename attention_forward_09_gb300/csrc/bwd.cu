@@ -60,30 +60,42 @@ struct BwdCfg {
     static constexpr bool KEYS = MODE != kBwdQ;       // keys resident, queries streamed
     static constexpr bool HAS_P = MODE == kBwdKV || MODE == kBwdV;  // sums dV
     static constexpr bool HAS_DS = MODE != kBwdV;     // needs dP; sums dK or dQ
+    static constexpr int ISSUERS = HAS_DS ? 2 : 1;    // warps that issue products
     static constexpr int ACCS = MODE == kBwdKV ? 2 : 1;
     static constexpr int NCH = (D + 63) / 64;         // 64-column chunks
     static constexpr int RES = HAS_DS ? 2 : 1;        // resident tiles: K (and V), or Q and dO
     static constexpr int R_BYTES = NCH * BM * 128;
     static constexpr int C_BYTES = NCH * BN * 128;    // one streamed tile
+    // Residents held in tensor memory (bf16 pairs, D / 2 columns each) where
+    // there is room: S and dP then read one operand of two from shared memory,
+    // whose bandwidth otherwise equals the tensor core's need to the byte, and
+    // their room goes to the ring.
+    static constexpr bool RT = !KEYS && D <= 64;
     static constexpr int STAT_BYTES = KEYS ? 2 * BN * 4 : 0;  // -lse log2 e, -delta of a streamed tile's rows
-    // TMEM: S buffers, dP, accumulators.  A second S buffer where it fits lets
-    // the next scores be formed before the current ones are used up.
-    static constexpr int SB = (2 + (HAS_DS ? 1 : 0)) * BN + ACCS * D <= 512 ? 2 : 1;
+    // TMEM: S buffers, dP, accumulators, residents.  A second S buffer where it
+    // fits lets the next scores be formed before the current ones are used up.
+    static constexpr int T_REST = (HAS_DS ? BN : 0) + ACCS * D + (RT ? D : 0);
+    static constexpr int SB = 2 * BN + T_REST <= 512 ? 2 : 1;
     static constexpr int T_S = 0;
     static constexpr int T_DP = SB * BN;
     static constexpr int T_ACC = T_DP + (HAS_DS ? BN : 0);
-    static constexpr int BARS_FIXED = 10;
-    static constexpr int ROOM = 232448 - 1024 - RES * R_BYTES - 16 - BARS_FIXED * 8;
-    static constexpr int FIT = ROOM / (C_BYTES + STAT_BYTES + 16);
-    static constexpr int SLOTS = FIT < 6 ? FIT : 6;
+    static constexpr int T_RES = T_ACC + ACCS * D;
+    static constexpr int STATS = D <= 64 ? 4 : 2;     // buffers of them
+    static constexpr int BARS_FIXED = 11 + 2 * STATS;
+    static constexpr int ROOM = 232448 - (RT ? 0 : RES * R_BYTES) - STATS * STAT_BYTES - 16 - BARS_FIXED * 8;
+    static constexpr int FIT = ROOM / (C_BYTES + 16);
+    static constexpr int SLOTS = FIT < 8 ? FIT : 8;
     static constexpr int NUM_BARS = BARS_FIXED + 2 * SLOTS;
-    static constexpr int SMEM_BYTES = 1024 + RES * R_BYTES + SLOTS * (C_BYTES + STAT_BYTES) + NUM_BARS * 8 + 16;
+    static constexpr int O_C = RT ? 0 : RES * R_BYTES;  // offsets in shared memory
+    static constexpr int O_STAT = O_C + SLOTS * C_BYTES;
+    static constexpr int O_BARS = O_STAT + STATS * STAT_BYTES;
+    static constexpr int SMEM_BYTES = O_BARS + NUM_BARS * 8 + 16;
     static constexpr int REG_MATH = 208, REG_OTHER = 88;  // setmaxnreg split of 384 x 168
-    static_assert(T_ACC + ACCS * D <= 512, "TMEM budget");
+    static_assert(T_ACC + ACCS * D + (RT ? D : 0) <= 512, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(!RT || (BM == BN && D % 32 == 0), "residents pass through the ring's slots");
     static_assert(SLOTS >= 3, "C1 of the next step is needed before C1 and C2 of this one are released");
     static_assert(SMEM_BYTES > 116 * 1024, "one CTA an SM: it takes all TMEM columns");
-    static_assert(SB == 2 || HAS_P, "one S buffer is freed by the P it becomes");
     static_assert(2 * 128 * REG_MATH + 128 * REG_OTHER <= 384 * 168, "register split");
 };
 
@@ -212,14 +224,16 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p) {
 //                   warpgroup one half of a streamed tile's columns
 //   warp 8          TMA producer: resident tiles, then a ring of streamed
 //                   tiles in the order C1(0) C2(0) C1(1) ... (C1 = Q or K, C2
-//                   = dO or V); a Q tile's slot also gets its rows' statistics
-//   warp 9          TMEM allocator and MMA issuer
+//                   = dO or V)
+//   warp 9          TMEM allocator; issues S and dV
+//   warp 10         (keys resident) the streamed rows' statistics
+//   warp 11         issues dP and dK or dQ
 // Order of the products, one S buffer:
-//   S(0) dP(0) | dV(j) S(j+1) dK(j) dP(j+1) | ...
-// so the exponentials of tile j + 1 run while the tensor core forms dK(j) and
-// dP(j+1), and its dS while it forms dV(j+1) and S(j+2).  The tensor core works
-// in order, so S(j+1) over P(j) and dP(j+1) over dS(j) need no wait of their
-// own.  With two S buffers S(j+1) comes first.
+//   warp 9:  S(0) | dV(0) S(1) | dV(1) S(2) | ...     after P(j) is there
+//   warp 11: dP(0) | dK(0) dP(1) | dK(1) dP(2) | ...  after dS(j) is there
+// The tensor core finishes what one thread issues in order, so S(j+1) over
+// P(j) and dP(j+1) over dS(j) need no wait of their own.  With two S buffers
+// S(j+1) comes first.
 // P and dS (bf16 pairs) are written over the half of the S or dP columns that
 // the same thread has read, so the two warpgroups need not meet.
 template <class C>
@@ -228,19 +242,20 @@ __global__ void __launch_bounds__(384, 1)
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const BwdParams p) {
     constexpr int D = C::D, BM = C::BM, BN = C::BN, NCH = C::NCH, SLOTS = C::SLOTS, SB = C::SB, H = BN / 2;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles lie on 1024 bytes
     const uint32_t sR = smem_u32(smem);
-    const uint32_t sC = sR + C::RES * C::R_BYTES;
-    const uint32_t sStat = sC + SLOTS * C::C_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RES * C::R_BYTES + SLOTS * (C::C_BYTES + C::STAT_BYTES));
+    const uint32_t sC = sR + C::O_C;
+    const uint32_t sStat = sR + C::O_STAT;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::O_BARS);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NUM_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     auto b_res = [&](int r) { return smem_u32(&bars[r]); };
     auto b_s_full = [&](int b) { return smem_u32(&bars[2 + b]); };
     auto b_p_full = [&](int b) { return smem_u32(&bars[4 + b]); };
     const uint32_t b_dp_full = smem_u32(&bars[6]), b_ds_full = smem_u32(&bars[7]);
-    const uint32_t b_done = smem_u32(&bars[8]), b_drain = smem_u32(&bars[9]);
+    const uint32_t b_done = smem_u32(&bars[8]), b_drain = smem_u32(&bars[9]), b_res_in = smem_u32(&bars[10]);
+    auto b_stat_full = [&](int b) { return smem_u32(&bars[11 + b]); };
+    auto b_stat_empty = [&](int b) { return smem_u32(&bars[11 + C::STATS + b]); };
     auto b_full = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + s]); };
     auto b_empty = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + SLOTS + s]); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -301,11 +316,16 @@ __global__ void __launch_bounds__(384, 1)
         mbar_init(b_p_full(0), 8);
         mbar_init(b_p_full(1), 8);
         mbar_init(b_ds_full, 8);
-        mbar_init(b_done, 1);
-        mbar_init(b_drain, 1);
+        mbar_init(b_done, C::ISSUERS);
+        mbar_init(b_drain, C::ISSUERS);
+        mbar_init(b_res_in, 8);
+        for (int b = 0; b < C::STATS; ++b) {
+            mbar_init(b_stat_full(b), 1);
+            mbar_init(b_stat_empty(b), 8);
+        }
         for (int s = 0; s < SLOTS; ++s) {
             mbar_init(b_full(s), 1);
-            mbar_init(b_empty(s), 1);
+            mbar_init(b_empty(s), C::ISSUERS);
         }
         *abort_flag = p.give_up ? 1 : 0;  // 1: give up every wait (failure-path test)
         fence_mbar_init();
@@ -328,15 +348,24 @@ __global__ void __launch_bounds__(384, 1)
             const CUtensorMap *mC1 = C::KEYS ? &tmQ : &tmK, *mC2 = C::KEYS ? &tmG : &tmV;
             const int res_head = head;
             int str_head = C::KEYS ? head * p.group : head / p.group;
-            for (int r = 0; r < C::RES; ++r) {
-                mbar_arrive_expect_tx(b_res(r), C::R_BYTES);
-                for (int c = 0; c < NCH; ++c)
-                    for (int b = 0; b < BM / BN; ++b)
-                        tma_load_3d(sR + r * C::R_BYTES + c * (BM * 128) + b * (BN * 128), r ? mR2 : mR1, b_res(r),
-                                    c * 64, res_head, res_start + r0 + b * BN);
-            }
             int slot = 0, issued = 0;
             uint32_t ph = 1;  // parity of the slot's previous release; the first turn needs none
+            auto next = [&]() {
+                ++issued;
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    ph ^= 1u;
+                }
+            };
+            for (int r = 0; r < C::RES; ++r) {
+                const uint32_t bar = C::RT ? b_full(slot) : b_res(r), to = C::RT ? sC + slot * C::C_BYTES : sR + r * C::R_BYTES;
+                mbar_arrive_expect_tx(bar, C::R_BYTES);
+                for (int c = 0; c < NCH; ++c)
+                    for (int b = 0; b < BM / BN; ++b)
+                        tma_load_3d(to + c * (BM * 128) + b * (BN * 128), r ? mR2 : mR1, bar, c * 64, res_head,
+                                    res_start + r0 + b * BN);
+                if (C::RT) next();
+            }
             int t = t_lo;
             for (int j = 0; ok && j < n; ++j) {
                 for (int x = 0; x < 2; ++x) {
@@ -344,22 +373,11 @@ __global__ void __launch_bounds__(384, 1)
                         ok = false;
                         break;
                     }
-                    const bool stat = C::KEYS && x == 0;
-                    mbar_arrive_expect_tx(b_full(slot), C::C_BYTES + (stat ? C::STAT_BYTES : 0));
+                    mbar_arrive_expect_tx(b_full(slot), C::C_BYTES);
                     for (int c = 0; c < NCH; ++c)
                         tma_load_3d(sC + slot * C::C_BYTES + c * (BN * 128), x ? mC2 : mC1, b_full(slot), c * 64,
                                     str_head, str_start + t * BN);
-                    if (stat) {
-                        const long long at =
-                            str_head * p.stat_stride + bwd_stat_base(d.q_start, doc) + static_cast<long long>(t) * BN;
-                        bulk_load(sStat + slot * C::STAT_BYTES, p.neg_lse2 + at, BN * 4, b_full(slot));
-                        bulk_load(sStat + slot * C::STAT_BYTES + BN * 4, p.neg_delta + at, BN * 4, b_full(slot));
-                    }
-                    ++issued;
-                    if (++slot == SLOTS) {
-                        slot = 0;
-                        ph ^= 1u;
-                    }
+                    next();
                 }
                 if (++t == t_hi) {
                     t = t_lo;
@@ -368,13 +386,35 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (!ok || *abort_flag) {
                 // Let every copy this thread started land before the CTA retires.
-                for (int r = 0; r < C::RES; ++r) mbar_wait_drain(b_res(r), 0);
+                for (int r = 0; !C::RT && r < C::RES; ++r) mbar_wait_drain(b_res(r), 0);
                 for (int g = (issued > SLOTS ? issued - SLOTS : 0); g < issued; ++g)
                     mbar_wait_drain(b_full(g % SLOTS), (g / SLOTS) & 1);
             }
-        } else if (warp == 9 && n > 0) {
+        } else if (C::KEYS && warp == 10 && lane == 0 && n > 0) {
+            // ------------------------------------ statistics of streamed rows
+            int h = head * p.group, t = t_lo, issued = 0;
+            for (int j = 0; j < n; ++j) {
+                const int b = j % C::STATS;
+                if (j >= C::STATS && !(ok = mbar_wait(b_stat_empty(b), (j / C::STATS - 1) & 1, abort_flag))) break;
+                const long long at = h * p.stat_stride + bwd_stat_base(d.q_start, doc) + static_cast<long long>(t) * BN;
+                mbar_arrive_expect_tx(b_stat_full(b), C::STAT_BYTES);
+                bulk_load(sStat + b * C::STAT_BYTES, p.neg_lse2 + at, BN * 4, b_stat_full(b));
+                bulk_load(sStat + b * C::STAT_BYTES + BN * 4, p.neg_delta + at, BN * 4, b_stat_full(b));
+                ++issued;
+                if (++t == t_hi) {
+                    t = t_lo;
+                    ++h;
+                }
+            }
+            if (!ok || *abort_flag)
+                for (int g = (issued > C::STATS ? issued - C::STATS : 0); g < issued; ++g)
+                    mbar_wait_drain(b_stat_full(g % C::STATS), (g / C::STATS) & 1);
+        } else if ((warp == 9 || (warp == 11 && C::ISSUERS == 2)) && n > 0) {
             // ------------------------------------------------------------- MMA
-            // The whole warp walks the schedule; one elected lane issues.
+            // Warp 9 issues S (and dV), warp 11 dP and dK or dQ: a product is
+            // issued about as fast as it runs, so what one warp waits the
+            // other's products fill.  Each walks its schedule as a whole warp;
+            // one elected lane issues.
             constexpr uint32_t kIdS = idesc_bf16_f32(BM, BN, false, false);
             constexpr uint32_t kIdA = idesc_bf16_f32(BM, D, false, true);
             const bool leader = elect_one();
@@ -384,39 +424,50 @@ __global__ void __launch_bounds__(384, 1)
             auto wait_all = [&](uint32_t bar, uint32_t ph) {
                 return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag));
             };
-            // The streamed tile of load g (2 j: C1, 2 j + 1: C2) is in slot g % SLOTS.
-            auto slot_of = [&](int g) { return g % SLOTS; };
+            // Load g is in slot g % SLOTS: the residents first where they pass
+            // through the ring, then C1 and C2 of each step.
+            constexpr int G0 = C::RT ? C::RES : 0;
+            struct Slot {
+                int s;
+                uint32_t ph;
+                __device__ explicit Slot(int g) : s(g % SLOTS), ph((g / SLOTS) & 1) {}
+                __device__ void step() {  // the same operand's tile of the next step
+                    s += 2;
+                    if (s >= SLOTS) {
+                        s -= SLOTS;
+                        ph ^= 1u;
+                    }
+                }
+            };
             // Rows of a streamed tile that no resident row may see at all (past
             // the document, the neighbours' rows, or rows without a key) may
             // hold anything; P and dS are 0 there but 0 * NaN is not, so the
-            // tile's rows are zeroed before the second products read them.
-            auto take = [&](int g, int t, bool zero) -> bool {
-                const int s = slot_of(g);
-                if (!wait_all(b_full(s), (g / SLOTS) & 1)) return false;
-                if (zero) {
-                    const int hi = min(BN, str_len - t * BN);
-                    const int lo = (C::KEYS && p.causal) ? min(hi, max(0, -diag - t * BN)) : 0;
-                    if (hi < BN || lo > 0) {
-                        for (int x = lane; x < (lo + BN - hi) * NCH * 8; x += 32) {
-                            const int u = x & 7, rc = x >> 3, c = rc % NCH, r = rc / NCH;
-                            st_shared_v4(sC + s * C::C_BYTES + c * (BN * 128) + (r < lo ? r : hi + r - lo) * 128 + u * 16,
-                                         0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
+            // tile's rows are zeroed before the second product reads them.
+            auto edge_rows = [&](int t) {
+                return (t + 1) * BN > str_len || (C::KEYS && p.causal && t * BN < -diag);
+            };
+            auto zero_rows = [&](int s, int t) {
+                const int hi = min(BN, str_len - t * BN);
+                const int lo = (C::KEYS && p.causal) ? min(hi, max(0, -diag - t * BN)) : 0;
+                for (int x = lane; x < (lo + BN - hi) * NCH * 8; x += 32) {
+                    const int u = x & 7, rc = x >> 3, c = rc % NCH, r = rc / NCH;
+                    st_shared_v4(sC + s * C::C_BYTES + c * (BN * 128) + (r < lo ? r : hi + r - lo) * 128 + u * 16, 0u, 0u, 0u,
+                                 0u);
                 }
-                tc_fence_after();
-                return true;
+                fence_proxy_async_smem();
+                __syncwarp();
             };
             // X (128 x BN) = resident r * streamed tile in slot s
             auto scores = [&](uint32_t to, int r, int s) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const int c = k >> 2, kk = k & 3;
-                    mma_bf16_ss(tmem + to, dR + ((r * C::R_BYTES + c * BM * 128 + kk * 32) >> 4),
-                                dCk + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((c * BN * 128 + kk * 32) >> 4), kIdS,
-                                k > 0 ? 1u : 0u);
+                    const uint64_t b = dCk + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((c * BN * 128 + kk * 32) >> 4);
+                    if constexpr (C::RT)
+                        mma_bf16_ts(tmem + to, tmem + C::T_RES + r * (D / 2) + k * 8, b, kIdS, k > 0 ? 1u : 0u);
+                    else
+                        mma_bf16_ss(tmem + to, dR + ((r * C::R_BYTES + c * BM * 128 + kk * 32) >> 4), b, kIdS,
+                                    k > 0 ? 1u : 0u);
                 }
             };
             // acc += A (bf16 pairs over X's columns, a half for each warpgroup) * streamed tile in slot s
@@ -427,58 +478,104 @@ __global__ void __launch_bounds__(384, 1)
                                 dCm + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((k * 16 * 128) >> 4), kIdA,
                                 (!first || k > 0) ? 1u : 0u);
             };
-            constexpr uint32_t kAccP = C::T_ACC, kAccDS = C::T_ACC + (C::HAS_P ? D : 0);
-            auto issue_s = [&](int j, int t) -> bool {
-                if (!take(2 * j, t, true)) return false;
-                if (leader) {
-                    scores(C::T_S + (j % SB) * BN, 0, slot_of(2 * j));
-                    mma_commit(b_s_full(j % SB));
+            ok = !*abort_flag;  // a launch told to give up issues nothing
+            if (C::RT) {  // the math warps have copied the residents into tensor memory
+                ok = ok && wait_all(b_res_in, 0);
+                if (ok && lane == 0) {
+                    mbar_arrive(b_empty(0));
+                    mbar_arrive(b_empty(1));
                 }
                 __syncwarp();
-                return true;
-            };
-            auto issue_dp = [&](int j, int t) -> bool {
-                if (!take(2 * j + 1, t, C::HAS_P)) return false;
-                if (leader) {
-                    scores(C::T_DP, 1, slot_of(2 * j + 1));
-                    if (!C::HAS_P) mma_commit(b_empty(slot_of(2 * j + 1)));
-                    mma_commit(b_dp_full);
-                }
-                __syncwarp();
-                return true;
-            };
+            } else {
+                ok = ok && wait_all(b_res(warp == 9 ? 0 : 1), 0);
+            }
+            Slot c1(G0), c2(G0 + 1);
             int t = t_lo;
-            ok = !*abort_flag && wait_all(b_res(0), 0);
-            ok = ok && issue_s(0, t);
-            if (C::HAS_DS) ok = ok && wait_all(b_res(1), 0) && issue_dp(0, t);
-            for (int j = 0; ok && j < n; ++j) {
-                const int tn = t + 1 == t_hi ? t_lo : t + 1;  // tile of step j + 1
-                const bool more = j + 1 < n;
-                if (SB == 2 && more && !(ok = issue_s(j + 1, tn))) break;
-                if (C::HAS_P) {
-                    if (!C::HAS_DS && !(ok = take(2 * j + 1, t, true))) break;
-                    if (!(ok = wait_all(b_p_full(j % SB), (j / SB) & 1))) break;
+            if (warp == 9) {
+                Slot c1n = c1;  // C1 of the step whose S comes next
+                auto issue_s = [&](int j) {
+                    scores(C::T_S + (j % SB) * BN, 0, c1n.s);
+                    mma_commit(b_empty(c1n.s));
+                    mma_commit(b_s_full(j % SB));
+                };
+                ok = ok && wait_all(b_full(c1n.s), c1n.ph);
+                if (ok) {
                     tc_fence_after();
-                    if (leader) {
-                        accumulate(kAccP, C::T_S + (j % SB) * BN, slot_of(2 * j + 1), j == 0);
-                        // (the math warps are done with the statistics in C1's slot, too)
-                        if (!C::HAS_DS) mma_commit(b_empty(slot_of(2 * j)));
-                        mma_commit(b_empty(slot_of(2 * j + 1)));
-                    }
+                    if (leader) issue_s(0);
                     __syncwarp();
                 }
-                if (SB == 1 && more && !(ok = issue_s(j + 1, tn))) break;
-                if (C::HAS_DS) {
+                for (int j = 0; ok && j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    c1n.step();
+                    if (more && !(ok = wait_all(b_full(c1n.s), c1n.ph))) break;
+                    // With a second buffer S_{j+1} need not wait for P_j: step
+                    // j - 1's scores have been used up (dV_{j-1} was issued
+                    // here, or the math warps have said so).
+                    if (SB == 2 && C::HAS_P) {
+                        tc_fence_after();
+                        if (more && leader) issue_s(j + 1);
+                        __syncwarp();
+                    }
+                    if (C::HAS_P) {
+                        if (!(ok = wait_all(b_full(c2.s), c2.ph))) break;
+                        if (edge_rows(t)) zero_rows(c2.s, t);
+                    }
+                    // P_j is there; without dV: S_j, or of two buffers S_{j-1}, has been read
+                    const int w = C::HAS_P || SB == 1 ? j : j - 1;
+                    if (w >= 0 && !(ok = wait_all(b_p_full(w % SB), (w / SB) & 1))) break;
+                    tc_fence_after();
+                    if (leader) {
+                        if (C::HAS_P) {
+                            accumulate(C::T_ACC, C::T_S + (j % SB) * BN, c2.s, j == 0);
+                            mma_commit(b_empty(c2.s));
+                        }
+                        if (more && (SB == 1 || !C::HAS_P)) issue_s(j + 1);
+                    }
+                    __syncwarp();
+                    c2.step();
+                    if (++t == t_hi) t = t_lo;
+                }
+            } else {
+                constexpr uint32_t kAcc = C::T_ACC + (C::HAS_P ? D : 0);
+                Slot c2n = c2;  // C2 of the step whose dP comes next
+                auto issue_dp = [&]() {
+                    scores(C::T_DP, 1, c2n.s);
+                    mma_commit(b_empty(c2n.s));
+                    if (!C::HAS_P) mma_commit(b_empty(c2n.s));  // (a slot is released twice)
+                    mma_commit(b_dp_full);
+                };
+                ok = ok && wait_all(b_full(c2n.s), c2n.ph);
+                if (ok) {
+                    tc_fence_after();
+                    if (leader) issue_dp();
+                    __syncwarp();
+                }
+                for (int j = 0; ok && j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    c2n.step();
+                    if (edge_rows(t)) {
+                        if (!(ok = wait_all(b_full(c1.s), c1.ph))) break;
+                        zero_rows(c1.s, t);
+                    }
+                    // (with three slots C2 of the next step comes into the slot of C1 of this one)
+                    if (SLOTS > 3 && more && !(ok = wait_all(b_full(c2n.s), c2n.ph))) break;
                     if (!(ok = wait_all(b_ds_full, j & 1))) break;
                     tc_fence_after();
                     if (leader) {
-                        accumulate(kAccDS, C::T_DP, slot_of(2 * j), j == 0);
-                        mma_commit(b_empty(slot_of(2 * j)));
+                        accumulate(kAcc, C::T_DP, c1.s, j == 0);
+                        mma_commit(b_empty(c1.s));
+                        if (SLOTS > 3 && more) issue_dp();
                     }
                     __syncwarp();
-                    if (more && !(ok = issue_dp(j + 1, tn))) break;
+                    if (SLOTS == 3 && more) {
+                        if (!(ok = wait_all(b_full(c2n.s), c2n.ph))) break;
+                        tc_fence_after();
+                        if (leader) issue_dp();
+                        __syncwarp();
+                    }
+                    c1.step();
+                    if (++t == t_hi) t = t_lo;
                 }
-                t = tn;
             }
             if (ok && leader) mma_commit(b_done);
             // Everything issued above must finish before TMEM is released.
@@ -500,8 +597,30 @@ __global__ void __launch_bounds__(384, 1)
             row_nl = p.neg_lse2[at];
             row_nd = p.neg_delta[at];
         }
+        if (C::RT && n > 0) {
+            // warpgroup w copies resident w from slot w of the ring into tensor memory
+            ok = __all_sync(0xffffffffu, mbar_wait(b_full(wg), 0, abort_flag));
+            if (ok) {
+                const uint32_t src = sC + wg * C::C_BYTES + r * 128;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float4 x = ld_shared_f4(src + (c >> 1) * (BM * 128) + (((((c & 1) << 2) + u) ^ (r & 7)) << 4));
+                        w[4 * u] = __float_as_uint(x.x), w[4 * u + 1] = __float_as_uint(x.y);
+                        w[4 * u + 2] = __float_as_uint(x.z), w[4 * u + 3] = __float_as_uint(x.w);
+                    }
+                    tmem_st16(tl + C::T_RES + wg * (D / 2) + c * 16, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_res_in);
+            }
+        }
         int t = t_lo;
-        for (int j = 0; j < n; ++j) {
+        for (int j = 0; ok && j < n; ++j) {
             const int c0 = t * BN + wg * H;  // this thread's first streamed row
             // columns [lo, hi) of the thread's H are visible
             int lo = 0, hi = str_len - c0;
@@ -512,8 +631,8 @@ __global__ void __launch_bounds__(384, 1)
                     hi = min(hi, row + diag + 1 - c0);
             }
             const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < H);
-            const uint32_t st = sStat + ((2 * j) % SLOTS) * C::STAT_BYTES + wg * (H * 4);
-            if (C::KEYS) ok = mbar_wait(b_full((2 * j) % SLOTS), ((2 * j) / SLOTS) & 1, abort_flag);
+            const uint32_t st = sStat + (j % C::STATS) * C::STAT_BYTES + wg * (H * 4);
+            if (C::KEYS) ok = mbar_wait(b_stat_full(j % C::STATS), (j / C::STATS) & 1, abort_flag);
             ok = __all_sync(0xffffffffu, ok && mbar_wait(b_s_full(j % SB), (j / SB) & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
@@ -522,6 +641,11 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int c = 0; c < H / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&pr[c * 32]));
             tmem_wait_ld();
+            if (!C::HAS_P) {  // the S buffer may be written again
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p_full(j % SB));
+            }
 #pragma unroll
             for (int e = 0; e < H; e += 4) {
                 float4 nl = make_float4(row_nl, row_nl, row_nl, row_nl);
@@ -594,6 +718,10 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_ds_full);
+            }
+            if (C::KEYS) {  // the statistics' buffer may be filled again
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_stat_empty(j % C::STATS));
             }
             if (++t == t_hi) t = t_lo;
         }
