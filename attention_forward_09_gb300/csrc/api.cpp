@@ -202,7 +202,7 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
     // Without rows (or keys) nothing of that side is ever loaded; its maps
     // then view the other side's tensor so that they are well-formed.
     CUtensorMap tq, tg, tk, tv;
-    const int box = gbattn::bwd_box_rows(D);
+    constexpr int box = 128;
     const long long rq = rows ? p.Tq : p.Tk, rk = keys ? p.Tk : p.Tq;
     const int hq = rows ? p.Hq : p.Hkv, hk = keys ? p.Hkv : p.Hq;
     if (!encode_rows_heads_d(&tq, rows ? q : k, rq, hq, D, box) || !encode_rows_heads_d(&tg, rows ? dout : v, rq, hq, D, box) ||

@@ -27,10 +27,9 @@
 // the forward kernels (at most 2^-8 of each term, independent of one another);
 // lse, delta, P in ds = p (dp - delta) and every sum are fp32.
 //
-// A resident tile is 128 rows (TMEM lanes); a streamed tile is BN = 128 rows,
-// 64 for D > 128 where the accumulators need the TMEM columns.  At D = 256 dV
-// and dK do not fit beside each other (2 x 256 columns): they are two
-// launches of the keys-resident kernel, one accumulator each.
+// Resident and streamed tiles are 128 rows.  Above D = 128 dV and dK do not fit
+// in TMEM beside the scores: they are two launches of the keys-resident
+// kernel, one accumulator each (eight products for five).
 //
 // Shared-memory layout and descriptors are those of the forward kernels: 64
 // column chunks of [rows x 128 B], 128-byte swizzle; a streamed tile is read
@@ -55,48 +54,56 @@ enum BwdMode {
 template <int D_, int MODE_>
 struct BwdCfg {
     static constexpr int D = D_, MODE = MODE_;
-    static constexpr int BM = 128;                    // resident rows
-    static constexpr int BN = D <= 128 ? 128 : 64;    // streamed rows
+    static constexpr int BM = 128, BN = 128;          // resident and streamed rows
     static constexpr bool KEYS = MODE != kBwdQ;       // keys resident, queries streamed
     static constexpr bool HAS_P = MODE == kBwdKV || MODE == kBwdV;  // sums dV
     static constexpr bool HAS_DS = MODE != kBwdV;     // needs dP; sums dK or dQ
-    static constexpr int ISSUERS = HAS_DS ? 2 : 1;    // warps that issue products
     static constexpr int ACCS = MODE == kBwdKV ? 2 : 1;
-    static constexpr int NCH = (D + 63) / 64;         // 64-column chunks
-    static constexpr int RES = HAS_DS ? 2 : 1;        // resident tiles: K (and V), or Q and dO
+    static constexpr int NCH = (D + 63) / 64;         // 64-column blocks of a tile
     static constexpr int R_BYTES = NCH * BM * 128;
-    static constexpr int C_BYTES = NCH * BN * 128;    // one streamed tile
-    // Residents held in tensor memory (bf16 pairs, D / 2 columns each) where
-    // there is room: S and dP then read one operand of two from shared memory,
-    // whose bandwidth otherwise equals the tensor core's need to the byte, and
-    // their room goes to the ring.
-    static constexpr bool RT = !KEYS && D <= 64;
-    static constexpr int STAT_BYTES = KEYS ? 2 * BN * 4 : 0;  // -lse log2 e, -delta of a streamed tile's rows
-    // TMEM: S buffers, dP, accumulators, residents.  A second S buffer where it
-    // fits lets the next scores be formed before the current ones are used up.
-    static constexpr int T_REST = (HAS_DS ? BN : 0) + ACCS * D + (RT ? D : 0);
-    static constexpr int SB = 2 * BN + T_REST <= 512 ? 2 : 1;
+    // A streamed tile comes in NCK chunks of CW columns, a slot of the ring each.
+    static constexpr int NCK = D == 256 ? 2 : 1, CW = D / NCK, CCH = NCH / NCK;
+    static constexpr int C_BYTES = CCH * BN * 128;
+    // Above D = 128 S, dP and the accumulator do not fit beside what else is
+    // needed: S and dP share their columns, and V (or dO) is held in tensor
+    // memory as bf16 pairs, which leaves the ring room for a tile ahead.
+    static constexpr bool SHARED = HAS_DS && D > 128;
+    // Residents in tensor memory: r >= RT0.
+    static constexpr int RT0 = SHARED ? 1 : (!KEYS && D == 64 ? 0 : 2);
+    static constexpr int RES = HAS_DS ? 2 : 1;        // resident tiles: K (and V), or Q and dO
+    static constexpr int RES_SMEM = RES < RT0 ? RES : RT0, RES_TMEM = RES - RES_SMEM;
+    static constexpr int G0 = RES_TMEM * NCK;         // the first ring's loads that bring those
+    // S and dP buffers.  Without dV the scores are free as soon as they have
+    // been read, and dP gets the second buffer; with it S does, where it fits.
+    static constexpr int DPB = HAS_DS && !HAS_P && !SHARED ? 2 : 1;
+    static constexpr int SB = HAS_P && (2 + (HAS_DS ? 1 : 0)) * BN + ACCS * D <= 512 ? 2 : 1;
     static constexpr int T_S = 0;
-    static constexpr int T_DP = SB * BN;
-    static constexpr int T_ACC = T_DP + (HAS_DS ? BN : 0);
+    static constexpr int T_DP = SHARED ? 0 : SB * BN;
+    static constexpr int T_ACC = T_DP + (HAS_DS ? DPB * BN : 0);
     static constexpr int T_RES = T_ACC + ACCS * D;
-    static constexpr int STATS = D <= 64 ? 4 : 2;     // buffers of them
-    static constexpr int BARS_FIXED = 11 + 2 * STATS;
-    static constexpr int ROOM = 232448 - (RT ? 0 : RES * R_BYTES) - STATS * STAT_BYTES - 16 - BARS_FIXED * 8;
+    static constexpr int ISSUERS = HAS_DS && !SHARED ? 2 : 1;  // warps that issue products
+    static constexpr int STAT_BYTES = KEYS ? 2 * BN * 4 : 0;   // -lse log2 e, -delta of a streamed tile's rows
+    static constexpr int STATS = D <= 64 ? 4 : 2;              // buffers of them
+    static constexpr int MATH_WARPS = 16;
+    static constexpr int THREADS = 32 * MATH_WARPS + 128;
+    static constexpr int BARS_FIXED = 16 + 2 * STATS;
+    static constexpr int ROOM = 232448 - RES_SMEM * R_BYTES - STATS * STAT_BYTES - 16 - BARS_FIXED * 8;
     static constexpr int FIT = ROOM / (C_BYTES + 16);
     static constexpr int SLOTS = FIT < 8 ? FIT : 8;
+    // Two rings, for C1 and C2, since one is released in another order than the
+    // other is needed.  dV alone uses a tile once each: one ring, in the order
+    // of use.
+    static constexpr int N2 = HAS_DS ? SLOTS * 2 / 5 : 0, N1 = SLOTS - N2;
     static constexpr int NUM_BARS = BARS_FIXED + 2 * SLOTS;
-    static constexpr int O_C = RT ? 0 : RES * R_BYTES;  // offsets in shared memory
+    static constexpr int O_C = RES_SMEM * R_BYTES;             // offsets in shared memory
     static constexpr int O_STAT = O_C + SLOTS * C_BYTES;
     static constexpr int O_BARS = O_STAT + STATS * STAT_BYTES;
     static constexpr int SMEM_BYTES = O_BARS + NUM_BARS * 8 + 16;
-    static constexpr int REG_MATH = 208, REG_OTHER = 88;  // setmaxnreg split of 384 x 168
-    static_assert(T_ACC + ACCS * D + (RT ? D : 0) <= 512, "TMEM budget");
+    static_assert(T_RES + RES_TMEM * D / 2 <= 512, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-    static_assert(!RT || (BM == BN && D % 32 == 0), "residents pass through the ring's slots");
-    static_assert(SLOTS >= 3, "C1 of the next step is needed before C1 and C2 of this one are released");
+    static_assert(!HAS_DS || (N2 >= NCK && N1 > NCK && N1 >= G0), "the rings hold what the issuing warps wait for at once");
     static_assert(SMEM_BYTES > 116 * 1024, "one CTA an SM: it takes all TMEM columns");
-    static_assert(2 * 128 * REG_MATH + 128 * REG_OTHER <= 384 * 168, "register split");
+    static_assert(NCH % NCK == 0 && D % 32 == 0 && (RES_TMEM == 0 || D % 64 == 0), "tile shape");
 };
 
 // One document's (or batch entry's) rows.
@@ -219,29 +226,35 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p) {
 }
 
 // ------------------------------------------------------------- the two passes
-// 384 threads:
-//   warps 0-3, 4-7  math: thread = one resident row (TMEM lane), each
-//                   warpgroup one half of a streamed tile's columns
-//   warp 8          TMA producer: resident tiles, then a ring of streamed
-//                   tiles in the order C1(0) C2(0) C1(1) ... (C1 = Q or K, C2
-//                   = dO or V)
-//   warp 9          TMEM allocator; issues S and dV
-//   warp 10         (keys resident) the streamed rows' statistics
-//   warp 11         issues dP and dK or dQ
-// Order of the products, one S buffer:
-//   warp 9:  S(0) | dV(0) S(1) | dV(1) S(2) | ...     after P(j) is there
-//   warp 11: dP(0) | dK(0) dP(1) | dK(1) dP(2) | ...  after dS(j) is there
-// The tensor core finishes what one thread issues in order, so S(j+1) over
-// P(j) and dP(j+1) over dS(j) need no wait of their own.  With two S buffers
-// S(j+1) comes first.
-// P and dS (bf16 pairs) are written over the half of the S or dP columns that
-// the same thread has read, so the two warpgroups need not meet.
+// 640 threads:
+//   warps 0-15  math, four warpgroups: thread = one resident row (TMEM lane) and
+//               32 of a streamed tile's 128 columns (four warps a scheduler,
+//               so that one's TMEM and exponential latencies hide another's)
+//   warp 16     TMA producer: resident tiles, then the tiles C1 (Q or K)
+//   warp 17     TMEM allocator; issues S and dV
+//   warp 18     TMA producer: the tiles C2 (dO or V), and with the keys resident
+//               the streamed rows' statistics
+//   warp 19     issues dP and dK or dQ
+// A product is issued about as fast as it runs, so what one issuing warp waits
+// the other's products fill; the tensor core finishes what one thread issues
+// in order.
+//   dV and dK, D <= 128: S(0) | dV(j) S(j+1) after P(j)  and  dP(0) | dK(j)
+//     dP(j+1) after dS(j).  With one S buffer the chain exponentials -> dV ->
+//     S -> exponentials is the longest, so dK(j) and dP(j+1) also wait until
+//     S(j+1) has been issued, and run beside the exponentials.
+//   dQ, D <= 128: S(j+1) once S(j) has been read; dP(j+1), then dQ(j) after dS(j).
+//   dV alone: S(j+1), then dV(j) after P(j).
+//   dK or dQ, D > 128, S and dP in the same columns: S(j) | dP(j) once S(j) has
+//     been read | after dS(j) the sum's product | S(j+1) ...
+// P and dS (bf16 pairs) are written over columns that the same thread has read,
+// so the warpgroups need not meet.
 template <class C>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(C::THREADS, 1)
     attn_bwd_sm103a(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const BwdParams p) {
-    constexpr int D = C::D, BM = C::BM, BN = C::BN, NCH = C::NCH, SLOTS = C::SLOTS, SB = C::SB, H = BN / 2;
+    constexpr int D = C::D, BM = C::BM, BN = C::BN, NCH = C::NCH, NCK = C::NCK, CCH = C::CCH, SLOTS = C::SLOTS;
+    constexpr int SB = C::SB, DPB = C::DPB, G0 = C::G0, MW = C::MATH_WARPS;
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles lie on 1024 bytes
     const uint32_t sR = smem_u32(smem);
     const uint32_t sC = sR + C::O_C;
@@ -251,11 +264,13 @@ __global__ void __launch_bounds__(384, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     auto b_res = [&](int r) { return smem_u32(&bars[r]); };
     auto b_s_full = [&](int b) { return smem_u32(&bars[2 + b]); };
-    auto b_p_full = [&](int b) { return smem_u32(&bars[4 + b]); };
-    const uint32_t b_dp_full = smem_u32(&bars[6]), b_ds_full = smem_u32(&bars[7]);
-    const uint32_t b_done = smem_u32(&bars[8]), b_drain = smem_u32(&bars[9]), b_res_in = smem_u32(&bars[10]);
-    auto b_stat_full = [&](int b) { return smem_u32(&bars[11 + b]); };
-    auto b_stat_empty = [&](int b) { return smem_u32(&bars[11 + C::STATS + b]); };
+    auto b_p_full = [&](int b) { return smem_u32(&bars[4 + b]); };  // P is there (without dV: S has been read)
+    auto b_dp_full = [&](int b) { return smem_u32(&bars[6 + b]); };
+    auto b_ds_full = [&](int b) { return smem_u32(&bars[8 + b]); };
+    auto b_turn = [&](int b) { return smem_u32(&bars[10 + b]); };
+    const uint32_t b_done = smem_u32(&bars[12]), b_drain = smem_u32(&bars[13]), b_res_in = smem_u32(&bars[14]);
+    auto b_stat_full = [&](int b) { return smem_u32(&bars[16 + b]); };
+    auto b_stat_empty = [&](int b) { return smem_u32(&bars[16 + C::STATS + b]); };
     auto b_full = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + s]); };
     auto b_empty = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + SLOTS + s]); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -308,20 +323,20 @@ __global__ void __launch_bounds__(384, 1)
 
     // ------------------------------------------------------------------ setup
     if (threadIdx.x == 0) {
-        mbar_init(b_res(0), 1);
-        mbar_init(b_res(1), 1);
-        mbar_init(b_s_full(0), 1);
-        mbar_init(b_s_full(1), 1);
-        mbar_init(b_dp_full, 1);
-        mbar_init(b_p_full(0), 8);
-        mbar_init(b_p_full(1), 8);
-        mbar_init(b_ds_full, 8);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(b_res(b), 1);
+            mbar_init(b_s_full(b), 1);
+            mbar_init(b_p_full(b), MW);
+            mbar_init(b_dp_full(b), 1);
+            mbar_init(b_ds_full(b), MW);
+            mbar_init(b_turn(b), 1);
+        }
         mbar_init(b_done, C::ISSUERS);
         mbar_init(b_drain, C::ISSUERS);
-        mbar_init(b_res_in, 8);
+        mbar_init(b_res_in, MW);
         for (int b = 0; b < C::STATS; ++b) {
             mbar_init(b_stat_full(b), 1);
-            mbar_init(b_stat_empty(b), 8);
+            mbar_init(b_stat_empty(b), MW);
         }
         for (int s = 0; s < SLOTS; ++s) {
             mbar_init(b_full(s), 1);
@@ -330,7 +345,7 @@ __global__ void __launch_bounds__(384, 1)
         *abort_flag = p.give_up ? 1 : 0;  // 1: give up every wait (failure-path test)
         fence_mbar_init();
     }
-    if (warp == 9) {
+    if (warp == MW + 1) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -340,60 +355,77 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
 
-    if (warp >= 8) {
-        regs_dec<C::REG_OTHER>();
-        if (warp == 8 && lane == 0 && n > 0) {
-            // -------------------------------------------------------- producer
-            const CUtensorMap *mR1 = C::KEYS ? &tmK : &tmQ, *mR2 = C::KEYS ? &tmV : &tmG;
-            const CUtensorMap *mC1 = C::KEYS ? &tmQ : &tmK, *mC2 = C::KEYS ? &tmG : &tmV;
-            const int res_head = head;
-            int str_head = C::KEYS ? head * p.group : head / p.group;
-            int slot = 0, issued = 0;
-            uint32_t ph = 1;  // parity of the slot's previous release; the first turn needs none
-            auto next = [&]() {
-                ++issued;
-                if (++slot == SLOTS) {
-                    slot = 0;
-                    ph ^= 1u;
-                }
-            };
-            for (int r = 0; r < C::RES; ++r) {
-                const uint32_t bar = C::RT ? b_full(slot) : b_res(r), to = C::RT ? sC + slot * C::C_BYTES : sR + r * C::R_BYTES;
-                mbar_arrive_expect_tx(bar, C::R_BYTES);
+    const CUtensorMap *mC1 = C::KEYS ? &tmQ : &tmK, *mC2 = C::KEYS ? &tmG : &tmV;
+    const int str_head = C::KEYS ? head * p.group : head / p.group;  // the first streamed head
+    // Slots [begin, begin + size) as a ring: load g is in slot begin + g % size.
+    struct Ring {
+        uint32_t base;  // shared memory of slot 0
+        int s, begin, size, issued;
+        uint32_t ph;    // parity of the slot's present turn
+        __device__ Ring(uint32_t b, int bg, int sz) : base(b), s(bg), begin(bg), size(sz), issued(0), ph(0) {}
+        __device__ void next() {
+            ++issued;
+            if (++s == begin + size) {
+                s = begin;
+                ph ^= 1u;
+            }
+        }
+    };
+    // Chunk of a tile into the ring's next slot, once that is free.
+    auto load = [&](Ring& r, const CUtensorMap* m, int h, int row, int chunk) -> bool {
+        if (r.issued >= r.size && !mbar_wait(b_empty(r.s), r.ph ^ 1u, abort_flag)) return false;
+        mbar_arrive_expect_tx(b_full(r.s), C::C_BYTES);
+        for (int c = 0; c < CCH; ++c)
+            tma_load_3d(r.base + r.s * C::C_BYTES + c * (BN * 128), m, b_full(r.s), (chunk * CCH + c) * 64, h, row);
+        r.next();
+        return true;
+    };
+    auto drain = [&](const Ring& r) {
+        for (int g = (r.issued > r.size ? r.issued - r.size : 0); g < r.issued; ++g)
+            mbar_wait_drain(b_full(r.begin + g % r.size), (g / r.size) & 1);
+    };
+    if (warp == MW && lane == 0 && n > 0) {
+        // ---------------------------------- producer: resident tiles, then C1
+        const CUtensorMap *mR1 = C::KEYS ? &tmK : &tmQ, *mR2 = C::KEYS ? &tmV : &tmG;
+        Ring ring(sC, 0, C::N1);
+        for (int r = 0; r < C::RES; ++r) {
+            const CUtensorMap* m = r ? mR2 : mR1;
+            if (r >= C::RT0) {
+                for (int c = 0; c < NCK; ++c) ok = ok && load(ring, m, head, res_start + r0, c);
+            } else {
+                mbar_arrive_expect_tx(b_res(r), C::R_BYTES);
                 for (int c = 0; c < NCH; ++c)
-                    for (int b = 0; b < BM / BN; ++b)
-                        tma_load_3d(to + c * (BM * 128) + b * (BN * 128), r ? mR2 : mR1, bar, c * 64, res_head,
-                                    res_start + r0 + b * BN);
-                if (C::RT) next();
+                    tma_load_3d(sR + r * C::R_BYTES + c * (BM * 128), m, b_res(r), c * 64, head, res_start + r0);
             }
-            int t = t_lo;
-            for (int j = 0; ok && j < n; ++j) {
-                for (int x = 0; x < 2; ++x) {
-                    if (issued >= SLOTS && !mbar_wait(b_empty(slot), ph, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(b_full(slot), C::C_BYTES);
-                    for (int c = 0; c < NCH; ++c)
-                        tma_load_3d(sC + slot * C::C_BYTES + c * (BN * 128), x ? mC2 : mC1, b_full(slot), c * 64,
-                                    str_head, str_start + t * BN);
-                    next();
-                }
-                if (++t == t_hi) {
-                    t = t_lo;
-                    ++str_head;
-                }
+        }
+        int t = t_lo, h = str_head;
+        for (int j = 0; ok && j < n; ++j) {
+            const int t2 = t, h2 = h;  // step j
+            if (++t == t_hi) {
+                t = t_lo;
+                ++h;
             }
-            if (!ok || *abort_flag) {
-                // Let every copy this thread started land before the CTA retires.
-                for (int r = 0; !C::RT && r < C::RES; ++r) mbar_wait_drain(b_res(r), 0);
-                for (int g = (issued > SLOTS ? issued - SLOTS : 0); g < issued; ++g)
-                    mbar_wait_drain(b_full(g % SLOTS), (g / SLOTS) & 1);
+            if (C::HAS_DS || j == 0)
+                for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC1, h2, str_start + t2 * BN, c);
+            if (!C::HAS_DS) {  // S(j + 1) comes before dV(j)
+                if (j + 1 < n)
+                    for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC1, h, str_start + t * BN, c);
+                for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h2, str_start + t2 * BN, c);
             }
-        } else if (C::KEYS && warp == 10 && lane == 0 && n > 0) {
-            // ------------------------------------ statistics of streamed rows
-            int h = head * p.group, t = t_lo, issued = 0;
-            for (int j = 0; j < n; ++j) {
+        }
+        if (!ok || *abort_flag) {
+            // Let every copy this thread started land before the CTA retires.
+            for (int r = 0; r < C::RES_SMEM; ++r) mbar_wait_drain(b_res(r), 0);
+            drain(ring);
+        }
+    } else if (warp == MW + 2 && lane == 0 && n > 0) {
+        // --------------------- producer: C2, and statistics of streamed rows
+        Ring ring(sC, C::N1, C::N2);
+        int t = t_lo, h = str_head, issued = 0;
+        for (int j = 0; ok && j < n; ++j) {
+            if (C::HAS_DS)
+                for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h, str_start + t * BN, c);
+            if (C::KEYS && ok) {
                 const int b = j % C::STATS;
                 if (j >= C::STATS && !(ok = mbar_wait(b_stat_empty(b), (j / C::STATS - 1) & 1, abort_flag))) break;
                 const long long at = h * p.stat_stride + bwd_stat_base(d.q_start, doc) + static_cast<long long>(t) * BN;
@@ -401,190 +433,280 @@ __global__ void __launch_bounds__(384, 1)
                 bulk_load(sStat + b * C::STAT_BYTES, p.neg_lse2 + at, BN * 4, b_stat_full(b));
                 bulk_load(sStat + b * C::STAT_BYTES + BN * 4, p.neg_delta + at, BN * 4, b_stat_full(b));
                 ++issued;
-                if (++t == t_hi) {
-                    t = t_lo;
-                    ++h;
-                }
             }
-            if (!ok || *abort_flag)
-                for (int g = (issued > C::STATS ? issued - C::STATS : 0); g < issued; ++g)
-                    mbar_wait_drain(b_stat_full(g % C::STATS), (g / C::STATS) & 1);
-        } else if ((warp == 9 || (warp == 11 && C::ISSUERS == 2)) && n > 0) {
-            // ------------------------------------------------------------- MMA
-            // Warp 9 issues S (and dV), warp 11 dP and dK or dQ: a product is
-            // issued about as fast as it runs, so what one warp waits the
-            // other's products fill.  Each walks its schedule as a whole warp;
-            // one elected lane issues.
-            constexpr uint32_t kIdS = idesc_bf16_f32(BM, BN, false, false);
-            constexpr uint32_t kIdA = idesc_bf16_f32(BM, D, false, true);
-            const bool leader = elect_one();
-            const uint64_t dR = sdesc_sw128(sR, 16, 1024);
-            const uint64_t dCk = sdesc_sw128(sC, 16, 1024);           // streamed tile, K-major
-            const uint64_t dCm = sdesc_sw128(sC, BN * 128, 1024);     // streamed tile, MN-major
-            auto wait_all = [&](uint32_t bar, uint32_t ph) {
-                return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag));
-            };
-            // Load g is in slot g % SLOTS: the residents first where they pass
-            // through the ring, then C1 and C2 of each step.
-            constexpr int G0 = C::RT ? C::RES : 0;
-            struct Slot {
-                int s;
-                uint32_t ph;
-                __device__ explicit Slot(int g) : s(g % SLOTS), ph((g / SLOTS) & 1) {}
-                __device__ void step() {  // the same operand's tile of the next step
-                    s += 2;
-                    if (s >= SLOTS) {
-                        s -= SLOTS;
-                        ph ^= 1u;
-                    }
-                }
-            };
-            // Rows of a streamed tile that no resident row may see at all (past
-            // the document, the neighbours' rows, or rows without a key) may
-            // hold anything; P and dS are 0 there but 0 * NaN is not, so the
-            // tile's rows are zeroed before the second product reads them.
-            auto edge_rows = [&](int t) {
-                return (t + 1) * BN > str_len || (C::KEYS && p.causal && t * BN < -diag);
-            };
-            auto zero_rows = [&](int s, int t) {
-                const int hi = min(BN, str_len - t * BN);
-                const int lo = (C::KEYS && p.causal) ? min(hi, max(0, -diag - t * BN)) : 0;
-                for (int x = lane; x < (lo + BN - hi) * NCH * 8; x += 32) {
-                    const int u = x & 7, rc = x >> 3, c = rc % NCH, r = rc / NCH;
-                    st_shared_v4(sC + s * C::C_BYTES + c * (BN * 128) + (r < lo ? r : hi + r - lo) * 128 + u * 16, 0u, 0u, 0u,
-                                 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-            };
-            // X (128 x BN) = resident r * streamed tile in slot s
-            auto scores = [&](uint32_t to, int r, int s) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const int c = k >> 2, kk = k & 3;
-                    const uint64_t b = dCk + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((c * BN * 128 + kk * 32) >> 4);
-                    if constexpr (C::RT)
-                        mma_bf16_ts(tmem + to, tmem + C::T_RES + r * (D / 2) + k * 8, b, kIdS, k > 0 ? 1u : 0u);
-                    else
-                        mma_bf16_ss(tmem + to, dR + ((r * C::R_BYTES + c * BM * 128 + kk * 32) >> 4), b, kIdS,
-                                    k > 0 ? 1u : 0u);
-                }
-            };
-            // acc += A (bf16 pairs over X's columns, a half for each warpgroup) * streamed tile in slot s
-            auto accumulate = [&](uint32_t acc, uint32_t a, int s, bool first) {
-#pragma unroll
-                for (int k = 0; k < BN / 16; ++k)
-                    mma_bf16_ts(tmem + acc, tmem + a + (k < BN / 32 ? k * 8 : H + (k - BN / 32) * 8),
-                                dCm + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((k * 16 * 128) >> 4), kIdA,
-                                (!first || k > 0) ? 1u : 0u);
-            };
-            ok = !*abort_flag;  // a launch told to give up issues nothing
-            if (C::RT) {  // the math warps have copied the residents into tensor memory
-                ok = ok && wait_all(b_res_in, 0);
-                if (ok && lane == 0) {
-                    mbar_arrive(b_empty(0));
-                    mbar_arrive(b_empty(1));
-                }
-                __syncwarp();
-            } else {
-                ok = ok && wait_all(b_res(warp == 9 ? 0 : 1), 0);
+            if (++t == t_hi) {
+                t = t_lo;
+                ++h;
             }
-            Slot c1(G0), c2(G0 + 1);
-            int t = t_lo;
-            if (warp == 9) {
-                Slot c1n = c1;  // C1 of the step whose S comes next
-                auto issue_s = [&](int j) {
-                    scores(C::T_S + (j % SB) * BN, 0, c1n.s);
-                    mma_commit(b_empty(c1n.s));
-                    mma_commit(b_s_full(j % SB));
-                };
-                ok = ok && wait_all(b_full(c1n.s), c1n.ph);
-                if (ok) {
-                    tc_fence_after();
-                    if (leader) issue_s(0);
-                    __syncwarp();
-                }
-                for (int j = 0; ok && j < n; ++j) {
-                    const bool more = j + 1 < n;
-                    c1n.step();
-                    if (more && !(ok = wait_all(b_full(c1n.s), c1n.ph))) break;
-                    // With a second buffer S_{j+1} need not wait for P_j: step
-                    // j - 1's scores have been used up (dV_{j-1} was issued
-                    // here, or the math warps have said so).
-                    if (SB == 2 && C::HAS_P) {
-                        tc_fence_after();
-                        if (more && leader) issue_s(j + 1);
-                        __syncwarp();
-                    }
-                    if (C::HAS_P) {
-                        if (!(ok = wait_all(b_full(c2.s), c2.ph))) break;
-                        if (edge_rows(t)) zero_rows(c2.s, t);
-                    }
-                    // P_j is there; without dV: S_j, or of two buffers S_{j-1}, has been read
-                    const int w = C::HAS_P || SB == 1 ? j : j - 1;
-                    if (w >= 0 && !(ok = wait_all(b_p_full(w % SB), (w / SB) & 1))) break;
-                    tc_fence_after();
-                    if (leader) {
-                        if (C::HAS_P) {
-                            accumulate(C::T_ACC, C::T_S + (j % SB) * BN, c2.s, j == 0);
-                            mma_commit(b_empty(c2.s));
-                        }
-                        if (more && (SB == 1 || !C::HAS_P)) issue_s(j + 1);
-                    }
-                    __syncwarp();
-                    c2.step();
-                    if (++t == t_hi) t = t_lo;
-                }
-            } else {
-                constexpr uint32_t kAcc = C::T_ACC + (C::HAS_P ? D : 0);
-                Slot c2n = c2;  // C2 of the step whose dP comes next
-                auto issue_dp = [&]() {
-                    scores(C::T_DP, 1, c2n.s);
-                    mma_commit(b_empty(c2n.s));
-                    if (!C::HAS_P) mma_commit(b_empty(c2n.s));  // (a slot is released twice)
-                    mma_commit(b_dp_full);
-                };
-                ok = ok && wait_all(b_full(c2n.s), c2n.ph);
-                if (ok) {
-                    tc_fence_after();
-                    if (leader) issue_dp();
-                    __syncwarp();
-                }
-                for (int j = 0; ok && j < n; ++j) {
-                    const bool more = j + 1 < n;
-                    c2n.step();
-                    if (edge_rows(t)) {
-                        if (!(ok = wait_all(b_full(c1.s), c1.ph))) break;
-                        zero_rows(c1.s, t);
-                    }
-                    // (with three slots C2 of the next step comes into the slot of C1 of this one)
-                    if (SLOTS > 3 && more && !(ok = wait_all(b_full(c2n.s), c2n.ph))) break;
-                    if (!(ok = wait_all(b_ds_full, j & 1))) break;
-                    tc_fence_after();
-                    if (leader) {
-                        accumulate(kAcc, C::T_DP, c1.s, j == 0);
-                        mma_commit(b_empty(c1.s));
-                        if (SLOTS > 3 && more) issue_dp();
-                    }
-                    __syncwarp();
-                    if (SLOTS == 3 && more) {
-                        if (!(ok = wait_all(b_full(c2n.s), c2n.ph))) break;
-                        tc_fence_after();
-                        if (leader) issue_dp();
-                        __syncwarp();
-                    }
-                    c1.step();
-                    if (++t == t_hi) t = t_lo;
-                }
-            }
-            if (ok && leader) mma_commit(b_done);
-            // Everything issued above must finish before TMEM is released.
-            if (leader) mma_commit(b_drain);
-            __syncwarp();
-            mbar_wait_drain(b_drain, 0);
         }
-    } else {
-        regs_inc<C::REG_MATH>();
+        if (!ok || *abort_flag) {
+            drain(ring);
+            for (int g = (issued > C::STATS ? issued - C::STATS : 0); g < issued; ++g)
+                mbar_wait_drain(b_stat_full(g % C::STATS), (g / C::STATS) & 1);
+        }
+    } else if ((warp == MW + 1 || (warp == MW + 3 && C::ISSUERS == 2)) && n > 0) {
+        // ----------------------------------------------------------------- MMA
+        // Each issuing warp walks its schedule as a whole; one elected lane issues.
+        constexpr uint32_t kIdS = idesc_bf16_f32(BM, BN, false, false);
+        constexpr uint32_t kIdA = idesc_bf16_f32(BM, C::CW, false, true);
+        const bool first_warp = warp == MW + 1;
+        const bool leader = elect_one();
+        const uint64_t dR = sdesc_sw128(sR, 16, 1024);
+        const uint64_t dCk = sdesc_sw128(sC, 16, 1024);           // streamed chunk, K-major
+        const uint64_t dCm = sdesc_sw128(sC, BN * 128, 1024);     // streamed chunk, MN-major
+        auto wait_all = [&](uint32_t bar, uint32_t ph) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag));
+        };
+        // Rows of a streamed tile that no resident row may see at all (past the
+        // document, the neighbours' rows, or rows without a key) may hold
+        // anything; P and dS are 0 there but 0 * NaN is not, so they are zeroed
+        // before the second product reads them.
+        auto edge_rows = [&](int t) { return (t + 1) * BN > str_len || (C::KEYS && p.causal && t * BN < -diag); };
+        auto zero_rows = [&](int s, int t) {
+            const int hi = min(BN, str_len - t * BN);
+            const int lo = (C::KEYS && p.causal) ? min(hi, max(0, -diag - t * BN)) : 0;
+            for (int x = lane; x < (lo + BN - hi) * CCH * 8; x += 32) {
+                const int u = x & 7, rc = x >> 3, c = rc % CCH, r = rc / CCH;
+                st_shared_v4(sC + s * C::C_BYTES + c * (BN * 128) + (r < lo ? r : hi + r - lo) * 128 + u * 16, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        // X (128 x BN) (+)= resident r * chunk c of a streamed tile, in slot s
+        auto scores = [&](uint32_t to, int r, int c, int s) {
+#pragma unroll
+            for (int k = 0; k < C::CW / 16; ++k) {
+                const int blk = k >> 2, kk = k & 3;
+                const uint64_t b = dCk + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((blk * BN * 128 + kk * 32) >> 4);
+                const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u;
+                if (r >= C::RT0)
+                    mma_bf16_ts(tmem + to, tmem + C::T_RES + (r - C::RT0) * (D / 2) + c * (C::CW / 2) + k * 8, b, kIdS, acc);
+                else
+                    mma_bf16_ss(tmem + to, dR + ((r * C::R_BYTES + (c * CCH + blk) * BM * 128 + kk * 32) >> 4), b, kIdS, acc);
+            }
+        };
+        // columns [c CW, (c + 1) CW) of acc += A (bf16 pairs in X's columns, 16
+        // of each warpgroup's 32) * chunk c of a streamed tile, in slot s
+        auto accumulate = [&](uint32_t acc, uint32_t a, int c, int s, bool first) {
+#pragma unroll
+            for (int k = 0; k < BN / 16; ++k)
+                mma_bf16_ts(tmem + acc + c * C::CW, tmem + a + (k >> 1) * 32 + (k & 1) * 8,
+                            dCm + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((k * 16 * 128) >> 4), kIdA,
+                            (!first || k > 0) ? 1u : 0u);
+        };
+        ok = !*abort_flag;  // a launch told to give up issues nothing
+        if (C::RES_TMEM > 0) {  // the math warps have copied those residents into tensor memory
+            ok = ok && wait_all(b_res_in, 0);
+            if (ok && lane == 0)
+                for (int g = 0; g < G0; ++g) mbar_arrive(b_empty(g));
+            __syncwarp();
+        }
+        // Cursors: the next chunk of C1 and of C2 that this warp uses (the
+        // first ring begins with the residents' G0).
+        Ring c1(sC, 0, C::N1), c2(sC, C::N1, C::N2);
+        for (int g = 0; g < G0; ++g) c1.next();
+        auto moved = [](Ring r) {
+            for (int c = 0; c < NCK; ++c) r.next();
+            return r;
+        };
+        int t = t_lo;
+        // All of a tile's chunks have landed.
+        auto landed = [&](Ring s) -> bool {
+            for (int c = 0; c < NCK; ++c) {
+                if (!wait_all(b_full(s.s), s.ph)) return false;
+                s.next();
+            }
+            return true;
+        };
+        // S of a step from C1's chunks, released once read when `free_c1`.
+        auto issue_s = [&](int j, Ring s, bool free_c1) {
+            for (int c = 0; c < NCK; ++c) {
+                scores(C::T_S + (j % SB) * BN, 0, c, s.s);
+                if (free_c1) mma_commit(b_empty(s.s));
+                s.next();
+            }
+            mma_commit(b_s_full(j % SB));
+        };
+        if constexpr (C::SHARED) {
+            // ---------------------------------- S and dP in the same columns
+            ok = ok && wait_all(b_res(0), 0) && landed(c1);
+            if (ok) {
+                tc_fence_after();
+                if (leader) issue_s(0, c1, false);
+                __syncwarp();
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                if (!(ok = landed(c2) && wait_all(b_p_full(0), j & 1))) break;
+                tc_fence_after();
+                if (leader) {
+                    Ring s = c2;
+                    for (int c = 0; c < NCK; ++c) {
+                        scores(C::T_DP, 1, c, s.s);
+                        mma_commit(b_empty(s.s));
+                        s.next();
+                    }
+                    mma_commit(b_dp_full(0));
+                }
+                __syncwarp();
+                c2 = moved(c2);
+                if (edge_rows(t)) {
+                    Ring s = c1;
+                    for (int c = 0; c < NCK; ++c) {
+                        zero_rows(s.s, t);
+                        s.next();
+                    }
+                }
+                if (!(ok = wait_all(b_ds_full(0), j & 1))) break;
+                tc_fence_after();
+                if (leader) {
+                    Ring s = c1;
+                    for (int c = 0; c < NCK; ++c) {
+                        accumulate(C::T_ACC, C::T_DP, c, s.s, j == 0);
+                        mma_commit(b_empty(s.s));
+                        s.next();
+                    }
+                }
+                __syncwarp();
+                c1 = moved(c1);
+                // (chunk by chunk: the last ones come into the slots released just now)
+                if (j + 1 < n) {
+                    Ring s = c1;
+                    for (int c = 0; c < NCK; ++c) {
+                        if (!(ok = wait_all(b_full(s.s), s.ph))) break;
+                        tc_fence_after();
+                        if (leader) {
+                            scores(C::T_S, 0, c, s.s);
+                            if (c == NCK - 1) mma_commit(b_s_full(0));
+                        }
+                        __syncwarp();
+                        s.next();
+                    }
+                }
+                if (++t == t_hi) t = t_lo;
+            }
+        } else if constexpr (!C::HAS_DS) {
+            // ---------------------------------------------------- dV alone
+            ok = ok && wait_all(b_res(0), 0) && landed(c1);
+            if (ok) {
+                tc_fence_after();
+                if (leader) issue_s(0, c1, true);
+                __syncwarp();
+            }
+            c1 = moved(c1);
+            for (int j = 0; ok && j < n; ++j) {
+                if (j + 1 < n) {
+                    if (!(ok = landed(c1))) break;
+                    tc_fence_after();
+                    if (leader) issue_s(j + 1, c1, true);
+                    __syncwarp();
+                    c1 = moved(c1);
+                }
+                if (!(ok = landed(c1))) break;  // dout's tile of step j
+                if (edge_rows(t)) {
+                    Ring s = c1;
+                    for (int c = 0; c < NCK; ++c) {
+                        zero_rows(s.s, t);
+                        s.next();
+                    }
+                }
+                if (!(ok = wait_all(b_p_full(j % SB), (j / SB) & 1))) break;
+                tc_fence_after();
+                if (leader) {
+                    Ring s = c1;
+                    for (int c = 0; c < NCK; ++c) {
+                        accumulate(C::T_ACC, C::T_S + (j % SB) * BN, c, s.s, j == 0);
+                        mma_commit(b_empty(s.s));
+                        s.next();
+                    }
+                }
+                __syncwarp();
+                c1 = moved(c1);
+                if (++t == t_hi) t = t_lo;
+            }
+        } else if (first_warp) {
+            // -------------------------------------------------- S (and dV)
+            if (C::RT0 > 0) ok = ok && wait_all(b_res(0), 0);
+            ok = ok && wait_all(b_full(c1.s), c1.ph);
+            if (ok) {
+                tc_fence_after();
+                if (leader) issue_s(0, c1, true);
+                __syncwarp();
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                const bool more = j + 1 < n;
+                c1.next();
+                if (more && !(ok = wait_all(b_full(c1.s), c1.ph))) break;
+                if (SB == 2) {  // dV(j - 1), which read the buffer, was issued here
+                    tc_fence_after();
+                    if (more && leader) issue_s(j + 1, c1, true);
+                    __syncwarp();
+                }
+                if (C::HAS_P) {
+                    if (!(ok = wait_all(b_full(c2.s), c2.ph))) break;
+                    if (edge_rows(t)) zero_rows(c2.s, t);
+                }
+                if (!(ok = wait_all(b_p_full(j % SB), (j / SB) & 1))) break;
+                tc_fence_after();
+                if (leader) {
+                    if (C::HAS_P) {
+                        accumulate(C::T_ACC, C::T_S + (j % SB) * BN, 0, c2.s, j == 0);
+                        mma_commit(b_empty(c2.s));
+                    }
+                    if (more && SB == 1) issue_s(j + 1, c1, true);
+                    if (C::HAS_P && SB == 1) mbar_arrive(b_turn(j & 1));
+                }
+                __syncwarp();
+                c2.next();
+                if (++t == t_hi) t = t_lo;
+            }
+        } else {
+            // --------------------------------------------- dP and dK or dQ
+            constexpr uint32_t kAcc = C::T_ACC + (C::HAS_P ? D : 0);
+            auto issue_dp = [&](int j) {
+                scores(C::T_DP + (j % DPB) * BN, 1, 0, c2.s);
+                mma_commit(b_empty(c2.s));
+                if (!C::HAS_P) mma_commit(b_empty(c2.s));  // (a slot is released twice)
+                mma_commit(b_dp_full(j % DPB));
+            };
+            if (C::RT0 > 1) ok = ok && wait_all(b_res(1), 0);
+            ok = ok && wait_all(b_full(c2.s), c2.ph);
+            if (ok) {
+                tc_fence_after();
+                if (leader) issue_dp(0);
+                __syncwarp();
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                const bool more = j + 1 < n;
+                c2.next();
+                if (edge_rows(t)) {
+                    if (!(ok = wait_all(b_full(c1.s), c1.ph))) break;
+                    zero_rows(c1.s, t);
+                }
+                if (more && !(ok = wait_all(b_full(c2.s), c2.ph))) break;
+                if (DPB == 2) {  // the product that read the buffer's dS(j - 1) was issued here
+                    tc_fence_after();
+                    if (more && leader) issue_dp(j + 1);
+                    __syncwarp();
+                }
+                if (!(ok = wait_all(b_ds_full(j % DPB), (j / DPB) & 1))) break;
+                if (C::HAS_P && SB == 1 && !(ok = wait_all(b_turn(j & 1), (j >> 1) & 1))) break;
+                tc_fence_after();
+                if (leader) {
+                    accumulate(kAcc, C::T_DP + (j % DPB) * BN, 0, c1.s, j == 0);
+                    mma_commit(b_empty(c1.s));
+                    if (more && DPB == 1) issue_dp(j + 1);
+                }
+                __syncwarp();
+                c1.next();
+                if (++t == t_hi) t = t_lo;
+            }
+        }
+        if (ok && leader) mma_commit(b_done);
+        // Everything issued above must finish before TMEM is released.
+        if (leader) mma_commit(b_drain);
+        __syncwarp();
+        mbar_wait_drain(b_drain, 0);
+    } else if (warp < MW) {
         // ---------------------------------------------------------------- math
         const int wg = warp >> 2;
         const int r = (warp & 3) * 32 + lane;   // resident row within the tile == TMEM lane
@@ -597,22 +719,25 @@ __global__ void __launch_bounds__(384, 1)
             row_nl = p.neg_lse2[at];
             row_nd = p.neg_delta[at];
         }
-        if (C::RT && n > 0) {
-            // warpgroup w copies resident w from slot w of the ring into tensor memory
-            ok = __all_sync(0xffffffffu, mbar_wait(b_full(wg), 0, abort_flag));
-            if (ok) {
-                const uint32_t src = sC + wg * C::C_BYTES + r * 128;
+        if (C::RES_TMEM > 0 && n > 0) {
+            // residents that go to tensor memory: a warpgroup copies every fourth 64-column block
+            for (int b = wg; ok && b < C::RES_TMEM * NCH; b += 4) {
+                const int s = b / CCH;  // the slot: blocks lie in the order they were loaded
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_full(s), 0, abort_flag)))) break;
+                const uint32_t src = sC + s * C::C_BYTES + (b % CCH) * (BM * 128) + r * 128;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
+                for (int h = 0; h < 2; ++h) {
                     uint32_t w[16];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        const float4 x = ld_shared_f4(src + (c >> 1) * (BM * 128) + (((((c & 1) << 2) + u) ^ (r & 7)) << 4));
+                        const float4 x = ld_shared_f4(src + (((h * 4 + u) ^ (r & 7)) << 4));
                         w[4 * u] = __float_as_uint(x.x), w[4 * u + 1] = __float_as_uint(x.y);
                         w[4 * u + 2] = __float_as_uint(x.z), w[4 * u + 3] = __float_as_uint(x.w);
                     }
-                    tmem_st16(tl + C::T_RES + wg * (D / 2) + c * 16, w);
+                    tmem_st16(tl + C::T_RES + b * 32 + h * 16, w);
                 }
+            }
+            if (ok) {
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -621,8 +746,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         int t = t_lo;
         for (int j = 0; ok && j < n; ++j) {
-            const int c0 = t * BN + wg * H;  // this thread's first streamed row
-            // columns [lo, hi) of the thread's H are visible
+            const int c0 = t * BN + wg * 32;  // this thread's first streamed row
+            // columns [lo, hi) of the thread's 32 are visible
             int lo = 0, hi = str_len - c0;
             if (p.causal) {
                 if (C::KEYS)
@@ -630,27 +755,26 @@ __global__ void __launch_bounds__(384, 1)
                 else
                     hi = min(hi, row + diag + 1 - c0);
             }
-            const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < H);
-            const uint32_t st = sStat + (j % C::STATS) * C::STAT_BYTES + wg * (H * 4);
+            const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < 32);
+            const uint32_t st = sStat + (j % C::STATS) * C::STAT_BYTES + wg * (32 * 4);
             if (C::KEYS) ok = mbar_wait(b_stat_full(j % C::STATS), (j / C::STATS) & 1, abort_flag);
             ok = __all_sync(0xffffffffu, ok && mbar_wait(b_s_full(j % SB), (j / SB) & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t tS = tl + C::T_S + (j % SB) * BN + wg * H, tDP = tl + C::T_DP + wg * H;
-            uint32_t pr[H];  // P, fp32
-#pragma unroll
-            for (int c = 0; c < H / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&pr[c * 32]));
+            const uint32_t tS = tl + C::T_S + (j % SB) * BN + wg * 32, tDP = tl + C::T_DP + (j % DPB) * BN + wg * 32;
+            uint32_t pr[32];  // P, fp32
+            tmem_ld32(tS, pr);
             tmem_wait_ld();
             if (!C::HAS_P) {  // the S buffer may be written again
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_p_full(j % SB));
             }
+            const float2 cc = make_float2(c2, c2);
 #pragma unroll
-            for (int e = 0; e < H; e += 4) {
+            for (int e = 0; e < 32; e += 4) {
                 float4 nl = make_float4(row_nl, row_nl, row_nl, row_nl);
                 if (C::KEYS) nl = ld_shared_f4(st + e * 4);
-                const float2 cc = make_float2(c2, c2);
                 const float2 a = __ffma2_rn(make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])), cc,
                                             make_float2(nl.x, nl.y));
                 const float2 b = __ffma2_rn(make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])), cc,
@@ -662,32 +786,27 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (edge) {
 #pragma unroll
-                for (int e = 0; e < H; ++e)
+                for (int e = 0; e < 32; ++e)
                     if (e < lo || e >= hi) pr[e] = 0u;
             }
             if (C::HAS_P) {
+                uint32_t pk[16];
 #pragma unroll
-                for (int c = 0; c < H / 32; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pk[e] = pack_bf16x2(__uint_as_float(pr[c * 32 + 2 * e]), __uint_as_float(pr[c * 32 + 2 * e + 1]));
-                    tmem_st16(tS + c * 16, pk);
-                }
+                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(__uint_as_float(pr[2 * e]), __uint_as_float(pr[2 * e + 1]));
+                tmem_st16(tS, pk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_p_full(j % SB));
             }
             if (C::HAS_DS) {
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_dp_full, j & 1, abort_flag)))) break;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_dp_full(j % DPB), (j / DPB) & 1, abort_flag)))) break;
                 tc_fence_after();
-                uint32_t dp[H];
-#pragma unroll
-                for (int c = 0; c < H / 32; ++c) tmem_ld32(tDP + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&dp[c * 32]));
+                uint32_t dp[32];
+                tmem_ld32(tDP, dp);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < H; e += 4) {
+                for (int e = 0; e < 32; e += 4) {
                     float4 nd = make_float4(row_nd, row_nd, row_nd, row_nd);
                     if (C::KEYS) nd = ld_shared_f4(st + BN * 4 + e * 4);
                     float2 a = __fadd2_rn(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
@@ -703,21 +822,17 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 if (edge) {  // 0 * (anything) is not always 0
 #pragma unroll
-                    for (int e = 0; e < H; ++e)
+                    for (int e = 0; e < 32; ++e)
                         if (e < lo || e >= hi) dp[e] = 0u;
                 }
+                uint32_t pk[16];
 #pragma unroll
-                for (int c = 0; c < H / 32; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pk[e] = pack_bf16x2(__uint_as_float(dp[c * 32 + 2 * e]), __uint_as_float(dp[c * 32 + 2 * e + 1]));
-                    tmem_st16(tDP + c * 16, pk);
-                }
+                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1]));
+                tmem_st16(tDP, pk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_ds_full);
+                if (lane == 0) mbar_arrive(b_ds_full(j % DPB));
             }
             if (C::KEYS) {  // the statistics' buffer may be filled again
                 __syncwarp();
@@ -731,19 +846,19 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
         }
         // ------------------------------------------------------------ epilogue
-        // Two accumulators: one a warpgroup.  One: the 32-column chunks in turn.
+        // Every fourth 32-column chunk of the accumulators is a warpgroup's.
         if (ok) {
             const bool used = n > 0 && row < res_len;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                if (C::ACCS == 1 && (c & 1) != wg) continue;
+            for (int x = wg; x < C::ACCS * (D / 32); x += 4) {
+                const int c = x % (D / 32);
                 uint32_t o[32];
                 if (n > 0) {
-                    tmem_ld32(tl + C::T_ACC + (C::ACCS == 2 ? wg * D : 0) + c * 32, o);
+                    tmem_ld32(tl + C::T_ACC + x * 32, o);
                     tmem_wait_ld();
                 }
                 if (row < res_all) {
-                    const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && wg == 0);
+                    const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && x < D / 32);
                     const float f = is_dv ? 1.f : p.scale;
                     void* base = C::KEYS ? (is_dv ? p.dv : p.dk) : p.dq;
                     uint16_t* dst = static_cast<uint16_t*>(base) +
@@ -752,8 +867,8 @@ __global__ void __launch_bounds__(384, 1)
                     for (int e = 0; e < 32; e += 8) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            w[x] = used ? pack_bf16x2(__uint_as_float(o[e + 2 * x]) * f, __uint_as_float(o[e + 2 * x + 1]) * f)
+                        for (int y = 0; y < 4; ++y)
+                            w[y] = used ? pack_bf16x2(__uint_as_float(o[e + 2 * y]) * f, __uint_as_float(o[e + 2 * y + 1]) * f)
                                         : 0u;
                         st_global_v4(dst + e, w[0], w[1], w[2], w[3]);
                     }
@@ -769,15 +884,13 @@ __global__ void __launch_bounds__(384, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == MW + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
 }
 
 // ------------------------------------------------------------------- launches
-int bwd_box_rows(int D) { return D <= 128 ? 128 : 64; }
-
 long long bwd_stat_stride(long long Tq, int num_docs) {
     // rows, the documents' alignment, and a last tile that is read whole
     return ((Tq + 4ll * num_docs + 3) & ~3ll) + 128;
@@ -793,7 +906,7 @@ cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmG, const CU
     if (items == 0) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(attn_bwd_sm103a<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    attn_bwd_sm103a<C><<<static_cast<unsigned>(items), 384, C::SMEM_BYTES, stream>>>(tmQ, tmG, tmK, tmV, p);
+    attn_bwd_sm103a<C><<<static_cast<unsigned>(items), C::THREADS, C::SMEM_BYTES, stream>>>(tmQ, tmG, tmK, tmV, p);
     return cudaGetLastError();
 }
 
@@ -812,7 +925,7 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUten
         if (e != cudaSuccess) return e;
     }
     cudaError_t e;
-    if constexpr (D <= 192) {
+    if constexpr (D <= 128) {
         e = launch_pass<BwdCfg<D, kBwdKV>>(tmQ, tmG, tmK, tmV, p, stream);
     } else {
         e = launch_pass<BwdCfg<D, kBwdV>>(tmQ, tmG, tmK, tmV, p, stream);

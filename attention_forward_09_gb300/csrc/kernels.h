@@ -342,9 +342,8 @@ struct BwdParams {
     int lse_row_global;
     int give_up;            // as PrefillParams
 };
-int bwd_box_rows(int D);  // rows of the tensor maps' boxes
 long long bwd_stat_stride(long long Tq, int num_docs);
-// tmQ, tmG (dout), tmK, tmV: [rows, heads, D] bf16, box {64, 1, bwd_box_rows(D)}, 128-byte swizzle.
+// tmQ, tmG (dout), tmK, tmV: [rows, heads, D] bf16, box {64, 1, 128}, 128-byte swizzle.
 cudaError_t launch_bwd(int D, const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK,
                        const CUtensorMap& tmV, const BwdParams& p, cudaStream_t stream);
 
