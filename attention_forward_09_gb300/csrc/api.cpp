@@ -208,7 +208,7 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
     if (!encode_rows_heads_d(&tq, rows ? q : k, rq, hq, D, box) || !encode_rows_heads_d(&tg, rows ? dout : v, rq, hq, D, box) ||
         !encode_rows_heads_d(&tk, keys ? k : q, rk, hk, D, box) || !encode_rows_heads_d(&tv, keys ? v : dout, rk, hk, D, box))
         return GBATTN_ERR_CUDA;
-    return gbattn::launch_bwd(D, tq, tg, tk, tv, p, st) == cudaSuccess ? GBATTN_OK : GBATTN_ERR_CUDA;
+    return gbattn::launch_bwd(D, tq, tg, tk, tv, p, di.sms, st) == cudaSuccess ? GBATTN_OK : GBATTN_ERR_CUDA;
 }
 
 // What the two calls on rotary positions have in common; `p` comes with their sizes.

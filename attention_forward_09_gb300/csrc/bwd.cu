@@ -35,6 +35,7 @@
 // column chunks of [rows x 128 B], 128-byte swizzle; a streamed tile is read
 // K-major by S / dP and MN-major by the second products.
 #include <math.h>
+#include <stddef.h>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -81,13 +82,16 @@ struct BwdCfg {
     static constexpr int T_DP = SHARED ? 0 : SB * BN;
     static constexpr int T_ACC = T_DP + (HAS_DS ? DPB * BN : 0);
     static constexpr int T_RES = T_ACC + ACCS * D;
-    static constexpr int ISSUERS = HAS_DS && !SHARED ? 2 : 1;  // warps that issue products
+    static constexpr int ISSUERS = SHARED ? 1 : 2;    // warps that issue products
     static constexpr int STAT_BYTES = KEYS ? 2 * BN * 4 : 0;   // -lse log2 e, -delta of a streamed tile's rows
     static constexpr int STATS = D <= 64 ? 4 : 2;              // buffers of them
-    static constexpr int MATH_WARPS = 16;
+    static constexpr int MATH_WARPS = 8, MATH_WGS = MATH_WARPS / 4, H = BN / MATH_WGS;  // H columns a thread
+    static constexpr int REG_MATH = 208, REG_OTHER = 88;       // setmaxnreg split of 384 x 168
     static constexpr int THREADS = 32 * MATH_WARPS + 128;
-    static constexpr int BARS_FIXED = 16 + 2 * STATS;
-    static constexpr int ROOM = 232448 - RES_SMEM * R_BYTES - STATS * STAT_BYTES - 16 - BARS_FIXED * 8;
+    static constexpr int ITEMS = 3;                            // items published ahead
+    static constexpr int BARS_FIXED = 18 + 2 * ITEMS + 2 * STATS;
+    static constexpr int RELEASES = HAS_DS && !SHARED ? 2 : 1;  // commits that release a slot
+    static constexpr int ROOM = 232448 - RES_SMEM * R_BYTES - STATS * STAT_BYTES - 16 - ITEMS * 64 - BARS_FIXED * 8;
     static constexpr int FIT = ROOM / (C_BYTES + 16);
     static constexpr int SLOTS = FIT < 8 ? FIT : 8;
     // Two rings, for C1 and C2, since one is released in another order than the
@@ -98,7 +102,8 @@ struct BwdCfg {
     static constexpr int O_C = RES_SMEM * R_BYTES;             // offsets in shared memory
     static constexpr int O_STAT = O_C + SLOTS * C_BYTES;
     static constexpr int O_BARS = O_STAT + STATS * STAT_BYTES;
-    static constexpr int SMEM_BYTES = O_BARS + NUM_BARS * 8 + 16;
+    static constexpr int SMEM_BYTES = O_BARS + NUM_BARS * 8 + 16 + ITEMS * 64;
+    static_assert(MATH_WARPS * 32 * REG_MATH + 128 * REG_OTHER <= THREADS * 168, "register split");
     static_assert(T_RES + RES_TMEM * D / 2 <= 512, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
     static_assert(!HAS_DS || (N2 >= NCK && N1 > NCK && N1 >= G0), "the rings hold what the issuing warps wait for at once");
@@ -159,6 +164,32 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
         "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// The products with descriptors given by their lower words: the upper one is
+// the same for every operand here (8-row groups 1024 bytes apart, 128-byte
+// swizzle; sdesc_sw128).  Half the registers of whole descriptors.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+    return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
         : "memory");
 }
 
@@ -226,15 +257,14 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p) {
 }
 
 // ------------------------------------------------------------- the two passes
-// 640 threads:
-//   warps 0-15  math, four warpgroups: thread = one resident row (TMEM lane) and
-//               32 of a streamed tile's 128 columns (four warps a scheduler,
-//               so that one's TMEM and exponential latencies hide another's)
-//   warp 16     TMA producer: resident tiles, then the tiles C1 (Q or K)
-//   warp 17     TMEM allocator; issues S and dV
-//   warp 18     TMA producer: the tiles C2 (dO or V), and with the keys resident
+// 384 threads:
+//   warps 0-7   math, two warpgroups: thread = one resident row (TMEM lane) and
+//               64 of a streamed tile's 128 columns
+//   warp 8      TMA producer: resident tiles, then the tiles C1 (Q or K)
+//   warp 9      TMEM allocator; issues S and dV (dV alone: S)
+//   warp 10     TMA producer: the tiles C2 (dO or V), and with the keys resident
 //               the streamed rows' statistics
-//   warp 19     issues dP and dK or dQ
+//   warp 11     issues dP and dK or dQ (dV alone: dV)
 // A product is issued about as fast as it runs, so what one issuing warp waits
 // the other's products fill; the tensor core finishes what one thread issues
 // in order.
@@ -254,7 +284,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const BwdParams p) {
     constexpr int D = C::D, BM = C::BM, BN = C::BN, NCH = C::NCH, NCK = C::NCK, CCH = C::CCH, SLOTS = C::SLOTS;
-    constexpr int SB = C::SB, DPB = C::DPB, G0 = C::G0, MW = C::MATH_WARPS;
+    constexpr int SB = C::SB, DPB = C::DPB, G0 = C::G0, MW = C::MATH_WARPS, WGS = C::MATH_WGS, H = C::H;
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles lie on 1024 bytes
     const uint32_t sR = smem_u32(smem);
     const uint32_t sC = sR + C::O_C;
@@ -269,57 +299,96 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     auto b_ds_full = [&](int b) { return smem_u32(&bars[8 + b]); };
     auto b_turn = [&](int b) { return smem_u32(&bars[10 + b]); };
     const uint32_t b_done = smem_u32(&bars[12]), b_drain = smem_u32(&bars[13]), b_res_in = smem_u32(&bars[14]);
-    auto b_stat_full = [&](int b) { return smem_u32(&bars[16 + b]); };
-    auto b_stat_empty = [&](int b) { return smem_u32(&bars[16 + C::STATS + b]); };
+    const uint32_t b_acc_free = smem_u32(&bars[15]);  // the accumulators have been read
+    auto b_res_free = [&](int r) { return smem_u32(&bars[16 + r]); };
+    auto b_item_full = [&](int b) { return smem_u32(&bars[18 + b]); };
+    auto b_item_free = [&](int b) { return smem_u32(&bars[18 + C::ITEMS + b]); };
+    auto b_stat_full = [&](int b) { return smem_u32(&bars[18 + 2 * C::ITEMS + b]); };
+    auto b_stat_empty = [&](int b) { return smem_u32(&bars[18 + 2 * C::ITEMS + C::STATS + b]); };
+    volatile int* const items = reinterpret_cast<volatile int*>(tmem_slot + 4);
     auto b_full = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + s]); };
     auto b_empty = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + SLOTS + s]); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // ------------------------------------------------------------------- item
-    // (tile, head, document): heads fastest and tiles slowest for causal
-    // launches (the keys' first tiles and the queries' last ones are the
+    // ------------------------------------------------------------------ items
+    // An item is a (tile, head, document).  Heads fastest and tiles slowest for
+    // causal launches (the keys' first tiles and the queries' last ones are the
     // heaviest and come first), tiles fastest otherwise (neighbouring CTAs
-    // stream the same head).
+    // stream the same head).  CTA b of G walks items k G + b (k even) and k G +
+    // G - 1 - b (k odd), so that falling costs even out.  The C1 producer walks
+    // them and publishes each in shared memory; rings, barriers and buffers
+    // carry on from item to item, so that the next item's loads and first
+    // products overlap the present one's last ones and its epilogue.
     const int heads = C::KEYS ? p.Hkv : p.Hq;
-    int tile, head, doc;
-    {
-        uint32_t it = blockIdx.x;
+    struct Item {
+        int n;                     // steps; 0: zeros to write; kItemEnd: no more items
+        int t_lo, t_hi;            // streamed tiles of each head
+        int head, r0;              // resident head, first resident row within the document
+        int diag;                  // causal: row i sees key j iff j <= i + diag
+        int res_start, res_all, res_len, str_start, str_len;
+        uint32_t stat;             // where the rows' statistics begin within a head's
+    };
+    constexpr int kItemEnd = -2;
+    static_assert(sizeof(Item) <= 64, "an item's room");
+    // The w-th word of the published item `it` (a count), by a role that has waited for it.
+    auto word = [&](int it, int w) -> int { return items[(it % C::ITEMS) * 16 + w]; };
+#define GBATTN_ITEM(it, field) word(it, static_cast<int>(offsetof(Item, field) / 4))
+    // Wait for item `it`: its steps, or kItemEnd, or -1 where the wait gave up.
+    auto next_item = [&](int it, bool all) -> int {
+        bool got = mbar_wait(b_item_full(it % C::ITEMS), (it / C::ITEMS) & 1, abort_flag);
+        if (all) got = __all_sync(0xffffffffu, got);
+        return got ? GBATTN_ITEM(it, n) : -1;
+    };
+    // The walk's k-th item; false past the end.  n = -1: nothing to write.
+    auto item_at = [&](int k, Item& it) -> bool {
+        const long long g = gridDim.x, first = k * g;
+        const long long i = first + ((k & 1) ? g - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
+        if (first >= p.items[C::KEYS ? 0 : 1]) return false;
+        it.n = -1;
+        if (i >= p.items[C::KEYS ? 0 : 1]) return true;
+        uint32_t x = static_cast<uint32_t>(i);
+        int tile, doc;
         if (p.causal) {
-            head = it % heads;
-            it /= heads;
-            doc = it % p.num_docs;
-            tile = it / p.num_docs;
+            it.head = x % heads;
+            x /= heads;
+            doc = x % p.num_docs;
+            tile = x / p.num_docs;
             if (!C::KEYS) tile = p.tiles_q - 1 - tile;
         } else {
             const int tiles = C::KEYS ? p.tiles_k : p.tiles_q;
-            tile = it % tiles;
-            it /= tiles;
-            head = it % heads;
-            doc = it / heads;
+            tile = x % tiles;
+            x /= tiles;
+            it.head = x % heads;
+            doc = x / heads;
         }
+        const BwdDoc d = bwd_doc(p, doc, false);
+        if (d.bad) return true;
+        it.r0 = tile * BM;
+        it.res_all = C::KEYS ? d.Lk_all : d.Lq_all;
+        if (it.r0 >= it.res_all) return true;
+        it.res_len = C::KEYS ? d.Lk : d.Lq;
+        it.str_len = C::KEYS ? d.Lq : d.Lk;
+        it.res_start = C::KEYS ? d.k_start : d.q_start;
+        it.str_start = C::KEYS ? d.q_start : d.k_start;
+        it.stat = static_cast<uint32_t>(bwd_stat_base(d.q_start, doc));
+        it.diag = d.Lk - d.Lq;
+        it.t_lo = 0;
+        it.t_hi = (it.str_len + BN - 1) / BN;
+        if (it.r0 >= it.res_len) {
+            it.t_hi = 0;
+        } else if (p.causal) {
+            if (C::KEYS)
+                it.t_lo = max(0, it.r0 - it.diag) / BN;  // the first row that sees key r0
+            else
+                it.t_hi = (max(0, min(d.Lk, min(it.r0 + BM, d.Lq) + it.diag)) + BN - 1) / BN;
+        }
+        it.n = max(0, it.t_hi - it.t_lo) * (C::KEYS ? p.group : 1);
+        return true;
+    };
+    if (status_has_timeout(p.status, kDevTimeout)) {
+        grid_dependency_wait();
+        return;
     }
-    const BwdDoc d = bwd_doc(p, doc, false);
-    if (d.bad) return;
-    const int r0 = tile * BM;                                   // first resident row within the document
-    const int res_all = C::KEYS ? d.Lk_all : d.Lq_all, res_len = C::KEYS ? d.Lk : d.Lq;
-    if (r0 >= res_all) return;  // CTA-uniform, before any barrier or TMEM use
-    if (status_has_timeout(p.status, kDevTimeout)) return;
-    const int res_start = C::KEYS ? d.k_start : d.q_start, str_start = C::KEYS ? d.q_start : d.k_start;
-    const int str_len = C::KEYS ? d.Lq : d.Lk;
-    const int diag = d.Lk - d.Lq;  // causal: row i sees key j iff j <= i + diag
-    // streamed tiles [t_lo, t_lo + nt) of each of `rounds` heads
-    int t_lo = 0, t_hi = (str_len + BN - 1) / BN;
-    if (r0 >= res_len) {
-        t_hi = 0;
-    } else if (p.causal) {
-        if (C::KEYS)
-            t_lo = max(0, r0 - diag) / BN;  // the first row that sees key r0
-        else
-            t_hi = (max(0, min(d.Lk, min(r0 + BM, d.Lq) + diag)) + BN - 1) / BN;
-    }
-    const int nt = max(0, t_hi - t_lo);
-    const int rounds = C::KEYS ? p.group : 1;
-    const int n = nt * rounds;
 
     // ------------------------------------------------------------------ setup
     if (threadIdx.x == 0) {
@@ -334,13 +403,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         mbar_init(b_done, C::ISSUERS);
         mbar_init(b_drain, C::ISSUERS);
         mbar_init(b_res_in, MW);
+        mbar_init(b_acc_free, MW);
+        mbar_init(b_res_free(0), 1);
+        mbar_init(b_res_free(1), 1);
+        for (int b = 0; b < C::ITEMS; ++b) {
+            mbar_init(b_item_full(b), 1);
+            mbar_init(b_item_free(b), MW + C::ISSUERS + 1);
+        }
         for (int b = 0; b < C::STATS; ++b) {
             mbar_init(b_stat_full(b), 1);
             mbar_init(b_stat_empty(b), MW);
         }
         for (int s = 0; s < SLOTS; ++s) {
             mbar_init(b_full(s), 1);
-            mbar_init(b_empty(s), C::ISSUERS);
+            mbar_init(b_empty(s), C::RELEASES);
         }
         *abort_flag = p.give_up ? 1 : 0;  // 1: give up every wait (failure-path test)
         fence_mbar_init();
@@ -356,7 +432,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     bool ok = true;
 
     const CUtensorMap *mC1 = C::KEYS ? &tmQ : &tmK, *mC2 = C::KEYS ? &tmG : &tmV;
-    const int str_head = C::KEYS ? head * p.group : head / p.group;  // the first streamed head
+    // The first streamed head of resident head h.
+    auto str_head = [&](int h) { return C::KEYS ? h * p.group : h / p.group; };
     // Slots [begin, begin + size) as a ring: load g is in slot begin + g % size.
     struct Ring {
         uint32_t base;  // shared memory of slot 0
@@ -384,59 +461,108 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int g = (r.issued > r.size ? r.issued - r.size : 0); g < r.issued; ++g)
             mbar_wait_drain(b_full(r.begin + g % r.size), (g / r.size) & 1);
     };
-    if (warp == MW && lane == 0 && n > 0) {
+    int res_loads[2] = {0, 0};  // (of the producer: loads of each resident tile so far)
+    if (warp >= MW) {
+    regs_dec<C::REG_OTHER>();
+    if (warp == MW && lane == 0) {
         // ---------------------------------- producer: resident tiles, then C1
         const CUtensorMap *mR1 = C::KEYS ? &tmK : &tmQ, *mR2 = C::KEYS ? &tmV : &tmG;
         Ring ring(sC, 0, C::N1);
-        for (int r = 0; r < C::RES; ++r) {
-            const CUtensorMap* m = r ? mR2 : mR1;
-            if (r >= C::RT0) {
-                for (int c = 0; c < NCK; ++c) ok = ok && load(ring, m, head, res_start + r0, c);
-            } else {
-                mbar_arrive_expect_tx(b_res(r), C::R_BYTES);
-                for (int c = 0; c < NCH; ++c)
-                    tma_load_3d(sR + r * C::R_BYTES + c * (BM * 128), m, b_res(r), c * 64, head, res_start + r0);
+        Item it;
+        int done = 0;       // items with steps so far
+        int published = 0;  // items published
+        auto publish = [&]() -> bool {
+            const int b = published % C::ITEMS;
+            if (published >= C::ITEMS && !mbar_wait(b_item_free(b), (published / C::ITEMS - 1) & 1, abort_flag)) return false;
+            for (int w = 0; w < static_cast<int>(sizeof(Item) / 4); ++w)
+                items[b * 16 + w] = reinterpret_cast<const int*>(&it)[w];
+            mbar_arrive(b_item_full(b));
+            ++published;
+            return true;
+        };
+#pragma unroll 1
+        for (int k = 0; ok; ++k) {
+            if (!item_at(k, it)) {
+                it.n = kItemEnd;
+                ok = publish();
+                break;
             }
-        }
-        int t = t_lo, h = str_head;
-        for (int j = 0; ok && j < n; ++j) {
-            const int t2 = t, h2 = h;  // step j
-            if (++t == t_hi) {
-                t = t_lo;
-                ++h;
+            if (it.n < 0) continue;
+            if (!(ok = publish())) break;
+            if (it.n == 0) continue;
+            for (int r = 0; r < C::RES; ++r) {
+                const CUtensorMap* m = r ? mR2 : mR1;
+                if (r >= C::RT0) {
+                    for (int c = 0; c < NCK; ++c) ok = ok && load(ring, m, it.head, it.res_start + it.r0, c);
+                } else if (ok && (done == 0 || mbar_wait(b_res_free(r), (done - 1) & 1, abort_flag))) {
+                    mbar_arrive_expect_tx(b_res(r), C::R_BYTES);
+                    for (int c = 0; c < NCH; ++c)
+                        tma_load_3d(sR + r * C::R_BYTES + c * (BM * 128), m, b_res(r), c * 64, it.head, it.res_start + it.r0);
+                    res_loads[r] = done + 1;
+                } else {
+                    ok = false;
+                }
             }
-            if (C::HAS_DS || j == 0)
-                for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC1, h2, str_start + t2 * BN, c);
-            if (!C::HAS_DS) {  // S(j + 1) comes before dV(j)
-                if (j + 1 < n)
-                    for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC1, h, str_start + t * BN, c);
-                for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h2, str_start + t2 * BN, c);
+            int t = it.t_lo, h = str_head(it.head);
+#pragma unroll 1
+            for (int j = 0; ok && j < it.n; ++j) {
+                const int t2 = t, h2 = h;  // step j
+                if (++t == it.t_hi) {
+                    t = it.t_lo;
+                    ++h;
+                }
+                if (C::HAS_DS || j == 0)
+                    for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC1, h2, it.str_start + t2 * BN, c);
+                if (!C::HAS_DS) {  // S(j + 1) comes before dV(j)
+                    if (j + 1 < it.n)
+                        for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC1, h, it.str_start + t * BN, c);
+                    for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h2, it.str_start + t2 * BN, c);
+                }
             }
+            ++done;
         }
         if (!ok || *abort_flag) {
             // Let every copy this thread started land before the CTA retires.
-            for (int r = 0; r < C::RES_SMEM; ++r) mbar_wait_drain(b_res(r), 0);
+            for (int r = 0; r < C::RES_SMEM; ++r)
+                if (res_loads[r] > 0) mbar_wait_drain(b_res(r), (res_loads[r] - 1) & 1);
             drain(ring);
         }
-    } else if (warp == MW + 2 && lane == 0 && n > 0) {
+    } else if (warp == MW + 2 && lane == 0) {
         // --------------------- producer: C2, and statistics of streamed rows
+        if (p.early_wait) grid_dependency_wait();  // the launch before this one writes the statistics
+        grid_launch_dependents();
         Ring ring(sC, C::N1, C::N2);
-        int t = t_lo, h = str_head, issued = 0;
-        for (int j = 0; ok && j < n; ++j) {
-            if (C::HAS_DS)
-                for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h, str_start + t * BN, c);
-            if (C::KEYS && ok) {
-                const int b = j % C::STATS;
-                if (j >= C::STATS && !(ok = mbar_wait(b_stat_empty(b), (j / C::STATS - 1) & 1, abort_flag))) break;
-                const long long at = h * p.stat_stride + bwd_stat_base(d.q_start, doc) + static_cast<long long>(t) * BN;
-                mbar_arrive_expect_tx(b_stat_full(b), C::STAT_BYTES);
-                bulk_load(sStat + b * C::STAT_BYTES, p.neg_lse2 + at, BN * 4, b_stat_full(b));
-                bulk_load(sStat + b * C::STAT_BYTES + BN * 4, p.neg_delta + at, BN * 4, b_stat_full(b));
-                ++issued;
+        int issued = 0;
+#pragma unroll 1
+        for (int i = 0; ok; ++i) {
+            const int n = next_item(i, false);
+            if (n < 0) {
+                ok = n == kItemEnd;
+                break;
             }
-            if (++t == t_hi) {
-                t = t_lo;
-                ++h;
+            const int t_lo = GBATTN_ITEM(i, t_lo), t_hi = GBATTN_ITEM(i, t_hi), start = GBATTN_ITEM(i, str_start);
+            const long long stat_base = static_cast<uint32_t>(GBATTN_ITEM(i, stat));
+            int t = t_lo, h = str_head(GBATTN_ITEM(i, head));
+            mbar_arrive(b_item_free(i % C::ITEMS));
+#pragma unroll 1
+            for (int j = 0; ok && j < n; ++j) {
+                if (C::HAS_DS)
+                    for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h, start + t * BN, c);
+                if (C::KEYS && ok) {
+                    const int b = issued % C::STATS;
+                    if (issued >= C::STATS &&
+                        !(ok = mbar_wait(b_stat_empty(b), (issued / C::STATS - 1) & 1, abort_flag)))
+                        break;
+                    const long long at = h * p.stat_stride + stat_base + static_cast<long long>(t) * BN;
+                    mbar_arrive_expect_tx(b_stat_full(b), C::STAT_BYTES);
+                    bulk_load(sStat + b * C::STAT_BYTES, p.neg_lse2 + at, BN * 4, b_stat_full(b));
+                    bulk_load(sStat + b * C::STAT_BYTES + BN * 4, p.neg_delta + at, BN * 4, b_stat_full(b));
+                    ++issued;
+                }
+                if (++t == t_hi) {
+                    t = t_lo;
+                    ++h;
+                }
             }
         }
         if (!ok || *abort_flag) {
@@ -444,16 +570,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int g = (issued > C::STATS ? issued - C::STATS : 0); g < issued; ++g)
                 mbar_wait_drain(b_stat_full(g % C::STATS), (g / C::STATS) & 1);
         }
-    } else if ((warp == MW + 1 || (warp == MW + 3 && C::ISSUERS == 2)) && n > 0) {
+    } else if (warp == MW + 1 || (warp == MW + 3 && C::ISSUERS == 2)) {
         // ----------------------------------------------------------------- MMA
         // Each issuing warp walks its schedule as a whole; one elected lane issues.
         constexpr uint32_t kIdS = idesc_bf16_f32(BM, BN, false, false);
         constexpr uint32_t kIdA = idesc_bf16_f32(BM, C::CW, false, true);
         const bool first_warp = warp == MW + 1;
         const bool leader = elect_one();
-        const uint64_t dR = sdesc_sw128(sR, 16, 1024);
-        const uint64_t dCk = sdesc_sw128(sC, 16, 1024);           // streamed chunk, K-major
-        const uint64_t dCm = sdesc_sw128(sC, BN * 128, 1024);     // streamed chunk, MN-major
+        const uint32_t dR = desc_lo(sR, 16);
+        const uint32_t dCk = desc_lo(sC, 16);           // streamed chunk, K-major
+        const uint32_t dCm = desc_lo(sC, BN * 128);     // streamed chunk, MN-major
         auto wait_all = [&](uint32_t bar, uint32_t ph) {
             return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag));
         };
@@ -461,10 +587,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // document, the neighbours' rows, or rows without a key) may hold
         // anything; P and dS are 0 there but 0 * NaN is not, so they are zeroed
         // before the second product reads them.
-        auto edge_rows = [&](int t) { return (t + 1) * BN > str_len || (C::KEYS && p.causal && t * BN < -diag); };
+        int item = 0, n = 0, edge_lo = 0, edge_hi = 0;  // tiles below edge_lo or from edge_hi on have such rows
+        auto edge_rows = [&](int t) { return t < edge_lo || t >= edge_hi; };
         auto zero_rows = [&](int s, int t) {
-            const int hi = min(BN, str_len - t * BN);
-            const int lo = (C::KEYS && p.causal) ? min(hi, max(0, -diag - t * BN)) : 0;
+            const int hi = min(BN, GBATTN_ITEM(item, str_len) - t * BN);
+            const int lo = (C::KEYS && p.causal) ? min(hi, max(0, -GBATTN_ITEM(item, diag) - t * BN)) : 0;
             for (int x = lane; x < (lo + BN - hi) * CCH * 8; x += 32) {
                 const int u = x & 7, rc = x >> 3, c = rc % CCH, r = rc / CCH;
                 st_shared_v4(sC + s * C::C_BYTES + c * (BN * 128) + (r < lo ? r : hi + r - lo) * 128 + u * 16, 0u, 0u, 0u, 0u);
@@ -474,41 +601,61 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         };
         // X (128 x BN) (+)= resident r * chunk c of a streamed tile, in slot s
         auto scores = [&](uint32_t to, int r, int c, int s) {
+            uint32_t a = r >= C::RT0 ? tmem + C::T_RES + (r - C::RT0) * (D / 2) + c * (C::CW / 2)
+                                     : dR + ((r * C::R_BYTES + c * CCH * BM * 128) >> 4);
+            uint32_t b = dCk + s * (C::C_BYTES >> 4);
+            asm volatile("" : "+r"(a), "+r"(b));  // (worked out here, not kept over the steps)
 #pragma unroll
             for (int k = 0; k < C::CW / 16; ++k) {
-                const int blk = k >> 2, kk = k & 3;
-                const uint64_t b = dCk + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((blk * BN * 128 + kk * 32) >> 4);
-                const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u;
+                const uint32_t off = ((k >> 2) * BN * 128 + (k & 3) * 32) >> 4, acc = (c > 0 || k > 0) ? 1u : 0u;
                 if (r >= C::RT0)
-                    mma_bf16_ts(tmem + to, tmem + C::T_RES + (r - C::RT0) * (D / 2) + c * (C::CW / 2) + k * 8, b, kIdS, acc);
+                    mma_ts(tmem + to, a + k * 8, b + off, kIdS, acc);
                 else
-                    mma_bf16_ss(tmem + to, dR + ((r * C::R_BYTES + (c * CCH + blk) * BM * 128 + kk * 32) >> 4), b, kIdS, acc);
+                    mma_ss(tmem + to, a + off, b + off, kIdS, acc);
             }
         };
         // columns [c CW, (c + 1) CW) of acc += A (bf16 pairs in X's columns, 16
-        // of each warpgroup's 32) * chunk c of a streamed tile, in slot s
-        auto accumulate = [&](uint32_t acc, uint32_t a, int c, int s, bool first) {
+        // of every 32) * chunk c of a streamed tile, in slot s
+        auto accumulate = [&](uint32_t acc, uint32_t x, int c, int s, bool first) {
+            uint32_t a = tmem + x, b = dCm + s * (C::C_BYTES >> 4);
+            asm volatile("" : "+r"(a), "+r"(b));
 #pragma unroll
             for (int k = 0; k < BN / 16; ++k)
-                mma_bf16_ts(tmem + acc + c * C::CW, tmem + a + (k >> 1) * 32 + (k & 1) * 8,
-                            dCm + static_cast<uint64_t>(s * (C::C_BYTES >> 4)) + ((k * 16 * 128) >> 4), kIdA,
-                            (!first || k > 0) ? 1u : 0u);
+                mma_ts(tmem + acc + c * C::CW, a + (k >> 1) * 32 + (k & 1) * 8, b + ((k * 16 * 128) >> 4), kIdA,
+                       (!first || k > 0) ? 1u : 0u);
         };
-        ok = !*abort_flag;  // a launch told to give up issues nothing
-        if (C::RES_TMEM > 0) {  // the math warps have copied those residents into tensor memory
-            ok = ok && wait_all(b_res_in, 0);
-            if (ok && lane == 0)
-                for (int g = 0; g < G0; ++g) mbar_arrive(b_empty(g));
-            __syncwarp();
-        }
-        // Cursors: the next chunk of C1 and of C2 that this warp uses (the
-        // first ring begins with the residents' G0).
+        // Cursors: the next chunk of C1 and of C2 that this warp uses.
         Ring c1(sC, 0, C::N1), c2(sC, C::N1, C::N2);
-        for (int g = 0; g < G0; ++g) c1.next();
         auto moved = [](Ring r) {
             for (int c = 0; c < NCK; ++c) r.next();
             return r;
         };
+        int J = 0;     // steps of the items so far: buffers and phases go by J + j
+        int done = 0;  // items with steps so far
+        auto acc_free = [&]() -> bool { return done == 0 || wait_all(b_acc_free, (done - 1) & 1); };
+        ok = !*abort_flag;  // a launch told to give up issues nothing
+#pragma unroll 1
+        for (; ok; ++item) {
+        n = next_item(item, true);
+        if (n <= 0) {
+            if (n < 0) {
+                ok = n == kItemEnd;
+                break;
+            }
+            if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
+            continue;
+        }
+        const int t_lo = GBATTN_ITEM(item, t_lo), t_hi = GBATTN_ITEM(item, t_hi);
+        edge_lo = C::KEYS && p.causal ? (max(0, -GBATTN_ITEM(item, diag)) + BN - 1) / BN : 0;
+        edge_hi = GBATTN_ITEM(item, str_len) / BN;
+        if (C::RES_TMEM > 0) {  // the math warps have copied those residents into tensor memory
+            ok = wait_all(b_res_in, done & 1);
+            for (int g = 0; g < G0; ++g) {
+                if (ok && lane == 0) mbar_arrive(b_empty(c1.s));
+                c1.next();
+            }
+            __syncwarp();
+        }
         int t = t_lo;
         // All of a tile's chunks have landed.
         auto landed = [&](Ring s) -> bool {
@@ -521,22 +668,34 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // S of a step from C1's chunks, released once read when `free_c1`.
         auto issue_s = [&](int j, Ring s, bool free_c1) {
             for (int c = 0; c < NCK; ++c) {
-                scores(C::T_S + (j % SB) * BN, 0, c, s.s);
+                scores(C::T_S + ((J + j) % SB) * BN, 0, c, s.s);
                 if (free_c1) mma_commit(b_empty(s.s));
                 s.next();
             }
-            mma_commit(b_s_full(j % SB));
+            mma_commit(b_s_full((J + j) % SB));
+            if (C::RES_SMEM > 0 && j + 1 == n) mma_commit(b_res_free(0));
         };
         if constexpr (C::SHARED) {
             // ---------------------------------- S and dP in the same columns
-            ok = ok && wait_all(b_res(0), 0) && landed(c1);
-            if (ok) {
-                tc_fence_after();
-                if (leader) issue_s(0, c1, false);
-                __syncwarp();
-            }
+            // S(j), chunk by chunk: the last ones come into slots released just before
+            auto next_s = [&](int j) -> bool {
+                Ring s = c1;
+                for (int c = 0; c < NCK; ++c) {
+                    if (!wait_all(b_full(s.s), s.ph)) return false;
+                    tc_fence_after();
+                    if (leader) {
+                        scores(C::T_S, 0, c, s.s);
+                        if (c == NCK - 1) mma_commit(b_s_full(0));
+                        if (c == NCK - 1 && j + 1 == n) mma_commit(b_res_free(0));
+                    }
+                    __syncwarp();
+                    s.next();
+                }
+                return true;
+            };
+            ok = ok && wait_all(b_res(0), done & 1) && next_s(0);
             for (int j = 0; ok && j < n; ++j) {
-                if (!(ok = landed(c2) && wait_all(b_p_full(0), j & 1))) break;
+                if (!(ok = landed(c2) && wait_all(b_p_full(0), (J + j) & 1))) break;
                 tc_fence_after();
                 if (leader) {
                     Ring s = c2;
@@ -556,7 +715,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         s.next();
                     }
                 }
-                if (!(ok = wait_all(b_ds_full(0), j & 1))) break;
+                if (!(ok = (j > 0 || acc_free()) && wait_all(b_ds_full(0), (J + j) & 1))) break;
                 tc_fence_after();
                 if (leader) {
                     Ring s = c1;
@@ -568,64 +727,60 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 __syncwarp();
                 c1 = moved(c1);
-                // (chunk by chunk: the last ones come into the slots released just now)
-                if (j + 1 < n) {
-                    Ring s = c1;
-                    for (int c = 0; c < NCK; ++c) {
-                        if (!(ok = wait_all(b_full(s.s), s.ph))) break;
-                        tc_fence_after();
-                        if (leader) {
-                            scores(C::T_S, 0, c, s.s);
-                            if (c == NCK - 1) mma_commit(b_s_full(0));
-                        }
-                        __syncwarp();
-                        s.next();
-                    }
-                }
+                if (j + 1 < n && !(ok = next_s(j + 1))) break;
                 if (++t == t_hi) t = t_lo;
             }
         } else if constexpr (!C::HAS_DS) {
-            // ---------------------------------------------------- dV alone
-            ok = ok && wait_all(b_res(0), 0) && landed(c1);
-            if (ok) {
-                tc_fence_after();
-                if (leader) issue_s(0, c1, true);
-                __syncwarp();
-            }
-            c1 = moved(c1);
-            for (int j = 0; ok && j < n; ++j) {
-                if (j + 1 < n) {
+            // ------------------------------------ dV alone: one ring, S(j + 1) before dV(j)
+            if (first_warp) {
+                ok = ok && wait_all(b_res(0), done & 1);
+                for (int j = 0; ok && j < n; ++j) {
                     if (!(ok = landed(c1))) break;
+                    // the buffer's P has been used up
+                    const int g = J + j - SB;
+                    if (g >= 0 && !(ok = wait_all(b_turn(g % SB), (g / SB) & 1))) break;
                     tc_fence_after();
-                    if (leader) issue_s(j + 1, c1, true);
+                    if (leader) issue_s(j, c1, true);
                     __syncwarp();
                     c1 = moved(c1);
+                    if (j > 0 || n == 1) c1 = moved(c1);  // past dout's tile
                 }
-                if (!(ok = landed(c1))) break;  // dout's tile of step j
-                if (edge_rows(t)) {
-                    Ring s = c1;
-                    for (int c = 0; c < NCK; ++c) {
-                        zero_rows(s.s, t);
-                        s.next();
-                    }
-                }
-                if (!(ok = wait_all(b_p_full(j % SB), (j / SB) & 1))) break;
-                tc_fence_after();
-                if (leader) {
-                    Ring s = c1;
-                    for (int c = 0; c < NCK; ++c) {
-                        accumulate(C::T_ACC, C::T_S + (j % SB) * BN, c, s.s, j == 0);
-                        mma_commit(b_empty(s.s));
-                        s.next();
-                    }
-                }
-                __syncwarp();
+                if (n > 1) c1 = moved(c1);
+            } else {
                 c1 = moved(c1);
-                if (++t == t_hi) t = t_lo;
+                if (n > 1) c1 = moved(c1);
+                for (int j = 0; ok && j < n; ++j) {
+                    // P(j) first: the slots' last turns were S(j)'s tiles or
+                    // earlier ones, and a wait by parity is exact only once
+                    // those have landed.
+                    if (!(ok = (j > 0 || acc_free()) && wait_all(b_p_full((J + j) % SB), ((J + j) / SB) & 1) && landed(c1)))
+                        break;
+                    if (edge_rows(t)) {
+                        Ring s = c1;
+                        for (int c = 0; c < NCK; ++c) {
+                            zero_rows(s.s, t);
+                            s.next();
+                        }
+                    }
+                    tc_fence_after();
+                    if (leader) {
+                        Ring s = c1;
+                        for (int c = 0; c < NCK; ++c) {
+                            accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, c, s.s, j == 0);
+                            mma_commit(b_empty(s.s));
+                            s.next();
+                        }
+                        mma_commit(b_turn((J + j) % SB));
+                    }
+                    __syncwarp();
+                    c1 = moved(c1);
+                    if (j + 2 < n) c1 = moved(c1);  // past the queries' tile of step j + 2
+                    if (++t == t_hi) t = t_lo;
+                }
             }
         } else if (first_warp) {
             // -------------------------------------------------- S (and dV)
-            if (C::RT0 > 0) ok = ok && wait_all(b_res(0), 0);
+            if (C::RT0 > 0) ok = ok && wait_all(b_res(0), done & 1);
             ok = ok && wait_all(b_full(c1.s), c1.ph);
             if (ok) {
                 tc_fence_after();
@@ -642,18 +797,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     __syncwarp();
                 }
                 if (C::HAS_P) {
-                    if (!(ok = wait_all(b_full(c2.s), c2.ph))) break;
+                    if (!(ok = wait_all(b_full(c2.s), c2.ph) && (j > 0 || acc_free()))) break;
                     if (edge_rows(t)) zero_rows(c2.s, t);
                 }
-                if (!(ok = wait_all(b_p_full(j % SB), (j / SB) & 1))) break;
+                if (!(ok = wait_all(b_p_full((J + j) % SB), ((J + j) / SB) & 1))) break;
                 tc_fence_after();
                 if (leader) {
                     if (C::HAS_P) {
-                        accumulate(C::T_ACC, C::T_S + (j % SB) * BN, 0, c2.s, j == 0);
+                        accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, 0, c2.s, j == 0);
                         mma_commit(b_empty(c2.s));
                     }
                     if (more && SB == 1) issue_s(j + 1, c1, true);
-                    if (C::HAS_P && SB == 1) mbar_arrive(b_turn(j & 1));
+                    if (C::HAS_P && SB == 1) mbar_arrive(b_turn((J + j) & 1));
                 }
                 __syncwarp();
                 c2.next();
@@ -663,12 +818,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // --------------------------------------------- dP and dK or dQ
             constexpr uint32_t kAcc = C::T_ACC + (C::HAS_P ? D : 0);
             auto issue_dp = [&](int j) {
-                scores(C::T_DP + (j % DPB) * BN, 1, 0, c2.s);
+                scores(C::T_DP + ((J + j) % DPB) * BN, 1, 0, c2.s);
                 mma_commit(b_empty(c2.s));
                 if (!C::HAS_P) mma_commit(b_empty(c2.s));  // (a slot is released twice)
-                mma_commit(b_dp_full(j % DPB));
+                mma_commit(b_dp_full((J + j) % DPB));
+                if (C::RES_SMEM > 1 && j + 1 == n) mma_commit(b_res_free(1));
             };
-            if (C::RT0 > 1) ok = ok && wait_all(b_res(1), 0);
+            if (C::RT0 > 1) ok = ok && wait_all(b_res(1), done & 1);
             ok = ok && wait_all(b_full(c2.s), c2.ph);
             if (ok) {
                 tc_fence_after();
@@ -688,11 +844,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (more && leader) issue_dp(j + 1);
                     __syncwarp();
                 }
-                if (!(ok = wait_all(b_ds_full(j % DPB), (j / DPB) & 1))) break;
-                if (C::HAS_P && SB == 1 && !(ok = wait_all(b_turn(j & 1), (j >> 1) & 1))) break;
+                if (!(ok = (j > 0 || acc_free()) && wait_all(b_ds_full((J + j) % DPB), ((J + j) / DPB) & 1))) break;
+                if (C::HAS_P && SB == 1 && !(ok = wait_all(b_turn((J + j) & 1), ((J + j) >> 1) & 1))) break;
                 tc_fence_after();
                 if (leader) {
-                    accumulate(kAcc, C::T_DP + (j % DPB) * BN, 0, c1.s, j == 0);
+                    accumulate(kAcc, C::T_DP + ((J + j) % DPB) * BN, 0, c1.s, j == 0);
                     mma_commit(b_empty(c1.s));
                     if (more && DPB == 1) issue_dp(j + 1);
                 }
@@ -702,28 +858,48 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
         }
         if (ok && leader) mma_commit(b_done);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
+        J += n;
+        ++done;
+        }
         // Everything issued above must finish before TMEM is released.
         if (leader) mma_commit(b_drain);
         __syncwarp();
         mbar_wait_drain(b_drain, 0);
-    } else if (warp < MW) {
+    }
+    } else {
+        regs_inc<C::REG_MATH>();
         // ---------------------------------------------------------------- math
         const int wg = warp >> 2;
         const int r = (warp & 3) * 32 + lane;   // resident row within the tile == TMEM lane
-        const int row = r0 + r;                 // within the document
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const float c2 = p.scale_log2;
+        if (!C::KEYS && p.early_wait) grid_dependency_wait();  // the launch before this one writes the statistics
+        int J = 0;     // steps of the items so far: buffers and phases go by J + j
+        int done = 0;  // items with steps so far
+        Ring res_ring(sC, 0, C::N1);  // where residents that go to tensor memory come in
+#pragma unroll 1
+        for (int item = 0; ok; ++item) {
+        const int n = next_item(item, true);
+        if (n < 0) {
+            ok = n == kItemEnd;
+            break;
+        }
+        const int row = GBATTN_ITEM(item, r0) + r;  // within the document
         float row_nl = -INFINITY, row_nd = 0.f;
-        if (!C::KEYS && row < d.Lq) {
-            const long long at = head * p.stat_stride + bwd_stat_base(d.q_start, doc) + row;
+        if (!C::KEYS && row < GBATTN_ITEM(item, res_len)) {
+            const long long at = GBATTN_ITEM(item, head) * p.stat_stride + static_cast<uint32_t>(GBATTN_ITEM(item, stat)) + row;
             row_nl = p.neg_lse2[at];
             row_nd = p.neg_delta[at];
         }
         if (C::RES_TMEM > 0 && n > 0) {
-            // residents that go to tensor memory: a warpgroup copies every fourth 64-column block
-            for (int b = wg; ok && b < C::RES_TMEM * NCH; b += 4) {
-                const int s = b / CCH;  // the slot: blocks lie in the order they were loaded
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_full(s), 0, abort_flag)))) break;
+            // residents that go to tensor memory: the warpgroups copy 64-column blocks in turn
+            for (int b = wg; ok && b < C::RES_TMEM * NCH; b += WGS) {
+                Ring at = res_ring;  // blocks lie in the order they were loaded
+                for (int c = 0; c < b / CCH; ++c) at.next();
+                const int s = at.s;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_full(s), at.ph, abort_flag)))) break;
                 const uint32_t src = sC + s * C::C_BYTES + (b % CCH) * (BM * 128) + r * 128;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -743,126 +919,146 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_res_in);
             }
+            // the next item's come G0 + n NCK loads on
+            const int by = G0 + n * NCK, turns = (res_ring.s + by) / C::N1;
+            res_ring.s = (res_ring.s + by) % C::N1;
+            res_ring.ph ^= turns & 1;
         }
+        // streamed rows [see_lo, see_hi) are visible
+        const int diag = GBATTN_ITEM(item, diag), str_len = GBATTN_ITEM(item, str_len);
+        const int see_lo = C::KEYS && p.causal ? row - diag : 0;
+        const int see_hi = !C::KEYS && p.causal ? min(str_len, row + diag + 1) : str_len;
+        const int t_lo = GBATTN_ITEM(item, t_lo), t_hi = GBATTN_ITEM(item, t_hi);
         int t = t_lo;
         for (int j = 0; ok && j < n; ++j) {
-            const int c0 = t * BN + wg * 32;  // this thread's first streamed row
-            // columns [lo, hi) of the thread's 32 are visible
-            int lo = 0, hi = str_len - c0;
-            if (p.causal) {
-                if (C::KEYS)
-                    lo = row - diag - c0;
-                else
-                    hi = min(hi, row + diag + 1 - c0);
-            }
-            const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < 32);
-            const uint32_t st = sStat + (j % C::STATS) * C::STAT_BYTES + wg * (32 * 4);
-            if (C::KEYS) ok = mbar_wait(b_stat_full(j % C::STATS), (j / C::STATS) & 1, abort_flag);
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(b_s_full(j % SB), (j / SB) & 1, abort_flag));
+            const int c0 = t * BN + wg * H;  // this thread's first streamed row
+            const int lo = see_lo - c0, hi = see_hi - c0;
+            const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < H);
+            const uint32_t st = sStat + ((J + j) % C::STATS) * C::STAT_BYTES + wg * (H * 4);
+            if (C::KEYS) ok = mbar_wait(b_stat_full((J + j) % C::STATS), ((J + j) / C::STATS) & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(b_s_full((J + j) % SB), ((J + j) / SB) & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t tS = tl + C::T_S + (j % SB) * BN + wg * 32, tDP = tl + C::T_DP + (j % DPB) * BN + wg * 32;
-            uint32_t pr[32];  // P, fp32
-            tmem_ld32(tS, pr);
+            const uint32_t tS = tl + C::T_S + ((J + j) % SB) * BN + wg * H, tDP = tl + C::T_DP + ((J + j) % DPB) * BN + wg * H;
+            uint32_t pr[H];  // P, fp32
+#pragma unroll
+            for (int c = 0; c < H; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&pr[c]));
             tmem_wait_ld();
             if (!C::HAS_P) {  // the S buffer may be written again
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_p_full(j % SB));
+                if (lane == 0) mbar_arrive(b_p_full((J + j) % SB));
             }
             const float2 cc = make_float2(c2, c2);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                float4 nl = make_float4(row_nl, row_nl, row_nl, row_nl);
-                if (C::KEYS) nl = ld_shared_f4(st + e * 4);
-                const float2 a = __ffma2_rn(make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])), cc,
-                                            make_float2(nl.x, nl.y));
-                const float2 b = __ffma2_rn(make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])), cc,
-                                            make_float2(nl.z, nl.w));
-                pr[e] = __float_as_uint(ex2(a.x));
-                pr[e + 1] = __float_as_uint(ex2(a.y));
-                pr[e + 2] = __float_as_uint(ex2(b.x));
-                pr[e + 3] = __float_as_uint(ex2(b.y));
-            }
-            if (edge) {
+            for (int c = 0; c < H; c += 32) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (e < lo || e >= hi) pr[e] = 0u;
+                for (int e = c; e < c + 32; e += 4) {
+                    float4 nl = make_float4(row_nl, row_nl, row_nl, row_nl);
+                    if (C::KEYS) nl = ld_shared_f4(st + e * 4);
+                    const float2 a = __ffma2_rn(make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])), cc,
+                                                make_float2(nl.x, nl.y));
+                    const float2 b = __ffma2_rn(make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])), cc,
+                                                make_float2(nl.z, nl.w));
+                    pr[e] = __float_as_uint(ex2(a.x));
+                    pr[e + 1] = __float_as_uint(ex2(a.y));
+                    pr[e + 2] = __float_as_uint(ex2(b.x));
+                    pr[e + 3] = __float_as_uint(ex2(b.y));
+                }
+                if (edge) {
+#pragma unroll
+                    for (int e = c; e < c + 32; ++e)
+                        if (e < lo || e >= hi) pr[e] = 0u;
+                }
+                if (C::HAS_P) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pk[e] = pack_bf16x2(__uint_as_float(pr[c + 2 * e]), __uint_as_float(pr[c + 2 * e + 1]));
+                    tmem_st16(tS + c, pk);
+                }
             }
             if (C::HAS_P) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(__uint_as_float(pr[2 * e]), __uint_as_float(pr[2 * e + 1]));
-                tmem_st16(tS, pk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_p_full(j % SB));
+                if (lane == 0) mbar_arrive(b_p_full((J + j) % SB));
             }
             if (C::HAS_DS) {
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_dp_full(j % DPB), (j / DPB) & 1, abort_flag)))) break;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_dp_full((J + j) % DPB), ((J + j) / DPB) & 1, abort_flag)))) break;
                 tc_fence_after();
-                uint32_t dp[32];
-                tmem_ld32(tDP, dp);
+                uint32_t dp[H];
+#pragma unroll
+                for (int c = 0; c < H; c += 32) tmem_ld32(tDP + c, *reinterpret_cast<uint32_t(*)[32]>(&dp[c]));
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float4 nd = make_float4(row_nd, row_nd, row_nd, row_nd);
-                    if (C::KEYS) nd = ld_shared_f4(st + BN * 4 + e * 4);
-                    float2 a = __fadd2_rn(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
-                                          make_float2(nd.x, nd.y));
-                    float2 b = __fadd2_rn(make_float2(__uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3])),
-                                          make_float2(nd.z, nd.w));
-                    a = __fmul2_rn(a, make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])));
-                    b = __fmul2_rn(b, make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])));
-                    dp[e] = __float_as_uint(a.x);
-                    dp[e + 1] = __float_as_uint(a.y);
-                    dp[e + 2] = __float_as_uint(b.x);
-                    dp[e + 3] = __float_as_uint(b.y);
-                }
-                if (edge) {  // 0 * (anything) is not always 0
+                for (int c = 0; c < H; c += 32) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e < lo || e >= hi) dp[e] = 0u;
-                }
-                uint32_t pk[16];
+                    for (int e = c; e < c + 32; e += 4) {
+                        float4 nd = make_float4(row_nd, row_nd, row_nd, row_nd);
+                        if (C::KEYS) nd = ld_shared_f4(st + BN * 4 + e * 4);
+                        float2 a = __fadd2_rn(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
+                                              make_float2(nd.x, nd.y));
+                        float2 b = __fadd2_rn(make_float2(__uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3])),
+                                              make_float2(nd.z, nd.w));
+                        a = __fmul2_rn(a, make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])));
+                        b = __fmul2_rn(b, make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])));
+                        dp[e] = __float_as_uint(a.x);
+                        dp[e + 1] = __float_as_uint(a.y);
+                        dp[e + 2] = __float_as_uint(b.x);
+                        dp[e + 3] = __float_as_uint(b.y);
+                    }
+                    if (edge) {  // 0 * (anything) is not always 0
 #pragma unroll
-                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1]));
-                tmem_st16(tDP, pk);
+                        for (int e = c; e < c + 32; ++e)
+                            if (e < lo || e >= hi) dp[e] = 0u;
+                    }
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pk[e] = pack_bf16x2(__uint_as_float(dp[c + 2 * e]), __uint_as_float(dp[c + 2 * e + 1]));
+                    tmem_st16(tDP + c, pk);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_ds_full(j % DPB));
+                if (lane == 0) mbar_arrive(b_ds_full((J + j) % DPB));
             }
             if (C::KEYS) {  // the statistics' buffer may be filled again
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_stat_empty(j % C::STATS));
+                if (lane == 0) mbar_arrive(b_stat_empty((J + j) % C::STATS));
             }
             if (++t == t_hi) t = t_lo;
         }
         ok = __all_sync(0xffffffffu, ok);
         if (ok && n > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(b_done, 0, abort_flag));
+            ok = __all_sync(0xffffffffu, mbar_wait(b_done, done & 1, abort_flag));
             tc_fence_after();
         }
         // ------------------------------------------------------------ epilogue
-        // Every fourth 32-column chunk of the accumulators is a warpgroup's.
+        // The warpgroups take 32-column chunks of the accumulators in turn.
         if (ok) {
-            const bool used = n > 0 && row < res_len;
+            const int res_all = GBATTN_ITEM(item, res_all);
+            const bool used = n > 0 && row < GBATTN_ITEM(item, res_len);
+            const long long to = ((static_cast<long long>(GBATTN_ITEM(item, res_start)) + row) * heads + GBATTN_ITEM(item, head)) * D;
 #pragma unroll 1
-            for (int x = wg; x < C::ACCS * (D / 32); x += 4) {
+            for (int x = wg; x < C::ACCS * (D / 32); x += WGS) {
                 const int c = x % (D / 32);
                 uint32_t o[32];
                 if (n > 0) {
                     tmem_ld32(tl + C::T_ACC + x * 32, o);
                     tmem_wait_ld();
+                    if (x + WGS >= C::ACCS * (D / 32)) {  // the warp's last chunk: the next item may sum
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_acc_free);
+                    }
                 }
                 if (row < res_all) {
                     const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && x < D / 32);
                     const float f = is_dv ? 1.f : p.scale;
                     void* base = C::KEYS ? (is_dv ? p.dv : p.dk) : p.dq;
-                    uint16_t* dst = static_cast<uint16_t*>(base) +
-                                    ((static_cast<long long>(res_start) + row) * heads + head) * D + c * 32;
+                    uint16_t* dst = static_cast<uint16_t*>(base) + to + c * 32;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint32_t w[4];
@@ -874,6 +1070,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                 }
             }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
+        if (n > 0) {
+            J += n;
+            ++done;
+        }
         }
     }
 
@@ -888,6 +1091,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    // A launch that began beside the one before it ends after it.
+    grid_dependency_wait();
+#undef GBATTN_ITEM
 }
 
 // ------------------------------------------------------------------- launches
@@ -898,53 +1104,66 @@ long long bwd_stat_stride(long long Tq, int num_docs) {
 
 namespace {
 
+// One pass, behind the launch that writes the statistics (early_wait) or beside
+// another pass: its CTAs take the SMs that one's leave.
 template <class C>
 cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                        const BwdParams& p, cudaStream_t stream) {
-    const long long items =
-        static_cast<long long>(C::KEYS ? p.tiles_k : p.tiles_q) * (C::KEYS ? p.Hkv : p.Hq) * p.num_docs;
+                        BwdParams& p, int num_sms, cudaStream_t stream) {
+    const long long items = p.items[C::KEYS ? 0 : 1];
     if (items == 0) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(attn_bwd_sm103a<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    attn_bwd_sm103a<C><<<static_cast<unsigned>(items), C::THREADS, C::SMEM_BYTES, stream>>>(tmQ, tmG, tmK, tmV, p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(items < num_sms ? items : num_sms));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attn_bwd_sm103a<C>, tmQ, tmG, tmK, tmV, static_cast<const BwdParams&>(p));
+    p.early_wait = 0;
+    return e;
 }
 
 template <int D>
 cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                     const BwdParams& p, cudaStream_t stream) {
-    if (p.max_q > 0) {
-        constexpr int PER_CTA = 256 / (D <= 64 ? 8 : (D <= 128 ? 16 : 32));
-        const long long ctas = (static_cast<long long>(p.max_q) * p.Hq + PER_CTA - 1) / PER_CTA;
-        const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(p.num_docs));
-        if (p.out_f32)
-            attn_bwd_stat_sm103a<D, true><<<grid, 256, 0, stream>>>(p);
-        else
-            attn_bwd_stat_sm103a<D, false><<<grid, 256, 0, stream>>>(p);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    cudaError_t e;
+                     BwdParams& p, int num_sms, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    constexpr int PER_CTA = 256 / (D <= 64 ? 8 : (D <= 128 ? 16 : 32));
+    // (without query rows one CTA a document still looks at its boundaries)
+    const long long ctas = p.max_q > 0 ? (static_cast<long long>(p.max_q) * p.Hq + PER_CTA - 1) / PER_CTA : 1;
+    const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(p.num_docs));
+    if (p.out_f32)
+        attn_bwd_stat_sm103a<D, true><<<grid, 256, 0, stream>>>(p);
+    else
+        attn_bwd_stat_sm103a<D, false><<<grid, 256, 0, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    p.early_wait = 1;
     if constexpr (D <= 128) {
-        e = launch_pass<BwdCfg<D, kBwdKV>>(tmQ, tmG, tmK, tmV, p, stream);
+        e = launch_pass<BwdCfg<D, kBwdKV>>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
     } else {
-        e = launch_pass<BwdCfg<D, kBwdV>>(tmQ, tmG, tmK, tmV, p, stream);
-        if (e == cudaSuccess) e = launch_pass<BwdCfg<D, kBwdK>>(tmQ, tmG, tmK, tmV, p, stream);
+        e = launch_pass<BwdCfg<D, kBwdV>>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
+        if (e == cudaSuccess) e = launch_pass<BwdCfg<D, kBwdK>>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
     }
     if (e != cudaSuccess) return e;
-    return launch_pass<BwdCfg<D, kBwdQ>>(tmQ, tmG, tmK, tmV, p, stream);
+    return launch_pass<BwdCfg<D, kBwdQ>>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_bwd(int D, const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK,
-                       const CUtensorMap& tmV, const BwdParams& p, cudaStream_t stream) {
+                       const CUtensorMap& tmV, BwdParams p, int num_sms, cudaStream_t stream) {
+    p.items[0] = static_cast<long long>(p.tiles_k) * p.Hkv * p.num_docs;
+    p.items[1] = static_cast<long long>(p.tiles_q) * p.Hq * p.num_docs;
     switch (D) {
-        case 64: return launch_d<64>(tmQ, tmG, tmK, tmV, p, stream);
-        case 96: return launch_d<96>(tmQ, tmG, tmK, tmV, p, stream);
-        case 128: return launch_d<128>(tmQ, tmG, tmK, tmV, p, stream);
-        case 192: return launch_d<192>(tmQ, tmG, tmK, tmV, p, stream);
-        case 256: return launch_d<256>(tmQ, tmG, tmK, tmV, p, stream);
+        case 64: return launch_d<64>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
+        case 96: return launch_d<96>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
+        case 128: return launch_d<128>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
+        case 192: return launch_d<192>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
+        case 256: return launch_d<256>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -287,3 +287,11 @@ def test_refusals_of_the_binding():
         gb.attn_bwd_dense(**ok, workspace=torch.empty(256, dtype=torch.uint8, device=dev()))
     with pytest.raises(ValueError):
         gb.attn_bwd_padded(**ok, lens_q=torch.zeros(2, dtype=torch.int32, device=dev()))
+
+
+@pytest.mark.parametrize("D", workloads.HEAD_SIZES)
+@pytest.mark.parametrize("causal", [False, True])
+def test_more_tiles_than_a_wave(D, causal):
+    """Several items a CTA, some without any work between them: every buffer, ring and barrier carries on from item to item."""
+    packed([130, 0, 513, 1, 250, 300], [130, 64, 260, 300, 250, 5], 48, 24, D, causal)
+    dense_case(1, 200, 200, 200, 100, D, causal)
