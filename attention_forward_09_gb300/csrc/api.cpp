@@ -201,14 +201,15 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
     p.out_f32 = out_dtype == GBATTN_OUT_F32;
     // Without rows (or keys) nothing of that side is ever loaded; its maps
     // then view the other side's tensor so that they are well-formed.
-    CUtensorMap tq, tg, tk, tv;
-    constexpr int box = 128;
+    gbattn::BwdMaps m;
     const long long rq = rows ? p.Tq : p.Tk, rk = keys ? p.Tk : p.Tq;
     const int hq = rows ? p.Hq : p.Hkv, hk = keys ? p.Hkv : p.Hq;
-    if (!encode_rows_heads_d(&tq, rows ? q : k, rq, hq, D, box) || !encode_rows_heads_d(&tg, rows ? dout : v, rq, hq, D, box) ||
-        !encode_rows_heads_d(&tk, keys ? k : q, rk, hk, D, box) || !encode_rows_heads_d(&tv, keys ? v : dout, rk, hk, D, box))
+    if (!encode_rows_heads_d(&m.q, rows ? q : k, rq, hq, D, 128) || !encode_rows_heads_d(&m.dout, rows ? dout : v, rq, hq, D, 128) ||
+        !encode_rows_heads_d(&m.k, keys ? k : q, rk, hk, D, 128) || !encode_rows_heads_d(&m.v, keys ? v : dout, rk, hk, D, 128) ||
+        !encode_rows_heads_d(&m.dq, rows ? dq : dk, rq, hq, D, 128) || !encode_rows_heads_d(&m.dk, keys ? dk : dq, rk, hk, D, 128) ||
+        !encode_rows_heads_d(&m.dv, keys ? dv : dq, rk, hk, D, 128))
         return GBATTN_ERR_CUDA;
-    return gbattn::launch_bwd(D, tq, tg, tk, tv, p, di.sms, st) == cudaSuccess ? GBATTN_OK : GBATTN_ERR_CUDA;
+    return gbattn::launch_bwd(D, m, p, di.sms, st) == cudaSuccess ? GBATTN_OK : GBATTN_ERR_CUDA;
 }
 
 // What the two calls on rotary positions have in common; `p` comes with their sizes.

@@ -88,8 +88,9 @@ struct BwdCfg {
     static constexpr int MATH_WARPS = 8, MATH_WGS = MATH_WARPS / 4, H = BN / MATH_WGS;  // H columns a thread
     static constexpr int REG_MATH = 208, REG_OTHER = 88;       // setmaxnreg split of 384 x 168
     static constexpr int THREADS = 32 * MATH_WARPS + 128;
+    static constexpr int STAGE1 = NCK, STAGE2 = ACCS == 2 ? NCK : 0;  // slots of each ring that an item's gradients leave through
     static constexpr int ITEMS = 3;                            // items published ahead
-    static constexpr int BARS_FIXED = 18 + 2 * ITEMS + 2 * STATS;
+    static constexpr int BARS_FIXED = 24 + 2 * ITEMS + 2 * STATS;
     static constexpr int RELEASES = HAS_DS && !SHARED ? 2 : 1;  // commits that release a slot
     static constexpr int ROOM = 232448 - RES_SMEM * R_BYTES - STATS * STAT_BYTES - 16 - ITEMS * 64 - BARS_FIXED * 8;
     static constexpr int FIT = ROOM / (C_BYTES + 16);
@@ -106,6 +107,7 @@ struct BwdCfg {
     static_assert(MATH_WARPS * 32 * REG_MATH + 128 * REG_OTHER <= THREADS * 168, "register split");
     static_assert(T_RES + RES_TMEM * D / 2 <= 512, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(C_BYTES == CCH * BM * 128, "a slot holds a chunk of a gradient tile");
     static_assert(!HAS_DS || (N2 >= NCK && N1 > NCK && N1 >= G0), "the rings hold what the issuing warps wait for at once");
     static_assert(SMEM_BYTES > 116 * 1024, "one CTA an SM: it takes all TMEM columns");
     static_assert(NCH % NCK == 0 && D % 32 == 0 && (RES_TMEM == 0 || D % 64 == 0), "tile shape");
@@ -282,6 +284,7 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     attn_bwd_sm103a(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmO1, const __grid_constant__ CUtensorMap tmO2,
                     const BwdParams p) {
     constexpr int D = C::D, BM = C::BM, BN = C::BN, NCH = C::NCH, NCK = C::NCK, CCH = C::CCH, SLOTS = C::SLOTS;
     constexpr int SB = C::SB, DPB = C::DPB, G0 = C::G0, MW = C::MATH_WARPS, WGS = C::MATH_WGS, H = C::H;
@@ -294,17 +297,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     auto b_res = [&](int r) { return smem_u32(&bars[r]); };
     auto b_s_full = [&](int b) { return smem_u32(&bars[2 + b]); };
-    auto b_p_full = [&](int b) { return smem_u32(&bars[4 + b]); };  // P is there (without dV: S has been read)
-    auto b_dp_full = [&](int b) { return smem_u32(&bars[6 + b]); };
-    auto b_ds_full = [&](int b) { return smem_u32(&bars[8 + b]); };
-    auto b_turn = [&](int b) { return smem_u32(&bars[10 + b]); };
-    const uint32_t b_done = smem_u32(&bars[12]), b_drain = smem_u32(&bars[13]), b_res_in = smem_u32(&bars[14]);
-    const uint32_t b_acc_free = smem_u32(&bars[15]);  // the accumulators have been read
-    auto b_res_free = [&](int r) { return smem_u32(&bars[16 + r]); };
-    auto b_item_full = [&](int b) { return smem_u32(&bars[18 + b]); };
-    auto b_item_free = [&](int b) { return smem_u32(&bars[18 + C::ITEMS + b]); };
-    auto b_stat_full = [&](int b) { return smem_u32(&bars[18 + 2 * C::ITEMS + b]); };
-    auto b_stat_empty = [&](int b) { return smem_u32(&bars[18 + 2 * C::ITEMS + C::STATS + b]); };
+    // P is there: of each warpgroup's columns the first 32, or the rest
+    // (without dV, the first: S has been read)
+    auto b_p_full = [&](int b, int half) { return smem_u32(&bars[4 + b + 2 * half]); };
+    auto b_dp_full = [&](int b) { return smem_u32(&bars[8 + b]); };
+    auto b_ds_full = [&](int b) { return smem_u32(&bars[10 + b]); };
+    auto b_turn = [&](int b) { return smem_u32(&bars[12 + b]); };
+    const uint32_t b_done = smem_u32(&bars[14]), b_drain = smem_u32(&bars[15]), b_res_in = smem_u32(&bars[16]);
+    const uint32_t b_acc_free = smem_u32(&bars[17]);  // the accumulators have been read
+    auto b_res_free = [&](int r) { return smem_u32(&bars[18 + r]); };
+    auto b_staged = [&](int a) { return smem_u32(&bars[20 + a]); };  // a gradient tile lies in its slots
+    auto b_copied = [&](int a) { return smem_u32(&bars[22 + a]); };  // what goes row by row has been read from them
+    auto b_item_full = [&](int b) { return smem_u32(&bars[24 + b]); };
+    auto b_item_free = [&](int b) { return smem_u32(&bars[24 + C::ITEMS + b]); };
+    auto b_stat_full = [&](int b) { return smem_u32(&bars[24 + 2 * C::ITEMS + b]); };
+    auto b_stat_empty = [&](int b) { return smem_u32(&bars[24 + 2 * C::ITEMS + C::STATS + b]); };
     volatile int* const items = reinterpret_cast<volatile int*>(tmem_slot + 4);
     auto b_full = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + s]); };
     auto b_empty = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + SLOTS + s]); };
@@ -395,10 +402,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(b_res(b), 1);
             mbar_init(b_s_full(b), 1);
-            mbar_init(b_p_full(b), MW);
+            mbar_init(b_p_full(b, 0), MW);
+            mbar_init(b_p_full(b, 1), MW);
             mbar_init(b_dp_full(b), 1);
             mbar_init(b_ds_full(b), MW);
             mbar_init(b_turn(b), 1);
+            mbar_init(b_staged(b), C::ACCS == 2 ? 4 : MW);
+            mbar_init(b_copied(b), C::ACCS == 2 ? 4 : MW);
         }
         mbar_init(b_done, C::ISSUERS);
         mbar_init(b_drain, C::ISSUERS);
@@ -454,6 +464,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         mbar_arrive_expect_tx(b_full(r.s), C::C_BYTES);
         for (int c = 0; c < CCH; ++c)
             tma_load_3d(r.base + r.s * C::C_BYTES + c * (BN * 128), m, b_full(r.s), (chunk * CCH + c) * 64, h, row);
+        r.next();
+        return true;
+    };
+    // The ring's next slot, once free, for the math warps to write an item's gradients through.
+    auto grant = [&](Ring& r) -> bool {
+        if (r.issued >= r.size && !mbar_wait(b_empty(r.s), r.ph ^ 1u, abort_flag)) return false;
+        mbar_arrive(b_full(r.s));
         r.next();
         return true;
     };
@@ -519,6 +536,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h2, it.str_start + t2 * BN, c);
                 }
             }
+            for (int c = 0; ok && c < C::STAGE1; ++c) ok = grant(ring);
             ++done;
         }
         if (!ok || *abort_flag) {
@@ -564,6 +582,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     ++h;
                 }
             }
+            for (int c = 0; ok && n > 0 && c < C::STAGE2; ++c) ok = grant(ring);
         }
         if (!ok || *abort_flag) {
             drain(ring);
@@ -616,13 +635,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         };
         // columns [c CW, (c + 1) CW) of acc += A (bf16 pairs in X's columns, 16
         // of every 32) * chunk c of a streamed tile, in slot s
-        auto accumulate = [&](uint32_t acc, uint32_t x, int c, int s, bool first) {
+        // Of the rows, those of the warpgroups' first 32 columns (half 0), the
+        // rest (half 1) or all (half 2).
+        auto accumulate = [&](uint32_t acc, uint32_t x, int c, int s, bool first, int half) {
             uint32_t a = tmem + x, b = dCm + s * (C::C_BYTES >> 4);
             asm volatile("" : "+r"(a), "+r"(b));
 #pragma unroll
             for (int k = 0; k < BN / 16; ++k)
-                mma_ts(tmem + acc + c * C::CW, a + (k >> 1) * 32 + (k & 1) * 8, b + ((k * 16 * 128) >> 4), kIdA,
-                       (!first || k > 0) ? 1u : 0u);
+                if (half == 2 || ((k >> 1) & 1) == half)
+                    mma_ts(tmem + acc + c * C::CW, a + (k >> 1) * 32 + (k & 1) * 8, b + ((k * 16 * 128) >> 4), kIdA,
+                           (!first || k > 0) ? 1u : 0u);
         };
         // Cursors: the next chunk of C1 and of C2 that this warp uses.
         Ring c1(sC, 0, C::N1), c2(sC, C::N1, C::N2);
@@ -695,7 +717,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             };
             ok = ok && wait_all(b_res(0), done & 1) && next_s(0);
             for (int j = 0; ok && j < n; ++j) {
-                if (!(ok = landed(c2) && wait_all(b_p_full(0), (J + j) & 1))) break;
+                if (!(ok = landed(c2) && wait_all(b_p_full(0, 0), (J + j) & 1))) break;
                 tc_fence_after();
                 if (leader) {
                     Ring s = c2;
@@ -720,7 +742,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (leader) {
                     Ring s = c1;
                     for (int c = 0; c < NCK; ++c) {
-                        accumulate(C::T_ACC, C::T_DP, c, s.s, j == 0);
+                        accumulate(C::T_ACC, C::T_DP, c, s.s, j == 0, 2);
                         mma_commit(b_empty(s.s));
                         s.next();
                     }
@@ -753,7 +775,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     // P(j) first: the slots' last turns were S(j)'s tiles or
                     // earlier ones, and a wait by parity is exact only once
                     // those have landed.
-                    if (!(ok = (j > 0 || acc_free()) && wait_all(b_p_full((J + j) % SB), ((J + j) / SB) & 1) && landed(c1)))
+                    if (!(ok = (j > 0 || acc_free()) && wait_all(b_p_full((J + j) % SB, 0), ((J + j) / SB) & 1) && landed(c1)))
                         break;
                     if (edge_rows(t)) {
                         Ring s = c1;
@@ -762,17 +784,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             s.next();
                         }
                     }
-                    tc_fence_after();
-                    if (leader) {
-                        Ring s = c1;
-                        for (int c = 0; c < NCK; ++c) {
-                            accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, c, s.s, j == 0);
-                            mma_commit(b_empty(s.s));
-                            s.next();
+                    for (int half = 0; half < 2; ++half) {
+                        if (half && !(ok = wait_all(b_p_full((J + j) % SB, 1), ((J + j) / SB) & 1))) break;
+                        tc_fence_after();
+                        if (leader) {
+                            Ring s = c1;
+                            for (int c = 0; c < NCK; ++c) {
+                                accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, c, s.s, j == 0 && half == 0, half);
+                                if (half) mma_commit(b_empty(s.s));
+                                s.next();
+                            }
+                            if (half) mma_commit(b_turn((J + j) % SB));
                         }
-                        mma_commit(b_turn((J + j) % SB));
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok) break;
                     c1 = moved(c1);
                     if (j + 2 < n) c1 = moved(c1);  // past the queries' tile of step j + 2
                     if (++t == t_hi) t = t_lo;
@@ -800,11 +826,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (!(ok = wait_all(b_full(c2.s), c2.ph) && (j > 0 || acc_free()))) break;
                     if (edge_rows(t)) zero_rows(c2.s, t);
                 }
-                if (!(ok = wait_all(b_p_full((J + j) % SB), ((J + j) / SB) & 1))) break;
+                if (!(ok = wait_all(b_p_full((J + j) % SB, 0), ((J + j) / SB) & 1))) break;
                 tc_fence_after();
+                if (C::HAS_P) {  // the first half of P's columns while the math warps work on the second
+                    if (leader) accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, 0, c2.s, j == 0, 0);
+                    __syncwarp();
+                    if (!(ok = wait_all(b_p_full((J + j) % SB, 1), ((J + j) / SB) & 1))) break;
+                    tc_fence_after();
+                }
                 if (leader) {
                     if (C::HAS_P) {
-                        accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, 0, c2.s, j == 0);
+                        accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, 0, c2.s, false, 1);
                         mma_commit(b_empty(c2.s));
                     }
                     if (more && SB == 1) issue_s(j + 1, c1, true);
@@ -848,7 +880,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (C::HAS_P && SB == 1 && !(ok = wait_all(b_turn((J + j) & 1), ((J + j) >> 1) & 1))) break;
                 tc_fence_after();
                 if (leader) {
-                    accumulate(kAcc, C::T_DP + ((J + j) % DPB) * BN, 0, c1.s, j == 0);
+                    accumulate(kAcc, C::T_DP + ((J + j) % DPB) * BN, 0, c1.s, j == 0, 2);
                     mma_commit(b_empty(c1.s));
                     if (more && DPB == 1) issue_dp(j + 1);
                 }
@@ -860,6 +892,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (ok && leader) mma_commit(b_done);
         __syncwarp();
         if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
+        for (int c = 0; c < C::STAGE1; ++c) c1.next();
+        for (int c = 0; c < C::STAGE2; ++c) c2.next();
         J += n;
         ++done;
         }
@@ -878,7 +912,30 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!C::KEYS && p.early_wait) grid_dependency_wait();  // the launch before this one writes the statistics
         int J = 0;     // steps of the items so far: buffers and phases go by J + j
         int done = 0;  // items with steps so far
-        Ring res_ring(sC, 0, C::N1);  // where residents that go to tensor memory come in
+        Ring ring1(sC, 0, C::N1), ring2(sC, C::N1, C::N2);  // where the next item's loads begin
+        auto ahead = [](Ring& r, int by) {
+            const int x = r.s - r.begin + by;
+            r.s = r.begin + x % r.size;
+            r.ph ^= (x / r.size) & 1;
+        };
+        // An item's gradients leave through ring slots by TMA; the thread that
+        // stores one gives its slots back once they have been read, which it
+        // looks after in the next item's first step.  (Where the next item's
+        // first tiles themselves need those slots, before it: RES_TMEM.)
+        const bool storer = lane == 0 && (warp == 0 || (C::ACCS == 2 && warp == 4));
+        int leaving = -1;  // the first of the slots that are being read
+        auto give_back = [&]() {
+            if (storer && leaving >= 0) {
+                bulk_wait_read0();
+                ok = mbar_wait(b_copied(C::ACCS == 2 ? wg : 0), (done - 1) & 1, abort_flag);
+                int s = leaving;
+                for (int c = 0; c < NCK; ++c) {
+                    for (int x = 0; x < C::RELEASES; ++x) mbar_arrive(b_empty(s));
+                    if (++s == (wg ? C::N1 + C::N2 : C::N1)) s = wg ? C::N1 : 0;
+                }
+                leaving = -1;
+            }
+        };
 #pragma unroll 1
         for (int item = 0; ok; ++item) {
         const int n = next_item(item, true);
@@ -894,9 +951,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             row_nd = p.neg_delta[at];
         }
         if (C::RES_TMEM > 0 && n > 0) {
+            give_back();
+            ok = __all_sync(0xffffffffu, ok);
             // residents that go to tensor memory: the warpgroups copy 64-column blocks in turn
             for (int b = wg; ok && b < C::RES_TMEM * NCH; b += WGS) {
-                Ring at = res_ring;  // blocks lie in the order they were loaded
+                Ring at = ring1;  // blocks lie in the order they were loaded
                 for (int c = 0; c < b / CCH; ++c) at.next();
                 const int s = at.s;
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_full(s), at.ph, abort_flag)))) break;
@@ -919,35 +978,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_res_in);
             }
-            // the next item's come G0 + n NCK loads on
-            const int by = G0 + n * NCK, turns = (res_ring.s + by) / C::N1;
-            res_ring.s = (res_ring.s + by) % C::N1;
-            res_ring.ph ^= turns & 1;
         }
-        // streamed rows [see_lo, see_hi) are visible
-        const int diag = GBATTN_ITEM(item, diag), str_len = GBATTN_ITEM(item, str_len);
+        // streamed rows [see_lo, see_hi) are visible; below tile edge_lo and from
+        // edge_hi on some row of the item sees only part of a tile
+        const int diag = GBATTN_ITEM(item, diag), str_len = GBATTN_ITEM(item, str_len), r0 = GBATTN_ITEM(item, r0);
         const int see_lo = C::KEYS && p.causal ? row - diag : 0;
         const int see_hi = !C::KEYS && p.causal ? min(str_len, row + diag + 1) : str_len;
+        const int edge_lo = C::KEYS && p.causal ? (max(0, r0 + BM - 1 - diag) + BN - 1) / BN : 0;
+        const int edge_hi = max(0, !C::KEYS && p.causal ? min(str_len, r0 + diag + 1) : str_len) / BN;
         const int t_lo = GBATTN_ITEM(item, t_lo), t_hi = GBATTN_ITEM(item, t_hi);
         int t = t_lo;
+#pragma unroll 1
         for (int j = 0; ok && j < n; ++j) {
+            const int g = J + j, sb = g % SB, db = g % DPB;
+            const bool edge = t < edge_lo || t >= edge_hi;
             const int c0 = t * BN + wg * H;  // this thread's first streamed row
             const int lo = see_lo - c0, hi = see_hi - c0;
-            const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < H);
-            const uint32_t st = sStat + ((J + j) % C::STATS) * C::STAT_BYTES + wg * (H * 4);
-            if (C::KEYS) ok = mbar_wait(b_stat_full((J + j) % C::STATS), ((J + j) / C::STATS) & 1, abort_flag);
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(b_s_full((J + j) % SB), ((J + j) / SB) & 1, abort_flag));
-            if (!ok) break;
+            const uint32_t st = sStat + (g % C::STATS) * C::STAT_BYTES + wg * (H * 4);
+            const uint32_t tS = tl + C::T_S + sb * BN + wg * H, tDP = tl + C::T_DP + db * BN + wg * H;
+            if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(b_s_full(sb), (g / SB) & 1, abort_flag)))) break;
             tc_fence_after();
-            const uint32_t tS = tl + C::T_S + ((J + j) % SB) * BN + wg * H, tDP = tl + C::T_DP + ((J + j) % DPB) * BN + wg * H;
             uint32_t pr[H];  // P, fp32
 #pragma unroll
             for (int c = 0; c < H; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&pr[c]));
+            if (C::KEYS) ok = __all_sync(0xffffffffu, mbar_wait(b_stat_full(g % C::STATS), (g / C::STATS) & 1, abort_flag));
             tmem_wait_ld();
+            if (!ok) break;
             if (!C::HAS_P) {  // the S buffer may be written again
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_p_full((J + j) % SB));
+                if (lane == 0) mbar_arrive(b_p_full(sb, 0));
             }
             const float2 cc = make_float2(c2, c2);
 #pragma unroll
@@ -976,16 +1036,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int e = 0; e < 16; ++e)
                         pk[e] = pack_bf16x2(__uint_as_float(pr[c + 2 * e]), __uint_as_float(pr[c + 2 * e + 1]));
                     tmem_st16(tS + c, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_p_full(sb, c / 32));
                 }
             }
-            if (C::HAS_P) {
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_p_full((J + j) % SB));
-            }
+            if (C::HAS_P && j == 0) give_back();
             if (C::HAS_DS) {
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_dp_full((J + j) % DPB), ((J + j) / DPB) & 1, abort_flag)))) break;
+                if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(b_dp_full(db), (g / DPB) & 1, abort_flag)))) break;
                 tc_fence_after();
                 uint32_t dp[H];
 #pragma unroll
@@ -1022,13 +1081,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_ds_full((J + j) % DPB));
+                if (lane == 0) mbar_arrive(b_ds_full(db));
             }
             if (C::KEYS) {  // the statistics' buffer may be filled again
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_stat_empty((J + j) % C::STATS));
+                if (!C::HAS_DS) __syncwarp();
+                if (lane == 0) mbar_arrive(b_stat_empty(g % C::STATS));
             }
             if (++t == t_hi) t = t_lo;
+            if (!C::HAS_P && j == 0) give_back();
         }
         ok = __all_sync(0xffffffffu, ok);
         if (ok && n > 0) {
@@ -1036,39 +1096,86 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             tc_fence_after();
         }
         // ------------------------------------------------------------ epilogue
-        // The warpgroups take 32-column chunks of the accumulators in turn.
+        // With two accumulators (dV, dK) each is a warpgroup's; of one the 32
+        // column chunks are taken in turn.  Rows are staged in the ring's slots,
+        // in the boxes' swizzle, and leave by TMA where the tile lies wholly
+        // inside its document, else row by row.
         if (ok) {
-            const int res_all = GBATTN_ITEM(item, res_all);
-            const bool used = n > 0 && row < GBATTN_ITEM(item, res_len);
-            const long long to = ((static_cast<long long>(GBATTN_ITEM(item, res_start)) + row) * heads + GBATTN_ITEM(item, head)) * D;
+            const int res_all = GBATTN_ITEM(item, res_all), res_len = GBATTN_ITEM(item, res_len);
+            const int head = GBATTN_ITEM(item, head), res_start = GBATTN_ITEM(item, res_start);
+            constexpr int PARTS = C::ACCS == 2 ? 1 : WGS;       // warpgroups that share an accumulator
+            const int acc = C::ACCS == 2 ? wg : 0, part = C::ACCS == 2 ? 0 : wg;
+            const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && acc == 0);
+            const float f = is_dv ? 1.f : p.scale;
+            uint16_t* const out = static_cast<uint16_t*>(C::KEYS ? (is_dv ? p.dv : p.dk) : p.dq);
+            auto row_ptr = [&](int i) { return out + ((static_cast<long long>(res_start) + r0 + i) * heads + head) * D; };
+            const int tid = (warp & 3) * 32 + lane + part * 128;  // among the threads that share the accumulator
+            constexpr int THR = 128 * PARTS, U = D / 8;            // 16-byte pieces of a row
+            const int rows = min(BM, res_all - r0);
+            if (n == 0) {
+                for (int x = tid; x < rows * U; x += THR) st_global_v4(row_ptr(x / U) + (x % U) * 8, 0u, 0u, 0u, 0u);
+            } else {
+                ahead(ring1, G0 + n * NCK * (C::HAS_DS ? 1 : 2));
+                if (C::ACCS == 2) ahead(ring2, n * NCK);
+                const Ring stage = acc ? ring2 : ring1;
+                Ring at = stage;
+                const bool used = row < res_len;
 #pragma unroll 1
-            for (int x = wg; x < C::ACCS * (D / 32); x += WGS) {
-                const int c = x % (D / 32);
-                uint32_t o[32];
-                if (n > 0) {
-                    tmem_ld32(tl + C::T_ACC + x * 32, o);
-                    tmem_wait_ld();
-                    if (x + WGS >= C::ACCS * (D / 32)) {  // the warp's last chunk: the next item may sum
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(b_acc_free);
-                    }
-                }
-                if (row < res_all) {
-                    const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && x < D / 32);
-                    const float f = is_dv ? 1.f : p.scale;
-                    void* base = C::KEYS ? (is_dv ? p.dv : p.dk) : p.dq;
-                    uint16_t* dst = static_cast<uint16_t*>(base) + to + c * 32;
+                for (int c = 0; c < NCK; ++c) {
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_full(at.s), at.ph, abort_flag)))) break;
+                    const uint32_t to = sC + at.s * C::C_BYTES + r * 128;
+#pragma unroll 1
+                    for (int x = part; x < C::CW / 32; x += PARTS) {
+                        uint32_t o[32];
+                        tmem_ld32(tl + C::T_ACC + acc * D + c * C::CW + x * 32, o);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t w[4];
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t w[4];
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            w[y] = used ? pack_bf16x2(__uint_as_float(o[e + 2 * y]) * f, __uint_as_float(o[e + 2 * y + 1]) * f)
-                                        : 0u;
-                        st_global_v4(dst + e, w[0], w[1], w[2], w[3]);
+                            for (int y = 0; y < 4; ++y)
+                                w[y] = used ? pack_bf16x2(__uint_as_float(o[8 * u + 2 * y]) * f, __uint_as_float(o[8 * u + 2 * y + 1]) * f)
+                                            : 0u;
+                            st_shared_v4(to + (x >> 1) * (BM * 128) + ((((x & 1) * 4 + u) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        }
                     }
+                    at.next();
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_acc_free);  // the next item may sum
+                fence_proxy_async_smem();                // generic-proxy writes -> the TMA engine
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_staged(acc));
+                if (ok && (storer || rows < BM)) ok = mbar_wait(b_staged(acc), done & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && rows == BM) {
+                    if (storer) {
+                        at = stage;
+                        for (int c = 0; c < NCK; ++c) {
+                            for (int b = 0; b < CCH; ++b)
+                                tma_store_3d(acc ? &tmO2 : &tmO1, sC + at.s * C::C_BYTES + b * (BM * 128), (c * CCH + b) * 64, head,
+                                             res_start + r0);
+                            at.next();
+                        }
+                        bulk_commit();
+                        leaving = stage.s;
+                    }
+                } else if (ok) {
+                    for (int x = tid; x < rows * U; x += THR) {
+                        const int i = x / U, u = x % U, b = u / 8;
+                        at = stage;
+                        for (int c = 0; c < b / CCH; ++c) at.next();
+                        const float4 v = ld_shared_f4(sC + at.s * C::C_BYTES + (b % CCH) * (BM * 128) + i * 128 + (((u & 7) ^ (i & 7)) << 4));
+                        st_global_v4(row_ptr(i) + u * 8, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                                     __float_as_uint(v.w));
+                    }
+                    if (storer) leaving = stage.s;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_copied(acc));
+                ahead(ring1, C::STAGE1);
+                if (C::ACCS == 2) ahead(ring2, C::STAGE2);
             }
         }
         __syncwarp();
@@ -1078,6 +1185,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             ++done;
         }
         }
+        give_back();
     }
 
     // --------------------------------------------------------------- teardown
@@ -1107,8 +1215,8 @@ namespace {
 // One pass, behind the launch that writes the statistics (early_wait) or beside
 // another pass: its CTAs take the SMs that one's leave.
 template <class C>
-cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                        BwdParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_pass(const BwdMaps& m, const CUtensorMap& o1, const CUtensorMap& o2, BwdParams& p, int num_sms,
+                        cudaStream_t stream) {
     const long long items = p.items[C::KEYS ? 0 : 1];
     if (items == 0) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(attn_bwd_sm103a<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
@@ -1123,14 +1231,13 @@ cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmG, const CU
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_bwd_sm103a<C>, tmQ, tmG, tmK, tmV, static_cast<const BwdParams&>(p));
+    e = cudaLaunchKernelEx(&cfg, attn_bwd_sm103a<C>, m.q, m.dout, m.k, m.v, o1, o2, static_cast<const BwdParams&>(p));
     p.early_wait = 0;
     return e;
 }
 
 template <int D>
-cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                     BwdParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_d(const BwdMaps& m, BwdParams& p, int num_sms, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
     constexpr int PER_CTA = 256 / (D <= 64 ? 8 : (D <= 128 ? 16 : 32));
     // (without query rows one CTA a document still looks at its boundaries)
@@ -1143,27 +1250,26 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUten
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     p.early_wait = 1;
     if constexpr (D <= 128) {
-        e = launch_pass<BwdCfg<D, kBwdKV>>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
+        e = launch_pass<BwdCfg<D, kBwdKV>>(m, m.dv, m.dk, p, num_sms, stream);
     } else {
-        e = launch_pass<BwdCfg<D, kBwdV>>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
-        if (e == cudaSuccess) e = launch_pass<BwdCfg<D, kBwdK>>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
+        e = launch_pass<BwdCfg<D, kBwdV>>(m, m.dv, m.dv, p, num_sms, stream);
+        if (e == cudaSuccess) e = launch_pass<BwdCfg<D, kBwdK>>(m, m.dk, m.dk, p, num_sms, stream);
     }
     if (e != cudaSuccess) return e;
-    return launch_pass<BwdCfg<D, kBwdQ>>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
+    return launch_pass<BwdCfg<D, kBwdQ>>(m, m.dq, m.dq, p, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_bwd(int D, const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK,
-                       const CUtensorMap& tmV, BwdParams p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_bwd(int D, const BwdMaps& m, BwdParams p, int num_sms, cudaStream_t stream) {
     p.items[0] = static_cast<long long>(p.tiles_k) * p.Hkv * p.num_docs;
     p.items[1] = static_cast<long long>(p.tiles_q) * p.Hq * p.num_docs;
     switch (D) {
-        case 64: return launch_d<64>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
-        case 96: return launch_d<96>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
-        case 128: return launch_d<128>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
-        case 192: return launch_d<192>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
-        case 256: return launch_d<256>(tmQ, tmG, tmK, tmV, p, num_sms, stream);
+        case 64: return launch_d<64>(m, p, num_sms, stream);
+        case 96: return launch_d<96>(m, p, num_sms, stream);
+        case 128: return launch_d<128>(m, p, num_sms, stream);
+        case 192: return launch_d<192>(m, p, num_sms, stream);
+        case 256: return launch_d<256>(m, p, num_sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -346,9 +346,11 @@ struct BwdParams {
     int early_wait;         // 1: the launch before this one writes the statistics
 };
 long long bwd_stat_stride(long long Tq, int num_docs);
-// tmQ, tmG (dout), tmK, tmV: [rows, heads, D] bf16, box {64, 1, 128}, 128-byte swizzle.
-cudaError_t launch_bwd(int D, const CUtensorMap& tmQ, const CUtensorMap& tmG, const CUtensorMap& tmK,
-                       const CUtensorMap& tmV, BwdParams p, int num_sms, cudaStream_t stream);
+// [rows, heads, D] bf16, boxes {64, 1, 128}, 128-byte swizzle.
+struct BwdMaps {
+    CUtensorMap q, dout, k, v, dq, dk, dv;
+};
+cudaError_t launch_bwd(int D, const BwdMaps& m, BwdParams p, int num_sms, cudaStream_t stream);
 
 // Rotary positions (rotary.cu) of q and k; with slot_mapping k_out is the
 // paged cache [2, num_slots, Hkv, D] and v is stored beside the keys.
