@@ -174,7 +174,7 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
     constexpr long long kMost = 0x7fffffffLL;
     const long long qh = static_cast<long long>(p.tiles_q) * p.num_docs, kh = static_cast<long long>(p.tiles_k) * p.num_docs;
     if (qh > kMost / p.Hq || kh > kMost / p.Hkv) return GBATTN_ERR_UNSUPPORTED;
-    if (static_cast<long long>(p.max_q) > kMost / p.Hq * 8) return GBATTN_ERR_UNSUPPORTED;
+    if ((p.Hq + 31) / 32 > 65535) return GBATTN_ERR_UNSUPPORTED;
     if (!rows && !keys) return GBATTN_OK;
     const size_t stat = bwd_stat_bytes(p.Tq, p.num_docs, p.Hq);
     if (!workspace || workspace_bytes < 2 * stat || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)

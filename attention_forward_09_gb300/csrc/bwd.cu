@@ -208,53 +208,71 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
 }  // namespace
 
 // ------------------------------------------------------------- row statistics
-// LANES lanes a (row, head); reads 16 bytes of dout and 16 or 32 of out a lane.
+// A CTA takes `rows` query rows of `heads` heads, 256 (row, head) pairs at
+// most: rows of dout and out are read whole, LANES lanes a pair and UN pairs in
+// flight a lane; the results cross shared memory, so that a head's statistics
+// are read and written for eight rows or more at a time.
 template <int D, bool F32>
-__global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p) {
-    constexpr int LANES = D <= 64 ? 8 : (D <= 128 ? 16 : 32), PER_CTA = 256 / LANES;
-    const int doc = blockIdx.y;
-    const BwdDoc d = bwd_doc(p, doc, threadIdx.x == 0 && blockIdx.x == 0);
+__global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, const int rows, const int heads) {
+    constexpr int LANES = D <= 64 ? 8 : (D <= 128 ? 16 : 32), UN = 4, PER_WARP = 32 / LANES;
+    __shared__ float dots[256];
+    grid_launch_dependents();
+    const int doc = blockIdx.z;
+    const BwdDoc d = bwd_doc(p, doc, threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0);
     if (d.bad) return;
-    const int sub = threadIdx.x % LANES;
-    const long long pair = static_cast<long long>(blockIdx.x) * PER_CTA + threadIdx.x / LANES;
-    const int i = static_cast<int>(pair / p.Hq), h = static_cast<int>(pair % p.Hq);
-    const bool live = i < d.Lq;
-    float acc = 0.f;
-    if (live && sub * 8 < D) {
-        const long long at = ((static_cast<long long>(d.q_start) + i) * p.Hq + h) * D + sub * 8;
-        const uint4 g = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dout) + at));
-        const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
-        float o[8];
-        if (F32) {
-            const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.out) + at);
-            const float4 a = __ldg(src), b = __ldg(src + 1);
-            o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
-        } else {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out) + at));
-            const uint32_t ow[4] = {w.x, w.y, w.z, w.w};
+    const long long i0 = static_cast<long long>(blockIdx.x) * rows;
+    if (i0 >= d.Lq) return;
+    const int h0 = blockIdx.y * heads, nh = min(heads, p.Hq - h0), nr = static_cast<int>(min(static_cast<long long>(rows), d.Lq - i0));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
+    for (int u0 = warp * PER_WARP + lane / LANES; u0 - lane / LANES < nr * nh; u0 += 8 * PER_WARP * UN) {
+        uint4 g[UN], o[UN], o2[UN];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack_bf16x2(ow[e]);
-                o[2 * e] = f.x, o[2 * e + 1] = f.y;
+        for (int x = 0; x < UN; ++x) {
+            const int u = u0 + x * 8 * PER_WARP;
+            g[x] = o[x] = o2[x] = make_uint4(0u, 0u, 0u, 0u);
+            if (u < nr * nh && sub * 8 < D) {
+                const int i = u / nh, h = h0 + u % nh;
+                const long long at = ((d.q_start + i0 + i) * p.Hq + h) * D + sub * 8;
+                g[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dout) + at));
+                if (F32) {
+                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const float*>(p.out) + at);
+                    o[x] = __ldg(src);
+                    o2[x] = __ldg(src + 1);
+                } else {
+                    o[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out) + at));
+                }
             }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack_bf16x2(gw[e]);
-            acc = fmaf(f.x, o[2 * e], acc);
-            acc = fmaf(f.y, o[2 * e + 1], acc);
+        for (int x = 0; x < UN; ++x) {
+            const uint32_t gw[4] = {g[x].x, g[x].y, g[x].z, g[x].w};
+            const uint32_t ow[8] = {o[x].x, o[x].y, o[x].z, o[x].w, o2[x].x, o2[x].y, o2[x].z, o2[x].w};
+            float acc = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack_bf16x2(gw[e]);
+                const float2 v = F32 ? make_float2(__uint_as_float(ow[2 * e]), __uint_as_float(ow[2 * e + 1])) : unpack_bf16x2(ow[e]);
+                acc = fmaf(f.x, v.x, acc);
+                acc = fmaf(f.y, v.y, acc);
+            }
+#pragma unroll
+            for (int s = LANES / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
+            const int u = u0 + x * 8 * PER_WARP;
+            if (sub == 0 && u < nr * nh) dots[(u % nh) * rows + u / nh] = acc;
         }
     }
-#pragma unroll
-    for (int s = LANES / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
-    if (live && sub == 0) {
-        const long long row = p.lse_row_global ? static_cast<long long>(d.q_start) + i : i;
-        const long long at = doc * p.lse_bstride + h * p.lse_hstride + row;
-        const long long to = h * p.stat_stride + bwd_stat_base(d.q_start, doc) + i;
+    __syncthreads();
+    const long long base = bwd_stat_base(d.q_start, doc);
+    for (int x = threadIdx.x; x < nh * rows; x += 256) {
+        const int h = h0 + x / rows;
+        const long long i = i0 + x % rows;
+        if (i >= d.Lq) continue;
+        const long long at = doc * p.lse_bstride + h * p.lse_hstride + (p.lse_row_global ? d.q_start + i : i);
+        const long long to = h * p.stat_stride + base + i;
         // a row that sees no key (lse = -inf) has p = 2^(s - inf) = 0
         const float lse = p.lse[at];
         p.neg_lse2[to] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
-        p.neg_delta[to] = (p.dlse ? p.dlse[at] : 0.f) - acc;
+        p.neg_delta[to] = (p.dlse ? p.dlse[at] : 0.f) - dots[x];
     }
 }
 
@@ -784,21 +802,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             s.next();
                         }
                     }
-                    for (int half = 0; half < 2; ++half) {
-                        if (half && !(ok = wait_all(b_p_full((J + j) % SB, 1), ((J + j) / SB) & 1))) break;
-                        tc_fence_after();
-                        if (leader) {
-                            Ring s = c1;
-                            for (int c = 0; c < NCK; ++c) {
-                                accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, c, s.s, j == 0 && half == 0, half);
-                                if (half) mma_commit(b_empty(s.s));
-                                s.next();
-                            }
-                            if (half) mma_commit(b_turn((J + j) % SB));
+                    tc_fence_after();
+                    if (leader) {
+                        Ring s = c1;
+                        for (int c = 0; c < NCK; ++c) {
+                            accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, c, s.s, j == 0, 2);
+                            mma_commit(b_empty(s.s));
+                            s.next();
                         }
-                        __syncwarp();
+                        mma_commit(b_turn((J + j) % SB));
                     }
-                    if (!ok) break;
+                    __syncwarp();
                     c1 = moved(c1);
                     if (j + 2 < n) c1 = moved(c1);  // past the queries' tile of step j + 2
                     if (++t == t_hi) t = t_lo;
@@ -828,15 +842,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 if (!(ok = wait_all(b_p_full((J + j) % SB, 0), ((J + j) / SB) & 1))) break;
                 tc_fence_after();
-                if (C::HAS_P) {  // the first half of P's columns while the math warps work on the second
-                    if (leader) accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, 0, c2.s, j == 0, 0);
-                    __syncwarp();
-                    if (!(ok = wait_all(b_p_full((J + j) % SB, 1), ((J + j) / SB) & 1))) break;
-                    tc_fence_after();
-                }
                 if (leader) {
                     if (C::HAS_P) {
-                        accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, 0, c2.s, false, 1);
+                        accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, 0, c2.s, j == 0, 2);
                         mma_commit(b_empty(c2.s));
                     }
                     if (more && SB == 1) issue_s(j + 1, c1, true);
@@ -950,9 +958,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             row_nl = p.neg_lse2[at];
             row_nd = p.neg_delta[at];
         }
-        if (C::RES_TMEM > 0 && n > 0) {
+        if (n > 0) {
             give_back();
             ok = __all_sync(0xffffffffu, ok);
+        }
+        if (C::RES_TMEM > 0 && n > 0) {
             // residents that go to tensor memory: the warpgroups copy 64-column blocks in turn
             for (int b = wg; ok && b < C::RES_TMEM * NCH; b += WGS) {
                 Ring at = ring1;  // blocks lie in the order they were loaded
@@ -991,19 +1001,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
         for (int j = 0; ok && j < n; ++j) {
             const int g = J + j, sb = g % SB, db = g % DPB;
-            const bool edge = t < edge_lo || t >= edge_hi;
             const int c0 = t * BN + wg * H;  // this thread's first streamed row
             const int lo = see_lo - c0, hi = see_hi - c0;
+            const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < H);
             const uint32_t st = sStat + (g % C::STATS) * C::STAT_BYTES + wg * (H * 4);
             const uint32_t tS = tl + C::T_S + sb * BN + wg * H, tDP = tl + C::T_DP + db * BN + wg * H;
+            if (C::KEYS) ok = ok && mbar_wait(b_stat_full(g % C::STATS), (g / C::STATS) & 1, abort_flag);
             if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(b_s_full(sb), (g / SB) & 1, abort_flag)))) break;
             tc_fence_after();
             uint32_t pr[H];  // P, fp32
 #pragma unroll
             for (int c = 0; c < H; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&pr[c]));
-            if (C::KEYS) ok = __all_sync(0xffffffffu, mbar_wait(b_stat_full(g % C::STATS), (g / C::STATS) & 1, abort_flag));
             tmem_wait_ld();
-            if (!ok) break;
             if (!C::HAS_P) {  // the S buffer may be written again
                 tc_fence_before();
                 __syncwarp();
@@ -1036,13 +1045,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int e = 0; e < 16; ++e)
                         pk[e] = pack_bf16x2(__uint_as_float(pr[c + 2 * e]), __uint_as_float(pr[c + 2 * e + 1]));
                     tmem_st16(tS + c, pk);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(b_p_full(sb, c / 32));
                 }
             }
-            if (C::HAS_P && j == 0) give_back();
+            if (C::HAS_P) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p_full(sb, 0));
+            }
             if (C::HAS_DS) {
                 if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(b_dp_full(db), (g / DPB) & 1, abort_flag)))) break;
                 tc_fence_after();
@@ -1088,7 +1098,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (lane == 0) mbar_arrive(b_stat_empty(g % C::STATS));
             }
             if (++t == t_hi) t = t_lo;
-            if (!C::HAS_P && j == 0) give_back();
         }
         ok = __all_sync(0xffffffffu, ok);
         if (ok && n > 0) {
@@ -1239,14 +1248,17 @@ cudaError_t launch_pass(const BwdMaps& m, const CUtensorMap& o1, const CUtensorM
 template <int D>
 cudaError_t launch_d(const BwdMaps& m, BwdParams& p, int num_sms, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
-    constexpr int PER_CTA = 256 / (D <= 64 ? 8 : (D <= 128 ? 16 : 32));
+    // 256 pairs a CTA: up to 32 heads, and a power of two rows, eight at least
+    const int heads = p.Hq < 32 ? p.Hq : 32;
+    int rows = 8;
+    while (2 * rows * heads <= 256) rows *= 2;
     // (without query rows one CTA a document still looks at its boundaries)
-    const long long ctas = p.max_q > 0 ? (static_cast<long long>(p.max_q) * p.Hq + PER_CTA - 1) / PER_CTA : 1;
-    const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(p.num_docs));
+    const dim3 grid(static_cast<unsigned>(p.max_q > 0 ? (p.max_q - 1) / rows + 1 : 1),
+                    static_cast<unsigned>((p.Hq + heads - 1) / heads), static_cast<unsigned>(p.num_docs));
     if (p.out_f32)
-        attn_bwd_stat_sm103a<D, true><<<grid, 256, 0, stream>>>(p);
+        attn_bwd_stat_sm103a<D, true><<<grid, 256, 0, stream>>>(p, rows, heads);
     else
-        attn_bwd_stat_sm103a<D, false><<<grid, 256, 0, stream>>>(p);
+        attn_bwd_stat_sm103a<D, false><<<grid, 256, 0, stream>>>(p, rows, heads);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     p.early_wait = 1;
     if constexpr (D <= 128) {
