@@ -149,7 +149,9 @@ gbattn_status check_fp8_cache(int num_blocks, int block_size, int Hkv, int D, gb
     return GBATTN_OK;
 }
 
-// The sections of the backward pass's workspace, each a multiple of 256 bytes.
+// The sections of the backward pass's workspace, each a multiple of 256 bytes:
+// two of row statistics, and kBwdCounters bytes.
+constexpr size_t kBwdCounters = 256;
 size_t bwd_stat_bytes(long long Tq, int num_docs, int Hq) {
     return ((static_cast<size_t>(gbattn::bwd_stat_stride(Tq, num_docs)) * Hq * 4) + 255) & ~size_t(255);
 }
@@ -177,7 +179,7 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
     if ((p.Hq + 31) / 32 > 65535) return GBATTN_ERR_UNSUPPORTED;
     if (!rows && !keys) return GBATTN_OK;
     const size_t stat = bwd_stat_bytes(p.Tq, p.num_docs, p.Hq);
-    if (!workspace || workspace_bytes < 2 * stat || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    if (!workspace || workspace_bytes < 2 * stat + kBwdCounters || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return GBATTN_ERR_WORKSPACE;
     DeviceInfo di;
     gbattn_status s = device_info(&di);
@@ -192,6 +194,7 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
     p.dv = dv;
     p.neg_lse2 = static_cast<float*>(workspace);
     p.neg_delta = reinterpret_cast<float*>(static_cast<char*>(workspace) + stat);
+    p.claims = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + 2 * stat);
     p.stat_stride = gbattn::bwd_stat_stride(p.Tq, p.num_docs);
     p.status = dev_status;
     p.group = p.Hq / p.Hkv;
@@ -917,7 +920,7 @@ gbattn_status attn_fwd_vsa(const void* q_tiled, const void* k_tiled, const void*
 
 size_t attn_bwd_workspace_size(int num_docs, int Tq, int Hq) {
     if (num_docs < 0 || num_docs > 65535 || Tq < 0 || Hq <= 0) return 0;
-    return 2 * bwd_stat_bytes(Tq, num_docs, Hq);
+    return 2 * bwd_stat_bytes(Tq, num_docs, Hq) + kBwdCounters;
 }
 
 gbattn_status attn_bwd_padded(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,

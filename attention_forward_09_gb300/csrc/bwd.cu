@@ -49,7 +49,8 @@ enum BwdMode {
     kBwdKV,  // keys resident: dV and dK
     kBwdV,   // keys resident: dV alone
     kBwdK,   // keys resident: dK alone
-    kBwdQ    // queries resident: dQ
+    kBwdQ,   // queries resident: dQ
+    kBwdPasses
 };
 
 template <int D_, int MODE_>
@@ -216,7 +217,7 @@ template <int D, bool F32>
 __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, const int rows, const int heads) {
     constexpr int LANES = D <= 64 ? 8 : (D <= 128 ? 16 : 32), UN = 4, PER_WARP = 32 / LANES;
     __shared__ float dots[256];
-    grid_launch_dependents();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < kBwdPasses) p.claims[threadIdx.x] = 0u;
     const int doc = blockIdx.z;
     const BwdDoc d = bwd_doc(p, doc, threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0);
     if (d.bad) return;
@@ -274,6 +275,9 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, c
         p.neg_lse2[to] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
         p.neg_delta[to] = (p.dlse ? p.dlse[at] : 0.f) - dots[x];
     }
+    // At the end: passes that began while this one's CTAs still came and went
+    // held their SMs (packed causal 2696 -> 2800 us).
+    grid_launch_dependents();
 }
 
 // ------------------------------------------------------------- the two passes
@@ -336,14 +340,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // ------------------------------------------------------------------ items
-    // An item is a (tile, head, document).  Heads fastest and tiles slowest for
-    // causal launches (the keys' first tiles and the queries' last ones are the
-    // heaviest and come first), tiles fastest otherwise (neighbouring CTAs
-    // stream the same head).  CTA b of G walks items k G + b (k even) and k G +
-    // G - 1 - b (k odd), so that falling costs even out.  The C1 producer walks
-    // them and publishes each in shared memory; rings, barriers and buffers
-    // carry on from item to item, so that the next item's loads and first
-    // products overlap the present one's last ones and its epilogue.
+    // An item is a (tile, head, document).  Causal launches list them by falling
+    // cost: tiles slowest (a document's first keys and last queries are seen
+    // the most; a key tile is counted from its document's last one), heads
+    // fastest.  Others have tiles fastest (neighbouring CTAs stream the same
+    // head).  The C1 producer claims them in that order from a counter, p.chunk
+    // at a time, and publishes each in shared memory; rings, barriers and
+    // buffers carry on from item to item, so that the next item's loads and
+    // first products overlap the present one's last ones and its epilogue.
     const int heads = C::KEYS ? p.Hkv : p.Hq;
     struct Item {
         int n;                     // steps; 0: zeros to write; kItemEnd: no more items
@@ -364,14 +368,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (all) got = __all_sync(0xffffffffu, got);
         return got ? GBATTN_ITEM(it, n) : -1;
     };
-    // The walk's k-th item; false past the end.  n = -1: nothing to write.
-    auto item_at = [&](int k, Item& it) -> bool {
-        const long long g = gridDim.x, first = k * g;
-        const long long i = first + ((k & 1) ? g - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
-        if (first >= p.items[C::KEYS ? 0 : 1]) return false;
+    // The i-th item; n = -1: nothing to write.
+    auto item_at = [&](uint32_t x, Item& it) {
         it.n = -1;
-        if (i >= p.items[C::KEYS ? 0 : 1]) return true;
-        uint32_t x = static_cast<uint32_t>(i);
         int tile, doc;
         if (p.causal) {
             it.head = x % heads;
@@ -387,10 +386,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             doc = x / heads;
         }
         const BwdDoc d = bwd_doc(p, doc, false);
-        if (d.bad) return true;
-        it.r0 = tile * BM;
+        if (d.bad) return;
         it.res_all = C::KEYS ? d.Lk_all : d.Lq_all;
-        if (it.r0 >= it.res_all) return true;
+        if (C::KEYS && p.causal) tile -= p.tiles_k - (it.res_all + BM - 1) / BM;
+        it.r0 = tile * BM;
+        if (tile < 0 || it.r0 >= it.res_all) return;
         it.res_len = C::KEYS ? d.Lk : d.Lq;
         it.str_len = C::KEYS ? d.Lq : d.Lk;
         it.res_start = C::KEYS ? d.k_start : d.q_start;
@@ -408,7 +408,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 it.t_hi = (max(0, min(d.Lk, min(it.r0 + BM, d.Lq) + it.diag)) + BN - 1) / BN;
         }
         it.n = max(0, it.t_hi - it.t_lo) * (C::KEYS ? p.group : 1);
-        return true;
     };
     if (status_has_timeout(p.status, kDevTimeout)) {
         grid_dependency_wait();
@@ -428,7 +427,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             mbar_init(b_staged(b), C::ACCS == 2 ? 4 : MW);
             mbar_init(b_copied(b), C::ACCS == 2 ? 4 : MW);
         }
-        mbar_init(b_done, C::ISSUERS);
+        mbar_init(b_done, C::HAS_DS ? C::ISSUERS : 1);
         mbar_init(b_drain, C::ISSUERS);
         mbar_init(b_res_in, MW);
         mbar_init(b_acc_free, MW);
@@ -515,13 +514,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             ++published;
             return true;
         };
+        if (p.early_wait) grid_dependency_wait();  // the launch before this one zeroes the counter
+        const uint32_t all = static_cast<uint32_t>(p.items[C::KEYS ? 0 : 1]), chunk = p.chunk[C::KEYS ? 0 : 1];
+        uint32_t* const counter = p.claims + C::MODE;
+        uint32_t left = 0, i = 0, next = atomicAdd(counter, chunk);
 #pragma unroll 1
-        for (int k = 0; ok; ++k) {
-            if (!item_at(k, it)) {
+        while (ok) {
+            if (left == 0) {  // (claimed one ahead: the answer takes a while)
+                i = next;
+                left = chunk;
+                if (i < all) next = atomicAdd(counter, chunk);
+            }
+            if (i >= all) {
                 it.n = kItemEnd;
                 ok = publish();
                 break;
             }
+            item_at(i++, it);
+            --left;
             if (it.n < 0) continue;
             if (!(ok = publish())) break;
             if (it.n == 0) continue;
@@ -897,7 +907,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (++t == t_hi) t = t_lo;
             }
         }
-        if (ok && leader) mma_commit(b_done);
+        // (dV alone: the warp that issues S runs an item ahead, and its commits would count for this one)
+        if (ok && leader && (C::HAS_DS || !first_warp)) mma_commit(b_done);
         __syncwarp();
         if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
         for (int c = 0; c < C::STAGE1; ++c) c1.next();
@@ -1276,6 +1287,12 @@ cudaError_t launch_d(const BwdMaps& m, BwdParams& p, int num_sms, cudaStream_t s
 cudaError_t launch_bwd(int D, const BwdMaps& m, BwdParams p, int num_sms, cudaStream_t stream) {
     p.items[0] = static_cast<long long>(p.tiles_k) * p.Hkv * p.num_docs;
     p.items[1] = static_cast<long long>(p.tiles_q) * p.Hq * p.num_docs;
+    // One item a claim until there are 64 a CTA (many short documents under a
+    // long bound: most are empty, and a claim costs more than a look at them).
+    for (int x = 0; x < 2; ++x) {
+        const long long c = p.items[x] / (64ll * num_sms);
+        p.chunk[x] = static_cast<uint32_t>(c < 1 ? 1 : (c > 256 ? 256 : c));
+    }
     switch (D) {
         case 64: return launch_d<64>(m, p, num_sms, stream);
         case 96: return launch_d<96>(m, p, num_sms, stream);

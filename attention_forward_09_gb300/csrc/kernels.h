@@ -327,6 +327,7 @@ struct BwdParams {
     void *dq, *dk, *dv;     // bf16, the shapes of q, k, v
     float* neg_lse2;        // workspace [Hq, stat_stride]: -lse log2 e (-inf: the row sees no key)
     float* neg_delta;       // workspace [Hq, stat_stride]: dlse - dout.out
+    uint32_t* claims;       // workspace [4]: items of each pass handed out
     long long stat_stride;
     uint32_t* status;
     const int32_t *cu_q, *cu_k;
@@ -343,6 +344,7 @@ struct BwdParams {
     int give_up;            // as PrefillParams
     // Set by launch_bwd:
     long long items[2];     // (tile, head, document) with the keys, with the queries resident
+    uint32_t chunk[2];      // items a claim
     int early_wait;         // 1: the launch before this one writes the statistics
 };
 long long bwd_stat_stride(long long Tq, int num_docs);

@@ -73,10 +73,10 @@ def test_header_and_exports(lib):
 
 def test_workspace_size(lib):
     f = lib.attn_bwd_workspace_size
-    # two fp32 arrays [Hq, rows + alignment of each document + a tile], each rounded up to 256 bytes
+    # two fp32 arrays [Hq, rows + alignment of each document + a tile], each rounded up to 256 bytes, and counters
     for n, t, h in ((1, 1, 1), (3, 1000, 7), (65535, 65535, 2), (2, 8192, 24)):
         stride = (t + 4 * n + 3) // 4 * 4 + 128
-        assert f(n, t, h) == 2 * ((stride * h * 4 + 255) // 256 * 256)
+        assert f(n, t, h) == 2 * ((stride * h * 4 + 255) // 256 * 256) + 256
     assert f(1, 2 ** 31 - 1, 64) > 2 ** 39  # no 32-bit product
     assert f(-1, 1, 1) == f(1, -1, 1) == f(1, 1, 0) == f(65536, 1, 1) == 0
 

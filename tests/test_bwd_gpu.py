@@ -295,3 +295,11 @@ def test_more_tiles_than_a_wave(D, causal):
     """Several items a CTA, some without any work between them: every buffer, ring and barrier carries on from item to item."""
     packed([130, 0, 513, 1, 250, 300], [130, 64, 260, 300, 250, 5], 48, 24, D, causal)
     dense_case(1, 200, 200, 200, 100, D, causal)
+
+
+@pytest.mark.parametrize("D", workloads.HEAD_SIZES)
+@pytest.mark.parametrize("Sq,Sk", [(64, 3000), (3000, 64), (130, 2500)])
+def test_items_of_one_or_two_steps_follow_one_another(D, Sq, Sk):
+    """Many more items than CTAs, each over after a step or two; then other values in the same places."""
+    for seed in (0, 1):
+        dense_case(1, Sq, Sk, 12, 12, D, False, seed=seed)
