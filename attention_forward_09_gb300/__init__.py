@@ -903,6 +903,14 @@ def _tensor(name, t, dev, dtype, shape):
         raise ValueError(f"{name} must be on cuda:{dev}, with q")
 
 
+def _like(stream, t):
+    """An uninitialised contiguous tensor of t's shape and type, of the stream that will write it."""
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def attn_bwd_workspace_size(num_docs, Tq, Hq) -> int:
     """Bytes of workspace a backward call needs for num_docs documents (or batch entries) of Tq query rows in all."""
     return int((_lib or load_library()).attn_bwd_workspace_size(_host_int("num_docs", num_docs), _host_int("Tq", Tq), Hq))
@@ -916,10 +924,14 @@ def _bwd(name, q, k, v, out, lse, dout, dlse, index, sizes, docs, heads, lse_sha
     if dev < 0:
         raise ValueError("the gradients take CUDA tensors")
     Hq, Hkv, D = heads
-    bf16 = torch.bfloat16
-    for n, t, like in (("q", q, q), ("k", k, k), ("v", v, k), ("dout", dout, q)):
-        _tensor(n, t, dev, bf16, like.shape)
-    _tensor("out", out, dev, bf16 if out.dtype == bf16 else torch.float32, q.shape)
+    bf16, qs, ks = torch.bfloat16, q.shape, k.shape
+    f32_out = out.dtype == torch.float32
+    if not (q.dtype == k.dtype == v.dtype == dout.dtype == bf16 and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous() and dout.is_contiguous() and v.shape == ks and dout.shape == qs
+            and k.get_device() == v.get_device() == dout.get_device() == dev):
+        for n, t, shape in (("q", q, qs), ("k", k, ks), ("v", v, ks), ("dout", dout, qs)):
+            _tensor(n, t, dev, bf16, shape)
+    _tensor("out", out, dev, torch.float32 if f32_out else bf16, qs)
     _tensor("lse", lse, dev, torch.float32, lse_shape)
     if dlse is not None:
         _tensor("dlse", dlse, dev, torch.float32, lse_shape)
@@ -929,13 +941,12 @@ def _bwd(name, q, k, v, out, lse, dout, dlse, index, sizes, docs, heads, lse_sha
     status = _status_ptr(dev_status)
     if dev_status is not None and dev_status.get_device() != dev:
         raise ValueError(f"dev_status must be on cuda:{dev}, with q")
-    grads = []
-    for n, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
-        if t is None:
-            t = _empty_on(stream, q, like.shape, bf16)
-        else:
-            _tensor(n, t, dev, bf16, like.shape)
-        grads.append(t)
+    for n, t, shape in (("dq", dq, qs), ("dk", dk, ks), ("dv", dv, ks)):
+        if t is not None:
+            _tensor(n, t, dev, bf16, shape)
+    dq = _like(stream, q) if dq is None else dq
+    dk = _like(stream, k) if dk is None else dk
+    dv = _like(stream, k) if dv is None else dv
     if workspace is None:
         ws_bytes = attn_bwd_workspace_size(docs, q.numel() // (Hq * D) if Hq * D else 0, Hq)
         workspace = _empty_on(stream, q, (ws_bytes,), torch.uint8)
@@ -945,11 +956,11 @@ def _bwd(name, q, k, v, out, lse, dout, dlse, index, sizes, docs, heads, lse_sha
         raise ValueError(f"workspace must be contiguous and on cuda:{dev}, with q")
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
     _run_on(name, dev, stream,
-            (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _out_code(out.dtype), lse.data_ptr(),
+            (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), OUT_F32 if f32_out else OUT_BF16, lse.data_ptr(),
              dout.data_ptr(), None if dlse is None else dlse.data_ptr(),
-             *(None if t is None else t.data_ptr() for _, t, _ in index), *sizes, Hq, Hkv, D, scale, 1 if causal else 0,
-             *(t.data_ptr() for t in grads), workspace.data_ptr(), ws_bytes, status))
-    return tuple(grads)
+             *[None if t is None else t.data_ptr() for _, t, _ in index], *sizes, Hq, Hkv, D, scale, 1 if causal else 0,
+             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), ws_bytes, status))
+    return dq, dk, dv
 
 
 def _bwd_batch(q, k):
@@ -1090,11 +1101,11 @@ def attn_rotary(q, k, positions, plan: RotaryPlan, transpose=False, q_out=None, 
     _tensor("positions", positions, dev, torch.int32, (T,))
     _tensor("plan.steps", plan.steps, dev, torch.int64, (plan.rot_dim // 2,))
     if q_out is None:
-        q_out = _empty_on(stream, q, q.shape, torch.bfloat16)
+        q_out = _like(stream, q)
     qos = _rotary_rows("q_out", q_out, dev, T, Hq, D)[2]
     if k is not None:
         if k_out is None:
-            k_out = _empty_on(stream, k, k.shape, torch.bfloat16)
+            k_out = _like(stream, k)
         kos = _rotary_rows("k_out", k_out, dev, T, Hkv, D)[2]
     _run_on("attn_rotary", dev, stream,
             (q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, positions.data_ptr(), T, plan.steps.data_ptr(),
@@ -1127,7 +1138,7 @@ def attn_rotary_kv_cache_write(q, key, value, positions, plan: RotaryPlan, slot_
     if dev_status is not None and dev_status.get_device() != dev:
         raise ValueError(f"dev_status must be on cuda:{dev}, with q")
     if q_out is None:
-        q_out = _empty_on(stream, q, q.shape, torch.bfloat16)
+        q_out = _like(stream, q)
     qos = _rotary_rows("q_out", q_out, dev, T, Hq, D)[2]
     _run_on("attn_rotary_kv_cache_write", dev, stream,
             (q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, positions.data_ptr(), slot_mapping.data_ptr(), T,

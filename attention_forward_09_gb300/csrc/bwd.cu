@@ -36,6 +36,7 @@
 // K-major by S / dP and MN-major by the second products.
 #include <math.h>
 #include <stddef.h>
+#include <atomic>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -86,8 +87,9 @@ struct BwdCfg {
     static constexpr int ISSUERS = SHARED ? 1 : 2;    // warps that issue products
     static constexpr int STAT_BYTES = KEYS ? 2 * BN * 4 : 0;   // -lse log2 e, -delta of a streamed tile's rows
     static constexpr int STATS = D <= 64 ? 4 : 2;              // buffers of them
-    static constexpr int MATH_WARPS = 8, MATH_WGS = MATH_WARPS / 4, H = BN / MATH_WGS;  // H columns a thread
-    static constexpr int REG_MATH = 208, REG_OTHER = 88;       // setmaxnreg split of 384 x 168
+    static constexpr int MATH_WARPS = 16, MATH_WGS = MATH_WARPS / 4, H = BN / MATH_WGS;  // H columns a thread
+    // setmaxnreg split of the 640 x 96 registers of the launch
+    static constexpr int REG_MATH = 104, REG_OTHER = 64;
     static constexpr int THREADS = 32 * MATH_WARPS + 128;
     static constexpr int STAGE1 = NCK, STAGE2 = ACCS == 2 ? NCK : 0;  // slots of each ring that an item's gradients leave through
     static constexpr int ITEMS = 3;                            // items published ahead
@@ -105,7 +107,7 @@ struct BwdCfg {
     static constexpr int O_STAT = O_C + SLOTS * C_BYTES;
     static constexpr int O_BARS = O_STAT + STATS * STAT_BYTES;
     static constexpr int SMEM_BYTES = O_BARS + NUM_BARS * 8 + 16 + ITEMS * 64;
-    static_assert(MATH_WARPS * 32 * REG_MATH + 128 * REG_OTHER <= THREADS * 168, "register split");
+        static_assert(MATH_WARPS * 32 * REG_MATH + 128 * REG_OTHER <= THREADS * 96, "register split");
     static_assert(T_RES + RES_TMEM * D / 2 <= 512, "TMEM budget");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
     static_assert(C_BYTES == CCH * BM * 128, "a slot holds a chunk of a gradient tile");
@@ -281,14 +283,16 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, c
 }
 
 // ------------------------------------------------------------- the two passes
-// 384 threads:
-//   warps 0-7   math, two warpgroups: thread = one resident row (TMEM lane) and
-//               64 of a streamed tile's 128 columns
-//   warp 8      TMA producer: resident tiles, then the tiles C1 (Q or K)
-//   warp 9      TMEM allocator; issues S and dV (dV alone: S)
-//   warp 10     TMA producer: the tiles C2 (dO or V), and with the keys resident
+// 640 threads:
+//   warps 0-15  math, four warpgroups: thread = one resident row (TMEM lane) and
+//               32 of a streamed tile's 128 columns (four warps a scheduler: one's
+//               latencies hide another's; two warpgroups of 64 columns were 3 %
+//               slower at D = 64 and 20 % on a batch of a few tiles)
+//   warp 16     TMA producer: claims items; resident tiles, then the tiles C1 (Q or K)
+//   warp 17     TMEM allocator; issues S and dV (dV alone: S)
+//   warp 18     TMA producer: the tiles C2 (dO or V), and with the keys resident
 //               the streamed rows' statistics
-//   warp 11     issues dP and dK or dQ (dV alone: dV)
+//   warp 19     issues dP and dK or dQ (dV alone: dV)
 // A product is issued about as fast as it runs, so what one issuing warp waits
 // the other's products fill; the tensor core finishes what one thread issues
 // in order.
@@ -424,8 +428,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             mbar_init(b_dp_full(b), 1);
             mbar_init(b_ds_full(b), MW);
             mbar_init(b_turn(b), 1);
-            mbar_init(b_staged(b), C::ACCS == 2 ? 4 : MW);
-            mbar_init(b_copied(b), C::ACCS == 2 ? 4 : MW);
+            mbar_init(b_staged(b), MW / C::ACCS);
+            mbar_init(b_copied(b), MW / C::ACCS);
         }
         mbar_init(b_done, C::HAS_DS ? C::ISSUERS : 1);
         mbar_init(b_drain, C::ISSUERS);
@@ -941,16 +945,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // stores one gives its slots back once they have been read, which it
         // looks after in the next item's first step.  (Where the next item's
         // first tiles themselves need those slots, before it: RES_TMEM.)
-        const bool storer = lane == 0 && (warp == 0 || (C::ACCS == 2 && warp == 4));
+        constexpr int PARTS = WGS / C::ACCS;                // warpgroups that share an accumulator
+        const int acc = wg / PARTS, part = wg % PARTS;
+        const bool storer = lane == 0 && warp % (4 * PARTS) == 0;
         int leaving = -1;  // the first of the slots that are being read
         auto give_back = [&]() {
             if (storer && leaving >= 0) {
                 bulk_wait_read0();
-                ok = mbar_wait(b_copied(C::ACCS == 2 ? wg : 0), (done - 1) & 1, abort_flag);
+                ok = mbar_wait(b_copied(acc), (done - 1) & 1, abort_flag);
                 int s = leaving;
                 for (int c = 0; c < NCK; ++c) {
                     for (int x = 0; x < C::RELEASES; ++x) mbar_arrive(b_empty(s));
-                    if (++s == (wg ? C::N1 + C::N2 : C::N1)) s = wg ? C::N1 : 0;
+                    if (++s == (acc ? C::N1 + C::N2 : C::N1)) s = acc ? C::N1 : 0;
                 }
                 leaving = -1;
             }
@@ -1116,15 +1122,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             tc_fence_after();
         }
         // ------------------------------------------------------------ epilogue
-        // With two accumulators (dV, dK) each is a warpgroup's; of one the 32
-        // column chunks are taken in turn.  Rows are staged in the ring's slots,
+        // An accumulator's 32 column chunks are taken in turn by its warpgroups.  Rows are staged in the ring's slots,
         // in the boxes' swizzle, and leave by TMA where the tile lies wholly
         // inside its document, else row by row.
         if (ok) {
             const int res_all = GBATTN_ITEM(item, res_all), res_len = GBATTN_ITEM(item, res_len);
             const int head = GBATTN_ITEM(item, head), res_start = GBATTN_ITEM(item, res_start);
-            constexpr int PARTS = C::ACCS == 2 ? 1 : WGS;       // warpgroups that share an accumulator
-            const int acc = C::ACCS == 2 ? wg : 0, part = C::ACCS == 2 ? 0 : wg;
             const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && acc == 0);
             const float f = is_dv ? 1.f : p.scale;
             uint16_t* const out = static_cast<uint16_t*>(C::KEYS ? (is_dv ? p.dv : p.dk) : p.dq);
@@ -1232,6 +1235,19 @@ long long bwd_stat_stride(long long Tq, int num_docs) {
 
 namespace {
 
+// The kernel's shared memory, asked for once a device.
+template <class C>
+cudaError_t allow_smem() {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(attn_bwd_sm103a<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
 // One pass, behind the launch that writes the statistics (early_wait) or beside
 // another pass: its CTAs take the SMs that one's leave.
 template <class C>
@@ -1239,7 +1255,7 @@ cudaError_t launch_pass(const BwdMaps& m, const CUtensorMap& o1, const CUtensorM
                         cudaStream_t stream) {
     const long long items = p.items[C::KEYS ? 0 : 1];
     if (items == 0) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(attn_bwd_sm103a<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    cudaError_t e = allow_smem<C>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[1];
