@@ -1070,17 +1070,22 @@ class RotaryPlan:
         self.steps = torch.tensor(steps, dtype=torch.int64).to(device)
 
 
-def _rotary_rows(name, t, dev, tokens=None, heads=None, d=None):
-    """(heads, D, token stride) of a bf16 [T, heads, D] tensor on device number dev."""
+def _rotary_rows(name, t, dev, shape):
+    """Token stride of a bf16 tensor [T, heads, D] (given as shape) on device number dev, whose [heads, D] rows are
+    contiguous."""
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bfloat16 tensor {list(shape)} on cuda:{dev}, as q")
+    T, heads, d = shape
+    tokens, row, col = t.stride()
+    if col != 1 or (row != d and heads > 1):
+        raise ValueError(f"{name}: a token's [heads, D] must be contiguous")
+    return tokens if T > 1 else heads * d
+
+
+def _rotary_shape(name, t):
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, D]")
-    T, H, D = t.shape
-    stride = _token_rows(name, t, H if heads is None else heads, D if d is None else d)
-    if tokens is not None and T != tokens:
-        raise ValueError(f"{name} must have {tokens} tokens, as q")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, with q")
-    return H, D, stride
+    return t.shape
 
 
 def attn_rotary(q, k, positions, plan: RotaryPlan, transpose=False, q_out=None, k_out=None, stream=None):
@@ -1092,21 +1097,29 @@ def attn_rotary(q, k, positions, plan: RotaryPlan, transpose=False, q_out=None, 
     dev = q.get_device()
     if dev < 0:
         raise ValueError("attn_rotary takes CUDA tensors")
-    Hq, D, qs = _rotary_rows("q", q, dev)
-    T, Hkv, ks, kos = q.shape[0], 0, 0, 0
+    shape = _rotary_shape("q", q)
+    T, Hq, D = shape
+    qs = _rotary_rows("q", q, dev, shape)
+    Hkv = ks = kos = 0
     if k is not None:
-        Hkv, _, ks = _rotary_rows("k", k, dev, T, None, D)
+        Hkv = _rotary_shape("k", k)[1]
+        k_shape = (T, Hkv, D)
+        ks = _rotary_rows("k", k, dev, k_shape)
     elif k_out is not None:
         raise ValueError("k_out is given without k")
     _tensor("positions", positions, dev, torch.int32, (T,))
     _tensor("plan.steps", plan.steps, dev, torch.int64, (plan.rot_dim // 2,))
     if q_out is None:
         q_out = _like(stream, q)
-    qos = _rotary_rows("q_out", q_out, dev, T, Hq, D)[2]
+        qos = Hq * D
+    else:
+        qos = _rotary_rows("q_out", q_out, dev, shape)
     if k is not None:
         if k_out is None:
             k_out = _like(stream, k)
-        kos = _rotary_rows("k_out", k_out, dev, T, Hkv, D)[2]
+            kos = Hkv * D
+        else:
+            kos = _rotary_rows("k_out", k_out, dev, k_shape)
     _run_on("attn_rotary", dev, stream,
             (q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, positions.data_ptr(), T, plan.steps.data_ptr(),
              plan.rot_dim, 1 if plan.interleaved else 0, 1 if transpose else 0, plan.gain, Hq, Hkv, D, q_out.data_ptr(), qos,
@@ -1124,10 +1137,12 @@ def attn_rotary_kv_cache_write(q, key, value, positions, plan: RotaryPlan, slot_
     dev = q.get_device()
     if dev < 0:
         raise ValueError("attn_rotary_kv_cache_write takes CUDA tensors")
-    Hq, D, qs = _rotary_rows("q", q, dev)
-    T = q.shape[0]
-    Hkv, _, ks = _rotary_rows("key", key, dev, T, None, D)
-    vs = _rotary_rows("value", value, dev, T, Hkv, D)[2]
+    shape = _rotary_shape("q", q)
+    T, Hq, D = shape
+    Hkv = _rotary_shape("key", key)[1]
+    k_shape = (T, Hkv, D)
+    qs, ks, vs = (_rotary_rows("q", q, dev, shape), _rotary_rows("key", key, dev, k_shape),
+                  _rotary_rows("value", value, dev, k_shape))
     _tensor("positions", positions, dev, torch.int32, (T,))
     _tensor("slot_mapping", slot_mapping, dev, torch.int32, (T,))
     _tensor("plan.steps", plan.steps, dev, torch.int64, (plan.rot_dim // 2,))
@@ -1139,7 +1154,9 @@ def attn_rotary_kv_cache_write(q, key, value, positions, plan: RotaryPlan, slot_
         raise ValueError(f"dev_status must be on cuda:{dev}, with q")
     if q_out is None:
         q_out = _like(stream, q)
-    qos = _rotary_rows("q_out", q_out, dev, T, Hq, D)[2]
+        qos = Hq * D
+    else:
+        qos = _rotary_rows("q_out", q_out, dev, shape)
     _run_on("attn_rotary_kv_cache_write", dev, stream,
             (q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, positions.data_ptr(), slot_mapping.data_ptr(), T,
              plan.steps.data_ptr(), plan.rot_dim, 1 if plan.interleaved else 0, plan.gain, q_out.data_ptr(), qos,

@@ -14,10 +14,12 @@
 // of a turn goes to fp32 and sincospif.
 //
 // HBM-bound: a value is read and written once.  A warp takes one token (or,
-// where tokens are few, an equal share of its heads): its lanes work out the
-// token's cosines and sines once, into the warp's part of shared memory, and
-// then move 16-byte vectors, pairs of them in the half layout, four units in
-// flight a lane.  Rotated widths that are no whole vectors (half layout: rot %
+// where tokens are few, an equal share of its heads): its lanes ask for the
+// first vectors, work out the token's cosines and sines once meanwhile, into
+// the warp's part of shared memory, and move 16-byte vectors, pairs of them in
+// the half layout, two units in flight a lane (27654 tokens of 32 + 8 heads of
+// 128: 86 us of kernel, 6.6 TB/s; with one unit 90, three 88, four 96: the
+// registers of more cost warps).  Rotated widths that are no whole vectors (half layout: rot %
 // 16, interleaved: rot % 8) are moved pair by pair.
 #include "kernels.h"
 #include "ptx.cuh"
@@ -48,7 +50,7 @@ __device__ __forceinline__ uint32_t bf_round(float x) { return pack_bf16x2(x, 0.
 
 template <int LAYOUT, bool STORE>
 __global__ void __launch_bounds__(256) rotary_sm103a(const RotaryParams p) {
-    constexpr int UN = 4;  // units in flight a lane
+    constexpr int UN = 2;  // units in flight a lane
     __shared__ __align__(16) float table[8][2][128];  // cosines and sines of a warp's token, times the gain
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long task = static_cast<long long>(blockIdx.x) * 8 + warp;
@@ -57,13 +59,6 @@ __global__ void __launch_bounds__(256) rotary_sm103a(const RotaryParams p) {
     const int part = static_cast<int>(task % p.parts);
     float *cs = table[warp][0], *sn = table[warp][1];
     const long long pos = p.positions[t];
-    for (int i = lane; i < p.half; i += 32) {
-        const unsigned long long turn = static_cast<unsigned long long>(pos) * p.steps[i];  // 2^-64 turns, modulo one
-        float s, c;
-        sincospif(__ll2float_rn(static_cast<long long>(turn)) * 0x1p-63f, &s, &c);
-        cs[i] = c * p.gain;
-        sn[i] = (p.transpose ? -s : s) * p.gain;
-    }
     long long slot = 0;
     if (STORE) {
         slot = p.slot_mapping[t];
@@ -72,13 +67,13 @@ __global__ void __launch_bounds__(256) rotary_sm103a(const RotaryParams p) {
             slot = -1;
         }
     }
-    __syncwarp();
 
     // Units of the token: the query heads', the key heads', then the value row's vectors.
     const int U = p.units, nq = p.Hq * U, nk = nq + p.Hkv * U, n = STORE ? nk + p.Hkv * (p.D >> 3) : nk;
     const int rot_units = LAYOUT == kHalfVec ? p.half >> 3 : (LAYOUT == kInterleavedVec ? p.half >> 2 : p.half);
     const int stride = p.parts * 32;
-    for (int i0 = part * 32 + lane; i0 < n; i0 += stride * UN) {
+    bool first = true;
+    for (int i0 = part * 32 + lane; first || i0 < n; i0 += stride * UN) {
         uint4 a[UN], b[UN];
         const uint16_t* src[UN];
         uint16_t* dst[UN];
@@ -113,6 +108,17 @@ __global__ void __launch_bounds__(256) rotary_sm103a(const RotaryParams p) {
                 a[x] = ld_row(src[x]);
                 if (LAYOUT == kHalfVec && unit[x] >= 0 && unit[x] < rot_units) b[x] = ld_row(src[x] + p.half);
             }
+        }
+        if (first) {  // the token's table, while the first vectors are on their way
+            first = false;
+            for (int i = lane; i < p.half; i += 32) {
+                const unsigned long long turn = static_cast<unsigned long long>(pos) * p.steps[i];  // 2^-64 turns, modulo one
+                float s, c;
+                sincospif(__ll2float_rn(static_cast<long long>(turn)) * 0x1p-63f, &s, &c);
+                cs[i] = c * p.gain;
+                sn[i] = (p.transpose ? -s : s) * p.gain;
+            }
+            __syncwarp();
         }
 #pragma unroll
         for (int x = 0; x < UN; ++x) {
