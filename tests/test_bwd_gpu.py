@@ -303,3 +303,77 @@ def test_items_of_one_or_two_steps_follow_one_another(D, Sq, Sk):
     """Many more items than CTAs, each over after a step or two; then other values in the same places."""
     for seed in (0, 1):
         dense_case(1, Sq, Sk, 12, 12, D, False, seed=seed)
+
+
+def test_offsets_past_32_bits():
+    """Element offsets beyond 2^31 in every tensor: the last documents of a pack of 82000 tokens of 208 heads of 128."""
+    n, L, H, D, s = 1640, 50, 208, 128, 128 ** -0.5
+    T = n * L
+    assert T * H * D > 2 ** 31
+    g = torch.Generator(device=dev()).manual_seed(4)
+    q, k, v, do = (torch.randn(T, H, D, generator=g, device=dev(), dtype=BF16) for _ in range(4))
+    cu = torch.arange(0, T + 1, L, dtype=torch.int32, device=dev())
+    out, lse = gb.attn_fwd_varlen(q, k, v, cu, cu, L, L, s, True, lse=True, out_dtype=BF16)
+    st = status_word()
+    got = gb.attn_bwd_varlen(q, k, v, out, lse, do, cu, cu, L, L, s, True, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    for d in (0, n // 2, n - 1):
+        i, h = slice(d * L, d * L + L), slice(H - 9, H)
+        ref = oracle.attention_gradients(q[i, h], k[i, h], v[i, h], out[i, h], lse[h, i], do[i, h], s, True, bounds=True)
+        check([x[i, h] for x in got], ref, f"document {d}")
+
+
+def test_many_documents_under_a_long_bound():
+    """3000 documents, most of them empty, bounded by the longest: items are claimed in runs, and skipped."""
+    g = torch.Generator().manual_seed(2)
+    lens = [0] * 3000
+    for i, x in ((0, 3), (700, 1100), (701, 1), (1500, 130), (2999, 257)):
+        lens[i] = x
+    packed(lens, lens, 4, 2, 64, True)
+
+
+@pytest.mark.parametrize("D", [64, 192, 256])
+def test_a_captured_call_at_other_head_sizes_and_two_graphs(D):
+    """Two graphs, each with its own workspace, replayed one after the other and on two streams at once."""
+    a, b = dense_case(1, 400, 300, 4, 2, D, True), dense_case(2, 130, 520, 2, 1, D, False)
+    graphs, outs = [], []
+    for (q, k, v, out, lse, do, s, got), causal in ((a, True), (b, False)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(gb.attn_bwd_dense(q, k, v, out, lse, do, s, causal))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for x in outs:
+        for t in x:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for x, c in zip(outs, (a, b)):
+        assert all(torch.equal(p, r) for p, r in zip(x, c[-1]))
+
+
+@pytest.mark.parametrize("D", workloads.HEAD_SIZES)
+def test_calls_behind_one_another_do_not_meet(D):
+    """Calls of other sizes in between, nothing waiting: the passes of one call end before the next begins."""
+    a, b = dense_case(1, 500, 700, 6, 2, D, True), dense_case(3, 90, 260, 40, 40, D, False)
+    for _ in range(10):
+        x = gb.attn_bwd_dense(*a[:6], a[6], True)
+        y = gb.attn_bwd_dense(*b[:6], b[6], False)
+        z = gb.attn_bwd_dense(*a[:6], a[6], True)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, r) for got, c in ((x, a), (y, b), (z, a)) for p, r in zip(got, c[-1]))
+
+
+def test_infinities_and_nan_behind_the_causal_diagonal_of_a_row():
+    """A query row's own gradient reads only the keys it sees; rows without a key read nothing at all."""
+    q, k, v, out, lse, do, s, got = dense_case(1, 300, 200, 2, 1, 128, True)  # rows 0 .. 99 see no key
+    q2, do2, out2 = q.clone(), do.clone(), out.clone()
+    for x in (q2, do2, out2):
+        x[:, :100] = float("nan")
+    again = gb.attn_bwd_dense(q2, k, v, out2, lse, do2, s, True)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))

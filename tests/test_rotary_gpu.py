@@ -249,3 +249,28 @@ def test_refusals_of_the_binding():
         with pytest.raises(ValueError):
             gb.attn_rotary_kv_cache_write(**{**dict(q=q, key=k, value=v, positions=pos, plan=plan, slot_mapping=slots,
                                                     kv_cache=cache), **kw})
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_offsets_past_32_bits(interleaved):
+    """Element offsets beyond 2^31 in queries, outputs and the cache."""
+    T, Hq, Hkv, D = 300000, 52, 52, 128
+    assert T * Hq * D < 2 ** 31 < T * (Hq + 2 * Hkv) * D and 2 * T * Hkv * D > 2 ** 31
+    g = torch.Generator(device=dev()).manual_seed(3)
+    x = torch.empty(T, Hq + 2 * Hkv, D, device=dev(), dtype=BF16)
+    for i in range(0, T, 50000):
+        x[i:i + 50000].normal_(generator=g)
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    pos = torch.arange(T, dtype=torch.int32, device=dev())
+    slots = pos.flip(0).contiguous()
+    cache = torch.zeros(2, T // 100, 100, Hkv, D, dtype=BF16, device=dev())
+    plan = gb.RotaryPlan(64, interleaved=interleaved)
+    a = gb.attn_rotary_kv_cache_write(q, k, v, pos, plan, slots, cache)
+    torch.cuda.synchronize()
+    rows = [0, 1, T // 2, T - 2, T - 1]
+    check(a[rows], q[rows], pos[rows], plan, "q")
+    keys, values = cache.view(2, T, Hkv, D)
+    check(keys[slots[rows].long()], k[rows], pos[rows], plan, "k")
+    assert torch.equal(values[slots[rows].long()], v[rows]) and torch.equal(values.flip(0), v)
+    b, c = gb.attn_rotary(q, k, pos, plan, q_out=q, k_out=k)  # in place, in the strided tensor
+    assert torch.equal(b, a) and torch.equal(c.flip(0), keys) and b is q
