@@ -220,6 +220,11 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, c
     constexpr int LANES = D <= 64 ? 8 : (D <= 128 ? 16 : 32), UN = 4, PER_WARP = 32 / LANES;
     __shared__ float dots[256];
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < kBwdPasses) p.claims[threadIdx.x] = 0u;
+    // Few CTAs: the next pass may set itself up beside them.  (Many: passes that
+    // began while CTAs of this launch still came and went held their SMs, packed
+    // causal 2696 -> 2800 us, so there it is the end that lets them begin.)
+    const bool few = gridDim.x * gridDim.y * gridDim.z <= 128;
+    if (few) grid_launch_dependents();
     const int doc = blockIdx.z;
     const BwdDoc d = bwd_doc(p, doc, threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0);
     if (d.bad) return;
@@ -277,9 +282,7 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, c
         p.neg_lse2[to] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
         p.neg_delta[to] = (p.dlse ? p.dlse[at] : 0.f) - dots[x];
     }
-    // At the end: passes that began while this one's CTAs still came and went
-    // held their SMs (packed causal 2696 -> 2800 us).
-    grid_launch_dependents();
+    if (!few) grid_launch_dependents();
 }
 
 // ------------------------------------------------------------- the two passes
@@ -518,16 +521,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             ++published;
             return true;
         };
-        if (p.early_wait) grid_dependency_wait();  // the launch before this one zeroes the counter
+        tma_prefetch_desc(mR1);
+        tma_prefetch_desc(mC1);
+        if (C::RES > 1) tma_prefetch_desc(mR2);
         const uint32_t all = static_cast<uint32_t>(p.items[C::KEYS ? 0 : 1]), chunk = p.chunk[C::KEYS ? 0 : 1];
         uint32_t* const counter = p.claims + C::MODE;
-        uint32_t left = 0, i = 0, next = atomicAdd(counter, chunk);
+        // A CTA's first items go by its number, so that their loads need not
+        // wait for the launch that zeroes the counter; the next ones are
+        // claimed before they are needed (the answer takes a while).
+        uint32_t left = chunk, i = blockIdx.x * chunk, next = 0;
+        bool claimed = false;
+        auto claim = [&]() {
+            if (p.early_wait) grid_dependency_wait();
+            next = gridDim.x * chunk + atomicAdd(counter, chunk);
+            claimed = true;
+        };
 #pragma unroll 1
         while (ok) {
-            if (left == 0) {  // (claimed one ahead: the answer takes a while)
+            if (left == 0) {
+                if (!claimed) claim();
                 i = next;
                 left = chunk;
-                if (i < all) next = atomicAdd(counter, chunk);
+                claimed = false;
             }
             if (i >= all) {
                 it.n = kItemEnd;
@@ -570,6 +585,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             for (int c = 0; ok && c < C::STAGE1; ++c) ok = grant(ring);
             ++done;
+            if (left == 0 && !claimed && ok) claim();
         }
         if (!ok || *abort_flag) {
             // Let every copy this thread started land before the CTA retires.
@@ -579,6 +595,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
     } else if (warp == MW + 2 && lane == 0) {
         // --------------------- producer: C2, and statistics of streamed rows
+        tma_prefetch_desc(mC2);
         if (p.early_wait) grid_dependency_wait();  // the launch before this one writes the statistics
         grid_launch_dependents();
         Ring ring(sC, C::N1, C::N2);
