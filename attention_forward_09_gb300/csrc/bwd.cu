@@ -109,6 +109,7 @@ struct BwdCfg {
     static constexpr int SMEM_BYTES = O_BARS + NUM_BARS * 8 + 16 + ITEMS * 64;
         static_assert(MATH_WARPS * 32 * REG_MATH + 128 * REG_OTHER <= THREADS * 96, "register split");
     static_assert(T_RES + RES_TMEM * D / 2 <= 512, "TMEM budget");
+    static_assert(BM * ACCS * D * 4 <= SLOTS * C_BYTES, "a split item's sums over the ring");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
     static_assert(C_BYTES == CCH * BM * 128, "a slot holds a chunk of a gradient tile");
     static_assert(!HAS_DS || (N2 >= NCK && N1 > NCK && N1 >= G0), "the rings hold what the issuing warps wait for at once");
@@ -355,10 +356,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // at a time, and publishes each in shared memory; rings, barriers and
     // buffers carry on from item to item, so that the next item's loads and
     // first products overlap the present one's last ones and its epilogue.
+    //   Launches of few items and many steps split each item's steps over a cluster
+    // of `split` CTAs, one item a cluster; their sums are added on chip.
+    const int split = p.split[C::KEYS ? 0 : 1], crank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int heads = C::KEYS ? p.Hkv : p.Hq;
     struct Item {
         int n;                     // steps; 0: zeros to write; kItemEnd: no more items
         int t_lo, t_hi;            // streamed tiles of each head
+        int t_first, h_first;      // the first step's tile, and its head from the first streamed one
         int head, r0;              // resident head, first resident row within the document
         int diag;                  // causal: row i sees key j iff j <= i + diag
         int res_start, res_all, res_len, str_start, str_len;
@@ -415,8 +420,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 it.t_hi = (max(0, min(d.Lk, min(it.r0 + BM, d.Lq) + it.diag)) + BN - 1) / BN;
         }
         it.n = max(0, it.t_hi - it.t_lo) * (C::KEYS ? p.group : 1);
+        it.t_first = it.t_lo;
+        it.h_first = 0;
+        if (split > 1 && it.n > 0) {  // this CTA's share of the steps
+            const int nt = it.t_hi - it.t_lo;
+            const int j0 = static_cast<int>(static_cast<long long>(it.n) * crank / split);
+            it.n = static_cast<int>(static_cast<long long>(it.n) * (crank + 1) / split) - j0;
+            it.t_first += j0 % nt;
+            it.h_first = j0 / nt;
+        }
     };
-    if (status_has_timeout(p.status, kDevTimeout)) {
+    // (a CTA of a cluster stays: the others read its shared memory)
+    if (split == 1 && status_has_timeout(p.status, kDevTimeout)) {
         grid_dependency_wait();
         return;
     }
@@ -529,7 +544,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // A CTA's first items go by its number, so that their loads need not
         // wait for the launch that zeroes the counter; the next ones are
         // claimed before they are needed (the answer takes a while).
-        uint32_t left = chunk, i = blockIdx.x * chunk, next = 0;
+        uint32_t left = chunk, i = blockIdx.x / split * chunk, next = 0;
         bool claimed = false;
         auto claim = [&]() {
             if (p.early_wait) grid_dependency_wait();
@@ -538,7 +553,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         };
 #pragma unroll 1
         while (ok) {
-            if (left == 0) {
+            if (left == 0 && split > 1) {  // one item a cluster
+                i = all;
+            } else if (left == 0) {
                 if (!claimed) claim();
                 i = next;
                 left = chunk;
@@ -567,7 +584,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     ok = false;
                 }
             }
-            int t = it.t_lo, h = str_head(it.head);
+            int t = it.t_first, h = str_head(it.head) + it.h_first;
 #pragma unroll 1
             for (int j = 0; ok && j < it.n; ++j) {
                 const int t2 = t, h2 = h;  // step j
@@ -583,8 +600,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h2, it.str_start + t2 * BN, c);
                 }
             }
-            for (int c = 0; ok && c < C::STAGE1; ++c) ok = grant(ring);
             ++done;
+            if (split > 1) continue;
+            for (int c = 0; ok && c < C::STAGE1; ++c) ok = grant(ring);
             if (left == 0 && !claimed && ok) claim();
         }
         if (!ok || *abort_flag) {
@@ -609,7 +627,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             const int t_lo = GBATTN_ITEM(i, t_lo), t_hi = GBATTN_ITEM(i, t_hi), start = GBATTN_ITEM(i, str_start);
             const long long stat_base = static_cast<uint32_t>(GBATTN_ITEM(i, stat));
-            int t = t_lo, h = str_head(GBATTN_ITEM(i, head));
+            int t = GBATTN_ITEM(i, t_first), h = str_head(GBATTN_ITEM(i, head)) + GBATTN_ITEM(i, h_first);
             mbar_arrive(b_item_free(i % C::ITEMS));
 #pragma unroll 1
             for (int j = 0; ok && j < n; ++j) {
@@ -631,7 +649,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     ++h;
                 }
             }
-            for (int c = 0; ok && n > 0 && c < C::STAGE2; ++c) ok = grant(ring);
+            for (int c = 0; ok && n > 0 && split == 1 && c < C::STAGE2; ++c) ok = grant(ring);
         }
         if (!ok || *abort_flag) {
             drain(ring);
@@ -727,7 +745,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             __syncwarp();
         }
-        int t = t_lo;
+        int t = GBATTN_ITEM(item, t_first);
         // All of a tile's chunks have landed.
         auto landed = [&](Ring s) -> bool {
             for (int c = 0; c < NCK; ++c) {
@@ -942,6 +960,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         mbar_wait_drain(b_drain, 0);
     }
+    if (split > 1) {  // with the math warps
+        cluster_sync();
+        cluster_sync();
+    }
     } else {
         regs_inc<C::REG_MATH>();
         // ---------------------------------------------------------------- math
@@ -966,6 +988,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int acc = wg / PARTS, part = wg % PARTS;
         const bool storer = lane == 0 && warp % (4 * PARTS) == 0;
         int leaving = -1;  // the first of the slots that are being read
+        bool have = false; // (split) there is an item
         auto give_back = [&]() {
             if (storer && leaving >= 0) {
                 bulk_wait_read0();
@@ -1031,7 +1054,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int edge_lo = C::KEYS && p.causal ? (max(0, r0 + BM - 1 - diag) + BN - 1) / BN : 0;
         const int edge_hi = max(0, !C::KEYS && p.causal ? min(str_len, r0 + diag + 1) : str_len) / BN;
         const int t_lo = GBATTN_ITEM(item, t_lo), t_hi = GBATTN_ITEM(item, t_hi);
-        int t = t_lo;
+        int t = GBATTN_ITEM(item, t_first);
 #pragma unroll 1
         for (int j = 0; ok && j < n; ++j) {
             const int g = J + j, sb = g % SB, db = g % DPB;
@@ -1142,7 +1165,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // An accumulator's 32 column chunks are taken in turn by its warpgroups.  Rows are staged in the ring's slots,
         // in the boxes' swizzle, and leave by TMA where the tile lies wholly
         // inside its document, else row by row.
-        if (ok) {
+        if (split > 1) {  // the sums, or zeros, as fp32 rows over the ring, 16-byte pieces swizzled by row
+            constexpr int P = C::ACCS * D / 4;  // pieces of a row
+            const uint32_t to = sC + static_cast<uint32_t>(r) * (P * 16);
+#pragma unroll 1
+            for (int x = wg; x < C::ACCS * D / 32; x += WGS) {
+                uint32_t o[32];
+                if (ok && n > 0) {
+                    tmem_ld32(tl + C::T_ACC + x * 32, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    st_shared_v4(to + (((x * 8 + e) ^ (r & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+            have = true;
+        } else if (ok) {
             const int res_all = GBATTN_ITEM(item, res_all), res_len = GBATTN_ITEM(item, res_len);
             const int head = GBATTN_ITEM(item, head), res_start = GBATTN_ITEM(item, res_start);
             const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && acc == 0);
@@ -1226,6 +1267,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         }
         give_back();
+        if (split > 1) {
+            cluster_sync();
+            if (ok && have) {
+                // CTA c adds up rows [c R, (c + 1) R) over the cluster, in rank order
+                constexpr int P = C::ACCS * D / 4;
+                const int R = BM / split, r0 = GBATTN_ITEM(0, r0), res_all = GBATTN_ITEM(0, res_all), res_len = GBATTN_ITEM(0, res_len);
+                for (int x = threadIdx.x; x < R * P; x += MW * 32) {
+                    const int i = crank * R + x / P, piece = x % P;
+                    if (r0 + i >= res_all) continue;
+                    const uint32_t at = sC + static_cast<uint32_t>(i) * (P * 16) + ((piece ^ (i & 7)) << 4);
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int c = 0; c < split; ++c) {
+                        const float4 v = ld_cluster_f4(mapa_shared(at, c));
+                        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                    }
+                    const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && piece < D / 4);
+                    const float f = r0 + i >= res_len ? 0.f : (is_dv ? 1.f : p.scale);
+                    uint16_t* out = static_cast<uint16_t*>(C::KEYS ? (is_dv ? p.dv : p.dk) : p.dq) +
+                                    ((static_cast<long long>(GBATTN_ITEM(0, res_start)) + r0 + i) * heads + GBATTN_ITEM(0, head)) * D +
+                                    piece % (D / 4) * 4;
+                    *reinterpret_cast<uint2*>(out) =
+                        f == 0.f ? make_uint2(0u, 0u)
+                                 : make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
+                }
+            }
+            cluster_sync();  // no CTA leaves while another still reads its shared memory
+        }
     }
 
     // --------------------------------------------------------------- teardown
@@ -1275,15 +1343,20 @@ cudaError_t launch_pass(const BwdMaps& m, const CUtensorMap& o1, const CUtensorM
     cudaError_t e = allow_smem<C>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(items < num_sms ? items : num_sms));
+    const int split = p.split[C::KEYS ? 0 : 1];
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = split;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(split > 1 ? items * split : (items < num_sms ? items : num_sms)));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = split > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, attn_bwd_sm103a<C>, m.q, m.dout, m.k, m.v, o1, o2, static_cast<const BwdParams&>(p));
     p.early_wait = 0;
     return e;
@@ -1325,6 +1398,11 @@ cudaError_t launch_bwd(int D, const BwdMaps& m, BwdParams p, int num_sms, cudaSt
     for (int x = 0; x < 2; ++x) {
         const long long c = p.items[x] / (64ll * num_sms);
         p.chunk[x] = static_cast<uint32_t>(c < 1 ? 1 : (c > 256 ? 256 : c));
+        // Half the SMs or fewer busy, with items of eight steps or more: as many
+        // CTAs an item as fill the SMs, four steps each at least.
+        const long long steps = x == 0 ? static_cast<long long>(p.tiles_q) * p.group : p.tiles_k;
+        p.split[x] = 1;
+        while (p.split[x] < 8 && p.items[x] * p.split[x] * 2 <= num_sms && steps >= 8ll * p.split[x]) p.split[x] *= 2;
     }
     switch (D) {
         case 64: return launch_d<64>(m, p, num_sms, stream);

@@ -345,6 +345,7 @@ struct BwdParams {
     // Set by launch_bwd:
     long long items[2];     // (tile, head, document) with the keys, with the queries resident
     uint32_t chunk[2];      // items a claim
+    int split[2];           // > 1: an item's steps are shared by a cluster of that many CTAs
     int early_wait;         // 1: the launch before this one writes the statistics
 };
 long long bwd_stat_stride(long long Tq, int num_docs);

@@ -258,8 +258,10 @@ def test_another_stream_and_a_captured_call():
 
 
 @pytest.mark.parametrize("D", [64, 128, 192, 256])
-def test_a_wait_that_gives_up_reports_it_and_the_context_stays_usable(D):
-    q, k, v, out, lse, do, s, got = dense_case(1, 128, 700, 1, 1, D, False)
+@pytest.mark.parametrize("Sk", [700, 2100])
+def test_a_wait_that_gives_up_reports_it_and_the_context_stays_usable(D, Sk):
+    """Items a CTA has for itself, and (the longer context) items that clusters share."""
+    q, k, v, out, lse, do, s, got = dense_case(1, 128, Sk, 1, 1, D, False)
     prev = gb.attn_set_wait_give_up(True)
     try:
         st = status_word()
@@ -377,3 +379,14 @@ def test_infinities_and_nan_behind_the_causal_diagonal_of_a_row():
         x[:, :100] = float("nan")
     again = gb.attn_bwd_dense(q2, k, v, out2, lse, do2, s, True)
     assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+@pytest.mark.parametrize("D", workloads.HEAD_SIZES)
+@pytest.mark.parametrize("causal", [False, True])
+def test_few_items_of_many_steps(D, causal):
+    """Steps shared by clusters of 2, 4 and 8 CTAs: of the keys' pass (many heads to a KV head, many queries), of the
+    queries' pass (long contexts), with tails, empty shares, empty entries and rows that see nothing."""
+    for shape in ((1, 700, 130, 8, 1), (2, 1100, 500, 4, 1), (1, 100, 2100, 2, 1), (1, 1500, 1030, 9, 3), (1, 3000, 1, 2, 2)):
+        dense_case(*shape, D, causal, dlse=True)
+    packed([0, 1300, 40], [70, 120, 3], 6, 1, D, causal, odt=torch.float32, dlse=True)
+    packed([130, 20], [1500, 0], 2, 1, D, causal, tail=30)
