@@ -13,15 +13,19 @@
 //     head (fp32), one pass over out and dout, HBM-bound;
 //   attn_bwd_sm103a, keys resident: a tile of 128 keys of one KV head stays
 //     in shared memory while the queries of every head that shares it stream
-//     by; S^T = K Q^T and dP^T = V dO^T go to TMEM, two warpgroups turn them
+//     by; S^T = K Q^T and dP^T = V dO^T go to TMEM, four warpgroups turn them
 //     into P^T and dS^T (bf16, written over them), which are the A operands
 //     of dV += P^T dO and dK += dS^T Q straight from TMEM;
 //   attn_bwd_sm103a, queries resident: the same pipeline with the roles
 //     exchanged: S = Q K^T, dP = dO V^T, dQ += dS K.
-// A gradient row is summed by one CTA in one order, the heads of a group
-// included, so results do not depend on timing: there are no atomics.  The
-// price is that S and dP are formed twice, seven products for the five that
-// one pass with atomics on dQ would need.
+// A gradient row is summed by one CTA, or by a cluster whose sums are added in
+// rank order, the heads of a group included, so results do not depend on
+// timing: there are no atomics.  The price is that S and dP are formed twice,
+// seven products for the five that one pass with atomics on dQ would need.
+//
+// DiT self-attention, 2 x 4096 rows, 24 heads, D = 128: 926 us a call, of them 23
+// for the statistics, 465 and 407 for the two passes by themselves; 1.11 PFLOP/s
+// of five products, 1.55 of the seven, at the power cap (1.83 GHz).
 //
 // P and dS are rounded to bf16 as operands of the second products, as P is in
 // the forward kernels (at most 2^-8 of each term, independent of one another);
@@ -91,9 +95,10 @@ struct BwdCfg {
     // setmaxnreg split of the 640 x 96 registers of the launch
     static constexpr int REG_MATH = 104, REG_OTHER = 64;
     static constexpr int THREADS = 32 * MATH_WARPS + 128;
-    static constexpr int STAGE1 = NCK, STAGE2 = ACCS == 2 ? NCK : 0;  // slots of each ring that an item's gradients leave through
+    // slots of each ring that an item's gradients leave through
+    static constexpr int STAGE1 = NCK, STAGE2 = ACCS == 2 ? NCK : 0;
     static constexpr int ITEMS = 3;                            // items published ahead
-    static constexpr int BARS_FIXED = 24 + 2 * ITEMS + 2 * STATS;
+    static constexpr int BARS_FIXED = 22 + 2 * ITEMS + 2 * STATS;
     static constexpr int RELEASES = HAS_DS && !SHARED ? 2 : 1;  // commits that release a slot
     static constexpr int ROOM = 232448 - RES_SMEM * R_BYTES - STATS * STAT_BYTES - 16 - ITEMS * 64 - BARS_FIXED * 8;
     static constexpr int FIT = ROOM / (C_BYTES + 16);
@@ -107,7 +112,7 @@ struct BwdCfg {
     static constexpr int O_STAT = O_C + SLOTS * C_BYTES;
     static constexpr int O_BARS = O_STAT + STATS * STAT_BYTES;
     static constexpr int SMEM_BYTES = O_BARS + NUM_BARS * 8 + 16 + ITEMS * 64;
-        static_assert(MATH_WARPS * 32 * REG_MATH + 128 * REG_OTHER <= THREADS * 96, "register split");
+    static_assert(MATH_WARPS * 32 * REG_MATH + 128 * REG_OTHER <= THREADS * 96, "register split");
     static_assert(T_RES + RES_TMEM * D / 2 <= 512, "TMEM budget");
     static_assert(BM * ACCS * D * 4 <= SLOTS * C_BYTES, "a split item's sums over the ring");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -231,7 +236,8 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, c
     if (d.bad) return;
     const long long i0 = static_cast<long long>(blockIdx.x) * rows;
     if (i0 >= d.Lq) return;
-    const int h0 = blockIdx.y * heads, nh = min(heads, p.Hq - h0), nr = static_cast<int>(min(static_cast<long long>(rows), d.Lq - i0));
+    const int h0 = blockIdx.y * heads, nh = min(heads, p.Hq - h0);
+    const int nr = static_cast<int>(min(static_cast<long long>(rows), d.Lq - i0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
     for (int u0 = warp * PER_WARP + lane / LANES; u0 - lane / LANES < nr * nh; u0 += 8 * PER_WARP * UN) {
         uint4 g[UN], o[UN], o2[UN];
@@ -260,7 +266,8 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, c
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 f = unpack_bf16x2(gw[e]);
-                const float2 v = F32 ? make_float2(__uint_as_float(ow[2 * e]), __uint_as_float(ow[2 * e + 1])) : unpack_bf16x2(ow[e]);
+                const float2 v = F32 ? make_float2(__uint_as_float(ow[2 * e]), __uint_as_float(ow[2 * e + 1]))
+                                     : unpack_bf16x2(ow[e]);
                 acc = fmaf(f.x, v.x, acc);
                 acc = fmaf(f.y, v.y, acc);
             }
@@ -327,21 +334,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     auto b_res = [&](int r) { return smem_u32(&bars[r]); };
     auto b_s_full = [&](int b) { return smem_u32(&bars[2 + b]); };
-    // P is there: of each warpgroup's columns the first 32, or the rest
-    // (without dV, the first: S has been read)
-    auto b_p_full = [&](int b, int half) { return smem_u32(&bars[4 + b + 2 * half]); };
-    auto b_dp_full = [&](int b) { return smem_u32(&bars[8 + b]); };
-    auto b_ds_full = [&](int b) { return smem_u32(&bars[10 + b]); };
-    auto b_turn = [&](int b) { return smem_u32(&bars[12 + b]); };
-    const uint32_t b_done = smem_u32(&bars[14]), b_drain = smem_u32(&bars[15]), b_res_in = smem_u32(&bars[16]);
-    const uint32_t b_acc_free = smem_u32(&bars[17]);  // the accumulators have been read
-    auto b_res_free = [&](int r) { return smem_u32(&bars[18 + r]); };
-    auto b_staged = [&](int a) { return smem_u32(&bars[20 + a]); };  // a gradient tile lies in its slots
-    auto b_copied = [&](int a) { return smem_u32(&bars[22 + a]); };  // what goes row by row has been read from them
-    auto b_item_full = [&](int b) { return smem_u32(&bars[24 + b]); };
-    auto b_item_free = [&](int b) { return smem_u32(&bars[24 + C::ITEMS + b]); };
-    auto b_stat_full = [&](int b) { return smem_u32(&bars[24 + 2 * C::ITEMS + b]); };
-    auto b_stat_empty = [&](int b) { return smem_u32(&bars[24 + 2 * C::ITEMS + C::STATS + b]); };
+    auto b_p_full = [&](int b) { return smem_u32(&bars[4 + b]); };  // P is there (without dV: S has been read)
+    auto b_dp_full = [&](int b) { return smem_u32(&bars[6 + b]); };
+    auto b_ds_full = [&](int b) { return smem_u32(&bars[8 + b]); };
+    auto b_turn = [&](int b) { return smem_u32(&bars[10 + b]); };  // S(j + 1) has been issued (dV alone: dV(j) is done)
+    const uint32_t b_done = smem_u32(&bars[12]), b_drain = smem_u32(&bars[13]), b_res_in = smem_u32(&bars[14]);
+    const uint32_t b_acc_free = smem_u32(&bars[15]);  // the accumulators have been read
+    auto b_res_free = [&](int r) { return smem_u32(&bars[16 + r]); };
+    auto b_staged = [&](int a) { return smem_u32(&bars[18 + a]); };  // a gradient tile lies in its slots
+    auto b_copied = [&](int a) { return smem_u32(&bars[20 + a]); };  // what goes row by row has been read from them
+    auto b_item_full = [&](int b) { return smem_u32(&bars[22 + b]); };
+    auto b_item_free = [&](int b) { return smem_u32(&bars[22 + C::ITEMS + b]); };
+    auto b_stat_full = [&](int b) { return smem_u32(&bars[22 + 2 * C::ITEMS + b]); };
+    auto b_stat_empty = [&](int b) { return smem_u32(&bars[22 + 2 * C::ITEMS + C::STATS + b]); };
     volatile int* const items = reinterpret_cast<volatile int*>(tmem_slot + 4);
     auto b_full = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + s]); };
     auto b_empty = [&](int s) { return smem_u32(&bars[C::BARS_FIXED + SLOTS + s]); };
@@ -380,29 +385,34 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (all) got = __all_sync(0xffffffffu, got);
         return got ? GBATTN_ITEM(it, n) : -1;
     };
-    // The i-th item; n = -1: nothing to write.
-    auto item_at = [&](uint32_t x, Item& it) {
+    // The i-th item (n = -1: nothing to write); how far on the next one is that
+    // may have something (a tile past its document has none for any head, nor
+    // have the tiles behind it).
+    auto item_at = [&](uint32_t x, Item& it) -> uint32_t {
         it.n = -1;
         int tile, doc;
+        uint32_t skip;
         if (p.causal) {
             it.head = x % heads;
             x /= heads;
             doc = x % p.num_docs;
             tile = x / p.num_docs;
             if (!C::KEYS) tile = p.tiles_q - 1 - tile;
+            skip = heads - it.head;
         } else {
             const int tiles = C::KEYS ? p.tiles_k : p.tiles_q;
             tile = x % tiles;
             x /= tiles;
             it.head = x % heads;
             doc = x / heads;
+            skip = tiles - tile;
         }
         const BwdDoc d = bwd_doc(p, doc, false);
-        if (d.bad) return;
+        if (d.bad) return skip;
         it.res_all = C::KEYS ? d.Lk_all : d.Lq_all;
         if (C::KEYS && p.causal) tile -= p.tiles_k - (it.res_all + BM - 1) / BM;
         it.r0 = tile * BM;
-        if (tile < 0 || it.r0 >= it.res_all) return;
+        if (tile < 0 || it.r0 >= it.res_all) return skip;
         it.res_len = C::KEYS ? d.Lk : d.Lq;
         it.str_len = C::KEYS ? d.Lq : d.Lk;
         it.res_start = C::KEYS ? d.k_start : d.q_start;
@@ -429,6 +439,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             it.t_first += j0 % nt;
             it.h_first = j0 / nt;
         }
+        return 1u;
     };
     // (a CTA of a cluster stays: the others read its shared memory)
     if (split == 1 && status_has_timeout(p.status, kDevTimeout)) {
@@ -441,8 +452,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(b_res(b), 1);
             mbar_init(b_s_full(b), 1);
-            mbar_init(b_p_full(b, 0), MW);
-            mbar_init(b_p_full(b, 1), MW);
+            mbar_init(b_p_full(b), MW);
             mbar_init(b_dp_full(b), 1);
             mbar_init(b_ds_full(b), MW);
             mbar_init(b_turn(b), 1);
@@ -519,451 +529,453 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     };
     int res_loads[2] = {0, 0};  // (of the producer: loads of each resident tile so far)
     if (warp >= MW) {
-    regs_dec<C::REG_OTHER>();
-    if (warp == MW && lane == 0) {
-        // ---------------------------------- producer: resident tiles, then C1
-        const CUtensorMap *mR1 = C::KEYS ? &tmK : &tmQ, *mR2 = C::KEYS ? &tmV : &tmG;
-        Ring ring(sC, 0, C::N1);
-        Item it;
-        int done = 0;       // items with steps so far
-        int published = 0;  // items published
-        auto publish = [&]() -> bool {
-            const int b = published % C::ITEMS;
-            if (published >= C::ITEMS && !mbar_wait(b_item_free(b), (published / C::ITEMS - 1) & 1, abort_flag)) return false;
-            for (int w = 0; w < static_cast<int>(sizeof(Item) / 4); ++w)
-                items[b * 16 + w] = reinterpret_cast<const int*>(&it)[w];
-            mbar_arrive(b_item_full(b));
-            ++published;
-            return true;
-        };
-        tma_prefetch_desc(mR1);
-        tma_prefetch_desc(mC1);
-        if (C::RES > 1) tma_prefetch_desc(mR2);
-        const uint32_t all = static_cast<uint32_t>(p.items[C::KEYS ? 0 : 1]), chunk = p.chunk[C::KEYS ? 0 : 1];
-        uint32_t* const counter = p.claims + C::MODE;
-        // A CTA's first items go by its number, so that their loads need not
-        // wait for the launch that zeroes the counter; the next ones are
-        // claimed before they are needed (the answer takes a while).
-        uint32_t left = chunk, i = blockIdx.x / split * chunk, next = 0;
-        bool claimed = false;
-        auto claim = [&]() {
-            if (p.early_wait) grid_dependency_wait();
-            next = gridDim.x * chunk + atomicAdd(counter, chunk);
-            claimed = true;
-        };
-#pragma unroll 1
-        while (ok) {
-            if (left == 0 && split > 1) {  // one item a cluster
-                i = all;
-            } else if (left == 0) {
-                if (!claimed) claim();
-                i = next;
-                left = chunk;
-                claimed = false;
-            }
-            if (i >= all) {
-                it.n = kItemEnd;
-                ok = publish();
-                break;
-            }
-            item_at(i++, it);
-            --left;
-            if (it.n < 0) continue;
-            if (!(ok = publish())) break;
-            if (it.n == 0) continue;
-            for (int r = 0; r < C::RES; ++r) {
-                const CUtensorMap* m = r ? mR2 : mR1;
-                if (r >= C::RT0) {
-                    for (int c = 0; c < NCK; ++c) ok = ok && load(ring, m, it.head, it.res_start + it.r0, c);
-                } else if (ok && (done == 0 || mbar_wait(b_res_free(r), (done - 1) & 1, abort_flag))) {
-                    mbar_arrive_expect_tx(b_res(r), C::R_BYTES);
-                    for (int c = 0; c < NCH; ++c)
-                        tma_load_3d(sR + r * C::R_BYTES + c * (BM * 128), m, b_res(r), c * 64, it.head, it.res_start + it.r0);
-                    res_loads[r] = done + 1;
-                } else {
-                    ok = false;
-                }
-            }
-            int t = it.t_first, h = str_head(it.head) + it.h_first;
-#pragma unroll 1
-            for (int j = 0; ok && j < it.n; ++j) {
-                const int t2 = t, h2 = h;  // step j
-                if (++t == it.t_hi) {
-                    t = it.t_lo;
-                    ++h;
-                }
-                if (C::HAS_DS || j == 0)
-                    for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC1, h2, it.str_start + t2 * BN, c);
-                if (!C::HAS_DS) {  // S(j + 1) comes before dV(j)
-                    if (j + 1 < it.n)
-                        for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC1, h, it.str_start + t * BN, c);
-                    for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h2, it.str_start + t2 * BN, c);
-                }
-            }
-            ++done;
-            if (split > 1) continue;
-            for (int c = 0; ok && c < C::STAGE1; ++c) ok = grant(ring);
-            if (left == 0 && !claimed && ok) claim();
-        }
-        if (!ok || *abort_flag) {
-            // Let every copy this thread started land before the CTA retires.
-            for (int r = 0; r < C::RES_SMEM; ++r)
-                if (res_loads[r] > 0) mbar_wait_drain(b_res(r), (res_loads[r] - 1) & 1);
-            drain(ring);
-        }
-    } else if (warp == MW + 2 && lane == 0) {
-        // --------------------- producer: C2, and statistics of streamed rows
-        tma_prefetch_desc(mC2);
-        if (p.early_wait) grid_dependency_wait();  // the launch before this one writes the statistics
-        grid_launch_dependents();
-        Ring ring(sC, C::N1, C::N2);
-        int issued = 0;
-#pragma unroll 1
-        for (int i = 0; ok; ++i) {
-            const int n = next_item(i, false);
-            if (n < 0) {
-                ok = n == kItemEnd;
-                break;
-            }
-            const int t_lo = GBATTN_ITEM(i, t_lo), t_hi = GBATTN_ITEM(i, t_hi), start = GBATTN_ITEM(i, str_start);
-            const long long stat_base = static_cast<uint32_t>(GBATTN_ITEM(i, stat));
-            int t = GBATTN_ITEM(i, t_first), h = str_head(GBATTN_ITEM(i, head)) + GBATTN_ITEM(i, h_first);
-            mbar_arrive(b_item_free(i % C::ITEMS));
-#pragma unroll 1
-            for (int j = 0; ok && j < n; ++j) {
-                if (C::HAS_DS)
-                    for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h, start + t * BN, c);
-                if (C::KEYS && ok) {
-                    const int b = issued % C::STATS;
-                    if (issued >= C::STATS &&
-                        !(ok = mbar_wait(b_stat_empty(b), (issued / C::STATS - 1) & 1, abort_flag)))
-                        break;
-                    const long long at = h * p.stat_stride + stat_base + static_cast<long long>(t) * BN;
-                    mbar_arrive_expect_tx(b_stat_full(b), C::STAT_BYTES);
-                    bulk_load(sStat + b * C::STAT_BYTES, p.neg_lse2 + at, BN * 4, b_stat_full(b));
-                    bulk_load(sStat + b * C::STAT_BYTES + BN * 4, p.neg_delta + at, BN * 4, b_stat_full(b));
-                    ++issued;
-                }
-                if (++t == t_hi) {
-                    t = t_lo;
-                    ++h;
-                }
-            }
-            for (int c = 0; ok && n > 0 && split == 1 && c < C::STAGE2; ++c) ok = grant(ring);
-        }
-        if (!ok || *abort_flag) {
-            drain(ring);
-            for (int g = (issued > C::STATS ? issued - C::STATS : 0); g < issued; ++g)
-                mbar_wait_drain(b_stat_full(g % C::STATS), (g / C::STATS) & 1);
-        }
-    } else if (warp == MW + 1 || (warp == MW + 3 && C::ISSUERS == 2)) {
-        // ----------------------------------------------------------------- MMA
-        // Each issuing warp walks its schedule as a whole; one elected lane issues.
-        constexpr uint32_t kIdS = idesc_bf16_f32(BM, BN, false, false);
-        constexpr uint32_t kIdA = idesc_bf16_f32(BM, C::CW, false, true);
-        const bool first_warp = warp == MW + 1;
-        const bool leader = elect_one();
-        const uint32_t dR = desc_lo(sR, 16);
-        const uint32_t dCk = desc_lo(sC, 16);           // streamed chunk, K-major
-        const uint32_t dCm = desc_lo(sC, BN * 128);     // streamed chunk, MN-major
-        auto wait_all = [&](uint32_t bar, uint32_t ph) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag));
-        };
-        // Rows of a streamed tile that no resident row may see at all (past the
-        // document, the neighbours' rows, or rows without a key) may hold
-        // anything; P and dS are 0 there but 0 * NaN is not, so they are zeroed
-        // before the second product reads them.
-        int item = 0, n = 0, edge_lo = 0, edge_hi = 0;  // tiles below edge_lo or from edge_hi on have such rows
-        auto edge_rows = [&](int t) { return t < edge_lo || t >= edge_hi; };
-        auto zero_rows = [&](int s, int t) {
-            const int hi = min(BN, GBATTN_ITEM(item, str_len) - t * BN);
-            const int lo = (C::KEYS && p.causal) ? min(hi, max(0, -GBATTN_ITEM(item, diag) - t * BN)) : 0;
-            for (int x = lane; x < (lo + BN - hi) * CCH * 8; x += 32) {
-                const int u = x & 7, rc = x >> 3, c = rc % CCH, r = rc / CCH;
-                st_shared_v4(sC + s * C::C_BYTES + c * (BN * 128) + (r < lo ? r : hi + r - lo) * 128 + u * 16, 0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-        };
-        // X (128 x BN) (+)= resident r * chunk c of a streamed tile, in slot s
-        auto scores = [&](uint32_t to, int r, int c, int s) {
-            uint32_t a = r >= C::RT0 ? tmem + C::T_RES + (r - C::RT0) * (D / 2) + c * (C::CW / 2)
-                                     : dR + ((r * C::R_BYTES + c * CCH * BM * 128) >> 4);
-            uint32_t b = dCk + s * (C::C_BYTES >> 4);
-            asm volatile("" : "+r"(a), "+r"(b));  // (worked out here, not kept over the steps)
-#pragma unroll
-            for (int k = 0; k < C::CW / 16; ++k) {
-                const uint32_t off = ((k >> 2) * BN * 128 + (k & 3) * 32) >> 4, acc = (c > 0 || k > 0) ? 1u : 0u;
-                if (r >= C::RT0)
-                    mma_ts(tmem + to, a + k * 8, b + off, kIdS, acc);
-                else
-                    mma_ss(tmem + to, a + off, b + off, kIdS, acc);
-            }
-        };
-        // columns [c CW, (c + 1) CW) of acc += A (bf16 pairs in X's columns, 16
-        // of every 32) * chunk c of a streamed tile, in slot s
-        // Of the rows, those of the warpgroups' first 32 columns (half 0), the
-        // rest (half 1) or all (half 2).
-        auto accumulate = [&](uint32_t acc, uint32_t x, int c, int s, bool first, int half) {
-            uint32_t a = tmem + x, b = dCm + s * (C::C_BYTES >> 4);
-            asm volatile("" : "+r"(a), "+r"(b));
-#pragma unroll
-            for (int k = 0; k < BN / 16; ++k)
-                if (half == 2 || ((k >> 1) & 1) == half)
-                    mma_ts(tmem + acc + c * C::CW, a + (k >> 1) * 32 + (k & 1) * 8, b + ((k * 16 * 128) >> 4), kIdA,
-                           (!first || k > 0) ? 1u : 0u);
-        };
-        // Cursors: the next chunk of C1 and of C2 that this warp uses.
-        Ring c1(sC, 0, C::N1), c2(sC, C::N1, C::N2);
-        auto moved = [](Ring r) {
-            for (int c = 0; c < NCK; ++c) r.next();
-            return r;
-        };
-        int J = 0;     // steps of the items so far: buffers and phases go by J + j
-        int done = 0;  // items with steps so far
-        auto acc_free = [&]() -> bool { return done == 0 || wait_all(b_acc_free, (done - 1) & 1); };
-        ok = !*abort_flag;  // a launch told to give up issues nothing
-#pragma unroll 1
-        for (; ok; ++item) {
-        n = next_item(item, true);
-        if (n <= 0) {
-            if (n < 0) {
-                ok = n == kItemEnd;
-                break;
-            }
-            if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
-            continue;
-        }
-        const int t_lo = GBATTN_ITEM(item, t_lo), t_hi = GBATTN_ITEM(item, t_hi);
-        edge_lo = C::KEYS && p.causal ? (max(0, -GBATTN_ITEM(item, diag)) + BN - 1) / BN : 0;
-        edge_hi = GBATTN_ITEM(item, str_len) / BN;
-        if (C::RES_TMEM > 0) {  // the math warps have copied those residents into tensor memory
-            ok = wait_all(b_res_in, done & 1);
-            for (int g = 0; g < G0; ++g) {
-                if (ok && lane == 0) mbar_arrive(b_empty(c1.s));
-                c1.next();
-            }
-            __syncwarp();
-        }
-        int t = GBATTN_ITEM(item, t_first);
-        // All of a tile's chunks have landed.
-        auto landed = [&](Ring s) -> bool {
-            for (int c = 0; c < NCK; ++c) {
-                if (!wait_all(b_full(s.s), s.ph)) return false;
-                s.next();
-            }
-            return true;
-        };
-        // S of a step from C1's chunks, released once read when `free_c1`.
-        auto issue_s = [&](int j, Ring s, bool free_c1) {
-            for (int c = 0; c < NCK; ++c) {
-                scores(C::T_S + ((J + j) % SB) * BN, 0, c, s.s);
-                if (free_c1) mma_commit(b_empty(s.s));
-                s.next();
-            }
-            mma_commit(b_s_full((J + j) % SB));
-            if (C::RES_SMEM > 0 && j + 1 == n) mma_commit(b_res_free(0));
-        };
-        if constexpr (C::SHARED) {
-            // ---------------------------------- S and dP in the same columns
-            // S(j), chunk by chunk: the last ones come into slots released just before
-            auto next_s = [&](int j) -> bool {
-                Ring s = c1;
-                for (int c = 0; c < NCK; ++c) {
-                    if (!wait_all(b_full(s.s), s.ph)) return false;
-                    tc_fence_after();
-                    if (leader) {
-                        scores(C::T_S, 0, c, s.s);
-                        if (c == NCK - 1) mma_commit(b_s_full(0));
-                        if (c == NCK - 1 && j + 1 == n) mma_commit(b_res_free(0));
-                    }
-                    __syncwarp();
-                    s.next();
-                }
+        regs_dec<C::REG_OTHER>();
+        if (warp == MW && lane == 0) {
+            // ---------------------------------- producer: resident tiles, then C1
+            const CUtensorMap *mR1 = C::KEYS ? &tmK : &tmQ, *mR2 = C::KEYS ? &tmV : &tmG;
+            Ring ring(sC, 0, C::N1);
+            Item it;
+            int done = 0;       // items with steps so far
+            int published = 0;  // items published
+            auto publish = [&]() -> bool {
+                const int b = published % C::ITEMS;
+                if (published >= C::ITEMS && !mbar_wait(b_item_free(b), (published / C::ITEMS - 1) & 1, abort_flag))
+                    return false;
+                for (int w = 0; w < static_cast<int>(sizeof(Item) / 4); ++w)
+                    items[b * 16 + w] = reinterpret_cast<const int*>(&it)[w];
+                mbar_arrive(b_item_full(b));
+                ++published;
                 return true;
             };
-            ok = ok && wait_all(b_res(0), done & 1) && next_s(0);
-            for (int j = 0; ok && j < n; ++j) {
-                if (!(ok = landed(c2) && wait_all(b_p_full(0, 0), (J + j) & 1))) break;
-                tc_fence_after();
-                if (leader) {
-                    Ring s = c2;
-                    for (int c = 0; c < NCK; ++c) {
-                        scores(C::T_DP, 1, c, s.s);
-                        mma_commit(b_empty(s.s));
-                        s.next();
-                    }
-                    mma_commit(b_dp_full(0));
-                }
-                __syncwarp();
-                c2 = moved(c2);
-                if (edge_rows(t)) {
-                    Ring s = c1;
-                    for (int c = 0; c < NCK; ++c) {
-                        zero_rows(s.s, t);
-                        s.next();
-                    }
-                }
-                if (!(ok = (j > 0 || acc_free()) && wait_all(b_ds_full(0), (J + j) & 1))) break;
-                tc_fence_after();
-                if (leader) {
-                    Ring s = c1;
-                    for (int c = 0; c < NCK; ++c) {
-                        accumulate(C::T_ACC, C::T_DP, c, s.s, j == 0, 2);
-                        mma_commit(b_empty(s.s));
-                        s.next();
-                    }
-                }
-                __syncwarp();
-                c1 = moved(c1);
-                if (j + 1 < n && !(ok = next_s(j + 1))) break;
-                if (++t == t_hi) t = t_lo;
-            }
-        } else if constexpr (!C::HAS_DS) {
-            // ------------------------------------ dV alone: one ring, S(j + 1) before dV(j)
-            if (first_warp) {
-                ok = ok && wait_all(b_res(0), done & 1);
-                for (int j = 0; ok && j < n; ++j) {
-                    if (!(ok = landed(c1))) break;
-                    // the buffer's P has been used up
-                    const int g = J + j - SB;
-                    if (g >= 0 && !(ok = wait_all(b_turn(g % SB), (g / SB) & 1))) break;
-                    tc_fence_after();
-                    if (leader) issue_s(j, c1, true);
-                    __syncwarp();
-                    c1 = moved(c1);
-                    if (j > 0 || n == 1) c1 = moved(c1);  // past dout's tile
-                }
-                if (n > 1) c1 = moved(c1);
-            } else {
-                c1 = moved(c1);
-                if (n > 1) c1 = moved(c1);
-                for (int j = 0; ok && j < n; ++j) {
-                    // P(j) first: the slots' last turns were S(j)'s tiles or
-                    // earlier ones, and a wait by parity is exact only once
-                    // those have landed.
-                    if (!(ok = (j > 0 || acc_free()) && wait_all(b_p_full((J + j) % SB, 0), ((J + j) / SB) & 1) && landed(c1)))
-                        break;
-                    if (edge_rows(t)) {
-                        Ring s = c1;
-                        for (int c = 0; c < NCK; ++c) {
-                            zero_rows(s.s, t);
-                            s.next();
-                        }
-                    }
-                    tc_fence_after();
-                    if (leader) {
-                        Ring s = c1;
-                        for (int c = 0; c < NCK; ++c) {
-                            accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, c, s.s, j == 0, 2);
-                            mma_commit(b_empty(s.s));
-                            s.next();
-                        }
-                        mma_commit(b_turn((J + j) % SB));
-                    }
-                    __syncwarp();
-                    c1 = moved(c1);
-                    if (j + 2 < n) c1 = moved(c1);  // past the queries' tile of step j + 2
-                    if (++t == t_hi) t = t_lo;
-                }
-            }
-        } else if (first_warp) {
-            // -------------------------------------------------- S (and dV)
-            if (C::RT0 > 0) ok = ok && wait_all(b_res(0), done & 1);
-            ok = ok && wait_all(b_full(c1.s), c1.ph);
-            if (ok) {
-                tc_fence_after();
-                if (leader) issue_s(0, c1, true);
-                __syncwarp();
-            }
-            for (int j = 0; ok && j < n; ++j) {
-                const bool more = j + 1 < n;
-                c1.next();
-                if (more && !(ok = wait_all(b_full(c1.s), c1.ph))) break;
-                if (SB == 2) {  // dV(j - 1), which read the buffer, was issued here
-                    tc_fence_after();
-                    if (more && leader) issue_s(j + 1, c1, true);
-                    __syncwarp();
-                }
-                if (C::HAS_P) {
-                    if (!(ok = wait_all(b_full(c2.s), c2.ph) && (j > 0 || acc_free()))) break;
-                    if (edge_rows(t)) zero_rows(c2.s, t);
-                }
-                if (!(ok = wait_all(b_p_full((J + j) % SB, 0), ((J + j) / SB) & 1))) break;
-                tc_fence_after();
-                if (leader) {
-                    if (C::HAS_P) {
-                        accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, 0, c2.s, j == 0, 2);
-                        mma_commit(b_empty(c2.s));
-                    }
-                    if (more && SB == 1) issue_s(j + 1, c1, true);
-                    if (C::HAS_P && SB == 1) mbar_arrive(b_turn((J + j) & 1));
-                }
-                __syncwarp();
-                c2.next();
-                if (++t == t_hi) t = t_lo;
-            }
-        } else {
-            // --------------------------------------------- dP and dK or dQ
-            constexpr uint32_t kAcc = C::T_ACC + (C::HAS_P ? D : 0);
-            auto issue_dp = [&](int j) {
-                scores(C::T_DP + ((J + j) % DPB) * BN, 1, 0, c2.s);
-                mma_commit(b_empty(c2.s));
-                if (!C::HAS_P) mma_commit(b_empty(c2.s));  // (a slot is released twice)
-                mma_commit(b_dp_full((J + j) % DPB));
-                if (C::RES_SMEM > 1 && j + 1 == n) mma_commit(b_res_free(1));
+            tma_prefetch_desc(mR1);
+            tma_prefetch_desc(mC1);
+            if (C::RES > 1) tma_prefetch_desc(mR2);
+            const uint32_t all = static_cast<uint32_t>(p.items[C::KEYS ? 0 : 1]), chunk = p.chunk[C::KEYS ? 0 : 1];
+            uint32_t* const counter = p.claims + C::MODE;
+            // A CTA's first items go by its number, so that their loads need not
+            // wait for the launch that zeroes the counter; the next ones are
+            // claimed before they are needed (the answer takes a while).
+            uint32_t left = chunk, i = blockIdx.x / split * chunk, next = 0;
+            bool claimed = false;
+            auto claim = [&]() {
+                if (p.early_wait) grid_dependency_wait();
+                next = gridDim.x * chunk + atomicAdd(counter, chunk);
+                claimed = true;
             };
-            if (C::RT0 > 1) ok = ok && wait_all(b_res(1), done & 1);
-            ok = ok && wait_all(b_full(c2.s), c2.ph);
-            if (ok) {
-                tc_fence_after();
-                if (leader) issue_dp(0);
-                __syncwarp();
-            }
-            for (int j = 0; ok && j < n; ++j) {
-                const bool more = j + 1 < n;
-                c2.next();
-                if (edge_rows(t)) {
-                    if (!(ok = wait_all(b_full(c1.s), c1.ph))) break;
-                    zero_rows(c1.s, t);
+#pragma unroll 1
+            while (ok) {
+                if (left == 0 && split > 1) {  // one item a cluster
+                    i = all;
+                } else if (left == 0) {
+                    if (!claimed) claim();
+                    i = next;
+                    left = chunk;
+                    claimed = false;
                 }
-                if (more && !(ok = wait_all(b_full(c2.s), c2.ph))) break;
-                if (DPB == 2) {  // the product that read the buffer's dS(j - 1) was issued here
-                    tc_fence_after();
-                    if (more && leader) issue_dp(j + 1);
+                if (i >= all) {
+                    it.n = kItemEnd;
+                    ok = publish();
+                    break;
+                }
+                const uint32_t by = min(item_at(i, it), left);
+                i += by;
+                left -= by;
+                if (it.n < 0) continue;
+                if (!(ok = publish())) break;
+                if (it.n == 0) continue;
+                for (int r = 0; r < C::RES; ++r) {
+                    const CUtensorMap* m = r ? mR2 : mR1;
+                    if (r >= C::RT0) {
+                        for (int c = 0; c < NCK; ++c) ok = ok && load(ring, m, it.head, it.res_start + it.r0, c);
+                    } else if (ok && (done == 0 || mbar_wait(b_res_free(r), (done - 1) & 1, abort_flag))) {
+                        mbar_arrive_expect_tx(b_res(r), C::R_BYTES);
+                        for (int c = 0; c < NCH; ++c)
+                            tma_load_3d(sR + r * C::R_BYTES + c * (BM * 128), m, b_res(r), c * 64, it.head,
+                                        it.res_start + it.r0);
+                        res_loads[r] = done + 1;
+                    } else {
+                        ok = false;
+                    }
+                }
+                int t = it.t_first, h = str_head(it.head) + it.h_first;
+#pragma unroll 1
+                for (int j = 0; ok && j < it.n; ++j) {
+                    const int t2 = t, h2 = h;  // step j
+                    if (++t == it.t_hi) {
+                        t = it.t_lo;
+                        ++h;
+                    }
+                    if (C::HAS_DS || j == 0)
+                        for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC1, h2, it.str_start + t2 * BN, c);
+                    if (!C::HAS_DS) {  // S(j + 1) comes before dV(j)
+                        if (j + 1 < it.n)
+                            for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC1, h, it.str_start + t * BN, c);
+                        for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h2, it.str_start + t2 * BN, c);
+                    }
+                }
+                ++done;
+                if (split > 1) continue;
+                for (int c = 0; ok && c < C::STAGE1; ++c) ok = grant(ring);
+                if (left == 0 && !claimed && ok) claim();
+            }
+            if (!ok || *abort_flag) {
+                // Let every copy this thread started land before the CTA retires.
+                for (int r = 0; r < C::RES_SMEM; ++r)
+                    if (res_loads[r] > 0) mbar_wait_drain(b_res(r), (res_loads[r] - 1) & 1);
+                drain(ring);
+            }
+        } else if (warp == MW + 2 && lane == 0) {
+            // --------------------- producer: C2, and statistics of streamed rows
+            tma_prefetch_desc(mC2);
+            if (p.early_wait) grid_dependency_wait();  // the launch before this one writes the statistics
+            grid_launch_dependents();
+            Ring ring(sC, C::N1, C::N2);
+            int issued = 0;
+#pragma unroll 1
+            for (int i = 0; ok; ++i) {
+                const int n = next_item(i, false);
+                if (n < 0) {
+                    ok = n == kItemEnd;
+                    break;
+                }
+                const int t_lo = GBATTN_ITEM(i, t_lo), t_hi = GBATTN_ITEM(i, t_hi), start = GBATTN_ITEM(i, str_start);
+                const long long stat_base = static_cast<uint32_t>(GBATTN_ITEM(i, stat));
+                int t = GBATTN_ITEM(i, t_first), h = str_head(GBATTN_ITEM(i, head)) + GBATTN_ITEM(i, h_first);
+                mbar_arrive(b_item_free(i % C::ITEMS));
+#pragma unroll 1
+                for (int j = 0; ok && j < n; ++j) {
+                    if (C::HAS_DS)
+                        for (int c = 0; ok && c < NCK; ++c) ok = load(ring, mC2, h, start + t * BN, c);
+                    if (C::KEYS && ok) {
+                        const int b = issued % C::STATS;
+                        if (issued >= C::STATS &&
+                            !(ok = mbar_wait(b_stat_empty(b), (issued / C::STATS - 1) & 1, abort_flag)))
+                            break;
+                        const long long at = h * p.stat_stride + stat_base + static_cast<long long>(t) * BN;
+                        mbar_arrive_expect_tx(b_stat_full(b), C::STAT_BYTES);
+                        bulk_load(sStat + b * C::STAT_BYTES, p.neg_lse2 + at, BN * 4, b_stat_full(b));
+                        bulk_load(sStat + b * C::STAT_BYTES + BN * 4, p.neg_delta + at, BN * 4, b_stat_full(b));
+                        ++issued;
+                    }
+                    if (++t == t_hi) {
+                        t = t_lo;
+                        ++h;
+                    }
+                }
+                for (int c = 0; ok && n > 0 && split == 1 && c < C::STAGE2; ++c) ok = grant(ring);
+            }
+            if (!ok || *abort_flag) {
+                drain(ring);
+                for (int g = (issued > C::STATS ? issued - C::STATS : 0); g < issued; ++g)
+                    mbar_wait_drain(b_stat_full(g % C::STATS), (g / C::STATS) & 1);
+            }
+        } else if (warp == MW + 1 || (warp == MW + 3 && C::ISSUERS == 2)) {
+            // ----------------------------------------------------------------- MMA
+            // Each issuing warp walks its schedule as a whole; one elected lane issues.
+            constexpr uint32_t kIdS = idesc_bf16_f32(BM, BN, false, false);
+            constexpr uint32_t kIdA = idesc_bf16_f32(BM, C::CW, false, true);
+            const bool first_warp = warp == MW + 1;
+            const bool leader = elect_one();
+            const uint32_t dR = desc_lo(sR, 16);
+            const uint32_t dCk = desc_lo(sC, 16);           // streamed chunk, K-major
+            const uint32_t dCm = desc_lo(sC, BN * 128);     // streamed chunk, MN-major
+            auto wait_all = [&](uint32_t bar, uint32_t ph) {
+                return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag));
+            };
+            // Rows of a streamed tile that no resident row may see at all (past the
+            // document, the neighbours' rows, or rows without a key) may hold
+            // anything; P and dS are 0 there but 0 * NaN is not, so they are zeroed
+            // before the second product reads them.
+            int item = 0, n = 0, edge_lo = 0, edge_hi = 0;  // tiles below edge_lo or from edge_hi on have such rows
+            auto edge_rows = [&](int t) { return t < edge_lo || t >= edge_hi; };
+            auto zero_rows = [&](int s, int t) {
+                const int hi = min(BN, GBATTN_ITEM(item, str_len) - t * BN);
+                const int lo = (C::KEYS && p.causal) ? min(hi, max(0, -GBATTN_ITEM(item, diag) - t * BN)) : 0;
+                for (int x = lane; x < (lo + BN - hi) * CCH * 8; x += 32) {
+                    const int u = x & 7, rc = x >> 3, c = rc % CCH, r = rc / CCH;
+                    const int row = r < lo ? r : hi + r - lo;
+                    st_shared_v4(sC + s * C::C_BYTES + c * (BN * 128) + row * 128 + u * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
+            // X (128 x BN) (+)= resident r * chunk c of a streamed tile, in slot s
+            auto scores = [&](uint32_t to, int r, int c, int s) {
+                uint32_t a = r >= C::RT0 ? tmem + C::T_RES + (r - C::RT0) * (D / 2) + c * (C::CW / 2)
+                                         : dR + ((r * C::R_BYTES + c * CCH * BM * 128) >> 4);
+                uint32_t b = dCk + s * (C::C_BYTES >> 4);
+                asm volatile("" : "+r"(a), "+r"(b));  // (worked out here, not kept over the steps)
+#pragma unroll
+                for (int k = 0; k < C::CW / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * BN * 128 + (k & 3) * 32) >> 4, acc = (c > 0 || k > 0) ? 1u : 0u;
+                    if (r >= C::RT0)
+                        mma_ts(tmem + to, a + k * 8, b + off, kIdS, acc);
+                    else
+                        mma_ss(tmem + to, a + off, b + off, kIdS, acc);
+                }
+            };
+            // columns [c CW, (c + 1) CW) of acc += A (bf16 pairs in X's columns, 16
+            // of every 32) * chunk c of a streamed tile, in slot s
+            auto accumulate = [&](uint32_t acc, uint32_t x, int c, int s, bool first) {
+                uint32_t a = tmem + x, b = dCm + s * (C::C_BYTES >> 4);
+                asm volatile("" : "+r"(a), "+r"(b));
+#pragma unroll
+                for (int k = 0; k < BN / 16; ++k)
+                    mma_ts(tmem + acc + c * C::CW, a + (k >> 1) * 32 + (k & 1) * 8, b + ((k * 16 * 128) >> 4), kIdA,
+                           (!first || k > 0) ? 1u : 0u);
+            };
+            // Cursors: the next chunk of C1 and of C2 that this warp uses.
+            Ring c1(sC, 0, C::N1), c2(sC, C::N1, C::N2);
+            auto moved = [](Ring r) {
+                for (int c = 0; c < NCK; ++c) r.next();
+                return r;
+            };
+            int J = 0;     // steps of the items so far: buffers and phases go by J + j
+            int done = 0;  // items with steps so far
+            auto acc_free = [&]() -> bool { return done == 0 || wait_all(b_acc_free, (done - 1) & 1); };
+            ok = !*abort_flag;  // a launch told to give up issues nothing
+#pragma unroll 1
+            for (; ok; ++item) {
+                n = next_item(item, true);
+                if (n <= 0) {
+                    if (n < 0) {
+                        ok = n == kItemEnd;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
+                    continue;
+                }
+                const int t_lo = GBATTN_ITEM(item, t_lo), t_hi = GBATTN_ITEM(item, t_hi);
+                edge_lo = C::KEYS && p.causal ? (max(0, -GBATTN_ITEM(item, diag)) + BN - 1) / BN : 0;
+                edge_hi = GBATTN_ITEM(item, str_len) / BN;
+                if (C::RES_TMEM > 0) {  // the math warps have copied those residents into tensor memory
+                    ok = wait_all(b_res_in, done & 1);
+                    for (int g = 0; g < G0; ++g) {
+                        if (ok && lane == 0) mbar_arrive(b_empty(c1.s));
+                        c1.next();
+                    }
                     __syncwarp();
                 }
-                if (!(ok = (j > 0 || acc_free()) && wait_all(b_ds_full((J + j) % DPB), ((J + j) / DPB) & 1))) break;
-                if (C::HAS_P && SB == 1 && !(ok = wait_all(b_turn((J + j) & 1), ((J + j) >> 1) & 1))) break;
-                tc_fence_after();
-                if (leader) {
-                    accumulate(kAcc, C::T_DP + ((J + j) % DPB) * BN, 0, c1.s, j == 0, 2);
-                    mma_commit(b_empty(c1.s));
-                    if (more && DPB == 1) issue_dp(j + 1);
+                int t = GBATTN_ITEM(item, t_first);
+                // All of a tile's chunks have landed.
+                auto landed = [&](Ring s) -> bool {
+                    for (int c = 0; c < NCK; ++c) {
+                        if (!wait_all(b_full(s.s), s.ph)) return false;
+                        s.next();
+                    }
+                    return true;
+                };
+                // S of a step from C1's chunks, released once read when `free_c1`.
+                auto issue_s = [&](int j, Ring s, bool free_c1) {
+                    for (int c = 0; c < NCK; ++c) {
+                        scores(C::T_S + ((J + j) % SB) * BN, 0, c, s.s);
+                        if (free_c1) mma_commit(b_empty(s.s));
+                        s.next();
+                    }
+                    mma_commit(b_s_full((J + j) % SB));
+                    if (C::RES_SMEM > 0 && j + 1 == n) mma_commit(b_res_free(0));
+                };
+                if constexpr (C::SHARED) {
+                    // ---------------------------------- S and dP in the same columns
+                    // S(j), chunk by chunk: the last ones come into slots released just before
+                    auto next_s = [&](int j) -> bool {
+                        Ring s = c1;
+                        for (int c = 0; c < NCK; ++c) {
+                            if (!wait_all(b_full(s.s), s.ph)) return false;
+                            tc_fence_after();
+                            if (leader) {
+                                scores(C::T_S, 0, c, s.s);
+                                if (c == NCK - 1) mma_commit(b_s_full(0));
+                                if (c == NCK - 1 && j + 1 == n) mma_commit(b_res_free(0));
+                            }
+                            __syncwarp();
+                            s.next();
+                        }
+                        return true;
+                    };
+                    ok = ok && wait_all(b_res(0), done & 1) && next_s(0);
+                    for (int j = 0; ok && j < n; ++j) {
+                        if (!(ok = landed(c2) && wait_all(b_p_full(0), (J + j) & 1))) break;
+                        tc_fence_after();
+                        if (leader) {
+                            Ring s = c2;
+                            for (int c = 0; c < NCK; ++c) {
+                                scores(C::T_DP, 1, c, s.s);
+                                mma_commit(b_empty(s.s));
+                                s.next();
+                            }
+                            mma_commit(b_dp_full(0));
+                        }
+                        __syncwarp();
+                        c2 = moved(c2);
+                        if (edge_rows(t)) {
+                            Ring s = c1;
+                            for (int c = 0; c < NCK; ++c) {
+                                zero_rows(s.s, t);
+                                s.next();
+                            }
+                        }
+                        if (!(ok = (j > 0 || acc_free()) && wait_all(b_ds_full(0), (J + j) & 1))) break;
+                        tc_fence_after();
+                        if (leader) {
+                            Ring s = c1;
+                            for (int c = 0; c < NCK; ++c) {
+                                accumulate(C::T_ACC, C::T_DP, c, s.s, j == 0);
+                                mma_commit(b_empty(s.s));
+                                s.next();
+                            }
+                        }
+                        __syncwarp();
+                        c1 = moved(c1);
+                        if (j + 1 < n && !(ok = next_s(j + 1))) break;
+                        if (++t == t_hi) t = t_lo;
+                    }
+                } else if constexpr (!C::HAS_DS) {
+                    // ------------------------------------ dV alone: one ring, S(j + 1) before dV(j)
+                    if (first_warp) {
+                        ok = ok && wait_all(b_res(0), done & 1);
+                        for (int j = 0; ok && j < n; ++j) {
+                            if (!(ok = landed(c1))) break;
+                            // the buffer's P has been used up
+                            const int g = J + j - SB;
+                            if (g >= 0 && !(ok = wait_all(b_turn(g % SB), (g / SB) & 1))) break;
+                            tc_fence_after();
+                            if (leader) issue_s(j, c1, true);
+                            __syncwarp();
+                            c1 = moved(c1);
+                            if (j > 0 || n == 1) c1 = moved(c1);  // past dout's tile
+                        }
+                        if (n > 1) c1 = moved(c1);
+                    } else {
+                        c1 = moved(c1);
+                        if (n > 1) c1 = moved(c1);
+                        for (int j = 0; ok && j < n; ++j) {
+                            // P(j) first: the slots' last turns were S(j)'s tiles or
+                            // earlier ones, and a wait by parity is exact only once
+                            // those have landed.
+                            if (!(ok = (j > 0 || acc_free()) &&
+                                       wait_all(b_p_full((J + j) % SB), ((J + j) / SB) & 1) && landed(c1)))
+                                break;
+                            if (edge_rows(t)) {
+                                Ring s = c1;
+                                for (int c = 0; c < NCK; ++c) {
+                                    zero_rows(s.s, t);
+                                    s.next();
+                                }
+                            }
+                            tc_fence_after();
+                            if (leader) {
+                                Ring s = c1;
+                                for (int c = 0; c < NCK; ++c) {
+                                    accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, c, s.s, j == 0);
+                                    mma_commit(b_empty(s.s));
+                                    s.next();
+                                }
+                                mma_commit(b_turn((J + j) % SB));
+                            }
+                            __syncwarp();
+                            c1 = moved(c1);
+                            if (j + 2 < n) c1 = moved(c1);  // past the queries' tile of step j + 2
+                            if (++t == t_hi) t = t_lo;
+                        }
+                    }
+                } else if (first_warp) {
+                    // -------------------------------------------------- S (and dV)
+                    if (C::RT0 > 0) ok = ok && wait_all(b_res(0), done & 1);
+                    ok = ok && wait_all(b_full(c1.s), c1.ph);
+                    if (ok) {
+                        tc_fence_after();
+                        if (leader) issue_s(0, c1, true);
+                        __syncwarp();
+                    }
+                    for (int j = 0; ok && j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        c1.next();
+                        if (more && !(ok = wait_all(b_full(c1.s), c1.ph))) break;
+                        if (SB == 2) {  // dV(j - 1), which read the buffer, was issued here
+                            tc_fence_after();
+                            if (more && leader) issue_s(j + 1, c1, true);
+                            __syncwarp();
+                        }
+                        if (C::HAS_P) {
+                            if (!(ok = wait_all(b_full(c2.s), c2.ph) && (j > 0 || acc_free()))) break;
+                            if (edge_rows(t)) zero_rows(c2.s, t);
+                        }
+                        if (!(ok = wait_all(b_p_full((J + j) % SB), ((J + j) / SB) & 1))) break;
+                        tc_fence_after();
+                        if (leader) {
+                            if (C::HAS_P) {
+                                accumulate(C::T_ACC, C::T_S + ((J + j) % SB) * BN, 0, c2.s, j == 0);
+                                mma_commit(b_empty(c2.s));
+                            }
+                            if (more && SB == 1) issue_s(j + 1, c1, true);
+                            if (C::HAS_P && SB == 1) mbar_arrive(b_turn((J + j) & 1));
+                        }
+                        __syncwarp();
+                        c2.next();
+                        if (++t == t_hi) t = t_lo;
+                    }
+                } else {
+                    // --------------------------------------------- dP and dK or dQ
+                    constexpr uint32_t kAcc = C::T_ACC + (C::HAS_P ? D : 0);
+                    auto issue_dp = [&](int j) {
+                        scores(C::T_DP + ((J + j) % DPB) * BN, 1, 0, c2.s);
+                        mma_commit(b_empty(c2.s));
+                        if (!C::HAS_P) mma_commit(b_empty(c2.s));  // (a slot is released twice)
+                        mma_commit(b_dp_full((J + j) % DPB));
+                        if (C::RES_SMEM > 1 && j + 1 == n) mma_commit(b_res_free(1));
+                    };
+                    if (C::RT0 > 1) ok = ok && wait_all(b_res(1), done & 1);
+                    ok = ok && wait_all(b_full(c2.s), c2.ph);
+                    if (ok) {
+                        tc_fence_after();
+                        if (leader) issue_dp(0);
+                        __syncwarp();
+                    }
+                    for (int j = 0; ok && j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        c2.next();
+                        if (edge_rows(t)) {
+                            if (!(ok = wait_all(b_full(c1.s), c1.ph))) break;
+                            zero_rows(c1.s, t);
+                        }
+                        if (more && !(ok = wait_all(b_full(c2.s), c2.ph))) break;
+                        if (DPB == 2) {  // the product that read the buffer's dS(j - 1) was issued here
+                            tc_fence_after();
+                            if (more && leader) issue_dp(j + 1);
+                            __syncwarp();
+                        }
+                        if (!(ok = (j > 0 || acc_free()) && wait_all(b_ds_full((J + j) % DPB), ((J + j) / DPB) & 1))) break;
+                        if (C::HAS_P && SB == 1 && !(ok = wait_all(b_turn((J + j) & 1), ((J + j) >> 1) & 1))) break;
+                        tc_fence_after();
+                        if (leader) {
+                            accumulate(kAcc, C::T_DP + ((J + j) % DPB) * BN, 0, c1.s, j == 0);
+                            mma_commit(b_empty(c1.s));
+                            if (more && DPB == 1) issue_dp(j + 1);
+                        }
+                        __syncwarp();
+                        c1.next();
+                        if (++t == t_hi) t = t_lo;
+                    }
                 }
+                // (dV alone: the warp that issues S runs an item ahead, and its commits would count for this one)
+                if (ok && leader && (C::HAS_DS || !first_warp)) mma_commit(b_done);
                 __syncwarp();
-                c1.next();
-                if (++t == t_hi) t = t_lo;
+                if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
+                for (int c = 0; c < C::STAGE1; ++c) c1.next();
+                for (int c = 0; c < C::STAGE2; ++c) c2.next();
+                J += n;
+                ++done;
             }
+            // Everything issued above must finish before TMEM is released.
+            if (leader) mma_commit(b_drain);
+            __syncwarp();
+            mbar_wait_drain(b_drain, 0);
         }
-        // (dV alone: the warp that issues S runs an item ahead, and its commits would count for this one)
-        if (ok && leader && (C::HAS_DS || !first_warp)) mma_commit(b_done);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
-        for (int c = 0; c < C::STAGE1; ++c) c1.next();
-        for (int c = 0; c < C::STAGE2; ++c) c2.next();
-        J += n;
-        ++done;
+        if (split > 1) {  // with the math warps
+            cluster_sync();
+            cluster_sync();
         }
-        // Everything issued above must finish before TMEM is released.
-        if (leader) mma_commit(b_drain);
-        __syncwarp();
-        mbar_wait_drain(b_drain, 0);
-    }
-    if (split > 1) {  // with the math warps
-        cluster_sync();
-        cluster_sync();
-    }
     } else {
         regs_inc<C::REG_MATH>();
         // ---------------------------------------------------------------- math
@@ -1003,268 +1015,272 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         };
 #pragma unroll 1
         for (int item = 0; ok; ++item) {
-        const int n = next_item(item, true);
-        if (n < 0) {
-            ok = n == kItemEnd;
-            break;
-        }
-        const int row = GBATTN_ITEM(item, r0) + r;  // within the document
-        float row_nl = -INFINITY, row_nd = 0.f;
-        if (!C::KEYS && row < GBATTN_ITEM(item, res_len)) {
-            const long long at = GBATTN_ITEM(item, head) * p.stat_stride + static_cast<uint32_t>(GBATTN_ITEM(item, stat)) + row;
-            row_nl = p.neg_lse2[at];
-            row_nd = p.neg_delta[at];
-        }
-        if (n > 0) {
-            give_back();
-            ok = __all_sync(0xffffffffu, ok);
-        }
-        if (C::RES_TMEM > 0 && n > 0) {
-            // residents that go to tensor memory: the warpgroups copy 64-column blocks in turn
-            for (int b = wg; ok && b < C::RES_TMEM * NCH; b += WGS) {
-                Ring at = ring1;  // blocks lie in the order they were loaded
-                for (int c = 0; c < b / CCH; ++c) at.next();
-                const int s = at.s;
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_full(s), at.ph, abort_flag)))) break;
-                const uint32_t src = sC + s * C::C_BYTES + (b % CCH) * (BM * 128) + r * 128;
+            const int n = next_item(item, true);
+            if (n < 0) {
+                ok = n == kItemEnd;
+                break;
+            }
+            const int row = GBATTN_ITEM(item, r0) + r;  // within the document
+            float row_nl = -INFINITY, row_nd = 0.f;
+            if (!C::KEYS && row < GBATTN_ITEM(item, res_len)) {
+                const long long at =
+                    GBATTN_ITEM(item, head) * p.stat_stride + static_cast<uint32_t>(GBATTN_ITEM(item, stat)) + row;
+                row_nl = p.neg_lse2[at];
+                row_nd = p.neg_delta[at];
+            }
+            if (n > 0) {
+                give_back();
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (C::RES_TMEM > 0 && n > 0) {
+                // residents that go to tensor memory: the warpgroups copy 64-column blocks in turn
+                for (int b = wg; ok && b < C::RES_TMEM * NCH; b += WGS) {
+                    Ring at = ring1;  // blocks lie in the order they were loaded
+                    for (int c = 0; c < b / CCH; ++c) at.next();
+                    const int s = at.s;
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_full(s), at.ph, abort_flag)))) break;
+                    const uint32_t src = sC + s * C::C_BYTES + (b % CCH) * (BM * 128) + r * 128;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[16];
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[16];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float4 x = ld_shared_f4(src + (((h * 4 + u) ^ (r & 7)) << 4));
-                        w[4 * u] = __float_as_uint(x.x), w[4 * u + 1] = __float_as_uint(x.y);
-                        w[4 * u + 2] = __float_as_uint(x.z), w[4 * u + 3] = __float_as_uint(x.w);
+                        for (int u = 0; u < 4; ++u) {
+                            const float4 x = ld_shared_f4(src + (((h * 4 + u) ^ (r & 7)) << 4));
+                            w[4 * u] = __float_as_uint(x.x), w[4 * u + 1] = __float_as_uint(x.y);
+                            w[4 * u + 2] = __float_as_uint(x.z), w[4 * u + 3] = __float_as_uint(x.w);
+                        }
+                        tmem_st16(tl + C::T_RES + b * 32 + h * 16, w);
                     }
-                    tmem_st16(tl + C::T_RES + b * 32 + h * 16, w);
+                }
+                if (ok) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_res_in);
                 }
             }
-            if (ok) {
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_res_in);
-            }
-        }
-        // streamed rows [see_lo, see_hi) are visible; below tile edge_lo and from
-        // edge_hi on some row of the item sees only part of a tile
-        const int diag = GBATTN_ITEM(item, diag), str_len = GBATTN_ITEM(item, str_len), r0 = GBATTN_ITEM(item, r0);
-        const int see_lo = C::KEYS && p.causal ? row - diag : 0;
-        const int see_hi = !C::KEYS && p.causal ? min(str_len, row + diag + 1) : str_len;
-        const int edge_lo = C::KEYS && p.causal ? (max(0, r0 + BM - 1 - diag) + BN - 1) / BN : 0;
-        const int edge_hi = max(0, !C::KEYS && p.causal ? min(str_len, r0 + diag + 1) : str_len) / BN;
-        const int t_lo = GBATTN_ITEM(item, t_lo), t_hi = GBATTN_ITEM(item, t_hi);
-        int t = GBATTN_ITEM(item, t_first);
+            // streamed rows [see_lo, see_hi) are visible; below tile edge_lo and from
+            // edge_hi on some row of the item sees only part of a tile
+            const int diag = GBATTN_ITEM(item, diag), str_len = GBATTN_ITEM(item, str_len), r0 = GBATTN_ITEM(item, r0);
+            const int see_lo = C::KEYS && p.causal ? row - diag : 0;
+            const int see_hi = !C::KEYS && p.causal ? min(str_len, row + diag + 1) : str_len;
+            const int edge_lo = C::KEYS && p.causal ? (max(0, r0 + BM - 1 - diag) + BN - 1) / BN : 0;
+            const int edge_hi = max(0, !C::KEYS && p.causal ? min(str_len, r0 + diag + 1) : str_len) / BN;
+            const int t_lo = GBATTN_ITEM(item, t_lo), t_hi = GBATTN_ITEM(item, t_hi);
+            int t = GBATTN_ITEM(item, t_first);
 #pragma unroll 1
-        for (int j = 0; ok && j < n; ++j) {
-            const int g = J + j, sb = g % SB, db = g % DPB;
-            const int c0 = t * BN + wg * H;  // this thread's first streamed row
-            const int lo = see_lo - c0, hi = see_hi - c0;
-            const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < H);
-            const uint32_t st = sStat + (g % C::STATS) * C::STAT_BYTES + wg * (H * 4);
-            const uint32_t tS = tl + C::T_S + sb * BN + wg * H, tDP = tl + C::T_DP + db * BN + wg * H;
-            if (C::KEYS) ok = ok && mbar_wait(b_stat_full(g % C::STATS), (g / C::STATS) & 1, abort_flag);
-            if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(b_s_full(sb), (g / SB) & 1, abort_flag)))) break;
-            tc_fence_after();
-            uint32_t pr[H];  // P, fp32
-#pragma unroll
-            for (int c = 0; c < H; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&pr[c]));
-            tmem_wait_ld();
-            if (!C::HAS_P) {  // the S buffer may be written again
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_p_full(sb, 0));
-            }
-            const float2 cc = make_float2(c2, c2);
-#pragma unroll
-            for (int c = 0; c < H; c += 32) {
-#pragma unroll
-                for (int e = c; e < c + 32; e += 4) {
-                    float4 nl = make_float4(row_nl, row_nl, row_nl, row_nl);
-                    if (C::KEYS) nl = ld_shared_f4(st + e * 4);
-                    const float2 a = __ffma2_rn(make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])), cc,
-                                                make_float2(nl.x, nl.y));
-                    const float2 b = __ffma2_rn(make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])), cc,
-                                                make_float2(nl.z, nl.w));
-                    pr[e] = __float_as_uint(ex2(a.x));
-                    pr[e + 1] = __float_as_uint(ex2(a.y));
-                    pr[e + 2] = __float_as_uint(ex2(b.x));
-                    pr[e + 3] = __float_as_uint(ex2(b.y));
-                }
-                if (edge) {
-#pragma unroll
-                    for (int e = c; e < c + 32; ++e)
-                        if (e < lo || e >= hi) pr[e] = 0u;
-                }
-                if (C::HAS_P) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pk[e] = pack_bf16x2(__uint_as_float(pr[c + 2 * e]), __uint_as_float(pr[c + 2 * e + 1]));
-                    tmem_st16(tS + c, pk);
-                }
-            }
-            if (C::HAS_P) {
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_p_full(sb, 0));
-            }
-            if (C::HAS_DS) {
-                if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(b_dp_full(db), (g / DPB) & 1, abort_flag)))) break;
+            for (int j = 0; ok && j < n; ++j) {
+                const int g = J + j, sb = g % SB, db = g % DPB;
+                const int c0 = t * BN + wg * H;  // this thread's first streamed row
+                const int lo = see_lo - c0, hi = see_hi - c0;
+                const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < H);
+                const uint32_t st = sStat + (g % C::STATS) * C::STAT_BYTES + wg * (H * 4);
+                const uint32_t tS = tl + C::T_S + sb * BN + wg * H, tDP = tl + C::T_DP + db * BN + wg * H;
+                if (C::KEYS) ok = ok && mbar_wait(b_stat_full(g % C::STATS), (g / C::STATS) & 1, abort_flag);
+                if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(b_s_full(sb), (g / SB) & 1, abort_flag)))) break;
                 tc_fence_after();
-                uint32_t dp[H];
+                uint32_t pr[H];  // P, fp32
 #pragma unroll
-                for (int c = 0; c < H; c += 32) tmem_ld32(tDP + c, *reinterpret_cast<uint32_t(*)[32]>(&dp[c]));
+                for (int c = 0; c < H; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&pr[c]));
                 tmem_wait_ld();
+                if (!C::HAS_P) {  // the S buffer may be written again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_p_full(sb));
+                }
+                const float2 cc = make_float2(c2, c2);
 #pragma unroll
                 for (int c = 0; c < H; c += 32) {
 #pragma unroll
                     for (int e = c; e < c + 32; e += 4) {
-                        float4 nd = make_float4(row_nd, row_nd, row_nd, row_nd);
-                        if (C::KEYS) nd = ld_shared_f4(st + BN * 4 + e * 4);
-                        float2 a = __fadd2_rn(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
-                                              make_float2(nd.x, nd.y));
-                        float2 b = __fadd2_rn(make_float2(__uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3])),
-                                              make_float2(nd.z, nd.w));
-                        a = __fmul2_rn(a, make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])));
-                        b = __fmul2_rn(b, make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])));
-                        dp[e] = __float_as_uint(a.x);
-                        dp[e + 1] = __float_as_uint(a.y);
-                        dp[e + 2] = __float_as_uint(b.x);
-                        dp[e + 3] = __float_as_uint(b.y);
+                        float4 nl = make_float4(row_nl, row_nl, row_nl, row_nl);
+                        if (C::KEYS) nl = ld_shared_f4(st + e * 4);
+                        const float2 a = __ffma2_rn(make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])), cc,
+                                                    make_float2(nl.x, nl.y));
+                        const float2 b = __ffma2_rn(make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])), cc,
+                                                    make_float2(nl.z, nl.w));
+                        pr[e] = __float_as_uint(ex2(a.x));
+                        pr[e + 1] = __float_as_uint(ex2(a.y));
+                        pr[e + 2] = __float_as_uint(ex2(b.x));
+                        pr[e + 3] = __float_as_uint(ex2(b.y));
                     }
-                    if (edge) {  // 0 * (anything) is not always 0
+                    if (edge) {
 #pragma unroll
                         for (int e = c; e < c + 32; ++e)
-                            if (e < lo || e >= hi) dp[e] = 0u;
+                            if (e < lo || e >= hi) pr[e] = 0u;
                     }
-                    uint32_t pk[16];
+                    if (C::HAS_P) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pk[e] = pack_bf16x2(__uint_as_float(dp[c + 2 * e]), __uint_as_float(dp[c + 2 * e + 1]));
-                    tmem_st16(tDP + c, pk);
+                        for (int e = 0; e < 16; ++e)
+                            pk[e] = pack_bf16x2(__uint_as_float(pr[c + 2 * e]), __uint_as_float(pr[c + 2 * e + 1]));
+                        tmem_st16(tS + c, pk);
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_ds_full(db));
-            }
-            if (C::KEYS) {  // the statistics' buffer may be filled again
-                if (!C::HAS_DS) __syncwarp();
-                if (lane == 0) mbar_arrive(b_stat_empty(g % C::STATS));
-            }
-            if (++t == t_hi) t = t_lo;
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok && n > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(b_done, done & 1, abort_flag));
-            tc_fence_after();
-        }
-        // ------------------------------------------------------------ epilogue
-        // An accumulator's 32 column chunks are taken in turn by its warpgroups.  Rows are staged in the ring's slots,
-        // in the boxes' swizzle, and leave by TMA where the tile lies wholly
-        // inside its document, else row by row.
-        if (split > 1) {  // the sums, or zeros, as fp32 rows over the ring, 16-byte pieces swizzled by row
-            constexpr int P = C::ACCS * D / 4;  // pieces of a row
-            const uint32_t to = sC + static_cast<uint32_t>(r) * (P * 16);
-#pragma unroll 1
-            for (int x = wg; x < C::ACCS * D / 32; x += WGS) {
-                uint32_t o[32];
-                if (ok && n > 0) {
-                    tmem_ld32(tl + C::T_ACC + x * 32, o);
+                if (C::HAS_P) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_p_full(sb));
+                }
+                if (C::HAS_DS) {
+                    if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(b_dp_full(db), (g / DPB) & 1, abort_flag)))) break;
+                    tc_fence_after();
+                    uint32_t dp[H];
+#pragma unroll
+                    for (int c = 0; c < H; c += 32) tmem_ld32(tDP + c, *reinterpret_cast<uint32_t(*)[32]>(&dp[c]));
                     tmem_wait_ld();
-                } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    for (int c = 0; c < H; c += 32) {
+#pragma unroll
+                        for (int e = c; e < c + 32; e += 4) {
+                            float4 nd = make_float4(row_nd, row_nd, row_nd, row_nd);
+                            if (C::KEYS) nd = ld_shared_f4(st + BN * 4 + e * 4);
+                            float2 a = __fadd2_rn(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
+                                                  make_float2(nd.x, nd.y));
+                            float2 b = __fadd2_rn(make_float2(__uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3])),
+                                                  make_float2(nd.z, nd.w));
+                            a = __fmul2_rn(a, make_float2(__uint_as_float(pr[e]), __uint_as_float(pr[e + 1])));
+                            b = __fmul2_rn(b, make_float2(__uint_as_float(pr[e + 2]), __uint_as_float(pr[e + 3])));
+                            dp[e] = __float_as_uint(a.x);
+                            dp[e + 1] = __float_as_uint(a.y);
+                            dp[e + 2] = __float_as_uint(b.x);
+                            dp[e + 3] = __float_as_uint(b.y);
+                        }
+                        if (edge) {  // 0 * (anything) is not always 0
+#pragma unroll
+                            for (int e = c; e < c + 32; ++e)
+                                if (e < lo || e >= hi) dp[e] = 0u;
+                        }
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            pk[e] = pack_bf16x2(__uint_as_float(dp[c + 2 * e]), __uint_as_float(dp[c + 2 * e + 1]));
+                        tmem_st16(tDP + c, pk);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_ds_full(db));
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    st_shared_v4(to + (((x * 8 + e) ^ (r & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                if (C::KEYS) {  // the statistics' buffer may be filled again
+                    if (!C::HAS_DS) __syncwarp();
+                    if (lane == 0) mbar_arrive(b_stat_empty(g % C::STATS));
+                }
+                if (++t == t_hi) t = t_lo;
             }
-            have = true;
-        } else if (ok) {
-            const int res_all = GBATTN_ITEM(item, res_all), res_len = GBATTN_ITEM(item, res_len);
-            const int head = GBATTN_ITEM(item, head), res_start = GBATTN_ITEM(item, res_start);
-            const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && acc == 0);
-            const float f = is_dv ? 1.f : p.scale;
-            uint16_t* const out = static_cast<uint16_t*>(C::KEYS ? (is_dv ? p.dv : p.dk) : p.dq);
-            auto row_ptr = [&](int i) { return out + ((static_cast<long long>(res_start) + r0 + i) * heads + head) * D; };
-            const int tid = (warp & 3) * 32 + lane + part * 128;  // among the threads that share the accumulator
-            constexpr int THR = 128 * PARTS, U = D / 8;            // 16-byte pieces of a row
-            const int rows = min(BM, res_all - r0);
-            if (n == 0) {
-                for (int x = tid; x < rows * U; x += THR) st_global_v4(row_ptr(x / U) + (x % U) * 8, 0u, 0u, 0u, 0u);
-            } else {
-                ahead(ring1, G0 + n * NCK * (C::HAS_DS ? 1 : 2));
-                if (C::ACCS == 2) ahead(ring2, n * NCK);
-                const Ring stage = acc ? ring2 : ring1;
-                Ring at = stage;
-                const bool used = row < res_len;
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && n > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(b_done, done & 1, abort_flag));
+                tc_fence_after();
+            }
+            // ------------------------------------------------------------ epilogue
+            // An accumulator's 32 column chunks are taken in turn by its warpgroups.
+            // Rows are staged in the ring's slots, in the boxes' swizzle, and leave
+            // by TMA where the tile lies wholly inside its document, else row by row.
+            if (split > 1) {  // the sums, or zeros, as fp32 rows over the ring, 16-byte pieces swizzled by row
+                constexpr int P = C::ACCS * D / 4;  // pieces of a row
+                const uint32_t to = sC + static_cast<uint32_t>(r) * (P * 16);
 #pragma unroll 1
-                for (int c = 0; c < NCK; ++c) {
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_full(at.s), at.ph, abort_flag)))) break;
-                    const uint32_t to = sC + at.s * C::C_BYTES + r * 128;
-#pragma unroll 1
-                    for (int x = part; x < C::CW / 32; x += PARTS) {
-                        uint32_t o[32];
-                        tmem_ld32(tl + C::T_ACC + acc * D + c * C::CW + x * 32, o);
+                for (int x = wg; x < C::ACCS * D / 32; x += WGS) {
+                    uint32_t o[32];
+                    if (ok && n > 0) {
+                        tmem_ld32(tl + C::T_ACC + x * 32, o);
                         tmem_wait_ld();
+                    } else {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            uint32_t w[4];
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    }
 #pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                w[y] = used ? pack_bf16x2(__uint_as_float(o[8 * u + 2 * y]) * f, __uint_as_float(o[8 * u + 2 * y + 1]) * f)
-                                            : 0u;
-                            st_shared_v4(to + (x >> 1) * (BM * 128) + ((((x & 1) * 4 + u) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-                        }
-                    }
-                    at.next();
+                    for (int e = 0; e < 8; ++e)
+                        st_shared_v4(to + (((x * 8 + e) ^ (r & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_acc_free);  // the next item may sum
-                fence_proxy_async_smem();                // generic-proxy writes -> the TMA engine
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_staged(acc));
-                if (ok && (storer || rows < BM)) ok = mbar_wait(b_staged(acc), done & 1, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-                if (ok && rows == BM) {
-                    if (storer) {
-                        at = stage;
-                        for (int c = 0; c < NCK; ++c) {
-                            for (int b = 0; b < CCH; ++b)
-                                tma_store_3d(acc ? &tmO2 : &tmO1, sC + at.s * C::C_BYTES + b * (BM * 128), (c * CCH + b) * 64, head,
-                                             res_start + r0);
-                            at.next();
+                have = true;
+            } else if (ok) {
+                const int res_all = GBATTN_ITEM(item, res_all), res_len = GBATTN_ITEM(item, res_len);
+                const int head = GBATTN_ITEM(item, head), res_start = GBATTN_ITEM(item, res_start);
+                const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && acc == 0);
+                const float f = is_dv ? 1.f : p.scale;
+                uint16_t* const out = static_cast<uint16_t*>(C::KEYS ? (is_dv ? p.dv : p.dk) : p.dq);
+                auto row_ptr = [&](int i) { return out + ((static_cast<long long>(res_start) + r0 + i) * heads + head) * D; };
+                const int tid = (warp & 3) * 32 + lane + part * 128;  // among the threads that share the accumulator
+                constexpr int THR = 128 * PARTS, U = D / 8;            // 16-byte pieces of a row
+                const int rows = min(BM, res_all - r0);
+                if (n == 0) {
+                    for (int x = tid; x < rows * U; x += THR) st_global_v4(row_ptr(x / U) + (x % U) * 8, 0u, 0u, 0u, 0u);
+                } else {
+                    ahead(ring1, G0 + n * NCK * (C::HAS_DS ? 1 : 2));
+                    if (C::ACCS == 2) ahead(ring2, n * NCK);
+                    const Ring stage = acc ? ring2 : ring1;
+                    Ring at = stage;
+                    const bool used = row < res_len;
+#pragma unroll 1
+                    for (int c = 0; c < NCK; ++c) {
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait(b_full(at.s), at.ph, abort_flag)))) break;
+                        const uint32_t to = sC + at.s * C::C_BYTES + r * 128;
+#pragma unroll 1
+                        for (int x = part; x < C::CW / 32; x += PARTS) {
+                            uint32_t o[32];
+                            tmem_ld32(tl + C::T_ACC + acc * D + c * C::CW + x * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    const int e = 8 * u + 2 * y;
+                                    w[y] = used ? pack_bf16x2(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f) : 0u;
+                                }
+                                st_shared_v4(to + (x >> 1) * (BM * 128) + ((((x & 1) * 4 + u) ^ (r & 7)) << 4), w[0], w[1],
+                                             w[2], w[3]);
+                            }
                         }
-                        bulk_commit();
-                        leaving = stage.s;
+                        at.next();
                     }
-                } else if (ok) {
-                    for (int x = tid; x < rows * U; x += THR) {
-                        const int i = x / U, u = x % U, b = u / 8;
-                        at = stage;
-                        for (int c = 0; c < b / CCH; ++c) at.next();
-                        const float4 v = ld_shared_f4(sC + at.s * C::C_BYTES + (b % CCH) * (BM * 128) + i * 128 + (((u & 7) ^ (i & 7)) << 4));
-                        st_global_v4(row_ptr(i) + u * 8, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
-                                     __float_as_uint(v.w));
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_acc_free);  // the next item may sum
+                    fence_proxy_async_smem();                // generic-proxy writes -> the TMA engine
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_staged(acc));
+                    if (ok && (storer || rows < BM)) ok = mbar_wait(b_staged(acc), done & 1, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok && rows == BM) {
+                        if (storer) {
+                            at = stage;
+                            for (int c = 0; c < NCK; ++c) {
+                                for (int b = 0; b < CCH; ++b)
+                                    tma_store_3d(acc ? &tmO2 : &tmO1, sC + at.s * C::C_BYTES + b * (BM * 128),
+                                                 (c * CCH + b) * 64, head, res_start + r0);
+                                at.next();
+                            }
+                            bulk_commit();
+                            leaving = stage.s;
+                        }
+                    } else if (ok) {
+                        for (int x = tid; x < rows * U; x += THR) {
+                            const int i = x / U, u = x % U, b = u / 8;
+                            at = stage;
+                            for (int c = 0; c < b / CCH; ++c) at.next();
+                            const float4 v = ld_shared_f4(sC + at.s * C::C_BYTES + (b % CCH) * (BM * 128) + i * 128 +
+                                                          (((u & 7) ^ (i & 7)) << 4));
+                            st_global_v4(row_ptr(i) + u * 8, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                                         __float_as_uint(v.w));
+                        }
+                        if (storer) leaving = stage.s;
                     }
-                    if (storer) leaving = stage.s;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_copied(acc));
+                    ahead(ring1, C::STAGE1);
+                    if (C::ACCS == 2) ahead(ring2, C::STAGE2);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_copied(acc));
-                ahead(ring1, C::STAGE1);
-                if (C::ACCS == 2) ahead(ring2, C::STAGE2);
             }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
-        if (n > 0) {
-            J += n;
-            ++done;
-        }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_item_free(item % C::ITEMS));
+            if (n > 0) {
+                J += n;
+                ++done;
+            }
         }
         give_back();
         if (split > 1) {
@@ -1272,7 +1288,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (ok && have) {
                 // CTA c adds up rows [c R, (c + 1) R) over the cluster, in rank order
                 constexpr int P = C::ACCS * D / 4;
-                const int R = BM / split, r0 = GBATTN_ITEM(0, r0), res_all = GBATTN_ITEM(0, res_all), res_len = GBATTN_ITEM(0, res_len);
+                const int R = BM / split, r0 = GBATTN_ITEM(0, r0);
+                const int res_all = GBATTN_ITEM(0, res_all), res_len = GBATTN_ITEM(0, res_len);
+                const long long row0 = static_cast<long long>(GBATTN_ITEM(0, res_start)) + r0;
                 for (int x = threadIdx.x; x < R * P; x += MW * 32) {
                     const int i = crank * R + x / P, piece = x % P;
                     if (r0 + i >= res_all) continue;
@@ -1285,8 +1303,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const bool is_dv = C::MODE == kBwdV || (C::MODE == kBwdKV && piece < D / 4);
                     const float f = r0 + i >= res_len ? 0.f : (is_dv ? 1.f : p.scale);
                     uint16_t* out = static_cast<uint16_t*>(C::KEYS ? (is_dv ? p.dv : p.dk) : p.dq) +
-                                    ((static_cast<long long>(GBATTN_ITEM(0, res_start)) + r0 + i) * heads + GBATTN_ITEM(0, head)) * D +
-                                    piece % (D / 4) * 4;
+                                    ((row0 + i) * heads + GBATTN_ITEM(0, head)) * D + piece % (D / 4) * 4;
                     *reinterpret_cast<uint2*>(out) =
                         f == 0.f ? make_uint2(0u, 0u)
                                  : make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
@@ -1397,7 +1414,7 @@ cudaError_t launch_bwd(int D, const BwdMaps& m, BwdParams p, int num_sms, cudaSt
     // long bound: most are empty, and a claim costs more than a look at them).
     for (int x = 0; x < 2; ++x) {
         const long long c = p.items[x] / (64ll * num_sms);
-        p.chunk[x] = static_cast<uint32_t>(c < 1 ? 1 : (c > 256 ? 256 : c));
+        p.chunk[x] = static_cast<uint32_t>(c < 1 ? 1 : (c > 1024 ? 1024 : c));
         // Half the SMs or fewer busy, with items of eight steps or more: as many
         // CTAs an item as fill the SMs, four steps each at least.
         const long long steps = x == 0 ? static_cast<long long>(p.tiles_q) * p.group : p.tiles_k;
