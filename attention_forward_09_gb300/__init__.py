@@ -977,7 +977,7 @@ def attn_bwd_dense(q, k, v, out, lse, dout, softmax_scale=None, causal=False, dl
     [B, Sq, Hq, D] and k, v [B, Sk, Hkv, D] bf16, out (bf16 or fp32) and lse
     [B, Hq, Sq] as it returned them, dout the gradient of out and dlse that of
     lse (None: lse is not used further on).  Returns (dq, dk, dv) in bf16;
-    tensors given for them are written.  A workspace of at least
+    tensors given for them are written and must not overlap the inputs.  A workspace of at least
     ``attn_bwd_workspace_size(B, B * Sq, Hq)`` bytes may be passed (it is
     allocated here otherwise); calls that can overlap need one each."""
     B, Sq, Sk, Hq, Hkv, D = _bwd_batch(q, k)
@@ -1093,7 +1093,7 @@ def attn_rotary(q, k, positions, plan: RotaryPlan, transpose=False, q_out=None, 
     strided, as parts of a fused projection's output; k may be None) by their
     positions [T] (int32).  transpose=True turns gradients back.  Returns
     (q_out, k_out): new tensors, or those given, which may be q and k
-    themselves (in place)."""
+    themselves (in place) and must not overlap the inputs in another way."""
     dev = q.get_device()
     if dev < 0:
         raise ValueError("attn_rotary takes CUDA tensors")

@@ -156,6 +156,30 @@ size_t bwd_stat_bytes(long long Tq, int num_docs, int Hq) {
     return ((static_cast<size_t>(gbattn::bwd_stat_stride(Tq, num_docs)) * Hq * 4) + 255) & ~size_t(255);
 }
 
+// Memory that a call reads or writes: `count` rows of `bytes` bytes, `stride` bytes apart.
+struct Span {
+    uintptr_t first;
+    size_t count, bytes, stride;
+};
+Span whole(const void* first, long long bytes) { return {reinterpret_cast<uintptr_t>(first), 1, static_cast<size_t>(bytes), 0}; }
+Span bf16_rows(const void* first, long long count, long long values, long long stride) {
+    return {reinterpret_cast<uintptr_t>(first), static_cast<size_t>(count), 2 * static_cast<size_t>(values),
+            2 * static_cast<size_t>(stride)};
+}
+
+// Whether two of them meet.  Rows at the same stride may lie between one
+// another (parts of a fused projection); spans that interleave at different
+// strides count as meeting.
+bool meet(const Span& a, const Span& b) {
+    if (!a.first || !b.first || !a.bytes || !b.bytes) return false;
+    const Span &lo = a.first <= b.first ? a : b, &hi = a.first <= b.first ? b : a;
+    const size_t apart = hi.first - lo.first;
+    if (apart >= (lo.count - 1) * lo.stride + lo.bytes) return false;
+    if (lo.count == 1 || hi.count == 1 || lo.stride != hi.stride) return true;
+    const size_t at = apart % lo.stride;
+    return at < lo.bytes || at + hi.bytes > lo.stride;
+}
+
 // What the entries of the backward pass have in common.  Sizes are validated
 // before anything is read; `p` comes with the row counts, bounds and layouts.
 gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
@@ -181,6 +205,18 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
     const size_t stat = bwd_stat_bytes(p.Tq, p.num_docs, p.Hq);
     if (!workspace || workspace_bytes < 2 * stat + kBwdCounters || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return GBATTN_ERR_WORKSPACE;
+    const long long q_bytes = 2ll * p.Tq * p.Hq * D, k_bytes = 2ll * p.Tk * p.Hkv * D, lse_bytes = 4ll * p.Tq * p.Hq;
+    const Span outs[] = {whole(dq, q_bytes), whole(dk, k_bytes), whole(dv, k_bytes),
+                         whole(workspace, static_cast<long long>(2 * stat + kBwdCounters))};
+    const Span ins[] = {whole(q, q_bytes), whole(k, k_bytes), whole(v, k_bytes), whole(dout, q_bytes),
+                        whole(out, out_dtype == GBATTN_OUT_F32 ? 2 * q_bytes : q_bytes), whole(lse, lse_bytes),
+                        whole(dlse, lse_bytes)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Span& in : ins)
+            if (meet(outs[i], in)) return GBATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (meet(outs[i], outs[j])) return GBATTN_ERR_INVALID_ARG;
+    }
     DeviceInfo di;
     gbattn_status s = device_info(&di);
     if (s != GBATTN_OK) return s;
@@ -1010,7 +1046,14 @@ gbattn_status attn_rotary(const void* q, long long q_stride, const void* k, long
         if (k_out_stride < static_cast<long long>(Hkv) * D) return GBATTN_ERR_INVALID_ARG;
         if ((k_out_stride & 7) != 0) return GBATTN_ERR_ALIGNMENT;
     }
-    p.in_place = q == q_out && q_stride == q_out_stride && (Hkv == 0 || (k == k_out && k_stride == k_out_stride));
+    const bool q_same = q == q_out && (num_tokens == 1 || q_stride == q_out_stride);
+    const bool k_same = Hkv == 0 || (k == k_out && (num_tokens == 1 || k_stride == k_out_stride));
+    p.in_place = q_same && k_same;
+    const long long q_row = static_cast<long long>(Hq) * D, k_row = static_cast<long long>(Hkv) * D;
+    const Span qi = bf16_rows(q, num_tokens, q_row, q_stride), qo = bf16_rows(q_out, num_tokens, q_row, q_out_stride);
+    const Span ki = bf16_rows(k, num_tokens, k_row, k_stride), ko = bf16_rows(k_out, num_tokens, k_row, k_out_stride);
+    if ((!q_same && meet(qo, qi)) || (!k_same && meet(ko, ki)) || meet(qo, ki) || meet(ko, qi) || meet(qo, ko))
+        return GBATTN_ERR_INVALID_ARG;
     DeviceInfo di;
     s = device_info(&di);
     if (s != GBATTN_OK) return s;
@@ -1054,6 +1097,14 @@ gbattn_status attn_rotary_kv_cache_write(const void* q, long long q_stride, cons
     if (!value || !slot_mapping) return GBATTN_ERR_INVALID_ARG;
     if (num_tokens > 1 && value_stride < p.k_out_stride) return GBATTN_ERR_INVALID_ARG;
     if (!aligned16(value) || (num_tokens > 1 && (value_stride & 7) != 0)) return GBATTN_ERR_ALIGNMENT;
+    const bool q_same = q == q_out && (num_tokens == 1 || q_stride == q_out_stride);
+    const long long q_row = static_cast<long long>(Hq) * D, k_row = p.k_out_stride;
+    const Span qi = bf16_rows(q, num_tokens, q_row, q_stride), qo = bf16_rows(q_out, num_tokens, q_row, q_out_stride);
+    const Span ki = bf16_rows(key, num_tokens, k_row, key_stride), vi = bf16_rows(value, num_tokens, k_row, value_stride);
+    const Span cache = whole(kv_cache, 4 * k_row * p.num_slots);
+    if ((!q_same && meet(qo, qi)) || meet(qo, ki) || meet(qo, vi) || meet(qo, cache) || meet(cache, qi) || meet(cache, ki) ||
+        meet(cache, vi))
+        return GBATTN_ERR_INVALID_ARG;
     DeviceInfo di;
     s = device_info(&di);
     if (s != GBATTN_OK) return s;

@@ -25,7 +25,8 @@
  *  - The same inputs give the same bits: each gradient row is summed in one
  *    order, without atomics.
  *  - dq, dk and dv are written whole but for the rows that belong to no
- *    document; they must not overlap the inputs.
+ *    document.  They and the workspace must not overlap the inputs or each
+ *    other (GBATTN_ERR_INVALID_ARG).
  *  - workspace: device buffer of at least attn_bwd_workspace_size bytes,
  *    256-byte aligned, needing no initialisation; calls that can overlap
  *    (other streams, graphs replayed together) need one each.

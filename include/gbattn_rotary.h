@@ -19,7 +19,8 @@
  *    contiguous, token t at t * stride elements (parts of a fused projection).
  *    Strides are multiples of 8 and at least heads * D.
  *  - an output may be its input (the same pointer and stride); else outputs
- *    must not overlap the inputs or each other.
+ *    must not overlap the inputs or each other (GBATTN_ERR_INVALID_ARG).  Parts
+ *    of one buffer that lie between one another have the same token stride.
  *  - products and cosines are fp32, rounded once to bf16.
  */
 #ifndef GBATTN_ROTARY_H

@@ -132,6 +132,27 @@ def test_packed_refusals(lib):
     assert varlen(lib, N=0) == varlen(lib, Tq=0, Tk=0, mq=0, mk=0) == OK
 
 
+def test_outputs_that_overlap_are_refused(lib):
+    """Of 8 rows, 4 query and 2 KV heads of 128: q, dout, dq 8192 bytes, out 16384 in fp32, k, v, dk, dv 4096, lse 128."""
+    at, where = 1 << 20, {}
+    for n in ("q", "k", "v", "out", "lse", "dlse", "dout", "dq", "dk", "dv", "ws"):
+        where[n] = at
+        at += 1 << 20
+    size = dict(q=8192, dout=8192, out=16384, k=4096, v=4096, lse=128, dlse=128, dq=8192, dk=4096, dv=4096,
+                ws=lib.attn_bwd_workspace_size(1, 8, 4))
+    for fn in ("attn_bwd_dense", "attn_bwd_padded"):
+        for o in ("dq", "dk", "dv", "ws"):
+            for n in where:
+                if n == o:
+                    continue
+                # the same place, the last bytes of the other, the other at this one's last bytes
+                step = 256 if o == "ws" else 16
+                for to in (where[n], where[n] + (size[n] - 1) // step * step):
+                    a = {x: ctypes.c_void_p(p) for x, p in where.items()}
+                    a[o] = ctypes.c_void_p(to)
+                    assert dense(lib, fn, odt=1, **a) == INVALID, (o, n, to)
+
+
 def test_binding_refuses_host_tensors():
     import torch
 

@@ -416,3 +416,20 @@ def test_a_scattered_padding_mask_through_the_packing_calls(causal):
                                          do[b].cpu()[kept], s, causal, bounds=True)
         check([x[b].cpu()[kept] for x in got], ref, f"row {b}")
         assert not any(x[b].cpu()[~kept].any() for x in got)
+
+
+def test_outputs_next_to_one_another_and_outputs_over_inputs():
+    """Gradients and workspace as neighbours in one buffer are as separate ones; over an input they are refused."""
+    g = torch.Generator().manual_seed(9)
+    B, S, Hq, Hkv, D, s = 2, 150, 4, 2, 64, 0.125
+    q, k, v, do = randn(g, B, S, Hq, D), randn(g, B, S, Hkv, D), randn(g, B, S, Hkv, D), randn(g, B, S, Hq, D)
+    out, lse = gb.attn_fwd_dense(q, k, v, s, True, lse=True, out_dtype=BF16)
+    ref = gb.attn_bwd_dense(q, k, v, out, lse, do, s, True)
+    nq, nk, nw = q.numel(), k.numel(), gb.attn_bwd_workspace_size(B, B * S, Hq) // 2
+    flat = torch.empty(nw + nq + 2 * nk, dtype=BF16, device=dev())
+    ws, dq, dk, dv = flat.split([nw, nq, nk, nk])
+    got = gb.attn_bwd_dense(q, k, v, out, lse, do, s, True, dq=dq.view_as(q), dk=dk.view_as(k), dv=dv.view_as(k), workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    for bad in (dict(dq=q), dict(dq=out), dict(dq=do), dict(dk=k), dict(dv=v), dict(dk=ref[1], dv=ref[1])):
+        with pytest.raises(gb.GbattnError):
+            gb.attn_bwd_dense(q, k, v, out, lse, do, s, True, **bad)

@@ -171,6 +171,31 @@ def test_refusals_of_each(lib):
     assert store(lib, nb=1 << 24, bs=128) == UNSUPPORTED
 
 
+def test_outputs_that_overlap_are_refused(lib):
+    """4 tokens of 4 query and 2 KV heads of 128: rows of 1024 and 512 bytes."""
+    def at(x):
+        return ctypes.c_void_p((1 << 20) + x)
+
+    far = {n: at(i << 20) for i, n in enumerate(("q", "k", "qo", "ko", "v", "cache"))}
+    turn = {n: far[n] for n in ("q", "k", "qo", "ko")}
+    for o, others in (("qo", ("k", "ko")), ("ko", ("q", "qo"))):
+        for n in others:
+            assert rotary(lib, **{**turn, o: far[n]}) == INVALID
+    assert rotary(lib, **{**turn, "qo": at(16)}) == INVALID                 # a part of q
+    assert rotary(lib, **{**turn, "qo": at(3 * 1024 + 1008)}) == INVALID    # its last bytes
+    assert rotary(lib, **{**turn, "qo": far["q"], "qos": 520}) == INVALID   # q at another stride
+    assert rotary(lib, **{**turn, "ko": far["k"], "kos": 512}) == INVALID
+    # q, k side by side in rows of 2048 bytes: an output one unit into the other part, or past the row's end
+    fused = dict(q=at(0), qs=1024, k=at(1024), ks=1024, qo=at(0), qos=1024, ko=at(1024), kos=1024)
+    assert rotary(lib, **{**fused, "ko": at(1008)}) == INVALID
+    assert rotary(lib, **{**fused, "ko": at(1552)}) == INVALID
+    store_far = {n: far[n] for n in ("q", "k", "v", "qo", "cache")}
+    for o, n in (("qo", "k"), ("qo", "v"), ("qo", "cache"), ("cache", "q"), ("cache", "k"), ("cache", "v"), ("cache", "qo")):
+        assert store(lib, **{**store_far, o: far[n]}) == INVALID
+    last = 2 * 4 * 128 * 512 - 16  # the cache's last unit
+    assert store(lib, **{**store_far, "v": ctypes.c_void_p(far["cache"].value + last)}) == INVALID
+
+
 def test_binding_refuses_host_tensors(lib):
     import torch
 

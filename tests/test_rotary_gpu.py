@@ -274,3 +274,19 @@ def test_offsets_past_32_bits(interleaved):
     assert torch.equal(values[slots[rows].long()], v[rows]) and torch.equal(values.flip(0), v)
     b, c = gb.attn_rotary(q, k, pos, plan, q_out=q, k_out=k)  # in place, in the strided tensor
     assert torch.equal(b, a) and torch.equal(c.flip(0), keys) and b is q
+
+
+def test_outputs_over_other_inputs_are_refused_and_neighbours_are_not():
+    g = torch.Generator().manual_seed(10)
+    T, H, D = 33, 4, 64
+    fused = torch.randn(T, 4, H, D, generator=g).to(torch.bfloat16).cuda()
+    q, k, qo, ko = fused.unbind(1)
+    pos, plan = torch.arange(T, dtype=torch.int32, device="cuda"), gb.RotaryPlan(D)
+    ref = gb.attn_rotary(q, k, pos, plan)
+    gb.attn_rotary(q, k, pos, plan, q_out=qo, k_out=ko)
+    assert torch.equal(qo, ref[0]) and torch.equal(ko, ref[1])
+    for q_out, k_out in ((k, q), (k, None), (None, q), (qo, qo), (q.as_strided((T, H, D), (H * D, D, 1)), None)):
+        with pytest.raises(gb.GbattnError):
+            gb.attn_rotary(q, k, pos, plan, q_out=q_out, k_out=k_out)
+    gb.attn_rotary(q, k, pos, plan, q_out=q, k_out=k)
+    assert torch.equal(q, ref[0]) and torch.equal(k, ref[1])
