@@ -210,6 +210,14 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ uint4 load_once(const void* src) {  // 16 bytes that nothing reads again soon
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(src));
+    return v;
+}
+
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
@@ -238,57 +246,71 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, c
     if (i0 >= d.Lq) return;
     const int h0 = blockIdx.y * heads, nh = min(heads, p.Hq - h0);
     const int nr = static_cast<int>(min(static_cast<long long>(rows), d.Lq - i0));
+    // the pair that this thread finishes
+    const int hp = threadIdx.x / rows;
+    const long long ip = i0 + threadIdx.x % rows;
+    const bool pair = hp < nh && ip < d.Lq;
+    float lse = 0.f, dlse = 0.f;
+    if (pair) {
+        const long long at = doc * p.lse_bstride + (h0 + hp) * p.lse_hstride + (p.lse_row_global ? d.q_start + ip : ip);
+        lse = p.lse[at];
+        if (p.dlse) dlse = p.dlse[at];
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
-    for (int u0 = warp * PER_WARP + lane / LANES; u0 - lane / LANES < nr * nh; u0 += 8 * PER_WARP * UN) {
+    const long long first = ((d.q_start + i0) * p.Hq + h0) * D + sub * 8;
+    const uint16_t* dout = static_cast<const uint16_t*>(p.dout) + first;
+    const uint16_t* out = static_cast<const uint16_t*>(p.out) + (F32 ? 2 : 1) * first;
+    constexpr int STEP = 8 * PER_WARP;  // pairs between one lane's loads
+    const int total = nr * nh, step_i = STEP / nh, step_h = STEP % nh;
+    int u = warp * PER_WARP + lane / LANES, i = u / nh, h = u % nh;
+    while (u - lane / LANES < total) {
         uint4 g[UN], o[UN], o2[UN];
+        int to[UN];  // in dots, or -1
 #pragma unroll
         for (int x = 0; x < UN; ++x) {
-            const int u = u0 + x * 8 * PER_WARP;
             g[x] = o[x] = o2[x] = make_uint4(0u, 0u, 0u, 0u);
-            if (u < nr * nh && sub * 8 < D) {
-                const int i = u / nh, h = h0 + u % nh;
-                const long long at = ((d.q_start + i0 + i) * p.Hq + h) * D + sub * 8;
-                g[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dout) + at));
-                if (F32) {
-                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const float*>(p.out) + at);
-                    o[x] = __ldg(src);
-                    o2[x] = __ldg(src + 1);
-                } else {
-                    o[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out) + at));
-                }
+            to[x] = u < total ? h * rows + i : -1;
+            if (u < total && sub * 8 < D) {
+                const long long at = static_cast<long long>(i * p.Hq + h) * D;
+                g[x] = load_once(dout + at);
+                const uint4* src = reinterpret_cast<const uint4*>(out + (F32 ? 2 : 1) * at);
+                o[x] = load_once(src);
+                if (F32) o2[x] = load_once(src + 1);
             }
+            u += STEP, i += step_i, h += step_h;
+            if (h >= nh) h -= nh, ++i;
         }
+        float acc[UN];
 #pragma unroll
         for (int x = 0; x < UN; ++x) {
             const uint32_t gw[4] = {g[x].x, g[x].y, g[x].z, g[x].w};
             const uint32_t ow[8] = {o[x].x, o[x].y, o[x].z, o[x].w, o2[x].x, o2[x].y, o2[x].z, o2[x].w};
-            float acc = 0.f;
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack_bf16x2(gw[e]);
-                const float2 v = F32 ? make_float2(__uint_as_float(ow[2 * e]), __uint_as_float(ow[2 * e + 1]))
-                                     : unpack_bf16x2(ow[e]);
-                acc = fmaf(f.x, v.x, acc);
-                acc = fmaf(f.y, v.y, acc);
-            }
-#pragma unroll
-            for (int s = LANES / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
-            const int u = u0 + x * 8 * PER_WARP;
-            if (sub == 0 && u < nr * nh) dots[(u % nh) * rows + u / nh] = acc;
+            for (int e = 0; e < 4; ++e)
+                sum = __ffma2_rn(unpack_bf16x2(gw[e]),
+                                 F32 ? make_float2(__uint_as_float(ow[2 * e]), __uint_as_float(ow[2 * e + 1]))
+                                     : unpack_bf16x2(ow[e]),
+                                 sum);
+            acc[x] = sum.x + sum.y;
         }
+        // Four sums over the lanes: each half of them goes on with two, each quarter
+        // with one (five exchanges for 16 lanes instead of sixteen).
+        const bool hi = sub & (LANES / 2), hi2 = sub & (LANES / 4);
+        const float s0 = (hi ? acc[2] : acc[0]) + __shfl_xor_sync(0xffffffffu, hi ? acc[0] : acc[2], LANES / 2);
+        const float s1 = (hi ? acc[3] : acc[1]) + __shfl_xor_sync(0xffffffffu, hi ? acc[1] : acc[3], LANES / 2);
+        float s = (hi2 ? s1 : s0) + __shfl_xor_sync(0xffffffffu, hi2 ? s0 : s1, LANES / 4);
+#pragma unroll
+        for (int m = LANES / 8; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+        const int at = hi ? (hi2 ? to[3] : to[2]) : (hi2 ? to[1] : to[0]);
+        if (sub % (LANES / 4) == 0 && at >= 0) dots[at] = s;
     }
     __syncthreads();
-    const long long base = bwd_stat_base(d.q_start, doc);
-    for (int x = threadIdx.x; x < nh * rows; x += 256) {
-        const int h = h0 + x / rows;
-        const long long i = i0 + x % rows;
-        if (i >= d.Lq) continue;
-        const long long at = doc * p.lse_bstride + h * p.lse_hstride + (p.lse_row_global ? d.q_start + i : i);
-        const long long to = h * p.stat_stride + base + i;
+    if (pair) {
+        const long long at = (h0 + hp) * p.stat_stride + bwd_stat_base(d.q_start, doc) + ip;
         // a row that sees no key (lse = -inf) has p = 2^(s - inf) = 0
-        const float lse = p.lse[at];
-        p.neg_lse2[to] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
-        p.neg_delta[to] = (p.dlse ? p.dlse[at] : 0.f) - dots[x];
+        p.neg_lse2[at] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+        p.neg_delta[at] = dlse - dots[threadIdx.x];
     }
     if (!few) grid_launch_dependents();
 }
