@@ -23,9 +23,9 @@
 // timing: there are no atomics.  The price is that S and dP are formed twice,
 // seven products for the five that one pass with atomics on dQ would need.
 //
-// DiT self-attention, 2 x 4096 rows, 24 heads, D = 128: 926 us a call, of them 23
-// for the statistics, 465 and 407 for the two passes by themselves; 1.11 PFLOP/s
-// of five products, 1.55 of the seven, at the power cap (1.83 GHz).
+// DiT self-attention, 2 x 4096 rows, 24 heads, D = 128: 921 us a call, of them 17
+// for the statistics, 464 and 410 for the two passes by themselves; 1.12 PFLOP/s
+// of five products, 1.56 of the seven, at the power cap (1.83 GHz).
 //
 // P and dS are rounded to bf16 as operands of the second products, as P is in
 // the forward kernels (at most 2^-8 of each term, independent of one another);
@@ -210,11 +210,19 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ uint4 load_once(const void* src) {  // 16 bytes that nothing reads again soon
+// 16 bytes that this kernel does not write.  ONCE: nor reads again (of a sector
+// that a lane's two loads share, the second would come from L2 too).
+template <bool ONCE>
+__device__ __forceinline__ uint4 load16(const void* src) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(src));
+    if (ONCE)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(src));
+    else
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(src));
     return v;
 }
 
@@ -229,8 +237,11 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
 // most: rows of dout and out are read whole, LANES lanes a pair and UN pairs in
 // flight a lane; the results cross shared memory, so that a head's statistics
 // are read and written for eight rows or more at a time.
+// HBM-bound: cross-attention of 16384 rows of 40 heads of 128 takes 51 us (348 MB,
+// the copy's rate), eight packed documents 69 (four CTAs an SM leave registers
+// for the loads in flight: 55 and 72 without the bound).
 template <int D, bool F32>
-__global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, const int rows, const int heads) {
+__global__ void __launch_bounds__(256, 4) attn_bwd_stat_sm103a(const BwdParams p, const int rows, const int heads) {
     constexpr int LANES = D <= 64 ? 8 : (D <= 128 ? 16 : 32), UN = 4, PER_WARP = 32 / LANES;
     __shared__ float dots[256];
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < kBwdPasses) p.claims[threadIdx.x] = 0u;
@@ -272,10 +283,10 @@ __global__ void __launch_bounds__(256) attn_bwd_stat_sm103a(const BwdParams p, c
             to[x] = u < total ? h * rows + i : -1;
             if (u < total && sub * 8 < D) {
                 const long long at = static_cast<long long>(i * p.Hq + h) * D;
-                g[x] = load_once(dout + at);
+                g[x] = load16<true>(dout + at);
                 const uint4* src = reinterpret_cast<const uint4*>(out + (F32 ? 2 : 1) * at);
-                o[x] = load_once(src);
-                if (F32) o2[x] = load_once(src + 1);
+                o[x] = load16<!F32>(src);
+                if (F32) o2[x] = load16<false>(src + 1);
             }
             u += STEP, i += step_i, h += step_h;
             if (h >= nh) h -= nh, ++i;
