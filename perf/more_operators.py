@@ -289,7 +289,7 @@ def prepare(case, seed):
                 st["out"][n, :a] = o.to(odt)
         else:
             o, st["lse"] = _forward(st["q"], st["k"], st["v"], st["scale"], _visible(Sq, Sk, case["causal"], dev))
-            st["out"], st["lse"] = o.to(odt).contiguous(), st["lse"].contiguous()  # laid out as the forward call leaves them
+            st["out"], st["lse"] = o.to(odt), st["lse"].contiguous()
     st["dlse"] = torch.randn(st["lse"].shape, generator=g, device=dev) if case["dlse"] else None
     return st
 
