@@ -19,7 +19,7 @@ Entry points (same names as the C ABI):
     attn_kv_cache_write_fp8, attn_kv_cache_read_fp8, attn_fwd_paged_fp8,
     attn_fwd_paged_fp8_workspace_size: the 8-bit paged KV cache
     attn_bwd_dense, attn_bwd_padded, attn_bwd_varlen, attn_bwd_workspace_size: gradients
-    (include/gbattn_bwd.h)
+    (include/gbattn_bwd.h, and include/gbattn_bwd_strided.h for an out that is not contiguous)
     attn_rotary, attn_rotary_kv_cache_write, attn_rotary_frequencies, attn_rotary_steps: rotary
     positions (include/gbattn_rotary.h), with RotaryPlan holding a head's frequencies on the device
 Compositions of those calls: attn_fwd_masked (padding mask), attn_vsa (block-sparse
@@ -86,6 +86,10 @@ SIGNATURES = {
                              _P, _P]),
     "attn_bwd_varlen": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P,
                              _P, _Z, _P, _P]),
+    "attn_bwd_padded_strided": (_I, [_P, _P, _P, _P, _I, _L, _L, _L, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P,
+                                     _P, _P, _P, _Z, _P, _P]),
+    "attn_bwd_varlen_strided": (_I, [_P, _P, _P, _P, _I, _L, _L, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I,
+                                     _P, _P, _P, _P, _Z, _P, _P]),
     "attn_rotary_frequencies": (_I, [_I, _D, _I, _D, _D, _D, _D, _P, _P]),
     "attn_rotary_steps": (_I, [_P, _I, _P]),
     "attn_rotary": (_I, [_P, _L, _P, _L, _P, _I, _P, _I, _I, _I, _F, _I, _I, _I, _P, _L, _P, _L, _P]),
@@ -895,12 +899,31 @@ def _run_on(name, dev, stream, args):
         raise GbattnError(name, st)
 
 
-def _tensor(name, t, dev, dtype, shape):
-    """Raise ValueError unless t is a contiguous tensor of this type and shape on CUDA device number dev."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)}")
+def _tensor(name, t, dev, dtype, shape, strided=False):
+    """Raise ValueError unless t is a contiguous (or strided) tensor of this type and shape on CUDA device number dev."""
+    if t.dtype != dtype or t.shape != shape or not (strided or t.is_contiguous()):
+        raise ValueError(f"{name} must be a {'' if strided else 'contiguous '}{str(dtype)[6:]} tensor {list(shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}, with q")
+
+
+def _laid_out(stream, t):
+    """t, or a contiguous copy of it made on the stream that will read it."""
+    if t is None or t.is_contiguous():
+        return t
+    if stream is None:
+        return t.detach().contiguous()
+    with torch.cuda.stream(stream):
+        return t.detach().contiguous()
+
+
+def _row_strides(t):
+    """Strides, up to the last dimension's, of a tensor whose rows of D values can be read where they lie: side by side, each
+    on 16 bytes.  None if they cannot.  (A dimension of one index has no stride.)"""
+    *strides, col = (0 if n == 1 else s for n, s in zip(t.shape, t.stride()))
+    if col != 1 or t.data_ptr() % 16 or any(s * t.element_size() % 16 for s in strides):
+        return None
+    return strides
 
 
 def _like(stream, t):
@@ -927,14 +950,14 @@ def _bwd(name, q, k, v, out, lse, dout, dlse, index, sizes, docs, heads, lse_sha
     bf16, qs, ks = torch.bfloat16, q.shape, k.shape
     f32_out = out.dtype == torch.float32
     if not (q.dtype == k.dtype == v.dtype == dout.dtype == bf16 and q.is_contiguous() and k.is_contiguous()
-            and v.is_contiguous() and dout.is_contiguous() and v.shape == ks and dout.shape == qs
+            and v.is_contiguous() and v.shape == ks and dout.shape == qs
             and k.get_device() == v.get_device() == dout.get_device() == dev):
         for n, t, shape in (("q", q, qs), ("k", k, ks), ("v", v, ks), ("dout", dout, qs)):
-            _tensor(n, t, dev, bf16, shape)
-    _tensor("out", out, dev, torch.float32 if f32_out else bf16, qs)
-    _tensor("lse", lse, dev, torch.float32, lse_shape)
+            _tensor(n, t, dev, bf16, shape, strided=n == "dout")
+    _tensor("out", out, dev, torch.float32 if f32_out else bf16, qs, strided=True)
+    _tensor("lse", lse, dev, torch.float32, lse_shape, strided=True)
     if dlse is not None:
-        _tensor("dlse", dlse, dev, torch.float32, lse_shape)
+        _tensor("dlse", dlse, dev, torch.float32, lse_shape, strided=True)
     for n, t, entries in index:
         if t is not None:
             _tensor(n, t, dev, torch.int32, (entries,))
@@ -955,9 +978,21 @@ def _bwd(name, q, k, v, out, lse, dout, dlse, index, sizes, docs, heads, lse_sha
     else:
         raise ValueError(f"workspace must be contiguous and on cuda:{dev}, with q")
     scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
+    # what other code computed or autograd hands over: out is read where it lies, the others are laid out
+    strides = ()
+    if not out.is_contiguous():
+        strides = _row_strides(out)
+        if strides is None:
+            out, strides = _laid_out(stream, out), ()
+        elif name == "attn_bwd_varlen":
+            name = "attn_bwd_varlen_strided"
+        else:
+            name = "attn_bwd_padded_strided"
+            index = index or (("lens_q", None, 0), ("lens_k", None, 0))
+    dout, lse, dlse = _laid_out(stream, dout), _laid_out(stream, lse), _laid_out(stream, dlse)
     _run_on(name, dev, stream,
-            (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), OUT_F32 if f32_out else OUT_BF16, lse.data_ptr(),
-             dout.data_ptr(), None if dlse is None else dlse.data_ptr(),
+            (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), OUT_F32 if f32_out else OUT_BF16, *strides,
+             lse.data_ptr(), dout.data_ptr(), None if dlse is None else dlse.data_ptr(),
              *[None if t is None else t.data_ptr() for _, t, _ in index], *sizes, Hq, Hkv, D, scale, 1 if causal else 0,
              dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), ws_bytes, status))
     return dq, dk, dv
@@ -976,10 +1011,13 @@ def attn_bwd_dense(q, k, v, out, lse, dout, softmax_scale=None, causal=False, dl
     """Gradients of attn_fwd_dense from what it took and returned: q, dout
     [B, Sq, Hq, D] and k, v [B, Sk, Hkv, D] bf16, out (bf16 or fp32) and lse
     [B, Hq, Sq] as it returned them, dout the gradient of out and dlse that of
-    lse (None: lse is not used further on).  Returns (dq, dk, dv) in bf16;
-    tensors given for them are written and must not overlap the inputs.  A workspace of at least
-    ``attn_bwd_workspace_size(B, B * Sq, Hq)`` bytes may be passed (it is
-    allocated here otherwise); calls that can overlap need one each."""
+    lse (None: lse is not used further on).  out, dout, lse and dlse may have
+    any strides: an out whose rows of D values lie on 16 bytes is read where it
+    is, the others are copied first unless they are contiguous.  Returns (dq,
+    dk, dv) in bf16; tensors given for them are written and must not overlap the
+    inputs.  A workspace of at least ``attn_bwd_workspace_size(B, B * Sq, Hq)``
+    bytes may be passed (it is allocated here otherwise); calls that can overlap
+    need one each."""
     B, Sq, Sk, Hq, Hkv, D = _bwd_batch(q, k)
     return _bwd("attn_bwd_dense", q, k, v, out, lse, dout, dlse, (), (B, Sq, Sk), B, (Hq, Hkv, D), (B, Hq, Sq),
                 softmax_scale, causal, dq, dk, dv, workspace, dev_status, stream)

@@ -3,6 +3,7 @@
 // synchronisation; every launch goes to the caller's stream.
 #include "../../include/gbattn.h"
 #include "../../include/gbattn_bwd.h"
+#include "../../include/gbattn_bwd_strided.h"
 #include "../../include/gbattn_rotary.h"
 
 #include <cuda.h>
@@ -180,6 +181,17 @@ bool meet(const Span& a, const Span& b) {
     return at < lo.bytes || at + hi.bytes > lo.stride;
 }
 
+// Strides of contiguous [.., rows, heads, D]; zeros for sizes that are refused.
+struct RowStrides {
+    long long entry = 0, row = 0, head = 0;
+    RowStrides(int rows, int heads, int D) {
+        if (rows < 0 || heads <= 0 || !head_size_ok(D)) return;
+        head = D;
+        row = static_cast<long long>(heads) * D;
+        entry = rows < (1ll << 58) / row ? rows * row : 0;
+    }
+};
+
 // What the entries of the backward pass have in common.  Sizes are validated
 // before anything is read; `p` comes with the row counts, bounds and layouts.
 gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
@@ -201,6 +213,23 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
     const long long qh = static_cast<long long>(p.tiles_q) * p.num_docs, kh = static_cast<long long>(p.tiles_k) * p.num_docs;
     if (qh > kMost / p.Hq || kh > kMost / p.Hkv) return GBATTN_ERR_UNSUPPORTED;
     if ((p.Hq + 31) / 32 > 65535) return GBATTN_ERR_UNSUPPORTED;
+    // out from its first byte to its last
+    const long long out_size = out_dtype == GBATTN_OUT_F32 ? 4 : 2;
+    long long out_bytes = 0;
+    if (rows) {
+        const bool packed = p.cu_q != nullptr;
+        const long long steps[3][2] = {{packed ? 0 : p.num_docs - 1ll, p.out_bstride},
+                                       {(packed ? p.Tq : p.max_q) - 1ll, p.out_rstride},
+                                       {p.Hq - 1ll, p.out_hstride}};
+        out_bytes = out_size * D;
+        for (const auto& x : steps) {
+            if (x[0] <= 0) continue;  // a stride that nothing uses
+            if (x[1] < 0) return GBATTN_ERR_INVALID_ARG;
+            if (x[1] * out_size % 16 != 0) return GBATTN_ERR_ALIGNMENT;
+            if (x[1] > (1ll << 58) / x[0]) return GBATTN_ERR_UNSUPPORTED;
+            out_bytes += out_size * x[0] * x[1];
+        }
+    }
     if (!rows && !keys) return GBATTN_OK;
     const size_t stat = bwd_stat_bytes(p.Tq, p.num_docs, p.Hq);
     if (!workspace || workspace_bytes < 2 * stat + kBwdCounters || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -208,9 +237,8 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
     const long long q_bytes = 2ll * p.Tq * p.Hq * D, k_bytes = 2ll * p.Tk * p.Hkv * D, lse_bytes = 4ll * p.Tq * p.Hq;
     const Span outs[] = {whole(dq, q_bytes), whole(dk, k_bytes), whole(dv, k_bytes),
                          whole(workspace, static_cast<long long>(2 * stat + kBwdCounters))};
-    const Span ins[] = {whole(q, q_bytes), whole(k, k_bytes), whole(v, k_bytes), whole(dout, q_bytes),
-                        whole(out, out_dtype == GBATTN_OUT_F32 ? 2 * q_bytes : q_bytes), whole(lse, lse_bytes),
-                        whole(dlse, lse_bytes)};
+    const Span ins[] = {whole(q, q_bytes),     whole(k, k_bytes),     whole(v, k_bytes),    whole(dout, q_bytes),
+                        whole(out, out_bytes), whole(lse, lse_bytes), whole(dlse, lse_bytes)};
     for (int i = 0; i < 4; ++i) {
         for (const Span& in : ins)
             if (meet(outs[i], in)) return GBATTN_ERR_INVALID_ARG;
@@ -959,11 +987,12 @@ size_t attn_bwd_workspace_size(int num_docs, int Tq, int Hq) {
     return 2 * bwd_stat_bytes(Tq, num_docs, Hq) + kBwdCounters;
 }
 
-gbattn_status attn_bwd_padded(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
-                              const float* lse, const void* dout, const float* dlse, const int32_t* lens_q,
-                              const int32_t* lens_k, int B, int Sq, int Sk, int Hq, int Hkv, int D, float softmax_scale,
-                              int causal, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
-                              uint32_t* dev_status, void* stream) {
+gbattn_status attn_bwd_padded_strided(const void* q, const void* k, const void* v, const void* out,
+                                      gbattn_dtype out_dtype, long long out_bstride, long long out_rstride,
+                                      long long out_hstride, const float* lse, const void* dout, const float* dlse,
+                                      const int32_t* lens_q, const int32_t* lens_k, int B, int Sq, int Sk, int Hq, int Hkv,
+                                      int D, float softmax_scale, int causal, void* dq, void* dk, void* dv,
+                                      void* workspace, size_t workspace_bytes, uint32_t* dev_status, void* stream) {
     if (B < 0 || Sq < 0 || Sk < 0) return GBATTN_ERR_INVALID_ARG;
     if (B > 65535 || static_cast<long long>(B) * Sq > 0x7fffffffLL || static_cast<long long>(B) * Sk > 0x7fffffffLL)
         return GBATTN_ERR_UNSUPPORTED;  // row counts are 32-bit on the device
@@ -979,8 +1008,22 @@ gbattn_status attn_bwd_padded(const void* q, const void* k, const void* v, const
     p.Hkv = Hkv;
     p.lse_bstride = static_cast<long long>(Hq) * Sq;
     p.lse_hstride = Sq;
+    p.out_bstride = out_bstride;
+    p.out_rstride = out_rstride;
+    p.out_hstride = out_hstride;
     return run_bwd(q, k, v, out, out_dtype, lse, dout, dlse, D, softmax_scale, causal, dq, dk, dv, workspace,
                    workspace_bytes, dev_status, p, static_cast<cudaStream_t>(stream));
+}
+
+gbattn_status attn_bwd_padded(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
+                              const float* lse, const void* dout, const float* dlse, const int32_t* lens_q,
+                              const int32_t* lens_k, int B, int Sq, int Sk, int Hq, int Hkv, int D, float softmax_scale,
+                              int causal, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                              uint32_t* dev_status, void* stream) {
+    const RowStrides o(Sq, Hq, D);
+    return attn_bwd_padded_strided(q, k, v, out, out_dtype, o.entry, o.row, o.head, lse, dout, dlse, lens_q, lens_k, B, Sq,
+                                   Sk, Hq, Hkv, D, softmax_scale, causal, dq, dk, dv, workspace, workspace_bytes,
+                                   dev_status, stream);
 }
 
 gbattn_status attn_bwd_dense(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
@@ -991,12 +1034,13 @@ gbattn_status attn_bwd_dense(const void* q, const void* k, const void* v, const 
                            softmax_scale, causal, dq, dk, dv, workspace, workspace_bytes, dev_status, stream);
 }
 
-gbattn_status attn_bwd_varlen(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
-                              const float* lse, const void* dout, const float* dlse, const int32_t* cu_seqlens_q,
-                              const int32_t* cu_seqlens_k, int num_docs, int Tq, int Tk, int max_seqlen_q,
-                              int max_seqlen_k, int Hq, int Hkv, int D, float softmax_scale, int causal, void* dq,
-                              void* dk, void* dv, void* workspace, size_t workspace_bytes, uint32_t* dev_status,
-                              void* stream) {
+gbattn_status attn_bwd_varlen_strided(const void* q, const void* k, const void* v, const void* out,
+                                      gbattn_dtype out_dtype, long long out_rstride, long long out_hstride,
+                                      const float* lse, const void* dout, const float* dlse, const int32_t* cu_seqlens_q,
+                                      const int32_t* cu_seqlens_k, int num_docs, int Tq, int Tk, int max_seqlen_q,
+                                      int max_seqlen_k, int Hq, int Hkv, int D, float softmax_scale, int causal, void* dq,
+                                      void* dk, void* dv, void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                      void* stream) {
     if (num_docs < 0 || Tq < 0 || Tk < 0 || max_seqlen_q < 0 || max_seqlen_k < 0) return GBATTN_ERR_INVALID_ARG;
     if (max_seqlen_q > Tq || max_seqlen_k > Tk) return GBATTN_ERR_INVALID_ARG;
     if (num_docs > 0 && (!cu_seqlens_q || !cu_seqlens_k)) return GBATTN_ERR_INVALID_ARG;
@@ -1013,8 +1057,22 @@ gbattn_status attn_bwd_varlen(const void* q, const void* k, const void* v, const
     p.Hkv = Hkv;
     p.lse_hstride = Tq;
     p.lse_row_global = 1;
+    p.out_rstride = out_rstride;
+    p.out_hstride = out_hstride;
     return run_bwd(q, k, v, out, out_dtype, lse, dout, dlse, D, softmax_scale, causal, dq, dk, dv, workspace,
                    workspace_bytes, dev_status, p, static_cast<cudaStream_t>(stream));
+}
+
+gbattn_status attn_bwd_varlen(const void* q, const void* k, const void* v, const void* out, gbattn_dtype out_dtype,
+                              const float* lse, const void* dout, const float* dlse, const int32_t* cu_seqlens_q,
+                              const int32_t* cu_seqlens_k, int num_docs, int Tq, int Tk, int max_seqlen_q,
+                              int max_seqlen_k, int Hq, int Hkv, int D, float softmax_scale, int causal, void* dq,
+                              void* dk, void* dv, void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                              void* stream) {
+    const RowStrides o(Tq, Hq, D);
+    return attn_bwd_varlen_strided(q, k, v, out, out_dtype, o.row, o.head, lse, dout, dlse, cu_seqlens_q, cu_seqlens_k,
+                                   num_docs, Tq, Tk, max_seqlen_q, max_seqlen_k, Hq, Hkv, D, softmax_scale, causal, dq, dk,
+                                   dv, workspace, workspace_bytes, dev_status, stream);
 }
 
 gbattn_status attn_rotary(const void* q, long long q_stride, const void* k, long long k_stride, const int32_t* positions,

@@ -240,7 +240,10 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
 // HBM-bound: cross-attention of 16384 rows of 40 heads of 128 takes 51 us (348 MB,
 // the copy's rate), eight packed documents 69 (four CTAs an SM leave registers
 // for the loads in flight: 55 and 72 without the bound).
-template <int D, bool F32>
+//   STRIDED: out lies by its strides.  (A contiguous one is read by dout's
+// offsets: the strides take registers that the fp32 loads need, and a padded
+// batch of D = 96 took 62 us for 57 with them.)
+template <int D, bool F32, bool STRIDED>
 __global__ void __launch_bounds__(256, 4) attn_bwd_stat_sm103a(const BwdParams p, const int rows, const int heads) {
     constexpr int LANES = D <= 64 ? 8 : (D <= 128 ? 16 : 32), UN = 4, PER_WARP = 32 / LANES;
     __shared__ float dots[256];
@@ -269,8 +272,11 @@ __global__ void __launch_bounds__(256, 4) attn_bwd_stat_sm103a(const BwdParams p
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES;
     const long long first = ((d.q_start + i0) * p.Hq + h0) * D + sub * 8;
+    const long long first_out = STRIDED ? doc * p.out_bstride + (p.cu_q ? d.q_start + i0 : i0) * p.out_rstride +
+                                              h0 * p.out_hstride + sub * 8
+                                        : first;
     const uint16_t* dout = static_cast<const uint16_t*>(p.dout) + first;
-    const uint16_t* out = static_cast<const uint16_t*>(p.out) + (F32 ? 2 : 1) * first;
+    const uint16_t* out = static_cast<const uint16_t*>(p.out) + (F32 ? 2 : 1) * first_out;
     constexpr int STEP = 8 * PER_WARP;  // pairs between one lane's loads
     const int total = nr * nh, step_i = STEP / nh, step_h = STEP % nh;
     int u = warp * PER_WARP + lane / LANES, i = u / nh, h = u % nh;
@@ -283,8 +289,9 @@ __global__ void __launch_bounds__(256, 4) attn_bwd_stat_sm103a(const BwdParams p
             to[x] = u < total ? h * rows + i : -1;
             if (u < total && sub * 8 < D) {
                 const long long at = static_cast<long long>(i * p.Hq + h) * D;
+                const long long at_out = STRIDED ? i * p.out_rstride + h * p.out_hstride : at;
                 g[x] = load16<true>(dout + at);
-                const uint4* src = reinterpret_cast<const uint4*>(out + (F32 ? 2 : 1) * at);
+                const uint4* src = reinterpret_cast<const uint4*>(out + (F32 ? 2 : 1) * at_out);
                 o[x] = load16<!F32>(src);
                 if (F32) o2[x] = load16<false>(src + 1);
             }
@@ -1422,10 +1429,17 @@ cudaError_t launch_d(const BwdMaps& m, BwdParams& p, int num_sms, cudaStream_t s
     // (without query rows one CTA a document still looks at its boundaries)
     const dim3 grid(static_cast<unsigned>(p.max_q > 0 ? (p.max_q - 1) / rows + 1 : 1),
                     static_cast<unsigned>((p.Hq + heads - 1) / heads), static_cast<unsigned>(p.num_docs));
-    if (p.out_f32)
-        attn_bwd_stat_sm103a<D, true><<<grid, 256, 0, stream>>>(p, rows, heads);
+    const long long row = static_cast<long long>(p.Hq) * D;
+    const bool strided = p.out_rstride != row || (p.Hq > 1 && p.out_hstride != D) ||
+                         (!p.cu_q && p.num_docs > 1 && p.out_bstride != p.max_q * row);
+    if (p.out_f32 && strided)
+        attn_bwd_stat_sm103a<D, true, true><<<grid, 256, 0, stream>>>(p, rows, heads);
+    else if (p.out_f32)
+        attn_bwd_stat_sm103a<D, true, false><<<grid, 256, 0, stream>>>(p, rows, heads);
+    else if (strided)
+        attn_bwd_stat_sm103a<D, false, true><<<grid, 256, 0, stream>>>(p, rows, heads);
     else
-        attn_bwd_stat_sm103a<D, false><<<grid, 256, 0, stream>>>(p, rows, heads);
+        attn_bwd_stat_sm103a<D, false, false><<<grid, 256, 0, stream>>>(p, rows, heads);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     p.early_wait = 1;
     if constexpr (D <= 128) {

@@ -320,7 +320,8 @@ cudaError_t launch_vsa_fwd(int D, const CUtensorMap& tmQ, const CUtensorMap& tmK
 // of out (and of lse).  Dense and padded batches have cu_q == nullptr and
 // max_q / max_k rows an entry; packed documents use cu_q / cu_k.
 struct BwdParams {
-    const void* out;        // [Tq, Hq, D] bf16 or fp32 (out_f32)
+    const void* out;        // bf16 or fp32 (out_f32), by the strides
+    long long out_bstride, out_rstride, out_hstride;  // elements from entry to entry (packed: 0), row to row, head to head
     const void* dout;       // [Tq, Hq, D] bf16
     const float* lse;       // as the forward pass wrote it
     const float* dlse;      // the same layout, or null
