@@ -51,14 +51,19 @@ def _compile(nv: str, src: str, verbose: bool) -> str:
     return obj
 
 
+def inputs() -> list:
+    """Every file the library is made of: sources, the headers beside them, the C ABI's headers, and this recipe."""
+    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    for d in (CSRC, os.path.join(os.path.dirname(PKG), "include")):
+        srcs += [os.path.join(d, h) for h in sorted(os.listdir(d)) if h.endswith((".h", ".cuh"))]
+    return srcs + [__file__]
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     """Compile and link; returns the path of libgbattn.so.  Skips the work
     when the library is newer than every source (unless ``force``)."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES] + [
-        os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".h", ".cuh"))
-    ] + [os.path.join(os.path.dirname(PKG), "include", "gbattn.h"), __file__]
     if not force and os.path.exists(LIB):
-        newest = max(os.path.getmtime(s) for s in srcs)
+        newest = max(os.path.getmtime(s) for s in inputs())
         if os.path.getmtime(LIB) >= newest:
             return LIB
     nv = nvcc()
