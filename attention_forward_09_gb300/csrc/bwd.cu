@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         return 1u;
     };
     // (a CTA of a cluster stays: the others read its shared memory)
-    if (split == 1 && status_has_timeout(p.status, kDevTimeout)) {
+    if (split == 1 && cta_has_timeout(p.status, kDevTimeout)) {
         grid_dependency_wait();
         return;
     }

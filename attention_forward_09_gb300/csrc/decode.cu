@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_hgroups = p.Hkv * (p.group / p.heads_per_cta);
-    if (status_has_timeout(p.status, kDevTimeout)) return;
+    if (cta_has_timeout(p.status, kDevTimeout)) return;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {

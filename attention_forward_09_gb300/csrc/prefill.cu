@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(192, 1)
     }
     const int q0 = tile * BM;
     if (q0 >= Lq) return;  // CTA-uniform, before any barrier or TMEM use
-    if (status_has_timeout(p.status, kDevTimeout)) return;
+    if (cta_has_timeout(p.status, kDevTimeout)) return;
     const int diag = Lk - Lqu;
     int kend = q0 < Lqu ? Lk : 0;
     if (p.causal && q0 < Lqu) kend = min(Lk, min(q0 + BM - 1, Lqu - 1) + diag + 1);
@@ -1004,7 +1004,7 @@ __global__ void __launch_bounds__(384, 1)
         Walk W0 = walk_here(0xffffffffu);  // set again by each role below, after the setup barrier
         if (!item_at(0, W0).valid) return;
     }
-    if (!split && status_has_timeout(p.status, kDevTimeout)) return;
+    if (!split && cta_has_timeout(p.status, kDevTimeout)) return;
     // The split last wave (launched behind this grid, independent of its
     // results) may take each SM as soon as this grid's CTA there is done.
     if (!split) grid_launch_dependents();

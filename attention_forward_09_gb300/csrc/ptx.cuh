@@ -82,6 +82,13 @@ __device__ __forceinline__ bool status_has_timeout(const uint32_t* status, uint3
     return status && (*reinterpret_cast<const volatile uint32_t*>(status) & bit);
 }
 
+// The same as one answer for the CTA, asked by all its threads together: the
+// word can change between two threads' reads, and a CTA that some of its
+// threads leave would go on without what they set up (barriers, tensor memory).
+__device__ __forceinline__ bool cta_has_timeout(const uint32_t* status, uint32_t bit) {
+    return status && __syncthreads_or(threadIdx.x == 0 && status_has_timeout(status, bit));
+}
+
 // ------------------------------------------------------------------ fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

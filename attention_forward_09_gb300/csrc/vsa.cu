@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(224, 1)
         n = n < 0 ? 0 : cap;
     }
     const int n_kv = (n + 1) >> 1;  // KV tile j = entries 2 j and 2 j + 1
-    if (status_has_timeout(p.status, kDevTimeout)) return;
+    if (cta_has_timeout(p.status, kDevTimeout)) return;
 
     // ------------------------------------------------------------------ setup
     if (threadIdx.x == 0) {
