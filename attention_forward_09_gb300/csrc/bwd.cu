@@ -98,6 +98,10 @@ struct BwdCfg {
     // slots of each ring that an item's gradients leave through
     static constexpr int STAGE1 = NCK, STAGE2 = ACCS == 2 ? NCK : 0;
     static constexpr int ITEMS = 3;                            // items published ahead
+    // Empty items looked at (well under a microsecond each) before the roles that
+    // wait for the next one hear that the producer is still at it: a wait is for
+    // a pipeline that stands still, not for a long search.
+    static constexpr int LOOKS = 4096;
     static constexpr int BARS_FIXED = 22 + 2 * ITEMS + 2 * STATS;
     static constexpr int RELEASES = HAS_DS && !SHARED ? 2 : 1;  // commits that release a slot
     static constexpr int ROOM = 232448 - RES_SMEM * R_BYTES - STATS * STAT_BYTES - 16 - ITEMS * 64 - BARS_FIXED * 8;
@@ -577,6 +581,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             Item it;
             int done = 0;       // items with steps so far
             int published = 0;  // items published
+            int looked = 0;     // empty ones since the last
             auto publish = [&]() -> bool {
                 const int b = published % C::ITEMS;
                 if (published >= C::ITEMS && !mbar_wait(b_item_free(b), (published / C::ITEMS - 1) & 1, abort_flag))
@@ -620,7 +625,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const uint32_t by = min(item_at(i, it), left);
                 i += by;
                 left -= by;
-                if (it.n < 0) continue;
+                if (it.n < 0) {
+                    if (++looked < C::LOOKS) continue;
+                    it = Item{};  // an item without rows or steps
+                }
+                looked = 0;
                 if (!(ok = publish())) break;
                 if (it.n == 0) continue;
                 for (int r = 0; r < C::RES; ++r) {
