@@ -22,6 +22,11 @@
  *    (out_dtype), lse and dlse fp32 in the forward call's layout.
  *  - Sums are kept in fp32 and rounded once; the probabilities and ds are
  *    rounded to bf16 as operands of the second products.
+ *  - Documents and batch entries are apart: nothing that one of them holds, NaN
+ *    and infinity included, reaches another's gradients.  Within a document a
+ *    value that is not finite may reach rows that do not see it: p and ds of a
+ *    hidden pair are 0, and 0 times it is NaN, as in the forward product p v.
+ *    (Rows that see no key, and rows past an entry's lengths, may hold anything.)
  *  - The same inputs give the same bits: each gradient row is summed in one
  *    order, without atomics.
  *  - dq, dk and dv are written whole but for the rows that belong to no
