@@ -208,7 +208,8 @@ gbattn_status run_bwd(const void* q, const void* k, const void* v, const void* o
         if (!aligned16(x)) return GBATTN_ERR_ALIGNMENT;
     p.tiles_q = static_cast<int>((static_cast<long long>(p.max_q) + 127) / 128);
     p.tiles_k = static_cast<int>((static_cast<long long>(p.max_k) + 127) / 128);
-    // grids are one-dimensional, an item a block
+    // An item's number and the counters that hand items out are 32-bit; each CTA
+    // claims once past the end, 1024 items at most.
     constexpr long long kMost = 0x7fffffffLL;
     const long long qh = static_cast<long long>(p.tiles_q) * p.num_docs, kh = static_cast<long long>(p.tiles_k) * p.num_docs;
     if (qh > kMost / p.Hq || kh > kMost / p.Hkv) return GBATTN_ERR_UNSUPPORTED;

@@ -241,7 +241,7 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
 // most: rows of dout and out are read whole, LANES lanes a pair and UN pairs in
 // flight a lane; the results cross shared memory, so that a head's statistics
 // are read and written for eight rows or more at a time.
-// HBM-bound: cross-attention of 16384 rows of 40 heads of 128 takes 51 us (348 MB,
+// HBM-bound: cross-attention of 16384 rows of 40 heads of 128 takes 51 us (346 MB,
 // the copy's rate), eight packed documents 69 (four CTAs an SM leave registers
 // for the loads in flight: 55 and 72 without the bound).
 //   STRIDED: out lies by its strides.  (A contiguous one is read by dout's
@@ -1108,13 +1108,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (lane == 0) mbar_arrive(b_res_in);
                 }
             }
-            // streamed rows [see_lo, see_hi) are visible; below tile edge_lo and from
-            // edge_hi on some row of the item sees only part of a tile
+            // this row sees (or is seen by) streamed rows [see_lo, see_hi)
             const int diag = GBATTN_ITEM(item, diag), str_len = GBATTN_ITEM(item, str_len), r0 = GBATTN_ITEM(item, r0);
             const int see_lo = C::KEYS && p.causal ? row - diag : 0;
             const int see_hi = !C::KEYS && p.causal ? min(str_len, row + diag + 1) : str_len;
-            const int edge_lo = C::KEYS && p.causal ? (max(0, r0 + BM - 1 - diag) + BN - 1) / BN : 0;
-            const int edge_hi = max(0, !C::KEYS && p.causal ? min(str_len, r0 + diag + 1) : str_len) / BN;
             const int t_lo = GBATTN_ITEM(item, t_lo), t_hi = GBATTN_ITEM(item, t_hi);
             int t = GBATTN_ITEM(item, t_first);
 #pragma unroll 1
