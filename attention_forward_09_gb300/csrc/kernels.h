@@ -320,8 +320,7 @@ cudaError_t launch_vsa_fwd(int D, const CUtensorMap& tmQ, const CUtensorMap& tmK
 // of out (and of lse).  Dense and padded batches have cu_q == nullptr and
 // max_q / max_k rows an entry; packed documents use cu_q / cu_k.
 struct BwdParams {
-    const void* out;        // bf16 or fp32 (out_f32), by the strides
-    long long out_bstride, out_rstride, out_hstride;  // elements from entry to entry (packed: 0), row to row, head to head
+    const void* out;        // bf16 or fp32 (out_f32), by its strides
     const void* dout;       // [Tq, Hq, D] bf16
     const float* lse;       // as the forward pass wrote it
     const float* dlse;      // the same layout, or null
@@ -348,6 +347,8 @@ struct BwdParams {
     uint32_t chunk[2];      // items a claim
     int split[2];           // > 1: an item's steps are shared by a cluster of that many CTAs
     int early_wait;         // 1: the launch before this one writes the statistics
+    // out: elements from entry to entry (packed: 0), row to row, head to head
+    long long out_bstride, out_rstride, out_hstride;
 };
 long long bwd_stat_stride(long long Tq, int num_docs);
 // [rows, heads, D] bf16, boxes {64, 1, 128}, 128-byte swizzle.
