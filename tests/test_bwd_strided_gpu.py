@@ -181,3 +181,24 @@ def test_what_stays_refused():
         B, S, H, D = out.shape
         o = room.as_strided(out.shape, (2 * S * H * D, D, S * D, 1)).copy_(out)
         run(o, lse, do, dlse, dq=room[S * H * D:][:out.numel()].view(out.shape))
+
+
+@pytest.mark.parametrize("D", workloads.HEAD_SIZES)
+def test_fp32_rows_on_16_bytes_and_rows_of_no_document(D):
+    """An fp32 `out` whose rows are D + 4 apart, packed, with rows behind the last document that are no numbers."""
+    g = torch.Generator().manual_seed(D)
+    lens, Hq, Hkv, s, tail = [90, 1, 140], 6, 3, D ** -0.5, 20
+    T = sum(lens) + tail
+    q, k, v, do = randn(g, T, Hq, D), randn(g, T, Hkv, D), randn(g, T, Hkv, D), randn(g, T, Hq, D)
+    cu = workloads.cu_from_lengths(lens).to(dev())
+    out, lse = gb.attn_fwd_varlen(q, k, v, cu, cu, 140, 140, s, True, lse=True, out_dtype=torch.float32)
+    wide = torch.full((T, Hq, D + 4), float("nan"), device=dev())
+    wide[:-tail, :, 4:] = out[:-tail]
+
+    def run(o):
+        grads = [torch.full_like(x, 777.0) for x in (q, k, v)]
+        return gb.attn_bwd_varlen(q, k, v, o, lse, do, cu, cu, 140, 140, s, True, dq=grads[0], dk=grads[1], dv=grads[2])
+
+    got = run(wide[..., 4:])
+    same(run(out), got)
+    assert all(bool((x[-tail:] == 777.0).all()) for x in got)
