@@ -1036,9 +1036,10 @@ def attn_bwd_padded(q, k, v, out, lse, dout, lens_q=None, lens_k=None, softmax_s
 def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, softmax_scale=None,
                     causal=False, dlse=None, dq=None, dk=None, dv=None, workspace=None, dev_status=None, stream=None):
     """Gradients of attn_fwd_varlen: q, out, dout [Tq, Hq, D], k, v [Tk, Hkv,
-    D], lse [Hq, Tq], cu_seqlens int32 [N + 1], max_seqlen_q/k host ints.
-    Returns (dq, dk, dv); rows that belong to no document are left as they
-    were.  Workspace: ``attn_bwd_workspace_size(N, Tq, Hq)`` bytes."""
+    D], lse [Hq, Tq], cu_seqlens int32 [N + 1], max_seqlen_q/k host ints;
+    strides as for attn_bwd_dense.  Returns (dq, dk, dv); rows that belong to no
+    document are left as they were.  Workspace: ``attn_bwd_workspace_size(N, Tq,
+    Hq)`` bytes."""
     if q.dim() != 3 or k.dim() != 3 or k.shape[2] != q.shape[2]:
         raise ValueError("q must be [Tq, Hq, D], k and v [Tk, Hkv, D]")
     Tq, Hq, D = q.shape

@@ -23,8 +23,8 @@
 // timing: there are no atomics.  The price is that S and dP are formed twice,
 // seven products for the five that one pass with atomics on dQ would need.
 //
-// DiT self-attention, 2 x 4096 rows, 24 heads, D = 128: 921 us a call, of them 17
-// for the statistics, 464 and 410 for the two passes by themselves; 1.12 PFLOP/s
+// DiT self-attention, 2 x 4096 rows, 24 heads, D = 128: 919 us a call, of them 18
+// for the statistics, 462 and 409 for the two passes by themselves; 1.12 PFLOP/s
 // of five products, 1.56 of the seven, at the power cap (1.83 GHz).
 //
 // P and dS are rounded to bf16 as operands of the second products, as P is in
@@ -244,7 +244,8 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
 // HBM-bound: cross-attention of 16384 rows of 40 heads of 128 takes 51 us (346 MB,
 // the copy's rate), eight packed documents 69 (four CTAs an SM leave registers
 // for the loads in flight: 55 and 72 without the bound).
-//   STRIDED: out lies by its strides.  (A contiguous one is read by dout's
+//   STRIDED: out lies by its strides (cross-attention from a transposed out: 53
+// us).  (A contiguous one is read by dout's
 // offsets: the strides take registers that the fp32 loads need, and a padded
 // batch of D = 96 took 62 us for 57 with them.)
 template <int D, bool F32, bool STRIDED>

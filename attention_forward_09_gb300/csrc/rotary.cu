@@ -20,7 +20,8 @@
 // the half layout, two units in flight a lane (27654 tokens of 32 + 8 heads of
 // 128: 86 us of kernel, 6.6 TB/s; with one unit 90, three 88, four 96: the
 // registers of more cost warps).  Rotated widths that are no whole vectors (half layout: rot %
-// 16, interleaved: rot % 8) are moved pair by pair.
+// 16, interleaved: rot % 8) are moved pair by pair, the copied rest value by
+// value: right and slow (the same tokens, rot 20 of 128, half layout: 570 us, 1.0 TB/s).
 #include "kernels.h"
 #include "ptx.cuh"
 

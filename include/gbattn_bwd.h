@@ -19,7 +19,8 @@
  * Conventions are those of gbattn.h (ownership, streams, errors, dev_status,
  * head sizes, masks), and:
  *  - q, k, v, dout and the gradients are bf16; out is bf16 or fp32
- *    (out_dtype), lse and dlse fp32 in the forward call's layout.
+ *    (out_dtype), lse and dlse fp32 in the forward call's layout.  All are
+ *    contiguous (an out that is not: gbattn_bwd_strided.h).
  *  - Sums are kept in fp32 and rounded once; the probabilities and ds are
  *    rounded to bf16 as operands of the second products.
  *  - Documents and batch entries are apart: nothing that one of them holds, NaN
